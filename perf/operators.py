@@ -244,35 +244,33 @@ _OWN = {"route": _own_route, "experts": _own_experts, "lora": _own_lora}
 
 
 def _sort_plain(ids, experts):
-    """Rows in expert order (ties by slot): offsets, the slot of each row, the row of each slot."""
+    """Slots in expert order (ties by slot, those of no expert last): offsets, the slot of each row, the
+    row of each slot and whether it has one."""
     flat = ids.flatten().long()
     live = (flat >= 0) & (flat < experts)
     expert, order = torch.sort(torch.where(live, flat, experts), stable=True)
     offsets = (expert[:, None] < torch.arange(experts + 1, device=flat.device)).sum(0)
     row = torch.empty_like(order)
     row[order] = torch.arange(order.numel(), device=flat.device)
-    return offsets, torch.where(expert < experts, order, -1), torch.where(live, row, -1), live
+    return offsets, order, row, live
 
 
 def _route_plain(s):
     dt, topk = s["x"].dtype, s["topk"]
-    offsets, order, slot, live = _sort_plain(s["ids"], s["experts"])
-    token = torch.where(order >= 0, order, 0) // topk
-    filled = (order >= 0)[:, None]
-    xs = torch.where(filled, s["x"][token], 0)
-    at = torch.where(live, slot, 0)
-    w = torch.where(live, s["weights"].flatten(), 0.0)
+    offsets, order, row, live = _sort_plain(s["ids"], s["experts"])
+    token, filled = order // topk, live[order][:, None]
     shape = (s["tokens"], topk, s["width"])
-    back = torch.where(live[:, None], s["ys"].float()[at], 0.0)
+    weights = s["weights"].flatten()
+    back = torch.where(live[:, None], s["ys"].float()[row], 0.0)
     out = {"offsets": offsets.to(torch.int32), "order": order.to(torch.int32),
-           "slot": slot.to(torch.int32).view(s["tokens"], topk), "xs": xs,
-           "y": (w[:, None] * back).view(shape).sum(1).to(dt)}
+           "slot": torch.where(live, row, -1).to(torch.int32).view(s["tokens"], topk),
+           "xs": torch.where(filled, s["x"][token], 0),
+           "y": (torch.where(live, weights, 0.0)[:, None] * back).view(shape).sum(1).to(dt)}
     if s["train"]:
         dy = s["dy"].float()
-        row_w = torch.where(order >= 0, s["weights"].flatten()[torch.where(order >= 0, order, 0)], 0.0)
-        out["dys"] = torch.where(filled, row_w[:, None] * dy[token], 0.0).to(dt)
+        out["dys"] = torch.where(filled, weights[order][:, None] * dy[token], 0.0).to(dt)
         out["dweights"] = (back.view(shape) * dy[:, None, :]).sum(2)
-        dxs = torch.where(live[:, None], s["dxs"].float()[at], 0.0)
+        dxs = torch.where(live[:, None], s["dxs"].float()[row], 0.0)
         out["dx"] = dxs.view(shape).sum(1).to(dt)
     return out
 
@@ -296,7 +294,7 @@ def _weights_plain(s):
 
 def _experts_plain(s):
     dt = s["x"].dtype
-    offsets, order, slot, _ = _sort_plain(s["ids"], s["experts"])
+    offsets, order, _, _ = _sort_plain(s["ids"], s["experts"])
     expert = s["ids"].flatten().long()[order]
     place = torch.arange(order.numel(), device="cuda") - offsets[expert]
     padded = torch.zeros(s["experts"], s["rows"], s["k"], device="cuda")
