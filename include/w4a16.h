@@ -229,6 +229,111 @@ w4a16_status w4a16_dequant_nf4(const int32_t* packed, const uint16_t* absmax,
                                const uint16_t* codebook, int K, int N, int block_size,
                                w4a16_dtype wdtype, void* w_out, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Routed operators: rows of one batch that go to different weights.
+ *
+ * A slot i = t * topk + j is choice j of token t; ids[i] is its group (an expert, or with topk 1
+ * a request's adapter). A group outside [0, groups) is none: the slot's row is zeros where rows
+ * are written, and adds nothing where rows come back. S = tokens * topk.
+ * Limits: 1 <= topk, 1 <= groups <= W4A16_MAX_GROUPS, S <= W4A16_MAX_SLOTS
+ * (W4A16_ERR_UNSUPPORTED past them). tokens = 0 is a no-op for every call but w4a16_route,
+ * whose plan then holds zero offsets.
+ * ------------------------------------------------------------------------------------------ */
+#define W4A16_MAX_GROUPS 1024
+#define W4A16_MAX_SLOTS (1 << 26)
+
+/* Bytes of a plan for this many tokens, choices and groups; 0 for bad arguments. */
+size_t w4a16_route_bytes(int tokens, int topk, int groups);
+
+/* The plan of a batch: its slots sorted by group (a stable sort), as int32 words in `plan`:
+ *   offsets [groups + 1]  at word 0: group e's sorted rows are [offsets[e], offsets[e + 1])
+ *   order   [S]           at word r(groups + 1): the slot of each sorted row; the slots of no
+ *                         group come last, in rows [offsets[groups], S)
+ *   slot    [tokens][topk] at word r(groups + 1) + r(S): the sorted row of each slot, or -1
+ * with r(n) = n rounded up to a multiple of 64; the words after them are private to the
+ * library. The plan depends on the ids only: calls on any number of tensors may share it.
+ *   ids   [in]  int32 [tokens][topk], 4-byte aligned
+ *   plan  [out] >= w4a16_route_bytes(tokens, topk, groups) bytes, 256-byte aligned */
+w4a16_status w4a16_route(const int32_t* ids, int tokens, int topk, int groups, int32_t* plan,
+                         size_t plan_bytes, void* stream);
+
+/* Rows into sorted order: xs[p] = x[order[p] / topk], zeros in the rows of no group.
+ *   x   [in]  dtype [tokens][width], any dtype, element-aligned (as are all rows below)
+ *   xs  [out] dtype [S][width]; must not overlap x
+ * The plan's tokens, topk and groups must be those it was made with (for every call below). */
+w4a16_status w4a16_dispatch(const void* x, const int32_t* plan, int tokens, int topk, int groups,
+                            int width, w4a16_dtype dtype, void* xs, void* stream);
+
+/* Gradient of w4a16_dispatch: dx[t] = sum_j dxs[slot[t][j]], summed in fp32, j ascending. */
+w4a16_status w4a16_dispatch_backward(const void* dxs, const int32_t* plan, int tokens, int topk,
+                                     int groups, int width, w4a16_dtype dtype, void* dx, void* stream);
+
+/* Sorted rows back to their tokens, weighted: y[t] = sum_j weights[t][j] ys[slot[t][j]], summed
+ * in fp32, j ascending, rounded once.
+ *   ys      [in]  dtype [S][width];  weights [in] float [tokens][topk], 4-byte aligned
+ *   y       [out] out_dtype [tokens][width], out_dtype = dtype, or any type for fp32 ys */
+w4a16_status w4a16_combine(const void* ys, const int32_t* plan, int tokens, int topk, int groups,
+                           const float* weights, int width, w4a16_dtype dtype, void* y,
+                           w4a16_dtype out_dtype, void* stream);
+
+/* Gradients of w4a16_combine: dys[slot[t][j]] = weights[t][j] dy[t] (zeros in the rows of no
+ * group) and dweights[t][j] = sum_n dy[t][n] ys[slot[t][j]][n] in fp32 (0 for a slot of no
+ * group).
+ *   dy [in] dtype [tokens][width], ys [in] dtype [S][width], dys [out] dtype [S][width] (not
+ *   overlapping ys), dweights [out] float [tokens][topk] */
+w4a16_status w4a16_combine_backward(const void* dy, const void* ys, const int32_t* plan, int tokens,
+                                    int topk, int groups, const float* weights, int width,
+                                    w4a16_dtype dtype, void* dys, float* dweights, void* stream);
+
+/* The W4A16 GEMM of sorted rows with their groups' weights: out[p] = row(p) * W_hat[e] for the
+ * rows p of group e, zeros for the rows of no group.
+ *   x       [in]  act [tokens][K] with gather != 0: row(p) = x[order[p] / topk], read in place
+ *                 (tokens * K * 2 < 2^31, else W4A16_ERR_UNSUPPORTED); else act [S][K]: row(p) = x[p]
+ *   packed  [in]  w4a16_packed_bytes(K, N) bytes a group, one after another
+ *   scales  [in]  act [groups][K/group_size][N]
+ *   qzeros  [in]  int32 [groups][K/group_size][N/8], or NULL for symmetric codes
+ *   out     [out] out_dtype [S][N]
+ * swiglu != 0: each weight is a fused gate+up projection (as for w4a16_gemm_swiglu, N % 32 == 0)
+ * and out is [S][N/2]. Other arguments, errors and determinism as for w4a16_gemm. */
+w4a16_status w4a16_gemm_grouped(const void* x, const int32_t* plan, int tokens, int topk, int groups,
+                                int gather, int K, int N, w4a16_dtype act, const int32_t* packed,
+                                const void* scales, const int32_t* qzeros, int group_size, int swiglu,
+                                void* out, w4a16_dtype out_dtype, void* stream);
+
+/* NF4 counterpart of w4a16_gemm_grouped: absmax fp16 [groups][K/block_size][N], one codebook. */
+w4a16_status w4a16_gemm_grouped_nf4(const void* x, const int32_t* plan, int tokens, int topk, int groups,
+                                    int gather, int K, int N, w4a16_dtype act, const int32_t* packed,
+                                    const uint16_t* absmax, const uint16_t* codebook, int block_size,
+                                    int swiglu, void* out, w4a16_dtype out_dtype, void* stream);
+
+/* Name of the kernel w4a16_gemm_grouped launches for S = tokens * topk rows over this many
+ * groups (static string; "none" for bad shapes). */
+const char* w4a16_grouped_kernel_name(int S, int K, int N, int groups, int group_size);
+
+/* Bytes of scratch w4a16_lora_add needs on the current device (`planned`: with a plan given);
+ * 0 for bad shapes. */
+size_t w4a16_lora_workspace_bytes(int M, int K, int N, int adapters, int rank, int planned);
+
+/* Low-rank adapters of many requests beside a projection all rows share:
+ *   out[m] = y[m] + scaling[a] (x[m] A[a]^T) B[a]^T, a = ids[m]; out[m] = y[m] where a is none
+ * for any shared projection y = x W (w4a16_gemm, NF4, AWQ, ...). x A^T is summed in fp32 and
+ * not rounded to 16 bits between the products; out is rounded once.
+ *   x        [in]  act [M][K], act = W4A16_F16 or W4A16_BF16; K % 32 == 0
+ *   y        [in]  y_dtype [M][N], y_dtype = act or W4A16_F32; N % 16 == 0
+ *   lora_a   [in]  act [adapters][rank][K];  lora_b [in] act [adapters][N][rank]
+ *                  rank a multiple of 8 up to 256 (W4A16_ERR_UNSUPPORTED otherwise; smaller
+ *                  adapters are padded with zeros); adapters <= W4A16_MAX_GROUPS
+ *   ids      [in]  int32 [M], each row's adapter; read only where plan is NULL
+ *   scaling  [in]  float [adapters]
+ *   plan     [in]  of w4a16_route(ids, M, 1, adapters), for calls that share it; or NULL
+ *   out      [out] y_dtype [M][N]; may be y (then rows of no adapter are left alone)
+ *   workspace [in/out] >= w4a16_lora_workspace_bytes(...), 256-byte aligned
+ * x, y, out, lora_a and lora_b need 16-byte alignment. M = 0 is a no-op. Deterministic. */
+w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w4a16_dtype act,
+                            w4a16_dtype y_dtype, const void* lora_a, const void* lora_b, int adapters,
+                            int rank, const int32_t* ids, const float* scaling, const int32_t* plan,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Name of the kernel w4a16_gemm / w4a16_gemm_nf4 launch for this shape (static string),
  * so a caller can log which path ran ("4.3 Weight-only INT4", section 4.1). */
 const char* w4a16_kernel_name(int M, int K, int N, int group_size);

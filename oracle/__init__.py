@@ -22,6 +22,7 @@ Modules
   gptq      GPTQ: row-by-row quantization with inverse-Hessian error compensation
   awq       AWQ: per-input-channel scale search, S W quantized, activations times S^-1
   w4a8      W4A8: per-token INT8 activations, per-channel INT4 weights, integer product
+  routed    rows sorted by group and back with gradients, grouped products, row adapters
   storage   bytes and bits per weight of the packed format
   roofline  memory/compute floors and the batch crossover
 
@@ -40,6 +41,7 @@ from .glu import silu, swiglu_split, swiglu_ref, swiglu_bound
 from .gptq import hessian, compensate, gptq_quantize
 from . import awq
 from . import w4a8
+from . import routed
 from .storage import storage_bytes, bits_per_weight, bytes_per_weight
 from . import roofline
 
@@ -52,6 +54,6 @@ __all__ = [
     "dequant_affine", "dequant_sym", "dequant_nf4",
     "gemm_ref", "gemm_ref_columns", "gemm_bruteforce",
     "silu", "swiglu_split", "swiglu_ref", "swiglu_bound",
-    "hessian", "compensate", "gptq_quantize", "awq", "w4a8",
+    "hessian", "compensate", "gptq_quantize", "awq", "w4a8", "routed",
     "storage_bytes", "bits_per_weight", "bytes_per_weight", "roofline",
 ]

@@ -72,6 +72,28 @@ def lib() -> ctypes.CDLL:
     L.w4a16_kernel_name.restype = ctypes.c_char_p
     L.w4a16_status_string.argtypes = [i32]
     L.w4a16_status_string.restype = ctypes.c_char_p
+    L.w4a16_route_bytes.argtypes = [i32, i32, i32]
+    L.w4a16_route_bytes.restype = sz
+    L.w4a16_route.argtypes = [vp, i32, i32, i32, vp, sz, vp]
+    L.w4a16_route.restype = i32
+    L.w4a16_dispatch.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp]
+    L.w4a16_dispatch.restype = i32
+    L.w4a16_dispatch_backward.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp]
+    L.w4a16_dispatch_backward.restype = i32
+    L.w4a16_combine.argtypes = [vp, vp, i32, i32, i32, vp, i32, i32, vp, i32, vp]
+    L.w4a16_combine.restype = i32
+    L.w4a16_combine_backward.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, vp, vp]
+    L.w4a16_combine_backward.restype = i32
+    L.w4a16_gemm_grouped.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, i32, i32, vp, i32, vp]
+    L.w4a16_gemm_grouped.restype = i32
+    L.w4a16_gemm_grouped_nf4.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, i32, i32, vp, i32, vp]
+    L.w4a16_gemm_grouped_nf4.restype = i32
+    L.w4a16_grouped_kernel_name.argtypes = [i32, i32, i32, i32, i32]
+    L.w4a16_grouped_kernel_name.restype = ctypes.c_char_p
+    L.w4a16_lora_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    L.w4a16_lora_workspace_bytes.restype = sz
+    L.w4a16_lora_add.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.w4a16_lora_add.restype = i32
     L.w4a16_read_probe.argtypes = [vp, sz, vp, vp]
     L.w4a16_read_probe.restype = i32
     L.w4a16_version.argtypes = []
@@ -448,6 +470,282 @@ def dequant_nf4(packed, absmax, codebook, K: int, block_size: int = 64, wdtype=N
                                  _dt(wdtype), _ptr(w), _stream(absmax))
     _check(st, "w4a16_dequant_nf4")
     return w
+
+
+# ---- routed operators: rows of one batch that go to different weights ----
+
+class Routing:
+    """A batch's plan (:func:`route`): which sorted row each slot (token, choice) has.
+
+    ``offsets`` int32 ``[groups + 1]``: group ``e``'s sorted rows; ``order`` int32 ``[S]``: the
+    slot of each sorted row, the slots of no group last; ``slot`` int32 ``[tokens, topk]``: the
+    sorted row of each slot, -1 for a slot of no group (S = tokens * topk). They are views of
+    ``plan``, the buffer the kernels read, and are not to be written."""
+
+    __slots__ = ("plan", "tokens", "topk", "groups")
+
+    def __init__(self, plan, tokens: int, topk: int, groups: int):
+        self.plan, self.tokens, self.topk, self.groups = plan, tokens, topk, groups
+
+    @property
+    def rows(self) -> int:
+        return self.tokens * self.topk
+
+    def _at(self):
+        return -(-(self.groups + 1) // 64) * 64
+
+    @property
+    def offsets(self):
+        return self.plan[:self.groups + 1]
+
+    @property
+    def order(self):
+        return self.plan[self._at():self._at() + self.rows]
+
+    @property
+    def slot(self):
+        first = self._at() + -(-self.rows // 64) * 64
+        return self.plan[first:first + self.rows].view(self.tokens, self.topk)
+
+
+def route(ids, groups: int) -> Routing:
+    """Sort a batch's slots by group: ``ids`` int32 ``[tokens, topk]`` (or ``[tokens]``, one
+    choice each), a value outside ``[0, groups)`` being no group. The plan serves any number of the
+    calls below."""
+    torch = _torch()
+    if ids is None or ids.dtype != torch.int32 or ids.dim() not in (1, 2):
+        _fail("ids must be an int32 tensor [tokens, topk] or [tokens]")
+    if not ids.is_contiguous():
+        _fail("ids must be contiguous")
+    tokens, topk = ids.shape[0], 1 if ids.dim() == 1 else ids.shape[1]
+    if topk < 1 or groups < 1:
+        _fail(f"topk={topk}, groups={groups}: both must be at least 1")
+    need = int(lib().w4a16_route_bytes(tokens, topk, groups))
+    if need == 0:
+        raise W4A16Error(f"unsupported routing: {tokens} x {topk} slots, {groups} groups", ERR_UNSUPPORTED)
+    plan = torch.empty(need // 4, dtype=torch.int32, device=ids.device)
+    st = lib().w4a16_route(_ptr(ids), tokens, topk, groups, _ptr(plan), need, _stream(ids))
+    _check(st, "w4a16_route")
+    return Routing(plan, tokens, topk, groups)
+
+
+def _route_args(r):
+    return _ptr(r.plan), r.tokens, r.topk, r.groups
+
+
+def _expect_rows(t, name, rows, r, dtypes=None):
+    """A tensor of whole rows on the plan's device; returns its width."""
+    torch = _torch()
+    if not isinstance(r, Routing):
+        _fail("routing must be the result of route()")
+    if t is None or t.dim() != 2:
+        _fail(f"{name} must be a 2-D tensor")
+    if t.shape[1] < 1:
+        _fail(f"{name} has rows of no elements")
+    _expect(t, name, (rows, t.shape[1]), dtypes or (torch.float16, torch.bfloat16, torch.float32), r.plan.device)
+    return t.shape[1]
+
+
+def _out_rows(out, shape, dtype, like, name="out", avoid=()):
+    if out is None:
+        return _torch().empty(shape, dtype=dtype, device=like.device)
+    _expect(out, name, shape, (dtype,), like.device)
+    _apart(out, name, avoid)
+    return out
+
+
+def _apart(out, name, others):
+    """``out`` shares no memory with the tensors a call reads."""
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in others:
+        if t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
+            _fail(f"{name} overlaps an input")
+
+
+def dispatch(x, routing: Routing, out=None):
+    """Tokens' rows into sorted order: ``xs[S, width]``, ``xs[p] = x[order[p] // topk]``, zeros in the
+    rows of no group. ``x[tokens, width]`` fp16, bf16 or fp32, any width."""
+    width = _expect_rows(x, "x", routing.tokens if isinstance(routing, Routing) else 0, routing)
+    out = _out_rows(out, (routing.rows, width), x.dtype, x, avoid=(x,))
+    st = lib().w4a16_dispatch(_ptr(x), *_route_args(routing), width, _dt(x.dtype), _ptr(out), _stream(x))
+    _check(st, "w4a16_dispatch")
+    return out
+
+
+def dispatch_backward(dxs, routing: Routing, out=None):
+    """Gradient of :func:`dispatch`: ``dx[t] = sum_j dxs[slot[t, j]]``, summed in fp32."""
+    width = _expect_rows(dxs, "dxs", routing.rows if isinstance(routing, Routing) else 0, routing)
+    out = _out_rows(out, (routing.tokens, width), dxs.dtype, dxs, avoid=(dxs,))
+    st = lib().w4a16_dispatch_backward(_ptr(dxs), *_route_args(routing), width, _dt(dxs.dtype), _ptr(out),
+                                       _stream(dxs))
+    _check(st, "w4a16_dispatch_backward")
+    return out
+
+
+def combine(ys, routing: Routing, weights, out_dtype=None, out=None):
+    """Sorted rows back to their tokens: ``y[t] = sum_j weights[t, j] * ys[slot[t, j]]`` in fp32,
+    rounded once to ``ys``'s dtype (fp32 ``ys``: to any ``out_dtype``). ``weights`` fp32
+    ``[tokens, topk]``; the weight of a slot of no group is not used."""
+    torch = _torch()
+    width = _expect_rows(ys, "ys", routing.rows if isinstance(routing, Routing) else 0, routing)
+    _expect(weights, "weights", (routing.tokens, routing.topk), (torch.float32,), ys.device)
+    if out_dtype is None:
+        out_dtype = ys.dtype if out is None else out.dtype
+    if out_dtype != ys.dtype and (ys.dtype != torch.float32 or out_dtype not in (torch.float16, torch.bfloat16)):
+        _fail(f"out dtype {out_dtype} for {ys.dtype} rows")
+    out = _out_rows(out, (routing.tokens, width), out_dtype, ys, avoid=(ys, weights))
+    st = lib().w4a16_combine(_ptr(ys), *_route_args(routing), _ptr(weights), width, _dt(ys.dtype), _ptr(out),
+                             _dt(out_dtype), _stream(ys))
+    _check(st, "w4a16_combine")
+    return out
+
+
+def combine_backward(dy, ys, routing: Routing, weights):
+    """Gradients of :func:`combine` for ``dy[tokens, width]`` in ``ys``'s dtype: ``(dys, dweights)``,
+    ``dys[slot[t, j]] = weights[t, j] * dy[t]`` and the fp32 ``dweights[t, j] = <dy[t], ys[slot[t, j]]>``."""
+    torch = _torch()
+    width = _expect_rows(ys, "ys", routing.rows if isinstance(routing, Routing) else 0, routing)
+    _expect(dy, "dy", (routing.tokens, width), (ys.dtype,), ys.device)
+    _expect(weights, "weights", (routing.tokens, routing.topk), (torch.float32,), ys.device)
+    dys = torch.empty_like(ys)
+    dweights = torch.empty_like(weights)
+    st = lib().w4a16_combine_backward(_ptr(dy), _ptr(ys), *_route_args(routing), _ptr(weights), width,
+                                      _dt(ys.dtype), _ptr(dys), _ptr(dweights), _stream(ys))
+    _check(st, "w4a16_combine_backward")
+    return dys, dweights
+
+
+def pack_grouped(qweight):
+    """Canonical ``qweight[groups, K/8, N]`` int32 -> the groups' device layouts, one after another."""
+    torch = _torch()
+    if qweight.dtype != torch.int32 or qweight.dim() != 3 or not qweight.is_contiguous():
+        _fail("qweight must be a contiguous int32 tensor [groups, K/8, N]")
+    K, N = qweight.shape[1] * 8, qweight.shape[2]
+    nb = packed_bytes(K, N)
+    if nb == 0:
+        raise W4A16Error(f"unsupported shape K={K} N={N}", ERR_UNSUPPORTED)
+    out = torch.empty((qweight.shape[0], nb // 4), dtype=torch.int32, device=qweight.device)
+    for e in range(qweight.shape[0]):
+        _check(lib().w4a16_pack(_ptr(qweight[e]), K, N, _ptr(out[e]), _stream(qweight)), "w4a16_pack")
+    return out
+
+
+def _grouped(x, routing, packed, scales, tail, group_size, glu, gather, out_dtype, out, nf4):
+    torch = _torch()
+    if not isinstance(routing, Routing):
+        _fail("routing must be the result of route()")
+    rows, K = _expect_x(x)
+    want = routing.tokens if gather else routing.rows
+    if rows != want:
+        _fail(f"x has {rows} rows, expected {want} ({'tokens' if gather else 'sorted rows'})")
+    if x.device != routing.plan.device:
+        _fail(f"x is on {x.device}, the routing on {routing.plan.device}")
+    if scales is None or scales.dim() != 3:
+        _fail("scales must be a 3-D [groups, K/g, N] tensor")
+    E, N, G = routing.groups, scales.shape[2], _groups(K, group_size)
+    _expect(scales, "scales", (E, G, N), (torch.float16 if nf4 else x.dtype,), x.device)
+    if N % 8:
+        _fail(f"N={N} is not a multiple of 8")
+    if nf4:
+        _expect(tail, "codebook", (16,), (torch.float16,), x.device)
+    elif tail is not None:
+        _expect(tail, "qzeros", (E, G, N // 8), (torch.int32,), x.device)
+    need = packed_bytes(K, N)
+    if need == 0:
+        raise W4A16Error(f"unsupported shape K={K} N={N}", ERR_UNSUPPORTED)
+    _expect(packed, "packed", (E, need // 4), (torch.int32,), x.device)
+    if glu and N % 2:
+        _fail(f"N={N} must be even (gate and up halves)")
+    out = _out(out, routing.rows, N // 2 if glu else N, out_dtype, x)
+    _apart(out, "out", (x,))
+    f = lib().w4a16_gemm_grouped_nf4 if nf4 else lib().w4a16_gemm_grouped
+    st = f(_ptr(x), *_route_args(routing), int(gather), K, N, _dt(x.dtype), _ptr(packed), _ptr(scales), _ptr(tail),
+           group_size, int(glu), _ptr(out), _dt(out.dtype), _stream(x))
+    _check(st, "w4a16_gemm_grouped_nf4" if nf4 else "w4a16_gemm_grouped")
+    return out
+
+
+def gemm_grouped(x, routing: Routing, packed, scales, qzeros, group_size: int, gather: bool = False,
+                 out_dtype=None, out=None):
+    """The experts' products: ``out[S, N]``, ``out[p] = row(p) @ W_hat[e]`` for group ``e``'s sorted rows,
+    zeros in the rows of no group. ``x[S, K]`` holds the sorted rows, or with ``gather`` the tokens' ``[tokens,
+    K]``, read through the plan. ``packed`` from :func:`pack_grouped`, ``scales[groups, K/g, N]`` in x's
+    dtype, ``qzeros[groups, K/g, N/8]`` int32 or None (symmetric)."""
+    return _grouped(x, routing, packed, scales, qzeros, group_size, False, gather, out_dtype, out, False)
+
+
+def gemm_grouped_swiglu(x, routing: Routing, packed, scales, qzeros, group_size: int, gather: bool = False,
+                        out_dtype=None, out=None):
+    """:func:`gemm_grouped` of fused gate+up weights (gate columns first) with the SwiGLU epilogue:
+    ``h[S, N/2]``."""
+    return _grouped(x, routing, packed, scales, qzeros, group_size, True, gather, out_dtype, out, False)
+
+
+def gemm_grouped_nf4(x, routing: Routing, packed, absmax, codebook, block_size: int = 64, gather: bool = False,
+                     out_dtype=None, out=None):
+    """NF4 counterpart of :func:`gemm_grouped`: fp16 ``absmax[groups, K/b, N]``, one fp16 ``codebook[16]``."""
+    return _grouped(x, routing, packed, absmax, codebook, block_size, False, gather, out_dtype, out, True)
+
+
+def gemm_grouped_nf4_swiglu(x, routing: Routing, packed, absmax, codebook, block_size: int = 64,
+                            gather: bool = False, out_dtype=None, out=None):
+    """NF4 counterpart of :func:`gemm_grouped_swiglu`."""
+    return _grouped(x, routing, packed, absmax, codebook, block_size, True, gather, out_dtype, out, True)
+
+
+def grouped_kernel_name(rows: int, K: int, N: int, groups: int, group_size: int) -> str:
+    return lib().w4a16_grouped_kernel_name(rows, K, N, groups, group_size).decode()
+
+
+def lora_workspace_bytes(M: int, K: int, N: int, adapters: int, rank: int, planned: bool = False) -> int:
+    return int(lib().w4a16_lora_workspace_bytes(M, K, N, adapters, rank, int(planned)))
+
+
+def lora_add(y, x, lora_a, lora_b, ids, scaling, routing: Routing | None = None, out=None, workspace=None):
+    """Low-rank adapters of many requests beside a shared projection: ``out[m] = y[m] + scaling[a] *
+    (x[m] @ lora_a[a].T) @ lora_b[a].T`` with ``a = ids[m]``, ``out[m] = y[m]`` where ``a`` is outside ``[0, adapters)``.
+
+    ``y[M, N]`` the projection's output (x's dtype or fp32), ``x[M, K]`` fp16/bf16,
+    ``lora_a[adapters, rank, K]``, ``lora_b[adapters, N, rank]`` in x's dtype, ``ids`` int32 ``[M]``, ``scaling``
+    fp32 ``[adapters]``. ``routing``: ``route(ids, adapters)`` made once for the projections of a step that share
+    the ids. ``out`` may be ``y``. ``workspace``: optional, ``lora_workspace_bytes(...)``."""
+    torch = _torch()
+    M, K = _expect_x(x)
+    if lora_a is None or lora_a.dim() != 3:
+        _fail("lora_a must be a 3-D [adapters, rank, K] tensor")
+    adapters, rank = lora_a.shape[0], lora_a.shape[1]
+    _expect(lora_a, "lora_a", (adapters, rank, K), (x.dtype,), x.device)
+    if y is None or y.dim() != 2:
+        _fail("y must be a 2-D [M, N] tensor")
+    N = y.shape[1]
+    _expect(y, "y", (M, N), (x.dtype, torch.float32), x.device)
+    _expect(lora_b, "lora_b", (adapters, N, rank), (x.dtype,), x.device)
+    _expect(scaling, "scaling", (adapters,), (torch.float32,), x.device)
+    if routing is None:
+        _expect(ids, "ids", (M,), (torch.int32,), x.device)
+        plan = None
+    else:
+        if not isinstance(routing, Routing) or (routing.tokens, routing.topk, routing.groups) != (M, 1, adapters):
+            _fail("routing must be route(ids, adapters) of these rows")
+        if routing.plan.device != x.device:
+            _fail(f"the routing is on {routing.plan.device}, expected {x.device}")
+        plan = routing.plan
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _expect(out, "out", (M, N), (y.dtype,), x.device)
+        _apart(out, "out", (x,) if out.data_ptr() == y.data_ptr() else (x, y))
+    need = lora_workspace_bytes(M, K, N, adapters, rank, plan is not None)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    else:
+        _expect_workspace(workspace, need, x.device)
+    st = lib().w4a16_lora_add(_ptr(x), _ptr(y), M, K, N, _dt(x.dtype), _dt(y.dtype), _ptr(lora_a), _ptr(lora_b),
+                              adapters, rank, _ptr(ids) if plan is None else None, _ptr(scaling), _ptr(plan),
+                              _ptr(out), *_ws_args(workspace), _stream(x))
+    _check(st, "w4a16_lora_add")
+    return out
 
 
 def read_probe(buf, sink):

@@ -8,6 +8,7 @@
 
 #include "w4a16.h"
 #include "w4a16_launch.hpp"
+#include "w4a16_routed.hpp"
 
 namespace {
 
@@ -466,6 +467,193 @@ const char* w4a16_status_string(w4a16_status s) {
     case W4A16_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
   }
   return "unknown status";
+}
+
+// ---- routed operators ----
+
+// tokens, topk and groups of a plan
+static w4a16_status check_route(int tokens, int topk, int groups) {
+  if (tokens < 0 || topk <= 0 || groups <= 0) return W4A16_ERR_ARG;
+  if (groups > w4a16::kMaxGroups || (long long)tokens * topk > w4a16::kMaxSlots) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+size_t w4a16_route_bytes(int tokens, int topk, int groups) {
+  if (check_route(tokens, topk, groups) != W4A16_OK) return 0;
+  return (size_t)w4a16::route_layout(tokens, topk, groups).words * 4;
+}
+
+w4a16_status w4a16_route(const int32_t* ids, int tokens, int topk, int groups, int32_t* plan,
+                         size_t plan_bytes, void* stream) {
+  const w4a16_status st = check_route(tokens, topk, groups);
+  if (st != W4A16_OK) return st;
+  if ((tokens && !ids) || !aligned(ids, 4)) return W4A16_ERR_ARG;
+  const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
+  if (!plan || !aligned(plan, 256) || plan_bytes < (size_t)r.words * 4) return W4A16_ERR_WORKSPACE;
+  return from_hip(w4a16::launch_route(ids, r, plan, static_cast<hipStream_t>(stream)));
+}
+
+static bool valid_dtype(w4a16_dtype d) { return d == W4A16_F16 || d == W4A16_BF16 || d == W4A16_F32; }
+static size_t dtype_bytes(w4a16_dtype d) { return d == W4A16_F32 ? 4 : 2; }
+
+// arguments common to the calls that move rows
+static w4a16_status check_rows(const int32_t* plan, int tokens, int topk, int groups, int width) {
+  const w4a16_status st = check_route(tokens, topk, groups);
+  if (st != W4A16_OK) return st;
+  if (width <= 0) return W4A16_ERR_ARG;
+  if ((long long)tokens * ((width + 255) / 256) >= (1LL << 30)) return W4A16_ERR_UNSUPPORTED;
+  if (tokens && (!plan || !aligned(plan, 256))) return W4A16_ERR_ARG;
+  return W4A16_OK;
+}
+
+static bool rows_ok(const void* p, w4a16_dtype d) { return p && aligned(p, dtype_bytes(d)); }
+
+w4a16_status w4a16_dispatch(const void* x, const int32_t* plan, int tokens, int topk, int groups,
+                            int width, w4a16_dtype dtype, void* xs, void* stream) {
+  if (!valid_dtype(dtype)) return W4A16_ERR_ARG;
+  const w4a16_status st = check_rows(plan, tokens, topk, groups, width);
+  if (st != W4A16_OK || tokens == 0) return st;
+  if (!rows_ok(x, dtype) || !rows_ok(xs, dtype) || x == xs) return W4A16_ERR_ARG;
+  return from_hip(w4a16::launch_dispatch(x, w4a16::route_layout(tokens, topk, groups), plan, width,
+                                         (int)dtype, xs, static_cast<hipStream_t>(stream)));
+}
+
+static w4a16_status combine_common(const void* ys, const int32_t* plan, int tokens, int topk, int groups,
+                                   const float* weights, int width, w4a16_dtype dtype, void* y,
+                                   w4a16_dtype out_dtype, void* stream) {
+  if (!valid_dtype(dtype) || !valid_dtype(out_dtype)) return W4A16_ERR_ARG;
+  if (out_dtype != dtype && dtype != W4A16_F32) return W4A16_ERR_ARG;
+  const w4a16_status st = check_rows(plan, tokens, topk, groups, width);
+  if (st != W4A16_OK || tokens == 0) return st;
+  if (!rows_ok(ys, dtype) || !rows_ok(y, out_dtype) || ys == y) return W4A16_ERR_ARG;
+  return from_hip(w4a16::launch_combine(ys, w4a16::route_layout(tokens, topk, groups), plan, weights, width,
+                                        (int)dtype, y, (int)out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+w4a16_status w4a16_dispatch_backward(const void* dxs, const int32_t* plan, int tokens, int topk,
+                                     int groups, int width, w4a16_dtype dtype, void* dx, void* stream) {
+  return combine_common(dxs, plan, tokens, topk, groups, nullptr, width, dtype, dx, dtype, stream);
+}
+
+w4a16_status w4a16_combine(const void* ys, const int32_t* plan, int tokens, int topk, int groups,
+                           const float* weights, int width, w4a16_dtype dtype, void* y,
+                           w4a16_dtype out_dtype, void* stream) {
+  if (tokens > 0 && (!weights || !aligned(weights, 4))) return W4A16_ERR_ARG;
+  return combine_common(ys, plan, tokens, topk, groups, weights, width, dtype, y, out_dtype, stream);
+}
+
+w4a16_status w4a16_combine_backward(const void* dy, const void* ys, const int32_t* plan, int tokens,
+                                    int topk, int groups, const float* weights, int width,
+                                    w4a16_dtype dtype, void* dys, float* dweights, void* stream) {
+  if (!valid_dtype(dtype)) return W4A16_ERR_ARG;
+  const w4a16_status st = check_rows(plan, tokens, topk, groups, width);
+  if (st != W4A16_OK || tokens == 0) return st;
+  if (!rows_ok(dy, dtype) || !rows_ok(ys, dtype) || !rows_ok(dys, dtype)) return W4A16_ERR_ARG;
+  if (dys == ys || dys == dy || !weights || !aligned(weights, 4) || !dweights || !aligned(dweights, 4))
+    return W4A16_ERR_ARG;
+  return from_hip(w4a16::launch_combine_backward(dy, ys, w4a16::route_layout(tokens, topk, groups), plan, weights,
+                                                 width, (int)dtype, dys, dweights,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+static w4a16_status grouped_common(GemmArgs& a, const int32_t* plan, int tokens, int topk, int groups, int gather,
+                                   w4a16_dtype act, w4a16_dtype out_dtype) {
+  w4a16_status st = check_route(tokens, topk, groups);
+  if (st != W4A16_OK) return st;
+  st = check_shape(a.K, a.N, a.group_size);
+  if (st != W4A16_OK) return st;
+  if (a.K % 32) return W4A16_ERR_UNSUPPORTED;
+  if (act != W4A16_F16 && act != W4A16_BF16) return W4A16_ERR_ARG;
+  if (out_dtype != act && out_dtype != W4A16_F32) return W4A16_ERR_ARG;
+  if (a.glu && a.N % 32) return W4A16_ERR_UNSUPPORTED;
+  if (gather && (long long)tokens * a.K * 2 >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;
+  if (tokens == 0) return W4A16_OK;
+  const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
+  if (!w4a16::grouped_fits(r, a.K, a.N)) return W4A16_ERR_UNSUPPORTED;
+  if (!plan || !a.x || !a.packed || !a.scales || !a.out || (a.nf4 && !a.codebook)) return W4A16_ERR_ARG;
+  if (!aligned(plan, 256) || !aligned(a.x, 16) || !aligned(a.packed, 16) || !aligned(a.out, 16)) return W4A16_ERR_ARG;
+  if (!aligned(a.scales, 2) || (a.qzeros && !aligned(a.qzeros, 4))) return W4A16_ERR_ARG;
+  if (a.codebook && !aligned(a.codebook, 2)) return W4A16_ERR_ARG;
+  a.act = act == W4A16_F16 ? w4a16::ACT_F16 : w4a16::ACT_BF16;
+  a.out_dtype = (int)out_dtype;
+  return from_hip(w4a16::launch_grouped(a, r, plan, gather != 0));
+}
+
+w4a16_status w4a16_gemm_grouped(const void* x, const int32_t* plan, int tokens, int topk, int groups,
+                                int gather, int K, int N, w4a16_dtype act, const int32_t* packed,
+                                const void* scales, const int32_t* qzeros, int group_size, int swiglu,
+                                void* out, w4a16_dtype out_dtype, void* stream) {
+  GemmArgs a{};
+  a.x = x; a.K = K; a.N = N;
+  a.packed = reinterpret_cast<const uint32_t*>(packed);
+  a.scales = scales;
+  a.qzeros = reinterpret_cast<const uint32_t*>(qzeros);
+  a.codebook = nullptr; a.nf4 = false; a.glu = swiglu != 0;
+  a.group_size = group_size;
+  a.out = out;
+  a.stream = static_cast<hipStream_t>(stream);
+  return grouped_common(a, plan, tokens, topk, groups, gather, act, out_dtype);
+}
+
+w4a16_status w4a16_gemm_grouped_nf4(const void* x, const int32_t* plan, int tokens, int topk, int groups,
+                                    int gather, int K, int N, w4a16_dtype act, const int32_t* packed,
+                                    const uint16_t* absmax, const uint16_t* codebook, int block_size,
+                                    int swiglu, void* out, w4a16_dtype out_dtype, void* stream) {
+  GemmArgs a{};
+  a.x = x; a.K = K; a.N = N;
+  a.packed = reinterpret_cast<const uint32_t*>(packed);
+  a.scales = absmax;
+  a.qzeros = nullptr;
+  a.codebook = codebook; a.nf4 = true; a.glu = swiglu != 0;
+  a.group_size = block_size;
+  a.out = out;
+  a.stream = static_cast<hipStream_t>(stream);
+  return grouped_common(a, plan, tokens, topk, groups, gather, act, out_dtype);
+}
+
+const char* w4a16_grouped_kernel_name(int S, int K, int N, int groups, int group_size) {
+  if (S <= 0 || groups <= 0 || groups > w4a16::kMaxGroups || check_shape(K, N, group_size) != W4A16_OK) return "none";
+  return w4a16::grouped_name(S, K, N, groups, group_size);
+}
+
+static w4a16_status check_lora(int M, int K, int N, int adapters, int rank) {
+  if (M < 0 || K <= 0 || N <= 0 || adapters <= 0 || rank <= 0) return W4A16_ERR_ARG;
+  if (K % 8 || N % 8) return W4A16_ERR_ARG;
+  if (K % 32 || N % 16 || rank % 8 || rank > w4a16::kMaxRank) return W4A16_ERR_UNSUPPORTED;
+  if (adapters > w4a16::kMaxGroups || M > w4a16::kMaxSlots || N > (1 << 23)) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+size_t w4a16_lora_workspace_bytes(int M, int K, int N, int adapters, int rank, int planned) {
+  if (check_lora(M, K, N, adapters, rank) != W4A16_OK || M == 0) return 0;
+  return w4a16::lora_workspace_bytes(M, K, N, adapters, rank, planned != 0);
+}
+
+w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w4a16_dtype act,
+                            w4a16_dtype y_dtype, const void* lora_a, const void* lora_b, int adapters,
+                            int rank, const int32_t* ids, const float* scaling, const int32_t* plan,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const w4a16_status st = check_lora(M, K, N, adapters, rank);
+  if (st != W4A16_OK) return st;
+  if (act != W4A16_F16 && act != W4A16_BF16) return W4A16_ERR_ARG;
+  if (y_dtype != act && y_dtype != W4A16_F32) return W4A16_ERR_ARG;
+  if (M == 0) return W4A16_OK;
+  if (!x || !y || !lora_a || !lora_b || !scaling || !out || (!plan && !ids)) return W4A16_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(out, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16))
+    return W4A16_ERR_ARG;
+  if (!aligned(scaling, 4) || (plan ? !aligned(plan, 256) : !aligned(ids, 4))) return W4A16_ERR_ARG;
+  const size_t need = w4a16::lora_workspace_bytes(M, K, N, adapters, rank, plan != nullptr);
+  if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  w4a16::LoraArgs a{};
+  a.x = x; a.y = y; a.lora_a = lora_a; a.lora_b = lora_b;
+  a.ids = ids; a.scaling = scaling; a.plan = plan;
+  a.out = out;
+  a.M = M; a.K = K; a.N = N; a.L = adapters; a.R = rank;
+  a.act = act == W4A16_F16 ? w4a16::ACT_F16 : w4a16::ACT_BF16;
+  a.ydtype = (int)y_dtype;
+  a.workspace = workspace;
+  a.stream = static_cast<hipStream_t>(stream);
+  return from_hip(w4a16::launch_lora(a));
 }
 
 w4a16_status w4a16_read_probe(const void* buf, size_t bytes, uint32_t* sink, void* stream) {

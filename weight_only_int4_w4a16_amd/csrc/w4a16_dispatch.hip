@@ -1,0 +1,359 @@
+// w4a16_dispatch.hip - rows moved into sorted order and back, with their gradients, by the plan
+// of w4a16_route.
+//
+//   dispatch            xs[p] = x[order[p] / topk]                       (0 past the last group)
+//   combine             y[t]  = sum_j w[t][j] ys[slot[t][j]]             (fp32, j ascending)
+//   combine, w == 1     dx[t] = sum_j dxs[slot[t][j]]                    (dispatch's gradient)
+//   combine_backward    dys[slot[t][j]] = w[t][j] dy[t],  dw[t][j] = <dy[t], ys[slot[t][j]]>
+//
+// A slot of no group adds nothing, whatever its weight and row hold. All are bound by HBM: every
+// kernel goes over the tokens, so that a token's own row is read or written once and its topk
+// sorted rows once each; no row is read twice and nothing is added with atomics. A wave takes 2 KiB
+// of a token's row (two 16-byte accesses per lane and sorted row), so the slots and weights of
+// its token are wave-uniform. Rows of a width that is no multiple of 16 bytes start at any
+// element: the vectors are declared with the element's alignment, which global accesses of
+// this GPU take as they are.
+#include "w4a16_device.hpp"
+#include "w4a16_routed.hpp"
+
+namespace w4a16 {
+
+namespace {
+
+enum { T_F16 = 0, T_BF16 = 1, T_F32 = 2 };
+
+typedef u4_t u4_any_t __attribute__((aligned(2)));  // sixteen bytes at any element's address
+
+template <int T>
+struct Elem {
+  typedef uint16_t raw;
+  static constexpr int kVec = 8;  // elements in 16 bytes
+};
+template <>
+struct Elem<T_F32> {
+  typedef uint32_t raw;
+  static constexpr int kVec = 4;
+};
+
+template <int T>
+__device__ __forceinline__ float elem_value(typename Elem<T>::raw b) {
+  if constexpr (T == T_F16) return (float)__builtin_bit_cast(_Float16, b);
+  if constexpr (T == T_BF16) return __builtin_bit_cast(float, (uint32_t)b << 16);
+  if constexpr (T == T_F32) return __builtin_bit_cast(float, b);
+}
+template <int T>
+__device__ __forceinline__ typename Elem<T>::raw elem_bits(float v) {  // one rounding, to nearest even
+  if constexpr (T == T_F16) return __builtin_bit_cast(uint16_t, (_Float16)v);
+  if constexpr (T == T_BF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  if constexpr (T == T_F32) return __builtin_bit_cast(uint32_t, v);
+}
+
+// element i of a loaded vector
+template <int T>
+__device__ __forceinline__ float vec_value(u4_t v, int i) {
+  if constexpr (T == T_F32)
+    return elem_value<T>(v[i]);
+  else
+    return elem_value<T>((uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+}
+template <int T>
+__device__ __forceinline__ u4_t vec_pack(const float* f) {
+  u4_t v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (T == T_F32)
+      v[i] = elem_bits<T>(f[i]);
+    else
+      v[i] = (uint32_t)elem_bits<T>(f[2 * i]) | (uint32_t)elem_bits<T>(f[2 * i + 1]) << 16;
+  }
+  return v;
+}
+
+// Vector c of a row of `width` elements; past its last whole vector the elements that are left
+// and zeros. Rows shorter than the vector index load nothing.
+template <int T>
+__device__ __forceinline__ u4_t load_vec(const typename Elem<T>::raw* row, int c, int width) {
+  constexpr int V = Elem<T>::kVec;
+  const int left = width - c * V;
+  if (left >= V) return *reinterpret_cast<const u4_any_t*>(row + c * V);
+  u4_t v = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < V - 1; ++i) {
+    if (i >= left) continue;
+    if constexpr (T == T_F32)
+      v[i] = row[c * V + i];
+    else
+      v[i >> 1] |= (uint32_t)row[c * V + i] << (16 * (i & 1));
+  }
+  return v;
+}
+template <int T>
+__device__ __forceinline__ void store_vec(typename Elem<T>::raw* row, int c, int width, u4_t v) {
+  constexpr int V = Elem<T>::kVec;
+  const int left = width - c * V;
+  if (left >= V) {
+    *reinterpret_cast<u4_any_t*>(row + c * V) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V - 1; ++i) {
+    if (i >= left) continue;
+    if constexpr (T == T_F32)
+      row[c * V + i] = v[i];
+    else
+      row[c * V + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+constexpr int kRowWaves = 4;     // waves per workgroup, each with an item of its own
+constexpr int kRowVecs = 2;      // vectors per lane and row: 2 KiB of a row per item
+constexpr int kTailWaves = 512;  // waves that clear the rows past the last group
+
+struct RowParams {
+  const void *x, *ys;
+  void* out;
+  const float* weights;
+  float* dweights;
+  const int32_t* plan;
+  int S, E, topk, order, slot;
+  int tokens, width;
+  int segs;        // items per token
+  int tail_waves;  // waves after the items
+};
+
+// rows [offsets[E], S) of `rows` cleared by waves w, w + waves, ...
+template <int T>
+__device__ __forceinline__ void clear_tail(const RowParams& p, void* rows, int w, int waves, int lane) {
+  const int vecs = (p.width + Elem<T>::kVec - 1) / Elem<T>::kVec;
+  for (int row = p.plan[p.E] + w; row < p.S; row += waves)
+    for (int c = lane; c < vecs; c += 64)
+      store_vec<T>(static_cast<typename Elem<T>::raw*>(rows) + (size_t)row * p.width, c, p.width, u4_t{0, 0, 0, 0});
+}
+
+template <int T>
+__global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(RowParams p) {
+  typedef typename Elem<T>::raw raw;
+  const int lane = threadIdx.x & 63;
+  const int item = __builtin_amdgcn_readfirstlane(blockIdx.x * kRowWaves + (threadIdx.x >> 6));
+  const int items = p.tokens * p.segs;
+  if (item >= items) {
+    if (item < items + p.tail_waves) clear_tail<T>(p, p.out, item - items, p.tail_waves, lane);
+    return;
+  }
+  const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * kRowVecs + lane;
+  const raw* src = static_cast<const raw*>(p.x) + (size_t)t * p.width;
+  u4_t v[kRowVecs];
+#pragma unroll
+  for (int u = 0; u < kRowVecs; ++u) v[u] = load_vec<T>(src, c0 + 64 * u, p.width);
+  const int32_t* slot = p.plan + p.slot + (size_t)t * p.topk;
+  for (int j = 0; j < p.topk; ++j) {
+    const int row = slot[j];
+    if (row < 0) continue;
+    raw* dst = static_cast<raw*>(p.out) + (size_t)row * p.width;
+#pragma unroll
+    for (int u = 0; u < kRowVecs; ++u) store_vec<T>(dst, c0 + 64 * u, p.width, v[u]);
+  }
+}
+
+template <int T, int TO>
+__global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
+  typedef typename Elem<T>::raw raw;
+  constexpr int V = Elem<T>::kVec, J = 4;  // sorted rows in flight
+  const int lane = threadIdx.x & 63;
+  const int item = __builtin_amdgcn_readfirstlane(blockIdx.x * kRowWaves + (threadIdx.x >> 6));
+  if (item >= p.tokens * p.segs) return;
+  const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * kRowVecs + lane;
+  const int32_t* slot = p.plan + p.slot + (size_t)t * p.topk;
+  const float* weight = p.weights ? p.weights + (size_t)t * p.topk : nullptr;
+  float acc[kRowVecs][V];
+#pragma unroll
+  for (int u = 0; u < kRowVecs; ++u)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+  for (int j0 = 0; j0 < p.topk; j0 += J) {
+    u4_t v[J][kRowVecs];
+    int row[J];
+    float w[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      row[j] = j0 + j < p.topk ? slot[j0 + j] : -1;
+      w[j] = row[j] >= 0 && weight ? weight[j0 + j] : 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (row[j] < 0) continue;
+      const raw* src = static_cast<const raw*>(p.ys) + (size_t)row[j] * p.width;
+#pragma unroll
+      for (int u = 0; u < kRowVecs; ++u) v[j][u] = load_vec<T>(src, c0 + 64 * u, p.width);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (row[j] < 0) continue;
+#pragma unroll
+      for (int u = 0; u < kRowVecs; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = __builtin_fmaf(w[j], vec_value<T>(v[j][u], i), acc[u][i]);
+    }
+  }
+  typedef typename Elem<TO>::raw out_raw;
+  out_raw* dst = static_cast<out_raw*>(p.out) + (size_t)t * p.width;
+#pragma unroll
+  for (int u = 0; u < kRowVecs; ++u) {
+    if constexpr (Elem<TO>::kVec == V) {
+      store_vec<TO>(dst, c0 + 64 * u, p.width, vec_pack<TO>(acc[u]));
+    } else {  // fp32 rows to 16-bit tokens: a lane's four elements are half a vector
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if ((c0 + 64 * u) * V + i < p.width) dst[(c0 + 64 * u) * V + i] = elem_bits<TO>(acc[u][i]);
+    }
+  }
+}
+
+// One workgroup per token (its waves share the row): the products of dy with the token's sorted
+// rows are summed per lane, then over the lanes and waves in a fixed order.
+template <int T, int J>
+__global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowParams p) {
+  typedef typename Elem<T>::raw raw;
+  constexpr int V = Elem<T>::kVec;
+  __shared__ float part[kRowWaves][J];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x;
+  if (t >= p.tokens) {  // the workgroups after the tokens'
+    clear_tail<T>(p, p.out, (t - p.tokens) * kRowWaves + wave, p.tail_waves, lane);
+    return;
+  }
+  const int vecs = (p.width + V - 1) / V;
+  const raw* dy = static_cast<const raw*>(p.x) + (size_t)t * p.width;
+  for (int j0 = 0; j0 < p.topk; j0 += J) {
+    int row[J];
+    float w[J], acc[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const size_t at = (size_t)t * p.topk + j0 + j;
+      row[j] = j0 + j < p.topk ? p.plan[p.slot + at] : -1;
+      w[j] = row[j] >= 0 ? p.weights[at] : 0.f;
+      acc[j] = 0.f;
+    }
+    for (int c = threadIdx.x; c < vecs; c += 64 * kRowWaves) {
+      const u4_t d = load_vec<T>(dy, c, p.width);
+      u4_t v[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (row[j] >= 0) v[j] = load_vec<T>(static_cast<const raw*>(p.ys) + (size_t)row[j] * p.width, c, p.width);
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = vec_value<T>(d, i);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (row[j] < 0) continue;
+        float g[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          acc[j] = __builtin_fmaf(f[i], vec_value<T>(v[j], i), acc[j]);
+          g[i] = w[j] * f[i];
+        }
+        store_vec<T>(static_cast<raw*>(p.out) + (size_t)row[j] * p.width, c, p.width, vec_pack<T>(g));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) acc[j] += __shfl_xor(acc[j], o);
+    if (j0) __syncthreads();  // the sums of the choices before have been read
+    if (lane == 0)
+#pragma unroll
+      for (int j = 0; j < J; ++j) part[wave][j] = acc[j];
+    __syncthreads();
+    if (threadIdx.x < J && j0 + threadIdx.x < p.topk) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRowWaves; ++i) s += part[i][threadIdx.x];
+      p.dweights[(size_t)t * p.topk + j0 + threadIdx.x] = s;
+    }
+  }
+}
+
+RowParams row_params(const RouteLayout& r, const int32_t* plan, int width, int vec) {
+  RowParams p = {};
+  p.plan = plan;
+  p.S = r.S;
+  p.E = r.E;
+  p.topk = r.topk;
+  p.order = r.order;
+  p.slot = r.slot;
+  p.tokens = r.S / r.topk;
+  p.width = width;
+  p.segs = ceil_div(width, 64 * kRowVecs * vec);
+  p.tail_waves = r.S < kTailWaves ? r.S : kTailWaves;
+  return p;
+}
+
+}  // namespace
+
+hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* plan, int width, int dtype,
+                           void* xs, hipStream_t s) {
+  RowParams p = row_params(r, plan, width, dtype == T_F32 ? 4 : 8);
+  p.x = x;
+  p.out = xs;
+  const dim3 grid(ceil_div(p.tokens * p.segs + p.tail_waves, kRowWaves)), block(64 * kRowWaves);
+  if (dtype == T_F32)
+    hipLaunchKernelGGL((dispatch_kernel<T_F32>), grid, block, 0, s, p);
+  else  // a copy: the 16-bit types are alike
+    hipLaunchKernelGGL((dispatch_kernel<T_F16>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* plan, const float* weights,
+                          int width, int dtype, void* y, int out_dtype, hipStream_t s) {
+  RowParams p = row_params(r, plan, width, dtype == T_F32 ? 4 : 8);
+  p.ys = ys;
+  p.weights = weights;
+  p.out = y;
+  const dim3 grid(ceil_div(p.tokens * p.segs, kRowWaves)), block(64 * kRowWaves);
+  if (dtype == T_F16)
+    hipLaunchKernelGGL((combine_kernel<T_F16, T_F16>), grid, block, 0, s, p);
+  else if (dtype == T_BF16)
+    hipLaunchKernelGGL((combine_kernel<T_BF16, T_BF16>), grid, block, 0, s, p);
+  else if (out_dtype == T_F32)
+    hipLaunchKernelGGL((combine_kernel<T_F32, T_F32>), grid, block, 0, s, p);
+  else if (out_dtype == T_F16)
+    hipLaunchKernelGGL((combine_kernel<T_F32, T_F16>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_kernel<T_F32, T_BF16>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+template <int T>
+static void launch_backward(const RowParams& p, hipStream_t s) {
+  const dim3 grid(p.tokens + ceil_div(p.tail_waves, kRowWaves)), block(64 * kRowWaves);
+  if (p.topk == 1)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 1>), grid, block, 0, s, p);
+  else if (p.topk == 2)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 2>), grid, block, 0, s, p);
+  else if (p.topk <= 4)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 4>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_backward_kernel<T, 8>), grid, block, 0, s, p);
+}
+
+hipError_t launch_combine_backward(const void* dy, const void* ys, const RouteLayout& r, const int32_t* plan,
+                                   const float* weights, int width, int dtype, void* dys, float* dweights,
+                                   hipStream_t s) {
+  RowParams p = row_params(r, plan, width, dtype == T_F32 ? 4 : 8);
+  p.x = dy;
+  p.ys = ys;
+  p.weights = weights;
+  p.out = dys;
+  p.dweights = dweights;
+  p.tail_waves = round64(p.tail_waves);  // whole workgroups
+  if (dtype == T_F16)
+    launch_backward<T_F16>(p, s);
+  else if (dtype == T_BF16)
+    launch_backward<T_BF16>(p, s);
+  else
+    launch_backward<T_F32>(p, s);
+  return hipGetLastError();
+}
+
+}  // namespace w4a16

@@ -1,0 +1,78 @@
+// w4a16_routed.hpp - internal launchers of the routed operators (rows of one batch that go to
+// different weights), behind the C ABI.
+#pragma once
+
+#include "w4a16_launch.hpp"
+
+namespace w4a16 {
+
+// The plan w4a16_route writes, in int32 words from its start: offsets [E + 1], order [S],
+// slot [S], the tile lists, and (many slots) the per-block counts of the sort. S = tokens * topk.
+// Tile list j cuts every group's rows into tiles of kTileRows[j] rows: a count, three unused words, then (group,
+// first row) pairs; group E's tiles are the slots of no group.
+constexpr int kTileLists = 4;
+constexpr int kTileRows[kTileLists] = {16, 32, 64, 128};
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxSlots = 1 << 26;
+constexpr int kRouteWaves = 16;                       // waves of a sorting workgroup
+constexpr int kRouteBatches = 8;                      // 64-slot batches per wave
+constexpr int kRouteSlots = kRouteWaves * kRouteBatches * 64;  // slots per sorting workgroup
+inline int round64(int n) { return (n + 63) & ~63; }
+// most tiles list j can hold: full tiles, and one more for each group with rows
+inline int tile_bound(int S, int E, int j) { return S / kTileRows[j] + (E + 1 < S ? E + 1 : S); }
+struct RouteLayout {
+  int S, E, topk;
+  int order, slot, tiles[kTileLists], hist, words;  // word offsets; the total
+  int blocks;                                        // workgroups of the sort
+};
+inline RouteLayout route_layout(int tokens, int topk, int E) {
+  RouteLayout r;
+  r.S = tokens * topk;
+  r.E = E;
+  r.topk = topk;
+  r.blocks = r.S > 0 ? (r.S + kRouteSlots - 1) / kRouteSlots : 1;
+  r.order = round64(E + 1);
+  r.slot = r.order + round64(r.S);
+  int at = r.slot + round64(r.S);
+  for (int j = 0; j < kTileLists; ++j) {
+    r.tiles[j] = at;
+    at += round64(4 + 2 * tile_bound(r.S, E, j));
+  }
+  r.hist = at;
+  r.words = at + (r.blocks > 1 ? round64(r.blocks * (E + 1)) : 0);
+  return r;
+}
+hipError_t launch_route(const int32_t* ids, const RouteLayout& r, int32_t* plan, hipStream_t s);
+// types of rows: 0 fp16, 1 bf16, 2 fp32 (as w4a16_dtype)
+hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* plan, int width, int dtype,
+                           void* xs, hipStream_t s);
+// weights NULL: every weight is 1
+hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* plan, const float* weights,
+                          int width, int dtype, void* y, int out_dtype, hipStream_t s);
+hipError_t launch_combine_backward(const void* dy, const void* ys, const RouteLayout& r, const int32_t* plan,
+                                   const float* weights, int width, int dtype, void* dys, float* dweights,
+                                   hipStream_t s);
+// a.x: the rows of the tokens (gather) or of the sorted slots; a.M unused; a.packed, a.scales and
+// a.qzeros hold the groups' weights one after another
+hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t* plan, bool gather);
+// whether the rows and columns make a launch the kernels can index
+bool grouped_fits(const RouteLayout& r, int K, int N);
+const char* grouped_name(int S, int K, int N, int E, int group_size);
+constexpr int kMaxRank = 256;
+struct LoraArgs {
+  const void* x;       // act [M][K]
+  const void* y;       // ydtype [M][N]
+  const void* lora_a;  // act [L][R][K]
+  const void* lora_b;  // act [L][N][R]
+  const int32_t* ids;  // [M] (read where no plan is given)
+  const float* scaling;
+  const int32_t* plan;
+  void* out;           // ydtype [M][N]; may be y
+  int M, K, N, L, R, act, ydtype;
+  void* workspace;
+  hipStream_t stream;
+};
+size_t lora_workspace_bytes(int M, int K, int N, int L, int R, bool planned);
+hipError_t launch_lora(const LoraArgs& a);
+
+}  // namespace w4a16
