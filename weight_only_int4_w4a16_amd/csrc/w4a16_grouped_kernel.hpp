@@ -37,13 +37,9 @@ struct ActT<ACT_F16> { typedef h8_t type; };
 template <>
 struct ActT<ACT_BF16> { typedef b8_t type; };
 
-// What a kernel needs of the plan and of the groups' weights
 struct GroupedParams {
   const uint16_t* x;
-  const int32_t* plan;
-  int S, E, topk, order, tiles;  // tiles: word offset of the tile list used
-  int bound;                     // most entries of the list
-  int tokens;                    // rows of x where rows are gathered, else 0
+  GroupTiles groups;
   int K, N;
   const u4_t* packed;
   const uint16_t* scales;
@@ -52,7 +48,7 @@ struct GroupedParams {
   void* out;
   int out_dtype;
   int KC, NT, NG, half;
-  int slice;                     // k-blocks per wave
+  int slice;  // k-blocks per wave
   int col_tiles;
 };
 
@@ -92,21 +88,17 @@ __global__ __launch_bounds__(64 * kMaxWaves) void grouped_kernel(GroupedParams p
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const int t = tile_of(blockIdx.x, p.bound * p.col_tiles);
-  const int tn = t / p.bound, ti = t - tn * p.bound;
-  const int32_t* const list = p.plan + p.tiles;
-  if (ti >= list[0]) return;
-  const int e = list[4 + 2 * ti], p0 = list[5 + 2 * ti];
-  const int rows = min(16, (e < p.E ? p.plan[e + 1] : p.S) - p0);
+  const int t = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
+  const int tn = t / p.groups.bound;
+  int e, p0, end;
+  if (!group_tile(p.groups, t - tn * p.groups.bound, e, p0, end)) return;
+  const int rows = min(16, end - p0);
   const int K = p.K, N = p.N, KC = p.KC;
   const int width = GLU ? N >> 1 : N;  // of an output row
   const int ocol0 = tn * OS * 16;
   const int ocols = min(OS * 16, width - ocol0);
-  if (e >= p.E) {  // the slots of no group: their rows are zeros
-    for (int i = threadIdx.x; i < rows * ocols; i += blockDim.x) {
-      const int r = i / ocols;
-      store_out(p.out, (size_t)(p0 + r) * width + ocol0 + (i - r * ocols), 0.f, p.out_dtype);
-    }
+  if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
+    zero_tile(p.out, p.out_dtype, p0, rows, width, ocol0, OS * 16);
     return;
   }
   if constexpr (FMT == FMT_NF4) {
@@ -130,9 +122,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void grouped_kernel(GroupedParams p
   const int arow = lane & 15;
   uint32_t aoff = kOutOfRange;
   if (arow < rows)
-    aoff = (uint32_t)(p.tokens ? p.plan[p.order + p0 + arow] / p.topk : arow) * (uint32_t)K * 2u + (lane >> 4) * 16u;
-  const __amdgpu_buffer_rsrc_t xrs = p.tokens ? make_rsrc(p.x, (uint32_t)p.tokens * (uint32_t)K * 2u)
-                                              : make_rsrc(p.x + (size_t)p0 * K, (uint32_t)rows * (uint32_t)K * 2u);
+    aoff = (uint32_t)(p.groups.tokens ? p.groups.plan[p.groups.order + p0 + arow] / p.groups.topk : arow) *
+               (uint32_t)K * 2u + (lane >> 4) * 16u;
+  const __amdgpu_buffer_rsrc_t xrs = p.groups.tokens
+      ? make_rsrc(p.x, (uint32_t)p.groups.tokens * (uint32_t)K * 2u)
+      : make_rsrc(p.x + (size_t)p0 * K, (uint32_t)rows * (uint32_t)K * 2u);
 
   struct Regs {
     u4_t b[SW], a[4];
@@ -209,7 +203,7 @@ struct GroupedGeometry {
 
 template <int ACT, int GPC, int FMT, int SW>
 hipError_t launch_sw(const GroupedParams& p, const GroupedGeometry& g, bool glu, hipStream_t s) {
-  const dim3 grid(p.bound * p.col_tiles), block(64 * g.waves);
+  const dim3 grid(p.groups.bound * p.col_tiles), block(64 * g.waves);
   const size_t lds = (size_t)g.waves * SW * 256 * 4;
   if (glu)
     hipLaunchKernelGGL((grouped_kernel<ACT, GPC, FMT, SW, true>), grid, block, lds, s, p);

@@ -42,6 +42,25 @@ inline RouteLayout route_layout(int tokens, int topk, int E) {
   r.words = at + (r.blocks > 1 ? round64(r.blocks * (E + 1)) : 0);
   return r;
 }
+
+// What a GEMM kernel's grouped instantiation reads besides its GEMM parameters
+struct GroupTiles {
+  const int32_t* plan;
+  int S, E, topk;
+  int order, list;  // word offsets in the plan: the sorted slots, the tile list used
+  int bound;        // most tiles the list can hold (the grid's)
+  int tokens;       // rows of x where they are gathered through the plan, else 0
+};
+// tile ti of a list: its group e and sorted rows [p0, end); false past the list's end
+__device__ __forceinline__ bool group_tile(const GroupTiles& g, int ti, int& e, int& p0, int& end) {
+  const int32_t* const list = g.plan + g.list;
+  if (ti >= list[0]) return false;
+  e = list[4 + 2 * ti];
+  p0 = list[5 + 2 * ti];
+  end = e < g.E ? g.plan[e + 1] : g.S;
+  return true;
+}
+
 hipError_t launch_route(const int32_t* ids, const RouteLayout& r, int32_t* plan, hipStream_t s);
 // types of rows: 0 fp16, 1 bf16, 2 fp32 (as w4a16_dtype)
 hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* plan, int width, int dtype,
@@ -56,9 +75,12 @@ hipError_t launch_combine_backward(const void* dy, const void* ys, const RouteLa
 // a.qzeros hold the groups' weights one after another
 hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t* plan, bool gather);
 // whether the rows and columns make a launch the kernels can index
-bool grouped_fits(const RouteLayout& r, int K, int N);
+bool grouped_fits(const RouteLayout& r, int N);
 const char* grouped_name(int S, int K, int N, int E, int group_size);
 constexpr int kMaxRank = 256;
+// its launches on the skinny kernel (tiles of 32 or 64 rows) and on the batched kernel (128)
+hipError_t launch_grouped_skinny(const GemmArgs& a, const GroupTiles& t, int rows);
+hipError_t launch_grouped_large(const GemmArgs& a, const GroupTiles& t);
 struct LoraArgs {
   const void* x;       // act [M][K]
   const void* y;       // ydtype [M][N]

@@ -49,7 +49,7 @@
 #include <type_traits>
 
 #include "w4a16_device.hpp"
-#include "w4a16_launch.hpp"
+#include "w4a16_routed.hpp"
 
 namespace w4a16 {
 namespace tiled {
@@ -123,6 +123,13 @@ struct TiledParams {
   int half;            // GLU: strips per half of the fused gate+up weight (NT / 2)
 };
 
+// Grouped: the rows are sorted by group and each group multiplies with its own weight. The row
+// tiles come from the plan's list, and x, packed, scales and qzeros hold what their group's
+// first elements are offset from; K is never split.
+struct GroupedTiledParams : TiledParams {
+  GroupTiles groups;
+};
+
 // workgroup -> output tile, so that tiles sharing weight columns run on the same XCD
 __device__ __forceinline__ int tile_of(int b, int G) {
   const int q = G >> 3, r = G & 7, x = b & 7;
@@ -153,8 +160,9 @@ __device__ __forceinline__ void wait_vmcnt() {
 // different bank groups. Each wave waits for its own copies of the block (vmcnt: only that
 // block's code and metadata loads were issued after them) and a barrier makes every wave's
 // copies visible; the same barrier frees the other slot, into which the next block loads.
-template <int ACT, int GPC, int FMT, class T, bool GLU>
-__global__ __launch_bounds__(T::kThreads) void tiled_kernel(TiledParams p) {
+template <int ACT, int GPC, int FMT, class T, bool GLU, class Params = TiledParams>
+__global__ __launch_bounds__(T::kThreads) void tiled_kernel(Params p) {
+  constexpr bool GROUPED = std::is_same<Params, GroupedTiledParams>::value;
   constexpr int kMT = T::kMT, kBM = T::kBM, kWaves = T::kWaves, kADma = T::kADma;
   constexpr int kPairs = T::kNP, kStrips = 2 * T::kNP, kStages = T::kStages, kKG = T::kKG;
   static_assert(kKG == 1 || kKG == 2, "k-groups differ by at most one block");
@@ -184,8 +192,20 @@ __global__ __launch_bounds__(T::kThreads) void tiled_kernel(TiledParams p) {
   const int t = tile_of(blockIdx.x, tiles);
   const int tm = t % p.tiles_m, tn = t / p.tiles_m;  // neighbours share weight columns
   const int z = blockIdx.y;
-  const int K = p.K, N = p.N, M = p.M, KC = p.KC;
-  const int m0 = tm * kBM;
+  const int K = p.K, N = p.N, KC = p.KC;
+  int M = p.M, m0 = tm * kBM;
+  if constexpr (GROUPED) {
+    int e;
+    if (!group_tile(p.groups, tm, e, m0, M)) return;
+    if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
+      const int width = GLU ? N >> 1 : N, cols = GLU ? T::kBN / 2 : T::kBN;
+      zero_tile(p.out, p.out_dtype, m0, min(M - m0, kBM), width, tn * cols, cols);
+      return;
+    }
+    p.packed += (size_t)e * p.NT * KC * 64;
+    p.scales += (size_t)e * p.NG * N;
+    if constexpr (ZEROS) p.qzeros += (size_t)e * p.NG * (N >> 3);
+  }
   // the workgroup's K slice [kc0, kc1), and this k-group's part of it [kb0, kb0 + nbg): the
   // groups take ceil(n / kKG) contiguous blocks each, the last possibly one fewer (or none)
   const int kc0 = z * p.kps;
@@ -208,13 +228,25 @@ __global__ __launch_bounds__(T::kThreads) void tiled_kernel(TiledParams p) {
   // past a ragged K, in the last block only, read out of range and land as zeros, so they
   // add nothing to the sums). Offsets are bytes from the tile's first row.
   const int tile_rows = min(kBM, M - m0);
-  const __amdgpu_buffer_rsrc_t xrs = make_rsrc(p.x + (size_t)m0 * K, (uint32_t)tile_rows * K * 2);
+  const uint16_t* xbase = p.x + (size_t)m0 * K;
+  uint32_t xbytes = (uint32_t)tile_rows * K * 2;
+  if constexpr (GROUPED) {
+    if (p.groups.tokens) {  // rows read in place: the row of sorted row r is order[r] / topk
+      xbase = p.x;
+      xbytes = (uint32_t)p.groups.tokens * (uint32_t)K * 2u;
+    }
+  }
+  const __amdgpu_buffer_rsrc_t xrs = make_rsrc(xbase, xbytes);
   uint32_t aoff[kADma];
 #pragma unroll
   for (int j = 0; j < kADma; ++j) {
     const int row = 4 * (wave * kADma + j) + (lane >> 4);
     const int chunk = (lane & 15) ^ (row & 15);
-    aoff[j] = (uint32_t)(min(row, tile_rows - 1) * K + chunk * 8) * 2;
+    int src = min(row, tile_rows - 1);
+    if constexpr (GROUPED) {
+      if (p.groups.tokens) src = p.groups.plan[p.groups.order + m0 + src] / p.groups.topk;
+    }
+    aoff[j] = ((uint32_t)src * (uint32_t)K + chunk * 8) * 2;
   }
   // RAGGED (K not a multiple of 128) is decided once per launch, outside the K loop: a
   // branch around the copies inside the loop would make the compiler lose count of the loads
@@ -606,7 +638,43 @@ hipError_t launch_act(const GemmArgs& a, const TiledParams& p, dim3 grid) {
 }
 
 
+// the grouped launches (grid: groups.bound * tiles_n workgroups)
+template <int ACT, int GPC, class T, bool GLU>
+hipError_t launch_grouped_glu(const GemmArgs& a, const GroupedTiledParams& p, dim3 grid) {
+  if (a.nf4)
+    hipLaunchKernelGGL((tiled_kernel<ACT, GPC, FMT_NF4, T, GLU, GroupedTiledParams>), grid, dim3(T::kThreads),
+                       T::kLdsBytes + kNf4PairEntries * 4, a.stream, p);
+  else if (a.qzeros)
+    hipLaunchKernelGGL((tiled_kernel<ACT, GPC, FMT_ASYM, T, GLU, GroupedTiledParams>), grid, dim3(T::kThreads), T::kLdsBytes, a.stream, p);
+  else
+    hipLaunchKernelGGL((tiled_kernel<ACT, GPC, FMT_SYM, T, GLU, GroupedTiledParams>), grid, dim3(T::kThreads), T::kLdsBytes, a.stream, p);
+  return hipGetLastError();
+}
+
+template <int ACT, int GPC, class T>
+hipError_t launch_grouped_fmt(const GemmArgs& a, const GroupedTiledParams& p, dim3 grid) {
+  return a.glu ? launch_grouped_glu<ACT, GPC, T, true>(a, p, grid) : launch_grouped_glu<ACT, GPC, T, false>(a, p, grid);
+}
+
+template <int ACT, class T>
+hipError_t launch_grouped_gpc(const GemmArgs& a, const GroupedTiledParams& p, dim3 grid) {
+  switch (a.group_size) {
+    case 128: return launch_grouped_fmt<ACT, 1, T>(a, p, grid);
+    case 64: return launch_grouped_fmt<ACT, 2, T>(a, p, grid);
+    default: return launch_grouped_fmt<ACT, 4, T>(a, p, grid);
+  }
+}
+
+template <class T>
+hipError_t launch_grouped_act(const GemmArgs& a, const GroupedTiledParams& p, dim3 grid) {
+  return a.act == ACT_F16 ? launch_grouped_gpc<ACT_F16, T>(a, p, grid) : launch_grouped_gpc<ACT_BF16, T>(a, p, grid);
+}
+
 // one instantiation per tile shape, each in its own translation unit
+#define W4A16_TILED_EXTERN_GROUPED(T) \
+  extern template hipError_t launch_grouped_act<T>(const GemmArgs&, const GroupedTiledParams&, dim3);
+#define W4A16_TILED_INSTANTIATE_GROUPED(T) \
+  template hipError_t launch_grouped_act<T>(const GemmArgs&, const GroupedTiledParams&, dim3);
 #define W4A16_TILED_EXTERN(T) \
   extern template hipError_t launch_act<T>(const GemmArgs&, const TiledParams&, dim3);
 #define W4A16_TILED_INSTANTIATE(T) \
