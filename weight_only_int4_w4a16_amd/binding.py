@@ -208,6 +208,16 @@ def _stream(t):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
+def _raw_stream(device):
+    """The current stream's handle on ``device``, without the 2 us a stream object takes to make
+    (a small routed call takes 4 us in all)."""
+    torch = _torch()
+    try:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
 def packed_bytes(K: int, N: int) -> int:
     return int(lib().w4a16_packed_bytes(K, N))
 
@@ -473,85 +483,46 @@ def dequant_nf4(packed, absmax, codebook, K: int, block_size: int = 64, wdtype=N
 
 
 # ---- routed operators: rows of one batch that go to different weights ----
+#
+# Decode calls of these take a few microseconds on the GPU, as long as a launch takes on the
+# host, so their checks compare what is expected first and look for what is wrong only after that fails.
 
-class Routing:
-    """A batch's plan (:func:`route`): which sorted row each slot (token, choice) has.
-
-    ``offsets`` int32 ``[groups + 1]``: group ``e``'s sorted rows; ``order`` int32 ``[S]``: the
-    slot of each sorted row, the slots of no group last; ``slot`` int32 ``[tokens, topk]``: the
-    sorted row of each slot, -1 for a slot of no group (S = tokens * topk). They are views of
-    ``plan``, the buffer the kernels read, and are not to be written."""
-
-    __slots__ = ("plan", "tokens", "topk", "groups")
-
-    def __init__(self, plan, tokens: int, topk: int, groups: int):
-        self.plan, self.tokens, self.topk, self.groups = plan, tokens, topk, groups
-
-    @property
-    def rows(self) -> int:
-        return self.tokens * self.topk
-
-    def _at(self):
-        return -(-(self.groups + 1) // 64) * 64
-
-    @property
-    def offsets(self):
-        return self.plan[:self.groups + 1]
-
-    @property
-    def order(self):
-        return self.plan[self._at():self._at() + self.rows]
-
-    @property
-    def slot(self):
-        first = self._at() + -(-self.rows // 64) * 64
-        return self.plan[first:first + self.rows].view(self.tokens, self.topk)
+_dtypes = {}      # torch dtype -> w4a16_dtype
+_act_dtypes = ()  # what activations may be
 
 
-def route(ids, groups: int) -> Routing:
-    """Sort a batch's slots by group: ``ids`` int32 ``[tokens, topk]`` (or ``[tokens]``, one
-    choice each), a value outside ``[0, groups)`` being no group. The plan serves any number of the
-    calls below."""
+def _load_dtypes():
+    global _act_dtypes
     torch = _torch()
-    if ids is None or ids.dtype != torch.int32 or ids.dim() not in (1, 2):
-        _fail("ids must be an int32 tensor [tokens, topk] or [tokens]")
-    if not ids.is_contiguous():
-        _fail("ids must be contiguous")
-    tokens, topk = ids.shape[0], 1 if ids.dim() == 1 else ids.shape[1]
-    if topk < 1 or groups < 1:
-        _fail(f"topk={topk}, groups={groups}: both must be at least 1")
-    need = int(lib().w4a16_route_bytes(tokens, topk, groups))
-    if need == 0:
-        raise W4A16Error(f"unsupported routing: {tokens} x {topk} slots, {groups} groups", ERR_UNSUPPORTED)
-    plan = torch.empty(need // 4, dtype=torch.int32, device=ids.device)
-    st = lib().w4a16_route(_ptr(ids), tokens, topk, groups, _ptr(plan), need, _stream(ids))
-    _check(st, "w4a16_route")
-    return Routing(plan, tokens, topk, groups)
+    _act_dtypes = (torch.float16, torch.bfloat16)
+    _dtypes.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
 
 
-def _route_args(r):
-    return _ptr(r.plan), r.tokens, r.topk, r.groups
+def _need(t, name, shape, dtype, device):
+    """A contiguous ``t`` of this shape and dtype on ``device``; returns its address."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _expect(t, name, shape, (dtype,), device)
+    return t.data_ptr()
 
 
-def _expect_rows(t, name, rows, r, dtypes=None):
-    """A tensor of whole rows on the plan's device; returns its width."""
-    torch = _torch()
-    if not isinstance(r, Routing):
-        _fail("routing must be the result of route()")
+def _need_rows(t, name, rows):
+    """A contiguous 2-D tensor of ``rows`` rows of fp16, bf16 or fp32; returns its width and w4a16 dtype."""
+    if not _dtypes:
+        _load_dtypes()
     if t is None or t.dim() != 2:
         _fail(f"{name} must be a 2-D tensor")
-    if t.shape[1] < 1:
+    n, width = t.shape
+    dt = _dtypes.get(t.dtype)
+    if dt is None or n != rows or not t.is_contiguous():
+        _expect(t, name, (rows, width), tuple(_dtypes))
+    if width < 1:
         _fail(f"{name} has rows of no elements")
-    _expect(t, name, (rows, t.shape[1]), dtypes or (torch.float16, torch.bfloat16, torch.float32), r.plan.device)
-    return t.shape[1]
+    return width, dt
 
 
-def _out_rows(out, shape, dtype, like, name="out", avoid=()):
-    if out is None:
-        return _torch().empty(shape, dtype=dtype, device=like.device)
-    _expect(out, name, shape, (dtype,), like.device)
-    _apart(out, name, avoid)
-    return out
+def _need_device(device, what="tensors"):
+    if device.type != "cuda":
+        _fail(f"{what} must be contiguous device tensors")
 
 
 def _apart(out, name, others):
@@ -562,23 +533,108 @@ def _apart(out, name, others):
             _fail(f"{name} overlaps an input")
 
 
+class Routing:
+    """A batch's plan (:func:`route`): which sorted row each slot (token, choice) has.
+
+    ``offsets`` int32 ``[groups + 1]``: group ``e``'s sorted rows are ``offsets[e]`` to ``offsets[e + 1]``;
+    ``order`` int32 ``[rows]``: the slot of each sorted row, the slots of no group last; ``slot`` int32 ``[tokens,
+    topk]``: the sorted row of each slot, -1 for a slot of no group (``rows = tokens * topk``). They
+    are views of ``plan``, the buffer the kernels read, and are not to be written."""
+
+    __slots__ = ("plan", "tokens", "topk", "groups", "rows", "device", "_views")
+
+    def __init__(self, plan, tokens: int, topk: int, groups: int):
+        self.plan, self.tokens, self.topk, self.groups = plan, tokens, topk, groups
+        self.rows, self.device, self._views = tokens * topk, plan.device, None
+
+    def _split(self):
+        if self._views is None:
+            e, n = self.groups + 1, self.rows
+            e64, n64 = -e % 64, -n % 64
+            at = e + e64 + n + n64 + n
+            parts = self.plan.split_with_sizes((e, e64, n, n64, n, self.plan.numel() - at))
+            self._views = parts[0], parts[2], parts[4].view(self.tokens, self.topk)
+        return self._views
+
+    @property
+    def offsets(self):
+        return self._split()[0]
+
+    @property
+    def order(self):
+        return self._split()[1]
+
+    @property
+    def slot(self):
+        return self._split()[2]
+
+
+def _need_routing(routing):
+    if not isinstance(routing, Routing):
+        _fail("routing must be the result of route()")
+
+
+def route(ids, groups: int) -> Routing:
+    """Sort a batch's slots by group: ``ids`` int32 ``[tokens, topk]`` (or ``[tokens]``, one choice
+    each), a value outside ``[0, groups)`` being no group. The plan serves any number of the calls
+    below."""
+    torch = _torch()
+    if ids is None or ids.dtype is not torch.int32 or ids.dim() not in (1, 2):
+        _fail("ids must be an int32 tensor [tokens, topk] or [tokens]")
+    if not ids.is_contiguous():
+        _fail("ids must be contiguous")
+    device = ids.device
+    _need_device(device, "ids")
+    tokens, topk = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
+    if topk < 1 or groups < 1:
+        _fail(f"topk={topk}, groups={groups}: both must be at least 1")
+    L = lib()
+    need = L.w4a16_route_bytes(tokens, topk, groups)
+    if need == 0:
+        raise W4A16Error(f"unsupported routing: {tokens} x {topk} slots, {groups} groups", ERR_UNSUPPORTED)
+    plan = torch.empty(need // 4, dtype=torch.int32, device=device)
+    st = L.w4a16_route(ids.data_ptr(), tokens, topk, groups, plan.data_ptr(), need, _raw_stream(device))
+    if st:
+        _check(st, "w4a16_route")
+    return Routing(plan, tokens, topk, groups)
+
+
 def dispatch(x, routing: Routing, out=None):
-    """Tokens' rows into sorted order: ``xs[S, width]``, ``xs[p] = x[order[p] // topk]``, zeros in the
+    """Tokens' rows into sorted order: ``xs[rows, width]``, ``xs[p] = x[order[p] // topk]``, zeros in the
     rows of no group. ``x[tokens, width]`` fp16, bf16 or fp32, any width."""
-    width = _expect_rows(x, "x", routing.tokens if isinstance(routing, Routing) else 0, routing)
-    out = _out_rows(out, (routing.rows, width), x.dtype, x, avoid=(x,))
-    st = lib().w4a16_dispatch(_ptr(x), *_route_args(routing), width, _dt(x.dtype), _ptr(out), _stream(x))
-    _check(st, "w4a16_dispatch")
+    _need_routing(routing)
+    r = routing
+    width, dt = _need_rows(x, "x", r.tokens)
+    if x.device != r.device:
+        _fail(f"x is on {x.device}, expected {r.device}")
+    if out is None:
+        out = x.new_empty((r.rows, width))
+    else:
+        _need(out, "out", (r.rows, width), x.dtype, r.device)
+        _apart(out, "out", (x,))
+    st = lib().w4a16_dispatch(x.data_ptr(), r.plan.data_ptr(), r.tokens, r.topk, r.groups, width, dt, out.data_ptr(),
+                              _raw_stream(r.device))
+    if st:
+        _check(st, "w4a16_dispatch")
     return out
 
 
 def dispatch_backward(dxs, routing: Routing, out=None):
     """Gradient of :func:`dispatch`: ``dx[t] = sum_j dxs[slot[t, j]]``, summed in fp32."""
-    width = _expect_rows(dxs, "dxs", routing.rows if isinstance(routing, Routing) else 0, routing)
-    out = _out_rows(out, (routing.tokens, width), dxs.dtype, dxs, avoid=(dxs,))
-    st = lib().w4a16_dispatch_backward(_ptr(dxs), *_route_args(routing), width, _dt(dxs.dtype), _ptr(out),
-                                       _stream(dxs))
-    _check(st, "w4a16_dispatch_backward")
+    _need_routing(routing)
+    r = routing
+    width, dt = _need_rows(dxs, "dxs", r.rows)
+    if dxs.device != r.device:
+        _fail(f"dxs is on {dxs.device}, expected {r.device}")
+    if out is None:
+        out = dxs.new_empty((r.tokens, width))
+    else:
+        _need(out, "out", (r.tokens, width), dxs.dtype, r.device)
+        _apart(out, "out", (dxs,))
+    st = lib().w4a16_dispatch_backward(dxs.data_ptr(), r.plan.data_ptr(), r.tokens, r.topk, r.groups, width, dt,
+                                       out.data_ptr(), _raw_stream(r.device))
+    if st:
+        _check(st, "w4a16_dispatch_backward")
     return out
 
 
@@ -586,39 +642,51 @@ def combine(ys, routing: Routing, weights, out_dtype=None, out=None):
     """Sorted rows back to their tokens: ``y[t] = sum_j weights[t, j] * ys[slot[t, j]]`` in fp32,
     rounded once to ``ys``'s dtype (fp32 ``ys``: to any ``out_dtype``). ``weights`` fp32
     ``[tokens, topk]``; the weight of a slot of no group is not used."""
-    torch = _torch()
-    width = _expect_rows(ys, "ys", routing.rows if isinstance(routing, Routing) else 0, routing)
-    _expect(weights, "weights", (routing.tokens, routing.topk), (torch.float32,), ys.device)
+    _need_routing(routing)
+    torch, r = _torch(), routing
+    width, dt = _need_rows(ys, "ys", r.rows)
+    if ys.device != r.device:
+        _fail(f"ys is on {ys.device}, expected {r.device}")
+    w = _need(weights, "weights", (r.tokens, r.topk), torch.float32, r.device)
     if out_dtype is None:
         out_dtype = ys.dtype if out is None else out.dtype
-    if out_dtype != ys.dtype and (ys.dtype != torch.float32 or out_dtype not in (torch.float16, torch.bfloat16)):
+    if out_dtype is not ys.dtype and (dt != F32 or out_dtype not in _act_dtypes):
         _fail(f"out dtype {out_dtype} for {ys.dtype} rows")
-    out = _out_rows(out, (routing.tokens, width), out_dtype, ys, avoid=(ys, weights))
-    st = lib().w4a16_combine(_ptr(ys), *_route_args(routing), _ptr(weights), width, _dt(ys.dtype), _ptr(out),
-                             _dt(out_dtype), _stream(ys))
-    _check(st, "w4a16_combine")
+    if out is None:
+        out = ys.new_empty((r.tokens, width), dtype=out_dtype)
+    else:
+        _need(out, "out", (r.tokens, width), out_dtype, r.device)
+        _apart(out, "out", (ys, weights))
+    st = lib().w4a16_combine(ys.data_ptr(), r.plan.data_ptr(), r.tokens, r.topk, r.groups, w, width, dt,
+                             out.data_ptr(), _dtypes[out_dtype], _raw_stream(r.device))
+    if st:
+        _check(st, "w4a16_combine")
     return out
 
 
 def combine_backward(dy, ys, routing: Routing, weights):
     """Gradients of :func:`combine` for ``dy[tokens, width]`` in ``ys``'s dtype: ``(dys, dweights)``,
     ``dys[slot[t, j]] = weights[t, j] * dy[t]`` and the fp32 ``dweights[t, j] = <dy[t], ys[slot[t, j]]>``."""
-    torch = _torch()
-    width = _expect_rows(ys, "ys", routing.rows if isinstance(routing, Routing) else 0, routing)
-    _expect(dy, "dy", (routing.tokens, width), (ys.dtype,), ys.device)
-    _expect(weights, "weights", (routing.tokens, routing.topk), (torch.float32,), ys.device)
+    _need_routing(routing)
+    torch, r = _torch(), routing
+    width, dt = _need_rows(ys, "ys", r.rows)
+    if ys.device != r.device:
+        _fail(f"ys is on {ys.device}, expected {r.device}")
+    g = _need(dy, "dy", (r.tokens, width), ys.dtype, r.device)
+    w = _need(weights, "weights", (r.tokens, r.topk), torch.float32, r.device)
     dys = torch.empty_like(ys)
     dweights = torch.empty_like(weights)
-    st = lib().w4a16_combine_backward(_ptr(dy), _ptr(ys), *_route_args(routing), _ptr(weights), width,
-                                      _dt(ys.dtype), _ptr(dys), _ptr(dweights), _stream(ys))
-    _check(st, "w4a16_combine_backward")
+    st = lib().w4a16_combine_backward(g, ys.data_ptr(), r.plan.data_ptr(), r.tokens, r.topk, r.groups, w, width, dt,
+                                      dys.data_ptr(), dweights.data_ptr(), _raw_stream(r.device))
+    if st:
+        _check(st, "w4a16_combine_backward")
     return dys, dweights
 
 
 def pack_grouped(qweight):
     """Canonical ``qweight[groups, K/8, N]`` int32 -> the groups' device layouts, one after another."""
     torch = _torch()
-    if qweight.dtype != torch.int32 or qweight.dim() != 3 or not qweight.is_contiguous():
+    if qweight is None or qweight.dtype != torch.int32 or qweight.dim() != 3 or not qweight.is_contiguous():
         _fail("qweight must be a contiguous int32 tensor [groups, K/8, N]")
     K, N = qweight.shape[1] * 8, qweight.shape[2]
     nb = packed_bytes(K, N)
@@ -631,53 +699,61 @@ def pack_grouped(qweight):
 
 
 def _grouped(x, routing, packed, scales, tail, group_size, glu, gather, out_dtype, out, nf4):
-    torch = _torch()
-    if not isinstance(routing, Routing):
-        _fail("routing must be the result of route()")
+    _need_routing(routing)
+    torch, r = _torch(), routing
+    if not _dtypes:
+        _load_dtypes()
+    device = r.device
     rows, K = _expect_x(x)
-    want = routing.tokens if gather else routing.rows
+    want = r.tokens if gather else r.rows
     if rows != want:
         _fail(f"x has {rows} rows, expected {want} ({'tokens' if gather else 'sorted rows'})")
-    if x.device != routing.plan.device:
-        _fail(f"x is on {x.device}, the routing on {routing.plan.device}")
+    if x.device != device:
+        _fail(f"x is on {x.device}, expected {device}")
     if scales is None or scales.dim() != 3:
         _fail("scales must be a 3-D [groups, K/g, N] tensor")
-    E, N, G = routing.groups, scales.shape[2], _groups(K, group_size)
-    _expect(scales, "scales", (E, G, N), (torch.float16 if nf4 else x.dtype,), x.device)
+    E, N, G = r.groups, scales.shape[2], _groups(K, group_size)
+    sp = _need(scales, "scales", (E, G, N), torch.float16 if nf4 else x.dtype, device)
     if N % 8:
         _fail(f"N={N} is not a multiple of 8")
     if nf4:
-        _expect(tail, "codebook", (16,), (torch.float16,), x.device)
-    elif tail is not None:
-        _expect(tail, "qzeros", (E, G, N // 8), (torch.int32,), x.device)
-    need = packed_bytes(K, N)
+        tp = _need(tail, "codebook", (16,), torch.float16, device)
+    else:
+        tp = None if tail is None else _need(tail, "qzeros", (E, G, N // 8), torch.int32, device)
+    L = lib()
+    need = L.w4a16_packed_bytes(K, N)
     if need == 0:
         raise W4A16Error(f"unsupported shape K={K} N={N}", ERR_UNSUPPORTED)
-    _expect(packed, "packed", (E, need // 4), (torch.int32,), x.device)
+    pp = _need(packed, "packed", (E, need // 4), torch.int32, device)
     if glu and N % 2:
         _fail(f"N={N} must be even (gate and up halves)")
-    out = _out(out, routing.rows, N // 2 if glu else N, out_dtype, x)
-    _apart(out, "out", (x,))
-    f = lib().w4a16_gemm_grouped_nf4 if nf4 else lib().w4a16_gemm_grouped
-    st = f(_ptr(x), *_route_args(routing), int(gather), K, N, _dt(x.dtype), _ptr(packed), _ptr(scales), _ptr(tail),
-           group_size, int(glu), _ptr(out), _dt(out.dtype), _stream(x))
-    _check(st, "w4a16_gemm_grouped_nf4" if nf4 else "w4a16_gemm_grouped")
+    width = N // 2 if glu else N
+    if out is None and out_dtype is None:
+        out = x.new_empty((r.rows, width))
+    else:
+        out = _out(out, r.rows, width, out_dtype, x)
+        _apart(out, "out", (x,))
+    f = L.w4a16_gemm_grouped_nf4 if nf4 else L.w4a16_gemm_grouped
+    st = f(x.data_ptr(), r.plan.data_ptr(), r.tokens, r.topk, E, int(gather), K, N, _dtypes[x.dtype], pp, sp, tp,
+           group_size, int(glu), out.data_ptr(), _dtypes[out.dtype], _raw_stream(device))
+    if st:
+        _check(st, "w4a16_gemm_grouped_nf4" if nf4 else "w4a16_gemm_grouped")
     return out
 
 
 def gemm_grouped(x, routing: Routing, packed, scales, qzeros, group_size: int, gather: bool = False,
                  out_dtype=None, out=None):
-    """The experts' products: ``out[S, N]``, ``out[p] = row(p) @ W_hat[e]`` for group ``e``'s sorted rows,
-    zeros in the rows of no group. ``x[S, K]`` holds the sorted rows, or with ``gather`` the tokens' ``[tokens,
-    K]``, read through the plan. ``packed`` from :func:`pack_grouped`, ``scales[groups, K/g, N]`` in x's
-    dtype, ``qzeros[groups, K/g, N/8]`` int32 or None (symmetric)."""
+    """The experts' products: ``out[rows, N]``, ``out[p] = row(p) @ W_hat[e]`` for group ``e``'s sorted rows,
+    zeros in the rows of no group. ``x[rows, K]`` holds the sorted rows, or with ``gather`` the tokens'
+    ``[tokens, K]``, read through the plan. ``packed`` from :func:`pack_grouped`, ``scales[groups, K/g, N]`` in
+    x's dtype, ``qzeros[groups, K/g, N/8]`` int32 or None (symmetric)."""
     return _grouped(x, routing, packed, scales, qzeros, group_size, False, gather, out_dtype, out, False)
 
 
 def gemm_grouped_swiglu(x, routing: Routing, packed, scales, qzeros, group_size: int, gather: bool = False,
                         out_dtype=None, out=None):
     """:func:`gemm_grouped` of fused gate+up weights (gate columns first) with the SwiGLU epilogue:
-    ``h[S, N/2]``."""
+    ``h[rows, N/2]``."""
     return _grouped(x, routing, packed, scales, qzeros, group_size, True, gather, out_dtype, out, False)
 
 
@@ -703,48 +779,59 @@ def lora_workspace_bytes(M: int, K: int, N: int, adapters: int, rank: int, plann
 
 def lora_add(y, x, lora_a, lora_b, ids, scaling, routing: Routing | None = None, out=None, workspace=None):
     """Low-rank adapters of many requests beside a shared projection: ``out[m] = y[m] + scaling[a] *
-    (x[m] @ lora_a[a].T) @ lora_b[a].T`` with ``a = ids[m]``, ``out[m] = y[m]`` where ``a`` is outside ``[0, adapters)``.
+    (x[m] @ lora_a[a].T) @ lora_b[a].T`` with ``a = ids[m]``, ``out[m] = y[m]`` where ``a`` is outside
+    ``[0, adapters)``.
 
     ``y[M, N]`` the projection's output (x's dtype or fp32), ``x[M, K]`` fp16/bf16,
-    ``lora_a[adapters, rank, K]``, ``lora_b[adapters, N, rank]`` in x's dtype, ``ids`` int32 ``[M]``, ``scaling``
-    fp32 ``[adapters]``. ``routing``: ``route(ids, adapters)`` made once for the projections of a step that share
-    the ids. ``out`` may be ``y``. ``workspace``: optional, ``lora_workspace_bytes(...)``."""
+    ``lora_a[adapters, rank, K]``, ``lora_b[adapters, N, rank]`` in x's dtype, ``ids`` int32 ``[M]``,
+    ``scaling`` fp32 ``[adapters]``. ``routing``: ``route(ids, adapters)``, made once for the projections of a step
+    that share the ids. ``out`` may be ``y``. ``workspace``: optional, ``lora_workspace_bytes(...)``."""
     torch = _torch()
+    if not _dtypes:
+        _load_dtypes()
     M, K = _expect_x(x)
+    device, dtype = x.device, x.dtype
+    _need_device(device)
     if lora_a is None or lora_a.dim() != 3:
         _fail("lora_a must be a 3-D [adapters, rank, K] tensor")
-    adapters, rank = lora_a.shape[0], lora_a.shape[1]
-    _expect(lora_a, "lora_a", (adapters, rank, K), (x.dtype,), x.device)
+    adapters, rank, _ = lora_a.shape
+    ap = _need(lora_a, "lora_a", (adapters, rank, K), dtype, device)
     if y is None or y.dim() != 2:
         _fail("y must be a 2-D [M, N] tensor")
     N = y.shape[1]
-    _expect(y, "y", (M, N), (x.dtype, torch.float32), x.device)
-    _expect(lora_b, "lora_b", (adapters, N, rank), (x.dtype,), x.device)
-    _expect(scaling, "scaling", (adapters,), (torch.float32,), x.device)
+    if y.dtype is not dtype:
+        _expect(y, "y", (M, N), (dtype, torch.float32), device)
+    yp = _need(y, "y", (M, N), y.dtype, device)
+    bp = _need(lora_b, "lora_b", (adapters, N, rank), dtype, device)
+    sp = _need(scaling, "scaling", (adapters,), torch.float32, device)
     if routing is None:
-        _expect(ids, "ids", (M,), (torch.int32,), x.device)
-        plan = None
+        ip, plan = _need(ids, "ids", (M,), torch.int32, device), None
     else:
-        if not isinstance(routing, Routing) or (routing.tokens, routing.topk, routing.groups) != (M, 1, adapters):
+        _need_routing(routing)
+        if (routing.tokens, routing.topk, routing.groups) != (M, 1, adapters):
             _fail("routing must be route(ids, adapters) of these rows")
-        if routing.plan.device != x.device:
-            _fail(f"the routing is on {routing.plan.device}, expected {x.device}")
-        plan = routing.plan
+        if routing.device != device:
+            _fail(f"the routing is on {routing.device}, expected {device}")
+        ip, plan = None, routing.plan.data_ptr()
     if out is None:
         out = torch.empty_like(y)
     else:
-        _expect(out, "out", (M, N), (y.dtype,), x.device)
-        _apart(out, "out", (x,) if out.data_ptr() == y.data_ptr() else (x, y))
-    need = lora_workspace_bytes(M, K, N, adapters, rank, plan is not None)
+        _need(out, "out", (M, N), y.dtype, device)
+        _apart(out, "out", (x,) if out.data_ptr() == yp else (x, y))
+    L = lib()
+    need = L.w4a16_lora_workspace_bytes(M, K, N, adapters, rank, plan is not None)
     if workspace is None:
+        wp = None
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            wp = workspace.data_ptr()
     else:
-        _expect_workspace(workspace, need, x.device)
-    st = lib().w4a16_lora_add(_ptr(x), _ptr(y), M, K, N, _dt(x.dtype), _dt(y.dtype), _ptr(lora_a), _ptr(lora_b),
-                              adapters, rank, _ptr(ids) if plan is None else None, _ptr(scaling), _ptr(plan),
-                              _ptr(out), *_ws_args(workspace), _stream(x))
-    _check(st, "w4a16_lora_add")
+        _expect_workspace(workspace, need, device)
+        wp, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = L.w4a16_lora_add(x.data_ptr(), yp, M, K, N, _dtypes[dtype], _dtypes[y.dtype], ap, bp, adapters, rank, ip, sp,
+                          plan, out.data_ptr(), wp, need, _raw_stream(device))
+    if st:
+        _check(st, "w4a16_lora_add")
     return out
 
 

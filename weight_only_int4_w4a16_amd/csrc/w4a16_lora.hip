@@ -2,25 +2,33 @@
 //
 //   out[m] = y[m] + s[a] (x[m] A[a]^T) B[a]^T,  a = ids[m]   (out[m] = y[m] where a is none)
 //
-// with x[M][K], A[L][R][K], B[L][N][R] of the activation type and y the projection's output. Rows
-// are grouped by adapter (the plan of w4a16_route), so a tile of rows reads its adapter once;
-// at decode the adapters' bytes R (K + N) bound the call, at prefill those of x, y and out.
+// with x[M][K], A[L][R][K], B[L][N][R] of the activation type and y the projection's output.
+// A workgroup takes a tile of rows with one adapter, so at decode the adapters' bytes
+// R (K + N) bound the call, at prefill those of x, y and out.
+//
+// Tiles. Up to 256 rows, workgroup b looks at row b: if the row is the first, 17th, 33rd.. of
+// its adapter, the tile is that row and the next fifteen of the adapter, found with one
+// ballot per 64 ids; else it leaves. More rows (or a plan in hand) take the plan's tile lists.
 //
 // Two launches. The first forms t = x A^T, at most R values a row: a workgroup takes a tile of
-// rows and a slice of K, its waves parts of the slice, added through LDS in wave order; the slices' fp32 sums go
-// to the workspace. The second adds the slices in order and multiplies by B.
+// rows and a slice of K, its waves parts of the slice, added through LDS in wave order; the
+// slices' fp32 sums go to the workspace. The second adds the slices in order and multiplies
+// by B.
 //
 // t in 16-bit MFMA operands. Rounding t once would cost as much as rounding the product, so t
 // is split into parts of the activation type, t = t0 + t1 (+ t2), each the rounding of what
 // the ones before left: 22 (fp16), 16 or 24 (bf16, three parts where out is fp32) bits of t,
 // and the parts' products with B add in fp32. fp16 parts of a large or small t could leave
 // the type's range, so a row is first scaled by the power of two that brings its largest |t|
-// into [1, 2); the scale goes back into s.
+// into [1, 2); the scale goes back into s. A workgroup splits its rows' t once, in LDS, for all its columns.
 //
 // Operands of the second product. B is the A operand (16 columns n of the output) and t the B
-// operand (16 rows m), so a lane ends with consecutive n of one row: the four MFMAs of a
-// 64-column strip take the columns n0 + 16 (i/4) + 4 q + i%4, and lane l then holds all
-// sixteen of n0 + 16 (l/16) .. of row l%16, two 16-byte accesses to y and out.
+// operand (16 rows m), so a lane ends with consecutive n of one row. The MFMAs q = 0..3 of a
+// 64-column strip take the columns n0 + 32 (q/2) + 8 (i/4) + 4 (q%2) + i%4, i < 16: lane l then holds the eight of
+// n0 + 32 c + 8 (l/16) .. of row l%16 for c = 0, 1, and every access to y and out covers 64
+// contiguous bytes of a row.
+#include <type_traits>
+
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"
 
@@ -39,135 +47,229 @@ struct ActT<ACT_BF16> { typedef b8_t type; };
 
 constexpr int kShrinkWaves = 8;
 constexpr int kExpandWaves = 4;
-constexpr int kRankChunk = 64;  // ranks per workgroup of the first product
+constexpr int kRankChunk = 64;   // ranks per workgroup of the first product
 constexpr int kMaxSlices = 16;
+constexpr int kLogU(int MT) { return MT == 1 ? 2 : 1; }
+constexpr int kSetSteps(int MT) { return 1 << kLogU(MT); }
+constexpr int kSelfRows = 256;   // most rows whose tiles the workgroups find themselves
+constexpr int kTileMax = 64;     // most rows of a tile
 
 struct LoraParams {
   const uint16_t *x, *a, *b;
   const void* y;
   void* out;
   const float* scaling;
-  const int32_t* plan;
-  float* part;  // [slices][M][R]
-  int order, tiles, bound;
+  const int32_t* ids;  // where the tiles are found here, else NULL
+  GroupTiles groups;   // else
+  float* part;         // [slices][M][R], by row of x
   int M, K, N, L, R;
-  int slices, steps;  // K slices; 32-deep steps per wave
+  int slices, steps;   // K slices; 32-deep steps per slice
+  int tile_rows;
+  int strips;          // 64-column strips per wave of the second product
+  int col_groups;      // workgroups per tile of it
 };
 
-__device__ __forceinline__ int group_end(const LoraParams& p, int e) { return e < p.L ? p.plan[e + 1] : p.M; }
+// This workgroup's tile: the rows of x (in LDS, complete after the caller's barrier), their number
+// and their adapter (L: none). False if it has none.
+__device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* rows_of, int& rows, int& e) {
+  const int lane = threadIdx.x & 63;
+  if (p.ids) {
+    const int b = tile;
+    const uint32_t id = (uint32_t)p.ids[b];
+    e = id < (uint32_t)p.L ? (int)id : p.L;
+    uint64_t same[kSelfRows / 64];
+    int before = 0;  // rows of this adapter ahead of row b
+#pragma unroll
+    for (int c = 0; c < kSelfRows / 64; ++c) {
+      const int m = 64 * c + lane;
+      uint32_t other = 0;
+      if (m < p.M) other = (uint32_t)p.ids[m];
+      same[c] = __ballot(m < p.M && (other < (uint32_t)p.L ? (int)other : p.L) == e);
+      const int left = b - 64 * c;  // rows of this batch ahead of b
+      if (left > 0) before += __popcll(left >= 64 ? same[c] : same[c] & ((1ull << left) - 1));
+    }
+    if (before & 15) return false;
+    int at = 0;  // rows of the adapter seen
+#pragma unroll
+    for (int c = 0; c < kSelfRows / 64; ++c) {
+      const int pos = at + __popcll(same[c] & ((1ull << lane) - 1)) - before;
+      if (((same[c] >> lane) & 1) && pos >= 0 && pos < 16 && threadIdx.x < 64) rows_of[pos] = 64 * c + lane;
+      at += __popcll(same[c]);
+    }
+    rows = min(16, at - before);
+    return true;
+  }
+  int p0, end;
+  if (!group_tile(p.groups, tile, e, p0, end)) return false;
+  rows = min(p.tile_rows, end - p0);
+  if ((int)threadIdx.x < rows) rows_of[threadIdx.x] = p.groups.plan[p.groups.order + p0 + threadIdx.x];
+  return true;
+}
 
 // t of 16 MT rows and up to 16 RT ranks over one K slice
 template <int ACT, int MT, int RT>
 __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p) {
   typedef typename ActT<ACT>::type AT;
-  extern __shared__ __attribute__((aligned(16))) float red[];  // [waves][MT][RT][4][64]
+  extern __shared__ __attribute__((aligned(16))) float red[];  // [waves / 2][MT][RT][4][64]
+  __shared__ int rows_of[kTileMax];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t* const list = p.plan + p.tiles;
-  if ((int)blockIdx.x >= list[0]) return;
-  const int e = list[4 + 2 * blockIdx.x], p0 = list[5 + 2 * blockIdx.x];
+  // consecutive workgroups (on consecutive XCDs) take a tile's slices
+  const int tile = blockIdx.x / p.slices, slice = blockIdx.x - tile * p.slices;
+  int rows, e;
+  if (!find_tile(p, tile, rows_of, rows, e)) return;
   if (e >= p.L) return;  // rows without an adapter
-  const int rows = min(16 * MT, group_end(p, e) - p0);
-  const int r0 = blockIdx.z * kRankChunk;
+  const int r0 = blockIdx.y * kRankChunk;
   const int koff = 8 * (lane >> 4);
   const uint16_t *xp[MT], *ap[RT];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)  // rows past the tile repeat its last, never stored
-    xp[mt] = p.x + (size_t)p.plan[p.order + p0 + min(16 * mt + (lane & 15), rows - 1)] * p.K + koff;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)  // and so do ranks past the last
+  for (int rt = 0; rt < RT; ++rt)  // ranks past the last repeat it, never stored
     ap[rt] = p.a + ((size_t)e * p.R + min(r0 + 16 * rt + (lane & 15), p.R - 1)) * p.K + koff;
+  __syncthreads();
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)  // and so do rows past the tile
+    xp[mt] = p.x + (size_t)rows_of[min(16 * mt + (lane & 15), rows - 1)] * p.K + koff;
   f4_t acc[MT][RT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[mt][rt] = f4_t{0.f, 0.f, 0.f, 0.f};
-  const int s0 = (blockIdx.y * kShrinkWaves + wave) * p.steps;
-  const int s1 = min(s0 + p.steps, p.K / 32);
-  constexpr int U = MT == 1 ? 4 : 2;  // steps in flight
-  for (int s = s0; s < s1; s += U) {
-    u4_t xv[U][MT], av[U][RT];
+  constexpr int U = kSetSteps(MT);  // steps per register set; one set loads while the other multiplies
+  struct Regs {
+    u4_t x[U][MT], a[U][RT];
+  };
+  // The slice's sets go to the waves in turn, 512 bytes of a row at a time (less where a wave
+  // would get none). The rows of x and of A are K apart, at a power of two K all in one memory
+  // channel; with the eight waves 512 bytes apart their loads cover 4 KiB of each row, and so every channel.
+  const int s0 = slice * p.steps, s1 = min(s0 + p.steps, p.K / 32);
+  const int all = (s1 - s0 + U - 1) / U;
+  const int shift = all >= 8 * kShrinkWaves / U ? 3 - kLogU(MT) : all >= 2 * kShrinkWaves ? 1 : 0;
+  const int full = (all / kShrinkWaves) >> shift;
+  const int sets = (full << shift) + min(max(all - ((full * kShrinkWaves + wave) << shift), 0), 1 << shift);
+  auto first = [&](int i) __attribute__((always_inline)) {
+    return s0 + ((((i >> shift) * kShrinkWaves + wave) << shift) + (i & ((1 << shift) - 1))) * U;
+  };
+  auto load = [&](Regs& R, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = 32 * min(s + u, s1 - 1);
+      const int k = 32 * min(first(i) + u, s1 - 1);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) xv[u][mt] = *reinterpret_cast<const u4_t*>(xp[mt] + k);
+      for (int mt = 0; mt < MT; ++mt) R.x[u][mt] = *reinterpret_cast<const u4_t*>(xp[mt] + k);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) av[u][rt] = *reinterpret_cast<const u4_t*>(ap[rt] + k);
+      for (int rt = 0; rt < RT; ++rt) R.a[u][rt] = *reinterpret_cast<const u4_t*>(ap[rt] + k);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&](const Regs& R, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (s + u >= s1) break;
+      if (first(i) + u >= s1) break;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-          acc[mt][rt] = mfma16(__builtin_bit_cast(AT, xv[u][mt]), __builtin_bit_cast(AT, av[u][rt]), acc[mt][rt]);
+          acc[mt][rt] = mfma16(__builtin_bit_cast(AT, R.x[u][mt]), __builtin_bit_cast(AT, R.a[u][rt]), acc[mt][rt]);
+    }
+  };
+  if (sets > 0) {
+    Regs A, B;
+    load(A, 0);
+    int i = 0;
+    for (; i + 2 < sets; i += 2) {
+      load(B, i + 1);
+      multiply(A, i);
+      load(A, i + 2);
+      multiply(B, i + 1);
+    }
+    if (i + 1 < sets) {
+      load(B, i + 1);
+      multiply(A, i);
+      multiply(B, i + 1);
+    } else {
+      multiply(A, i);
     }
   }
-  // lane l holds rank l%16 and rows 4 (l/16) + i, i < 4
+  // The waves' sums, in two rounds through half the LDS that all would take (so that two workgroups
+  // share a compute unit): wave w + 4's go to wave w, then the four sums in order. Lane l holds
+  // rank l%16 and rows 4 (l/16) + i, i < 4.
+  constexpr int H = kShrinkWaves / 2, TILE = MT * RT * 256;
+  if (wave >= H) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[(((wave * MT + mt) * RT + rt) * 4 + i) * 64 + lane] = acc[mt][rt][i];
+        for (int i = 0; i < 4; ++i) red[(wave - H) * TILE + ((mt * RT + rt) * 4 + i) * 64 + lane] = acc[mt][rt][i];
+  }
   __syncthreads();
-  float* const part = p.part + ((size_t)blockIdx.y * p.M + p0) * p.R + r0;
+  if (wave < H) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float* const at = red + wave * TILE + ((mt * RT + rt) * 4 + i) * 64 + lane;
+          *at = acc[mt][rt][i] + *at;
+        }
+  }
+  __syncthreads();
   for (int q = threadIdx.x; q < rows * RT * 16; q += 64 * kShrinkWaves) {
     const int m = q / (RT * 16), r = q - m * (RT * 16);
     if (r0 + r >= p.R) continue;
     const int at = ((((m >> 4) * RT + (r >> 4)) * 4 + (m & 3)) * 64) + ((m >> 2) & 3) * 16 + (r & 15);
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kShrinkWaves; ++w) v += red[w * MT * RT * 256 + at];
-    part[(size_t)m * p.R + r] = v;
+    for (int w = 0; w < H; ++w) v += red[w * TILE + at];
+    p.part[((size_t)slice * p.M + rows_of[m]) * p.R + r0 + r] = v;
   }
 }
 
-// sixteen consecutive elements of a row of y or out
+// A lane's sixteen columns of a row: access h covers elements kPer h .. of them, at column
+// offset(h) of the strip
 template <int YT>
-__device__ __forceinline__ void load16(const void* base, size_t at, float (&f)[16]) {
-  if constexpr (YT == T_F32) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const f4_t v = *reinterpret_cast<const f4_t*>(static_cast<const float*>(base) + at + 4 * c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[4 * c + i] = v[i];
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const u4_t v = *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(base) + at + 8 * c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint16_t b = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-        f[8 * c + i] = YT == T_F16 ? (float)__builtin_bit_cast(_Float16, b) : __builtin_bit_cast(float, (uint32_t)b << 16);
-      }
-    }
+struct Cols {
+  static constexpr int kPer = YT == T_F32 ? 4 : 8, kAccesses = 16 / kPer;
+  static __device__ __forceinline__ int offset(int h, int g) {
+    return YT == T_F32 ? 32 * (h >> 1) + 8 * g + 4 * (h & 1) : 32 * h + 8 * g;
   }
+};
+template <int YT>
+__device__ __forceinline__ u4_t load_cols(const void* base, size_t at) {
+  if constexpr (YT == T_F32) return *reinterpret_cast<const u4_t*>(static_cast<const float*>(base) + at);
+  return *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(base) + at);
 }
 template <int YT>
-__device__ __forceinline__ void store16(void* base, size_t at, const float (&f)[16]) {
-  if constexpr (YT == T_F32) {
+__device__ __forceinline__ void store_cols(void* base, size_t at, u4_t v) {
+  if constexpr (YT == T_F32)
+    *reinterpret_cast<u4_t*>(static_cast<float*>(base) + at) = v;
+  else
+    *reinterpret_cast<u4_t*>(static_cast<uint16_t*>(base) + at) = v;
+}
+// v + back * acc for the elements of access h, rounded once to the type
+template <int YT>
+__device__ __forceinline__ u4_t add_cols(u4_t v, const f4_t* acc, float back) {
+  u4_t r;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<f4_t*>(static_cast<float*>(base) + at + 4 * c) = f4_t{f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]};
-  } else {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      u4_t v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = f[8 * c + 2 * i], hi = f[8 * c + 2 * i + 1];
-        if constexpr (YT == T_F16)
-          v[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
-        else
-          v[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (YT == T_F32) {
+      const uint32_t bits = v[i];  // a vector's element is no object of its own to a bit cast
+      const float sum = __builtin_fmaf(back, acc[0][i], __builtin_bit_cast(float, bits));
+      r[i] = __builtin_bit_cast(uint32_t, sum);
+    } else {
+      const float a0 = acc[i >> 1][2 * (i & 1)], a1 = acc[i >> 1][2 * (i & 1) + 1];
+      if constexpr (YT == T_F16) {
+        const float lo = __builtin_fmaf(back, a0, (float)__builtin_bit_cast(_Float16, (uint16_t)v[i]));
+        const float hi = __builtin_fmaf(back, a1, (float)__builtin_bit_cast(_Float16, (uint16_t)(v[i] >> 16)));
+        r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+      } else {
+        const float lo = __builtin_fmaf(back, a0, __builtin_bit_cast(float, v[i] << 16));
+        const float hi = __builtin_fmaf(back, a1, __builtin_bit_cast(float, v[i] & 0xFFFF0000u));
+        r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16;
       }
-      *reinterpret_cast<u4_t*>(static_cast<uint16_t*>(base) + at + 8 * c) = v;
     }
   }
+  return r;
 }
 
 // The parts of eight values of t (the first the rounding of t, each next that of the rest). An
@@ -188,66 +290,96 @@ __device__ __forceinline__ void split8(const float (&t)[8], typename ActT<ACT>::
   }
 }
 
+template <int ACT, int YT>
+constexpr int parts_of() { return ACT == ACT_BF16 && YT == T_F32 ? 3 : 2; }
+// halves between a row's parts in LDS: eight more than its ranks, so that the 16-byte reads of
+// eight rows fall in different banks
+constexpr int part_stride(int RS) { return 32 * RS + 8; }
+
 // RS: 32-rank steps
 template <int ACT, int YT, int RS>
-__global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p, int tile_rows) {
+__global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p) {
   typedef typename ActT<ACT>::type AT;
-  constexpr int PARTS = ACT == ACT_BF16 && YT == T_F32 ? 3 : 2;
-  const int lane = threadIdx.x & 63;
+  constexpr int PARTS = parts_of<ACT, YT>(), STRIDE = part_stride(RS), NH = Cols<YT>::kAccesses;
+  extern __shared__ __attribute__((aligned(16))) uint16_t tp[];  // [tile rows][PARTS][STRIDE]
+  __shared__ int rows_of[kTileMax];
+  __shared__ float backs[kTileMax];
+  const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t* const list = p.plan + p.tiles;
-  if ((int)blockIdx.x >= list[0]) return;
-  const int e = list[4 + 2 * blockIdx.x], p0 = list[5 + 2 * blockIdx.x];
-  const int rows = min(tile_rows, group_end(p, e) - p0);
-  const int n0 = (blockIdx.y * kExpandWaves + wave) * 64;
-  const int col = n0 + 16 * (lane >> 4);  // this lane's sixteen columns
-  if (n0 >= p.N) return;
-  const bool mine = col < p.N;  // N is a multiple of 16
-  if (e >= p.L) {               // no adapter: out is y
+  // consecutive workgroups take a tile's columns: neighbours in memory, and each XCD's share of a
+  // matrix B is an eighth
+  const int tile = blockIdx.x / p.col_groups, cg = blockIdx.x - tile * p.col_groups;
+  int rows, e;
+  if (!find_tile(p, tile, rows_of, rows, e)) return;
+  // this wave's strips of 64 columns: n_first, n_first + step, ... below n_end
+  constexpr int step = 64 * kExpandWaves;
+  const int n_first = cg * p.strips * step + wave * 64;
+  const int n_end = min(p.N, (cg + 1) * p.strips * step);
+  if (e >= p.L) {  // no adapter: out is y
     if (p.out == p.y) return;
-    for (int m = lane & 15; m < rows; m += 16) {
-      const size_t at = (size_t)p.plan[p.order + p0 + m] * p.N + col;
-      float f[16];
-      if (mine) {
-        load16<YT>(p.y, at, f);
-        store16<YT>(p.out, at, f);
-      }
-    }
+    __syncthreads();
+    for (int n0 = n_first; n0 < n_end; n0 += step)
+      for (int m = lane & 15; m < rows; m += 16)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const int n = n0 + Cols<YT>::offset(h, g);
+          const size_t at = (size_t)rows_of[m] * p.N + n;
+          if (n < p.N) store_cols<YT>(p.out, at, load_cols<YT>(p.y, at));
+        }
     return;
   }
-  u4_t bv[4][RS];
+  const uint16_t* const b = p.b + (size_t)e * p.N * p.R;
+  auto load_b = [&](u4_t (&v)[4][RS], int n0) __attribute__((always_inline)) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int i = lane & 15, n = min(n0 + 16 * (i >> 2) + 4 * q + (i & 3), p.N - 1);
-    const uint16_t* src = p.b + ((size_t)e * p.N + n) * p.R;
-#pragma unroll
-    for (int rs = 0; rs < RS; ++rs) {
-      const int r = 32 * rs + 8 * (lane >> 4);  // R is a multiple of 8
-      bv[q][rs] = r < p.R ? *reinterpret_cast<const u4_t*>(src + r) : u4_t{0, 0, 0, 0};
-    }
-  }
-  const float scaling = p.scaling[e];
-  for (int m0 = 0; m0 < rows; m0 += 16) {
-    const int m = min(m0 + (lane & 15), rows - 1);
-    const size_t at = (size_t)p.plan[p.order + p0 + m] * p.N + col;
-    float f[16];
-    if (mine) load16<YT>(p.y, at, f);
-    float t[RS][8];
-#pragma unroll
-    for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[rs][i] = 0.f;
-    for (int s = 0; s < p.slices; ++s) {
-      const float* src = p.part + ((size_t)s * p.M + p0 + m) * p.R;
+    for (int q = 0; q < 4; ++q) {
+      const int i = lane & 15, n = min(n0 + 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3), p.N - 1);
 #pragma unroll
       for (int rs = 0; rs < RS; ++rs) {
-        const int r = 32 * rs + 8 * (lane >> 4);
-        if (r >= p.R) continue;
-        const f4_t lo = *reinterpret_cast<const f4_t*>(src + r), hi = *reinterpret_cast<const f4_t*>(src + r + 4);
+        const int r = 32 * rs + 8 * g;  // R is a multiple of 8
+        v[q][rs] = r < p.R ? *reinterpret_cast<const u4_t*>(b + (size_t)n * p.R + r) : u4_t{0, 0, 0, 0};
+      }
+    }
+  };
+  // N is a multiple of 16: an access is all in or out
+  auto load_y = [&](u4_t (&v)[NH], int n0, int m0) __attribute__((always_inline)) {
+    const size_t row = (size_t)rows_of[min(m0 + (lane & 15), rows - 1)] * p.N;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          t[rs][i] += lo[i];
-          t[rs][4 + i] += hi[i];
+    for (int h = 0; h < NH; ++h) {
+      const int n = n0 + Cols<YT>::offset(h, g);
+      if (n < p.N) v[h] = load_cols<YT>(p.y, row + n);
+    }
+  };
+  u4_t bv[4][RS], yv[NH];
+  load_b(bv, n_first);
+  const float scaling = p.scaling[e];
+  __syncthreads();  // rows_of
+  load_y(yv, n_first, 0);
+  // the rows' t: 4 RS threads a row, eight ranks each
+  constexpr int C = 4 * RS;
+  for (int q = threadIdx.x; q < ((rows + 15) & ~15) * C; q += 64 * kExpandWaves) {
+    const int row = q / C, r = 8 * (q - row * C);
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = 0.f;
+    if (r < p.R) {
+      const float* src = p.part + (size_t)rows_of[min(row, rows - 1)] * p.R + r;
+      const size_t next = (size_t)p.M * p.R;
+      for (int s0 = 0; s0 < p.slices; s0 += 4) {
+        f4_t lo[4], hi[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float* v = src + min(s0 + s, p.slices - 1) * next;
+          lo[s] = *reinterpret_cast<const f4_t*>(v);
+          hi[s] = *reinterpret_cast<const f4_t*>(v + 4);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          if (s0 + s >= p.slices) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            t[i] += lo[s][i];
+            t[4 + i] += hi[s][i];
+          }
         }
       }
     }
@@ -255,69 +387,116 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p,
     if constexpr (ACT == ACT_F16) {
       float big = 0.f;
 #pragma unroll
-      for (int rs = 0; rs < RS; ++rs)
+      for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(t[i]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(t[rs][i]));
-      big = fmaxf(big, __shfl_xor(big, 16));
-      big = fmaxf(big, __shfl_xor(big, 32));
+      for (int o = 1; o < C; o <<= 1) big = fmaxf(big, __shfl_xor(big, o));
       // 2^-e of the row's largest value, from its exponent bits (kept off the ends of the range)
       const int ex = min(max((int)(__builtin_bit_cast(uint32_t, big) >> 23), 27), 227);
       const float down = __builtin_bit_cast(float, (uint32_t)(254 - ex) << 23);
       back *= __builtin_bit_cast(float, (uint32_t)ex << 23);
 #pragma unroll
-      for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[rs][i] *= down;
+      for (int i = 0; i < 8; ++i) t[i] *= down;
     }
+    AT part[PARTS];
+    split8<ACT, PARTS>(t, part);
+#pragma unroll
+    for (int s = 0; s < PARTS; ++s)
+      *reinterpret_cast<u4_t*>(tp + (row * PARTS + s) * STRIDE + r) = __builtin_bit_cast(u4_t, part[s]);
+    if (r == 0) backs[row] = back;
+  }
+  __syncthreads();
+  auto add_tile = [&](const u4_t (&y)[NH], int n0, int m0) __attribute__((always_inline)) {
+    const int m = m0 + (lane & 15);
     f4_t acc[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int rs = 0; rs < RS; ++rs) {
-      AT part[PARTS];
-      split8<ACT, PARTS>(t[rs], part);
+    for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
-      for (int s = 0; s < PARTS; ++s)
+      for (int s = 0; s < PARTS; ++s) {
+        const u4_t t = *reinterpret_cast<const u4_t*>(tp + (m * PARTS + s) * STRIDE + 32 * rs + 8 * g);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = mfma16(__builtin_bit_cast(AT, bv[q][rs]), part[s], acc[q]);
+        for (int q = 0; q < 4; ++q)
+          acc[q] = mfma16(__builtin_bit_cast(AT, bv[q][rs]), __builtin_bit_cast(AT, t), acc[q]);
+      }
+    if (m >= rows) return;
+    const size_t row = (size_t)rows_of[m] * p.N;
+    const float back = backs[m];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int n = n0 + Cols<YT>::offset(h, g);
+      if (n < p.N) store_cols<YT>(p.out, row + n, add_cols<YT>(y[h], acc + h * (4 / NH), back));
     }
+  };
+  // One strip; y of the next tile (and with MORE the next strip's first y and B) loads meanwhile. Loads
+  // under a branch would make the compiler wait for all that are in flight, so the last tile
+  // and the last strip are passes of their own.
+  auto strip = [&](int n0, auto more) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(more)::value, AHEAD = MORE && RS <= 2;
+    u4_t bn[4][RS], next[NH];
+    if constexpr (AHEAD) load_b(bn, n0 + step);
+    int m0 = 0;
+    for (; m0 + 16 < rows; m0 += 16) {
+      load_y(next, n0, m0 + 16);
+      add_tile(yv, n0, m0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+      for (int h = 0; h < NH; ++h) yv[h] = next[h];
+    }
+    if constexpr (MORE) load_y(next, n0 + step, 0);
+    add_tile(yv, n0, m0);
+    if constexpr (MORE) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[4 * q + i] = __builtin_fmaf(back, acc[q][i], f[4 * q + i]);
-    if (mine && m0 + (lane & 15) < rows) store16<YT>(p.out, at, f);
-  }
+      for (int h = 0; h < NH; ++h) yv[h] = next[h];
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int rs = 0; rs < RS; ++rs) bv[q][rs] = bn[q][rs];
+      } else {
+        load_b(bv, n0 + step);
+      }
+    }
+  };
+  int n0 = n_first;
+  for (; n0 + step < n_end; n0 += step) strip(n0, std::true_type{});
+  if (n0 < n_end) strip(n0, std::false_type{});
 }
 
 struct LoraGeometry {
-  int shrink_list, expand_list;  // tile lists
-  int slices, steps;
+  int list;  // tile list
+  int slices, steps, strips;
 };
 
 LoraGeometry lora_geometry(int M, int K, int N, int L, int R) {
-  (void)N;
   LoraGeometry g;
   const int groups = L < M ? L : M;
-  const int per_group = M / (groups > 0 ? groups : 1);
-  g.shrink_list = per_group >= 48 ? 2 : 0;
-  g.expand_list = per_group >= 48 ? 2 : 0;
+  g.list = M / (groups > 0 ? groups : 1) >= 48 ? 2 : 0;
+  // tiles to expect: full ones, and about one part-filled for every second adapter
+  const long long tiles = M / kTileRows[g.list] + (groups + 1) / 2;
+  const long long cus = device_cu_count();
   // slices of K until the tiles fill the compute units, at least four steps a wave
-  const long long tiles = (long long)(M / kTileRows[g.shrink_list] + (groups + 1) / 2 + 1) * ceil_div(R, kRankChunk);
   const int steps = K / 32;
-  int slices = (int)(device_cu_count() / tiles);
+  int slices = (int)(cus / ((tiles > 0 ? tiles : 1) * ceil_div(R, kRankChunk)));
   const int most = steps / (4 * kShrinkWaves);
   if (slices > most) slices = most;
   if (slices > kMaxSlices) slices = kMaxSlices;
   if (slices < 1) slices = 1;
-  g.steps = ceil_div(steps, slices * kShrinkWaves);
-  g.slices = ceil_div(steps, g.steps * kShrinkWaves);
+  const int set = kSetSteps(kTileRows[g.list] / 16);
+  g.steps = ceil_div(ceil_div(steps, slices), set) * set;
+  g.slices = ceil_div(steps, g.steps);
+  // strips per wave (each saves the others' search for rows and splitting of t) while two workgroups
+  // a compute unit are left
+  const long long wgs = tiles * ceil_div(N, 64 * kExpandWaves);
+  g.strips = g.list ? 1 : (int)(wgs / (2 * cus));
+  if (g.strips > 8) g.strips = 8;
+  if (g.strips < 1) g.strips = 1;
   return g;
 }
 
 template <int ACT, int MT>
 void launch_shrink(const LoraParams& p, dim3 grid, hipStream_t s) {
   const dim3 block(64 * kShrinkWaves);
-  const size_t lds = (size_t)kShrinkWaves * MT * 256 * 4;  // per rank tile
+  const size_t lds = (size_t)kShrinkWaves / 2 * MT * 256 * 4;  // per rank tile
   if (p.R <= 16)
     hipLaunchKernelGGL((shrink_kernel<ACT, MT, 1>), grid, block, lds, s, p);
   else if (p.R <= 32)
@@ -327,38 +506,56 @@ void launch_shrink(const LoraParams& p, dim3 grid, hipStream_t s) {
 }
 
 template <int ACT, int YT>
-void launch_expand(const LoraParams& p, dim3 grid, int rows, hipStream_t s) {
+void launch_expand(const LoraParams& p, dim3 grid, hipStream_t s) {
   const dim3 block(64 * kExpandWaves);
+  const size_t lds = (size_t)p.tile_rows * parts_of<ACT, YT>() * 2;  // per half of a part's row
   if (p.R <= 32)
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 1>), grid, block, 0, s, p, rows);
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, 1>), grid, block, lds * part_stride(1), s, p);
   else if (p.R <= 64)
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 2>), grid, block, 0, s, p, rows);
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, 2>), grid, block, lds * part_stride(2), s, p);
   else if (p.R <= 128)
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 4>), grid, block, 0, s, p, rows);
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, 4>), grid, block, lds * part_stride(4), s, p);
   else
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 8>), grid, block, 0, s, p, rows);
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, 8>), grid, block, lds * part_stride(8), s, p);
 }
+
+// tiles found by the workgroups themselves: few rows, no plan
+bool self_tiles(int M, bool planned) { return !planned && M <= kSelfRows; }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int M, int K, int N, int L, int R, bool planned) {
   const LoraGeometry g = lora_geometry(M, K, N, L, R);
-  const size_t plan = planned ? 0 : align256((size_t)route_layout(M, 1, L).words * 4);
+  const size_t plan = planned || self_tiles(M, planned) ? 0 : align256((size_t)route_layout(M, 1, L).words * 4);
   return plan + align256((size_t)g.slices * M * R * 4);
 }
 
 hipError_t launch_lora(const LoraArgs& a) {
-  const LoraGeometry g = lora_geometry(a.M, a.K, a.N, a.L, a.R);
-  const RouteLayout r = route_layout(a.M, 1, a.L);
+  LoraGeometry g = lora_geometry(a.M, a.K, a.N, a.L, a.R);
   char* ws = static_cast<char*>(a.workspace);
   LoraParams p;
-  p.plan = a.plan;
-  if (!p.plan) {
-    int32_t* plan = reinterpret_cast<int32_t*>(ws);
-    ws += align256((size_t)r.words * 4);
-    const hipError_t e = launch_route(a.ids, r, plan, a.stream);
-    if (e != hipSuccess) return e;
-    p.plan = plan;
+  p.ids = nullptr;
+  p.groups = GroupTiles{};
+  int tiles = a.M;  // of a launch
+  if (self_tiles(a.M, a.plan != nullptr)) {
+    p.ids = a.ids;
+    g.list = 0;
+  } else {
+    const RouteLayout r = route_layout(a.M, 1, a.L);
+    p.groups.plan = a.plan;
+    if (!a.plan) {
+      int32_t* plan = reinterpret_cast<int32_t*>(ws);
+      ws += align256((size_t)r.words * 4);
+      const hipError_t e = launch_route(a.ids, r, plan, a.stream);
+      if (e != hipSuccess) return e;
+      p.groups.plan = plan;
+    }
+    p.groups.S = r.S;
+    p.groups.E = r.E;
+    p.groups.topk = 1;
+    p.groups.order = r.order;
+    p.groups.list = r.tiles[g.list];
+    p.groups.bound = tiles = tile_bound(r.S, r.E, g.list);
   }
   p.x = static_cast<const uint16_t*>(a.x);
   p.a = static_cast<const uint16_t*>(a.lora_a);
@@ -367,7 +564,6 @@ hipError_t launch_lora(const LoraArgs& a) {
   p.out = a.out;
   p.scaling = a.scaling;
   p.part = reinterpret_cast<float*>(ws);
-  p.order = r.order;
   p.M = a.M;
   p.K = a.K;
   p.N = a.N;
@@ -375,25 +571,21 @@ hipError_t launch_lora(const LoraArgs& a) {
   p.R = a.R;
   p.slices = g.slices;
   p.steps = g.steps;
-  p.tiles = r.tiles[g.shrink_list];
-  p.bound = tile_bound(r.S, r.E, g.shrink_list);
-  const dim3 sgrid(p.bound, g.slices, ceil_div(a.R, kRankChunk));
+  p.tile_rows = kTileRows[g.list];
+  p.strips = g.strips;
+  const dim3 sgrid(tiles * g.slices, ceil_div(a.R, kRankChunk));
   if (a.act == ACT_F16)
-    g.shrink_list ? launch_shrink<ACT_F16, 4>(p, sgrid, a.stream) : launch_shrink<ACT_F16, 1>(p, sgrid, a.stream);
+    g.list ? launch_shrink<ACT_F16, 4>(p, sgrid, a.stream) : launch_shrink<ACT_F16, 1>(p, sgrid, a.stream);
   else
-    g.shrink_list ? launch_shrink<ACT_BF16, 4>(p, sgrid, a.stream) : launch_shrink<ACT_BF16, 1>(p, sgrid, a.stream);
-  hipError_t e = hipGetLastError();
+    g.list ? launch_shrink<ACT_BF16, 4>(p, sgrid, a.stream) : launch_shrink<ACT_BF16, 1>(p, sgrid, a.stream);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  p.tiles = r.tiles[g.expand_list];
-  p.bound = tile_bound(r.S, r.E, g.expand_list);
-  const dim3 egrid(p.bound, ceil_div(a.N, 64 * kExpandWaves));
-  const int rows = kTileRows[g.expand_list];
+  p.col_groups = ceil_div(a.N, 64 * kExpandWaves * g.strips);
+  const dim3 egrid(tiles * p.col_groups);
   if (a.act == ACT_F16)
-    a.ydtype == T_F32 ? launch_expand<ACT_F16, T_F32>(p, egrid, rows, a.stream)
-                      : launch_expand<ACT_F16, T_F16>(p, egrid, rows, a.stream);
+    a.ydtype == T_F32 ? launch_expand<ACT_F16, T_F32>(p, egrid, a.stream) : launch_expand<ACT_F16, T_F16>(p, egrid, a.stream);
   else
-    a.ydtype == T_F32 ? launch_expand<ACT_BF16, T_F32>(p, egrid, rows, a.stream)
-                      : launch_expand<ACT_BF16, T_BF16>(p, egrid, rows, a.stream);
+    a.ydtype == T_F32 ? launch_expand<ACT_BF16, T_F32>(p, egrid, a.stream) : launch_expand<ACT_BF16, T_BF16>(p, egrid, a.stream);
   return hipGetLastError();
 }
 
