@@ -30,22 +30,38 @@ int forced_tile() {
   return forced;
 }
 
-// The rows of each group are known on the device only, so the tile goes by their mean over the groups that can have
-// rows.
-Tile choose_tile(int S, int E) {
+// The rows of each group are known on the device only, so the tile goes by their mean over the
+// groups that can have rows. A taller tile forms W_hat once for more rows and is part-filled
+// more often, so the limits lie where tiles win on routings as uneven as gates make them (top-k of normal scores
+// with expert biases of 0.7 sigma; 8 experts of 4096x14336 g128, us with 16/32/64/128 rows a
+// tile): mean 6 44/44/56/101, 12 65/70/71/114, 16 61/54/70/108, 48 133/108/104/189, 64
+// 161/123/116/117, 128 310/231/195/207, 192 470/357/324/235; 64 experts of 2048x2816 NF4: 8
+// 53/55/72/136, 24 87/78/90/141, 64 178/140/140/208, 128 333/246/227/275, 192 495/368/321/286.
+// Past 144 rows the 128 x 512 tile can still leave most of the chip idle (few groups, narrow N): then
+// 64-row tiles, by a model of compute-unit time (0.42 us per 64x64 tile and k-block; 2.6 us per
+// 128x512 tile and k-block in one round of workgroups, 3.2 us in more).
+Tile choose_tile(int S, int E, int K, int N) {
   if (forced_tile() >= 0) return (Tile)forced_tile();
-  const int mean = S / (E < S ? E : S);
-  return mean <= 12 ? TILE_16 : mean <= 24 ? TILE_32 : mean <= 64 ? TILE_64 : TILE_128;
+  const int groups = E < S ? E : S;
+  const int mean = S / (groups > 0 ? groups : 1);
+  if (mean <= 10) return TILE_16;
+  if (mean <= 48) return TILE_32;
+  if (mean <= 144) return TILE_64;
+  const long long cus = device_cu_count();
+  const long long rounds = ((S / 128 + groups / 2) * (long long)ceil_div(N, 512) + cus - 1) / cus;
+  const double large = rounds * (rounds > 1 ? 3.2 : 2.6);
+  const double small = (S / 64.0 + groups / 2) * ceil_div(N, 64) * 0.42 / cus;
+  (void)K;  // both grow with it alike
+  return small < large ? TILE_64 : TILE_128;
 }
 
 int tile_cols(Tile t) { return t == TILE_128 ? 512 : 64; }
-int tile_threads(Tile) { return 64 * 8; }
 
 }  // namespace
 
 const char* grouped_name(int S, int K, int N, int E, int group_size) {
-  (void)K, (void)N, (void)group_size;
-  switch (choose_tile(S, E)) {
+  (void)group_size;
+  switch (choose_tile(S, E, K, N)) {
     case TILE_16: return "w4a16_grouped_16x64";
     case TILE_32: return "w4a16_grouped_32x64";
     case TILE_64: return "w4a16_grouped_64x64";
@@ -54,24 +70,22 @@ const char* grouped_name(int S, int K, int N, int E, int group_size) {
 }
 
 // a launch holds fewer than 2^32 threads
-bool grouped_fits(const RouteLayout& r, int N) {
-  const Tile t = choose_tile(r.S, r.E);
-  return (long long)tile_bound(r.S, r.E, t) * ceil_div(N, tile_cols(t)) * tile_threads(t) < (1LL << 32);
+bool grouped_fits(const RouteLayout& r, int K, int N) {
+  const Tile t = choose_tile(r.S, r.E, K, N);
+  return (long long)tile_bound(r.S, r.E, t) * ceil_div(N, tile_cols(t)) * 512 < (1LL << 32);
 }
 
 hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t* plan, bool gather) {
-  const Tile tile = choose_tile(r.S, r.E);
+  const Tile tile = choose_tile(r.S, r.E, a.K, a.N);
   GroupTiles t;
   t.plan = plan;
   t.S = r.S;
   t.E = r.E;
-  t.topk = r.topk;
-  t.order = r.order;
+  t.token = r.token;
   t.list = r.tiles[tile];
   t.bound = tile_bound(r.S, r.E, tile);
   t.tokens = gather ? r.S / r.topk : 0;
   if (tile == TILE_128) return launch_grouped_large(a, t);
-  if (tile != TILE_16) return launch_grouped_skinny(a, t, kTileRows[tile]);
   GroupedParams p;
   p.x = static_cast<const uint16_t*>(a.x);
   p.groups = t;
@@ -87,11 +101,10 @@ hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t
   p.NT = a.N / 16;
   p.NG = a.K / a.group_size;
   p.half = p.NT / 2;
+  p.slice = ceil_div(p.KC, kWaves);
+  p.col_tiles = ceil_div(p.NT, kStrips);
   GroupedGeometry g;
-  g.SW = 4;
-  g.waves = p.KC >= 2 * kMaxWaves ? kMaxWaves : p.KC >= 8 ? 4 : 2;
-  p.slice = ceil_div(p.KC, g.waves);
-  p.col_tiles = ceil_div(p.NT, g.SW);
+  g.MT = kTileRows[tile] / 16;
   return a.act == ACT_F16 ? launch_few<ACT_F16>(p, g, a.group_size, a.nf4, a.glu, a.stream)
                           : launch_few<ACT_BF16>(p, g, a.group_size, a.nf4, a.glu, a.stream);
 }

@@ -102,7 +102,7 @@ __device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* ro
   int p0, end;
   if (!group_tile(p.groups, tile, e, p0, end)) return false;
   rows = min(p.tile_rows, end - p0);
-  if ((int)threadIdx.x < rows) rows_of[threadIdx.x] = p.groups.plan[p.groups.order + p0 + threadIdx.x];
+  if ((int)threadIdx.x < rows) rows_of[threadIdx.x] = p.groups.plan[p.groups.token + p0 + threadIdx.x];
   return true;
 }
 
@@ -552,8 +552,7 @@ hipError_t launch_lora(const LoraArgs& a) {
     }
     p.groups.S = r.S;
     p.groups.E = r.E;
-    p.groups.topk = 1;
-    p.groups.order = r.order;
+    p.groups.token = r.token;
     p.groups.list = r.tiles[g.list];
     p.groups.bound = tiles = tile_bound(r.S, r.E, g.list);
   }

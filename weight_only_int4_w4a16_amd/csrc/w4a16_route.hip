@@ -123,8 +123,8 @@ __device__ __forceinline__ void write_groups(const RouteParams& p, const int* to
         else
           hi = mid - 1;
       }
-      list[4 + 2 * i] = lo;
-      list[5 + 2 * i] = scan[lo] + (i - first[lo]) * kTileRows[j];
+      const int row = scan[lo] + (i - first[lo]) * kTileRows[j];
+      *reinterpret_cast<int4*>(list + 4 + 4 * i) = int4{lo, row, min(row + kTileRows[j], scan[lo + 1]), 0};
     }
   }
 }
@@ -140,6 +140,7 @@ __device__ __forceinline__ void scatter_wave(const RouteParams& p, int first, in
     const int i = first + b * 64 + lane;
     const int row = base[g] + ws.rank[b];
     p.plan[p.r.order + row] = i;
+    if (p.r.topk > 1) p.plan[p.r.token + row] = i / p.r.topk;
     p.plan[p.r.slot + i] = g < E ? row : -1;
   }
 }

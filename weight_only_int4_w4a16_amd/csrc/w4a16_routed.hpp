@@ -7,9 +7,10 @@
 namespace w4a16 {
 
 // The plan w4a16_route writes, in int32 words from its start: offsets [E + 1], order [S],
-// slot [S], the tile lists, and (many slots) the per-block counts of the sort. S = tokens * topk.
-// Tile list j cuts every group's rows into tiles of kTileRows[j] rows: a count, three unused words, then (group,
-// first row) pairs; group E's tiles are the slots of no group.
+// slot [S], the token of each sorted row [S] (with topk 1 the order itself), the tile lists, and
+// (many slots) the per-block counts of the sort. S = tokens * topk.
+// Tile list j cuts every group's rows into tiles of kTileRows[j] rows: a count, three unused
+// words, then (group, first row, end, 0) per tile; group E's tiles are the slots of no group.
 constexpr int kTileLists = 4;
 constexpr int kTileRows[kTileLists] = {16, 32, 64, 128};
 constexpr int kMaxGroups = 1024;
@@ -22,7 +23,7 @@ inline int round64(int n) { return (n + 63) & ~63; }
 inline int tile_bound(int S, int E, int j) { return S / kTileRows[j] + (E + 1 < S ? E + 1 : S); }
 struct RouteLayout {
   int S, E, topk;
-  int order, slot, tiles[kTileLists], hist, words;  // word offsets; the total
+  int order, slot, token, tiles[kTileLists], hist, words;  // word offsets; the total
   int blocks;                                        // workgroups of the sort
 };
 inline RouteLayout route_layout(int tokens, int topk, int E) {
@@ -34,9 +35,14 @@ inline RouteLayout route_layout(int tokens, int topk, int E) {
   r.order = round64(E + 1);
   r.slot = r.order + round64(r.S);
   int at = r.slot + round64(r.S);
+  r.token = r.order;
+  if (topk > 1) {
+    r.token = at;
+    at += round64(r.S);
+  }
   for (int j = 0; j < kTileLists; ++j) {
     r.tiles[j] = at;
-    at += round64(4 + 2 * tile_bound(r.S, E, j));
+    at += round64(4 + 4 * tile_bound(r.S, E, j));
   }
   r.hist = at;
   r.words = at + (r.blocks > 1 ? round64(r.blocks * (E + 1)) : 0);
@@ -46,19 +52,21 @@ inline RouteLayout route_layout(int tokens, int topk, int E) {
 // What a GEMM kernel's grouped instantiation reads besides its GEMM parameters
 struct GroupTiles {
   const int32_t* plan;
-  int S, E, topk;
-  int order, list;  // word offsets in the plan: the sorted slots, the tile list used
+  int S, E;
+  int token, list;  // word offsets in the plan: the sorted rows' tokens, the tile list used
   int bound;        // most tiles the list can hold (the grid's)
   int tokens;       // rows of x where they are gathered through the plan, else 0
 };
-// tile ti of a list: its group e and sorted rows [p0, end); false past the list's end
+// tile ti of a list: its group e and sorted rows [p0, end); false past the list's end (an entry is in the plan
+// whatever ti < bound, so that the count and the entry load at once)
 __device__ __forceinline__ bool group_tile(const GroupTiles& g, int ti, int& e, int& p0, int& end) {
   const int32_t* const list = g.plan + g.list;
-  if (ti >= list[0]) return false;
-  e = list[4 + 2 * ti];
-  p0 = list[5 + 2 * ti];
-  end = e < g.E ? g.plan[e + 1] : g.S;
-  return true;
+  const int4 t = *reinterpret_cast<const int4*>(list + 4 + 4 * ti);
+  const int count = list[0];
+  e = t.x;
+  p0 = t.y;
+  end = t.z;
+  return ti < count;
 }
 
 hipError_t launch_route(const int32_t* ids, const RouteLayout& r, int32_t* plan, hipStream_t s);
@@ -75,11 +83,10 @@ hipError_t launch_combine_backward(const void* dy, const void* ys, const RouteLa
 // a.qzeros hold the groups' weights one after another
 hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t* plan, bool gather);
 // whether the rows and columns make a launch the kernels can index
-bool grouped_fits(const RouteLayout& r, int N);
+bool grouped_fits(const RouteLayout& r, int K, int N);
 const char* grouped_name(int S, int K, int N, int E, int group_size);
 constexpr int kMaxRank = 256;
-// its launches on the skinny kernel (tiles of 32 or 64 rows) and on the batched kernel (128)
-hipError_t launch_grouped_skinny(const GemmArgs& a, const GroupTiles& t, int rows);
+// its launches on the batched kernel (128-row tiles)
 hipError_t launch_grouped_large(const GemmArgs& a, const GroupTiles& t);
 struct LoraArgs {
   const void* x;       // act [M][K]

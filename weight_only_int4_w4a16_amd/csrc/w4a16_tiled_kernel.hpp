@@ -231,7 +231,7 @@ __global__ __launch_bounds__(T::kThreads) void tiled_kernel(Params p) {
   const uint16_t* xbase = p.x + (size_t)m0 * K;
   uint32_t xbytes = (uint32_t)tile_rows * K * 2;
   if constexpr (GROUPED) {
-    if (p.groups.tokens) {  // rows read in place: the row of sorted row r is order[r] / topk
+    if (p.groups.tokens) {  // rows read in place: the row of sorted row r is token[r]
       xbase = p.x;
       xbytes = (uint32_t)p.groups.tokens * (uint32_t)K * 2u;
     }
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(T::kThreads) void tiled_kernel(Params p) {
     const int chunk = (lane & 15) ^ (row & 15);
     int src = min(row, tile_rows - 1);
     if constexpr (GROUPED) {
-      if (p.groups.tokens) src = p.groups.plan[p.groups.order + m0 + src] / p.groups.topk;
+      if (p.groups.tokens) src = p.groups.plan[p.groups.token + m0 + src];
     }
     aoff[j] = ((uint32_t)src * (uint32_t)K + chunk * 8) * 2;
   }
