@@ -84,6 +84,8 @@ def _routed(ids, groups):
     (16, 4, 8, "none"), (33, 2, 7, "one"), (64, 8, 64, "all"), (100, 1, 63, "skewed"),
     (1000, 3, 64, "mixed"), (4095, 2, 1024, "mixed"), (8192, 1, 3, "mixed"),   # one workgroup
     (8193, 1, 3, "mixed"), (20011, 4, 130, "skewed"), (40000, 1, 1024, "mixed"), (9000, 2, 5, "none"),
+    (256, 2, 9, "mixed"), (257, 2, 9, "mixed"), (4096, 1, 70, "mixed"), (4097, 1, 70, "mixed"),
+    (200000, 1, 1024, "mixed"),                                                # counts scanned by a kernel
 ])
 def test_route_is_the_stable_sort(tokens, topk, groups, how):
     _announce(f"route {tokens}x{topk} groups={groups} {how}")

@@ -13,8 +13,11 @@
 // the rank inside a wave needs no atomics and the order never varies.
 //
 // The bytes are few (4 S read, 8 S written); a call is bound by the latency of its dependent
-// steps. Up to 8192 slots one workgroup does everything in one launch; more take a count, a
-// scan and a scatter launch over workgroups of 8192 slots.
+// steps. Up to 4096 slots one workgroup does everything in one launch (four waves up to 512 slots, whose
+// barriers are cheaper). More take two launches over workgroups of 2048 slots: the first counts
+// its slots per group, and in the second every workgroup adds up all the counts itself, which
+// saves a launch between them; only where the counts are many (over 64 Ki words) does a third
+// kernel scan them once in between.
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"
 
@@ -22,26 +25,27 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kThreads = 64 * kRouteWaves;
-
 struct RouteParams {
   const int32_t* ids;
   int32_t* plan;
   RouteLayout r;
-  int bits;  // of the largest group number E (the slots of no group)
+  int bits;      // of the largest group number E (the slots of no group)
+  bool scanned;  // hist holds each block's first rows, and the plan its offsets and lists
 };
 
+template <int B>
 struct WaveSlots {
-  int g[kRouteBatches], rank[kRouteBatches];  // group (-1 past the end); earlier slots of it in the wave
+  int g[B], rank[B];  // group (-1 past the end); earlier slots of it in the wave
 };
 
 // The wave's share of the block's slots: each lane's groups and their ranks within the wave, and
 // in cnt[0..E] (LDS, zeroed) the wave's slots per group.
+template <int B>
 __device__ __forceinline__ void count_wave(const RouteParams& p, int first, int batches, int lane,
-                                           int* cnt, WaveSlots& ws) {
+                                           int* cnt, WaveSlots<B>& ws) {
   const int E = p.r.E;
 #pragma unroll
-  for (int b = 0; b < kRouteBatches; ++b) {
+  for (int b = 0; b < B; ++b) {
     const int i = first + b * 64 + lane;
     ws.g[b] = -1;
     if (b < batches && i < p.r.S) {
@@ -50,7 +54,7 @@ __device__ __forceinline__ void count_wave(const RouteParams& p, int first, int 
     }
   }
 #pragma unroll
-  for (int b = 0; b < kRouteBatches; ++b) {
+  for (int b = 0; b < B; ++b) {
     if (b >= batches) break;
     const int g = ws.g[b];
     uint64_t same = __ballot(g >= 0);
@@ -98,42 +102,41 @@ __device__ __forceinline__ void scan_groups(const int* tot, int* out, int E, int
   if (lane == 0) out[E + 1] = carry;
 }
 
-// The groups' totals (LDS) -> offsets and tile lists of the plan, and off[0..E] in LDS. `scan`:
-// (kTileLists + 1) * (E + 2) words of LDS.
-__device__ __forceinline__ void write_groups(const RouteParams& p, const int* tot, int* scan) {
-  const int E = p.r.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (wave == 0)
-    scan_groups(tot, scan, E, 1, lane);
-  else if (wave <= kTileLists)
-    scan_groups(tot, scan + wave * (E + 2), E, kTileRows[wave - 1], lane);
+// scan[0..E+1]: the groups' first rows and S; scan + (j + 1) (E + 2): their first tiles in list j
+__device__ __forceinline__ void scan_all(const int* tot, int* scan, int E, int W) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int j = wave; j <= kTileLists; j += W)
+    scan_groups(tot, scan + j * (E + 2), E, j ? kTileRows[j - 1] : 1, lane);
   __syncthreads();
-  for (int g = threadIdx.x; g <= E; g += kThreads) p.plan[g] = scan[g];
-#pragma unroll
-  for (int j = 0; j < kTileLists; ++j) {
-    const int* first = scan + (j + 1) * (E + 2);
-    int32_t* const list = p.plan + p.r.tiles[j];
-    const int n = first[E + 1];
-    if (threadIdx.x == 0) list[0] = n;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      int lo = 0, hi = E;  // the last group whose first tile is at or before i
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] <= i)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      const int row = scan[lo] + (i - first[lo]) * kTileRows[j];
-      *reinterpret_cast<int4*>(list + 4 + 4 * i) = int4{lo, row, min(row + kTileRows[j], scan[lo + 1]), 0};
+}
+
+// tile list j of the plan from the scans
+__device__ __forceinline__ void write_list(const RouteParams& p, const int* scan, int j) {
+  const int E = p.r.E;
+  const int* first = scan + (j + 1) * (E + 2);
+  int32_t* const list = p.plan + p.r.tiles[j];
+  const int n = first[E + 1], tile_rows = kTileRows[j];
+  if (threadIdx.x == 0) list[0] = n;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    int lo = 0, hi = E;  // the last group whose first tile is at or before i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= i)
+        lo = mid;
+      else
+        hi = mid - 1;
     }
+    const int row = scan[lo] + (i - first[lo]) * tile_rows;
+    *reinterpret_cast<int4*>(list + 4 + 4 * i) = int4{lo, row, min(row + tile_rows, scan[lo + 1]), 0};
   }
 }
 
+template <int B>
 __device__ __forceinline__ void scatter_wave(const RouteParams& p, int first, int batches, int lane,
-                                             const int* base, const WaveSlots& ws) {
+                                             const int* base, const WaveSlots<B>& ws) {
   const int E = p.r.E;
 #pragma unroll
-  for (int b = 0; b < kRouteBatches; ++b) {
+  for (int b = 0; b < B; ++b) {
     if (b >= batches) break;
     const int g = ws.g[b];
     if (g < 0) continue;
@@ -145,73 +148,105 @@ __device__ __forceinline__ void scatter_wave(const RouteParams& p, int first, in
   }
 }
 
-// cnt[w][g] -> the slots of group g in earlier waves (in place), tot[g] the block's
-__device__ __forceinline__ void prefix_waves(int* cnt, int* tot, int E) {
-  for (int g = threadIdx.x; g <= E; g += kThreads) {
+// WHOLE: one workgroup sorts every slot. COUNT and SCATTER: a workgroup of several; COUNT fills the
+// block's row of hist, SCATTER places its slots. W waves of at most B 64-slot batches.
+enum { WHOLE = 0, COUNT = 1, SCATTER = 2 };
+template <int PASS, int W, int B>
+__global__ __launch_bounds__(64 * W) void route_kernel(RouteParams p) {
+  extern __shared__ int lds[];
+  const int E = p.r.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int* const cnt = lds;                  // [W][E + 1]
+  int* const tot = cnt + W * (E + 1);    // [E + 1]: the block's (SCATTER: all blocks') slots per group
+  int* const base = tot + (E + 1);       // [E + 1]: SCATTER: slots of the group in earlier blocks
+  int* const scan = base + (E + 1);      // [kTileLists + 1][E + 2]
+  for (int i = threadIdx.x; i < W * (E + 1); i += 64 * W) cnt[i] = 0;
+  __syncthreads();
+  // the waves take equal shares of the block's slots, in whole batches
+  const int s0 = blockIdx.x * (64 * W * B);
+  const int n = min(64 * W * B, p.r.S - s0);
+  const int batches = (n + 64 * W - 1) / (64 * W);
+  const int first = s0 + wave * batches * 64;
+  WaveSlots<B> ws;
+  count_wave(p, first, batches, lane, cnt + wave * (E + 1), ws);
+  __syncthreads();
+  // cnt[w][g] -> the slots of group g in earlier waves
+  for (int g = threadIdx.x; g <= E; g += 64 * W) {
     int s = 0;
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       const int v = cnt[w * (E + 1) + g];
       cnt[w * (E + 1) + g] = s;
       s += v;
     }
-    tot[g] = s;
+    if constexpr (PASS == COUNT)
+      p.plan[p.r.hist + blockIdx.x * (E + 1) + g] = s;
+    else
+      tot[g] = s;
   }
-}
-
-// WHOLE: one workgroup sorts every slot. Otherwise the SCATTER pass of a block, after its
-// first rows per group were scanned into the plan's hist, or the COUNT pass that fills hist.
-enum { WHOLE = 0, COUNT = 1, SCATTER = 2 };
-template <int PASS>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteParams p) {
-  extern __shared__ int lds[];
-  const int E = p.r.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int* const cnt = lds;                            // [kRouteWaves][E + 1]
-  int* const tot = cnt + kRouteWaves * (E + 1);    // [E + 1]
-  int* const scan = tot + (E + 1);                 // [kTileLists + 1][E + 2] (WHOLE)
-  for (int i = threadIdx.x; i < kRouteWaves * (E + 1); i += kThreads) cnt[i] = 0;
+  if constexpr (PASS == COUNT) return;
   __syncthreads();
-  // the waves take equal shares of the block's slots, in whole batches
-  const int s0 = blockIdx.x * kRouteSlots;
-  const int n = min(kRouteSlots, p.r.S - s0);
-  const int batches = (n + 64 * kRouteWaves - 1) / (64 * kRouteWaves);
-  const int first = s0 + wave * batches * 64;
-  WaveSlots ws;
-  count_wave(p, first, batches, lane, cnt + wave * (E + 1), ws);
-  __syncthreads();
-  prefix_waves(cnt, tot, E);
-  __syncthreads();
-  if constexpr (PASS == COUNT) {
-    for (int g = threadIdx.x; g <= E; g += kThreads) p.plan[p.r.hist + blockIdx.x * (E + 1) + g] = tot[g];
-    return;
+  if constexpr (PASS == WHOLE) {
+    scan_all(tot, scan, E, W);
+    for (int g = threadIdx.x; g <= E; g += 64 * W) p.plan[g] = scan[g];
+    for (int j = 0; j < kTileLists; ++j) write_list(p, scan, j);
   } else {
-    if constexpr (PASS == WHOLE) {
-      write_groups(p, tot, scan);
+    const int32_t* const hist = p.plan + p.r.hist;
+    if (p.scanned) {
+      for (int g = threadIdx.x; g <= E; g += 64 * W) scan[g] = hist[blockIdx.x * (E + 1) + g];
+      __syncthreads();
     } else {
-      for (int g = threadIdx.x; g <= E; g += kThreads) scan[g] = p.plan[p.r.hist + blockIdx.x * (E + 1) + g];
+      // every block's counts, over all blocks and over those before this one: the threads of a group
+      // take the blocks in turn and add with LDS atomics (whole numbers, so in any order)
+      for (int g = threadIdx.x; g <= E; g += 64 * W) tot[g] = base[g] = 0;
+      __syncthreads();
+      const int parts = max(1, 64 * W / (E + 1));
+      for (int i = threadIdx.x; i < parts * (E + 1); i += 64 * W) {
+        const int part = i / (E + 1), g = i - part * (E + 1);
+        int all = 0, before = 0;
+#pragma unroll 8
+        for (int b = part; b < p.r.blocks; b += parts) {
+          const int v = hist[b * (E + 1) + g];
+          all += v;
+          before += b < (int)blockIdx.x ? v : 0;
+        }
+        atomicAdd(tot + g, all);
+        atomicAdd(base + g, before);
+      }
+      __syncthreads();
+      scan_all(tot, scan, E, W);
+      if (blockIdx.x == 0)
+        for (int g = threadIdx.x; g <= E; g += 64 * W) p.plan[g] = scan[g];
+      for (int j = 0; j < kTileLists; ++j)
+        if (j % p.r.blocks == (int)blockIdx.x) write_list(p, scan, j);
+      __syncthreads();
+      for (int g = threadIdx.x; g <= E; g += 64 * W) scan[g] += base[g];
       __syncthreads();
     }
-    for (int i = threadIdx.x; i < kRouteWaves * (E + 1); i += kThreads) cnt[i] += scan[i % (E + 1)];
-    __syncthreads();
-    scatter_wave(p, first, batches, lane, cnt + wave * (E + 1), ws);
   }
+  for (int i = threadIdx.x; i < W * (E + 1); i += 64 * W) cnt[i] += scan[i % (E + 1)];
+  __syncthreads();
+  scatter_wave(p, first, batches, lane, cnt + wave * (E + 1), ws);
 }
 
-// Between COUNT and SCATTER, one workgroup: hist[b][g] becomes block b's first row of group g
-__global__ __launch_bounds__(kThreads) void route_scan_kernel(RouteParams p) {
+// Between COUNT and SCATTER where the counts are many: hist[b][g] becomes block b's first row of group g
+constexpr int kScanWaves = 16;
+__global__ __launch_bounds__(64 * kScanWaves) void route_scan_kernel(RouteParams p) {
   extern __shared__ int lds[];
   const int E = p.r.E;
   int* const tot = lds;
   int* const scan = lds + (E + 1);
   int32_t* const hist = p.plan + p.r.hist;
-  for (int g = threadIdx.x; g <= E; g += kThreads) {
+  for (int g = threadIdx.x; g <= E; g += 64 * kScanWaves) {
     int s = 0;
+#pragma unroll 8
     for (int b = 0; b < p.r.blocks; ++b) s += hist[b * (E + 1) + g];
     tot[g] = s;
   }
   __syncthreads();
-  write_groups(p, tot, scan);
-  for (int g = threadIdx.x; g <= E; g += kThreads) {
+  scan_all(tot, scan, E, kScanWaves);
+  for (int g = threadIdx.x; g <= E; g += 64 * kScanWaves) p.plan[g] = scan[g];
+  for (int j = 0; j < kTileLists; ++j) write_list(p, scan, j);
+  for (int g = threadIdx.x; g <= E; g += 64 * kScanWaves) {
     int s = scan[g];
     for (int b = 0; b < p.r.blocks; ++b) {
       const int v = hist[b * (E + 1) + g];
@@ -219,6 +254,13 @@ __global__ __launch_bounds__(kThreads) void route_scan_kernel(RouteParams p) {
       s += v;
     }
   }
+}
+
+template <int PASS, int W, int B>
+void launch_pass(const RouteParams& p, hipStream_t s) {
+  const int E = p.r.E;
+  const size_t words = (size_t)(W + 2) * (E + 1) + (size_t)(kTileLists + 1) * (E + 2);
+  hipLaunchKernelGGL((route_kernel<PASS, W, B>), dim3(p.r.blocks), dim3(64 * W), words * 4, s, p);
 }
 
 }  // namespace
@@ -230,15 +272,20 @@ hipError_t launch_route(const int32_t* ids, const RouteLayout& r, int32_t* plan,
   p.r = r;
   p.bits = 0;
   while ((r.E >> p.bits) != 0) ++p.bits;
-  const size_t count_lds = (size_t)(kRouteWaves + 1) * (r.E + 1) * 4;
-  const size_t groups_lds = (size_t)(kTileLists + 1) * (r.E + 2) * 4;
-  if (r.blocks == 1) {
-    hipLaunchKernelGGL((route_kernel<WHOLE>), dim3(1), dim3(kThreads), count_lds + groups_lds, s, p);
-    return hipGetLastError();
+  p.scanned = false;
+  if (r.S <= 512) {
+    launch_pass<WHOLE, 4, 2>(p, s);
+  } else if (r.blocks == 1) {
+    launch_pass<WHOLE, 16, kRouteWholeSlots / 1024>(p, s);
+  } else {
+    launch_pass<COUNT, 16, kRouteBlockSlots / 1024>(p, s);
+    if ((long long)r.blocks * (r.E + 1) > (1 << 16)) {
+      p.scanned = true;
+      const size_t words = (size_t)(r.E + 1) + (size_t)(kTileLists + 1) * (r.E + 2);
+      hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(64 * kScanWaves), words * 4, s, p);
+    }
+    launch_pass<SCATTER, 16, kRouteBlockSlots / 1024>(p, s);
   }
-  hipLaunchKernelGGL((route_kernel<COUNT>), dim3(r.blocks), dim3(kThreads), count_lds, s, p);
-  hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kThreads), (size_t)(r.E + 1) * 4 + groups_lds, s, p);
-  hipLaunchKernelGGL((route_kernel<SCATTER>), dim3(r.blocks), dim3(kThreads), count_lds + (size_t)(r.E + 1) * 4, s, p);
   return hipGetLastError();
 }
 

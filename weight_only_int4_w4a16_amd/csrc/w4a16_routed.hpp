@@ -15,9 +15,8 @@ constexpr int kTileLists = 4;
 constexpr int kTileRows[kTileLists] = {16, 32, 64, 128};
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSlots = 1 << 26;
-constexpr int kRouteWaves = 16;                       // waves of a sorting workgroup
-constexpr int kRouteBatches = 8;                      // 64-slot batches per wave
-constexpr int kRouteSlots = kRouteWaves * kRouteBatches * 64;  // slots per sorting workgroup
+constexpr int kRouteBlockSlots = 2048;  // slots per workgroup of the sort where there are several
+constexpr int kRouteWholeSlots = 4096;  // most slots that one workgroup sorts alone
 inline int round64(int n) { return (n + 63) & ~63; }
 // most tiles list j can hold: full tiles, and one more for each group with rows
 inline int tile_bound(int S, int E, int j) { return S / kTileRows[j] + (E + 1 < S ? E + 1 : S); }
@@ -31,7 +30,7 @@ inline RouteLayout route_layout(int tokens, int topk, int E) {
   r.S = tokens * topk;
   r.E = E;
   r.topk = topk;
-  r.blocks = r.S > 0 ? (r.S + kRouteSlots - 1) / kRouteSlots : 1;
+  r.blocks = r.S <= kRouteWholeSlots ? 1 : (r.S + kRouteBlockSlots - 1) / kRouteBlockSlots;
   r.order = round64(E + 1);
   r.slot = r.order + round64(r.S);
   int at = r.slot + round64(r.S);
