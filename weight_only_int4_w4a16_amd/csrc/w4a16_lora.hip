@@ -49,8 +49,7 @@ constexpr int kShrinkWaves = 8;
 constexpr int kExpandWaves = 4;
 constexpr int kRankChunk = 64;   // ranks per workgroup of the first product
 constexpr int kMaxSlices = 16;
-constexpr int kLogU(int MT) { return MT == 1 ? 2 : 1; }
-constexpr int kSetSteps(int MT) { return 1 << kLogU(MT); }
+constexpr int kSetSteps = 4;     // 32-deep steps of a register set in the first product
 constexpr int kSelfRows = 256;   // most rows whose tiles the workgroups find themselves
 constexpr int kTileMax = 64;     // most rows of a tile
 
@@ -82,8 +81,7 @@ __device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* ro
 #pragma unroll
     for (int c = 0; c < kSelfRows / 64; ++c) {
       const int m = 64 * c + lane;
-      uint32_t other = 0;
-      if (m < p.M) other = (uint32_t)p.ids[m];
+      const uint32_t other = (uint32_t)p.ids[min(m, p.M - 1)];
       same[c] = __ballot(m < p.M && (other < (uint32_t)p.L ? (int)other : p.L) == e);
       const int left = b - 64 * c;  // rows of this batch ahead of b
       if (left > 0) before += __popcll(left >= 64 ? same[c] : same[c] & ((1ull << left) - 1));
@@ -106,11 +104,11 @@ __device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* ro
   return true;
 }
 
-// t of 16 MT rows and up to 16 RT ranks over one K slice
-template <int ACT, int MT, int RT>
+// t of a 16-row tile and up to 16 RT ranks over one K slice
+template <int ACT, int RT>
 __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p) {
   typedef typename ActT<ACT>::type AT;
-  extern __shared__ __attribute__((aligned(16))) float red[];  // [waves / 2][MT][RT][4][64]
+  extern __shared__ __attribute__((aligned(16))) float red[];  // [waves / 2][RT][4][64]
   __shared__ int rows_of[kTileMax];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -121,29 +119,25 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
   if (e >= p.L) return;  // rows without an adapter
   const int r0 = blockIdx.y * kRankChunk;
   const int koff = 8 * (lane >> 4);
-  const uint16_t *xp[MT], *ap[RT];
+  const uint16_t* ap[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)  // ranks past the last repeat it, never stored
     ap[rt] = p.a + ((size_t)e * p.R + min(r0 + 16 * rt + (lane & 15), p.R - 1)) * p.K + koff;
   __syncthreads();
+  const uint16_t* const xp = p.x + (size_t)rows_of[min(lane & 15, rows - 1)] * p.K + koff;  // and so do rows past the tile
+  f4_t acc[RT];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)  // and so do rows past the tile
-    xp[mt] = p.x + (size_t)rows_of[min(16 * mt + (lane & 15), rows - 1)] * p.K + koff;
-  f4_t acc[MT][RT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) acc[mt][rt] = f4_t{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = kSetSteps(MT);  // steps per register set; one set loads while the other multiplies
+  for (int rt = 0; rt < RT; ++rt) acc[rt] = f4_t{0.f, 0.f, 0.f, 0.f};
+  constexpr int U = kSetSteps;  // steps per register set; one set loads while the other multiplies
   struct Regs {
-    u4_t x[U][MT], a[U][RT];
+    u4_t x[U], a[U][RT];
   };
   // The slice's sets go to the waves in turn, 512 bytes of a row at a time (less where a wave
   // would get none). The rows of x and of A are K apart, at a power of two K all in one memory
   // channel; with the eight waves 512 bytes apart their loads cover 4 KiB of each row, and so every channel.
   const int s0 = slice * p.steps, s1 = min(s0 + p.steps, p.K / 32);
   const int all = (s1 - s0 + U - 1) / U;
-  const int shift = all >= 8 * kShrinkWaves / U ? 3 - kLogU(MT) : all >= 2 * kShrinkWaves ? 1 : 0;
+  const int shift = all >= 2 * kShrinkWaves ? 1 : 0;
   const int full = (all / kShrinkWaves) >> shift;
   const int sets = (full << shift) + min(max(all - ((full * kShrinkWaves + wave) << shift), 0), 1 << shift);
   auto first = [&](int i) __attribute__((always_inline)) {
@@ -153,8 +147,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = 32 * min(first(i) + u, s1 - 1);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) R.x[u][mt] = *reinterpret_cast<const u4_t*>(xp[mt] + k);
+      R.x[u] = *reinterpret_cast<const u4_t*>(xp + k);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) R.a[u][rt] = *reinterpret_cast<const u4_t*>(ap[rt] + k);
     }
@@ -165,10 +158,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
     for (int u = 0; u < U; ++u) {
       if (first(i) + u >= s1) break;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          acc[mt][rt] = mfma16(__builtin_bit_cast(AT, R.x[u][mt]), __builtin_bit_cast(AT, R.a[u][rt]), acc[mt][rt]);
+      for (int rt = 0; rt < RT; ++rt)
+        acc[rt] = mfma16(__builtin_bit_cast(AT, R.x[u]), __builtin_bit_cast(AT, R.a[u][rt]), acc[rt]);
     }
   };
   if (sets > 0) {
@@ -192,32 +183,28 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
   // The waves' sums, in two rounds through half the LDS that all would take (so that two workgroups
   // share a compute unit): wave w + 4's go to wave w, then the four sums in order. Lane l holds
   // rank l%16 and rows 4 (l/16) + i, i < 4.
-  constexpr int H = kShrinkWaves / 2, TILE = MT * RT * 256;
+  constexpr int H = kShrinkWaves / 2, TILE = RT * 256;
   if (wave >= H) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[(wave - H) * TILE + ((mt * RT + rt) * 4 + i) * 64 + lane] = acc[mt][rt][i];
+      for (int i = 0; i < 4; ++i) red[(wave - H) * TILE + (rt * 4 + i) * 64 + lane] = acc[rt][i];
   }
   __syncthreads();
   if (wave < H) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float* const at = red + wave * TILE + ((mt * RT + rt) * 4 + i) * 64 + lane;
-          *at = acc[mt][rt][i] + *at;
-        }
+      for (int i = 0; i < 4; ++i) {
+        float* const at = red + wave * TILE + (rt * 4 + i) * 64 + lane;
+        *at = acc[rt][i] + *at;
+      }
   }
   __syncthreads();
   for (int q = threadIdx.x; q < rows * RT * 16; q += 64 * kShrinkWaves) {
     const int m = q / (RT * 16), r = q - m * (RT * 16);
     if (r0 + r >= p.R) continue;
-    const int at = ((((m >> 4) * RT + (r >> 4)) * 4 + (m & 3)) * 64) + ((m >> 2) & 3) * 16 + (r & 15);
+    const int at = ((r >> 4) * 4 + (m & 3)) * 64 + (m >> 2) * 16 + (r & 15);
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < H; ++w) v += red[w * TILE + at];
@@ -225,14 +212,113 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
   }
 }
 
-// A lane's sixteen columns of a row: access h covers elements kPer h .. of them, at column
-// offset(h) of the strip
+// t of a 64-row tile over one K slice, for prefill: the same product, but with x and A through
+// LDS. Loaded in the MFMA's layout, sixteen lanes touch sixteen rows of x (or of A): a 1 KiB
+// load then takes the address unit 64 cycles, and 66 tiles of 64 rows over 8192 columns took 27 us, three times
+// what the bytes take. Here a 128-column block of both goes from memory straight into one of
+// kStages slots, four rows of 256 bytes per instruction, three blocks ahead of the product. Row r of a slot
+// holds its chunks at positions c ^ (r % 16), so a fragment read touches every bank once. Wave w owns rows
+// 16 w .. 16 w + 15 and every rank, so nothing is added between waves.
+constexpr int kStages = 4, kTallWaves = 4;
+template <int RT>
+constexpr int tall_slot() { return (64 + 16 * RT) * 128; }  // halves
+
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+__device__ __forceinline__ void copy16_to_lds(const uint16_t* src, uint16_t* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+template <int ACT, int RT>
+__global__ __launch_bounds__(64 * kTallWaves) void shrink_tall_kernel(LoraParams p) {
+  typedef typename ActT<ACT>::type AT;
+  constexpr int LOADS = 4 + RT;  // of a wave per block: its sixteen rows of x, its share of A's 16 RT ranks
+  extern __shared__ __attribute__((aligned(16))) uint16_t ring[];  // [kStages][tall_slot]
+  __shared__ int rows_of[kTileMax];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = blockIdx.x / p.slices, slice = blockIdx.x - tile * p.slices;
+  int rows, e;
+  if (!find_tile(p, tile, rows_of, rows, e)) return;
+  if (e >= p.L) return;  // rows without an adapter
+  const int r0 = blockIdx.y * kRankChunk;
+  __syncthreads();
+  // instruction j covers four rows; lane l row l/16 of them, position l%16. Rows and ranks past the last
+  // repeat it, never stored; chunks past a ragged K repeat its last, never multiplied.
+  const uint16_t* src[LOADS];
+  int chunk[LOADS];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int r = j < 4 ? 16 * wave + 4 * j + (lane >> 4) : 4 * (wave * RT + j - 4) + (lane >> 4);
+    chunk[j] = 8 * ((lane & 15) ^ (r & 15));
+    src[j] = j < 4 ? p.x + (size_t)rows_of[min(r, rows - 1)] * p.K
+                   : p.a + ((size_t)e * p.R + min(r0 + r, p.R - 1)) * p.K;
+  }
+  auto load = [&](int kb, int slot) __attribute__((always_inline)) {
+    uint16_t* const base = ring + slot * tall_slot<RT>();
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      uint16_t* const dst = base + (j < 4 ? 16 * wave + 4 * j : 64 + 4 * (wave * RT + j - 4)) * 128;
+      copy16_to_lds(src[j] + min(128 * kb + chunk[j], p.K - 8), dst);
+    }
+  };
+  f4_t acc[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) acc[rt] = f4_t{0.f, 0.f, 0.f, 0.f};
+  const int b0 = slice * p.steps / 4, b1 = min(b0 + p.steps / 4, (p.K + 127) / 128);  // steps: whole blocks
+  const int nb = b1 - b0;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i)
+    if (i < nb) load(b0 + i, i);
+  for (int i = 0; i < nb; ++i) {
+    // block i has landed: only the loads of the up to two blocks after it may be in flight
+    const int later = nb - 1 - i;
+    if (later >= 2)
+      wait_loads<2 * LOADS>();
+    else if (later == 1)
+      wait_loads<LOADS>();
+    else
+      wait_loads<0>();
+    __builtin_amdgcn_s_barrier();  // every wave's part of it, and every wave is done with block i - 1
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + kStages - 1 < nb) load(b0 + i + kStages - 1, (i + kStages - 1) % kStages);
+    const uint16_t* const base = ring + (i % kStages) * tall_slot<RT>();
+    const int row = lane & 15;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (128 * (b0 + i) + 32 * s >= p.K) break;
+      const int at = ((4 * s + (lane >> 4)) ^ row) * 8;
+      const u4_t xv = *reinterpret_cast<const u4_t*>(base + (16 * wave + row) * 128 + at);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const u4_t av = *reinterpret_cast<const u4_t*>(base + (64 + 16 * rt + row) * 128 + at);
+        acc[rt] = mfma16(__builtin_bit_cast(AT, xv), __builtin_bit_cast(AT, av), acc[rt]);
+      }
+    }
+  }
+  // lane l holds rank l%16 of each tile and rows 4 (l/16) + i, i < 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = 16 * wave + 4 * (lane >> 4) + i;
+    if (m >= rows) continue;
+    float* const part = p.part + ((size_t)slice * p.M + rows_of[m]) * p.R + r0;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+      if (r0 + 16 * rt + (lane & 15) < p.R) part[16 * rt + (lane & 15)] = acc[rt][i];
+  }
+}
+
+// Sixteen bytes of a row of y or out per lane and access: kPer columns; a 16 x 64 tile takes
+// kAccesses of them, access h rows kRows h .. of the tile
 template <int YT>
 struct Cols {
-  static constexpr int kPer = YT == T_F32 ? 4 : 8, kAccesses = 16 / kPer;
-  static __device__ __forceinline__ int offset(int h, int g) {
-    return YT == T_F32 ? 32 * (h >> 1) + 8 * g + 4 * (h & 1) : 32 * h + 8 * g;
-  }
+  static constexpr int kPer = YT == T_F32 ? 4 : 8, kLanes = 64 / kPer, kRows = 64 / kLanes, kAccesses = 16 / kRows;
 };
 template <int YT>
 __device__ __forceinline__ u4_t load_cols(const void* base, size_t at) {
@@ -246,27 +332,24 @@ __device__ __forceinline__ void store_cols(void* base, size_t at, u4_t v) {
   else
     *reinterpret_cast<u4_t*>(static_cast<uint16_t*>(base) + at) = v;
 }
-// v + back * acc for the elements of access h, rounded once to the type
+// v + back * d for an access's columns, rounded once to the type
 template <int YT>
-__device__ __forceinline__ u4_t add_cols(u4_t v, const f4_t* acc, float back) {
+__device__ __forceinline__ u4_t add_cols(u4_t v, const float* d, float back) {
   u4_t r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    const uint32_t bits = v[i];  // a vector's element is no object of its own to a bit cast
     if constexpr (YT == T_F32) {
-      const uint32_t bits = v[i];  // a vector's element is no object of its own to a bit cast
-      const float sum = __builtin_fmaf(back, acc[0][i], __builtin_bit_cast(float, bits));
+      const float sum = __builtin_fmaf(back, d[i], __builtin_bit_cast(float, bits));
       r[i] = __builtin_bit_cast(uint32_t, sum);
+    } else if constexpr (YT == T_F16) {
+      const h2_t y = as_h2(bits);
+      const float lo = __builtin_fmaf(back, d[2 * i], (float)y[0]), hi = __builtin_fmaf(back, d[2 * i + 1], (float)y[1]);
+      r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
     } else {
-      const float a0 = acc[i >> 1][2 * (i & 1)], a1 = acc[i >> 1][2 * (i & 1) + 1];
-      if constexpr (YT == T_F16) {
-        const float lo = __builtin_fmaf(back, a0, (float)__builtin_bit_cast(_Float16, (uint16_t)v[i]));
-        const float hi = __builtin_fmaf(back, a1, (float)__builtin_bit_cast(_Float16, (uint16_t)(v[i] >> 16)));
-        r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
-      } else {
-        const float lo = __builtin_fmaf(back, a0, __builtin_bit_cast(float, v[i] << 16));
-        const float hi = __builtin_fmaf(back, a1, __builtin_bit_cast(float, v[i] & 0xFFFF0000u));
-        r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16;
-      }
+      const float lo = __builtin_fmaf(back, d[2 * i], __builtin_bit_cast(float, bits << 16));
+      const float hi = __builtin_fmaf(back, d[2 * i + 1], __builtin_bit_cast(float, bits & 0xFFFF0000u));
+      r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16;
     }
   }
   return r;
@@ -296,12 +379,18 @@ constexpr int parts_of() { return ACT == ACT_BF16 && YT == T_F32 ? 3 : 2; }
 // eight rows fall in different banks
 constexpr int part_stride(int RS) { return 32 * RS + 8; }
 
-// RS: 32-rank steps
-template <int ACT, int YT, int RS>
+// floats between rows of a wave's 16 x 64 product in LDS
+constexpr int kTurnStride = 68;
+constexpr size_t turn_bytes() { return 16 * kTurnStride * 4; }
+
+// RS: 32-rank steps. TALL: tiles of up to 64 rows, one strip a wave, whose y is all in flight before
+// t is split; else tiles of 16 rows, several strips, the next one's B and y in flight.
+template <int ACT, int YT, int RS, bool TALL>
 __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p) {
   typedef typename ActT<ACT>::type AT;
-  constexpr int PARTS = parts_of<ACT, YT>(), STRIDE = part_stride(RS), NH = Cols<YT>::kAccesses;
-  extern __shared__ __attribute__((aligned(16))) uint16_t tp[];  // [tile rows][PARTS][STRIDE]
+  typedef Cols<YT> Y;
+  constexpr int PARTS = parts_of<ACT, YT>(), STRIDE = part_stride(RS), NH = Y::kAccesses;
+  extern __shared__ __attribute__((aligned(16))) uint16_t tp[];  // [tile rows][PARTS][STRIDE], then the waves' own
   __shared__ int rows_of[kTileMax];
   __shared__ float backs[kTileMax];
   const int lane = threadIdx.x & 63, g = lane >> 4;
@@ -315,24 +404,24 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
   constexpr int step = 64 * kExpandWaves;
   const int n_first = cg * p.strips * step + wave * 64;
   const int n_end = min(p.N, (cg + 1) * p.strips * step);
+  const int yrow = lane / Y::kLanes, ycol = (lane % Y::kLanes) * Y::kPer;  // N is a multiple of 16: an access is all in or out
   if (e >= p.L) {  // no adapter: out is y
     if (p.out == p.y) return;
     __syncthreads();
     for (int n0 = n_first; n0 < n_end; n0 += step)
-      for (int m = lane & 15; m < rows; m += 16)
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const int n = n0 + Cols<YT>::offset(h, g);
-          const size_t at = (size_t)rows_of[m] * p.N + n;
-          if (n < p.N) store_cols<YT>(p.out, at, load_cols<YT>(p.y, at));
-        }
+      for (int m = yrow; m < rows; m += Y::kRows) {
+        const size_t at = (size_t)rows_of[m] * p.N + n0 + ycol;
+        if (n0 + ycol < p.N) store_cols<YT>(p.out, at, load_cols<YT>(p.y, at));
+      }
     return;
   }
+  char* const own = reinterpret_cast<char*>(tp) + (size_t)p.tile_rows * PARTS * STRIDE * 2;
+  float* const turn = reinterpret_cast<float*>(own + wave * turn_bytes());
   const uint16_t* const b = p.b + (size_t)e * p.N * p.R;
   auto load_b = [&](u4_t (&v)[4][RS], int n0) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int i = lane & 15, n = min(n0 + 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3), p.N - 1);
+      const int n = min(n0 + 16 * q + (lane & 15), p.N - 1);
 #pragma unroll
       for (int rs = 0; rs < RS; ++rs) {
         const int r = 32 * rs + 8 * g;  // R is a multiple of 8
@@ -340,20 +429,20 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
       }
     }
   };
-  // N is a multiple of 16: an access is all in or out
   auto load_y = [&](u4_t (&v)[NH], int n0, int m0) __attribute__((always_inline)) {
-    const size_t row = (size_t)rows_of[min(m0 + (lane & 15), rows - 1)] * p.N;
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      const int n = n0 + Cols<YT>::offset(h, g);
-      if (n < p.N) v[h] = load_cols<YT>(p.y, row + n);
-    }
+    for (int h = 0; h < NH; ++h)
+      if (n0 + ycol < p.N)
+        v[h] = load_cols<YT>(p.y, (size_t)rows_of[min(m0 + Y::kRows * h + yrow, rows - 1)] * p.N + n0 + ycol);
   };
-  u4_t bv[4][RS], yv[NH];
+  constexpr int TILES = TALL ? kTileMax / 16 : 1;
+  u4_t bv[4][RS], yv[TILES][NH];
   load_b(bv, n_first);
   const float scaling = p.scaling[e];
   __syncthreads();  // rows_of
-  load_y(yv, n_first, 0);
+#pragma unroll
+  for (int k = 0; k < TILES; ++k)
+    if (16 * k < rows) load_y(yv[k], n_first, 16 * k);
   // the rows' t: 4 RS threads a row, eight ranks each
   constexpr int C = 4 * RS;
   for (int q = threadIdx.x; q < ((rows + 15) & ~15) * C; q += 64 * kExpandWaves) {
@@ -365,7 +454,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
       const float* src = p.part + (size_t)rows_of[min(row, rows - 1)] * p.R + r;
       const size_t next = (size_t)p.M * p.R;
       for (int s0 = 0; s0 < p.slices; s0 += 4) {
-        f4_t lo[4], hi[4];
+        f4_t lo[4], hi[4];  // four slices' loads in flight
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const float* v = src + min(s0 + s, p.slices - 1) * next;
@@ -373,14 +462,12 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
           hi[s] = *reinterpret_cast<const f4_t*>(v + 4);
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (s0 + s >= p.slices) break;
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            t[i] += lo[s][i];
-            t[4 + i] += hi[s][i];
+            t[i] += s0 + s < p.slices ? lo[s][i] : 0.f;
+            t[4 + i] += s0 + s < p.slices ? hi[s][i] : 0.f;
           }
-        }
       }
     }
     float back = scaling;
@@ -405,8 +492,10 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
     if (r == 0) backs[row] = back;
   }
   __syncthreads();
+  // one 16 x 64 tile: the product turned through LDS, so that y and out are accessed by whole runs of a
+  // row (lane l holds row l%16 and columns 16 q + 4 (l/16) .. + 3 of it; straight from there, sixteen lanes would
+  // access sixteen rows)
   auto add_tile = [&](const u4_t (&y)[NH], int n0, int m0) __attribute__((always_inline)) {
-    const int m = m0 + (lane & 15);
     f4_t acc[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] = f4_t{0.f, 0.f, 0.f, 0.f};
@@ -414,39 +503,40 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
     for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
       for (int s = 0; s < PARTS; ++s) {
-        const u4_t t = *reinterpret_cast<const u4_t*>(tp + (m * PARTS + s) * STRIDE + 32 * rs + 8 * g);
+        const u4_t t = *reinterpret_cast<const u4_t*>(tp + ((m0 + (lane & 15)) * PARTS + s) * STRIDE + 32 * rs + 8 * g);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           acc[q] = mfma16(__builtin_bit_cast(AT, bv[q][rs]), __builtin_bit_cast(AT, t), acc[q]);
       }
-    if (m >= rows) return;
-    const size_t row = (size_t)rows_of[m] * p.N;
-    const float back = backs[m];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<f4_t*>(turn + (lane & 15) * kTurnStride + 16 * q + 4 * g) = acc[q];
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      const int n = n0 + Cols<YT>::offset(h, g);
-      if (n < p.N) store_cols<YT>(p.out, row + n, add_cols<YT>(y[h], acc + h * (4 / NH), back));
+      const int r = Y::kRows * h + yrow, m = m0 + r;
+      float d[Y::kPer];
+#pragma unroll
+      for (int i = 0; i < Y::kPer; i += 4)
+        *reinterpret_cast<f4_t*>(d + i) = *reinterpret_cast<const f4_t*>(turn + r * kTurnStride + ycol + i);
+      if (m < rows && n0 + ycol < p.N)
+        store_cols<YT>(p.out, (size_t)rows_of[m] * p.N + n0 + ycol, add_cols<YT>(y[h], d, backs[m]));
     }
+    __builtin_amdgcn_wave_barrier();
   };
-  // One strip; y of the next tile (and with MORE the next strip's first y and B) loads meanwhile. Loads
-  // under a branch would make the compiler wait for all that are in flight, so the last tile
-  // and the last strip are passes of their own.
+  // One strip; with MORE the next strip's B and y load meanwhile. Loads under a branch would make the
+  // compiler wait for all that are in flight, so the last strip is a pass of its own.
   auto strip = [&](int n0, auto more) __attribute__((always_inline)) {
     constexpr bool MORE = decltype(more)::value, AHEAD = MORE && RS <= 2;
-    u4_t bn[4][RS], next[NH];
+    u4_t next[NH], bn[4][RS];
     if constexpr (AHEAD) load_b(bn, n0 + step);
-    int m0 = 0;
-    for (; m0 + 16 < rows; m0 += 16) {
-      load_y(next, n0, m0 + 16);
-      add_tile(yv, n0, m0);
-#pragma unroll
-      for (int h = 0; h < NH; ++h) yv[h] = next[h];
-    }
     if constexpr (MORE) load_y(next, n0 + step, 0);
-    add_tile(yv, n0, m0);
+#pragma unroll
+    for (int k = 0; k < TILES; ++k)
+      if (16 * k < rows) add_tile(yv[k], n0, 16 * k);
     if constexpr (MORE) {
 #pragma unroll
-      for (int h = 0; h < NH; ++h) yv[h] = next[h];
+      for (int h = 0; h < NH; ++h) yv[0][h] = next[h];
       if constexpr (AHEAD) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -458,7 +548,8 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
     }
   };
   int n0 = n_first;
-  for (; n0 + step < n_end; n0 += step) strip(n0, std::true_type{});
+  if constexpr (!TALL)
+    for (; n0 + step < n_end; n0 += step) strip(n0, std::true_type{});
   if (n0 < n_end) strip(n0, std::false_type{});
 }
 
@@ -481,8 +572,7 @@ LoraGeometry lora_geometry(int M, int K, int N, int L, int R) {
   if (slices > most) slices = most;
   if (slices > kMaxSlices) slices = kMaxSlices;
   if (slices < 1) slices = 1;
-  const int set = kSetSteps(kTileRows[g.list] / 16);
-  g.steps = ceil_div(ceil_div(steps, slices), set) * set;
+  g.steps = ceil_div(ceil_div(steps, slices), kSetSteps) * kSetSteps;  // whole sets, whole 128-column blocks
   g.slices = ceil_div(steps, g.steps);
   // strips per wave (each saves the others' search for rows and splitting of t) while two workgroups
   // a compute unit are left
@@ -493,30 +583,47 @@ LoraGeometry lora_geometry(int M, int K, int N, int L, int R) {
   return g;
 }
 
-template <int ACT, int MT>
-void launch_shrink(const LoraParams& p, dim3 grid, hipStream_t s) {
+template <int ACT>
+void launch_shrink(const LoraParams& p, bool tall, dim3 grid, hipStream_t s) {
+  if (tall) {
+    const dim3 block(64 * kTallWaves);
+    if (p.R <= 16)
+      hipLaunchKernelGGL((shrink_tall_kernel<ACT, 1>), grid, block, kStages * tall_slot<1>() * 2, s, p);
+    else if (p.R <= 32)
+      hipLaunchKernelGGL((shrink_tall_kernel<ACT, 2>), grid, block, kStages * tall_slot<2>() * 2, s, p);
+    else
+      hipLaunchKernelGGL((shrink_tall_kernel<ACT, 4>), grid, block, kStages * tall_slot<4>() * 2, s, p);
+    return;
+  }
   const dim3 block(64 * kShrinkWaves);
-  const size_t lds = (size_t)kShrinkWaves / 2 * MT * 256 * 4;  // per rank tile
+  const size_t lds = (size_t)kShrinkWaves / 2 * 256 * 4;  // per rank tile
   if (p.R <= 16)
-    hipLaunchKernelGGL((shrink_kernel<ACT, MT, 1>), grid, block, lds, s, p);
+    hipLaunchKernelGGL((shrink_kernel<ACT, 1>), grid, block, lds, s, p);
   else if (p.R <= 32)
-    hipLaunchKernelGGL((shrink_kernel<ACT, MT, 2>), grid, block, 2 * lds, s, p);
+    hipLaunchKernelGGL((shrink_kernel<ACT, 2>), grid, block, 2 * lds, s, p);
   else
-    hipLaunchKernelGGL((shrink_kernel<ACT, MT, 4>), grid, block, 4 * lds, s, p);
+    hipLaunchKernelGGL((shrink_kernel<ACT, 4>), grid, block, 4 * lds, s, p);
+}
+
+template <int ACT, int YT, int RS>
+void launch_expand_rs(const LoraParams& p, dim3 grid, hipStream_t s) {
+  const size_t lds = (size_t)p.tile_rows * parts_of<ACT, YT>() * part_stride(RS) * 2 + kExpandWaves * turn_bytes();
+  if (p.tile_rows > 16)
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, true>), grid, dim3(64 * kExpandWaves), lds, s, p);
+  else
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, false>), grid, dim3(64 * kExpandWaves), lds, s, p);
 }
 
 template <int ACT, int YT>
 void launch_expand(const LoraParams& p, dim3 grid, hipStream_t s) {
-  const dim3 block(64 * kExpandWaves);
-  const size_t lds = (size_t)p.tile_rows * parts_of<ACT, YT>() * 2;  // per half of a part's row
   if (p.R <= 32)
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 1>), grid, block, lds * part_stride(1), s, p);
+    launch_expand_rs<ACT, YT, 1>(p, grid, s);
   else if (p.R <= 64)
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 2>), grid, block, lds * part_stride(2), s, p);
+    launch_expand_rs<ACT, YT, 2>(p, grid, s);
   else if (p.R <= 128)
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 4>), grid, block, lds * part_stride(4), s, p);
+    launch_expand_rs<ACT, YT, 4>(p, grid, s);
   else
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, 8>), grid, block, lds * part_stride(8), s, p);
+    launch_expand_rs<ACT, YT, 8>(p, grid, s);
 }
 
 // tiles found by the workgroups themselves: few rows, no plan
@@ -574,9 +681,9 @@ hipError_t launch_lora(const LoraArgs& a) {
   p.strips = g.strips;
   const dim3 sgrid(tiles * g.slices, ceil_div(a.R, kRankChunk));
   if (a.act == ACT_F16)
-    g.list ? launch_shrink<ACT_F16, 4>(p, sgrid, a.stream) : launch_shrink<ACT_F16, 1>(p, sgrid, a.stream);
+    launch_shrink<ACT_F16>(p, g.list != 0, sgrid, a.stream);
   else
-    g.list ? launch_shrink<ACT_BF16, 4>(p, sgrid, a.stream) : launch_shrink<ACT_BF16, 1>(p, sgrid, a.stream);
+    launch_shrink<ACT_BF16>(p, g.list != 0, sgrid, a.stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   p.col_groups = ceil_div(a.N, 64 * kExpandWaves * g.strips);
