@@ -6,11 +6,12 @@
 // A workgroup takes a tile of rows with one adapter, so at decode the adapters' bytes
 // R (K + N) bound the call, at prefill those of x, y and out.
 //
-// Tiles. Up to 256 rows, workgroup b looks at row b: if the row is the first, 17th, 33rd.. of
-// its adapter, the tile is that row and the next fifteen of the adapter, found with one
-// ballot per 64 ids; else it leaves. More rows (or a plan in hand) take the plan's tile lists.
+// Tiles. Up to 96 rows, workgroup b looks at row b: if the row is the first, 17th, 33rd.. of its
+// adapter, the tile is that row and the next fifteen of the adapter, found with one ballot
+// per 64 ids; else it leaves. That saves the sort's launch (5 us; at 256 rows the workgroups that leave
+// cost more: 33 us against 16 + 5 at 8192x8192 rank 64). More rows, or a plan in hand, take the plan's tile lists.
 //
-// Two launches. The first forms t = x A^T, at most R values a row: a workgroup takes a tile of
+// Two launches, or one where t is cheap (below). The first forms t = x A^T, at most R values a row: a workgroup takes a tile of
 // rows and a slice of K, its waves parts of the slice, added through LDS in wave order; the
 // slices' fp32 sums go to the workspace. The second adds the slices in order and multiplies
 // by B.
@@ -46,11 +47,11 @@ template <>
 struct ActT<ACT_BF16> { typedef b8_t type; };
 
 constexpr int kShrinkWaves = 8;
-constexpr int kExpandWaves = 4;
+constexpr int expand_waves(bool one) { return one ? kShrinkWaves : 4; }  // of the second product
 constexpr int kRankChunk = 64;   // ranks per workgroup of the first product
 constexpr int kMaxSlices = 16;
 constexpr int kSetSteps = 4;     // 32-deep steps of a register set in the first product
-constexpr int kSelfRows = 256;   // most rows whose tiles the workgroups find themselves
+constexpr int kSelfRows = 96;    // most rows whose tiles the workgroups find themselves
 constexpr int kTileMax = 64;     // most rows of a tile
 
 struct LoraParams {
@@ -76,10 +77,11 @@ __device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* ro
     const int b = tile;
     const uint32_t id = (uint32_t)p.ids[b];
     e = id < (uint32_t)p.L ? (int)id : p.L;
-    uint64_t same[kSelfRows / 64];
+    constexpr int kBatches = (kSelfRows + 63) / 64;
+    uint64_t same[kBatches];
     int before = 0;  // rows of this adapter ahead of row b
 #pragma unroll
-    for (int c = 0; c < kSelfRows / 64; ++c) {
+    for (int c = 0; c < kBatches; ++c) {
       const int m = 64 * c + lane;
       const uint32_t other = (uint32_t)p.ids[min(m, p.M - 1)];
       same[c] = __ballot(m < p.M && (other < (uint32_t)p.L ? (int)other : p.L) == e);
@@ -89,7 +91,7 @@ __device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* ro
     if (before & 15) return false;
     int at = 0;  // rows of the adapter seen
 #pragma unroll
-    for (int c = 0; c < kSelfRows / 64; ++c) {
+    for (int c = 0; c < kBatches; ++c) {
       const int pos = at + __popcll(same[c] & ((1ull << lane) - 1)) - before;
       if (((same[c] >> lane) & 1) && pos >= 0 && pos < 16 && threadIdx.x < 64) rows_of[pos] = 64 * c + lane;
       at += __popcll(same[c]);
@@ -104,26 +106,19 @@ __device__ __forceinline__ bool find_tile(const LoraParams& p, int tile, int* ro
   return true;
 }
 
-// t of a 16-row tile and up to 16 RT ranks over one K slice
+// t of a 16-row tile and up to 16 RT ranks from r0 on, over the 32-deep steps [s0, s1), by kShrinkWaves waves
+// (rows_of complete). It ends in red, [kShrinkWaves / 2][RT][4][64], whose first index shrink_sum adds up.
 template <int ACT, int RT>
-__global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p) {
+__device__ __forceinline__ void shrink_tile(const LoraParams& p, const int* rows_of, int rows, int e, int r0, int s0,
+                                            int s1, float* red) {
   typedef typename ActT<ACT>::type AT;
-  extern __shared__ __attribute__((aligned(16))) float red[];  // [waves / 2][RT][4][64]
-  __shared__ int rows_of[kTileMax];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // consecutive workgroups (on consecutive XCDs) take a tile's slices
-  const int tile = blockIdx.x / p.slices, slice = blockIdx.x - tile * p.slices;
-  int rows, e;
-  if (!find_tile(p, tile, rows_of, rows, e)) return;
-  if (e >= p.L) return;  // rows without an adapter
-  const int r0 = blockIdx.y * kRankChunk;
   const int koff = 8 * (lane >> 4);
   const uint16_t* ap[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)  // ranks past the last repeat it, never stored
     ap[rt] = p.a + ((size_t)e * p.R + min(r0 + 16 * rt + (lane & 15), p.R - 1)) * p.K + koff;
-  __syncthreads();
   const uint16_t* const xp = p.x + (size_t)rows_of[min(lane & 15, rows - 1)] * p.K + koff;  // and so do rows past the tile
   f4_t acc[RT];
 #pragma unroll
@@ -135,7 +130,6 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
   // The slice's sets go to the waves in turn, 512 bytes of a row at a time (less where a wave
   // would get none). The rows of x and of A are K apart, at a power of two K all in one memory
   // channel; with the eight waves 512 bytes apart their loads cover 4 KiB of each row, and so every channel.
-  const int s0 = slice * p.steps, s1 = min(s0 + p.steps, p.K / 32);
   const int all = (s1 - s0 + U - 1) / U;
   const int shift = all >= 2 * kShrinkWaves ? 1 : 0;
   const int full = (all / kShrinkWaves) >> shift;
@@ -201,14 +195,33 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
       }
   }
   __syncthreads();
+}
+// rank r (of the tile's 16 RT) of row m of it
+template <int RT>
+__device__ __forceinline__ float shrink_sum(const float* red, int m, int r) {
+  const int at = ((r >> 4) * 4 + (m & 3)) * 64 + (m >> 2) * 16 + (r & 15);
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kShrinkWaves / 2; ++w) v += red[w * RT * 256 + at];
+  return v;
+}
+
+// one K slice of t
+template <int ACT, int RT>
+__global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p) {
+  extern __shared__ __attribute__((aligned(16))) float red[];
+  __shared__ int rows_of[kTileMax];
+  // consecutive workgroups (on consecutive XCDs) take a tile's slices
+  const int tile = blockIdx.x / p.slices, slice = blockIdx.x - tile * p.slices;
+  int rows, e;
+  if (!find_tile(p, tile, rows_of, rows, e)) return;
+  if (e >= p.L) return;  // rows without an adapter
+  __syncthreads();
+  const int r0 = blockIdx.y * kRankChunk, s0 = slice * p.steps;
+  shrink_tile<ACT, RT>(p, rows_of, rows, e, r0, s0, min(s0 + p.steps, p.K / 32), red);
   for (int q = threadIdx.x; q < rows * RT * 16; q += 64 * kShrinkWaves) {
     const int m = q / (RT * 16), r = q - m * (RT * 16);
-    if (r0 + r >= p.R) continue;
-    const int at = ((r >> 4) * 4 + (m & 3)) * 64 + (m >> 2) * 16 + (r & 15);
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < H; ++w) v += red[w * TILE + at];
-    p.part[((size_t)slice * p.M + rows_of[m]) * p.R + r0 + r] = v;
+    if (r0 + r < p.R) p.part[((size_t)slice * p.M + rows_of[m]) * p.R + r0 + r] = shrink_sum<RT>(red, m, r);
   }
 }
 
@@ -385,11 +398,13 @@ constexpr size_t turn_bytes() { return 16 * kTurnStride * 4; }
 
 // RS: 32-rank steps. TALL: tiles of up to 64 rows, one strip a wave, whose y is all in flight before
 // t is split; else tiles of 16 rows, several strips, the next one's B and y in flight.
-template <int ACT, int YT, int RS, bool TALL>
-__global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p) {
+// RT > 0: t is formed here too, 16 RT ranks by every workgroup of a tile for itself (no slices, one launch).
+template <int ACT, int YT, int RS, bool TALL, int RT = 0>
+__global__ __launch_bounds__(64 * expand_waves(RT > 0)) void expand_kernel(LoraParams p) {
   typedef typename ActT<ACT>::type AT;
+  constexpr bool ONE = RT > 0;
   typedef Cols<YT> Y;
-  constexpr int PARTS = parts_of<ACT, YT>(), STRIDE = part_stride(RS), NH = Y::kAccesses;
+  constexpr int PARTS = parts_of<ACT, YT>(), STRIDE = part_stride(RS), NH = Y::kAccesses, W = expand_waves(ONE);
   extern __shared__ __attribute__((aligned(16))) uint16_t tp[];  // [tile rows][PARTS][STRIDE], then the waves' own
   __shared__ int rows_of[kTileMax];
   __shared__ float backs[kTileMax];
@@ -401,7 +416,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
   int rows, e;
   if (!find_tile(p, tile, rows_of, rows, e)) return;
   // this wave's strips of 64 columns: n_first, n_first + step, ... below n_end
-  constexpr int step = 64 * kExpandWaves;
+  constexpr int step = 64 * W;
   const int n_first = cg * p.strips * step + wave * 64;
   const int n_end = min(p.N, (cg + 1) * p.strips * step);
   const int yrow = lane / Y::kLanes, ycol = (lane % Y::kLanes) * Y::kPer;  // N is a multiple of 16: an access is all in or out
@@ -443,14 +458,20 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
 #pragma unroll
   for (int k = 0; k < TILES; ++k)
     if (16 * k < rows) load_y(yv[k], n_first, 16 * k);
+  __shared__ __attribute__((aligned(16))) float red[ONE ? kShrinkWaves / 2 * RT * 256 : 1];
+  if constexpr (ONE) shrink_tile<ACT, ONE ? RT : 1>(p, rows_of, rows, e, 0, 0, p.K / 32, red);
   // the rows' t: 4 RS threads a row, eight ranks each
   constexpr int C = 4 * RS;
-  for (int q = threadIdx.x; q < ((rows + 15) & ~15) * C; q += 64 * kExpandWaves) {
+  for (int q = threadIdx.x; q < ((rows + 15) & ~15) * C; q += 64 * W) {
     const int row = q / C, r = 8 * (q - row * C);
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = 0.f;
-    if (r < p.R) {
+    if constexpr (ONE) {
+      if (r < p.R)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = shrink_sum<ONE ? RT : 1>(red, row, r + i);
+    } else if (r < p.R) {
       const float* src = p.part + (size_t)rows_of[min(row, rows - 1)] * p.R + r;
       const size_t next = (size_t)p.M * p.R;
       for (int s0 = 0; s0 < p.slices; s0 += 4) {
@@ -553,13 +574,21 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(LoraParams p)
   if (n0 < n_end) strip(n0, std::false_type{});
 }
 
+// tiles found by the workgroups themselves: few rows, no plan
+bool self_tiles(int M, bool planned) { return !planned && M <= kSelfRows; }
+
 struct LoraGeometry {
   int list;  // tile list
   int slices, steps, strips;
+  bool one;  // both products in one launch
 };
 
-LoraGeometry lora_geometry(int M, int K, int N, int L, int R) {
+LoraGeometry lora_geometry(int M, int K, int N, int L, int R, bool self) {
   LoraGeometry g;
+  // One launch where every workgroup can afford its tile's t: an adapter's A of at most 256 KiB, read by all the
+  // workgroups of a tile of 512 columns (from L2), 16 MiB of such reads in all.
+  g.one = self && R <= kRankChunk && (long long)R * K <= (1 << 17) &&
+          (long long)M * ceil_div(N, 64 * expand_waves(true)) * R * K <= (1 << 23);
   const int groups = L < M ? L : M;
   g.list = M / (groups > 0 ? groups : 1) >= 48 ? 2 : 0;
   // tiles to expect: full ones, and about one part-filled for every second adapter
@@ -576,10 +605,10 @@ LoraGeometry lora_geometry(int M, int K, int N, int L, int R) {
   g.slices = ceil_div(steps, g.steps);
   // strips per wave (each saves the others' search for rows and splitting of t) while two workgroups
   // a compute unit are left
-  const long long wgs = tiles * ceil_div(N, 64 * kExpandWaves);
+  const long long wgs = tiles * ceil_div(N, 64 * expand_waves(false));
   g.strips = g.list ? 1 : (int)(wgs / (2 * cus));
   if (g.strips > 8) g.strips = 8;
-  if (g.strips < 1) g.strips = 1;
+  if (g.strips < 1 || g.one) g.strips = 1;
   return g;
 }
 
@@ -605,13 +634,31 @@ void launch_shrink(const LoraParams& p, bool tall, dim3 grid, hipStream_t s) {
     hipLaunchKernelGGL((shrink_kernel<ACT, 4>), grid, block, 4 * lds, s, p);
 }
 
+template <int ACT, int YT>
+constexpr size_t expand_lds(int tile_rows, int RS, bool one) {
+  return (size_t)tile_rows * parts_of<ACT, YT>() * part_stride(RS) * 2 + expand_waves(one) * turn_bytes();
+}
+
 template <int ACT, int YT, int RS>
 void launch_expand_rs(const LoraParams& p, dim3 grid, hipStream_t s) {
-  const size_t lds = (size_t)p.tile_rows * parts_of<ACT, YT>() * part_stride(RS) * 2 + kExpandWaves * turn_bytes();
+  const dim3 block(64 * expand_waves(false));
+  const size_t lds = expand_lds<ACT, YT>(p.tile_rows, RS, false);
   if (p.tile_rows > 16)
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, true>), grid, dim3(64 * kExpandWaves), lds, s, p);
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, true>), grid, block, lds, s, p);
   else
-    hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, false>), grid, dim3(64 * kExpandWaves), lds, s, p);
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, false>), grid, block, lds, s, p);
+}
+
+template <int ACT, int YT>
+void launch_one(const LoraParams& p, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * expand_waves(true));
+  const size_t lds = expand_lds<ACT, YT>(16, p.R <= 32 ? 1 : 2, true);
+  if (p.R <= 16)
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, 1, false, 1>), grid, block, lds, s, p);
+  else if (p.R <= 32)
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, 1, false, 2>), grid, block, lds, s, p);
+  else
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, 2, false, 4>), grid, block, lds, s, p);
 }
 
 template <int ACT, int YT>
@@ -626,25 +673,25 @@ void launch_expand(const LoraParams& p, dim3 grid, hipStream_t s) {
     launch_expand_rs<ACT, YT, 8>(p, grid, s);
 }
 
-// tiles found by the workgroups themselves: few rows, no plan
-bool self_tiles(int M, bool planned) { return !planned && M <= kSelfRows; }
-
 }  // namespace
 
 size_t lora_workspace_bytes(int M, int K, int N, int L, int R, bool planned) {
-  const LoraGeometry g = lora_geometry(M, K, N, L, R);
-  const size_t plan = planned || self_tiles(M, planned) ? 0 : align256((size_t)route_layout(M, 1, L).words * 4);
+  const bool self = self_tiles(M, planned);
+  const LoraGeometry g = lora_geometry(M, K, N, L, R, self);
+  if (g.one) return 0;
+  const size_t plan = planned || self ? 0 : align256((size_t)route_layout(M, 1, L).words * 4);
   return plan + align256((size_t)g.slices * M * R * 4);
 }
 
 hipError_t launch_lora(const LoraArgs& a) {
-  LoraGeometry g = lora_geometry(a.M, a.K, a.N, a.L, a.R);
+  const bool self = self_tiles(a.M, a.plan != nullptr);
+  LoraGeometry g = lora_geometry(a.M, a.K, a.N, a.L, a.R, self);
   char* ws = static_cast<char*>(a.workspace);
   LoraParams p;
   p.ids = nullptr;
   p.groups = GroupTiles{};
   int tiles = a.M;  // of a launch
-  if (self_tiles(a.M, a.plan != nullptr)) {
+  if (self) {
     p.ids = a.ids;
     g.list = 0;
   } else {
@@ -679,6 +726,15 @@ hipError_t launch_lora(const LoraArgs& a) {
   p.steps = g.steps;
   p.tile_rows = kTileRows[g.list];
   p.strips = g.strips;
+  p.col_groups = ceil_div(a.N, 64 * expand_waves(g.one) * g.strips);
+  const dim3 egrid(tiles * p.col_groups);
+  if (g.one) {
+    if (a.act == ACT_F16)
+      a.ydtype == T_F32 ? launch_one<ACT_F16, T_F32>(p, egrid, a.stream) : launch_one<ACT_F16, T_F16>(p, egrid, a.stream);
+    else
+      a.ydtype == T_F32 ? launch_one<ACT_BF16, T_F32>(p, egrid, a.stream) : launch_one<ACT_BF16, T_BF16>(p, egrid, a.stream);
+    return hipGetLastError();
+  }
   const dim3 sgrid(tiles * g.slices, ceil_div(a.R, kRankChunk));
   if (a.act == ACT_F16)
     launch_shrink<ACT_F16>(p, g.list != 0, sgrid, a.stream);
@@ -686,8 +742,6 @@ hipError_t launch_lora(const LoraArgs& a) {
     launch_shrink<ACT_BF16>(p, g.list != 0, sgrid, a.stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  p.col_groups = ceil_div(a.N, 64 * kExpandWaves * g.strips);
-  const dim3 egrid(tiles * p.col_groups);
   if (a.act == ACT_F16)
     a.ydtype == T_F32 ? launch_expand<ACT_F16, T_F32>(p, egrid, a.stream) : launch_expand<ACT_F16, T_F16>(p, egrid, a.stream);
   else
