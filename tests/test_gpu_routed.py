@@ -283,6 +283,9 @@ def test_grouped_every_format(act, fmt, g, glu):
     (24, 2, 3, 2048, 272, 128, "none"),  # no row at all has a group
     (150, 2, 4, 512, 320, 128, "skewed"), (400, 2, 3, 1184, 560, 32, "mixed"), (700, 1, 2, 640, 1040, 64, "skewed"),
     (64, 2, 2, 4224, 64, 128, "mixed"),
+    (5, 1, 2, 8320, 96, 128, "all"),                                              # a deep K over eight waves
+    (500, 1, 8, 160, 12560, 32, "mixed"),                                         # 64-row tiles, waves side by side
+    (2100, 1, 2, 160, 4112, 32, "mixed"),                                         # 128-row tiles
 ])
 @pytest.mark.parametrize("gather", [False, True])
 def test_grouped_sizes(tokens, topk, groups, K, N, g, how, gather):
@@ -293,6 +296,27 @@ def test_grouped_sizes(tokens, topk, groups, K, N, g, how, gather):
 @pytest.mark.parametrize("act,fmt,g", [("bf16", "asym", 32), ("f16", "sym", 32), ("bf16", "nf4", 64 // 2)])
 def test_grouped_more_rows(tokens, groups, K, N, act, fmt, g):
     _check_grouped(tokens, 1, groups, K, N, g, act, fmt, True, gather=False)
+
+
+@pytest.mark.parametrize("act,fmt,g", [("bf16", "asym", 64), ("bf16", "sym", 32), ("f16", "nf4", 64), ("bf16", "nf4", 32)])
+@pytest.mark.parametrize("tokens,groups,K,N", [(500, 8, 192, 12576), (2100, 2, 192, 4128)])
+def test_grouped_many_rows_in_every_format(tokens, groups, K, N, act, fmt, g):
+    _check_grouped(tokens, 1, groups, K, N, g, act, fmt, fmt != "asym", gather=True)
+
+
+def test_no_tokens():
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    d, _ = _experts(256, 64, 128, "f16", "asym", 3, 7)
+    r = w4.route(torch.zeros(0, 2, dtype=torch.int32, device="cuda"), 3)
+    assert r.offsets.tolist() == [0, 0, 0, 0] and r.order.numel() == 0 and r.slot.shape == (0, 2)
+    x, w = torch.zeros(0, 256, device="cuda").half(), torch.zeros(0, 2, device="cuda")
+    assert w4.dispatch(x, r).shape == (0, 256) and w4.dispatch_backward(x, r).shape == (0, 256)
+    assert w4.combine(x, r, w).shape == (0, 256) and w4.combine_backward(x, x, r, w)[1].shape == (0, 2)
+    assert w4.gemm_grouped(x, r, d["packed"], d["scales"], d["tail"], 128, gather=True).shape == (0, 64)
+    a, b = torch.zeros(2, 8, 256, device="cuda").half(), torch.zeros(2, 64, 8, device="cuda").half()
+    y = w4.lora_add(x[:, :64].contiguous(), x, a, b, torch.zeros(0, dtype=torch.int32, device="cuda"), torch.ones(2, device="cuda"))
+    assert y.shape == (0, 64)
 
 
 def test_grouped_rows_do_not_mix():
@@ -433,3 +457,47 @@ def test_one_layer_in_a_graph_and_on_a_side_stream():
     side.synchronize()
     for t, e in zip((y, z, dys, dw), eager):
         assert torch.equal(t, e)
+
+
+def test_the_example_layer():
+    """The example runs the operators together; five roundings to bf16 (y, its adapter's sum, h, e and z; 2^-9 each in
+    the mean square, and h's and e's gains near one) keep the whole within 5 * 2^-9 of fp64."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import routed_layer
+    assert routed_layer.main(rows=40, width=512, inner=256, experts=5, adapters=3, rank=8) < 5 * 2.0 ** -9
+
+
+# ------------------------------------------------------------------ refusals that need device tensors
+
+def test_refusals_on_the_device():
+    """Checked on the host before anything is launched."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    M, K, N, L, rank = 4, 64, 48, 3, 8
+    x, y = torch.zeros(M, K, device="cuda").half(), torch.zeros(M, N, device="cuda").half()
+    a, b = torch.zeros(L, rank, K, device="cuda").half(), torch.zeros(L, N, rank, device="cuda").half()
+    ids, s = torch.zeros(M, device="cuda", dtype=torch.int32), torch.ones(L, device="cuda")
+
+    def refused(match, fn):
+        with pytest.raises(w4.W4A16Error, match=match):
+            fn()
+
+    refused("lora_b", lambda: w4.lora_add(y, x, a, b[:, :, :4].contiguous(), ids, s))
+    refused("lora_a", lambda: w4.lora_add(y, x, a.float(), b, ids, s))
+    refused("ids", lambda: w4.lora_add(y, x, a, b, ids.long(), s))
+    refused("ids", lambda: w4.lora_add(y, x, a, b, None, s))
+    refused("scaling", lambda: w4.lora_add(y, x, a, b, ids, s[:2]))
+    refused("out", lambda: w4.lora_add(y, x, a, b, ids, s, out=y.float()))
+    refused("routing", lambda: w4.lora_add(y, x, a, b, ids, s, routing=w4.route(ids, L + 1)))
+    refused("unsupported", lambda: w4.lora_add(y[:, :24].contiguous(), x, a, b[:, :24].contiguous(), ids, s))
+    r = w4.route(ids, L)
+    refused("expected", lambda: w4.dispatch(x.cpu(), r))
+    refused("expected", lambda: w4.combine(y, r, torch.ones(M, 1)))
+    refused("overlaps", lambda: w4.dispatch_backward(x, r, out=x))
+    big = torch.zeros(3 * M, N, device="cuda").half()
+    refused("overlaps", lambda: w4.lora_add(big[:M], x, a, b, ids, s, out=big[1:M + 1]))
+    refused("unsupported", lambda: w4.route(ids, 1025))
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    refused("bytes", lambda: w4.lora_add(y, x, a, b, None, s, routing=r, workspace=ws))

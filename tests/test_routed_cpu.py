@@ -133,6 +133,7 @@ def _rows_call(L, name, a):
     (dict(tokens=-1), ARG), (dict(topk=0), ARG), (dict(groups=1025), UNSUPPORTED), (dict(width=0), ARG),
     (dict(dtype=3), ARG), (dict(src=0), ARG), (dict(dst=0), ARG), (dict(plan=0), ARG), (dict(plan=Q + 4), ARG),
     (dict(src=P + 1), ARG), (dict(dst=P), ARG), (dict(tokens=1 << 25, width=1 << 20), UNSUPPORTED),
+    (dict(tokens=1 << 24, topk=1, width=8), UNSUPPORTED),
 ])
 def test_rows_refuse(L, name, kw, status):
     assert _rows_call(L, name, {**ROWS, **kw}) == status
@@ -186,7 +187,7 @@ def test_grouped_kernel_names(L):
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), ARG), (dict(K=100), ARG), (dict(K=4104), UNSUPPORTED), (dict(N=4100), ARG), (dict(N=4104), UNSUPPORTED),
     (dict(rank=0), ARG), (dict(rank=12), UNSUPPORTED), (dict(rank=264), UNSUPPORTED), (dict(adapters=0), ARG),
-    (dict(adapters=1025), UNSUPPORTED), (dict(act=2), ARG), (dict(act=0, ydt=1), ARG), (dict(x=0), ARG), (dict(y=0), ARG),
+    (dict(adapters=1025), UNSUPPORTED), (dict(M=1 << 26, N=1 << 20), UNSUPPORTED), (dict(act=2), ARG), (dict(act=0, ydt=1), ARG), (dict(x=0), ARG), (dict(y=0), ARG),
     (dict(a=0), ARG), (dict(b=0), ARG), (dict(ids=0), ARG), (dict(scaling=0), ARG), (dict(out=0), ARG),
     (dict(x=P + 8), ARG), (dict(out=P + 8), ARG), (dict(ids=P + 2), ARG), (dict(plan=Q + 4), ARG),
     (dict(ws=0), WORKSPACE), (dict(ws=Q + 64), WORKSPACE), (dict(wsb=64), WORKSPACE),

@@ -501,7 +501,7 @@ static w4a16_status check_rows(const int32_t* plan, int tokens, int topk, int gr
   const w4a16_status st = check_route(tokens, topk, groups);
   if (st != W4A16_OK) return st;
   if (width <= 0) return W4A16_ERR_ARG;
-  if ((long long)tokens * ((width + 255) / 256) >= (1LL << 30)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::rows_fit(tokens, width)) return W4A16_ERR_UNSUPPORTED;
   if (tokens && (!plan || !aligned(plan, 256))) return W4A16_ERR_ARG;
   return W4A16_OK;
 }
@@ -620,7 +620,7 @@ static w4a16_status check_lora(int M, int K, int N, int adapters, int rank) {
   if (M < 0 || K <= 0 || N <= 0 || adapters <= 0 || rank <= 0) return W4A16_ERR_ARG;
   if (K % 8 || N % 8) return W4A16_ERR_ARG;
   if (K % 32 || N % 16 || rank % 8 || rank > w4a16::kMaxRank) return W4A16_ERR_UNSUPPORTED;
-  if (adapters > w4a16::kMaxGroups || M > w4a16::kMaxSlots || N > (1 << 23)) return W4A16_ERR_UNSUPPORTED;
+  if (adapters > w4a16::kMaxGroups || !w4a16::lora_fits(M, K, N, adapters, rank)) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }
 

@@ -291,6 +291,12 @@ RowParams row_params(const RouteLayout& r, const int32_t* plan, int width, int v
 
 }  // namespace
 
+bool rows_fit(int tokens, int width) {
+  // a wave per token and 512 elements at most (fp32), a workgroup per token in the backward pass
+  const long long waves = (long long)tokens * ceil_div(width, 64 * kRowVecs * 4) + kTailWaves;
+  return waves < (1LL << 26) && ((long long)tokens + kTailWaves) * 64 * kRowWaves < (1LL << 32);
+}
+
 hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* plan, int width, int dtype,
                            void* xs, hipStream_t s) {
   RowParams p = row_params(r, plan, width, dtype == T_F32 ? 4 : 8);

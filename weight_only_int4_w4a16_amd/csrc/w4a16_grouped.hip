@@ -32,26 +32,27 @@ int forced_tile() {
 
 // The rows of each group are known on the device only, so the tile goes by their mean over the
 // groups that can have rows. A taller tile forms W_hat once for more rows and is part-filled
-// more often, so the limits lie where tiles win on routings as uneven as gates make them (top-k of normal scores
-// with expert biases of 0.7 sigma; 8 experts of 4096x14336 g128, us with 16/32/64/128 rows a
-// tile): mean 6 44/44/56/101, 12 65/70/71/114, 16 61/54/70/108, 48 133/108/104/189, 64
-// 161/123/116/117, 128 310/231/195/207, 192 470/357/324/235; 64 experts of 2048x2816 NF4: 8
-// 53/55/72/136, 24 87/78/90/141, 64 178/140/140/208, 128 333/246/227/275, 192 495/368/321/286.
-// Past 144 rows the 128 x 512 tile can still leave most of the chip idle (few groups, narrow N): then
+// more often, so the limits lie where tiles win on routings as uneven as gates make them (top-k of
+// normal scores with expert biases of 0.7 sigma; us with 16/32/64/128 rows a tile). 8 experts of
+// 4096x14336 g128: mean 6 44/44/56/101, 12 56/49/60/114, 24 86/73/79/114, 48 135/103/101/189, 64
+// 161/120/108/198, 128 310/231/177/214, 192 470/357/213/227, 384 -/816/415/437, 512 -/-/529/530; 64
+// experts of 2048x2816 g128: 8 38/40/51/116, 24 71/61/68/121, 48 111/88/85/170, 128 245/194/139/233, 384
+// -/572/338/420. Deep and narrow weights (8 of 14336x4096) leave the 128-row tile earlier room: 192 -/475/239/283, 256
+// -/646/319/293.
+// Past 384 rows the 128 x 512 tile can still leave most of the chip idle (few groups, narrow N): then
 // 64-row tiles, by a model of compute-unit time (0.42 us per 64x64 tile and k-block; 2.6 us per
 // 128x512 tile and k-block in one round of workgroups, 3.2 us in more).
 Tile choose_tile(int S, int E, int K, int N) {
   if (forced_tile() >= 0) return (Tile)forced_tile();
   const int groups = E < S ? E : S;
   const int mean = S / (groups > 0 ? groups : 1);
-  if (mean <= 10) return TILE_16;
-  if (mean <= 48) return TILE_32;
-  if (mean <= 144) return TILE_64;
+  if (mean <= 9) return TILE_16;
+  if (mean <= 44) return TILE_32;
+  if (mean <= (K > 8192 ? 144 : 384)) return TILE_64;
   const long long cus = device_cu_count();
   const long long rounds = ((S / 128 + groups / 2) * (long long)ceil_div(N, 512) + cus - 1) / cus;
   const double large = rounds * (rounds > 1 ? 3.2 : 2.6);
   const double small = (S / 64.0 + groups / 2) * ceil_div(N, 64) * 0.42 / cus;
-  (void)K;  // both grow with it alike
   return small < large ? TILE_64 : TILE_128;
 }
 
@@ -69,8 +70,9 @@ const char* grouped_name(int S, int K, int N, int E, int group_size) {
   }
 }
 
-// a launch holds fewer than 2^32 threads
+// a launch holds fewer than 2^32 threads, and a tile's rows fewer than 2^31 bytes
 bool grouped_fits(const RouteLayout& r, int K, int N) {
+  if (K >= (1 << 23)) return false;
   const Tile t = choose_tile(r.S, r.E, K, N);
   return (long long)tile_bound(r.S, r.E, t) * ceil_div(N, tile_cols(t)) * 512 < (1LL << 32);
 }
@@ -101,10 +103,23 @@ hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t
   p.NT = a.N / 16;
   p.NG = a.K / a.group_size;
   p.half = p.NT / 2;
-  p.slice = ceil_div(p.KC, kWaves);
-  p.col_tiles = ceil_div(p.NT, kStrips);
   GroupedGeometry g;
   g.MT = kTileRows[tile] / 16;
+  g.waves = kWaves;
+  const long long cus = device_cu_count();
+  const int groups = r.E < r.S ? r.E : r.S;
+  const long long tiles = r.S / kTileRows[tile] + (groups + 1) / 2;  // to expect
+  // Sixteen rows: eight waves share a deep K where the workgroups leave room on the compute units
+  // (8 experts of 14336x4096 at 4 rows each, 512 workgroups: 55 -> 43 us; at K 4096 and 2048 four
+  // waves are as good or better by up to 10%).
+  const long long wgs = (tiles > groups ? tiles : groups) * ceil_div(p.NT, kStrips);
+  if (g.MT == 1 && p.KC >= 64 && wgs <= 3 * cus) g.waves = 8;
+  // Sixty-four rows: the waves side by side where that still makes two workgroups a compute unit (8
+  // experts of 4096x14336 at 64/128 rows each 119/206 -> 104/169 us; 64 of 2048x2816 at 64/128: 105/177
+  // -> 91/142).
+  if (g.MT == 4 && tiles * ceil_div(p.NT, kStrips * kWaves) >= 2 * cus) g.waves = 0;
+  p.slice = g.waves ? ceil_div(p.KC, g.waves) : p.KC;
+  p.col_tiles = ceil_div(p.NT, kStrips * (g.waves ? 1 : kWaves));
   return a.act == ACT_F16 ? launch_few<ACT_F16>(p, g, a.group_size, a.nf4, a.glu, a.stream)
                           : launch_few<ACT_BF16>(p, g, a.group_size, a.nf4, a.glu, a.stream);
 }

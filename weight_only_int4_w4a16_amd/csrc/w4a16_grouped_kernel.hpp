@@ -194,8 +194,8 @@ constexpr int waves_per_simd(int MT, int GPC) { return (MT == 1 ? 4 : MT == 2 ? 
 
 // GLU: the first two strips are gate strips, the others the matching up strips, and the output
 // is h = SiLU(gate) * up, [S][N / 2].
-template <int ACT, int GPC, int FMT, int MT, bool GLU>
-__global__ __launch_bounds__(64 * kWaves, waves_per_simd(MT, GPC)) void grouped_kernel(GroupedParams p) {
+template <int ACT, int GPC, int FMT, int MT, bool GLU, int W>
+__global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kernel(GroupedParams p) {
   typedef typename ActT<ACT>::type AT;
   constexpr bool ZEROS = FMT == FMT_ASYM;
   constexpr int SW = kStrips, OS = GLU ? SW / 2 : SW;  // strips, output strips
@@ -335,14 +335,14 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(MT, GPC)) void grouped_
         red[wave * TILE + (16 * mt + 4 * (lane >> 4) + i) * kRedStride + 16 * s + (lane & 15)] = acc[mt][s][i];
   __syncthreads();
   constexpr int QUADS = OS * 4;  // of columns in a row
-  for (int q = threadIdx.x; q < rows * QUADS; q += 64 * kWaves) {
+  for (int q = threadIdx.x; q < rows * QUADS; q += 64 * W) {
     const int r = q / QUADS, c = 4 * (q % QUADS);
     if (c >= ocols) continue;  // whole quads: the width is a multiple of 16
     const float* const at = red + r * kRedStride + c;
     f4_t v = *reinterpret_cast<const f4_t*>(at), u = {0.f, 0.f, 0.f, 0.f};
     if constexpr (GLU) u = *reinterpret_cast<const f4_t*>(at + OS * 16);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
+    for (int w = 1; w < W; ++w) {
       v += *reinterpret_cast<const f4_t*>(at + w * TILE);
       if constexpr (GLU) u += *reinterpret_cast<const f4_t*>(at + w * TILE + OS * 16);
     }
@@ -354,18 +354,199 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(MT, GPC)) void grouped_
   }
 }
 
+// ---------------------------------------------------------------------------------------
+// The same product with the waves side by side: a wave owns four strips over all of K, a
+// workgroup 256 columns, and x is shared. Nothing is added between waves, a wave's fixed work is spread
+// over four times the blocks, and x costs a quarter of the copies and LDS, so that more waves
+// fit; but the workgroups are a quarter as many, which only fills the chip with enough tiles.
+//
+// Two slots of x: at block i every wave waits for its own codes and copies of it, a barrier
+// makes all copies visible and frees the other slot, and block i + 1's loads go out before block i is multiplied.
+// ---------------------------------------------------------------------------------------
+constexpr int cols_waves_per_simd(int MT, int GPC) { return (MT == 4 ? 3 : 4) - (GPC == 4 ? 1 : 0); }
+// the slots, later one 16-row partial tile a wave
+constexpr size_t cols_lds(int MT) {
+  const size_t ring = 2 * (size_t)slot_halves(MT) * 2, turn = (size_t)kWaves * 16 * kRedStride * 4;
+  return ring > turn ? ring : turn;
+}
+
+template <int ACT, int GPC, int FMT, int MT, bool GLU>
+__global__ __launch_bounds__(64 * kWaves, cols_waves_per_simd(MT, GPC)) void grouped_cols_kernel(GroupedParams p) {
+  typedef typename ActT<ACT>::type AT;
+  constexpr bool ZEROS = FMT == FMT_ASYM;
+  constexpr int SW = kStrips, OS = GLU ? SW / 2 : SW;  // strips of a wave, output strips
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries * kNf4Copies : 1];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = p.K, N = p.N, KC = p.KC;
+  const int width = GLU ? N >> 1 : N;  // of an output row
+  const int shift = 4 * (lane & 7);
+  const uint32_t* const mytab = ptab + (FMT == FMT_NF4 ? lane % kNf4Copies : 0);
+  const int item = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
+  const int tn = item / p.groups.bound;
+  int e, p0, end;
+  if (!group_tile(p.groups, item - tn * p.groups.bound, e, p0, end)) return;
+  const int rows = end - p0;
+  if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
+    zero_tile(p.out, p.out_dtype, p0, rows, width, tn * kWaves * OS * 16, kWaves * OS * 16);
+    return;
+  }
+  const int s0 = (tn * kWaves + wave) * OS;  // the wave's first (gate) strip
+  const u4_t* const wbase = p.packed + (size_t)e * p.NT * KC * 64;
+  const uint16_t* const sbase = p.scales + (size_t)e * p.NG * N;
+  const uint32_t* const zbase = ZEROS ? p.qzeros + (size_t)e * p.NG * (N >> 3) : nullptr;
+  const __amdgpu_buffer_rsrc_t srs = make_rsrc(sbase, (uint32_t)p.NG * N * 2);
+  const __amdgpu_buffer_rsrc_t zrs = make_rsrc(ZEROS ? (const void*)zbase : (const void*)sbase, (uint32_t)p.NG * (N >> 3) * 4);
+  // strip s of the wave, clamped in bounds for loads (never stored past the last one)
+  auto strip = [&](int s) __attribute__((always_inline)) {
+    return GLU ? min(s0 + (s < OS ? s : s - OS), p.half - 1) + (s < OS ? 0 : p.half) : min(s0 + s, p.NT - 1);
+  };
+  struct Codes {
+    u4_t b[SW];
+    uint32_t s[SW][GPC], z[SW][GPC];
+  };
+  auto load_codes = [&](Codes& R, int kc) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < SW; ++s)
+      R.b[s] = __builtin_nontemporal_load(wbase + ((size_t)strip(s) * KC + kc) * 64 + lane);
+#pragma unroll
+    for (int s = 0; s < SW; ++s) {
+#pragma unroll
+      for (int gi = 0; gi < GPC; ++gi) {
+        const int g = min(kc * GPC + gi, p.NG - 1);
+        R.s[s][gi] = __builtin_amdgcn_raw_buffer_load_b16(srs, (lane & 15) * 2, (g * N + strip(s) * 16) * 2, 0);
+        if constexpr (ZEROS)
+          R.z[s][gi] = __builtin_amdgcn_raw_buffer_load_b32(zrs, ((lane & 15) >> 3) * 4, (g * (N >> 3) + strip(s) * 2) * 4, 0);
+      }
+    }
+  };
+  Codes R;
+  load_codes(R, 0);
+  // instruction i of wave w copies rows 16 i + 4 w .. + 3 of the tile, laid out as above
+  const __amdgpu_buffer_rsrc_t xrs = p.groups.tokens
+      ? make_rsrc(p.x, (uint32_t)p.groups.tokens * (uint32_t)K * 2u)
+      : make_rsrc(p.x + (size_t)p0 * K, (uint32_t)rows * (uint32_t)K * 2u);
+  const int crow = 4 * wave + (lane >> 4), cchunk = (lane & 15) ^ (crow & 15);
+  uint32_t xoff[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    int src = min(16 * i + crow, rows - 1);
+    if (p.groups.tokens) src = p.groups.plan[p.groups.token + p0 + src];
+    xoff[i] = ((uint32_t)src * (uint32_t)K + cchunk * 8) * 2u;
+  }
+  auto copy_x = [&](int kc) __attribute__((always_inline)) {
+    uint16_t* const slot = lds + (kc & 1) * slot_halves(MT) + wave * 512;
+    const bool in = kc * 128 + cchunk * 8 < K;  // chunks past a ragged K read out of range (zeros)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if (16 * i + 4 * wave >= rows) break;
+      buffer_copy16_to_lds(xrs, in ? xoff[i] : kOutOfRange, kc * 256, slot + i * 2048);
+    }
+  };
+  copy_x(0);
+  if constexpr (FMT == FMT_NF4) nf4_copies_fill(ptab, p.codebook);  // complete at the first barrier
+
+  f4_t acc[MT][SW];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int s = 0; s < SW; ++s) acc[mt][s] = f4_t{0.f, 0.f, 0.f, 0.f};
+  for (int kc = 0; kc < KC; ++kc) {
+    wait_loads();
+    __syncthreads();
+    const Codes C = R;
+    if (kc + 1 < KC) {
+      load_codes(R, kc + 1);
+      copy_x(kc + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const uint16_t* const slot = lds + (kc & 1) * slot_halves(MT);
+    GroupScale gs[SW][GPC];
+#pragma unroll
+    for (int s = 0; s < SW; ++s)
+#pragma unroll
+      for (int gi = 0; gi < GPC; ++gi)
+        gs[s][gi] = group_scale<ACT, FMT>(C.s[s][gi], ZEROS ? (C.z[s][gi] >> shift) & 0xFu : 8u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (kc * 128 + 32 * j >= K) break;
+      u4_t a[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int row = 16 * mt + (lane & 15);
+        a[mt] = *reinterpret_cast<const u4_t*>(slot + row * 128 + (((4 * j + (lane >> 4)) ^ (row & 15)) * 8));
+        if constexpr (FMT == FMT_NF4) a[mt] = act8_to_pair_order(a[mt]);
+      }
+#pragma unroll
+      for (int s = 0; s < SW; ++s) {
+        const AT w = dequant_word<ACT, FMT>(C.b[s][j], gs[s][j * GPC / 4], mytab);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) acc[mt][s] = mfma16(__builtin_bit_cast(AT, a[mt]), w, acc[mt][s]);
+      }
+    }
+  }
+  // Each 16 rows through the wave's part of LDS and out by whole runs of a row. Lane l holds column
+  // l%16 of each strip and rows 4 (l/16) + i, i < 4.
+  __syncthreads();  // every wave is done with the slots
+  float* const turn = reinterpret_cast<float*>(lds) + wave * 16 * kRedStride;
+  constexpr int QUADS = OS * 4;  // of the wave's output columns
+  const int c = 4 * (lane % QUADS), col = s0 * 16 + c;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    if (16 * mt >= rows) break;
+#pragma unroll
+    for (int s = 0; s < SW; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) turn[(4 * (lane >> 4) + i) * kRedStride + 16 * s + (lane & 15)] = acc[mt][s][i];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int r0 = 0; r0 < 16; r0 += 64 / QUADS) {
+      const int r = r0 + lane / QUADS, m = 16 * mt + r;
+      const float* const at = turn + r * kRedStride + c;
+      f4_t v = *reinterpret_cast<const f4_t*>(at);
+      if constexpr (GLU) {
+        const f4_t u = *reinterpret_cast<const f4_t*>(at + OS * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = v[i] / (1.0f + __expf(-v[i])) * u[i];
+      }
+      if (m < rows && col < width) store_quad(p.out, (size_t)(p0 + m) * width + col, v, p.out_dtype);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 struct GroupedGeometry {
   int MT;
+  int waves;  // that share K; 0: waves side by side
 };
 
 template <int ACT, int GPC, int FMT, int MT>
 hipError_t launch_mt(const GroupedParams& p, const GroupedGeometry& g, bool glu, hipStream_t s) {
   const dim3 grid(p.groups.bound * p.col_tiles), block(64 * kWaves);
-  const size_t lds = kWaves * wave_lds(MT);
+  if constexpr (MT == 4) {
+    if (g.waves == 0) {  // side by side
+      if (glu)
+        hipLaunchKernelGGL((grouped_cols_kernel<ACT, GPC, FMT, MT, true>), grid, block, cols_lds(MT), s, p);
+      else
+        hipLaunchKernelGGL((grouped_cols_kernel<ACT, GPC, FMT, MT, false>), grid, block, cols_lds(MT), s, p);
+      return hipGetLastError();
+    }
+  }
+  if constexpr (MT == 1) {
+    if (g.waves == 8) {
+      if (glu)
+        hipLaunchKernelGGL((grouped_kernel<ACT, GPC, FMT, MT, true, 8>), grid, dim3(512), 8 * wave_lds(MT), s, p);
+      else
+        hipLaunchKernelGGL((grouped_kernel<ACT, GPC, FMT, MT, false, 8>), grid, dim3(512), 8 * wave_lds(MT), s, p);
+      return hipGetLastError();
+    }
+  }
   if (glu)
-    hipLaunchKernelGGL((grouped_kernel<ACT, GPC, FMT, MT, true>), grid, block, lds, s, p);
+    hipLaunchKernelGGL((grouped_kernel<ACT, GPC, FMT, MT, true, kWaves>), grid, block, kWaves * wave_lds(MT), s, p);
   else
-    hipLaunchKernelGGL((grouped_kernel<ACT, GPC, FMT, MT, false>), grid, block, lds, s, p);
+    hipLaunchKernelGGL((grouped_kernel<ACT, GPC, FMT, MT, false, kWaves>), grid, block, kWaves * wave_lds(MT), s, p);
   return hipGetLastError();
 }
 

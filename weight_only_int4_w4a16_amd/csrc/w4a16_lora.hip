@@ -675,6 +675,19 @@ void launch_expand(const LoraParams& p, dim3 grid, hipStream_t s) {
 
 }  // namespace
 
+bool lora_fits(int M, int K, int N, int L, int R) {
+  if (M > kMaxSlots) return false;
+  for (int planned = 0; planned < 2; ++planned) {
+    const bool self = self_tiles(M, planned != 0);
+    const LoraGeometry g = lora_geometry(M, K, N, L, R, self);
+    const long long tiles = self ? M : tile_bound(M, L, g.list);
+    const long long first = tiles * g.slices * 64 * kShrinkWaves;
+    const long long second = tiles * ceil_div(N, 64 * expand_waves(g.one) * g.strips) * 64 * expand_waves(g.one);
+    if (first >= (1LL << 32) || second >= (1LL << 32)) return false;
+  }
+  return true;
+}
+
 size_t lora_workspace_bytes(int M, int K, int N, int L, int R, bool planned) {
   const bool self = self_tiles(M, planned);
   const LoraGeometry g = lora_geometry(M, K, N, L, R, self);

@@ -69,6 +69,8 @@ __device__ __forceinline__ bool group_tile(const GroupTiles& g, int ti, int& e, 
 }
 
 hipError_t launch_route(const int32_t* ids, const RouteLayout& r, int32_t* plan, hipStream_t s);
+// A launch holds fewer than 2^32 threads: whether the tokens' rows make launches of the row movers
+bool rows_fit(int tokens, int width);
 // types of rows: 0 fp16, 1 bf16, 2 fp32 (as w4a16_dtype)
 hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* plan, int width, int dtype,
                            void* xs, hipStream_t s);
@@ -100,6 +102,7 @@ struct LoraArgs {
   void* workspace;
   hipStream_t stream;
 };
+bool lora_fits(int M, int K, int N, int L, int R);  // its launches too, with a plan or without
 size_t lora_workspace_bytes(int M, int K, int N, int L, int R, bool planned);
 hipError_t launch_lora(const LoraArgs& a);
 
