@@ -70,22 +70,6 @@ __device__ __forceinline__ int tile_of(int b, int G) {
 constexpr int kStrips = 4;
 constexpr int kWaves = 4;
 
-// The NF4 level pairs, kNf4Copies times: lane l reads copy l % kNf4Copies, whose words lie in
-// every kNf4Copies-th bank. The lanes' codes are random, and over one copy six or so of 64 meet in
-// one bank.
-constexpr int kNf4Copies = 8;
-__device__ __forceinline__ void nf4_copies_fill(uint32_t* tab, const uint16_t* codebook) {
-  for (int i = threadIdx.x; i < kNf4PairEntries * kNf4Copies; i += blockDim.x) {
-    const int b = i / kNf4Copies;
-    tab[i] = (uint32_t)codebook[b & 15] | ((uint32_t)codebook[b >> 4] << 16);
-  }
-}
-// the eight levels of a word in the order k = 0, 2, 4, 6, 1, 3, 5, 7 (`tab`: this lane's copy)
-__device__ __forceinline__ h8_t nf4_levels(uint32_t w, const uint32_t* tab) {
-  constexpr uint32_t C = kNf4Copies;
-  const u4_t r{tab[(w & 0xFFu) * C], tab[((w >> 8) & 0xFFu) * C], tab[((w >> 16) & 0xFFu) * C], tab[(w >> 24) * C]};
-  return __builtin_bit_cast(h8_t, r);
-}
 // (q - z) s of one packed word in bf16 by one fma per weight; c1024 = -(1024 + z) s,
 // c64 = -(64 + z) s
 __device__ __forceinline__ b8_t dequant_word_bf16_fma(uint32_t w, float s, float c1024, float c64) {
@@ -126,7 +110,7 @@ template <int ACT, int FMT>
 __device__ __forceinline__ typename ActT<ACT>::type dequant_word(uint32_t w, const GroupScale& g, const uint32_t* ptab) {
   if constexpr (FMT == FMT_NF4) {
     // the levels in the pair table's order; the activations are put in the same order
-    const h8_t c = nf4_levels(w, ptab);
+    const h8_t c = nf4_levels_f16_pairs(w, ptab);
     if constexpr (ACT == ACT_F16) {
       const h2_t a2 = as_h2(g.raw * 0x00010001u);
       h8_t r;
@@ -200,14 +184,13 @@ __global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kerne
   constexpr bool ZEROS = FMT == FMT_ASYM;
   constexpr int SW = kStrips, OS = GLU ? SW / 2 : SW;  // strips, output strips
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];  // [waves][wave_lds(MT)]
-  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries * kNf4Copies : 1];
+  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries : 1];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = p.K, N = p.N, KC = p.KC;
   const int width = GLU ? N >> 1 : N;  // of an output row
   const int shift = 4 * (lane & 7);
-  const uint32_t* const mytab = ptab + (FMT == FMT_NF4 ? lane % kNf4Copies : 0);
   uint16_t* const slot = lds + wave * (wave_lds(MT) / 2);
   const int kc0 = min(wave * p.slice, KC), kc1 = min(kc0 + p.slice, KC);
   const int item = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
@@ -273,7 +256,7 @@ __global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kerne
     }
   };
   if constexpr (FMT == FMT_NF4) {
-    nf4_copies_fill(ptab, p.codebook);
+    nf4_pair_table_fill(ptab, p.codebook);
     __syncthreads();
   }
   f4_t acc[MT][SW];
@@ -316,7 +299,7 @@ __global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kerne
       if (kc * 128 + 32 * j >= K) break;
 #pragma unroll
       for (int s = 0; s < SW; ++s) {
-        const AT w = dequant_word<ACT, FMT>(C.b[s][j], gs[s][j * GPC / 4], mytab);
+        const AT w = dequant_word<ACT, FMT>(C.b[s][j], gs[s][j * GPC / 4], ptab);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[mt][s] = mfma16(__builtin_bit_cast(AT, a[j][mt]), w, acc[mt][s]);
       }
@@ -376,14 +359,13 @@ __global__ __launch_bounds__(64 * kWaves, cols_waves_per_simd(MT, GPC)) void gro
   constexpr bool ZEROS = FMT == FMT_ASYM;
   constexpr int SW = kStrips, OS = GLU ? SW / 2 : SW;  // strips of a wave, output strips
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
-  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries * kNf4Copies : 1];
+  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries : 1];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = p.K, N = p.N, KC = p.KC;
   const int width = GLU ? N >> 1 : N;  // of an output row
   const int shift = 4 * (lane & 7);
-  const uint32_t* const mytab = ptab + (FMT == FMT_NF4 ? lane % kNf4Copies : 0);
   const int item = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
   const int tn = item / p.groups.bound;
   int e, p0, end;
@@ -446,7 +428,7 @@ __global__ __launch_bounds__(64 * kWaves, cols_waves_per_simd(MT, GPC)) void gro
     }
   };
   copy_x(0);
-  if constexpr (FMT == FMT_NF4) nf4_copies_fill(ptab, p.codebook);  // complete at the first barrier
+  if constexpr (FMT == FMT_NF4) nf4_pair_table_fill(ptab, p.codebook);  // complete at the first barrier
 
   f4_t acc[MT][SW];
 #pragma unroll
@@ -481,7 +463,7 @@ __global__ __launch_bounds__(64 * kWaves, cols_waves_per_simd(MT, GPC)) void gro
       }
 #pragma unroll
       for (int s = 0; s < SW; ++s) {
-        const AT w = dequant_word<ACT, FMT>(C.b[s][j], gs[s][j * GPC / 4], mytab);
+        const AT w = dequant_word<ACT, FMT>(C.b[s][j], gs[s][j * GPC / 4], ptab);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[mt][s] = mfma16(__builtin_bit_cast(AT, a[mt]), w, acc[mt][s]);
       }
