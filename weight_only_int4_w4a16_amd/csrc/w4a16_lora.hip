@@ -8,13 +8,14 @@
 //
 // Tiles. Up to 96 rows, workgroup b looks at row b: if the row is the first, 17th, 33rd.. of its
 // adapter, the tile is that row and the next fifteen of the adapter, found with one ballot
-// per 64 ids; else it leaves. That saves the sort's launch (5 us; at 256 rows the workgroups that leave
-// cost more: 33 us against 16 + 5 at 8192x8192 rank 64). More rows, or a plan in hand, take the plan's tile lists.
+// per 64 ids; else it leaves. That saves the sort's launch (5 us; at 256 rows the workgroups
+// that leave cost more: 33 us against 16 + 5 at 8192x8192 rank 64). More rows, or a plan in
+// hand, take the plan's tile lists.
 //
-// Two launches, or one where t is cheap (below). The first forms t = x A^T, at most R values a row: a workgroup takes a tile of
-// rows and a slice of K, its waves parts of the slice, added through LDS in wave order; the
-// slices' fp32 sums go to the workspace. The second adds the slices in order and multiplies
-// by B.
+// Two launches, or one where t is cheap. The first forms t = x A^T, at most R values a row: a
+// workgroup takes a tile of rows and a slice of K, its waves parts of the slice, added through
+// LDS in a fixed order; the slices' fp32 sums go to the workspace. The second adds the slices in
+// order and multiplies by B.
 //
 // t in 16-bit MFMA operands. Rounding t once would cost as much as rounding the product, so t
 // is split into parts of the activation type, t = t0 + t1 (+ t2), each the rounding of what
@@ -24,10 +25,13 @@
 // into [1, 2); the scale goes back into s. A workgroup splits its rows' t once, in LDS, for all its columns.
 //
 // Operands of the second product. B is the A operand (16 columns n of the output) and t the B
-// operand (16 rows m), so a lane ends with consecutive n of one row. The MFMAs q = 0..3 of a
-// 64-column strip take the columns n0 + 32 (q/2) + 8 (i/4) + 4 (q%2) + i%4, i < 16: lane l then holds the eight of
-// n0 + 32 c + 8 (l/16) .. of row l%16 for c = 0, 1, and every access to y and out covers 64
-// contiguous bytes of a row.
+// operand (16 rows m), so a lane ends with four consecutive n of one row. A wave's 16 x 64 product is
+// turned through its own LDS, so that y and out are accessed by whole 128-byte runs of a row.
+//
+// Measured: one row, 4096x4096 rank 16 fp16 9.8 us (one launch; two took 14.0); 96 rows with 64
+// adapters, 4096x14336 rank 32 bf16 18 us (62 MB; first product 7.7, second 11.7 at 5.5 TB/s); 4096 rows
+// with 9 adapters, 8192x8192 rank 64 bf16 66 us (220 MB; sort 8.6, first product 18.2, second 35 at 4.7
+// TB/s, near a copy's rate).
 #include <type_traits>
 
 #include "w4a16_device.hpp"
@@ -225,14 +229,24 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(LoraParams p)
   }
 }
 
+// workgroup -> item, so that consecutive items run on the same XCD
+__device__ __forceinline__ int tile_of(int b, int G) {
+  const int q = G >> 3, r = G & 7, x = b & 7;
+  return x * q + (x < r ? x : r) + (b >> 3);
+}
+
 // t of a 64-row tile over one K slice, for prefill: the same product, but with x and A through
 // LDS. Loaded in the MFMA's layout, sixteen lanes touch sixteen rows of x (or of A): a 1 KiB
-// load then takes the address unit 64 cycles, and 66 tiles of 64 rows over 8192 columns took 27 us, three times
-// what the bytes take. Here a 128-column block of both goes from memory straight into one of
-// kStages slots, four rows of 256 bytes per instruction, three blocks ahead of the product. Row r of a slot
-// holds its chunks at positions c ^ (r % 16), so a fragment read touches every bank once. Wave w owns rows
-// 16 w .. 16 w + 15 and every rank, so nothing is added between waves.
-constexpr int kStages = 4, kTallWaves = 4;
+// load then takes the address unit 64 cycles, and 66 tiles of 64 rows over 8192 columns, rank 64,
+// took 27 us. Here a 128-column block of both goes from memory straight into one of
+// kStages slots, four rows of 256 bytes per instruction, three blocks ahead of the product. Row
+// r of a slot holds its chunks at positions c ^ (r % 16), so a fragment read touches every bank
+// once. Two waves share 16 rows, each with half of a block's columns and every rank, and are added
+// at the end: alone on its SIMD, a wave of 16 rows left its pipes idle half the time (22 us; with two
+// 18.2; the bytes, 75 MB, take 11-14). The slots fill the LDS, so one workgroup runs a compute unit; two with
+// two slots each and twice the slices took 20-23 us. A slice's tiles are neighbours on one XCD, where
+// they share A (19.5 us without).
+constexpr int kStages = 4, kTallWaves = 8;
 template <int RT>
 constexpr int tall_slot() { return (64 + 16 * RT) * 128; }  // halves
 
@@ -250,16 +264,20 @@ __device__ __forceinline__ void copy16_to_lds(const uint16_t* src, uint16_t* dst
 template <int ACT, int RT>
 __global__ __launch_bounds__(64 * kTallWaves) void shrink_tall_kernel(LoraParams p) {
   typedef typename ActT<ACT>::type AT;
-  constexpr int LOADS = 4 + RT;  // of a wave per block: its sixteen rows of x, its share of A's 16 RT ranks
+  // A wave's loads of a block: eight rows of x, and its share of A's 16 RT ranks (one rank tile's
+  // twice, by two waves)
+  constexpr int XL = 2, AL = RT > 1 ? RT / 2 : 1, LOADS = XL + AL;
   extern __shared__ __attribute__((aligned(16))) uint16_t ring[];  // [kStages][tall_slot]
   __shared__ int rows_of[kTileMax];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x / p.slices, slice = blockIdx.x - tile * p.slices;
+  const int item = tile_of(blockIdx.x, p.groups.bound * p.slices);
+  const int slice = item / p.groups.bound, tile = item - slice * p.groups.bound;
   int rows, e;
   if (!find_tile(p, tile, rows_of, rows, e)) return;
   if (e >= p.L) return;  // rows without an adapter
   const int r0 = blockIdx.y * kRankChunk;
+  const int strip = wave & 3, half = wave >> 2;
   __syncthreads();
   // instruction j covers four rows; lane l row l/16 of them, position l%16. Rows and ranks past the last
   // repeat it, never stored; chunks past a ragged K repeat its last, never multiplied.
@@ -267,16 +285,16 @@ __global__ __launch_bounds__(64 * kTallWaves) void shrink_tall_kernel(LoraParams
   int chunk[LOADS];
 #pragma unroll
   for (int j = 0; j < LOADS; ++j) {
-    const int r = j < 4 ? 16 * wave + 4 * j + (lane >> 4) : 4 * (wave * RT + j - 4) + (lane >> 4);
+    const int r = j < XL ? 4 * (wave * XL + j) + (lane >> 4) : 4 * ((wave * AL + j - XL) % (4 * RT)) + (lane >> 4);
     chunk[j] = 8 * ((lane & 15) ^ (r & 15));
-    src[j] = j < 4 ? p.x + (size_t)rows_of[min(r, rows - 1)] * p.K
+    src[j] = j < XL ? p.x + (size_t)rows_of[min(r, rows - 1)] * p.K
                    : p.a + ((size_t)e * p.R + min(r0 + r, p.R - 1)) * p.K;
   }
   auto load = [&](int kb, int slot) __attribute__((always_inline)) {
     uint16_t* const base = ring + slot * tall_slot<RT>();
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      uint16_t* const dst = base + (j < 4 ? 16 * wave + 4 * j : 64 + 4 * (wave * RT + j - 4)) * 128;
+      uint16_t* const dst = base + (j < XL ? 4 * (wave * XL + j) : 64 + 4 * ((wave * AL + j - XL) % (4 * RT))) * 128;
       copy16_to_lds(src[j] + min(128 * kb + chunk[j], p.K - 8), dst);
     }
   };
@@ -303,22 +321,37 @@ __global__ __launch_bounds__(64 * kTallWaves) void shrink_tall_kernel(LoraParams
     if (i + kStages - 1 < nb) load(b0 + i + kStages - 1, (i + kStages - 1) % kStages);
     const uint16_t* const base = ring + (i % kStages) * tall_slot<RT>();
     const int row = lane & 15;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (128 * (b0 + i) + 32 * s >= p.K) break;
+    auto step = [&](int s) __attribute__((always_inline)) {
       const int at = ((4 * s + (lane >> 4)) ^ row) * 8;
-      const u4_t xv = *reinterpret_cast<const u4_t*>(base + (16 * wave + row) * 128 + at);
+      const u4_t xv = *reinterpret_cast<const u4_t*>(base + (16 * strip + row) * 128 + at);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         const u4_t av = *reinterpret_cast<const u4_t*>(base + (64 + 16 * rt + row) * 128 + at);
         acc[rt] = mfma16(__builtin_bit_cast(AT, xv), __builtin_bit_cast(AT, av), acc[rt]);
       }
+    };
+    const int left = p.K - 128 * (b0 + i);
+    if (left >= 128) {  // without branches the steps' reads are all in flight together
+#pragma unroll
+      for (int s = 0; s < 2; ++s) step(2 * half + s);
+    } else {
+      for (int s = 2 * half; s < 2 * half + 2 && 32 * s < left; ++s) step(s);
     }
   }
+  // the second halves of the blocks, through LDS
+  __syncthreads();  // every wave is done with the slots
+  f4_t* const other = reinterpret_cast<f4_t*>(ring) + strip * RT * 64 + lane;
+  if (half == 1)
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) other[rt * 64] = acc[rt];
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) acc[rt] += other[rt * 64];
   // lane l holds rank l%16 of each tile and rows 4 (l/16) + i, i < 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int m = 16 * wave + 4 * (lane >> 4) + i;
+    const int m = 16 * strip + 4 * (lane >> 4) + i;
     if (m >= rows) continue;
     float* const part = p.part + ((size_t)slice * p.M + rows_of[m]) * p.R + r0;
 #pragma unroll
