@@ -102,6 +102,8 @@ ROW_CASES = [
     (1, 1, 1, 8, "f16"), (1, 2, 8, 4096, "bf16"), (5, 2, 3, 1, "f16"), (9, 3, 4, 7, "bf16"), (40, 2, 6, 2885, "bf16"),
     (17, 8, 64, 1030, "f16"), (70, 4, 16, 512, "f32"), (33, 5, 9, 1027, "f32"), (12, 9, 11, 264, "f16"),
     (300, 1, 40, 2048, "bf16"),
+    # narrower than a vector, just wider, and one wave's share and one element
+    (7, 3, 4, 3, "f32"), (6, 6, 5, 2, "bf16"), (8, 8, 3, 5, "f32"), (10, 4, 5, 9, "f16"), (21, 6, 4, 1025, "f16"),
 ]
 
 
@@ -147,13 +149,14 @@ def test_rows_into_order_and_back(tokens, topk, groups, width, kind):
     _within(dx, ref, 2 * topk * EPS * mag * (1 + U[kind]) + U[kind] * np.abs(ref) + D[kind], "dx")
 
 
+@pytest.mark.parametrize("width", [333, 3, 6])
 @pytest.mark.parametrize("to", ["f16", "bf16"])
-def test_combine_of_fp32_rows_to_16_bits(to):
+def test_combine_of_fp32_rows_to_16_bits(to, width):
     import weight_only_int4_w4a16_amd as w4
     torch = torch_mod()
     ids = _ids(30, 2, 5, 3)
     r, (_, _, slot) = _routed(ids, 5)
-    ys, _ = _rows((60, 333), "f32", 4)
+    ys, _ = _rows((60, width), "f32", 4)
     w = torch.rand(30, 2, device="cuda")
     y32 = w4.combine(ys, r, w)
     y16 = w4.combine(ys, r, w, out_dtype=_dtype(to))

@@ -15,9 +15,10 @@
 // this GPU take as they are.
 //
 // Measured, against a copy of a large tensor at 5.2 TB/s: bf16 dispatch of 8192 tokens x 4096 to two
-// rows each 35 us (201 MB, 5.8 TB/s: it writes more than it reads), combine of them 40 us (5.0
-// TB/s); 16384 tokens x 2048 with eight rows each, combine's gradients 207 us (1141 MB, 5.5 TB/s).
-// At rows of 2885 elements, whose vectors cross cache lines, 3.6-4 TB/s.
+// rows each 35 us (201 MB, 5.8 TB/s), combine of them 41 us (4.9 TB/s); 16384 tokens x 2048 with
+// eight rows each, dispatch 90 us (604 MB, 6.7 TB/s; some of its writes reach memory only while
+// the next kernel runs), combine 150 us (4.0 TB/s), combine's gradients 204 us (1141 MB, 5.6 TB/s). At rows
+// of 2885 elements, whose vectors cross cache lines, 3.6-4.5 TB/s.
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"
 
@@ -78,23 +79,20 @@ __device__ __forceinline__ u4_t vec_pack(const float* f) {
 // no multiple of V, is moved back to end with the row: its first elements are then its
 // neighbour's too, who reads and writes the same values. (Taken one by one, the last elements
 // made the sort, the two moves and their gradients of 4099 bf16 tokens of 2885 elements, topk 3,
-// take 133 us; so they take 112 us.)
-// Rows shorter than a vector are taken element by element.
+// take 133 us; so they took 112 us.) Vectors past the row read its last one and store nothing, so that
+// loads need no branch: the compiler puts a wait for all that is in flight before a load under
+// one. NARROW rows, shorter than a vector, are taken element by element.
 template <int T>
 __device__ __forceinline__ int vec_at(int c, int width) {
-  constexpr int V = Elem<T>::kVec;
-  return width >= V ? min(c * V, width - V) : c * V;
+  return min(c * Elem<T>::kVec, width - Elem<T>::kVec);
 }
-// zeros past the row
-template <int T>
+template <int T, bool NARROW>
 __device__ __forceinline__ u4_t load_vec(const typename Elem<T>::raw* row, int c, int width) {
-  constexpr int V = Elem<T>::kVec;
+  if constexpr (!NARROW) return *reinterpret_cast<const u4_any_t*>(row + vec_at<T>(c, width));
   u4_t v = {0, 0, 0, 0};
-  if (c * V >= width) return v;
-  if (width >= V) return *reinterpret_cast<const u4_any_t*>(row + vec_at<T>(c, width));
 #pragma unroll
-  for (int i = 0; i < V - 1; ++i) {
-    if (i >= width) continue;
+  for (int i = 0; i < Elem<T>::kVec - 1; ++i) {
+    if (c > 0 || i >= width) continue;
     if constexpr (T == T_F32)
       v[i] = row[i];
     else
@@ -102,16 +100,15 @@ __device__ __forceinline__ u4_t load_vec(const typename Elem<T>::raw* row, int c
   }
   return v;
 }
-template <int T>
+template <int T, bool NARROW>
 __device__ __forceinline__ void store_vec(typename Elem<T>::raw* row, int c, int width, u4_t v) {
-  constexpr int V = Elem<T>::kVec;
-  if (c * V >= width) return;
-  if (width >= V) {
+  if (c * Elem<T>::kVec >= width) return;
+  if constexpr (!NARROW) {
     *reinterpret_cast<u4_any_t*>(row + vec_at<T>(c, width)) = v;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < V - 1; ++i) {
+  for (int i = 0; i < Elem<T>::kVec - 1; ++i) {
     if (i >= width) continue;
     if constexpr (T == T_F32)
       row[i] = v[i];
@@ -137,49 +134,68 @@ struct RowParams {
 };
 
 // rows [offsets[E], S) of `rows` cleared by waves w, w + waves, ...
-template <int T>
+template <int T, bool NARROW>
 __device__ __forceinline__ void clear_tail(const RowParams& p, void* rows, int w, int waves, int lane) {
   const int vecs = (p.width + Elem<T>::kVec - 1) / Elem<T>::kVec;
   for (int row = p.plan[p.E] + w; row < p.S; row += waves)
     for (int c = lane; c < vecs; c += 64)
-      store_vec<T>(static_cast<typename Elem<T>::raw*>(rows) + (size_t)row * p.width, c, p.width, u4_t{0, 0, 0, 0});
+      store_vec<T, NARROW>(static_cast<typename Elem<T>::raw*>(rows) + (size_t)row * p.width, c, p.width, u4_t{0, 0, 0, 0});
 }
 
-template <int T>
+template <int T, bool NARROW>
 __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
   const int lane = threadIdx.x & 63;
   const int item = __builtin_amdgcn_readfirstlane(blockIdx.x * kRowWaves + (threadIdx.x >> 6));
   const int items = p.tokens * p.segs;
   if (item >= items) {
-    if (item < items + p.tail_waves) clear_tail<T>(p, p.out, item - items, p.tail_waves, lane);
+    if (item < items + p.tail_waves) clear_tail<T, NARROW>(p, p.out, item - items, p.tail_waves, lane);
     return;
   }
   const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * kRowVecs + lane;
   const raw* src = static_cast<const raw*>(p.x) + (size_t)t * p.width;
   u4_t v[kRowVecs];
 #pragma unroll
-  for (int u = 0; u < kRowVecs; ++u) v[u] = load_vec<T>(src, c0 + 64 * u, p.width);
+  for (int u = 0; u < kRowVecs; ++u) v[u] = load_vec<T, NARROW>(src, c0 + 64 * u, p.width);
   const int32_t* slot = p.plan + p.slot + (size_t)t * p.topk;
   for (int j = 0; j < p.topk; ++j) {
     const int row = slot[j];
     if (row < 0) continue;
     raw* dst = static_cast<raw*>(p.out) + (size_t)row * p.width;
 #pragma unroll
-    for (int u = 0; u < kRowVecs; ++u) store_vec<T>(dst, c0 + 64 * u, p.width, v[u]);
+    for (int u = 0; u < kRowVecs; ++u) store_vec<T, NARROW>(dst, c0 + 64 * u, p.width, v[u]);
   }
 }
 
-template <int T, int TO>
+// The sorted rows and weights of choices j0 .. j0 + J - 1 of a token, all read at once: row -1 for
+// slots of no group and past the last choice
+template <int J>
+__device__ __forceinline__ void load_choices(const RowParams& p, int t, int j0, int (&row)[J], float (&w)[J]) {
+  const int32_t* slot = p.plan + p.slot + (size_t)t * p.topk;
+  // no weights: any words there are, and 1
+  const float* weight = p.weights ? p.weights + (size_t)t * p.topk : reinterpret_cast<const float*>(slot);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int at = min(j0 + j, p.topk - 1);
+    row[j] = slot[at];
+    w[j] = weight[at];
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    row[j] = j0 + j < p.topk ? row[j] : -1;
+    w[j] = p.weights ? w[j] : 1.0f;
+  }
+}
+
+// J: sorted rows in flight, min(topk, 4) or 8. A choice of no row reads row 0 and adds nothing.
+template <int T, int TO, int J, bool NARROW>
 __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
-  constexpr int V = Elem<T>::kVec, J = 4;  // sorted rows in flight
+  constexpr int V = Elem<T>::kVec;
   const int lane = threadIdx.x & 63;
   const int item = __builtin_amdgcn_readfirstlane(blockIdx.x * kRowWaves + (threadIdx.x >> 6));
   if (item >= p.tokens * p.segs) return;
   const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * kRowVecs + lane;
-  const int32_t* slot = p.plan + p.slot + (size_t)t * p.topk;
-  const float* weight = p.weights ? p.weights + (size_t)t * p.topk : nullptr;
   float acc[kRowVecs][V];
 #pragma unroll
   for (int u = 0; u < kRowVecs; ++u)
@@ -189,17 +205,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
     u4_t v[J][kRowVecs];
     int row[J];
     float w[J];
+    load_choices(p, t, j0, row, w);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      row[j] = j0 + j < p.topk ? slot[j0 + j] : -1;
-      w[j] = row[j] >= 0 && weight ? weight[j0 + j] : 1.0f;
-    }
+      const raw* src = static_cast<const raw*>(p.ys) + (size_t)max(row[j], 0) * p.width;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (row[j] < 0) continue;
-      const raw* src = static_cast<const raw*>(p.ys) + (size_t)row[j] * p.width;
-#pragma unroll
-      for (int u = 0; u < kRowVecs; ++u) v[j][u] = load_vec<T>(src, c0 + 64 * u, p.width);
+      for (int u = 0; u < kRowVecs; ++u) v[j][u] = load_vec<T, NARROW>(src, c0 + 64 * u, p.width);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -215,19 +226,19 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
 #pragma unroll
   for (int u = 0; u < kRowVecs; ++u) {
     if constexpr (Elem<TO>::kVec == V) {
-      store_vec<TO>(dst, c0 + 64 * u, p.width, vec_pack<TO>(acc[u]));
+      store_vec<TO, NARROW>(dst, c0 + 64 * u, p.width, vec_pack<TO>(acc[u]));
     } else {  // fp32 rows to 16-bit tokens: a lane's four elements are half a vector
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if ((c0 + 64 * u) * V < p.width && i < p.width)
-          dst[vec_at<T>(c0 + 64 * u, p.width) + i] = elem_bits<TO>(acc[u][i]);
+        if ((c0 + 64 * u) * V < p.width && (!NARROW || i < p.width))
+          dst[(NARROW ? 0 : vec_at<T>(c0 + 64 * u, p.width)) + i] = elem_bits<TO>(acc[u][i]);
     }
   }
 }
 
 // One workgroup per token (its waves share the row): the products of dy with the token's sorted
 // rows are summed per lane, then over the lanes and waves in a fixed order.
-template <int T, int J>
+template <int T, int J, bool NARROW>
 __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
   constexpr int V = Elem<T>::kVec;
@@ -236,7 +247,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x;
   if (t >= p.tokens) {  // the workgroups after the tokens'
-    clear_tail<T>(p, p.out, (t - p.tokens) * kRowWaves + wave, p.tail_waves, lane);
+    clear_tail<T, NARROW>(p, p.out, (t - p.tokens) * kRowWaves + wave, p.tail_waves, lane);
     return;
   }
   const int vecs = (p.width + V - 1) / V;
@@ -244,24 +255,20 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
   for (int j0 = 0; j0 < p.topk; j0 += J) {
     int row[J];
     float w[J], acc[J];
+    load_choices(p, t, j0, row, w);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const size_t at = (size_t)t * p.topk + j0 + j;
-      row[j] = j0 + j < p.topk ? p.plan[p.slot + at] : -1;
-      w[j] = row[j] >= 0 ? p.weights[at] : 0.f;
-      acc[j] = 0.f;
-    }
+    for (int j = 0; j < J; ++j) acc[j] = 0.f;
     for (int c = threadIdx.x; c < vecs; c += 64 * kRowWaves) {
-      const u4_t d = load_vec<T>(dy, c, p.width);
+      const u4_t d = load_vec<T, NARROW>(dy, c, p.width);
       u4_t v[J];
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (row[j] >= 0) v[j] = load_vec<T>(static_cast<const raw*>(p.ys) + (size_t)row[j] * p.width, c, p.width);
+        v[j] = load_vec<T, NARROW>(static_cast<const raw*>(p.ys) + (size_t)max(row[j], 0) * p.width, c, p.width);
       float f[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = vec_value<T>(d, i);
       // a last vector that was moved back: its neighbour's elements are not summed again
-      const int again = c * V - vec_at<T>(c, p.width);
+      const int again = NARROW ? 0 : c * V - vec_at<T>(c, p.width);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if (row[j] < 0) continue;
@@ -276,7 +283,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
           for (int i = 0; i < V; ++i)
             if (i >= again) acc[j] = __builtin_fmaf(f[i], vec_value<T>(v[j], i), acc[j]);
         }
-        store_vec<T>(static_cast<raw*>(p.out) + (size_t)row[j] * p.width, c, p.width, vec_pack<T>(g));
+        store_vec<T, NARROW>(static_cast<raw*>(p.out) + (size_t)row[j] * p.width, c, p.width, vec_pack<T>(g));
       }
     }
 #pragma unroll
@@ -320,17 +327,42 @@ bool rows_fit(int tokens, int width) {
   return waves < (1LL << 26) && ((long long)tokens + kTailWaves) * 64 * kRowWaves < (1LL << 32);
 }
 
+template <int T>
+static void launch_dispatch_t(const RowParams& p, dim3 grid, hipStream_t s) {
+  if (p.width < Elem<T>::kVec)
+    hipLaunchKernelGGL((dispatch_kernel<T, true>), grid, dim3(64 * kRowWaves), 0, s, p);
+  else
+    hipLaunchKernelGGL((dispatch_kernel<T, false>), grid, dim3(64 * kRowWaves), 0, s, p);
+}
+
 hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* plan, int width, int dtype,
                            void* xs, hipStream_t s) {
   RowParams p = row_params(r, plan, width, dtype == T_F32 ? 4 : 8);
   p.x = x;
   p.out = xs;
-  const dim3 grid(ceil_div(p.tokens * p.segs + p.tail_waves, kRowWaves)), block(64 * kRowWaves);
+  const dim3 grid(ceil_div(p.tokens * p.segs + p.tail_waves, kRowWaves));
   if (dtype == T_F32)
-    hipLaunchKernelGGL((dispatch_kernel<T_F32>), grid, block, 0, s, p);
+    launch_dispatch_t<T_F32>(p, grid, s);
   else  // a copy: the 16-bit types are alike
-    hipLaunchKernelGGL((dispatch_kernel<T_F16>), grid, block, 0, s, p);
+    launch_dispatch_t<T_F16>(p, grid, s);
   return hipGetLastError();
+}
+
+template <int T, int TO>
+static void launch_combine_t(const RowParams& p, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * kRowWaves);
+  if (p.width < Elem<T>::kVec)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 1, true>), grid, block, 0, s, p);
+  else if (p.topk == 1)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 1, false>), grid, block, 0, s, p);
+  else if (p.topk == 2)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 2, false>), grid, block, 0, s, p);
+  else if (p.topk == 3)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 3, false>), grid, block, 0, s, p);
+  else if (p.topk == 4)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 4, false>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_kernel<T, TO, 8, false>), grid, block, 0, s, p);
 }
 
 hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* plan, const float* weights,
@@ -339,31 +371,35 @@ hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* p
   p.ys = ys;
   p.weights = weights;
   p.out = y;
-  const dim3 grid(ceil_div(p.tokens * p.segs, kRowWaves)), block(64 * kRowWaves);
+  const dim3 grid(ceil_div(p.tokens * p.segs, kRowWaves));
   if (dtype == T_F16)
-    hipLaunchKernelGGL((combine_kernel<T_F16, T_F16>), grid, block, 0, s, p);
+    launch_combine_t<T_F16, T_F16>(p, grid, s);
   else if (dtype == T_BF16)
-    hipLaunchKernelGGL((combine_kernel<T_BF16, T_BF16>), grid, block, 0, s, p);
+    launch_combine_t<T_BF16, T_BF16>(p, grid, s);
   else if (out_dtype == T_F32)
-    hipLaunchKernelGGL((combine_kernel<T_F32, T_F32>), grid, block, 0, s, p);
+    launch_combine_t<T_F32, T_F32>(p, grid, s);
   else if (out_dtype == T_F16)
-    hipLaunchKernelGGL((combine_kernel<T_F32, T_F16>), grid, block, 0, s, p);
+    launch_combine_t<T_F32, T_F16>(p, grid, s);
   else
-    hipLaunchKernelGGL((combine_kernel<T_F32, T_BF16>), grid, block, 0, s, p);
+    launch_combine_t<T_F32, T_BF16>(p, grid, s);
   return hipGetLastError();
 }
 
 template <int T>
 static void launch_backward(const RowParams& p, hipStream_t s) {
   const dim3 grid(p.tokens + ceil_div(p.tail_waves, kRowWaves)), block(64 * kRowWaves);
-  if (p.topk == 1)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 1>), grid, block, 0, s, p);
+  if (p.width < Elem<T>::kVec)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 1, true>), grid, block, 0, s, p);
+  else if (p.topk == 1)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 1, false>), grid, block, 0, s, p);
   else if (p.topk == 2)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 2>), grid, block, 0, s, p);
-  else if (p.topk <= 4)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 4>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((combine_backward_kernel<T, 2, false>), grid, block, 0, s, p);
+  else if (p.topk == 3)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 3, false>), grid, block, 0, s, p);
+  else if (p.topk == 4)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 4, false>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((combine_backward_kernel<T, 8>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((combine_backward_kernel<T, 8, false>), grid, block, 0, s, p);
 }
 
 hipError_t launch_combine_backward(const void* dy, const void* ys, const RouteLayout& r, const int32_t* plan,
