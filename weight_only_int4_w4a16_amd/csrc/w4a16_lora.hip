@@ -30,7 +30,7 @@
 //
 // Measured: one row, 4096x4096 rank 16 fp16 9.8 us (one launch; two took 14.0); 96 rows with 64
 // adapters, 4096x14336 rank 32 bf16 18 us (62 MB; first product 7.7, second 11.7 at 5.5 TB/s); 4096 rows
-// with 9 adapters, 8192x8192 rank 64 bf16 68 us (220 MB; sort 8.6, first product 18.2, second 35 at 4.7
+// with 9 adapters, 8192x8192 rank 64 bf16 68 us (208 MB; sort 8.6, first product 18.2, second 35 at 4.7
 // TB/s, near a copy's rate).
 #include <type_traits>
 
