@@ -60,6 +60,10 @@ def _ids(tokens, topk, groups, seed, how="mixed"):
         ids[:] = -1
     elif how == "skewed":
         ids = np.minimum(ids, g.integers(0, groups, size=(tokens, topk)) // 3)
+    elif how == "steps":  # 1, 16, 17, 32, 33 .. rows, the rest in the last group: every share of a tile
+        ids = np.repeat(np.arange(groups), [16 * (e // 2) + (1 if e % 2 == 0 else 16) for e in range(groups)])[:tokens * topk]
+        ids = np.concatenate([ids, np.full(tokens * topk - len(ids), groups - 1)])
+        ids = ids[g.permutation(len(ids))].reshape(tokens, topk)
     return ids.astype(np.int32)
 
 
@@ -305,6 +309,20 @@ def test_grouped_more_rows(tokens, groups, K, N, act, fmt, g):
 @pytest.mark.parametrize("tokens,groups,K,N", [(500, 8, 192, 12576), (2100, 2, 192, 4128)])
 def test_grouped_many_rows_in_every_format(tokens, groups, K, N, act, fmt, g):
     _check_grouped(tokens, 1, groups, K, N, g, act, fmt, fmt != "asym", gather=True)
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt,g", [("asym", 32), ("asym", 64), ("sym", 32), ("sym", 128), ("nf4", 32), ("nf4", 64)])
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("tokens,groups", [(70, 4), (330, 8)])  # tiles of 32 and of 64 rows
+def test_grouped_every_share_of_a_tile(tokens, groups, act, fmt, g, glu):
+    _check_grouped(tokens, 1, groups, 384, 96, g, act, fmt, glu, False, "steps")
+
+
+@pytest.mark.parametrize("act,fmt,g,glu", [("f16", "asym", 64, False), ("f16", "nf4", 64, True), ("bf16", "sym", 128, True),
+                                           ("bf16", "nf4", 32, False)])
+def test_grouped_every_share_of_a_tile_side_by_side(act, fmt, g, glu):
+    _check_grouped(500, 1, 8, 256, 12576, g, act, fmt, glu, True, "steps")
 
 
 def test_no_tokens():

@@ -31,14 +31,16 @@ int forced_tile() {
 }
 
 // The rows of each group are known on the device only, so the tile goes by their mean over the
-// groups that can have rows. A taller tile forms W_hat once for more rows and is part-filled
-// more often, so the limits lie where tiles win on routings as uneven as gates make them (top-k of
-// normal scores with expert biases of 0.7 sigma; us with 16/32/64/128 rows a tile). 8 experts of
-// 4096x14336 g128: mean 6 44/44/56/101, 12 56/49/60/114, 24 86/73/79/114, 48 135/103/101/189, 64
-// 161/120/108/198, 128 310/231/177/214, 192 470/357/213/227, 384 -/816/415/437, 512 -/-/529/530; 64
-// experts of 2048x2816 g128: 8 38/40/51/116, 24 71/61/68/121, 48 111/88/85/170, 128 245/194/139/233, 384
-// -/572/338/420. Deep and narrow weights (8 of 14336x4096) leave the 128-row tile earlier room: 192 -/475/239/283, 256
-// -/646/319/293.
+// groups that can have rows. A taller tile forms W_hat once for more rows, but takes more registers
+// and LDS, so that fewer waves run; the limits lie where tiles win on routings as uneven as gates make
+// them (top-k of normal scores with expert biases of 0.7 sigma). us with 16/32/64/128 rows a tile, fp16
+// g128 with zeros, by mean rows:
+//   8 of 4096x14336   4 51/50/55, 8 45/43/46, 16 72/60/62, 24 88/70/75, 32 101/85/70, 48 135/104/92,
+//                     128 320/237/167/217, 256 -/-/295/323, 384 -/-/432/430, 512 -/-/559/552, 768 -/-/821/711
+//   64 of 2048x2816   4 31/33/37, 8 41/39/43, 16 53/46/45, 24 68/57/54, 32 83/69/61, 128 261/193/136/222,
+//                     384 -/-/349/407, 768 -/-/664/669
+//   8 of 14336x4096   4 41/53/44, 8 45/59/51, 16 64/72/56, 32 104/83/75, 128 388/320/244/281, 192 -/-/389/291,
+//                     256 -/-/324/314
 // Past 384 rows the 128 x 512 tile can still leave most of the chip idle (few groups, narrow N): then
 // 64-row tiles, by a model of compute-unit time (0.42 us per 64x64 tile and k-block; 2.6 us per
 // 128x512 tile and k-block in one round of workgroups, 3.2 us in more).
@@ -46,8 +48,8 @@ Tile choose_tile(int S, int E, int K, int N) {
   if (forced_tile() >= 0) return (Tile)forced_tile();
   const int groups = E < S ? E : S;
   const int mean = S / (groups > 0 ? groups : 1);
-  if (mean <= 9) return TILE_16;
-  if (mean <= 44) return TILE_32;
+  if (mean <= (K > 8192 ? 9 : 6)) return TILE_16;
+  if (mean <= 28) return TILE_32;
   if (mean <= (K > 8192 ? 144 : 384)) return TILE_64;
   const long long cus = device_cu_count();
   const long long rounds = ((S / 128 + groups / 2) * (long long)ceil_div(N, 512) + cus - 1) / cus;

@@ -15,6 +15,12 @@
 // LDS in wave order. Row tiles of one group and column tile are neighbours on one XCD, so a
 // second tile of the same group finds the codes in that L2.
 //
+// A tile has up to MT sixteens of rows, and the kernel a whole body for each number of them: the
+// workgroup takes the one that its rows need, so that a part-filled tile costs no MFMAs, fragment
+// reads or sums for rows that it has not (8 experts of 14336x4096 at a mean of 8 rows in 64-row tiles
+// 61 -> 46 us, of 4096x14336 at 32 rows 91 -> 71). Branches per sixteen inside one body cost registers for
+// all paths at once, and spilled.
+//
 // Operands. v_mfma_f32_16x16x32: word j of a lane's 16-byte chunk of a packed block is its B
 // operand for k-step j. The A operand's sixteen rows go through LDS: read from memory in its
 // layout, sixteen lanes at a time would touch sixteen rows' cache lines (a 1 KiB load then
@@ -30,6 +36,8 @@
 // (exact in fp16), fma(v, s, -(1024 + z) s) is exact: both products have at most 19 significant
 // bits. 17 instructions. The constants cost two multiplications per strip and scale group.
 #pragma once
+
+#include <type_traits>
 
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"
@@ -135,6 +143,19 @@ __device__ __forceinline__ typename ActT<ACT>::type dequant_word(uint32_t w, con
   }
 }
 
+// f(n), n a constant: the sixteens of rows that a tile of up to MT of them has
+template <int MT, typename F>
+__device__ __forceinline__ void for_active(int rows, F&& f) {
+  if constexpr (MT == 1) {
+    f(std::integral_constant<int, 1>{});
+  } else {
+    if (rows <= 16 * (MT - 1))
+      for_active<MT - 1>(rows, f);
+    else
+      f(std::integral_constant<int, MT>{});
+  }
+}
+
 constexpr int slot_halves(int MT) { return 16 * MT * 128; }
 // floats between rows of a partial tile: four rows written at once then fall in different banks
 constexpr int kRedStride = 16 * kStrips + 4;
@@ -179,12 +200,11 @@ constexpr int waves_per_simd(int MT, int GPC) { return (MT == 1 ? 4 : MT == 2 ? 
 // GLU: the first two strips are gate strips, the others the matching up strips, and the output
 // is h = SiLU(gate) * up, [S][N / 2].
 template <int ACT, int GPC, int FMT, int MT, bool GLU, int W>
-__global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kernel(GroupedParams p) {
+__device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint16_t* lds, uint32_t* ptab, int tn, int e,
+                                             int p0, int rows) {
   typedef typename ActT<ACT>::type AT;
   constexpr bool ZEROS = FMT == FMT_ASYM;
   constexpr int SW = kStrips, OS = GLU ? SW / 2 : SW;  // strips, output strips
-  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];  // [waves][wave_lds(MT)]
-  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries : 1];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -193,16 +213,7 @@ __global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kerne
   const int shift = 4 * (lane & 7);
   uint16_t* const slot = lds + wave * (wave_lds(MT) / 2);
   const int kc0 = min(wave * p.slice, KC), kc1 = min(kc0 + p.slice, KC);
-  const int item = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
-  const int tn = item / p.groups.bound;
-  int e, p0, end;
-  if (!group_tile(p.groups, item - tn * p.groups.bound, e, p0, end)) return;
-  const int rows = end - p0;
   const int ocol0 = tn * OS * 16, ocols = min(OS * 16, width - ocol0);
-  if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
-    zero_tile(p.out, p.out_dtype, p0, rows, width, ocol0, OS * 16);
-    return;
-  }
   struct Codes {
     u4_t b[SW];
     uint32_t s[SW][GPC], z[SW][GPC];
@@ -337,6 +348,26 @@ __global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kerne
   }
 }
 
+template <int ACT, int GPC, int FMT, int MT, bool GLU, int W>
+__global__ __launch_bounds__(64 * W, waves_per_simd(MT, GPC)) void grouped_kernel(GroupedParams p) {
+  constexpr int OS = GLU ? kStrips / 2 : kStrips;
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];  // [waves][wave_lds(MT)]
+  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries : 1];
+  const int item = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
+  const int tn = item / p.groups.bound;
+  int e, p0, end;
+  if (!group_tile(p.groups, item - tn * p.groups.bound, e, p0, end)) return;
+  const int rows = end - p0;
+  const int width = GLU ? p.N >> 1 : p.N;
+  if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
+    zero_tile(p.out, p.out_dtype, p0, rows, width, tn * OS * 16, OS * 16);
+    return;
+  }
+  for_active<MT>(rows, [&](auto active) __attribute__((always_inline)) {
+    grouped_tile<ACT, GPC, FMT, decltype(active)::value, GLU, W>(p, lds, ptab, tn, e, p0, rows);
+  });
+}
+
 // ---------------------------------------------------------------------------------------
 // The same product with the waves side by side: a wave owns four strips over all of K, a
 // workgroup 256 columns, and x is shared. Nothing is added between waves, a wave's fixed work is spread
@@ -354,27 +385,17 @@ constexpr size_t cols_lds(int MT) {
 }
 
 template <int ACT, int GPC, int FMT, int MT, bool GLU>
-__global__ __launch_bounds__(64 * kWaves, cols_waves_per_simd(MT, GPC)) void grouped_cols_kernel(GroupedParams p) {
+__device__ __forceinline__ void grouped_cols_tile(const GroupedParams& p, uint16_t* lds, uint32_t* ptab, int tn, int e,
+                                                  int p0, int rows) {
   typedef typename ActT<ACT>::type AT;
   constexpr bool ZEROS = FMT == FMT_ASYM;
   constexpr int SW = kStrips, OS = GLU ? SW / 2 : SW;  // strips of a wave, output strips
-  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
-  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries : 1];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = p.K, N = p.N, KC = p.KC;
   const int width = GLU ? N >> 1 : N;  // of an output row
   const int shift = 4 * (lane & 7);
-  const int item = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
-  const int tn = item / p.groups.bound;
-  int e, p0, end;
-  if (!group_tile(p.groups, item - tn * p.groups.bound, e, p0, end)) return;
-  const int rows = end - p0;
-  if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
-    zero_tile(p.out, p.out_dtype, p0, rows, width, tn * kWaves * OS * 16, kWaves * OS * 16);
-    return;
-  }
   const int s0 = (tn * kWaves + wave) * OS;  // the wave's first (gate) strip
   const u4_t* const wbase = p.packed + (size_t)e * p.NT * KC * 64;
   const uint16_t* const sbase = p.scales + (size_t)e * p.NG * N;
@@ -497,6 +518,26 @@ __global__ __launch_bounds__(64 * kWaves, cols_waves_per_simd(MT, GPC)) void gro
     }
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+template <int ACT, int GPC, int FMT, int MT, bool GLU>
+__global__ __launch_bounds__(64 * kWaves, cols_waves_per_simd(MT, GPC)) void grouped_cols_kernel(GroupedParams p) {
+  constexpr int OS = GLU ? kStrips / 2 : kStrips;
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  __shared__ uint32_t ptab[FMT == FMT_NF4 ? kNf4PairEntries : 1];
+  const int item = tile_of(blockIdx.x, p.groups.bound * p.col_tiles);
+  const int tn = item / p.groups.bound;
+  int e, p0, end;
+  if (!group_tile(p.groups, item - tn * p.groups.bound, e, p0, end)) return;
+  const int rows = end - p0;
+  const int width = GLU ? p.N >> 1 : p.N;
+  if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
+    zero_tile(p.out, p.out_dtype, p0, rows, width, tn * kWaves * OS * 16, kWaves * OS * 16);
+    return;
+  }
+  for_active<MT>(rows, [&](auto active) __attribute__((always_inline)) {
+    grouped_cols_tile<ACT, GPC, FMT, decltype(active)::value, GLU>(p, lds, ptab, tn, e, p0, rows);
+  });
 }
 
 struct GroupedGeometry {
