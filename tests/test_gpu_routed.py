@@ -98,6 +98,20 @@ def test_route_is_the_stable_sort(tokens, topk, groups, how):
     assert np.array_equal(r.offsets.cpu().numpy(), offsets)
     assert np.array_equal(r.order.cpu().numpy(), order)
     assert np.array_equal(r.slot.cpu().numpy(), slot)
+    # behind them the sorted rows' tokens (the order itself for topk 1), then the lists of row tiles
+    plan, S = r.plan.cpu().numpy(), tokens * topk
+    up = lambda n: (n + 63) // 64 * 64
+    at = up(groups + 1) + 2 * up(S)
+    if topk > 1:
+        assert np.array_equal(plan[at:at + S], order // topk)
+        at += up(S)
+    bounds = np.append(offsets, S)  # the slots of no group are the last
+    for rows in (16, 32, 64, 128):
+        want = [(e, p, min(p + rows, bounds[e + 1]), 0) for e in range(groups + 1)
+                for p in range(bounds[e], bounds[e + 1], rows)]
+        assert plan[at] == len(want)
+        assert np.array_equal(plan[at + 4:at + 4 + 4 * len(want)].reshape(-1, 4), np.array(want, np.int32).reshape(-1, 4))
+        at += up(4 + 4 * (S // rows + min(groups + 1, S)))
 
 
 # ------------------------------------------------------------------ rows into order and back

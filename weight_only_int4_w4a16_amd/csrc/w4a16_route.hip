@@ -13,11 +13,17 @@
 // the rank inside a wave needs no atomics and the order never varies.
 //
 // The bytes are few (4 S read, 8 S written); a call is bound by the latency of its dependent
-// steps. Up to 4096 slots one workgroup does everything in one launch (four waves up to 512 slots, whose
-// barriers are cheaper). More take two launches over workgroups of 2048 slots: the first counts
-// its slots per group, and in the second every workgroup adds up all the counts itself, which
-// saves a launch between them; only where the counts are many (over 64 Ki words) does a third
-// kernel scan them once in between.
+// steps: read, rank, count, scan, place. So the scans use DPP, and the tile lists are written side by
+// side, each by its share of the threads. Up to 4096 slots one workgroup does everything in one
+// launch (four waves up to 512 slots, whose barriers are cheaper). More take two launches over
+// workgroups of 2048 slots: the first counts its slots per group, and in the second every
+// workgroup adds up all the counts itself, which saves a launch between them, and writes its share
+// of the lists; only where the counts are many (over 64 Ki words) does a third kernel scan them once in
+// between.
+//
+// Measured (us): 32 slots of 8 groups 3.5, 512 of 64 5.6, 1600 of 64 6.2, 4096 of 16 7.2; 16384 of 8 4.7 + 6.8,
+// 131072 of 128 5.0 + 10.6. (With shuffles for the scans and the lists one after another: 5.1, 7.6, 8.0,
+// 8.3; 7.2 and 15.3 for the second launches.)
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"
 
@@ -76,15 +82,21 @@ __device__ __forceinline__ void count_wave(const RouteParams& p, int first, int 
   }
 }
 
-// exclusive sums over the wave's lanes
-__device__ __forceinline__ int wave_exclusive(int v, int lane, int& total) {
+// v of the lane that a DPP control names, 0 where it names none or the row is masked off
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_0(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+// exclusive sums over the wave's lanes (DPP: a shuffle goes through LDS, six in a row for each scan)
+__device__ __forceinline__ int wave_exclusive(int v, int& total) {
   int s = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(s, o);
-    if (lane >= o) s += u;
-  }
-  total = __shfl(s, 63);
+  s += dpp_or_0<0x111, 0xF>(s);  // one lane to the right in its row of sixteen, then 2, 4, 8
+  s += dpp_or_0<0x112, 0xF>(s);
+  s += dpp_or_0<0x114, 0xF>(s);
+  s += dpp_or_0<0x118, 0xF>(s);
+  s += dpp_or_0<0x142, 0xA>(s);  // lane 15 of rows 0 and 2 to rows 1 and 3
+  s += dpp_or_0<0x143, 0xC>(s);  // lane 31 to rows 2 and 3
+  total = __builtin_amdgcn_readlane(s, 63);
   return s - v;
 }
 
@@ -95,7 +107,7 @@ __device__ __forceinline__ void scan_groups(const int* tot, int* out, int E, int
     const int g = g0 + lane;
     int total;
     const int n = g <= E ? (tot[g] + rows - 1) / rows : 0;
-    const int s = wave_exclusive(n, lane, total);
+    const int s = wave_exclusive(n, total);
     if (g <= E) out[g] = carry + s;
     carry += total;
   }
@@ -110,14 +122,14 @@ __device__ __forceinline__ void scan_all(const int* tot, int* scan, int E, int W
   __syncthreads();
 }
 
-// tile list j of the plan from the scans
-__device__ __forceinline__ void write_list(const RouteParams& p, const int* scan, int j) {
+// tile list j of the plan from the scans, by threads `thread` of `threads`
+__device__ __forceinline__ void write_list(const RouteParams& p, const int* scan, int j, int thread, int threads) {
   const int E = p.r.E;
   const int* first = scan + (j + 1) * (E + 2);
   int32_t* const list = p.plan + p.r.tiles[j];
   const int n = first[E + 1], tile_rows = kTileRows[j];
-  if (threadIdx.x == 0) list[0] = n;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+  if (thread == 0) list[0] = n;
+  for (int i = thread; i < n; i += threads) {
     int lo = 0, hi = E;  // the last group whose first tile is at or before i
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -155,6 +167,7 @@ template <int PASS, int W, int B>
 __global__ __launch_bounds__(64 * W) void route_kernel(RouteParams p) {
   extern __shared__ int lds[];
   const int E = p.r.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int PER = 64 * W / kTileLists;  // threads of a tile list
   int* const cnt = lds;                  // [W][E + 1]
   int* const tot = cnt + W * (E + 1);    // [E + 1]: the block's (SCATTER: all blocks') slots per group
   int* const base = tot + (E + 1);       // [E + 1]: SCATTER: slots of the group in earlier blocks
@@ -188,7 +201,7 @@ __global__ __launch_bounds__(64 * W) void route_kernel(RouteParams p) {
   if constexpr (PASS == WHOLE) {
     scan_all(tot, scan, E, W);
     for (int g = threadIdx.x; g <= E; g += 64 * W) p.plan[g] = scan[g];
-    for (int j = 0; j < kTileLists; ++j) write_list(p, scan, j);
+    write_list(p, scan, threadIdx.x / PER, threadIdx.x % PER, PER);
   } else {
     const int32_t* const hist = p.plan + p.r.hist;
     if (p.scanned) {
@@ -216,8 +229,7 @@ __global__ __launch_bounds__(64 * W) void route_kernel(RouteParams p) {
       scan_all(tot, scan, E, W);
       if (blockIdx.x == 0)
         for (int g = threadIdx.x; g <= E; g += 64 * W) p.plan[g] = scan[g];
-      for (int j = 0; j < kTileLists; ++j)
-        if (j % p.r.blocks == (int)blockIdx.x) write_list(p, scan, j);
+      write_list(p, scan, threadIdx.x / PER, blockIdx.x * PER + threadIdx.x % PER, p.r.blocks * PER);
       __syncthreads();
       for (int g = threadIdx.x; g <= E; g += 64 * W) scan[g] += base[g];
       __syncthreads();
@@ -245,7 +257,8 @@ __global__ __launch_bounds__(64 * kScanWaves) void route_scan_kernel(RouteParams
   __syncthreads();
   scan_all(tot, scan, E, kScanWaves);
   for (int g = threadIdx.x; g <= E; g += 64 * kScanWaves) p.plan[g] = scan[g];
-  for (int j = 0; j < kTileLists; ++j) write_list(p, scan, j);
+  constexpr int PER = 64 * kScanWaves / kTileLists;
+  write_list(p, scan, threadIdx.x / PER, threadIdx.x % PER, PER);
   for (int g = threadIdx.x; g <= E; g += 64 * kScanWaves) {
     int s = scan[g];
     for (int b = 0; b < p.r.blocks; ++b) {
