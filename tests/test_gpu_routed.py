@@ -122,6 +122,8 @@ ROW_CASES = [
     (300, 1, 40, 2048, "bf16"),
     # narrower than a vector, just wider, and one wave's share and one element
     (7, 3, 4, 3, "f32"), (6, 6, 5, 2, "bf16"), (8, 8, 3, 5, "f32"), (10, 4, 5, 9, "f16"), (21, 6, 4, 1025, "f16"),
+    # sorted rows past the size where they are streamed, in whole cache lines and not
+    (8256, 2, 5, 2048, "bf16"), (4200, 2, 9, 4001, "f16"), (4200, 1, 3, 4096, "f32"),
 ]
 
 

@@ -27,6 +27,7 @@ namespace w4a16 {
 namespace {
 
 enum { T_F16 = 0, T_BF16 = 1, T_F32 = 2 };
+enum { NARROW = 0, CACHED = 1, STREAM = 2, STREAM_LINES = 3 };
 
 typedef u4_t u4_any_t __attribute__((aligned(2)));  // sixteen bytes at any element's address
 
@@ -81,14 +82,23 @@ __device__ __forceinline__ u4_t vec_pack(const float* f) {
 // made the sort, the two moves and their gradients of 4099 bf16 tokens of 2885 elements, topk 3,
 // take 133 us; so they took 112 us.) Vectors past the row read its last one and store nothing, so that
 // loads need no branch: the compiler puts a wait for all that is in flight before a load under
-// one. NARROW rows, shorter than a vector, are taken element by element.
+// one.
+//
+// Rows come in four modes. NARROW: shorter than a vector, taken element by element. CACHED.
+// STREAM: the sorted rows take 64 MiB or more (kStreamBytes), a quarter of the last-level cache, and
+// stores are non-temporal; STREAM_LINES: also the loads of the sorted rows, where these are whole
+// cache lines (shared lines would be fetched twice).
 template <int T>
 __device__ __forceinline__ int vec_at(int c, int width) {
   return min(c * Elem<T>::kVec, width - Elem<T>::kVec);
 }
-template <int T, bool NARROW>
+// ONCE: the row is read for the last time
+template <int T, int MODE, bool ONCE>
 __device__ __forceinline__ u4_t load_vec(const typename Elem<T>::raw* row, int c, int width) {
-  if constexpr (!NARROW) return *reinterpret_cast<const u4_any_t*>(row + vec_at<T>(c, width));
+  if constexpr (MODE != NARROW) {
+    const u4_any_t* const at = reinterpret_cast<const u4_any_t*>(row + vec_at<T>(c, width));
+    return ONCE && MODE == STREAM_LINES ? __builtin_nontemporal_load(at) : *at;
+  }
   u4_t v = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < Elem<T>::kVec - 1; ++i) {
@@ -100,11 +110,15 @@ __device__ __forceinline__ u4_t load_vec(const typename Elem<T>::raw* row, int c
   }
   return v;
 }
-template <int T, bool NARROW>
+template <int T, int MODE>
 __device__ __forceinline__ void store_vec(typename Elem<T>::raw* row, int c, int width, u4_t v) {
   if (c * Elem<T>::kVec >= width) return;
-  if constexpr (!NARROW) {
-    *reinterpret_cast<u4_any_t*>(row + vec_at<T>(c, width)) = v;
+  if constexpr (MODE != NARROW) {
+    u4_any_t* const at = reinterpret_cast<u4_any_t*>(row + vec_at<T>(c, width));
+    if constexpr (MODE >= STREAM)
+      __builtin_nontemporal_store(v, at);
+    else
+      *at = v;
     return;
   }
 #pragma unroll
@@ -134,36 +148,36 @@ struct RowParams {
 };
 
 // rows [offsets[E], S) of `rows` cleared by waves w, w + waves, ...
-template <int T, bool NARROW>
+template <int T, int MODE>
 __device__ __forceinline__ void clear_tail(const RowParams& p, void* rows, int w, int waves, int lane) {
   const int vecs = (p.width + Elem<T>::kVec - 1) / Elem<T>::kVec;
   for (int row = p.plan[p.E] + w; row < p.S; row += waves)
     for (int c = lane; c < vecs; c += 64)
-      store_vec<T, NARROW>(static_cast<typename Elem<T>::raw*>(rows) + (size_t)row * p.width, c, p.width, u4_t{0, 0, 0, 0});
+      store_vec<T, MODE>(static_cast<typename Elem<T>::raw*>(rows) + (size_t)row * p.width, c, p.width, u4_t{0, 0, 0, 0});
 }
 
-template <int T, bool NARROW>
+template <int T, int MODE>
 __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
   const int lane = threadIdx.x & 63;
   const int item = __builtin_amdgcn_readfirstlane(blockIdx.x * kRowWaves + (threadIdx.x >> 6));
   const int items = p.tokens * p.segs;
   if (item >= items) {
-    if (item < items + p.tail_waves) clear_tail<T, NARROW>(p, p.out, item - items, p.tail_waves, lane);
+    if (item < items + p.tail_waves) clear_tail<T, MODE>(p, p.out, item - items, p.tail_waves, lane);
     return;
   }
   const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * kRowVecs + lane;
   const raw* src = static_cast<const raw*>(p.x) + (size_t)t * p.width;
   u4_t v[kRowVecs];
 #pragma unroll
-  for (int u = 0; u < kRowVecs; ++u) v[u] = load_vec<T, NARROW>(src, c0 + 64 * u, p.width);
+  for (int u = 0; u < kRowVecs; ++u) v[u] = load_vec<T, MODE, false>(src, c0 + 64 * u, p.width);
   const int32_t* slot = p.plan + p.slot + (size_t)t * p.topk;
   for (int j = 0; j < p.topk; ++j) {
     const int row = slot[j];
     if (row < 0) continue;
     raw* dst = static_cast<raw*>(p.out) + (size_t)row * p.width;
 #pragma unroll
-    for (int u = 0; u < kRowVecs; ++u) store_vec<T, NARROW>(dst, c0 + 64 * u, p.width, v[u]);
+    for (int u = 0; u < kRowVecs; ++u) store_vec<T, MODE>(dst, c0 + 64 * u, p.width, v[u]);
   }
 }
 
@@ -188,7 +202,7 @@ __device__ __forceinline__ void load_choices(const RowParams& p, int t, int j0, 
 }
 
 // J: sorted rows in flight, min(topk, 4) or 8. A choice of no row reads row 0 and adds nothing.
-template <int T, int TO, int J, bool NARROW>
+template <int T, int TO, int J, int MODE>
 __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
   constexpr int V = Elem<T>::kVec;
@@ -210,7 +224,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
     for (int j = 0; j < J; ++j) {
       const raw* src = static_cast<const raw*>(p.ys) + (size_t)max(row[j], 0) * p.width;
 #pragma unroll
-      for (int u = 0; u < kRowVecs; ++u) v[j][u] = load_vec<T, NARROW>(src, c0 + 64 * u, p.width);
+      for (int u = 0; u < kRowVecs; ++u) v[j][u] = load_vec<T, MODE, true>(src, c0 + 64 * u, p.width);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -226,19 +240,19 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
 #pragma unroll
   for (int u = 0; u < kRowVecs; ++u) {
     if constexpr (Elem<TO>::kVec == V) {
-      store_vec<TO, NARROW>(dst, c0 + 64 * u, p.width, vec_pack<TO>(acc[u]));
+      store_vec<TO, MODE>(dst, c0 + 64 * u, p.width, vec_pack<TO>(acc[u]));
     } else {  // fp32 rows to 16-bit tokens: a lane's four elements are half a vector
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if ((c0 + 64 * u) * V < p.width && (!NARROW || i < p.width))
-          dst[(NARROW ? 0 : vec_at<T>(c0 + 64 * u, p.width)) + i] = elem_bits<TO>(acc[u][i]);
+        if ((c0 + 64 * u) * V < p.width && (MODE != NARROW || i < p.width))
+          dst[(MODE == NARROW ? 0 : vec_at<T>(c0 + 64 * u, p.width)) + i] = elem_bits<TO>(acc[u][i]);
     }
   }
 }
 
 // One workgroup per token (its waves share the row): the products of dy with the token's sorted
 // rows are summed per lane, then over the lanes and waves in a fixed order.
-template <int T, int J, bool NARROW>
+template <int T, int J, int MODE>
 __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
   constexpr int V = Elem<T>::kVec;
@@ -247,7 +261,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x;
   if (t >= p.tokens) {  // the workgroups after the tokens'
-    clear_tail<T, NARROW>(p, p.out, (t - p.tokens) * kRowWaves + wave, p.tail_waves, lane);
+    clear_tail<T, MODE>(p, p.out, (t - p.tokens) * kRowWaves + wave, p.tail_waves, lane);
     return;
   }
   const int vecs = (p.width + V - 1) / V;
@@ -259,16 +273,16 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[j] = 0.f;
     for (int c = threadIdx.x; c < vecs; c += 64 * kRowWaves) {
-      const u4_t d = load_vec<T, NARROW>(dy, c, p.width);
+      const u4_t d = load_vec<T, MODE, false>(dy, c, p.width);
       u4_t v[J];
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        v[j] = load_vec<T, NARROW>(static_cast<const raw*>(p.ys) + (size_t)max(row[j], 0) * p.width, c, p.width);
+        v[j] = load_vec<T, MODE, true>(static_cast<const raw*>(p.ys) + (size_t)max(row[j], 0) * p.width, c, p.width);
       float f[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = vec_value<T>(d, i);
       // a last vector that was moved back: its neighbour's elements are not summed again
-      const int again = NARROW ? 0 : c * V - vec_at<T>(c, p.width);
+      const int again = MODE == NARROW ? 0 : c * V - vec_at<T>(c, p.width);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if (row[j] < 0) continue;
@@ -283,7 +297,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
           for (int i = 0; i < V; ++i)
             if (i >= again) acc[j] = __builtin_fmaf(f[i], vec_value<T>(v[j], i), acc[j]);
         }
-        store_vec<T, NARROW>(static_cast<raw*>(p.out) + (size_t)row[j] * p.width, c, p.width, vec_pack<T>(g));
+        store_vec<T, MODE>(static_cast<raw*>(p.out) + (size_t)row[j] * p.width, c, p.width, vec_pack<T>(g));
       }
     }
 #pragma unroll
@@ -327,12 +341,24 @@ bool rows_fit(int tokens, int width) {
   return waves < (1LL << 26) && ((long long)tokens + kTailWaves) * 64 * kRowWaves < (1LL << 32);
 }
 
+constexpr size_t kStreamBytes = (size_t)64 << 20;
+
+template <int T>
+static int row_mode(const RowParams& p) {
+  constexpr size_t bytes = sizeof(typename Elem<T>::raw);
+  if (p.width < Elem<T>::kVec) return NARROW;
+  if (p.S * (size_t)p.width * bytes < kStreamBytes) return CACHED;
+  return p.width * bytes % 128 ? STREAM : STREAM_LINES;
+}
+
 template <int T>
 static void launch_dispatch_t(const RowParams& p, dim3 grid, hipStream_t s) {
-  if (p.width < Elem<T>::kVec)
-    hipLaunchKernelGGL((dispatch_kernel<T, true>), grid, dim3(64 * kRowWaves), 0, s, p);
-  else
-    hipLaunchKernelGGL((dispatch_kernel<T, false>), grid, dim3(64 * kRowWaves), 0, s, p);
+  const dim3 block(64 * kRowWaves);
+  switch (row_mode<T>(p)) {
+    case NARROW: hipLaunchKernelGGL((dispatch_kernel<T, NARROW>), grid, block, 0, s, p); break;
+    case CACHED: hipLaunchKernelGGL((dispatch_kernel<T, CACHED>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((dispatch_kernel<T, STREAM>), grid, block, 0, s, p);
+  }
 }
 
 hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* plan, int width, int dtype,
@@ -348,21 +374,28 @@ hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* p
   return hipGetLastError();
 }
 
+template <int T, int TO, int MODE>
+static void launch_combine_m(const RowParams& p, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * kRowWaves);
+  if (p.topk == 1)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 1, MODE>), grid, block, 0, s, p);
+  else if (p.topk == 2)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 2, MODE>), grid, block, 0, s, p);
+  else if (p.topk == 3)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 3, MODE>), grid, block, 0, s, p);
+  else if (p.topk == 4)
+    hipLaunchKernelGGL((combine_kernel<T, TO, 4, MODE>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_kernel<T, TO, 8, MODE>), grid, block, 0, s, p);
+}
 template <int T, int TO>
 static void launch_combine_t(const RowParams& p, dim3 grid, hipStream_t s) {
-  const dim3 block(64 * kRowWaves);
-  if (p.width < Elem<T>::kVec)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 1, true>), grid, block, 0, s, p);
-  else if (p.topk == 1)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 1, false>), grid, block, 0, s, p);
-  else if (p.topk == 2)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 2, false>), grid, block, 0, s, p);
-  else if (p.topk == 3)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 3, false>), grid, block, 0, s, p);
-  else if (p.topk == 4)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 4, false>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((combine_kernel<T, TO, 8, false>), grid, block, 0, s, p);
+  switch (row_mode<T>(p)) {
+    case NARROW: hipLaunchKernelGGL((combine_kernel<T, TO, 1, NARROW>), grid, dim3(64 * kRowWaves), 0, s, p); break;
+    case CACHED: launch_combine_m<T, TO, CACHED>(p, grid, s); break;
+    case STREAM: launch_combine_m<T, TO, STREAM>(p, grid, s); break;
+    default: launch_combine_m<T, TO, STREAM_LINES>(p, grid, s);
+  }
 }
 
 hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* plan, const float* weights,
@@ -385,21 +418,29 @@ hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* p
   return hipGetLastError();
 }
 
+template <int T, int MODE>
+static void launch_backward_m(const RowParams& p, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * kRowWaves);
+  if (p.topk == 1)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 1, MODE>), grid, block, 0, s, p);
+  else if (p.topk == 2)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 2, MODE>), grid, block, 0, s, p);
+  else if (p.topk == 3)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 3, MODE>), grid, block, 0, s, p);
+  else if (p.topk == 4)
+    hipLaunchKernelGGL((combine_backward_kernel<T, 4, MODE>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_backward_kernel<T, 8, MODE>), grid, block, 0, s, p);
+}
 template <int T>
 static void launch_backward(const RowParams& p, hipStream_t s) {
-  const dim3 grid(p.tokens + ceil_div(p.tail_waves, kRowWaves)), block(64 * kRowWaves);
-  if (p.width < Elem<T>::kVec)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 1, true>), grid, block, 0, s, p);
-  else if (p.topk == 1)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 1, false>), grid, block, 0, s, p);
-  else if (p.topk == 2)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 2, false>), grid, block, 0, s, p);
-  else if (p.topk == 3)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 3, false>), grid, block, 0, s, p);
-  else if (p.topk == 4)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 4, false>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((combine_backward_kernel<T, 8, false>), grid, block, 0, s, p);
+  const dim3 grid(p.tokens + ceil_div(p.tail_waves, kRowWaves));
+  switch (row_mode<T>(p)) {
+    case NARROW: hipLaunchKernelGGL((combine_backward_kernel<T, 1, NARROW>), grid, dim3(64 * kRowWaves), 0, s, p); break;
+    case CACHED: launch_backward_m<T, CACHED>(p, grid, s); break;
+    case STREAM: launch_backward_m<T, STREAM>(p, grid, s); break;
+    default: launch_backward_m<T, STREAM_LINES>(p, grid, s);
+  }
 }
 
 hipError_t launch_combine_backward(const void* dy, const void* ys, const RouteLayout& r, const int32_t* plan,
