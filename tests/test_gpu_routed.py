@@ -428,6 +428,13 @@ def test_lora_runs_of_rows():
     _check_lora(800, 1024, 400, 3, 32, "f16", "f16", ids, 42, planned=True)
 
 
+@pytest.mark.parametrize("act,ykind,N,rank", [("bf16", "bf16", 16288, 16), ("f16", "f32", 8208, 40), ("f16", "f16", 16288, 8)])
+def test_lora_of_rows_past_the_caches(act, ykind, N, rank):
+    """So many rows that y and out are streamed, in place as well."""
+    ids = np.repeat(np.array([1, -1, 0, 2], dtype=np.int32), [1001, 30, 333, 700])
+    _check_lora(2064, 128, N, 3, rank, act, ykind, ids, 43, alias=ykind == "f16")
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -12, 2.0 ** 9])
 def test_lora_scales_of_t(scale):
     """t far from 1: its fp16 parts are taken on a power-of-two scale."""

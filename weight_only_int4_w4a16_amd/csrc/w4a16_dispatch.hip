@@ -341,8 +341,6 @@ bool rows_fit(int tokens, int width) {
   return waves < (1LL << 26) && ((long long)tokens + kTailWaves) * 64 * kRowWaves < (1LL << 32);
 }
 
-constexpr size_t kStreamBytes = (size_t)64 << 20;
-
 template <int T>
 static int row_mode(const RowParams& p) {
   constexpr size_t bytes = sizeof(typename Elem<T>::raw);

@@ -30,8 +30,7 @@
 //
 // Measured: one row, 4096x4096 rank 16 fp16 9.8 us (one launch; two took 14.0); 96 rows with 64
 // adapters, 4096x14336 rank 32 bf16 18 us (62 MB; first product 7.7, second 11.7 at 5.5 TB/s); 4096 rows
-// with 9 adapters, 8192x8192 rank 64 bf16 68 us (208 MB; sort 8.6, first product 18.2, second 35 at 4.7
-// TB/s, near a copy's rate).
+// with 9 adapters, 8192x8192 rank 64 bf16 60 us (208 MB; sort 7.2, first product 18.2, then the second).
 #include <type_traits>
 
 #include "w4a16_device.hpp"
@@ -366,17 +365,20 @@ template <int YT>
 struct Cols {
   static constexpr int kPer = YT == T_F32 ? 4 : 8, kLanes = 64 / kPer, kRows = 64 / kLanes, kAccesses = 16 / kRows;
 };
-template <int YT>
+// STREAM: past the caches
+template <int YT, bool STREAM>
 __device__ __forceinline__ u4_t load_cols(const void* base, size_t at) {
-  if constexpr (YT == T_F32) return *reinterpret_cast<const u4_t*>(static_cast<const float*>(base) + at);
-  return *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(base) + at);
+  const u4_t* const v = reinterpret_cast<const u4_t*>(static_cast<const char*>(base) + at * (YT == T_F32 ? 4 : 2));
+  if constexpr (STREAM) return __builtin_nontemporal_load(v);
+  return *v;
 }
-template <int YT>
+template <int YT, bool STREAM>
 __device__ __forceinline__ void store_cols(void* base, size_t at, u4_t v) {
-  if constexpr (YT == T_F32)
-    *reinterpret_cast<u4_t*>(static_cast<float*>(base) + at) = v;
+  u4_t* const to = reinterpret_cast<u4_t*>(static_cast<char*>(base) + at * (YT == T_F32 ? 4 : 2));
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, to);
   else
-    *reinterpret_cast<u4_t*>(static_cast<uint16_t*>(base) + at) = v;
+    *to = v;
 }
 // v + back * d for an access's columns, rounded once to the type
 template <int YT>
@@ -432,7 +434,8 @@ constexpr size_t turn_bytes() { return 16 * kTurnStride * 4; }
 // RS: 32-rank steps. TALL: tiles of up to 64 rows, one strip a wave, whose y is all in flight before
 // t is split; else tiles of 16 rows, several strips, the next one's B and y in flight.
 // RT > 0: t is formed here too, 16 RT ranks by every workgroup of a tile for itself (no slices, one launch).
-template <int ACT, int YT, int RS, bool TALL, int RT = 0>
+// STREAM (of TALL): y and out past the caches.
+template <int ACT, int YT, int RS, bool TALL, int RT = 0, bool STREAM = false>
 __global__ __launch_bounds__(64 * expand_waves(RT > 0)) void expand_kernel(LoraParams p) {
   typedef typename ActT<ACT>::type AT;
   constexpr bool ONE = RT > 0;
@@ -459,7 +462,7 @@ __global__ __launch_bounds__(64 * expand_waves(RT > 0)) void expand_kernel(LoraP
     for (int n0 = n_first; n0 < n_end; n0 += step)
       for (int m = yrow; m < rows; m += Y::kRows) {
         const size_t at = (size_t)rows_of[m] * p.N + n0 + ycol;
-        if (n0 + ycol < p.N) store_cols<YT>(p.out, at, load_cols<YT>(p.y, at));
+        if (n0 + ycol < p.N) store_cols<YT, STREAM>(p.out, at, load_cols<YT, STREAM>(p.y, at));
       }
     return;
   }
@@ -481,7 +484,7 @@ __global__ __launch_bounds__(64 * expand_waves(RT > 0)) void expand_kernel(LoraP
 #pragma unroll
     for (int h = 0; h < NH; ++h)
       if (n0 + ycol < p.N)
-        v[h] = load_cols<YT>(p.y, (size_t)rows_of[min(m0 + Y::kRows * h + yrow, rows - 1)] * p.N + n0 + ycol);
+        v[h] = load_cols<YT, STREAM>(p.y, (size_t)rows_of[min(m0 + Y::kRows * h + yrow, rows - 1)] * p.N + n0 + ycol);
   };
   constexpr int TILES = TALL ? kTileMax / 16 : 1;
   u4_t bv[4][RS], yv[TILES][NH];
@@ -574,7 +577,7 @@ __global__ __launch_bounds__(64 * expand_waves(RT > 0)) void expand_kernel(LoraP
       for (int i = 0; i < Y::kPer; i += 4)
         *reinterpret_cast<f4_t*>(d + i) = *reinterpret_cast<const f4_t*>(turn + r * kTurnStride + ycol + i);
       if (m < rows && n0 + ycol < p.N)
-        store_cols<YT>(p.out, (size_t)rows_of[m] * p.N + n0 + ycol, add_cols<YT>(y[h], d, backs[m]));
+        store_cols<YT, STREAM>(p.out, (size_t)rows_of[m] * p.N + n0 + ycol, add_cols<YT>(y[h], d, backs[m]));
     }
     __builtin_amdgcn_wave_barrier();
   };
@@ -676,7 +679,9 @@ template <int ACT, int YT, int RS>
 void launch_expand_rs(const LoraParams& p, dim3 grid, hipStream_t s) {
   const dim3 block(64 * expand_waves(false));
   const size_t lds = expand_lds<ACT, YT>(p.tile_rows, RS, false);
-  if (p.tile_rows > 16)
+  if (p.tile_rows > 16 && (size_t)p.M * p.N * (YT == T_F32 ? 4 : 2) >= kStreamBytes)
+    hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, true, 0, true>), grid, block, lds, s, p);
+  else if (p.tile_rows > 16)
     hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, true>), grid, block, lds, s, p);
   else
     hipLaunchKernelGGL((expand_kernel<ACT, YT, RS, false>), grid, block, lds, s, p);

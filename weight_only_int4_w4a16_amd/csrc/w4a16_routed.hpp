@@ -17,6 +17,12 @@ constexpr int kMaxGroups = 1024;
 constexpr int kMaxSlots = 1 << 26;
 constexpr int kRouteBlockSlots = 2048;  // slots per workgroup of the sort where there are several
 constexpr int kRouteWholeSlots = 4096;  // most slots that one workgroup sorts alone
+// Rows of so many bytes in one call, a quarter of the last-level cache, are stored (and read for the last
+// time) past the caches: from cold, bf16, dispatch and combine of 8192 x 4096 at topk 2 (128 MiB of sorted
+// rows) 88 -> 71 us, adapters of 4096 x 8192 (64 MiB) 68 -> 60. A call that reads the rows right
+// after loses what it would have found there: dispatch and combine of the same rows at 64/128/256/512 MiB
+// 32/61/153/255 us cached, 34/64/124/209 streamed; a grouped product of them takes the same time.
+constexpr size_t kStreamBytes = (size_t)64 << 20;
 inline int round64(int n) { return (n + 63) & ~63; }
 // most tiles list j can hold: full tiles, and one more for each group with rows
 inline int tile_bound(int S, int E, int j) { return S / kTileRows[j] + (E + 1 < S ? E + 1 : S); }
