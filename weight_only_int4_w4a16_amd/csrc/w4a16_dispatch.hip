@@ -132,7 +132,7 @@ __device__ __forceinline__ void store_vec(typename Elem<T>::raw* row, int c, int
 }
 
 constexpr int kRowWaves = 4;     // waves per workgroup, each with an item of its own
-constexpr int kRowVecs = 2;      // vectors per lane and row: 2 KiB of a row per item
+constexpr int kRowVecs = 2;      // vectors per lane and row, 2 KiB of a row per item; one for shorter rows than 1 KiB
 constexpr int kTailWaves = 512;  // waves that clear the rows past the last group
 
 struct RowParams {
@@ -143,6 +143,7 @@ struct RowParams {
   const int32_t* plan;
   int S, E, topk, order, slot;
   int tokens, width;
+  int vecs;        // vectors per lane and row: kRowVecs or 1
   int segs;        // items per token
   int tail_waves;  // waves after the items
 };
@@ -156,7 +157,7 @@ __device__ __forceinline__ void clear_tail(const RowParams& p, void* rows, int w
       store_vec<T, MODE>(static_cast<typename Elem<T>::raw*>(rows) + (size_t)row * p.width, c, p.width, u4_t{0, 0, 0, 0});
 }
 
-template <int T, int MODE>
+template <int T, int MODE, int U>
 __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
   const int lane = threadIdx.x & 63;
@@ -166,18 +167,18 @@ __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(RowParams p) {
     if (item < items + p.tail_waves) clear_tail<T, MODE>(p, p.out, item - items, p.tail_waves, lane);
     return;
   }
-  const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * kRowVecs + lane;
+  const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * U + lane;
   const raw* src = static_cast<const raw*>(p.x) + (size_t)t * p.width;
-  u4_t v[kRowVecs];
+  u4_t v[U];
 #pragma unroll
-  for (int u = 0; u < kRowVecs; ++u) v[u] = load_vec<T, MODE, false>(src, c0 + 64 * u, p.width);
+  for (int u = 0; u < U; ++u) v[u] = load_vec<T, MODE, false>(src, c0 + 64 * u, p.width);
   const int32_t* slot = p.plan + p.slot + (size_t)t * p.topk;
   for (int j = 0; j < p.topk; ++j) {
     const int row = slot[j];
     if (row < 0) continue;
     raw* dst = static_cast<raw*>(p.out) + (size_t)row * p.width;
 #pragma unroll
-    for (int u = 0; u < kRowVecs; ++u) store_vec<T, MODE>(dst, c0 + 64 * u, p.width, v[u]);
+    for (int u = 0; u < U; ++u) store_vec<T, MODE>(dst, c0 + 64 * u, p.width, v[u]);
   }
 }
 
@@ -201,22 +202,22 @@ __device__ __forceinline__ void load_choices(const RowParams& p, int t, int j0, 
   }
 }
 
-// J: sorted rows in flight, min(topk, 4) or 8. A choice of no row reads row 0 and adds nothing.
-template <int T, int TO, int J, int MODE>
+// J: sorted rows in flight. A choice of no row reads row 0 and adds nothing.
+template <int T, int TO, int J, int MODE, int U>
 __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
   constexpr int V = Elem<T>::kVec;
   const int lane = threadIdx.x & 63;
   const int item = __builtin_amdgcn_readfirstlane(blockIdx.x * kRowWaves + (threadIdx.x >> 6));
   if (item >= p.tokens * p.segs) return;
-  const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * kRowVecs + lane;
-  float acc[kRowVecs][V];
+  const int t = item / p.segs, c0 = (item - t * p.segs) * 64 * U + lane;
+  float acc[U][V];
 #pragma unroll
-  for (int u = 0; u < kRowVecs; ++u)
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
   for (int j0 = 0; j0 < p.topk; j0 += J) {
-    u4_t v[J][kRowVecs];
+    u4_t v[J][U];
     int row[J];
     float w[J];
     load_choices(p, t, j0, row, w);
@@ -224,13 +225,13 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
     for (int j = 0; j < J; ++j) {
       const raw* src = static_cast<const raw*>(p.ys) + (size_t)max(row[j], 0) * p.width;
 #pragma unroll
-      for (int u = 0; u < kRowVecs; ++u) v[j][u] = load_vec<T, MODE, true>(src, c0 + 64 * u, p.width);
+      for (int u = 0; u < U; ++u) v[j][u] = load_vec<T, MODE, true>(src, c0 + 64 * u, p.width);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       if (row[j] < 0) continue;
 #pragma unroll
-      for (int u = 0; u < kRowVecs; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[u][i] = __builtin_fmaf(w[j], vec_value<T>(v[j][u], i), acc[u][i]);
     }
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
   typedef typename Elem<TO>::raw out_raw;
   out_raw* dst = static_cast<out_raw*>(p.out) + (size_t)t * p.width;
 #pragma unroll
-  for (int u = 0; u < kRowVecs; ++u) {
+  for (int u = 0; u < U; ++u) {
     if constexpr (Elem<TO>::kVec == V) {
       store_vec<TO, MODE>(dst, c0 + 64 * u, p.width, vec_pack<TO>(acc[u]));
     } else {  // fp32 rows to 16-bit tokens: a lane's four elements are half a vector
@@ -328,7 +329,8 @@ RowParams row_params(const RouteLayout& r, const int32_t* plan, int width, int v
   p.slot = r.slot;
   p.tokens = r.S / r.topk;
   p.width = width;
-  p.segs = ceil_div(width, 64 * kRowVecs * vec);
+  p.vecs = width <= 64 * vec ? 1 : kRowVecs;
+  p.segs = ceil_div(width, 64 * p.vecs * vec);
   p.tail_waves = r.S < kTailWaves ? r.S : kTailWaves;
   return p;
 }
@@ -349,13 +351,19 @@ static int row_mode(const RowParams& p) {
   return p.width * bytes % 128 ? STREAM : STREAM_LINES;
 }
 
+template <int T, int MODE>
+static void launch_dispatch_m(const RowParams& p, dim3 grid, hipStream_t s) {
+  if (p.vecs == 1)
+    hipLaunchKernelGGL((dispatch_kernel<T, MODE, 1>), grid, dim3(64 * kRowWaves), 0, s, p);
+  else
+    hipLaunchKernelGGL((dispatch_kernel<T, MODE, kRowVecs>), grid, dim3(64 * kRowWaves), 0, s, p);
+}
 template <int T>
 static void launch_dispatch_t(const RowParams& p, dim3 grid, hipStream_t s) {
-  const dim3 block(64 * kRowWaves);
   switch (row_mode<T>(p)) {
-    case NARROW: hipLaunchKernelGGL((dispatch_kernel<T, NARROW>), grid, block, 0, s, p); break;
-    case CACHED: hipLaunchKernelGGL((dispatch_kernel<T, CACHED>), grid, block, 0, s, p); break;
-    default: hipLaunchKernelGGL((dispatch_kernel<T, STREAM>), grid, block, 0, s, p);
+    case NARROW: hipLaunchKernelGGL((dispatch_kernel<T, NARROW, 1>), grid, dim3(64 * kRowWaves), 0, s, p); break;
+    case CACHED: launch_dispatch_m<T, CACHED>(p, grid, s); break;
+    default: launch_dispatch_m<T, STREAM>(p, grid, s);
   }
 }
 
@@ -372,24 +380,29 @@ hipError_t launch_dispatch(const void* x, const RouteLayout& r, const int32_t* p
   return hipGetLastError();
 }
 
+template <int T, int TO, int J, int MODE>
+static void launch_combine_j(const RowParams& p, dim3 grid, hipStream_t s) {
+  if (p.vecs == 1)
+    hipLaunchKernelGGL((combine_kernel<T, TO, J, MODE, 1>), grid, dim3(64 * kRowWaves), 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_kernel<T, TO, J, MODE, kRowVecs>), grid, dim3(64 * kRowWaves), 0, s, p);
+}
+// Choices past the last read a row again, so five and six are taken by threes
+static int rows_in_flight(int topk) { return topk <= 4 ? topk : topk <= 6 ? 3 : 8; }
 template <int T, int TO, int MODE>
 static void launch_combine_m(const RowParams& p, dim3 grid, hipStream_t s) {
-  const dim3 block(64 * kRowWaves);
-  if (p.topk == 1)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 1, MODE>), grid, block, 0, s, p);
-  else if (p.topk == 2)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 2, MODE>), grid, block, 0, s, p);
-  else if (p.topk == 3)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 3, MODE>), grid, block, 0, s, p);
-  else if (p.topk == 4)
-    hipLaunchKernelGGL((combine_kernel<T, TO, 4, MODE>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((combine_kernel<T, TO, 8, MODE>), grid, block, 0, s, p);
+  switch (rows_in_flight(p.topk)) {
+    case 1: launch_combine_j<T, TO, 1, MODE>(p, grid, s); break;
+    case 2: launch_combine_j<T, TO, 2, MODE>(p, grid, s); break;
+    case 3: launch_combine_j<T, TO, 3, MODE>(p, grid, s); break;
+    case 4: launch_combine_j<T, TO, 4, MODE>(p, grid, s); break;
+    default: launch_combine_j<T, TO, 8, MODE>(p, grid, s);
+  }
 }
 template <int T, int TO>
 static void launch_combine_t(const RowParams& p, dim3 grid, hipStream_t s) {
   switch (row_mode<T>(p)) {
-    case NARROW: hipLaunchKernelGGL((combine_kernel<T, TO, 1, NARROW>), grid, dim3(64 * kRowWaves), 0, s, p); break;
+    case NARROW: hipLaunchKernelGGL((combine_kernel<T, TO, 1, NARROW, 1>), grid, dim3(64 * kRowWaves), 0, s, p); break;
     case CACHED: launch_combine_m<T, TO, CACHED>(p, grid, s); break;
     case STREAM: launch_combine_m<T, TO, STREAM>(p, grid, s); break;
     default: launch_combine_m<T, TO, STREAM_LINES>(p, grid, s);
@@ -419,16 +432,13 @@ hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* p
 template <int T, int MODE>
 static void launch_backward_m(const RowParams& p, dim3 grid, hipStream_t s) {
   const dim3 block(64 * kRowWaves);
-  if (p.topk == 1)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 1, MODE>), grid, block, 0, s, p);
-  else if (p.topk == 2)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 2, MODE>), grid, block, 0, s, p);
-  else if (p.topk == 3)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 3, MODE>), grid, block, 0, s, p);
-  else if (p.topk == 4)
-    hipLaunchKernelGGL((combine_backward_kernel<T, 4, MODE>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((combine_backward_kernel<T, 8, MODE>), grid, block, 0, s, p);
+  switch (rows_in_flight(p.topk)) {
+    case 1: hipLaunchKernelGGL((combine_backward_kernel<T, 1, MODE>), grid, block, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((combine_backward_kernel<T, 2, MODE>), grid, block, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((combine_backward_kernel<T, 3, MODE>), grid, block, 0, s, p); break;
+    case 4: hipLaunchKernelGGL((combine_backward_kernel<T, 4, MODE>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((combine_backward_kernel<T, 8, MODE>), grid, block, 0, s, p);
+  }
 }
 template <int T>
 static void launch_backward(const RowParams& p, hipStream_t s) {
