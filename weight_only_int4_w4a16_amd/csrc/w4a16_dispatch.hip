@@ -14,11 +14,10 @@
 // element: the vectors are declared with the element's alignment, which global accesses of
 // this GPU take as they are.
 //
-// Measured, against a copy of a large tensor at 5.2 TB/s: bf16 dispatch of 8192 tokens x 4096 to two
-// rows each 35 us (201 MB, 5.8 TB/s), combine of them 41 us (4.9 TB/s); 16384 tokens x 2048 with
-// eight rows each, dispatch 90 us (604 MB, 6.7 TB/s; some of its writes reach memory only while
-// the next kernel runs), combine 150 us (4.0 TB/s), combine's gradients 204 us (1141 MB, 5.6 TB/s). At rows
-// of 2885 elements, whose vectors cross cache lines, 3.6-4.5 TB/s.
+// Measured from cold, against a copy of a large tensor at 5.2 TB/s (bf16): 8192 tokens x 4096 to two rows
+// each and back 71 us with the sort (389 MB); 16384 x 2048, eight rows each, with all gradients 557 us
+// (2953 MB, 5.3 TB/s); 4099 x 2885, three rows each, whose vectors cross cache lines, dispatch and combine 20
+// us each, gradients 36 (3.6-4 TB/s; rows of 2880: 15.5, 18, 33).
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"
 
@@ -80,7 +79,7 @@ __device__ __forceinline__ u4_t vec_pack(const float* f) {
 // no multiple of V, is moved back to end with the row: its first elements are then its
 // neighbour's too, who reads and writes the same values. (Taken one by one, the last elements
 // made the sort, the two moves and their gradients of 4099 bf16 tokens of 2885 elements, topk 3,
-// take 133 us; so they took 112 us.) Vectors past the row read its last one and store nothing, so that
+// take 133 us; moved back, 112.) Vectors past the row read its last one and store nothing, so that
 // loads need no branch: the compiler puts a wait for all that is in flight before a load under
 // one.
 //
@@ -251,20 +250,24 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_kernel(RowParams p) {
   }
 }
 
-// One workgroup per token (its waves share the row): the products of dy with the token's sorted
-// rows are summed per lane, then over the lanes and waves in a fixed order.
-template <int T, int J, int MODE>
+// PER waves share a token: the products of dy with the token's sorted rows are summed per lane, then
+// over the lanes and waves in a fixed order. Four waves, or one for rows up to 2 KiB, which leave most of
+// four idle (30000 tokens x 160 bf16, topk 8: 138 -> 61 us).
+template <int T, int J, int MODE, int PER>
 __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowParams p) {
   typedef typename Elem<T>::raw raw;
-  constexpr int V = Elem<T>::kVec;
+  constexpr int V = Elem<T>::kVec, TOKENS = kRowWaves / PER;  // tokens of a workgroup
   __shared__ float part[kRowWaves][J];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t = blockIdx.x;
-  if (t >= p.tokens) {  // the workgroups after the tokens'
-    clear_tail<T, MODE>(p, p.out, (t - p.tokens) * kRowWaves + wave, p.tail_waves, lane);
+  const int blocks = (p.tokens + TOKENS - 1) / TOKENS;
+  if ((int)blockIdx.x >= blocks) {  // the workgroups after the tokens'
+    clear_tail<T, MODE>(p, p.out, (blockIdx.x - blocks) * kRowWaves + wave, p.tail_waves, lane);
     return;
   }
+  const int t = blockIdx.x * TOKENS + (PER == 1 ? wave : 0);
+  if (PER == 1 && t >= p.tokens) return;
+  const int first = PER == 1 ? lane : threadIdx.x;
   const int vecs = (p.width + V - 1) / V;
   const raw* dy = static_cast<const raw*>(p.x) + (size_t)t * p.width;
   for (int j0 = 0; j0 < p.topk; j0 += J) {
@@ -273,7 +276,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
     load_choices(p, t, j0, row, w);
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[j] = 0.f;
-    for (int c = threadIdx.x; c < vecs; c += 64 * kRowWaves) {
+    for (int c = first; c < vecs; c += 64 * PER) {
       const u4_t d = load_vec<T, MODE, false>(dy, c, p.width);
       u4_t v[J];
 #pragma unroll
@@ -305,16 +308,22 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_backward_kernel(RowPar
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int o = 32; o >= 1; o >>= 1) acc[j] += __shfl_xor(acc[j], o);
-    if (j0) __syncthreads();  // the sums of the choices before have been read
-    if (lane == 0)
+    if constexpr (PER > 1) {
+      if (j0) __syncthreads();  // the sums of the choices before have been read
+      if (lane == 0)
 #pragma unroll
-      for (int j = 0; j < J; ++j) part[wave][j] = acc[j];
-    __syncthreads();
-    if (threadIdx.x < J && j0 + threadIdx.x < p.topk) {
-      float s = 0.f;
+        for (int j = 0; j < J; ++j) part[wave][j] = acc[j];
+      __syncthreads();
+      if (threadIdx.x < J && j0 + threadIdx.x < p.topk) {
+        float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRowWaves; ++i) s += part[i][threadIdx.x];
-      p.dweights[(size_t)t * p.topk + j0 + threadIdx.x] = s;
+        for (int i = 0; i < PER; ++i) s += part[i][threadIdx.x];
+        p.dweights[(size_t)t * p.topk + j0 + threadIdx.x] = s;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (lane == j && j0 + j < p.topk) p.dweights[(size_t)t * p.topk + j0 + j] = acc[j];
     }
   }
 }
@@ -429,25 +438,33 @@ hipError_t launch_combine(const void* ys, const RouteLayout& r, const int32_t* p
   return hipGetLastError();
 }
 
-template <int T, int MODE>
-static void launch_backward_m(const RowParams& p, dim3 grid, hipStream_t s) {
+template <int T, int J, int MODE>
+static void launch_backward_j(const RowParams& p, hipStream_t s) {
   const dim3 block(64 * kRowWaves);
+  const int tail = ceil_div(p.tail_waves, kRowWaves);
+  if (p.width <= 128 * Elem<T>::kVec)
+    hipLaunchKernelGGL((combine_backward_kernel<T, J, MODE, 1>), dim3(ceil_div(p.tokens, kRowWaves) + tail), block, 0, s, p);
+  else if constexpr (MODE != NARROW)
+    hipLaunchKernelGGL((combine_backward_kernel<T, J, MODE, kRowWaves>), dim3(p.tokens + tail), block, 0, s, p);
+}
+template <int T, int MODE>
+static void launch_backward_m(const RowParams& p, hipStream_t s) {
   switch (rows_in_flight(p.topk)) {
-    case 1: hipLaunchKernelGGL((combine_backward_kernel<T, 1, MODE>), grid, block, 0, s, p); break;
-    case 2: hipLaunchKernelGGL((combine_backward_kernel<T, 2, MODE>), grid, block, 0, s, p); break;
-    case 3: hipLaunchKernelGGL((combine_backward_kernel<T, 3, MODE>), grid, block, 0, s, p); break;
-    case 4: hipLaunchKernelGGL((combine_backward_kernel<T, 4, MODE>), grid, block, 0, s, p); break;
-    default: hipLaunchKernelGGL((combine_backward_kernel<T, 8, MODE>), grid, block, 0, s, p);
+    case 1: launch_backward_j<T, 1, MODE>(p, s); break;
+    case 2: launch_backward_j<T, 2, MODE>(p, s); break;
+    case 3: launch_backward_j<T, 3, MODE>(p, s); break;
+    case 4: launch_backward_j<T, 4, MODE>(p, s); break;
+    default: launch_backward_j<T, 8, MODE>(p, s);
   }
 }
 template <int T>
 static void launch_backward(const RowParams& p, hipStream_t s) {
-  const dim3 grid(p.tokens + ceil_div(p.tail_waves, kRowWaves));
   switch (row_mode<T>(p)) {
-    case NARROW: hipLaunchKernelGGL((combine_backward_kernel<T, 1, NARROW>), grid, dim3(64 * kRowWaves), 0, s, p); break;
-    case CACHED: launch_backward_m<T, CACHED>(p, grid, s); break;
-    case STREAM: launch_backward_m<T, STREAM>(p, grid, s); break;
-    default: launch_backward_m<T, STREAM_LINES>(p, grid, s);
+    case NARROW: launch_backward_j<T, 1, NARROW>(p, s); break;
+    // three streams at once share too many lines: 4099 x 2885, topk 3, 36 us cached, 41 streamed
+    case CACHED:
+    case STREAM: launch_backward_m<T, CACHED>(p, s); break;
+    default: launch_backward_m<T, STREAM_LINES>(p, s);
   }
 }
 
