@@ -461,9 +461,10 @@ template <int T>
 static void launch_backward(const RowParams& p, hipStream_t s) {
   switch (row_mode<T>(p)) {
     case NARROW: launch_backward_j<T, 1, NARROW>(p, s); break;
-    // three streams at once share too many lines: 4099 x 2885, topk 3, 36 us cached, 41 streamed
-    case CACHED:
-    case STREAM: launch_backward_m<T, CACHED>(p, s); break;
+    // odd rows, 4099 x 2885 at topk 3: over and over by itself 36 us cached, 41 streamed, but between the other
+    // moves of a training step streamed (all of them 99 us, 104 cached)
+    case CACHED: launch_backward_m<T, CACHED>(p, s); break;
+    case STREAM: launch_backward_m<T, STREAM>(p, s); break;
     default: launch_backward_m<T, STREAM_LINES>(p, s);
   }
 }
