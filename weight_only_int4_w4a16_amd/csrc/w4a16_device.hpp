@@ -326,14 +326,4 @@ __device__ inline void store_out(void* out, size_t idx, float v, int out_dtype) 
   }
 }
 
-// rows [row0, row0 + rows) by columns [col0, min(col0 + cols, width)) of an output of `width`
-// columns cleared by the workgroup
-__device__ inline void zero_tile(void* out, int out_dtype, int row0, int rows, int width, int col0, int cols) {
-  const int n = min(cols, width - col0);
-  for (int i = threadIdx.x; i < rows * n; i += blockDim.x) {
-    const int r = i / n;
-    store_out(out, (size_t)(row0 + r) * width + col0 + (i - r * n), 0.f, out_dtype);
-  }
-}
-
 }  // namespace w4a16

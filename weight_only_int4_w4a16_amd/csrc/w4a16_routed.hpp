@@ -2,6 +2,7 @@
 // different weights), behind the C ABI.
 #pragma once
 
+#include "w4a16_device.hpp"
 #include "w4a16_launch.hpp"
 
 namespace w4a16 {
@@ -72,6 +73,16 @@ __device__ __forceinline__ bool group_tile(const GroupTiles& g, int ti, int& e, 
   p0 = t.y;
   end = t.z;
   return ti < count;
+}
+
+// rows [row0, row0 + rows) by columns [col0, min(col0 + cols, width)) of an output of `width`
+// columns cleared by the workgroup
+__device__ inline void zero_tile(void* out, int out_dtype, int row0, int rows, int width, int col0, int cols) {
+  const int n = min(cols, width - col0);
+  for (int i = threadIdx.x; i < rows * n; i += blockDim.x) {
+    const int r = i / n;
+    store_out(out, (size_t)(row0 + r) * width + col0 + (i - r * n), 0.f, out_dtype);
+  }
 }
 
 hipError_t launch_route(const int32_t* ids, const RouteLayout& r, int32_t* plan, hipStream_t s);
