@@ -117,8 +117,8 @@ hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t
   const long long wgs = (tiles > groups ? tiles : groups) * ceil_div(p.NT, kStrips);
   if (g.MT == 1 && p.KC >= 64 && wgs <= 3 * cus) g.waves = 8;
   // Sixty-four rows: the waves side by side where that still makes two workgroups a compute unit (8
-  // experts of 4096x14336 at 64/128 rows each 119/206 -> 104/169 us; 64 of 2048x2816 at 64/128: 105/177
-  // -> 91/142).
+  // experts of 4096x14336 at a mean of 64/128 rows 113/199 -> 102/166 us; 64 of 2048x2816 at 24/64/128:
+  // 59/100/174 -> 53/81/138).
   if (g.MT == 4 && tiles * ceil_div(p.NT, kStrips * kWaves) >= 2 * cus) g.waves = 0;
   p.slice = g.waves ? ceil_div(p.KC, g.waves) : p.KC;
   p.col_tiles = ceil_div(p.NT, kStrips * (g.waves ? 1 : kWaves));
