@@ -592,7 +592,7 @@ def route(ids, groups: int) -> Routing:
     need = L.w4a16_route_bytes(tokens, topk, groups)
     if need == 0:
         raise W4A16Error(f"unsupported routing: {tokens} x {topk} slots, {groups} groups", ERR_UNSUPPORTED)
-    plan = torch.empty(need // 4, dtype=torch.int32, device=device)
+    plan = ids.new_empty(need // 4)
     st = L.w4a16_route(ids.data_ptr(), tokens, topk, groups, plan.data_ptr(), need, _raw_stream(device))
     if st:
         _check(st, "w4a16_route")
