@@ -236,9 +236,9 @@ w4a16_status w4a16_dequant_nf4(const int32_t* packed, const uint16_t* absmax,
  * a request's adapter). A group outside [0, groups) is none: the slot's row is zeros where rows
  * are written, and adds nothing where rows come back. S = tokens * topk.
  * Limits: 1 <= topk, 1 <= groups <= W4A16_MAX_GROUPS, S <= W4A16_MAX_SLOTS, and what one launch
- * can hold (2^32 threads: about 2^24 tokens or 2^26 kilobytes of a token's rows)
- * (W4A16_ERR_UNSUPPORTED past them). tokens = 0 is a no-op for every call but w4a16_route,
- * whose plan then holds zero offsets.
+ * can hold (2^32 threads: about 2^24 tokens or 2^26 kilobytes of a token's rows; rows of at most
+ * 2^31 - 2048 elements): W4A16_ERR_UNSUPPORTED past them. tokens = 0 is a no-op for every call
+ * but w4a16_route, whose plan then holds zero offsets.
  * ------------------------------------------------------------------------------------------ */
 #define W4A16_MAX_GROUPS 1024
 #define W4A16_MAX_SLOTS (1 << 26)

@@ -18,6 +18,8 @@
 // each and back 71 us with the sort (389 MB); 16384 x 2048, eight rows each, with all gradients 557 us
 // (2953 MB, 5.3 TB/s); 4099 x 2885, three rows each, whose vectors cross cache lines, dispatch and combine 20
 // us each, gradients 36 (3.6-4 TB/s; rows of 2880: 15.5, 18, 33).
+#include <limits.h>
+
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"
 
@@ -347,6 +349,8 @@ RowParams row_params(const RouteLayout& r, const int32_t* plan, int width, int v
 }  // namespace
 
 bool rows_fit(int tokens, int width) {
+  // an item's last lanes index up to 1023 elements past the row before they are held back to it
+  if (width > INT_MAX - 1023) return false;
   // a wave per token and 512 elements at most (fp32), a workgroup per token in the backward pass
   const long long waves = (long long)tokens * ceil_div(width, 64 * kRowVecs * 4) + kTailWaves;
   return waves < (1LL << 26) && ((long long)tokens + kTailWaves) * 64 * kRowWaves < (1LL << 32);

@@ -31,6 +31,8 @@
 // Measured: one row, 4096x4096 rank 16 fp16 9.8 us (one launch; two took 14.0); 96 rows with 64
 // adapters, 4096x14336 rank 32 bf16 18 us (62 MB; first product 7.7, second 11.7 at 5.5 TB/s); 4096 rows
 // with 9 adapters, 8192x8192 rank 64 bf16 60 us (208 MB; sort 7.2, first product 18.2, then the second).
+#include <limits.h>
+
 #include <type_traits>
 
 #include "w4a16_device.hpp"
@@ -715,6 +717,8 @@ void launch_expand(const LoraParams& p, dim3 grid, hipStream_t s) {
 
 bool lora_fits(int M, int K, int N, int L, int R) {
   if (M > kMaxSlots) return false;
+  // the last block of K and the last workgroup's columns (up to eight strips of four waves) end past them
+  if (K > INT_MAX - 127 || N > INT_MAX - 2047) return false;
   for (int planned = 0; planned < 2; ++planned) {
     const bool self = self_tiles(M, planned != 0);
     const LoraGeometry g = lora_geometry(M, K, N, L, R, self);
