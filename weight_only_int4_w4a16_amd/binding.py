@@ -505,6 +505,15 @@ def _need(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _need_ints(*sizes):
+    """Sizes that the library's C ints hold: ctypes drops the bits above them without a word."""
+    if max(sizes) > _INT_MAX:
+        raise W4A16Error(f"unsupported size {max(sizes)}: sizes must be below 2^31", ERR_UNSUPPORTED)
+
+
 def _need_rows(t, name, rows):
     """A contiguous 2-D tensor of ``rows`` rows of fp16, bf16 or fp32; returns its width and w4a16 dtype."""
     if not _dtypes:
@@ -517,6 +526,7 @@ def _need_rows(t, name, rows):
         _expect(t, name, (rows, width), tuple(_dtypes))
     if width < 1:
         _fail(f"{name} has rows of no elements")
+    _need_ints(width)
     return width, dt
 
 
@@ -583,9 +593,10 @@ def route(ids, groups: int) -> Routing:
         _fail("ids must be an int32 tensor [tokens, topk] or [tokens]")
     if not ids.is_contiguous():
         _fail("ids must be contiguous")
+    tokens, topk = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
+    _need_ints(tokens, topk, groups)
     device = ids.device
     _need_device(device, "ids")
-    tokens, topk = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
     if topk < 1 or groups < 1:
         _fail(f"topk={topk}, groups={groups}: both must be at least 1")
     L = lib()
@@ -689,6 +700,7 @@ def pack_grouped(qweight):
     if qweight is None or qweight.dtype != torch.int32 or qweight.dim() != 3 or not qweight.is_contiguous():
         _fail("qweight must be a contiguous int32 tensor [groups, K/8, N]")
     K, N = qweight.shape[1] * 8, qweight.shape[2]
+    _need_ints(K, N)
     nb = packed_bytes(K, N)
     if nb == 0:
         raise W4A16Error(f"unsupported shape K={K} N={N}", ERR_UNSUPPORTED)
@@ -713,6 +725,7 @@ def _grouped(x, routing, packed, scales, tail, group_size, glu, gather, out_dtyp
     if scales is None or scales.dim() != 3:
         _fail("scales must be a 3-D [groups, K/g, N] tensor")
     E, N, G = r.groups, scales.shape[2], _groups(K, group_size)
+    _need_ints(K, N)
     sp = _need(scales, "scales", (E, G, N), torch.float16 if nf4 else x.dtype, device)
     if N % 8:
         _fail(f"N={N} is not a multiple of 8")
@@ -770,10 +783,14 @@ def gemm_grouped_nf4_swiglu(x, routing: Routing, packed, absmax, codebook, block
 
 
 def grouped_kernel_name(rows: int, K: int, N: int, groups: int, group_size: int) -> str:
+    if max(rows, K, N, groups, group_size) > _INT_MAX:
+        return "none"
     return lib().w4a16_grouped_kernel_name(rows, K, N, groups, group_size).decode()
 
 
 def lora_workspace_bytes(M: int, K: int, N: int, adapters: int, rank: int, planned: bool = False) -> int:
+    if max(M, K, N, adapters, rank) > _INT_MAX:
+        return 0
     return int(lib().w4a16_lora_workspace_bytes(M, K, N, adapters, rank, int(planned)))
 
 
@@ -799,6 +816,7 @@ def lora_add(y, x, lora_a, lora_b, ids, scaling, routing: Routing | None = None,
     if y is None or y.dim() != 2:
         _fail("y must be a 2-D [M, N] tensor")
     N = y.shape[1]
+    _need_ints(M, K, N, adapters, rank)
     if y.dtype is not dtype:
         _expect(y, "y", (M, N), (dtype, torch.float32), device)
     yp = _need(y, "y", (M, N), y.dtype, device)
