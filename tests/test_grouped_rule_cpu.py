@@ -1,0 +1,50 @@
+"""The grouped products' row tile against measured times: the rule's tile is to be the fastest of those timed, or near it.
+
+Times in us on one MI355X, routings as uneven as gates make them (top-k of normal scores, expert biases of
+0.7 sigma). Without a device the rule counts 256 compute units, as many as that card has.
+"""
+import pytest
+
+
+def _tile(E, K, N, group_size, mean):
+    import weight_only_int4_w4a16_amd as w4
+    name = w4.grouped_kernel_name(E * mean, K, N, E, group_size)
+    return int(name.rsplit("_", 1)[1].split("x")[0])
+
+
+# (groups, K, N, group size): mean rows a group -> us of the 64-row and of the 128-row tile. A repeated measurement
+# differs by up to 3%, and the model behind the rule is 5% off at most of its points: together 8%.
+MANY_ROWS = [
+    ((64, 2048, 2816, 128), {400: (364, 413), 448: (393, 424), 512: (440, 477), 640: (539, 596), 768: (645, 666), 1024: (877, 869), 1536: (1417, 1256)}),
+    ((64, 1024, 2048, 128), {400: (142, 189), 512: (174, 226), 640: (210, 264), 1024: (333, 384), 1536: (495, 543)}),
+    ((64, 512, 2048, 128), {400: (78, 124), 640: (118, 175), 1024: (187, 253)}),
+    ((128, 2048, 768, 128), {400: (218, 301), 640: (340, 417), 1024: (530, 596)}),
+    ((64, 2048, 2816, 32), {400: (457, 434), 512: (551, 494), 640: (679, 611), 768: (789, 685)}),
+    ((8, 4096, 4096, 128), {400: (145, 120), 512: (174, 205), 640: (205, 209), 1024: (309, 322)}),
+    ((8, 4096, 4096, 32), {400: (172, 121), 768: (289, 221), 1024: (371, 334)}),
+    ((8, 4096, 14336, 128), {400: (453, 435), 512: (547, 533), 640: (676, 589), 768: (802, 700), 1024: (1053, 913)}),
+    ((2, 4096, 14336, 128), {400: (134, 117), 512: (138, 114), 640: (169, 201), 1024: (253, 221)}),
+    ((1, 4096, 4096, 128), {400: (28, 87), 640: (46, 88), 1024: (53, 89)}),
+    ((8, 14336, 4096, 128), {160: (387, 299), 192: (482, 295), 320: (378, 343), 400: (480, 384), 512: (598, 656), 640: (715, 674), 1024: (1086, 1041)}),
+    ((2, 14336, 4096, 128), {160: (80, 277), 256: (86, 278), 400: (180, 278)}),
+    ((16, 11008, 4096, 128), {320: (571, 542), 400: (684, 581), 640: (1050, 892), 1024: (1651, 1416)}),
+    ((8, 28672, 8192, 128), {256: (1248, 1302), 400: (1814, 1511), 640: (2804, 2249), 1024: (4395, 3752)}),
+]
+
+
+@pytest.mark.parametrize("shape,times", MANY_ROWS, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else "")
+def test_rule_of_many_rows(shape, times):
+    for mean, (small, large) in times.items():
+        tile = _tile(*shape, mean)
+        assert tile in (64, 128)
+        took = {64: small, 128: large}[tile]
+        assert took <= 1.08 * min(small, large), f"mean {mean}: {tile}-row tiles, {took} us for {min(small, large)}"
+
+
+def test_rule_refuses_no_launch_that_fits():
+    """2^20 rows of a shallow, wide weight: 64-row tiles would be quicker, but 2^32 threads are too many."""
+    import weight_only_int4_w4a16_amd as w4
+    assert _tile(8, 1024, 28672, 128, 1 << 14) == 64
+    assert _tile(8, 1024, 57344, 128, 1 << 17) == 128
+    P = 1 << 20  # aligned placeholder addresses; a launch without its scales is refused after the sizes
+    assert w4.lib().w4a16_gemm_grouped(P, P, 1 << 20, 1, 8, 0, 1024, 57344, 0, P, None, None, 128, 0, P, 0, None) == 1

@@ -569,7 +569,7 @@ static w4a16_status grouped_common(GemmArgs& a, const int32_t* plan, int tokens,
   if (gather && (long long)tokens * a.K * 2 >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;
   if (tokens == 0) return W4A16_OK;
   const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
-  if (!w4a16::grouped_fits(r, a.K, a.N)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::grouped_fits(r, a.K, a.N, a.group_size)) return W4A16_ERR_UNSUPPORTED;
   if (!plan || !a.x || !a.packed || !a.scales || !a.out || (a.nf4 && !a.codebook)) return W4A16_ERR_ARG;
   if (!aligned(plan, 256) || !aligned(a.x, 16) || !aligned(a.packed, 16) || !aligned(a.out, 16)) return W4A16_ERR_ARG;
   if (!aligned(a.scales, 2) || (a.qzeros && !aligned(a.qzeros, 4))) return W4A16_ERR_ARG;

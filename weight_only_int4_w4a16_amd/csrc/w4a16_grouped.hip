@@ -30,6 +30,16 @@ int forced_tile() {
   return forced;
 }
 
+// row tiles to expect: full ones, and about one part-filled for every second group
+long long expected_tiles(int S, int groups, int rows) { return S / rows + (groups + 1) / 2; }
+
+// Sixty-four rows: the waves side by side where that still makes two workgroups a compute unit (8
+// experts of 4096x14336 at a mean of 64/128 rows 113/199 -> 102/166 us; 64 of 2048x2816 at 24/64/128:
+// 59/100/174 -> 53/81/138).
+bool side_by_side(int S, int groups, int N, long long cus) {
+  return expected_tiles(S, groups, 64) * ceil_div(N / 16, kStrips * kWaves) >= 2 * cus;
+}
+
 // The rows of each group are known on the device only, so the tile goes by their mean over the
 // groups that can have rows. A taller tile forms W_hat once for more rows, but takes more registers
 // and LDS, so that fewer waves run; the limits lie where tiles win on routings as uneven as gates make
@@ -41,10 +51,32 @@ int forced_tile() {
 //                     384 -/-/349/407, 768 -/-/664/669
 //   8 of 14336x4096   4 41/53/44, 8 45/59/51, 16 64/72/56, 32 104/83/75, 128 388/320/244/281, 192 -/-/389/291,
 //                     256 -/-/324/314
-// Past 384 rows the 128 x 512 tile can still leave most of the chip idle (few groups, narrow N): then
-// 64-row tiles, by a model of compute-unit time (0.42 us per 64x64 tile and k-block; 2.6 us per
-// 128x512 tile and k-block in one round of workgroups, 3.2 us in more).
-Tile choose_tile(int S, int E, int K, int N) {
+// Past 384 rows (144 where K > 8192) the 128 x 512 tile can still leave much of the chip idle (few groups, narrow N,
+// a last round of workgroups with little in it): there the tile goes by a model of the time, in us. 64 x 64 tiles:
+// 0.32 a tile and k-block with the waves side by side, 0.5 with K split over them (groups of 32: 0.42 and 0.65), divided
+// by the compute units; 128 x 512: 26 a round of workgroups and 2.8 a round and k-block, 2.6 where one round holds them
+// all. Fitted to both tiles' times at 320 points (28 shapes from 2 of 256x4096 to 8 of 28672x8192, means of 160 to 1536;
+// fp16 g128 and g32, bf16 g128 and NF4): its choice is 0.7% above the better tile's time on average, more than 5% at 13
+// points, among them one round and a few workgroups (16 of 11008x4096 at 192 rows: 510 for 390). 64/128 rows a tile:
+//   64 of 1024x2048   400 142/189, 640 210/264, 1024 333/384;  64 of 2048x2816  400 364/413, 640 539/596, 1024 877/869
+//   8 of 4096x14336   400 453/435, 640 676/589, 1024 1053/913; 8 of 14336x4096  256 343/305, 400 480/384, 512 598/656
+double large_tile_us(int S, int groups, int KC, int N, long long cus) {
+  const long long wgs = (S / 128 + groups / 2) * (long long)ceil_div(N, 512);
+  const long long rounds = (wgs + cus - 1) / cus;
+  return rounds > 1 ? rounds * (26 + 2.8 * KC) : 26 + 2.6 * KC;
+}
+double small_tile_us(int S, int groups, int KC, int N, int group_size, long long cus) {
+  const bool split = !side_by_side(S, groups, N, cus);
+  const double each = group_size == 32 ? (split ? 0.65 : 0.42) : (split ? 0.5 : 0.32);
+  return (S / 64.0 + groups / 2) * ceil_div(N, 64) * KC * each / cus;
+}
+
+// a launch holds fewer than 2^32 threads
+bool tile_fits(Tile t, int S, int E, int N) {
+  return (long long)tile_bound(S, E, t) * ceil_div(N, t == TILE_128 ? 512 : 64) * 512 < (1LL << 32);
+}
+
+Tile choose_tile(int S, int E, int K, int N, int group_size) {
   if (forced_tile() >= 0) return (Tile)forced_tile();
   const int groups = E < S ? E : S;
   const int mean = S / (groups > 0 ? groups : 1);
@@ -52,19 +84,15 @@ Tile choose_tile(int S, int E, int K, int N) {
   if (mean <= 28) return TILE_32;
   if (mean <= (K > 8192 ? 144 : 384)) return TILE_64;
   const long long cus = device_cu_count();
-  const long long rounds = ((S / 128 + groups / 2) * (long long)ceil_div(N, 512) + cus - 1) / cus;
-  const double large = rounds * (rounds > 1 ? 3.2 : 2.6);
-  const double small = (S / 64.0 + groups / 2) * ceil_div(N, 64) * 0.42 / cus;
-  return small < large ? TILE_64 : TILE_128;
+  const int KC = ceil_div(K, 128);
+  const bool small = small_tile_us(S, groups, KC, N, group_size, cus) < large_tile_us(S, groups, KC, N, cus);
+  return small && tile_fits(TILE_64, S, E, N) ? TILE_64 : TILE_128;
 }
-
-int tile_cols(Tile t) { return t == TILE_128 ? 512 : 64; }
 
 }  // namespace
 
 const char* grouped_name(int S, int K, int N, int E, int group_size) {
-  (void)group_size;
-  switch (choose_tile(S, E, K, N)) {
+  switch (choose_tile(S, E, K, N, group_size)) {
     case TILE_16: return "w4a16_grouped_16x64";
     case TILE_32: return "w4a16_grouped_32x64";
     case TILE_64: return "w4a16_grouped_64x64";
@@ -72,15 +100,13 @@ const char* grouped_name(int S, int K, int N, int E, int group_size) {
   }
 }
 
-// a launch holds fewer than 2^32 threads, and a tile's rows fewer than 2^31 bytes
-bool grouped_fits(const RouteLayout& r, int K, int N) {
-  if (K >= (1 << 23)) return false;
-  const Tile t = choose_tile(r.S, r.E, K, N);
-  return (long long)tile_bound(r.S, r.E, t) * ceil_div(N, tile_cols(t)) * 512 < (1LL << 32);
+// a tile's rows hold fewer than 2^31 bytes
+bool grouped_fits(const RouteLayout& r, int K, int N, int group_size) {
+  return K < (1 << 23) && tile_fits(choose_tile(r.S, r.E, K, N, group_size), r.S, r.E, N);
 }
 
 hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t* plan, bool gather) {
-  const Tile tile = choose_tile(r.S, r.E, a.K, a.N);
+  const Tile tile = choose_tile(r.S, r.E, a.K, a.N, a.group_size);
   GroupTiles t;
   t.plan = plan;
   t.S = r.S;
@@ -110,16 +136,13 @@ hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t
   g.waves = kWaves;
   const long long cus = device_cu_count();
   const int groups = r.E < r.S ? r.E : r.S;
-  const long long tiles = r.S / kTileRows[tile] + (groups + 1) / 2;  // to expect
+  const long long tiles = expected_tiles(r.S, groups, kTileRows[tile]);
   // Sixteen rows: eight waves share a deep K where the workgroups leave room on the compute units
   // (8 experts of 14336x4096 at 4 rows each, 512 workgroups: 55 -> 43 us; at K 4096 and 2048 four
   // waves are as good or better by up to 10%).
   const long long wgs = (tiles > groups ? tiles : groups) * ceil_div(p.NT, kStrips);
   if (g.MT == 1 && p.KC >= 64 && wgs <= 3 * cus) g.waves = 8;
-  // Sixty-four rows: the waves side by side where that still makes two workgroups a compute unit (8
-  // experts of 4096x14336 at a mean of 64/128 rows 113/199 -> 102/166 us; 64 of 2048x2816 at 24/64/128:
-  // 59/100/174 -> 53/81/138).
-  if (g.MT == 4 && tiles * ceil_div(p.NT, kStrips * kWaves) >= 2 * cus) g.waves = 0;
+  if (g.MT == 4 && side_by_side(r.S, groups, a.N, cus)) g.waves = 0;
   p.slice = g.waves ? ceil_div(p.KC, g.waves) : p.KC;
   p.col_tiles = ceil_div(p.NT, kStrips * (g.waves ? 1 : kWaves));
   return a.act == ACT_F16 ? launch_few<ACT_F16>(p, g, a.group_size, a.nf4, a.glu, a.stream)

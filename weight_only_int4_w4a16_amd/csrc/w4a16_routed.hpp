@@ -101,7 +101,7 @@ hipError_t launch_combine_backward(const void* dy, const void* ys, const RouteLa
 // a.qzeros hold the groups' weights one after another
 hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t* plan, bool gather);
 // whether the rows and columns make a launch the kernels can index
-bool grouped_fits(const RouteLayout& r, int K, int N);
+bool grouped_fits(const RouteLayout& r, int K, int N, int group_size);
 const char* grouped_name(int S, int K, int N, int E, int group_size);
 constexpr int kMaxRank = 256;
 // its launches on the batched kernel (128-row tiles)
