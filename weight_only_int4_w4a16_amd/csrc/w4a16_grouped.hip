@@ -49,8 +49,14 @@ bool side_by_side(int S, int groups, int N, long long cus) {
 //                     128 320/237/167/217, 256 -/-/295/323, 384 -/-/432/430, 512 -/-/559/552, 768 -/-/821/711
 //   64 of 2048x2816   4 31/33/37, 8 41/39/43, 16 53/46/45, 24 68/57/54, 32 83/69/61, 128 261/193/136/222,
 //                     384 -/-/349/407, 768 -/-/664/669
-//   8 of 14336x4096   4 41/53/44, 8 45/59/51, 16 64/72/56, 32 104/83/75, 128 388/320/244/281, 192 -/-/389/291,
-//                     256 -/-/324/314
+// Deeper K (sorted rows, cold weights, the mean of four routings): the 32-row tile gains little between the others, but
+// for groups of 32, whose four scales and zeros a block cost the 64-row tile a wave a SIMD:
+//   8 of 14336x4096   g128 4 43/53/43, 8 50/59/48, 12 64/52/55, 16 72/70/61, 20 84/77/62, 28 109/85/92, 36 136/108/100,
+//                     96 331/264/195/283, 128 406/369/292/283, 144 463/414/342/282, 192 577/536/471/287
+//                     g32 4 59/56/79, 8 66/59/88, 16 94/87/99, 28 132/113/134, 40 164/129/154, 48 198/159/162
+//                     NF4 bf16 4 54/73/56, 8 65/76/60, 12 84/64/64, 20 103/86/73, 28 130/94/106, 40 164/128/124
+//   8 of 28672x8192   g128 3 154/146/152, 7 199/188/182, 12 234/207/205, 16 271/242/229, 24 393/310/292
+//                     g32 5 201/204/289, 9 253/235/347, 16 321/292/372, 24 432/364/423
 // Past 384 rows (144 where K > 8192) the 128 x 512 tile can still leave much of the chip idle (few groups, narrow N,
 // a last round of workgroups with little in it): there the tile goes by a model of the time, in us. 64 x 64 tiles:
 // 0.32 a tile and k-block with the waves side by side, 0.5 with K split over them (groups of 32: 0.42 and 0.65), divided
@@ -80,9 +86,15 @@ Tile choose_tile(int S, int E, int K, int N, int group_size) {
   if (forced_tile() >= 0) return (Tile)forced_tile();
   const int groups = E < S ? E : S;
   const int mean = S / (groups > 0 ? groups : 1);
-  if (mean <= (K > 8192 ? 9 : 6)) return TILE_16;
-  if (mean <= 28) return TILE_32;
-  if (mean <= (K > 8192 ? 144 : 384)) return TILE_64;
+  if (K > 8192) {
+    if (mean <= 5) return TILE_16;
+    if (group_size == 32 && mean <= 44) return TILE_32;
+    if (mean <= 144) return TILE_64;
+  } else {
+    if (mean <= 6) return TILE_16;
+    if (mean <= 28) return TILE_32;
+    if (mean <= 384) return TILE_64;
+  }
   const long long cus = device_cu_count();
   const int KC = ceil_div(K, 128);
   const bool small = small_tile_us(S, groups, KC, N, group_size, cus) < large_tile_us(S, groups, KC, N, cus);
