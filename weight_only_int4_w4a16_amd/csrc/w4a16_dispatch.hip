@@ -142,7 +142,7 @@ struct RowParams {
   const float* weights;
   float* dweights;
   const int32_t* plan;
-  int S, E, topk, order, slot;
+  int S, E, topk, slot;
   int tokens, width;
   int vecs;        // vectors per lane and row: kRowVecs or 1
   int segs;        // items per token
@@ -336,7 +336,6 @@ RowParams row_params(const RouteLayout& r, const int32_t* plan, int width, int v
   p.S = r.S;
   p.E = r.E;
   p.topk = r.topk;
-  p.order = r.order;
   p.slot = r.slot;
   p.tokens = r.S / r.topk;
   p.width = width;

@@ -121,7 +121,6 @@ hipError_t launch_grouped(const GemmArgs& a, const RouteLayout& r, const int32_t
   const Tile tile = choose_tile(r.S, r.E, a.K, a.N, a.group_size);
   GroupTiles t;
   t.plan = plan;
-  t.S = r.S;
   t.E = r.E;
   t.token = r.token;
   t.list = r.tiles[tile];

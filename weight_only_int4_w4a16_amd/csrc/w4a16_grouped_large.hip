@@ -10,7 +10,7 @@ W4A16_TILED_INSTANTIATE_GROUPED(LargeTile)
 hipError_t launch_grouped_large(const GemmArgs& a, const GroupTiles& t) {
   tiled::GroupedTiledParams p;
   p.x = static_cast<const uint16_t*>(a.x);
-  p.M = t.S;
+  p.M = 0;  // a tile ends where its entry in the list says
   p.K = a.K;
   p.N = a.N;
   p.packed = reinterpret_cast<const u4_t*>(a.packed);

@@ -759,7 +759,6 @@ hipError_t launch_lora(const LoraArgs& a) {
       if (e != hipSuccess) return e;
       p.groups.plan = plan;
     }
-    p.groups.S = r.S;
     p.groups.E = r.E;
     p.groups.token = r.token;
     p.groups.list = r.tiles[g.list];

@@ -58,7 +58,7 @@ inline RouteLayout route_layout(int tokens, int topk, int E) {
 // What a GEMM kernel's grouped instantiation reads besides its GEMM parameters
 struct GroupTiles {
   const int32_t* plan;
-  int S, E;
+  int E;
   int token, list;  // word offsets in the plan: the sorted rows' tokens, the tile list used
   int bound;        // most tiles the list can hold (the grid's)
   int tokens;       // rows of x where they are gathered through the plan, else 0

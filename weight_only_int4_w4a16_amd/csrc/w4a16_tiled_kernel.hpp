@@ -671,8 +671,6 @@ hipError_t launch_grouped_act(const GemmArgs& a, const GroupedTiledParams& p, di
 }
 
 // one instantiation per tile shape, each in its own translation unit
-#define W4A16_TILED_EXTERN_GROUPED(T) \
-  extern template hipError_t launch_grouped_act<T>(const GemmArgs&, const GroupedTiledParams&, dim3);
 #define W4A16_TILED_INSTANTIATE_GROUPED(T) \
   template hipError_t launch_grouped_act<T>(const GemmArgs&, const GroupedTiledParams&, dim3);
 #define W4A16_TILED_EXTERN(T) \
