@@ -272,7 +272,8 @@ w4a16_status w4a16_dispatch_backward(const void* dxs, const int32_t* plan, int t
 /* Sorted rows back to their tokens, weighted: y[t] = sum_j weights[t][j] ys[slot[t][j]], summed
  * in fp32, j ascending, rounded once.
  *   ys      [in]  dtype [S][width];  weights [in] float [tokens][topk], 4-byte aligned
- *   y       [out] out_dtype [tokens][width], out_dtype = dtype, or any type for fp32 ys */
+ *   y       [out] out_dtype [tokens][width], out_dtype = dtype, or any type for fp32 ys;
+ *           must not overlap an input */
 w4a16_status w4a16_combine(const void* ys, const int32_t* plan, int tokens, int topk, int groups,
                            const float* weights, int width, w4a16_dtype dtype, void* y,
                            w4a16_dtype out_dtype, void* stream);
@@ -280,8 +281,8 @@ w4a16_status w4a16_combine(const void* ys, const int32_t* plan, int tokens, int 
 /* Gradients of w4a16_combine: dys[slot[t][j]] = weights[t][j] dy[t] (zeros in the rows of no
  * group) and dweights[t][j] = sum_n dy[t][n] ys[slot[t][j]][n] in fp32 (0 for a slot of no
  * group).
- *   dy [in] dtype [tokens][width], ys [in] dtype [S][width], dys [out] dtype [S][width] (not
- *   overlapping ys), dweights [out] float [tokens][topk] */
+ *   dy [in] dtype [tokens][width], ys [in] dtype [S][width], dys [out] dtype [S][width],
+ *   dweights [out] float [tokens][topk]; neither may overlap an input */
 w4a16_status w4a16_combine_backward(const void* dy, const void* ys, const int32_t* plan, int tokens,
                                     int topk, int groups, const float* weights, int width,
                                     w4a16_dtype dtype, void* dys, float* dweights, void* stream);
@@ -293,7 +294,7 @@ w4a16_status w4a16_combine_backward(const void* dy, const void* ys, const int32_
  *   packed  [in]  w4a16_packed_bytes(K, N) bytes a group, one after another
  *   scales  [in]  act [groups][K/group_size][N]
  *   qzeros  [in]  int32 [groups][K/group_size][N/8], or NULL for symmetric codes
- *   out     [out] out_dtype [S][N]
+ *   out     [out] out_dtype [S][N]; must not overlap an input
  * swiglu != 0: each weight is a fused gate+up projection (as for w4a16_gemm_swiglu, N % 32 == 0)
  * and out is [S][N/2]. Other arguments, errors and determinism as for w4a16_gemm. */
 w4a16_status w4a16_gemm_grouped(const void* x, const int32_t* plan, int tokens, int topk, int groups,
@@ -317,8 +318,10 @@ size_t w4a16_lora_workspace_bytes(int M, int K, int N, int adapters, int rank, i
 
 /* Low-rank adapters of many requests beside a projection all rows share:
  *   out[m] = y[m] + scaling[a] (x[m] A[a]^T) B[a]^T, a = ids[m]; out[m] = y[m] where a is none
- * for any shared projection y = x W (w4a16_gemm, NF4, AWQ, ...). x A^T is summed in fp32 and
- * not rounded to 16 bits between the products; out is rounded once.
+ * for any shared projection y = x W (w4a16_gemm, NF4, AWQ, ...). t = x A^T is summed in fp32 and
+ * enters the second product as a sum of 16-bit parts: bf16 with 16 significant bits of each t
+ * (24 where y is fp32), fp16 to 2^-22 of each t or 2^-25 of the row's largest |t|, whichever is
+ * more. out is rounded once.
  *   x        [in]  act [M][K], act = W4A16_F16 or W4A16_BF16; K % 32 == 0
  *   y        [in]  y_dtype [M][N], y_dtype = act or W4A16_F32; N % 16 == 0
  *   lora_a   [in]  act [adapters][rank][K];  lora_b [in] act [adapters][N][rank]
@@ -327,7 +330,8 @@ size_t w4a16_lora_workspace_bytes(int M, int K, int N, int adapters, int rank, i
  *   ids      [in]  int32 [M], each row's adapter; read only where plan is NULL
  *   scaling  [in]  float [adapters]
  *   plan     [in]  of w4a16_route(ids, M, 1, adapters), for calls that share it; or NULL
- *   out      [out] y_dtype [M][N]; may be y (then rows of no adapter are left alone)
+ *   out      [out] y_dtype [M][N]; may be y (then rows of no adapter are left alone), must not
+ *                  overlap an input otherwise
  *   workspace [in/out] >= w4a16_lora_workspace_bytes(...), 256-byte aligned
  * x, y, out, lora_a and lora_b need 16-byte alignment. M = 0 is a no-op. Deterministic. */
 w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w4a16_dtype act,

@@ -486,6 +486,10 @@ def dequant_nf4(packed, absmax, codebook, K: int, block_size: int = 64, wdtype=N
 #
 # Decode calls of these take a few microseconds on the GPU, as long as a launch takes on the
 # host, so their checks compare what is expected first and look for what is wrong only after that fails.
+#
+# As everywhere in this binding, autograd is not told of a call: a result never requires a gradient, whatever its inputs do.
+# dispatch_backward and combine_backward are calls for a training loop to make (or to put into a
+# torch.autograd.Function); there is none that takes a gradient through 4-bit weights or through an adapter.
 
 _dtypes = {}      # torch dtype -> w4a16_dtype
 _act_dtypes = ()  # what activations may be
@@ -615,7 +619,7 @@ def route(ids, groups: int) -> Routing:
 
 def dispatch(x, routing: Routing, out=None):
     """Tokens' rows into sorted order: ``xs[rows, width]``, ``xs[p] = x[order[p] // topk]``, zeros in the
-    rows of no group. ``x[tokens, width]`` fp16, bf16 or fp32, any width."""
+    rows of no group. ``x[tokens, width]`` fp16, bf16 or fp32, any width. The result has no autograd history."""
     _need_routing(routing)
     r = routing
     width, dt = _need_rows(x, "x", r.tokens)
@@ -634,7 +638,8 @@ def dispatch(x, routing: Routing, out=None):
 
 
 def dispatch_backward(dxs, routing: Routing, out=None):
-    """Gradient of :func:`dispatch`: ``dx[t] = sum_j dxs[slot[t, j]]``, summed in fp32."""
+    """Gradient of :func:`dispatch`: ``dx[t] = sum_j dxs[slot[t, j]]``, summed in fp32. ``dxs`` comes from the
+    experts' own backward pass, which for 4-bit weights is not in this library."""
     _need_routing(routing)
     r = routing
     width, dt = _need_rows(dxs, "dxs", r.rows)
@@ -655,7 +660,7 @@ def dispatch_backward(dxs, routing: Routing, out=None):
 def combine(ys, routing: Routing, weights, out_dtype=None, out=None):
     """Sorted rows back to their tokens: ``y[t] = sum_j weights[t, j] * ys[slot[t, j]]`` in fp32,
     rounded once to ``ys``'s dtype (fp32 ``ys``: to any ``out_dtype``). ``weights`` fp32
-    ``[tokens, topk]``; the weight of a slot of no group is not used."""
+    ``[tokens, topk]``; the weight of a slot of no group is not used. The result has no autograd history."""
     _need_routing(routing)
     torch, r = _torch(), routing
     width, dt = _need_rows(ys, "ys", r.rows)
@@ -680,7 +685,8 @@ def combine(ys, routing: Routing, weights, out_dtype=None, out=None):
 
 def combine_backward(dy, ys, routing: Routing, weights):
     """Gradients of :func:`combine` for ``dy[tokens, width]`` in ``ys``'s dtype: ``(dys, dweights)``,
-    ``dys[slot[t, j]] = weights[t, j] * dy[t]`` and the fp32 ``dweights[t, j] = <dy[t], ys[slot[t, j]]>``."""
+    ``dys[slot[t, j]] = weights[t, j] * dy[t]`` and the fp32 ``dweights[t, j] = <dy[t], ys[slot[t, j]]>``.
+    ``dweights`` trains a gate over frozen 4-bit experts; ``dys`` is for experts whose backward pass the caller has."""
     _need_routing(routing)
     torch, r = _torch(), routing
     width, dt = _need_rows(ys, "ys", r.rows)
@@ -806,7 +812,8 @@ def lora_add(y, x, lora_a, lora_b, ids, scaling, routing: Routing | None = None,
     ``y[M, N]`` the projection's output (x's dtype or fp32), ``x[M, K]`` fp16/bf16,
     ``lora_a[adapters, rank, K]``, ``lora_b[adapters, N, rank]`` in x's dtype, ``ids`` int32 ``[M]``,
     ``scaling`` fp32 ``[adapters]``. ``routing``: ``route(ids, adapters)``, made once for the projections of a step
-    that share the ids. ``out`` may be ``y``. ``workspace``: optional, ``lora_workspace_bytes(...)``."""
+    that share the ids. ``out`` may be ``y``. ``workspace``: optional, ``lora_workspace_bytes(...)``. The
+    result has no autograd history."""
     torch = _torch()
     if not _dtypes:
         _load_dtypes()

@@ -17,7 +17,9 @@
 // Measured from cold, against a copy of a large tensor at 5.2 TB/s (bf16): 8192 tokens x 4096 to two rows
 // each and back 71 us with the sort (389 MB); 16384 x 2048, eight rows each, with all gradients 557 us
 // (2953 MB, 5.3 TB/s); 4099 x 2885, three rows each, whose vectors cross cache lines, dispatch and combine 20
-// us each, gradients 36 (3.6-4 TB/s; rows of 2880: 15.5, 18, 33).
+// us each, gradients 40 (4.7 and 4.1 TB/s; with a fifth of the slots dropped 21, 18 and 38, and 16, 16 and 32 for
+// rows of 2880). fp32 rows of 8192 x 4096, two each, combined to fp32 64 us, to bf16 55 (6.1 TB/s, although a lane then
+// stores its four elements one by one).
 #include <limits.h>
 
 #include "w4a16_device.hpp"
@@ -465,7 +467,7 @@ static void launch_backward(const RowParams& p, hipStream_t s) {
   switch (row_mode<T>(p)) {
     case NARROW: launch_backward_j<T, 1, NARROW>(p, s); break;
     // odd rows, 4099 x 2885 at topk 3: over and over by itself 36 us cached, 41 streamed, but between the other
-    // moves of a training step streamed (all of them 99 us, 104 cached)
+    // moves of a training step streamed (all of them 99 us, 104 cached); that one case is all that decides it
     case CACHED: launch_backward_m<T, CACHED>(p, s); break;
     case STREAM: launch_backward_m<T, STREAM>(p, s); break;
     default: launch_backward_m<T, STREAM_LINES>(p, s);

@@ -19,10 +19,11 @@
 //
 // t in 16-bit MFMA operands. Rounding t once would cost as much as rounding the product, so t
 // is split into parts of the activation type, t = t0 + t1 (+ t2), each the rounding of what
-// the ones before left: 22 (fp16), 16 or 24 (bf16, three parts where out is fp32) bits of t,
-// and the parts' products with B add in fp32. fp16 parts of a large or small t could leave
+// the ones before left, and the parts' products with B add in fp32. bf16 parts hold 16 bits of
+// each t (24 in three parts, where out is fp32). fp16 parts of a large or small t could leave
 // the type's range, so a row is first scaled by the power of two that brings its largest |t|
-// into [1, 2); the scale goes back into s. A workgroup splits its rows' t once, in LDS, for all its columns.
+// into [1, 2), and the scale goes back into s: they hold 22 bits of that largest t, and of a smaller one
+// what is above 2^-25 of it. A workgroup splits its rows' t once, in LDS, for all its columns.
 //
 // Operands of the second product. B is the A operand (16 columns n of the output) and t the B
 // operand (16 rows m), so a lane ends with four consecutive n of one row. A wave's 16 x 64 product is
@@ -627,6 +628,8 @@ LoraGeometry lora_geometry(int M, int K, int N, int L, int R, bool self) {
   // workgroups of a tile of 512 columns (from L2), 16 MiB of such reads in all.
   g.one = self && R <= kRankChunk && (long long)R * K <= (1 << 17) &&
           (long long)M * ceil_div(N, 64 * expand_waves(true)) * R * K <= (1 << 23);
+  // by the adapters that can have rows: with many loaded and few in use the mean is low, and 16-row tiles are taken
+  // for what 64-row tiles would do (4096 rows of 9 adapters, 8192x8192 rank 64: 62 us with 9 loaded, 86 with 64, 128 with 128)
   const int groups = L < M ? L : M;
   g.list = M / (groups > 0 ? groups : 1) >= 48 ? 2 : 0;
   // tiles to expect: full ones, and about one part-filled for every second adapter

@@ -22,7 +22,8 @@
 // between.
 //
 // Measured (us): 32 slots of 8 groups 3.5, 512 of 64 5.6, 1600 of 64 6.2, 4096 of 16 7.2; 16384 of 8 4.7 + 6.8,
-// 131072 of 128 5.0 + 10.6. (With shuffles for the scans and the lists one after another: 5.1, 7.6, 8.0,
+// 131072 of 128 5.0 + 10.6. With the third kernel, whose one workgroup walks all the counts twice, whole calls:
+// 131072 of 1024 62, 200000 of 1024 85, 4 Mi of 128 1200. (With shuffles for the scans and the lists one after another: 5.1, 7.6, 8.0,
 // 8.3; 7.2 and 15.3 for the second launches.)
 #include "w4a16_device.hpp"
 #include "w4a16_routed.hpp"

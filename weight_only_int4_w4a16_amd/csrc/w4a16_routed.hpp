@@ -19,10 +19,15 @@ constexpr int kMaxSlots = 1 << 26;
 constexpr int kRouteBlockSlots = 2048;  // slots per workgroup of the sort where there are several
 constexpr int kRouteWholeSlots = 4096;  // most slots that one workgroup sorts alone
 // Rows of so many bytes in one call, a quarter of the last-level cache, are stored (and read for the last
-// time) past the caches: from cold, bf16, dispatch and combine of 8192 x 4096 at topk 2 (128 MiB of sorted
-// rows) 88 -> 71 us, adapters of 4096 x 8192 (64 MiB) 68 -> 60. A call that reads the rows right
-// after loses what it would have found there: dispatch and combine of the same rows at 64/128/256/512 MiB
-// 32/61/153/255 us cached, 34/64/124/209 streamed; a grouped product of them takes the same time.
+// time) past the caches. The gain is on rows that the caches do not hold: bf16, dispatch and combine of 8192 x 4096
+// at topk 2 (128 MiB of sorted rows) 88 -> 71 us, adapters of 4096 x 8192 (64 MiB) 68 -> 60. Where a call's rows were
+// just written, or are read next, the caches would have served it up to about their size (us by MiB of
+// rows, 64/128/256/512, cached then streamed):
+//   dispatch, combine                              32/60/153/298        34/64/123/245
+//   combine_backward, one reader of dys            47/110/219/432       52/105/217/434
+//   dispatch, product (4096 deep), combine         356/623/1160/2265    360/621/1160/2244
+//   projection, adapters in place, projection      209/364/684/1350     210/366/692/1344
+// so between products, as a layer has them, either way costs the other at most 1%.
 constexpr size_t kStreamBytes = (size_t)64 << 20;
 inline int round64(int n) { return (n + 63) & ~63; }
 // most tiles list j can hold: full tiles, and one more for each group with rows
