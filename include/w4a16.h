@@ -45,7 +45,9 @@
 extern "C" {
 #endif
 
-typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1, W4A16_F32 = 2 } w4a16_dtype;
+/* W4A16_E4M3: 8-bit floating point codes (OCP e4m3: largest 448, no infinities), one a byte, with
+ * scales of their own; only the calls that name it take it. */
+typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1, W4A16_F32 = 2, W4A16_E4M3 = 3 } w4a16_dtype;
 
 typedef enum {
   W4A16_OK = 0,
@@ -338,6 +340,108 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
                             w4a16_dtype y_dtype, const void* lora_a, const void* lora_b, int adapters,
                             int rank, const int32_t* ids, const float* scaling, const int32_t* plan,
                             void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * 8-bit floating point operators: e4m3 codes with one fp32 scale for each 128 values along the
+ * product's depth (activations and gradients), or for each block of 128 x 128 (weights).
+ *
+ *   scale = max(RN_f32(max |v| / 448), 2^-126)      code = RN_e4m3(RN_f32(v / scale))
+ *
+ * over the group's values (the last group of a row, column or weight may be short): two correctly
+ * rounded fp32 steps and one rounding to 8 bits, ties to even. A group of zeros has the least scale
+ * and zero codes. A group that holds an infinity or a NaN has a NaN scale and NaN codes, so that
+ * every result it enters is NaN.
+ * Products: the codes' products of a block of 128 k are summed in fp32 on the matrix cores, the
+ * block's sum is multiplied by its two scales and added to the result in fp32, which is rounded
+ * once. Results are deterministic.
+ * Limits, else W4A16_ERR_UNSUPPORTED: a product's depth is a multiple of 16; operands whose
+ * offsets 31 bits hold (K < 2^23; rows * K / 32 < 2^31; a SwiGLU weight below 2 GiB a group).
+ * Codes, 16-bit x and dy need 16-byte alignment, other arrays that of their elements (outputs of
+ * products 16 bytes).
+ * ------------------------------------------------------------------------------------------ */
+
+/* Rows to codes, for the operand of a product of depth K: one scale for 128 values of a row.
+ *   x       [in]  dtype [M][K], K % 16 == 0
+ *   codes   [out] [M][K]
+ *   scales  [out] float [ceil(K/128)][M] */
+w4a16_status w4a16_quantize_fp8(const void* x, int M, int K, w4a16_dtype dtype, uint8_t* codes,
+                                float* scales, void* stream);
+
+/* Columns to codes, transposed, for an operand whose depth is the rows (a weight's gradient): one
+ * scale for 128 values of a column.
+ *   x       [in]  dtype [M][K], element-aligned
+ *   codes   [out] [K][M rounded up to a multiple of 16], zeros past M; 16-byte aligned
+ *   scales  [out] float [ceil(M/128)][K] */
+w4a16_status w4a16_quantize_fp8_columns(const void* x, int M, int K, w4a16_dtype dtype, uint8_t* codes,
+                                        float* scales, void* stream);
+
+/* A weight to codes: one scale for a block of 128 x 128.
+ *   w        [in]  dtype [N][K], element-aligned
+ *   codes    [out] [N][K];  scales [out] float [ceil(N/128)][ceil(K/128)]
+ *   codes_t, scales_t [out] the same transposed ([K][N] and [ceil(K/128)][ceil(N/128)]), the weight
+ *                    that gradients are multiplied with; both or neither may be NULL */
+w4a16_status w4a16_quantize_fp8_weight(const void* w, int N, int K, w4a16_dtype dtype, uint8_t* codes,
+                                       float* scales, uint8_t* codes_t, float* scales_t, void* stream);
+
+/* Bytes of scratch w4a16_gemm_fp8 needs on the current device: the codes and scales of a 16-bit x
+ * (M * K and about M * K / 32 bytes), and for e4m3 out of shapes whose kernel cannot quantize it h in
+ * fp32. 0 for M = 0 or bad shapes. */
+size_t w4a16_fp8_workspace_bytes(int M, int K, int N, w4a16_dtype x_dtype, int swiglu,
+                                 w4a16_dtype out_dtype);
+
+/* y = x W^T for 8-bit weights.
+ *   x         [in]  [M][K]: F16 or BF16 (quantized by a first kernel into the workspace), or E4M3
+ *                   codes with x_scales, as w4a16_quantize_fp8 writes them (NULL for 16-bit x)
+ *   codes     [in]  [N][K], one row an output feature;  scales [in] float [ceil(N/128)][ceil(K/128)]
+ *   out       [out] out_dtype [M][N]: x's 16-bit type or F32; any of F16, BF16, F32 for E4M3 x
+ * swiglu != 0: the weight is a fused gate+up projection, gate rows first (N % 2 == 0), each half
+ * with blocks of its own (scales [2 ceil(N/256)][ceil(K/128)]: for N % 256 == 0 those of the whole),
+ * and out is h = SiLU(g) u, [M][N/2]; out_dtype E4M3 then gives h as codes with out_scales (float
+ * [ceil(N/256)][M], N % 32 == 0), quantized from the fp32 h as w4a16_quantize_fp8 does.
+ *   workspace [in/out] >= w4a16_fp8_workspace_bytes(...), 256-byte aligned (may be NULL when 0)
+ * M = 0 is a no-op. out must not overlap an input. */
+w4a16_status w4a16_gemm_fp8(const void* x, w4a16_dtype x_dtype, const float* x_scales, int M, int K, int N,
+                            const uint8_t* codes, const float* scales, int swiglu, void* out,
+                            w4a16_dtype out_dtype, float* out_scales, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Name of the kernel w4a16_gemm_fp8 launches for the product ("none" for bad shapes). */
+const char* w4a16_fp8_kernel_name(int M, int K, int N, int swiglu);
+
+/* w4a16_gemm_fp8 of a plan's sorted rows with their groups' weights (codes [groups][N][K], scales
+ * [groups][...], as there); the rows of no group are zeros (E4M3 out: zero codes, least scales).
+ *   x, gather as for w4a16_gemm_grouped: the tokens' rows (tokens * K < 2^31) or the sorted rows;
+ *             x_scales has as many rows as x
+ *   out       [S][N] or [S][N/2], out_scales [ceil(N/256)][S] */
+size_t w4a16_fp8_grouped_workspace_bytes(int tokens, int topk, int groups, int gather, int K, int N,
+                                         w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype);
+w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const float* x_scales,
+                                    const int32_t* plan, int tokens, int topk, int groups, int gather, int K,
+                                    int N, const uint8_t* codes, const float* scales, int swiglu, void* out,
+                                    w4a16_dtype out_dtype, float* out_scales, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Gradients of y = x W^T: dx = dy W, with dy quantized by rows, and dw = dy^T x, with both quantized
+ * by columns (each call quantizes them anew).
+ *   dy       [in]  act [M][N], x [in] act [M][K]; N % 16 == 0, K % 16 == 0
+ *   codes_t, scales_t [in] the transposed weight's [K][N] and float [ceil(K/128)][ceil(N/128)]
+ *   dx       [out] act [M][K], or NULL;  dw [out] float [N][K], or NULL (x is read for dw alone,
+ *                  codes_t and scales_t for dx alone)
+ * M = 0: dw is cleared. */
+size_t w4a16_fp8_backward_workspace_bytes(int M, int K, int N);
+w4a16_status w4a16_gemm_fp8_backward(const void* dy, const void* x, int M, int K, int N, w4a16_dtype act,
+                                     const uint8_t* codes_t, const float* scales_t, void* dx, float* dw,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for sorted rows (dy [S][N], x [S][K]) and their groups' weights: dx [S][K] has zeros in the
+ * rows of no group, dw [groups][N][K] zeros for a group of no rows. For dw a group's rows are cut in
+ * 128s from its first one. */
+size_t w4a16_fp8_grouped_backward_workspace_bytes(int tokens, int topk, int groups, int K, int N);
+w4a16_status w4a16_gemm_fp8_grouped_backward(const void* dy, const void* x, const int32_t* plan, int tokens,
+                                             int topk, int groups, int K, int N, w4a16_dtype act,
+                                             const uint8_t* codes_t, const float* scales_t, void* dx,
+                                             float* dw, void* workspace, size_t workspace_bytes,
+                                             void* stream);
 
 /* Name of the kernel w4a16_gemm / w4a16_gemm_nf4 launch for this shape (static string),
  * so a caller can log which path ran ("4.3 Weight-only INT4", section 4.1). */

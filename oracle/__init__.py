@@ -22,6 +22,7 @@ Modules
   gptq      GPTQ: row-by-row quantization with inverse-Hessian error compensation
   awq       AWQ: per-input-channel scale search, S W quantized, activations times S^-1
   w4a8      W4A8: per-token INT8 activations, per-channel INT4 weights, integer product
+  fp8       e4m3 codes with a scale for each 128 values or block of 128 x 128, their products and gradients
   routed    rows sorted by group and back with gradients, grouped products, row adapters
   storage   bytes and bits per weight of the packed format
   roofline  memory/compute floors and the batch crossover
@@ -42,6 +43,7 @@ from .gptq import hessian, compensate, gptq_quantize
 from . import awq
 from . import w4a8
 from . import routed
+from . import fp8
 from .storage import storage_bytes, bits_per_weight, bytes_per_weight
 from . import roofline
 
@@ -54,6 +56,6 @@ __all__ = [
     "dequant_affine", "dequant_sym", "dequant_nf4",
     "gemm_ref", "gemm_ref_columns", "gemm_bruteforce",
     "silu", "swiglu_split", "swiglu_ref", "swiglu_bound",
-    "hessian", "compensate", "gptq_quantize", "awq", "w4a8", "routed",
+    "hessian", "compensate", "gptq_quantize", "awq", "w4a8", "routed", "fp8",
     "storage_bytes", "bits_per_weight", "bytes_per_weight", "roofline",
 ]

@@ -13,7 +13,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libw4a16.so")
 
-F16, BF16, F32 = 0, 1, 2
+F16, BF16, F32, E4M3 = 0, 1, 2, 3
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE = 0, 1, 2, 3, 4
 
 _lib = None
@@ -94,6 +94,30 @@ def lib() -> ctypes.CDLL:
     L.w4a16_lora_workspace_bytes.restype = sz
     L.w4a16_lora_add.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     L.w4a16_lora_add.restype = i32
+    L.w4a16_quantize_fp8.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+    L.w4a16_quantize_fp8.restype = i32
+    L.w4a16_quantize_fp8_columns.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+    L.w4a16_quantize_fp8_columns.restype = i32
+    L.w4a16_quantize_fp8_weight.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.w4a16_quantize_fp8_weight.restype = i32
+    L.w4a16_fp8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    L.w4a16_fp8_workspace_bytes.restype = sz
+    L.w4a16_gemm_fp8.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, sz, vp]
+    L.w4a16_gemm_fp8.restype = i32
+    L.w4a16_fp8_kernel_name.argtypes = [i32, i32, i32, i32]
+    L.w4a16_fp8_kernel_name.restype = ctypes.c_char_p
+    L.w4a16_fp8_grouped_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
+    L.w4a16_fp8_grouped_workspace_bytes.restype = sz
+    L.w4a16_gemm_fp8_grouped.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, sz, vp]
+    L.w4a16_gemm_fp8_grouped.restype = i32
+    L.w4a16_fp8_backward_workspace_bytes.argtypes = [i32, i32, i32]
+    L.w4a16_fp8_backward_workspace_bytes.restype = sz
+    L.w4a16_gemm_fp8_backward.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.w4a16_gemm_fp8_backward.restype = i32
+    L.w4a16_fp8_grouped_backward_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.w4a16_fp8_grouped_backward_workspace_bytes.restype = sz
+    L.w4a16_gemm_fp8_grouped_backward.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.w4a16_gemm_fp8_grouped_backward.restype = i32
     L.w4a16_read_probe.argtypes = [vp, sz, vp, vp]
     L.w4a16_read_probe.restype = i32
     L.w4a16_version.argtypes = []
@@ -863,6 +887,333 @@ def lora_add(y, x, lora_a, lora_b, ids, scaling, routing: Routing | None = None,
     if st:
         _check(st, "w4a16_lora_add")
     return out
+
+
+# ---- 8-bit floating point: e4m3 codes with a scale for each 128 values, or block of 128 x 128 of a weight ----
+#
+# Codes are torch.float8_e4m3fn tensors, scales fp32. Scales of rows lie by blocks of the depth, [ceil(K / 128), rows].
+# As for the routed operators, checks compare what is expected first, autograd is not told of a call, and
+# scratch is torch's own (a call's alone, whatever stream or graph it is in).
+
+
+class _Device:
+    """Makes a tensor's device the current one for a launch."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        torch = _torch()
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.before != self.index:
+            _torch().cuda.set_device(self.before)
+
+
+def _fp8_values(x, name):
+    """A contiguous 2-D device tensor of fp16, bf16 or fp32; returns its sizes and w4a16 dtype."""
+    if not _dtypes:
+        _load_dtypes()
+    if x is None or x.dim() != 2:
+        _fail(f"{name} must be a 2-D tensor")
+    m, k = x.shape
+    dt = _dtypes.get(x.dtype)
+    if dt is None or not x.is_contiguous():
+        _expect(x, name, (m, k), tuple(_dtypes))
+    if m + k > _INT_MAX:
+        _need_ints(m, k)
+    if k < 1:
+        _fail(f"{name} has rows of no elements")
+    _need_device(x.device, name)
+    return m, k, dt
+
+
+def _up128(n):
+    return (n + 127) // 128
+
+
+def quantize_fp8(x):
+    """Rows to e4m3: ``(codes[M, K], scales[ceil(K/128), M])``, ``scale = max(max|v| / 448, 2^-126)`` over 128 values of
+    a row and ``code = v / scale`` rounded to fp32, then to e4m3 (ties to even). ``x[M, K]`` fp16, bf16 or fp32, K a
+    multiple of 16. A group that holds an infinity or a NaN becomes NaN."""
+    torch = _torch()
+    M, K, dt = _fp8_values(x, "x")
+    codes = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
+    scales = x.new_empty((_up128(K), M), dtype=torch.float32)
+    with _Device(x.device.index):
+        st = lib().w4a16_quantize_fp8(x.data_ptr(), M, K, dt, codes.data_ptr(), scales.data_ptr(), _raw_stream(x.device))
+    if st:
+        _check(st, "w4a16_quantize_fp8")
+    return codes, scales
+
+
+def quantize_fp8_columns(x):
+    """Columns to e4m3, transposed: ``(codes[K, M'], scales[ceil(M/128), K])`` with a scale for 128 values of a
+    column; M' is M rounded up to a multiple of 16, its last codes zeros. Both operands of a weight's gradient."""
+    torch = _torch()
+    M, K, dt = _fp8_values(x, "x")
+    codes = x.new_empty((K, (M + 15) // 16 * 16), dtype=torch.float8_e4m3fn)
+    scales = x.new_empty((_up128(M), K), dtype=torch.float32)
+    with _Device(x.device.index):
+        st = lib().w4a16_quantize_fp8_columns(x.data_ptr(), M, K, dt, codes.data_ptr(), scales.data_ptr(),
+                                              _raw_stream(x.device))
+    if st:
+        _check(st, "w4a16_quantize_fp8_columns")
+    return codes, scales
+
+
+def quantize_fp8_weight(w, transposed: bool = False):
+    """A weight ``w[N, K]`` to e4m3 with a scale for each block of 128 x 128: ``(codes[N, K], scales[ceil(N/128),
+    ceil(K/128)])``, and with ``transposed`` both transposed as well, ``(codes, scales, codes_t[K, N], scales_t)``,
+    which gradients are multiplied with."""
+    torch = _torch()
+    N, K, dt = _fp8_values(w, "w")
+    codes = w.new_empty((N, K), dtype=torch.float8_e4m3fn)
+    scales = w.new_empty((_up128(N), _up128(K)), dtype=torch.float32)
+    codes_t = scales_t = cp = sp = None
+    if transposed:
+        codes_t = w.new_empty((K, N), dtype=torch.float8_e4m3fn)
+        scales_t = w.new_empty((_up128(K), _up128(N)), dtype=torch.float32)
+        cp, sp = codes_t.data_ptr(), scales_t.data_ptr()
+    with _Device(w.device.index):
+        st = lib().w4a16_quantize_fp8_weight(w.data_ptr(), N, K, dt, codes.data_ptr(), scales.data_ptr(), cp, sp,
+                                             _raw_stream(w.device))
+    if st:
+        _check(st, "w4a16_quantize_fp8_weight")
+    return (codes, scales, codes_t, scales_t) if transposed else (codes, scales)
+
+
+def _fp8_x(x, x_scales):
+    """x of a product: 16-bit rows, or codes with their scales. Returns (rows, K, w4a16 dtype, scales' address)."""
+    torch = _torch()
+    if not _dtypes:
+        _load_dtypes()
+    if x is None or x.dim() != 2:
+        _fail("x must be a 2-D [M, K] tensor")
+    M, K = x.shape
+    if not x.is_contiguous():
+        _fail("x must be contiguous")
+    _need_device(x.device, "x")
+    if M + K > _INT_MAX:
+        _need_ints(M, K)
+    if x.dtype is torch.float8_e4m3fn:
+        return M, K, E4M3, _need(x_scales, "x_scales", (_up128(K), M), torch.float32, x.device)
+    if x.dtype not in _act_dtypes:
+        _fail(f"x: dtype {x.dtype}, expected float16, bfloat16 or float8_e4m3fn")
+    if x_scales is not None:
+        _fail("x_scales is for float8_e4m3fn x")
+    return M, K, _dtypes[x.dtype], None
+
+
+def _fp8_weight(codes, scales, lead, K, glu, device, kind="codes"):
+    """The weight's codes ``[*lead, N, K]`` and block scales; returns N and their addresses."""
+    torch = _torch()
+    if codes is None or codes.dim() != len(lead) + 2:
+        _fail(f"{kind} must be a {len(lead) + 2}-D tensor of float8_e4m3fn")
+    N = codes.shape[-2]
+    if N > _INT_MAX:
+        _need_ints(N)
+    cp = _need(codes, kind, (*lead, N, K), torch.float8_e4m3fn, device)
+    if N < 1:
+        _fail(f"{kind} has no rows")
+    if glu and N % 2:
+        _fail(f"N={N} must be even (gate and up halves)")
+    blocks = 2 * _up128(N // 2) if glu else _up128(N)
+    return N, cp, _need(scales, "scales" if kind == "codes" else "scales_t", (*lead, blocks, _up128(K)), torch.float32, device)
+
+
+def _fp8_out(x, x_dt, rows, width, glu, quantized, out_dtype, out):
+    """The output and its w4a16 dtype, and with ``quantized`` its scales."""
+    torch = _torch()
+    if quantized:
+        if out is not None or out_dtype is not None:
+            _fail("quantized results take neither out nor out_dtype")
+        return (x.new_empty((rows, width), dtype=torch.float8_e4m3fn), E4M3,
+                x.new_empty((_up128(width), rows), dtype=torch.float32))
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else x.dtype if x_dt != E4M3 else torch.bfloat16
+    dt = _dtypes.get(out_dtype)
+    if dt is None or (x_dt != E4M3 and dt != F32 and dt != x_dt):
+        _fail(f"out dtype {out_dtype}: must be {'a 16-bit type' if x_dt == E4M3 else 'the activation dtype'} or float32")
+    if out is None:
+        return x.new_empty((rows, width), dtype=out_dtype), dt, None
+    _need(out, "out", (rows, width), out_dtype, x.device)
+    _apart(out, "out", (x,))
+    return out, dt, None
+
+
+def _fp8_scratch(x, need, workspace):
+    """A call's workspace: the caller's, or one of torch's for this call. Returns it, its address and bytes."""
+    if workspace is not None:
+        _expect_workspace(workspace, need, x.device)
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if not need:
+        return None, None, 0
+    ws = x.new_empty(need, dtype=_torch().uint8)
+    return ws, ws.data_ptr(), need
+
+
+def fp8_workspace_bytes(M: int, K: int, N: int, x_dtype, swiglu: bool = False, quantized: bool = False) -> int:
+    """Bytes that :func:`gemm_fp8` (``swiglu``: :func:`gemm_fp8_swiglu`) needs for ``x[M, K]`` of ``x_dtype``."""
+    torch = _torch()
+    if not _dtypes:
+        _load_dtypes()
+    if max(M, K, N) > _INT_MAX:
+        return 0
+    dt = E4M3 if x_dtype is torch.float8_e4m3fn else _dtypes[x_dtype]
+    return int(lib().w4a16_fp8_workspace_bytes(M, K, N, dt, int(swiglu), E4M3 if quantized else F32))
+
+
+def _gemm_fp8(x, codes, scales, x_scales, glu, quantized, out_dtype, out, workspace):
+    M, K, x_dt, xsp = _fp8_x(x, x_scales)
+    device = x.device
+    N, cp, sp = _fp8_weight(codes, scales, (), K, glu, device)
+    out, dt, out_scales = _fp8_out(x, x_dt, M, N // 2 if glu else N, glu, quantized, out_dtype, out)
+    L = lib()
+    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_workspace_bytes(M, K, N, x_dt, glu, dt), workspace)
+    with _Device(device.index):
+        st = L.w4a16_gemm_fp8(x.data_ptr(), x_dt, xsp, M, K, N, cp, sp, glu, out.data_ptr(), dt,
+                              None if out_scales is None else out_scales.data_ptr(), wp, nbytes, _raw_stream(device))
+    if st:
+        _check(st, "w4a16_gemm_fp8")
+    return (out, out_scales) if quantized else out
+
+
+def gemm_fp8(x, codes, scales, x_scales=None, out_dtype=None, out=None, workspace=None):
+    """``y = x @ W.T`` for an 8-bit weight: ``codes[N, K]`` float8_e4m3fn, ``scales[ceil(N/128), ceil(K/128)]`` fp32
+    (:func:`quantize_fp8_weight`).
+
+    ``x[M, K]`` fp16 or bf16, quantized as by :func:`quantize_fp8` within the call, or codes with ``x_scales`` (made once
+    for the products that share them). Sums are fp32, each block of 128 scaled as it is added; the result is rounded
+    once to ``out_dtype``: x's dtype or float32 (for codes: bfloat16 unless given). K is a multiple of 16.
+    ``workspace``: optional, ``fp8_workspace_bytes(...)``. The result has no autograd history."""
+    return _gemm_fp8(x, codes, scales, x_scales, 0, False, out_dtype, out, workspace)
+
+
+def gemm_fp8_swiglu(x, codes, scales, x_scales=None, quantized: bool = False, out_dtype=None, out=None, workspace=None):
+    """``h = SiLU(x @ W_gate.T) * (x @ W_up.T)`` for a fused gate+up weight ``codes[N2, K]``, gate rows first, each half
+    with blocks of its own: ``scales[2 * ceil(N2/256), ceil(K/128)]``. Returns ``h[M, N2/2]``, or with ``quantized``
+    the codes and scales that :func:`quantize_fp8` makes of the fp32 h, the next product's operand (N2 a multiple of
+    32). Other arguments as for :func:`gemm_fp8`."""
+    return _gemm_fp8(x, codes, scales, x_scales, 1, quantized, out_dtype, out, workspace)
+
+
+def fp8_kernel_name(M: int, K: int, N: int, swiglu: bool = False) -> str:
+    if max(M, K, N) > _INT_MAX:
+        return "none"
+    return lib().w4a16_fp8_kernel_name(M, K, N, int(swiglu)).decode()
+
+
+def _gemm_fp8_grouped(x, routing, codes, scales, x_scales, glu, quantized, gather, out_dtype, out, workspace):
+    _need_routing(routing)
+    r = routing
+    rows, K, x_dt, xsp = _fp8_x(x, x_scales)
+    device = r.device
+    want = r.tokens if gather else r.rows
+    if rows != want:
+        _fail(f"x has {rows} rows, expected {want} ({'tokens' if gather else 'sorted rows'})")
+    if x.device != device:
+        _fail(f"x is on {x.device}, expected {device}")
+    N, cp, sp = _fp8_weight(codes, scales, (r.groups,), K, glu, device)
+    out, dt, out_scales = _fp8_out(x, x_dt, r.rows, N // 2 if glu else N, glu, quantized, out_dtype, out)
+    L, gather = lib(), int(gather)
+    need = L.w4a16_fp8_grouped_workspace_bytes(r.tokens, r.topk, r.groups, gather, K, N, x_dt, glu, dt)
+    ws, wp, nbytes = _fp8_scratch(x, need, workspace)
+    with _Device(device.index):
+        st = L.w4a16_gemm_fp8_grouped(x.data_ptr(), x_dt, xsp, r.plan.data_ptr(), r.tokens, r.topk, r.groups, gather, K, N,
+                                      cp, sp, glu, out.data_ptr(), dt, None if out_scales is None else out_scales.data_ptr(),
+                                      wp, nbytes, _raw_stream(device))
+    if st:
+        _check(st, "w4a16_gemm_fp8_grouped")
+    return (out, out_scales) if quantized else out
+
+
+def gemm_fp8_grouped(x, routing: Routing, codes, scales, x_scales=None, gather: bool = False, out_dtype=None, out=None,
+                     workspace=None):
+    """:func:`gemm_fp8` of sorted rows with their groups' weights ``codes[groups, N, K]``, ``scales[groups, ...]``: zeros
+    in the rows of no group. ``x`` (and ``x_scales``) holds the sorted rows, or with ``gather`` the tokens', read
+    through the plan."""
+    return _gemm_fp8_grouped(x, routing, codes, scales, x_scales, 0, False, gather, out_dtype, out, workspace)
+
+
+def gemm_fp8_grouped_swiglu(x, routing: Routing, codes, scales, x_scales=None, quantized: bool = False,
+                            gather: bool = False, out_dtype=None, out=None, workspace=None):
+    """:func:`gemm_fp8_swiglu` of sorted rows with their groups' weights. With ``quantized`` the rows of no group have
+    zero codes and the least scale."""
+    return _gemm_fp8_grouped(x, routing, codes, scales, x_scales, 1, quantized, gather, out_dtype, out, workspace)
+
+
+def _fp8_gradients(dy, x, rows, lead, codes_t, scales_t):
+    """The operands of a backward call; returns (N, K, w4a16 dtype, addresses)."""
+    if not _dtypes:
+        _load_dtypes()
+    if dy is None or dy.dim() != 2 or x is None or x.dim() != 2:
+        _fail("dy and x must be 2-D tensors")
+    if x.dtype not in _act_dtypes:
+        _fail(f"x: dtype {x.dtype}, expected float16 or bfloat16")
+    device = x.device
+    _need_device(device, "x")
+    M, K = x.shape
+    if rows is not None and M != rows:
+        _fail(f"x has {M} rows, expected {rows} (sorted rows)")
+    N = dy.shape[1]
+    if M + K + N > _INT_MAX:
+        _need_ints(M, K, N)
+    xp = _need(x, "x", (M, K), x.dtype, device)
+    yp = _need(dy, "dy", (M, N), x.dtype, device)
+    if N < 1 or K < 1:
+        _fail("dy and x must have columns")
+    k, cp, sp = _fp8_weight(codes_t, scales_t, lead, N, 0, device, "codes_t")
+    if k != K:
+        _fail(f"codes_t has {k} rows, expected K={K}")
+    return M, N, K, _dtypes[x.dtype], yp, xp, cp, sp
+
+
+def gemm_fp8_backward(dy, x, codes_t, scales_t, workspace=None):
+    """Gradients of ``y = x @ W.T``: ``(dx, dw)`` for ``dy[M, N]`` and ``x[M, K]`` of one 16-bit type and the transposed
+    weight ``codes_t[K, N]``, ``scales_t[ceil(K/128), ceil(N/128)]`` (:func:`quantize_fp8_weight`).
+
+    ``dx = dy @ W`` in x's dtype, dy quantized by rows; ``dw = dy.T @ x`` in fp32 ``[N, K]``, both quantized by columns
+    (scales over 128 rows). N and K are multiples of 16."""
+    torch = _torch()
+    M, N, K, dt, yp, xp, cp, sp = _fp8_gradients(dy, x, None, (), codes_t, scales_t)
+    dx = torch.empty_like(x)
+    dw = x.new_empty((N, K), dtype=torch.float32)
+    L = lib()
+    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_backward_workspace_bytes(M, K, N), workspace)
+    with _Device(x.device.index):
+        st = L.w4a16_gemm_fp8_backward(yp, xp, M, K, N, dt, cp, sp, dx.data_ptr(), dw.data_ptr(), wp, nbytes,
+                                       _raw_stream(x.device))
+    if st:
+        _check(st, "w4a16_gemm_fp8_backward")
+    return dx, dw
+
+
+def gemm_fp8_grouped_backward(dy, x, routing: Routing, codes_t, scales_t, workspace=None):
+    """:func:`gemm_fp8_backward` of sorted rows ``dy[rows, N]``, ``x[rows, K]`` and their groups' transposed weights
+    ``codes_t[groups, K, N]``: ``dx[rows, K]`` with zeros in the rows of no group, ``dw[groups, N, K]`` with zeros for a
+    group of no rows. For ``dw`` a group's rows are cut in 128s from its first one."""
+    _need_routing(routing)
+    torch, r = _torch(), routing
+    _, N, K, dt, yp, xp, cp, sp = _fp8_gradients(dy, x, r.rows, (r.groups,), codes_t, scales_t)
+    if x.device != r.device:
+        _fail(f"x is on {x.device}, expected {r.device}")
+    dx = torch.empty_like(x)
+    dw = x.new_empty((r.groups, N, K), dtype=torch.float32)
+    L = lib()
+    need = L.w4a16_fp8_grouped_backward_workspace_bytes(r.tokens, r.topk, r.groups, K, N)
+    ws, wp, nbytes = _fp8_scratch(x, need, workspace)
+    with _Device(x.device.index):
+        st = L.w4a16_gemm_fp8_grouped_backward(yp, xp, r.plan.data_ptr(), r.tokens, r.topk, r.groups, K, N, dt, cp, sp,
+                                               dx.data_ptr(), dw.data_ptr(), wp, nbytes, _raw_stream(x.device))
+    if st:
+        _check(st, "w4a16_gemm_fp8_grouped_backward")
+    return dx, dw
 
 
 def read_probe(buf, sink):

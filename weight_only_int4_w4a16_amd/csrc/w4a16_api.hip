@@ -9,6 +9,7 @@
 #include "w4a16.h"
 #include "w4a16_launch.hpp"
 #include "w4a16_routed.hpp"
+#include "w4a16_fp8.hpp"
 
 namespace {
 
@@ -654,6 +655,339 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
   a.workspace = workspace;
   a.stream = static_cast<hipStream_t>(stream);
   return from_hip(w4a16::launch_lora(a));
+}
+
+// ---- 8-bit floating point ----
+
+// dtypes may be any int from a C caller
+static bool is_act(w4a16_dtype d) { return d == W4A16_F16 || d == W4A16_BF16; }
+static bool is_e4m3(w4a16_dtype d) { return (int)d == w4a16::kE4M3; }
+
+// launches hold fewer than 2^32 threads: a tile of 128 x 128 values takes 256, a group of a row 16
+static bool fp8_quantize_fits(int M, int K) {
+  return (long long)w4a16::fp8_blocks(M) * w4a16::fp8_blocks(K) < (1 << 24) && (long long)M * w4a16::fp8_blocks(K) < (1LL << 27);
+}
+
+w4a16_status w4a16_quantize_fp8(const void* x, int M, int K, w4a16_dtype dtype, uint8_t* codes,
+                                float* scales, void* stream) {
+  if (M < 0 || K <= 0 || !valid_dtype(dtype)) return W4A16_ERR_ARG;
+  if (K % 16 || !fp8_quantize_fits(M, K)) return W4A16_ERR_UNSUPPORTED;
+  if (M == 0) return W4A16_OK;
+  if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return W4A16_ERR_ARG;
+  return from_hip(w4a16::launch_fp8_rows(x, M, K, (int)dtype, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+w4a16_status w4a16_quantize_fp8_columns(const void* x, int M, int K, w4a16_dtype dtype, uint8_t* codes,
+                                        float* scales, void* stream) {
+  if (M < 0 || K <= 0 || !valid_dtype(dtype)) return W4A16_ERR_ARG;
+  if (M > 0x7FFFFFF0 || !fp8_quantize_fits(M, K)) return W4A16_ERR_UNSUPPORTED;
+  if (M == 0) return W4A16_OK;
+  if (!x || !codes || !scales || !aligned(x, dtype_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 4))
+    return W4A16_ERR_ARG;
+  return from_hip(w4a16::launch_fp8_columns(x, M, K, (int)dtype, codes, (size_t)w4a16::ceil16(M), scales, nullptr,
+                                            nullptr, static_cast<hipStream_t>(stream)));
+}
+
+w4a16_status w4a16_quantize_fp8_weight(const void* w, int N, int K, w4a16_dtype dtype, uint8_t* codes,
+                                       float* scales, uint8_t* codes_t, float* scales_t, void* stream) {
+  if (N < 0 || K <= 0 || !valid_dtype(dtype) || !codes_t != !scales_t) return W4A16_ERR_ARG;
+  if (!fp8_quantize_fits(N, K)) return W4A16_ERR_UNSUPPORTED;
+  if (N == 0) return W4A16_OK;
+  if (!w || !codes || !scales || !aligned(w, dtype_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 4))
+    return W4A16_ERR_ARG;
+  if (!aligned(codes_t, 16) || !aligned(scales_t, 4)) return W4A16_ERR_ARG;
+  return from_hip(w4a16::launch_fp8_weight(w, N, K, (int)dtype, codes, scales, codes_t, scales_t,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+// The sizes and types of a product; rows: of its output
+static w4a16_status check_fp8(int rows, int K, int N, w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
+  if (rows < 0 || K <= 0 || N <= 0) return W4A16_ERR_ARG;
+  if (!is_act(x_dtype) && !is_e4m3(x_dtype)) return W4A16_ERR_ARG;
+  if (is_e4m3(out_dtype) ? !swiglu : out_dtype != W4A16_F32 && !is_act(out_dtype)) return W4A16_ERR_ARG;
+  if (is_act(x_dtype) && is_act(out_dtype) && x_dtype != out_dtype) return W4A16_ERR_ARG;
+  if (swiglu && N % 2) return W4A16_ERR_ARG;
+  if (K % 16 || (is_e4m3(out_dtype) && N % 32)) return W4A16_ERR_UNSUPPORTED;
+  if (!fp8_quantize_fits(rows, K) || (is_e4m3(out_dtype) && !fp8_quantize_fits(rows, N / 2))) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+// pointers of a product; x of 16 bits takes codes and scales at the workspace's start
+static w4a16_status check_fp8_pointers(const void* x, w4a16_dtype x_dtype, const float* x_scales, const uint8_t* codes,
+                                       const float* scales, const void* out, w4a16_dtype out_dtype,
+                                       const float* out_scales, const void* workspace, size_t have, size_t need) {
+  if (!x || !codes || !scales || !out || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16))
+    return W4A16_ERR_ARG;
+  if (is_e4m3(x_dtype) && (!x_scales || !aligned(x_scales, 4))) return W4A16_ERR_ARG;
+  if (is_e4m3(out_dtype) && (!out_scales || !aligned(out_scales, 4))) return W4A16_ERR_ARG;
+  if (out == x) return W4A16_ERR_ARG;
+  if (need && (!workspace || !aligned(workspace, 256) || have < need)) return W4A16_ERR_WORKSPACE;
+  return W4A16_OK;
+}
+
+// codes and scales of M rows of depth K
+static size_t fp8_rows_bytes(int M, int K) {
+  return w4a16::align256((size_t)M * K) + w4a16::align256((size_t)M * w4a16::fp8_blocks(K) * 4);
+}
+
+// A product's operands; 16-bit x is quantized into the workspace first
+static w4a16_status fp8_operands(w4a16::Fp8Args& a, const void* x, w4a16_dtype x_dtype, const float* x_scales,
+                                 int x_rows, int K, int N, const uint8_t* codes, const float* scales, int swiglu,
+                                 void* out, w4a16_dtype out_dtype, float* out_scales, void* workspace, void* stream) {
+  char* ws = static_cast<char*>(workspace);
+  a.K = a.ldk = K;
+  a.N = swiglu ? N / 2 : N;
+  a.xs_ld = x_rows;
+  a.w = codes;
+  a.ws = scales;
+  a.glu = swiglu != 0;
+  a.out = out;
+  a.out_dtype = (int)out_dtype;
+  a.out_scales = out_scales;
+  a.stream = static_cast<hipStream_t>(stream);
+  if (is_e4m3(x_dtype)) {
+    a.x = static_cast<const uint8_t*>(x);
+    a.xs = x_scales;
+  } else {
+    uint8_t* const xq = reinterpret_cast<uint8_t*>(ws);
+    float* const xs = reinterpret_cast<float*>(ws + w4a16::align256((size_t)x_rows * K));
+    const hipError_t e = w4a16::launch_fp8_rows(x, x_rows, K, (int)x_dtype, xq, xs, a.stream);
+    if (e != hipSuccess) return W4A16_ERR_HIP;
+    a.x = xq;
+    a.xs = xs;
+    ws += fp8_rows_bytes(x_rows, K);
+  }
+  a.scratch = reinterpret_cast<float*>(ws);
+  return W4A16_OK;
+}
+
+size_t w4a16_fp8_workspace_bytes(int M, int K, int N, w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
+  if (check_fp8(M, K, N, x_dtype, swiglu, out_dtype) != W4A16_OK || M == 0) return 0;
+  return (is_e4m3(x_dtype) ? 0 : fp8_rows_bytes(M, K)) +
+         w4a16::fp8_scratch_bytes(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype);
+}
+
+w4a16_status w4a16_gemm_fp8(const void* x, w4a16_dtype x_dtype, const float* x_scales, int M, int K, int N,
+                            const uint8_t* codes, const float* scales, int swiglu, void* out,
+                            w4a16_dtype out_dtype, float* out_scales, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  w4a16_status st = check_fp8(M, K, N, x_dtype, swiglu, out_dtype);
+  if (st != W4A16_OK) return st;
+  if (!w4a16::fp8_fits(M, swiglu ? N / 2 : N, K, swiglu != 0)) return W4A16_ERR_UNSUPPORTED;
+  if (M == 0) return W4A16_OK;
+  st = check_fp8_pointers(x, x_dtype, x_scales, codes, scales, out, out_dtype, out_scales, workspace, workspace_bytes,
+                          w4a16_fp8_workspace_bytes(M, K, N, x_dtype, swiglu, out_dtype));
+  if (st != W4A16_OK) return st;
+  w4a16::Fp8Args a{};
+  a.M = M;
+  st = fp8_operands(a, x, x_dtype, x_scales, M, K, N, codes, scales, swiglu, out, out_dtype, out_scales, workspace, stream);
+  return st != W4A16_OK ? st : from_hip(w4a16::launch_fp8(a));
+}
+
+const char* w4a16_fp8_kernel_name(int M, int K, int N, int swiglu) {
+  if (M <= 0 || check_fp8(M, K, N, W4A16_E4M3, swiglu, W4A16_F32) != W4A16_OK) return "none";
+  return w4a16::fp8_name(M, swiglu ? N / 2 : N, K, swiglu != 0);
+}
+
+static w4a16_status check_fp8_grouped(int tokens, int topk, int groups, int gather, int K, int N, w4a16_dtype x_dtype,
+                                      int swiglu, w4a16_dtype out_dtype) {
+  const w4a16_status st = check_route(tokens, topk, groups);
+  if (st != W4A16_OK) return st;
+  if (gather && (long long)tokens * K >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;
+  return check_fp8(tokens * topk, K, N, x_dtype, swiglu, out_dtype);
+}
+
+size_t w4a16_fp8_grouped_workspace_bytes(int tokens, int topk, int groups, int gather, int K, int N,
+                                         w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
+  if (check_fp8_grouped(tokens, topk, groups, gather, K, N, x_dtype, swiglu, out_dtype) != W4A16_OK || tokens == 0) return 0;
+  return (is_e4m3(x_dtype) ? 0 : fp8_rows_bytes(gather ? tokens : tokens * topk, K)) +
+         w4a16::fp8_grouped_scratch_bytes(w4a16::route_layout(tokens, topk, groups), swiglu ? N / 2 : N, K, swiglu != 0,
+                                          (int)out_dtype);
+}
+
+w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const float* x_scales,
+                                    const int32_t* plan, int tokens, int topk, int groups, int gather, int K,
+                                    int N, const uint8_t* codes, const float* scales, int swiglu, void* out,
+                                    w4a16_dtype out_dtype, float* out_scales, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  w4a16_status st = check_fp8_grouped(tokens, topk, groups, gather, K, N, x_dtype, swiglu, out_dtype);
+  if (st != W4A16_OK || tokens == 0) return st;
+  const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
+  if (!w4a16::fp8_grouped_fits(r, swiglu ? N / 2 : N, K, swiglu != 0)) return W4A16_ERR_UNSUPPORTED;
+  if (!plan || !aligned(plan, 256)) return W4A16_ERR_ARG;
+  st = check_fp8_pointers(
+      x, x_dtype, x_scales, codes, scales, out, out_dtype, out_scales, workspace, workspace_bytes,
+      w4a16_fp8_grouped_workspace_bytes(tokens, topk, groups, gather, K, N, x_dtype, swiglu, out_dtype));
+  if (st != W4A16_OK) return st;
+  w4a16::Fp8Args a{};
+  a.M = r.S;
+  st = fp8_operands(a, x, x_dtype, x_scales, gather ? tokens : r.S, K, N, codes, scales, swiglu, out, out_dtype, out_scales,
+                    workspace, stream);
+  return st != W4A16_OK ? st : from_hip(w4a16::launch_fp8_grouped(a, r, plan, gather != 0));
+}
+
+// dy and x transposed for dw, `rows` deep with their padding: codes and scales of each
+struct Fp8ColumnsLayout {
+  size_t dy, dys, x, xs, total;
+};
+static Fp8ColumnsLayout fp8_columns_layout(size_t pitch, size_t blocks, int K, int N) {
+  Fp8ColumnsLayout l;
+  l.dy = 0;
+  l.dys = l.dy + w4a16::align256(pitch * N);
+  l.x = l.dys + w4a16::align256(blocks * N * 4);
+  l.xs = l.x + w4a16::align256(pitch * K);
+  l.total = l.xs + w4a16::align256(blocks * K * 4);
+  return l;
+}
+
+static w4a16_status check_fp8_backward(int rows, size_t depth, int K, int N) {
+  if (rows < 0 || K <= 0 || N <= 0) return W4A16_ERR_ARG;
+  if (K % 16 || N % 16) return W4A16_ERR_UNSUPPORTED;
+  if (depth >= (1u << 23) || !fp8_quantize_fits((int)depth, K) || !fp8_quantize_fits((int)depth, N)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::fp8_fits(rows, K, N, false) || !w4a16::fp8_fits(N, K, (int)depth, false)) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+// what dx's and dw's launches read stands in turn in the same scratch
+static size_t fp8_backward_bytes(int rows, int K, int N, size_t pitch, size_t blocks) {
+  const size_t dx = fp8_rows_bytes(rows, N), dw = fp8_columns_layout(pitch, blocks, K, N).total;
+  return dx > dw ? dx : dw;
+}
+
+static w4a16_status check_fp8_backward_pointers(const void* dy, const void* x, w4a16_dtype act, const uint8_t* codes_t,
+                                                const float* scales_t, const void* dx, const float* dw,
+                                                const void* workspace, size_t have, size_t need) {
+  if (!is_act(act) || !dy || !aligned(dy, 16)) return W4A16_ERR_ARG;
+  if (dx && (!codes_t || !scales_t || !aligned(codes_t, 16) || !aligned(scales_t, 4) || !aligned(dx, 16) || dx == dy))
+    return W4A16_ERR_ARG;
+  if (dw && (!x || !aligned(x, 16) || !aligned(dw, 16))) return W4A16_ERR_ARG;
+  if (need && (!workspace || !aligned(workspace, 256) || have < need)) return W4A16_ERR_WORKSPACE;
+  return W4A16_OK;
+}
+
+// dw[m = n][n = k]: dy's columns are the rows, x's the weight's
+static w4a16::Fp8Args fp8_dw_args(char* ws, const Fp8ColumnsLayout& l, size_t pitch, int K, int N, float* dw, hipStream_t s) {
+  w4a16::Fp8Args a{};
+  a.x = reinterpret_cast<const uint8_t*>(ws + l.dy);
+  a.xs = reinterpret_cast<const float*>(ws + l.dys);
+  a.w = reinterpret_cast<const uint8_t*>(ws + l.x);
+  a.ws = reinterpret_cast<const float*>(ws + l.xs);
+  a.w_rows = true;
+  a.M = N;
+  a.N = K;
+  a.K = a.ldk = (int)pitch;
+  a.xs_ld = N;
+  a.out = dw;
+  a.out_dtype = 2;
+  a.stream = s;
+  return a;
+}
+
+// both operands of dw, through the tiles of a plan or plain
+static hipError_t fp8_dw_operands(const void* dy, const void* x, int rows, int K, int N, w4a16_dtype act, char* ws,
+                                  const Fp8ColumnsLayout& l, size_t pitch, const w4a16::RouteLayout* r,
+                                  const int32_t* plan, hipStream_t s) {
+  const hipError_t e = w4a16::launch_fp8_columns(dy, rows, N, (int)act, reinterpret_cast<uint8_t*>(ws + l.dy), pitch,
+                                                 reinterpret_cast<float*>(ws + l.dys), r, plan, s);
+  if (e != hipSuccess) return e;
+  return w4a16::launch_fp8_columns(x, rows, K, (int)act, reinterpret_cast<uint8_t*>(ws + l.x), pitch,
+                                   reinterpret_cast<float*>(ws + l.xs), r, plan, s);
+}
+
+size_t w4a16_fp8_backward_workspace_bytes(int M, int K, int N) {
+  if (M < 0 || M > 0x7FFFFF00) return 0;
+  const size_t pitch = (size_t)w4a16::ceil16(M);
+  if (check_fp8_backward(M, pitch, K, N) != W4A16_OK || M == 0) return 0;
+  return fp8_backward_bytes(M, K, N, pitch, w4a16::fp8_blocks(M));
+}
+
+w4a16_status w4a16_gemm_fp8_backward(const void* dy, const void* x, int M, int K, int N, w4a16_dtype act,
+                                     const uint8_t* codes_t, const float* scales_t, void* dx, float* dw,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0) return W4A16_ERR_ARG;
+  if (M > 0x7FFFFF00) return W4A16_ERR_UNSUPPORTED;
+  const size_t pitch = (size_t)w4a16::ceil16(M);
+  w4a16_status st = check_fp8_backward(M, pitch, K, N);
+  if (st != W4A16_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (M == 0) {
+    if (!is_act(act) || (dw && !aligned(dw, 16))) return W4A16_ERR_ARG;
+    if (!dw) return W4A16_OK;
+    w4a16::Fp8Args a = fp8_dw_args(nullptr, Fp8ColumnsLayout{}, 0, K, N, dw, s);  // a product of no depth
+    return from_hip(w4a16::launch_fp8(a));
+  }
+  st = check_fp8_backward_pointers(dy, x, act, codes_t, scales_t, dx, dw, workspace, workspace_bytes,
+                                   w4a16_fp8_backward_workspace_bytes(M, K, N));
+  if (st != W4A16_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  if (dx) {
+    w4a16::Fp8Args a{};
+    a.M = M;
+    st = fp8_operands(a, dy, act, nullptr, M, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream);
+    if (st != W4A16_OK) return st;
+    const hipError_t e = w4a16::launch_fp8(a);
+    if (e != hipSuccess) return W4A16_ERR_HIP;
+  }
+  if (dw) {
+    const Fp8ColumnsLayout l = fp8_columns_layout(pitch, w4a16::fp8_blocks(M), K, N);
+    hipError_t e = fp8_dw_operands(dy, x, M, K, N, act, ws, l, pitch, nullptr, nullptr, s);
+    if (e == hipSuccess) e = w4a16::launch_fp8(fp8_dw_args(ws, l, pitch, K, N, dw, s));
+    if (e != hipSuccess) return W4A16_ERR_HIP;
+  }
+  return W4A16_OK;
+}
+
+// rows of the sorted batch's tiles, each of 128
+static size_t fp8_grouped_depth(const w4a16::RouteLayout& r) {
+  return (size_t)w4a16::tile_bound(r.S, r.E, w4a16::kTileLists - 1) * 128;
+}
+
+size_t w4a16_fp8_grouped_backward_workspace_bytes(int tokens, int topk, int groups, int K, int N) {
+  if (check_route(tokens, topk, groups) != W4A16_OK || tokens == 0) return 0;
+  const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
+  const size_t depth = fp8_grouped_depth(r);
+  if (check_fp8_backward(r.S, depth, K, N) != W4A16_OK) return 0;
+  return fp8_backward_bytes(r.S, K, N, depth, depth / 128);
+}
+
+w4a16_status w4a16_gemm_fp8_grouped_backward(const void* dy, const void* x, const int32_t* plan, int tokens,
+                                             int topk, int groups, int K, int N, w4a16_dtype act,
+                                             const uint8_t* codes_t, const float* scales_t, void* dx,
+                                             float* dw, void* workspace, size_t workspace_bytes,
+                                             void* stream) {
+  w4a16_status st = check_route(tokens, topk, groups);
+  if (st != W4A16_OK) return st;
+  const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
+  const size_t depth = fp8_grouped_depth(r);
+  st = check_fp8_backward(r.S, depth, K, N);
+  if (st != W4A16_OK) return st;
+  if (!w4a16::fp8_grouped_fits(r, K, N, false)) return W4A16_ERR_UNSUPPORTED;
+  if (!plan || !aligned(plan, 256)) return W4A16_ERR_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (tokens == 0) {  // the plan's offsets are zeros: every group's product has no depth
+    if (!is_act(act) || (dw && !aligned(dw, 16))) return W4A16_ERR_ARG;
+    if (!dw) return W4A16_OK;
+    return from_hip(w4a16::launch_fp8_by_group(fp8_dw_args(nullptr, Fp8ColumnsLayout{}, 0, K, N, dw, s), r, plan));
+  }
+  st = check_fp8_backward_pointers(dy, x, act, codes_t, scales_t, dx, dw, workspace, workspace_bytes,
+                                   w4a16_fp8_grouped_backward_workspace_bytes(tokens, topk, groups, K, N));
+  if (st != W4A16_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  if (dx) {
+    w4a16::Fp8Args a{};
+    a.M = r.S;
+    st = fp8_operands(a, dy, act, nullptr, r.S, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream);
+    if (st != W4A16_OK) return st;
+    const hipError_t e = w4a16::launch_fp8_grouped(a, r, plan, false);
+    if (e != hipSuccess) return W4A16_ERR_HIP;
+  }
+  if (dw) {
+    const Fp8ColumnsLayout l = fp8_columns_layout(depth, depth / 128, K, N);
+    hipError_t e = fp8_dw_operands(dy, x, r.S, K, N, act, ws, l, depth, &r, plan, s);
+    if (e == hipSuccess) e = w4a16::launch_fp8_by_group(fp8_dw_args(ws, l, depth, K, N, dw, s), r, plan);
+    if (e != hipSuccess) return W4A16_ERR_HIP;
+  }
+  return W4A16_OK;
 }
 
 w4a16_status w4a16_read_probe(const void* buf, size_t bytes, uint32_t* sink, void* stream) {

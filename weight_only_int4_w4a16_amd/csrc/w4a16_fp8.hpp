@@ -1,0 +1,115 @@
+// w4a16_fp8.hpp - 8-bit floating point operators (e4m3 codes with a scale for each 128 values or block of
+// 128 x 128): internal launchers, and what their kernels share.
+//
+// A scale is s = max|v| / 448 (448 the largest e4m3 value), at least 2^-126, and a code RN_e4m3(RN_f32(v / s)): two
+// correctly rounded 32-bit steps and one to 8 bits, so that codes are reproducible decisions. A group that holds
+// an infinity or a NaN becomes NaN throughout.
+//
+// Scales of rows lie by blocks of k: scales[kb][row], so that the rows of a tile read one block's scales as
+// consecutive words.
+#pragma once
+
+#include "w4a16_device.hpp"
+#include "w4a16_routed.hpp"
+
+namespace w4a16 {
+
+constexpr float kE4M3Most = 448.0f;
+constexpr float kLeastScale = 0x1p-126f;
+constexpr int kE4M3 = 3;  // as w4a16_dtype: codes with scales
+
+// One product out[m][n] = sum over k blocks of (scale of x's row m) (scale of w's block or row n) (codes of row m) .
+// (codes of row n). Pointers of grouped products are to the first group's.
+struct Fp8Args {
+  const uint8_t* x;   // codes [M][ldk]
+  const float* xs;    // scales [KB][xs_ld]
+  const uint8_t* w;   // codes [N][ldk] (swiglu: 2 N rows, gate first)
+  const float* ws;    // block scales [ceil(N / 128)][KB] (swiglu: each half's blocks), or with w_rows [KB][N]
+  bool w_rows;
+  int M, N, K;        // N: columns of out
+  int ldk;            // bytes from one row of codes to the next
+  int xs_ld;          // x scales of one block of k
+  bool glu;
+  void* out;
+  int out_dtype;      // 0 fp16, 1 bf16, 2 fp32, 3 e4m3 (glu: codes with scales)
+  float* out_scales;  // [ceil(N / 128)][M], for e4m3
+  float* scratch;     // fp32 h [M][N] where a kernel cannot quantize it by itself
+  hipStream_t stream;
+};
+
+inline size_t fp8_blocks(int n) { return ((size_t)n + 127) / 128; }
+inline int ceil16(int n) { return (n + 15) & ~15; }
+
+// rows: codes [M][K], scales [ceil(K / 128)][M]; K % 16 == 0
+hipError_t launch_fp8_rows(const void* x, int M, int K, int dtype, uint8_t* codes, float* scales, hipStream_t s);
+// columns: codes [K][pitch] transposed, scales [row tiles][K]; a tile is 128 rows, or with a plan (r) one of
+// its 128-row tiles (those past its list are left alone; pitch: 128 times the list's bound)
+hipError_t launch_fp8_columns(const void* x, int M, int K, int dtype, uint8_t* codes, size_t pitch, float* scales,
+                              const RouteLayout* r, const int32_t* plan, hipStream_t s);
+// blocks of 128 x 128: codes [N][K], scales [ceil(N / 128)][ceil(K / 128)]; codes_t, scales_t the same transposed, or NULL
+hipError_t launch_fp8_weight(const void* w, int N, int K, int dtype, uint8_t* codes, float* scales, uint8_t* codes_t,
+                             float* scales_t, hipStream_t s);
+
+hipError_t launch_fp8(const Fp8Args& a);
+// the rows and weights of a plan's groups; gather: x holds the tokens' rows
+hipError_t launch_fp8_grouped(const Fp8Args& a, const RouteLayout& r, const int32_t* plan, bool gather);
+// out[e][m][n] over the 128-row tiles of group e, which are the blocks of k (both operands scaled by rows)
+hipError_t launch_fp8_by_group(const Fp8Args& a, const RouteLayout& r, const int32_t* plan);
+
+// bytes of Fp8Args::scratch that a launch needs (0: none)
+size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype);
+size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int K, bool glu, int out_dtype);
+bool fp8_fits(int M, int N, int K, bool glu);  // whether launches can index it
+bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu);
+const char* fp8_name(int M, int N, int K, bool glu);
+
+// ---- device side ----
+
+// The scale of a group whose largest magnitude has these bits
+__device__ __forceinline__ float fp8_scale(uint32_t amax) {
+  if (amax >= 0x7F800000u) return __builtin_nanf("");
+  const float s = __builtin_bit_cast(float, amax) / kE4M3Most;
+  return s < kLeastScale ? kLeastScale : s;
+}
+
+// Division by a scale, correctly rounded: with r = RN(1 / s), two steps of q += r (v - q s) after q = v r
+// give RN(v / s) (the remainders are exact). Scales under 2^-60 are taken 2^64 times as large, and so are
+// their values, so that no remainder reaches the subnormal numbers where the quotient's code is not 0.
+struct Fp8Divisor {
+  float s, r, up;
+};
+__device__ __forceinline__ Fp8Divisor fp8_divisor(float scale) {
+  Fp8Divisor d;
+  d.up = scale < 0x1p-60f ? 0x1p64f : 1.0f;
+  d.s = scale * d.up;
+  d.r = 1.0f / d.s;
+  return d;
+}
+__device__ __forceinline__ float fp8_quotient(float v, const Fp8Divisor& d) {
+  v *= d.up;
+  float q = v * d.r;
+  q = __builtin_fmaf(__builtin_fmaf(-q, d.s, v), d.r, q);
+  q = __builtin_fmaf(__builtin_fmaf(-q, d.s, v), d.r, q);
+  return __builtin_copysignf(q, v);  // the steps make +0 of -0
+}
+
+// four values as codes, one a byte
+__device__ __forceinline__ uint32_t fp8_pack(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+
+// v of the lane that a DPP control names
+template <int CTRL>
+__device__ __forceinline__ uint32_t fp8_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+// the largest of each sixteen lanes, in all of them (rotations by 8, 4, 2, 1)
+__device__ __forceinline__ uint32_t max_of_16_lanes(uint32_t v) {
+  v = max(v, fp8_dpp<0x128>(v));
+  v = max(v, fp8_dpp<0x124>(v));
+  v = max(v, fp8_dpp<0x122>(v));
+  return max(v, fp8_dpp<0x121>(v));
+}
+
+}  // namespace w4a16

@@ -1,0 +1,361 @@
+// w4a16_fp8_quantize.hip - values of 16 or 32 bits to e4m3 codes with a scale for each 128 (or block of 128 x 128).
+//
+// All forms read every value once and write its code once; they are bound by those bytes (at decode sizes by
+// one launch). The largest magnitude of a group is taken from the bits of |v|, which order as the values do and put
+// infinities and NaNs above them.
+#include <type_traits>
+
+#include "w4a16_fp8.hpp"
+
+namespace w4a16 {
+
+namespace {
+
+typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
+// 16 bytes at any address that its elements may have
+typedef u4_t u4_any_t __attribute__((aligned(2)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+typedef u2_t u2_any_t __attribute__((aligned(1)));
+typedef u4_t u4_byte_t __attribute__((aligned(1)));
+
+// types of values, as w4a16_dtype
+template <int DT>
+struct Eight;  // eight consecutive values of a row
+
+template <int DT>
+struct Eight16 {
+  u4_t v;
+  __device__ __forceinline__ void clear() { v = u4_t{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const void* row, size_t i) {
+    v = *reinterpret_cast<const u4_any_t*>(static_cast<const uint16_t*>(row) + i);
+  }
+  __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
+    clear();
+    for (int j = 0; j < 8; ++j)
+      if (j < n) v[j >> 1] |= (uint32_t)static_cast<const uint16_t*>(row)[i + j] << (16 * (j & 1));
+  }
+  __device__ __forceinline__ float value(int j) const {
+    const uint16_t b = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+    if constexpr (DT == 0) return (float)__builtin_bit_cast(_Float16, b);
+    else return __builtin_bit_cast(float, (uint32_t)b << 16);
+  }
+  // magnitudes, two a word
+  static constexpr int kWords = 4;
+  __device__ __forceinline__ uint32_t magnitude(int w) const { return v[w] & 0x7FFF7FFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, a), __builtin_bit_cast(us2_t, b)));
+  }
+  // the bits of a magnitude as a 32-bit float's: of value h of a word, or of the word's largest
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t w, int h) {
+    const uint16_t b = (uint16_t)(w >> (16 * h));
+    if constexpr (DT == 0) return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, b));
+    else return (uint32_t)b << 16;
+  }
+  static __device__ __forceinline__ uint32_t largest_bits(uint32_t w) { return float_bits(max(w & 0xFFFFu, w >> 16), 0); }
+  static constexpr int kPerWord = 2;
+};
+template <>
+struct Eight<0> : Eight16<0> {};
+template <>
+struct Eight<1> : Eight16<1> {};
+template <>
+struct Eight<2> {
+  float v[8];
+  __device__ __forceinline__ void clear() {
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  }
+  __device__ __forceinline__ void load(const void* row, size_t i) {
+    typedef f4_t f4_any_t __attribute__((aligned(4)));
+    const float* p = static_cast<const float*>(row) + i;
+    const f4_t a = *reinterpret_cast<const f4_any_t*>(p), b = *reinterpret_cast<const f4_any_t*>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+  }
+  __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? static_cast<const float*>(row)[i + j] : 0.f;
+  }
+  __device__ __forceinline__ float value(int j) const { return v[j]; }
+  static constexpr int kWords = 8;
+  __device__ __forceinline__ uint32_t magnitude(int w) const { return __builtin_bit_cast(uint32_t, v[w]) & 0x7FFFFFFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t w, int) { return w; }
+  static __device__ __forceinline__ uint32_t largest_bits(uint32_t w) { return w; }
+  static constexpr int kPerWord = 1;
+};
+
+template <int DT>
+constexpr size_t kValueBytes = DT == 2 ? 4 : 2;
+
+// ---- rows ----
+// Sixteen lanes hold a group of 128, eight values each; a wave takes four groups of R rows, all of whose loads are
+// in flight at once, and writes a block's scales of its rows as consecutive words. Four waves take rows below each other.
+constexpr int kRowWaves = 4;
+template <int DT, int R>
+__global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(const void* __restrict__ x, int M, int K,
+                                                                  uint8_t* __restrict__ codes,
+                                                                  float* __restrict__ scales, int chunks) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int chunk = blockIdx.x % chunks;
+  const int m0 = (int)(blockIdx.x / chunks) * (kRowWaves * R) + wave * R;
+  const int kb = chunk * 4 + (lane >> 4), li = lane & 15;
+  const int k = kb * 128 + li * 8;
+  const bool in_k = k < K;  // K is a multiple of 8: a lane's values are in the row, or none
+  Eight<DT> v[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (in_k && m0 + r < M) v[r].load(x, (size_t)(m0 + r) * K + k);
+    else v[r].clear();
+  }
+  float mine = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    uint32_t w = v[r].magnitude(0);
+#pragma unroll
+    for (int i = 1; i < Eight<DT>::kWords; ++i) w = Eight<DT>::larger(w, v[r].magnitude(i));
+    const float s = fp8_scale(max_of_16_lanes(Eight<DT>::largest_bits(w)));
+    const Fp8Divisor d = fp8_divisor(s);
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = fp8_quotient(v[r].value(j), d);
+    if (in_k && m0 + r < M)
+      *reinterpret_cast<u2_t*>(codes + (size_t)(m0 + r) * K + k) =
+          u2_t{fp8_pack(q[0], q[1], q[2], q[3]), fp8_pack(q[4], q[5], q[6], q[7])};
+    if (li == r) mine = s;
+  }
+  if (li < R && m0 + li < M && kb * 128 < K) scales[(size_t)kb * M + m0 + li] = mine;
+}
+
+// ---- columns, and blocks of a weight ----
+// A workgroup takes 128 x 128 values, a thread eight rows by eight columns of them. Column scales: the threads above
+// each other join their maxima through LDS; block scales: all threads do. The transposed codes go through LDS, eight
+// rows of a column (8 bytes) a store: column c's store t lies at slot t ^ (c / 8), so that the sixteen threads side by side
+// use every bank once, and leave as whole 16-byte pieces of a column.
+constexpr int kTileThreads = 256;
+
+struct Fp8TileParams {
+  const void* x;
+  int M, K;
+  uint8_t* codes;    // as they lie (blocks only)
+  float* scales;
+  uint8_t* codes_t;  // transposed, or NULL
+  float* scales_t;   // blocks only
+  size_t pitch;      // bytes between columns of codes_t
+  int limit;         // columns of codes_t that are written: a tile's from 128 (its number) up to here
+  int tiles_k;
+  const int32_t* list;  // the plan's 128-row tiles, or NULL
+  int groups;
+};
+
+template <int DT, bool BLOCKS>
+__global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p) {
+  typedef Eight<DT> E;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[128 * 128];
+  uint32_t* const red = reinterpret_cast<uint32_t*>(lds);  // [16][16 * kWords], before the codes
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tk = blockIdx.x % p.tiles_k, tm = blockIdx.x / p.tiles_k;
+  int row0 = tm * 128, end = p.M;
+  if (p.list) {
+    const int4 t = *reinterpret_cast<const int4*>(p.list + 4 + 4 * tm);
+    if (tm >= p.list[0] || t.x >= p.groups) return;
+    row0 = t.y;
+    end = t.z;
+  }
+  const int c = tk * 128 + tx * 8, some = p.K - c;
+  E v[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int row = row0 + ty * 8 + r;
+    if (row < end && some >= 8) v[r].load(p.x, (size_t)row * p.K + c);
+    else v[r].clear();
+  }
+  if (some > 0 && some < 8) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int row = row0 + ty * 8 + r;
+      if (row < end) v[r].load_some(p.x, (size_t)row * p.K + c, some);
+    }
+  }
+  constexpr int WORDS = E::kWords;
+  uint32_t most[WORDS];
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) {
+    most[w] = v[0].magnitude(w);
+#pragma unroll
+    for (int r = 1; r < 8; ++r) most[w] = E::larger(most[w], v[r].magnitude(w));
+  }
+  Fp8Divisor d[BLOCKS ? 1 : 8];
+  if constexpr (BLOCKS) {
+    uint32_t one = most[0];
+#pragma unroll
+    for (int w = 1; w < WORDS; ++w) one = E::larger(one, most[w]);
+    one = max_of_16_lanes(E::largest_bits(one));
+    if (tx == 0) red[ty] = one;
+    __syncthreads();
+    one = red[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) one = max(one, red[i]);
+    const float s = fp8_scale(one);
+    d[0] = fp8_divisor(s);
+    if (threadIdx.x == 0) {
+      const int tiles_m = (p.M + 127) / 128;
+      p.scales[(size_t)tm * p.tiles_k + tk] = s;
+      if (p.scales_t) p.scales_t[(size_t)tk * tiles_m + tm] = s;
+    }
+  } else {
+#pragma unroll
+    for (int w = 0; w < WORDS; w += 4)
+      *reinterpret_cast<u4_t*>(red + ty * 16 * WORDS + tx * WORDS + w) = u4_t{most[w], most[w + 1], most[w + 2], most[w + 3]};
+    __syncthreads();
+#pragma unroll
+    for (int i = 1; i < 16; ++i)
+#pragma unroll
+      for (int w = 0; w < WORDS; w += 4) {
+        const u4_t o = *reinterpret_cast<const u4_t*>(red + ((ty + i) & 15) * 16 * WORDS + tx * WORDS + w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most[w + j] = E::larger(most[w + j], o[j]);
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = fp8_scale(E::float_bits(most[j / E::kPerWord], j % E::kPerWord));
+      d[j] = fp8_divisor(s);
+      if (ty == 0 && j < some) p.scales[(size_t)tm * p.K + c + j] = s;
+    }
+  }
+  __syncthreads();
+  uint32_t lo[8], hi[8];  // a column's eight codes
+  if constexpr (BLOCKS) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {  // a row's eight codes
+      float q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = fp8_quotient(v[r].value(j), d[0]);
+      const int row = row0 + ty * 8 + r;
+      lo[r] = fp8_pack(q[0], q[1], q[2], q[3]);
+      hi[r] = fp8_pack(q[4], q[5], q[6], q[7]);
+      if (row < end && some > 0) {
+        uint8_t* const dst = p.codes + (size_t)row * p.K + c;
+        if (some >= 8) {
+          *reinterpret_cast<u2_any_t*>(dst) = u2_t{lo[r], hi[r]};
+        } else {
+          for (int j = 0; j < some; ++j) dst[j] = (uint8_t)((j < 4 ? lo[r] : hi[r]) >> (8 * (j & 3)));
+        }
+      }
+    }
+    if (!p.codes_t) return;
+    // rows of codes to columns: two 4 x 4 byte transposes for each half of the rows
+    uint32_t tlo[8], thi[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t* src = h ? hi : lo;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const uint32_t a = src[4 * part], b = src[4 * part + 1], cc = src[4 * part + 2], e = src[4 * part + 3];
+        const uint32_t ab0 = perm_b32(b, a, 0x05010400u), ab1 = perm_b32(b, a, 0x07030602u);
+        const uint32_t ce0 = perm_b32(e, cc, 0x05010400u), ce1 = perm_b32(e, cc, 0x07030602u);
+        uint32_t* dst = part ? thi : tlo;
+        dst[4 * h + 0] = perm_b32(ce0, ab0, 0x05040100u);
+        dst[4 * h + 1] = perm_b32(ce0, ab0, 0x07060302u);
+        dst[4 * h + 2] = perm_b32(ce1, ab1, 0x05040100u);
+        dst[4 * h + 3] = perm_b32(ce1, ab1, 0x07060302u);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) lo[j] = tlo[j], hi[j] = thi[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float q[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) q[r] = fp8_quotient(v[r].value(j), d[j]);
+      lo[j] = fp8_pack(q[0], q[1], q[2], q[3]);
+      hi[j] = fp8_pack(q[4], q[5], q[6], q[7]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<u2_t*>(lds + (tx * 8 + j) * 128 + ((ty ^ tx) & 15) * 8) = u2_t{lo[j], hi[j]};
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 128 * 8 / kTileThreads; ++i) {
+    const int piece = threadIdx.x + i * kTileThreads;
+    const int col = piece >> 3, part = piece & 7, cx = col >> 3;
+    const u4_t q = *reinterpret_cast<const u4_t*>(lds + col * 128 + ((part ^ (cx >> 1)) & 7) * 16);
+    const u4_t o = cx & 1 ? u4_t{q[2], q[3], q[0], q[1]} : q;
+    const int at = tm * 128 + part * 16, n = p.limit - at;
+    if (tk * 128 + col >= p.K || n <= 0) continue;
+    uint8_t* const dst = p.codes_t + (size_t)(tk * 128 + col) * p.pitch + at;
+    if (n >= 16) {
+      *reinterpret_cast<u4_byte_t*>(dst) = o;
+    } else {
+      for (int j = 0; j < n; ++j) dst[j] = (uint8_t)(o[j >> 2] >> (8 * (j & 3)));
+    }
+  }
+}
+
+template <int DT>
+void launch_rows(const void* x, int M, int K, uint8_t* codes, float* scales, hipStream_t s) {
+  const int chunks = (int)((fp8_blocks(K) + 3) / 4);
+  const auto grid = [&](int R) { return dim3((unsigned)((size_t)chunks * ((M + kRowWaves * R - 1) / (kRowWaves * R)))); };
+  // eight rows a wave where that still fills the chip, else one
+  if ((size_t)M * chunks >= 32768)
+    hipLaunchKernelGGL((fp8_rows_kernel<DT, 8>), grid(8), dim3(64 * kRowWaves), 0, s, x, M, K, codes, scales, chunks);
+  else
+    hipLaunchKernelGGL((fp8_rows_kernel<DT, 1>), grid(1), dim3(64 * kRowWaves), 0, s, x, M, K, codes, scales, chunks);
+}
+
+template <bool BLOCKS>
+void launch_tiles(const Fp8TileParams& p, int tiles_m, int dtype, hipStream_t s) {
+  const dim3 grid((unsigned)((size_t)tiles_m * p.tiles_k)), threads(kTileThreads);
+  if (dtype == 0) hipLaunchKernelGGL((fp8_tile_kernel<0, BLOCKS>), grid, threads, 0, s, p);
+  else if (dtype == 1) hipLaunchKernelGGL((fp8_tile_kernel<1, BLOCKS>), grid, threads, 0, s, p);
+  else hipLaunchKernelGGL((fp8_tile_kernel<2, BLOCKS>), grid, threads, 0, s, p);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_rows(const void* x, int M, int K, int dtype, uint8_t* codes, float* scales, hipStream_t s) {
+  if (dtype == 0) launch_rows<0>(x, M, K, codes, scales, s);
+  else if (dtype == 1) launch_rows<1>(x, M, K, codes, scales, s);
+  else launch_rows<2>(x, M, K, codes, scales, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_columns(const void* x, int M, int K, int dtype, uint8_t* codes, size_t pitch, float* scales,
+                              const RouteLayout* r, const int32_t* plan, hipStream_t s) {
+  Fp8TileParams p{};
+  p.x = x;
+  p.M = M;
+  p.K = K;
+  p.scales = scales;
+  p.codes_t = codes;
+  p.pitch = pitch;
+  p.limit = (int)pitch;
+  p.tiles_k = (int)fp8_blocks(K);
+  int tiles = (int)fp8_blocks(M);
+  if (r) {
+    p.list = plan + r->tiles[kTileLists - 1];
+    p.groups = r->E;
+    tiles = tile_bound(r->S, r->E, kTileLists - 1);
+  }
+  launch_tiles<false>(p, tiles, dtype, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_weight(const void* w, int N, int K, int dtype, uint8_t* codes, float* scales, uint8_t* codes_t,
+                             float* scales_t, hipStream_t s) {
+  Fp8TileParams p{};
+  p.x = w;
+  p.M = N;
+  p.K = K;
+  p.codes = codes;
+  p.scales = scales;
+  p.codes_t = codes_t;
+  p.scales_t = scales_t;
+  p.pitch = (size_t)N;
+  p.limit = N;
+  p.tiles_k = (int)fp8_blocks(K);
+  launch_tiles<true>(p, (int)fp8_blocks(N), dtype, s);
+  return hipGetLastError();
+}
+
+}  // namespace w4a16
