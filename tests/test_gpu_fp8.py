@@ -271,7 +271,6 @@ def test_swiglu_on_large_tiles(M, K, N2):
     """Enough tiles of 256 x 256 to fill the chip: h is quantized where it is made."""
     import weight_only_int4_w4a16_amd as w4
     torch = torch_mod()
-    assert w4.fp8_kernel_name(M, K, N2, True) == "w4a16_fp8_256x256"
     _announce(f"gemm_fp8_swiglu {M}x{K}x{N2}, large tiles")
     x, xv = _rows((M, K), "bf16", M)
     codes, scales, wv = _weight((), N2, K, K, halves=2)
@@ -286,15 +285,17 @@ def test_swiglu_on_large_tiles(M, K, N2):
     _within(h16[at].cpu().double().numpy(), h, _stored(h, dh, "bf16"), "h")
 
 
-@pytest.mark.parametrize("M,K,N", [(2048, 256, 4100), (4000, 400, 2056)])
+LARGE = [(2048, 256, 4100), (4000, 400, 2056), (1000, 640, 1300), (3000, 144, 3000), (4096, 512, 9000), (4100, 256, 5000), (530, 4096, 520), (500, 512, 9000), (250, 4096, 9000)]
+
+
+@pytest.mark.parametrize("M,K,N", LARGE)
 def test_products_on_large_tiles(M, K, N):
     import weight_only_int4_w4a16_amd as w4
     torch = torch_mod()
-    assert w4.fp8_kernel_name(M, K, N) == "w4a16_fp8_256x256"
-    _announce(f"gemm_fp8 {M}x{K}x{N}, large tiles")
+    _announce(f"gemm_fp8 {M}x{K}x{N}, {w4.fp8_kernel_name(M, K, N)}")
     x, xv = _rows((M, K), "f16", M)
     codes, scales, wv = _weight((), N, K, K)
-    some = np.unique(np.concatenate([np.arange(0, M, 31), [255, 256, M - 1]]))
+    some = np.unique(np.concatenate([np.arange(0, M, 31), [127, 128, M - 1]]))
     xv = F.rows_value(*F.quantize_rows(xv[some]))
     ref = F.gemm_fp8_ref(xv, wv)
     at = torch.from_numpy(some).cuda()
@@ -302,6 +303,14 @@ def test_products_on_large_tiles(M, K, N):
     _within(y[at].cpu().double().numpy(), ref, _stored(ref, _sum_bound(xv, wv, "f16"), "f16"), "16-bit out")
     y = w4.gemm_fp8(x, codes, scales, out_dtype=torch.float32)
     _within(y[at].cpu().double().numpy(), ref, _stored(ref, _sum_bound(xv, wv, "f32"), "f32"), "fp32 out")
+
+
+def test_every_kernel_is_reached():
+    """The shapes of these tests run on tiles of each height, with k whole and in slices."""
+    import weight_only_int4_w4a16_amd as w4
+    names = {w4.fp8_kernel_name(M, K, N) for M, K, N in PRODUCTS + LARGE}
+    assert names >= {"w4a16_fp8_16", "w4a16_fp8_32x128", "w4a16_fp8_64x128", "w4a16_fp8_128x256", "w4a16_fp8_256x256"}, names
+    assert {n.split("_")[2] for n in names if n.endswith("splitk")} >= {"32x128", "64x128"}, names
 
 
 def test_not_finite_rows():

@@ -22,9 +22,10 @@ SOURCES = ["w4a16_api.hip", "w4a16_pack.hip", "w4a16_decode.hip", "w4a16_tiled.h
            "w4a16_skinny.hip", "w4a16_w4a8.hip", "w4a16_probe.hip",
            "w4a16_route.hip", "w4a16_dispatch.hip", "w4a16_grouped.hip", "w4a16_grouped_f16.hip",
            "w4a16_grouped_bf16.hip", "w4a16_grouped_large.hip", "w4a16_lora.hip",
-           "w4a16_fp8.hip", "w4a16_fp8_quantize.hip"] + [
+           "w4a16_fp8.hip", "w4a16_fp8_quantize.hip", "w4a16_fp8_stream.hip"] + [
     f"w4a16_decode_{a}_{f}.hip" for a in ("f16", "bf16") for f in ("asym", "sym", "nf4")] + [
-    f"w4a16_tiled_{t}.hip" for t in ("large", "small", "smalldeep", "small2", "med")]
+    f"w4a16_tiled_{t}.hip" for t in ("large", "small", "smalldeep", "small2", "med")] + [
+    f"w4a16_fp8_{t}.hip" for t in ("dense", "glu", "grouped", "grouped_glu", "columns")]
 ARCH = os.environ.get("W4A16_ARCH", "gfx950")
 
 

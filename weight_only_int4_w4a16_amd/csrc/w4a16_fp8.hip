@@ -1,24 +1,181 @@
 // w4a16_fp8.hip - which kernel takes a product of e4m3 codes, and its launch geometry.
-#include "w4a16_fp8_tile.hpp"
+#include <stdlib.h>
+
+#include "w4a16_fp8_stream.hpp"
 
 namespace w4a16 {
 
 using namespace fp8;
 
+namespace fp8 {
+// The kernels' instantiations, one source for each kind of product (w4a16_fp8_{dense,glu,grouped,grouped_glu,columns}.hip)
+#define W4A16_FP8_EXTERN(NAME) hipError_t NAME(const TileParams& p, int kind, bool exact, unsigned grid, int gy, hipStream_t s)
+W4A16_FP8_EXTERN(launch_dense);
+W4A16_FP8_EXTERN(launch_glu);
+W4A16_FP8_EXTERN(launch_grouped_plain);
+W4A16_FP8_EXTERN(launch_grouped_glu);
+W4A16_FP8_EXTERN(launch_columns);
+W4A16_FP8_EXTERN(launch_by_group);
+hipError_t launch_stream(const StreamParams& p, int NT, int XC, int W, bool glu, bool grouped, unsigned grid, hipStream_t s);
+}  // namespace fp8
+
 namespace {
 
-template <class T, bool GLU, bool WROWS, int MODE>
-hipError_t launch_tile(TileParams p, int gy, hipStream_t s) {
-  const unsigned grid = (unsigned)((size_t)p.tiles_m * p.tiles_n);
-  const dim3 blocks(grid, gy), threads(T::kThreads);
-  if constexpr (WROWS) {  // a weight's gradient: fp32
-    hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, true, MODE, true>), blocks, threads, T::kLdsBytes, s, p);
-  } else if (p.out_dtype >= 2) {
-    hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, false, MODE, true>), blocks, threads, T::kLdsBytes, s, p);
-  } else {
-    hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, false, MODE, false>), blocks, threads, T::kLdsBytes, s, p);
+// ---- after a product: sums of its slices of k, and h to codes ----
+// Sixteen lanes take 128 columns of a row, eight each; the partial sums [S][M][width] are added in slice order. GLU: width is
+// 2 N, gate columns first. Bound by the partial sums' bytes.
+template <bool GLU>
+__global__ __launch_bounds__(256) void fp8_finish_kernel(const float* __restrict__ part, int S, int M, int N, void* out,
+                                                         int out_dtype, float* __restrict__ out_scales, int chunks) {
+  const int lane = threadIdx.x & 63, item = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int m = item / chunks, n = (item - m * chunks) * 512 + lane * 8;
+  if (m >= M) return;
+  const size_t width = GLU ? 2 * (size_t)N : N, slice = (size_t)M * width;
+  const int some = N - n;
+  float v[8], u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+  auto add = [&](const float* row, float (&sum)[8]) __attribute__((always_inline)) {
+    if (some >= 8 && N % 4 == 0) {
+      const f4_t a = *reinterpret_cast<const f4_t*>(row), b = *reinterpret_cast<const f4_t*>(row + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] += a[j], sum[4 + j] += b[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < some) sum[j] += row[j];
+    }
+  };
+  if (some > 0)
+    for (int s = 0; s < S; ++s) {
+      const float* row = part + s * slice + (size_t)m * width + n;
+      add(row, v);
+      if constexpr (GLU) add(row + N, u);
+    }
+  if constexpr (GLU) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] / (1.0f + __expf(-v[j])) * u[j];
   }
+  const size_t at = (size_t)m * N + n;
+  if (out_dtype == kE4M3) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = max(most, j < some ? __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu : 0u);
+    const float sc = fp8_scale(max_of_16_lanes(most));
+    const Fp8Divisor d = fp8_divisor(sc);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fp8_quotient(v[j], d);
+    if (some > 0) {  // N is a multiple of 16
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + at) = uint2{fp8_pack(v[0], v[1], v[2], v[3]), fp8_pack(v[4], v[5], v[6], v[7])};
+      if ((lane & 15) == 0) out_scales[(size_t)(n >> 7) * M + m] = sc;
+    }
+  } else if (some >= 8 && N % 8 == 0 && out_dtype != 2) {
+    if (out_dtype == 0) {
+      h8_t o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (_Float16)v[j];
+      *reinterpret_cast<h8_t*>(static_cast<_Float16*>(out) + at) = o;
+    } else {
+      b8_t o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
+      *reinterpret_cast<b8_t*>(static_cast<__bf16*>(out) + at) = o;
+    }
+  } else if (some >= 8 && N % 4 == 0) {
+    *reinterpret_cast<f4_t*>(static_cast<float*>(out) + at) = f4_t{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f4_t*>(static_cast<float*>(out) + at + 4) = f4_t{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < some) store_out(out, at + j, v[j], out_dtype);
+  }
+}
+
+hipError_t launch_finish(const float* part, int S, int M, int N, bool glu, void* out, int out_dtype, float* out_scales,
+                         hipStream_t s) {
+  const int chunks = ceil_div(N, 512);
+  const dim3 grid((unsigned)(((size_t)M * chunks + 3) / 4));
+  if (glu) hipLaunchKernelGGL(fp8_finish_kernel<true>, grid, dim3(256), 0, s, part, S, M, N, out, out_dtype, out_scales, chunks);
+  else hipLaunchKernelGGL(fp8_finish_kernel<false>, grid, dim3(256), 0, s, part, S, M, N, out, out_dtype, out_scales, chunks);
   return hipGetLastError();
+}
+
+// ---- which kernel ----
+
+constexpr int kRows[] = {16, 32, 64, 128, 256};  // rows of x of a kind's tile (STREAM, LOW, MID, HALF, WHOLE)
+constexpr int kCols[] = {16, 128, 128, 256, 256};
+
+// W4A16_FP8_ROWS=16|32|64|128|256 pins the row tile (for benchmarking one against another); read once
+// per process.
+int forced_kind() {
+  static const int forced = [] {
+    const char* v = getenv("W4A16_FP8_ROWS");
+    if (!v) return -1;
+    for (int j = 0; j < 5; ++j)
+      if (atoi(v) == kRows[j]) return j;
+    return -1;
+  }();
+  return forced;
+}
+
+struct Plan {
+  int kind;
+  int S;  // slices of k, added by a second kernel
+};
+
+// us of a product on tiles of a kind with k in S slices: 3 and, for each round of workgroups, the blocks of k by what
+// one takes, and 1.5 more a round; at least the weight's bytes at 5.6 TB/s; and the slices' sums, written and read at
+// 4 TB/s with another launch. What a block takes was measured on 1024x4096 to 8192x32768, 24 to 2048 rows, S 1 to
+// 12, cold weights: `one` with few workgroups, `full` with one on every compute unit, `pair` with two on each (the kinds
+// of which two fit), or in later rounds.
+struct BlockTimes {
+  double one, full, pair;
+};
+constexpr BlockTimes kBlock[2][5] = {{{}, {0.42, 0.52, 0.85}, {0.50, 0.66, 0.83}, {0.82, 0.95, 1.02}, {1.60, 1.68, 1.70}},
+                                     {{}, {0.56, 0.66, 0.95}, {0.78, 0.92, 1.15}, {1.60, 1.75, 1.82}, {}}};
+// whether a product's last round of tiles runs as halves of them, all at once
+bool halved(int kind, int S, long long tiles, long long cus) {
+  const long long left = tiles % cus;
+  return kind == WHOLE && S == 1 && tiles > cus && left && 2 * left <= cus;
+}
+double model_us(int kind, int S, int M, int N, int KB, bool exact, long long cus) {
+  const long long wgs = (long long)ceil_div(M, kRows[kind]) * ceil_div(N, kCols[kind]) * S;
+  const int steps = ceil_div(KB, S);
+  const BlockTimes& b = kBlock[exact][kind];
+  const long long slots = kind <= MID ? 2 * cus : cus;
+  double t = 3;
+  if (wgs <= cus) {
+    t += steps * (b.one + (b.full - b.one) * wgs / cus);
+  } else {
+    double rounds = (double)((wgs + slots - 1) / slots);
+    if (halved(kind, S, wgs, cus)) rounds -= 0.4;
+    t += rounds * steps * b.pair + 1.5 * (rounds - 1);
+  }
+  const double memory = 3 + (double)N * KB * 128 / 5.6e6;
+  if (t < memory) t = memory;
+  if (S > 1) t += 2.5 + 2.0 * S * M * N * 4 / 4e6;
+  return t;
+}
+
+Plan choose(int M, int N, int K, bool glu, bool exact) {
+  // N: columns that are multiplied (GLU: both halves)
+  const int KB = (int)fp8_blocks(K);
+  if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE)) return Plan{forced_kind(), 1};
+  if (M <= 16) return Plan{STREAM, 1};
+  const long long cus = device_cu_count();
+  const bool sliced = !glu || (N / 2) % 128 == 0;  // sums of both halves as plain columns: their blocks follow each other
+  Plan best{MID, 1};
+  double least = 1e30;
+  for (int kind = LOW; kind <= (exact ? HALF : WHOLE); ++kind)
+    for (int S = 1; S <= (sliced ? 12 : 1); ++S) {
+      if (S > 1 && KB < 4 * S) break;
+      const double t = model_us(kind, S, M, N, KB, exact, cus);
+      if (t < least * 0.999) {
+        least = t;
+        best = Plan{kind, S};
+      }
+    }
+  return best;
 }
 
 TileParams tile_params(const Fp8Args& a) {
@@ -33,7 +190,7 @@ TileParams tile_params(const Fp8Args& a) {
   p.M = a.M;
   p.N = a.N;
   p.K = a.K;
-  p.KB = (int)fp8_blocks(a.K);
+  p.KB = p.slice = (int)fp8_blocks(a.K);
   p.ldk = a.ldk;
   p.xs_ld = a.xs_ld;
   p.up_blocks = (int)fp8_blocks(a.N);
@@ -41,16 +198,57 @@ TileParams tile_params(const Fp8Args& a) {
   return p;
 }
 
-template <class T>
-void set_tiles(TileParams& p, bool glu, int tiles_m) {
+void set_tiles(TileParams& p, int kind, bool glu, int tiles_m) {
   p.tiles_m = tiles_m;
-  p.tiles_n = ceil_div(p.N, glu ? T::kBN / 2 : T::kBN);
+  p.tiles_n = ceil_div(p.N, glu ? kCols[kind] / 2 : kCols[kind]);
 }
 
-// Whether the 256 x 256 tiles fill the chip
-bool large_fills(long long rows_tiles, int N, bool glu) {
-  return rows_tiles * ceil_div(N, glu ? 128 : 256) * 2 >= device_cu_count();
+// Sixteen-row products: eight waves share k where the workgroups are few (up to two a compute unit), else four;
+// 32 columns a workgroup where 16 would make many, and for more than eight rows over a deep K, whose x no
+// cache near the compute unit holds. us by (columns, waves), 16/4, 16/8, 32/4, 32/8, one row and sixteen rows:
+//   4096x4096   8.5, 6.2, 9.7, 7.3;   8.2, 6.2, 10.4, 7.9    8192x10240  18.6, 19.2, 20.7, 24.2;  20.1, 22.1, 22.4, 25.3
+//   4096x14336  13.6, 15.1, 13.8, 16.9;  15.7, 17.0, 14.7, 17.8    14336x4096  24.8, 15.3, 28.5, 18.0;  23.5, 14.8, 30.7, 19.7
+//   28672x8192  53.4, 42.0, 57.6, 42.0;  51.1, 50.0, 64.1, 42.8
+void stream_shape(int M, int N, int K, bool glu, long long cus, long long tiles_m, int& NT, int& W) {
+  const long long tiles = tiles_m * ceil_div(N, 16);
+  NT = glu || tiles > 3 * cus || (M > 8 && K > 16384) ? 2 : 1;
+  W = tiles_m * ceil_div(N, glu ? 16 : 16 * NT) <= 2 * cus ? 8 : 4;
 }
+
+hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, hipStream_t s) {
+  StreamParams p{};
+  p.x = t.x;
+  p.xs = t.xs;
+  p.w = t.w;
+  p.ws = t.ws;
+  p.out = t.out;
+  p.out_dtype = t.out_dtype;
+  p.M = t.M;
+  p.N = t.N;
+  p.K = t.K;
+  p.KB = t.KB;
+  p.ldk = t.ldk;
+  p.xs_ld = t.xs_ld;
+  p.up_blocks = t.up_blocks;
+  p.groups = t.groups;
+  int NT, W;
+  p.tiles_m = grouped ? t.groups.bound : ceil_div(t.M, 16);
+  // of a grouped launch's tiles at most one a group is part-filled, and those past the list's end leave at once
+  const long long full = grouped ? (t.groups.bound + 1) / 2 : p.tiles_m;
+  stream_shape(M, t.N, t.K, glu, device_cu_count(), full, NT, W);
+  p.tiles_n = ceil_div(t.N, glu ? 8 * NT : 16 * NT);
+  p.slice = ceil_div(t.KB, W);
+  const unsigned grid = (unsigned)((size_t)p.tiles_m * p.tiles_n);
+  return launch_stream(p, NT, grouped || M > 8 ? 2 : 1, W, glu, grouped, grid, s);
+}
+
+bool grid_fits(long long tiles_m, int N, int kind, bool glu, int S) {
+  const long long cols = kind == STREAM ? 16 : kCols[kind] / (glu ? 2 : 1);
+  return tiles_m * ((N + cols - 1) / cols) * 512 * S < (1LL << 32);
+}
+
+// h of a swiglu product in e4m3 is quantized by the HALF tiles themselves (128 columns of h each); else from fp32
+bool by_finish(int kind, int S, int out_dtype) { return S > 1 || (out_dtype == kE4M3 && kind != HALF); }
 
 }  // namespace
 
@@ -60,61 +258,87 @@ bool fp8_fits(int M, int N, int K, bool glu) {
   if ((long long)K >= (1LL << 23) || wrows * K >= (1LL << 31)) return false;
   if ((long long)fp8_blocks(K) * M * 4 >= (1LL << 31) || (long long)(fp8_blocks(N) + 1) * 2 * fp8_blocks(K) * 4 >= (1LL << 31))
     return false;
-  return (long long)ceil_div(M, 128) * ceil_div(N, glu ? 64 : 128) * 256 < (1LL << 32);
+  const Plan c = choose(M, glu ? 2 * N : N, K, glu, true), d = choose(M, glu ? 2 * N : N, K, glu, false);
+  if ((long long)M * ceil_div(N, 512) >= (1LL << 25)) return false;
+  return grid_fits(ceil_div(M, kRows[c.kind]), N, c.kind, glu, c.S) && grid_fits(ceil_div(M, kRows[d.kind]), N, d.kind, glu, d.S);
 }
 
 size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype) {
-  if (out_dtype != kE4M3 || large_fills(ceil_div(M, 256), N, glu)) return 0;
-  return align256((size_t)M * N * 4);
+  const Plan c = choose(M, glu ? 2 * N : N, K, glu, out_dtype >= 2);
+  if (c.S > 1) return align256((size_t)c.S * M * (glu ? 2 * (size_t)N : N) * 4);
+  return by_finish(c.kind, c.S, out_dtype) ? align256((size_t)M * N * 4) : 0;
 }
 
 const char* fp8_name(int M, int N, int K, bool glu) {
-  return large_fills(ceil_div(M, 256), N, glu) ? "w4a16_fp8_256x256" : "w4a16_fp8_128x128";
+  const Plan c = choose(M, glu ? 2 * N : N, K, glu, false);
+  static const char* const names[2][5] = {
+      {"w4a16_fp8_16", "w4a16_fp8_32x128", "w4a16_fp8_64x128", "w4a16_fp8_128x256", "w4a16_fp8_256x256"},
+      {"w4a16_fp8_16", "w4a16_fp8_32x128_splitk", "w4a16_fp8_64x128_splitk", "w4a16_fp8_128x256_splitk", "w4a16_fp8_256x256_splitk"}};
+  return names[c.S > 1][c.kind];
 }
 
 hipError_t launch_fp8(const Fp8Args& a) {
+  const bool exact = a.out_dtype >= 2;
+  const Plan c = choose(a.M, a.glu ? 2 * a.N : a.N, a.K, a.glu, exact);
   TileParams p = tile_params(a);
-  const bool large = large_fills(ceil_div(a.M, 256), a.N, a.glu);
-  const bool after = a.out_dtype == kE4M3 && !large;  // h in fp32 first
-  if (after) {
+  const bool finish = by_finish(c.kind, c.S, a.out_dtype);
+  if (finish) {
     p.out = a.scratch;
     p.out_dtype = 2;
   }
   hipError_t e;
-  if (large) {
-    set_tiles<Large>(p, a.glu, ceil_div(a.M, 256));
-    e = a.glu      ? launch_tile<Large, true, false, DENSE>(p, 1, a.stream)
-        : a.w_rows ? launch_tile<Large, false, true, DENSE>(p, 1, a.stream)
-                   : launch_tile<Large, false, false, DENSE>(p, 1, a.stream);
+  if (c.kind == STREAM && !a.w_rows) {
+    e = launch_rows16(p, a.M, a.glu, false, a.stream);
   } else {
-    set_tiles<Small>(p, a.glu, ceil_div(a.M, 128));
-    e = a.glu      ? launch_tile<Small, true, false, DENSE>(p, 1, a.stream)
-        : a.w_rows ? launch_tile<Small, false, true, DENSE>(p, 1, a.stream)
-                   : launch_tile<Small, false, false, DENSE>(p, 1, a.stream);
+    const bool glu = a.glu && c.S == 1;
+    if (a.glu && !glu) p.N = 2 * a.N;
+    const int kind = c.kind == STREAM ? LOW : c.kind;
+    set_tiles(p, kind, glu, ceil_div(a.M, kRows[kind]));
+    p.slice = ceil_div(p.KB, c.S);
+    const auto launch = a.w_rows ? launch_columns : glu ? launch_glu : fp8::launch_dense;
+    const long long tiles = (long long)p.tiles_m * p.tiles_n, cus = device_cu_count(), left = tiles % cus;
+    if (halved(kind, c.S, tiles, cus)) {
+      // the last round fills half the chip at most: its tiles run as halves, all at once
+      p.first = (int)(tiles - left);
+      TileParams whole = p;
+      whole.first = 0;
+      e = launch(whole, WHOLE, exact, (unsigned)p.first, 1, a.stream);
+      if (e != hipSuccess) return e;
+      e = launch(p, HALF, exact, (unsigned)(2 * left), 1, a.stream);
+    } else {
+      e = launch(p, kind, exact, (unsigned)tiles, c.S, a.stream);
+    }
   }
-  if (e != hipSuccess || !after) return e;
-  return launch_fp8_rows(a.scratch, a.M, a.N, 2, static_cast<uint8_t*>(a.out), a.out_scales, a.stream);
+  if (e != hipSuccess || !finish) return e;
+  return launch_finish(a.scratch, c.S, a.M, a.N, a.glu && c.S > 1, a.out, a.out_dtype, a.out_scales, a.stream);
 }
 
 // ---- grouped ----
 
 namespace {
 
-constexpr int kList128 = kTileLists - 1;
-
-// row tiles of 256 to expect: full ones, and one part-filled a group
-bool grouped_large(const RouteLayout& r, int N, bool glu) {
+// The rows of each group are known on the device only, so the tile goes by their mean over the groups that can have rows
+int choose_grouped(const RouteLayout& r, int N, bool glu, bool exact) {
+  if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE)) return forced_kind();
   const int groups = r.E < r.S ? r.E : r.S;
-  return r.S / (groups > 0 ? groups : 1) >= 192 && large_fills(r.S / 256 + (groups + 1) / 2, N, glu);
+  const int mean = r.S / (groups > 0 ? groups : 1);
+  if (mean <= 8) return STREAM;
+  if (mean <= 24) return LOW;
+  if (mean <= 80) return MID;
+  if (exact || mean <= 160) return HALF;
+  const long long tiles = (r.S / 256 + (groups + 1) / 2) * (long long)ceil_div(glu ? 2 * N : N, 256);
+  return 2 * tiles >= device_cu_count() ? WHOLE : HALF;
 }
 
-GroupTiles group_tiles(const RouteLayout& r, const int32_t* plan, bool gather) {
+int list_of(int kind) { return kind < HALF ? kind : HALF; }  // the plan's lists have 16, 32, 64 and 128 rows a tile
+
+GroupTiles group_tiles(const RouteLayout& r, const int32_t* plan, bool gather, int list) {
   GroupTiles t;
   t.plan = plan;
   t.E = r.E;
   t.token = r.token;
-  t.list = r.tiles[kList128];
-  t.bound = tile_bound(r.S, r.E, kList128);
+  t.list = r.tiles[list];
+  t.bound = tile_bound(r.S, r.E, list);
   t.tokens = gather ? r.S / r.topk : 0;
   return t;
 }
@@ -122,48 +346,54 @@ GroupTiles group_tiles(const RouteLayout& r, const int32_t* plan, bool gather) {
 }  // namespace
 
 bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu) {
-  if (!fp8_fits(r.S, N, K, glu)) return false;
-  return (long long)tile_bound(r.S, r.E, kList128) * ceil_div(N, glu ? 64 : 128) * 512 < (1LL << 32);
+  const long long wrows = glu ? 2LL * N : 256;
+  if ((long long)K >= (1LL << 23) || wrows * K >= (1LL << 31)) return false;
+  if ((long long)fp8_blocks(K) * r.S * 4 >= (1LL << 31) || (long long)(fp8_blocks(N) + 1) * 2 * fp8_blocks(K) * 4 >= (1LL << 31))
+    return false;
+  if ((long long)r.S * ceil_div(N, 512) >= (1LL << 25)) return false;
+  for (int exact = 0; exact < 2; ++exact) {
+    const int kind = choose_grouped(r, N, glu, exact != 0);
+    if (!grid_fits(tile_bound(r.S, r.E, list_of(kind)), N, kind, glu, 1)) return false;
+  }
+  return true;
 }
 
-size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int K, bool glu, int out_dtype) {
-  if (out_dtype != kE4M3 || grouped_large(r, N, glu)) return 0;
+size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int, bool glu, int out_dtype) {
+  if (!by_finish(choose_grouped(r, N, glu, out_dtype >= 2), 1, out_dtype)) return 0;
   return align256((size_t)r.S * N * 4);
 }
 
 hipError_t launch_fp8_grouped(const Fp8Args& a, const RouteLayout& r, const int32_t* plan, bool gather) {
+  const bool exact = a.out_dtype >= 2;
+  const int kind = choose_grouped(r, a.N, a.glu, exact);
   TileParams p = tile_params(a);
   p.M = p.scale_rows = r.S;
-  p.groups = group_tiles(r, plan, gather);
-  const bool large = grouped_large(r, a.N, a.glu);
-  const bool after = a.out_dtype == kE4M3 && !large;
-  if (after) {
+  p.groups = group_tiles(r, plan, gather, list_of(kind));
+  const bool finish = by_finish(kind, 1, a.out_dtype);
+  if (finish) {
     p.out = a.scratch;
     p.out_dtype = 2;
   }
   hipError_t e;
-  if (large) {
-    set_tiles<Large>(p, a.glu, p.groups.bound);
-    e = a.glu ? launch_tile<Large, true, false, GROUPED>(p, 1, a.stream)
-              : launch_tile<Large, false, false, GROUPED>(p, 1, a.stream);
+  if (kind == STREAM) {
+    e = launch_rows16(p, 16, a.glu, true, a.stream);
   } else {
-    set_tiles<Small>(p, a.glu, p.groups.bound);
-    e = a.glu ? launch_tile<Small, true, false, GROUPED>(p, 1, a.stream)
-              : launch_tile<Small, false, false, GROUPED>(p, 1, a.stream);
+    set_tiles(p, kind, a.glu, p.groups.bound);
+    const auto launch = a.glu ? launch_grouped_glu : launch_grouped_plain;
+    e = launch(p, kind, exact, (unsigned)((size_t)p.tiles_m * p.tiles_n), 1, a.stream);
   }
-  if (e != hipSuccess || !after) return e;
-  return launch_fp8_rows(a.scratch, r.S, a.N, 2, static_cast<uint8_t*>(a.out), a.out_scales, a.stream);
+  if (e != hipSuccess || !finish) return e;
+  return launch_finish(a.scratch, 1, r.S, a.N, false, a.out, a.out_dtype, a.out_scales, a.stream);
 }
 
 hipError_t launch_fp8_by_group(const Fp8Args& a, const RouteLayout& r, const int32_t* plan) {
   TileParams p = tile_params(a);
-  p.groups = group_tiles(r, plan, false);
-  if (large_fills((long long)ceil_div(a.M, 256) * r.E, a.N, false)) {
-    set_tiles<Large>(p, false, ceil_div(a.M, 256));
-    return launch_tile<Large, false, true, BY_GROUP>(p, r.E, a.stream);
-  }
-  set_tiles<Small>(p, false, ceil_div(a.M, 128));
-  return launch_tile<Small, false, true, BY_GROUP>(p, r.E, a.stream);
+  p.groups = group_tiles(r, plan, false, kTileLists - 1);
+  // tall tiles where they still fill the chip
+  const long long tall = (long long)ceil_div(a.M, kRows[HALF]) * ceil_div(a.N, kCols[HALF]) * r.E;
+  const int kind = tall >= device_cu_count() ? HALF : MID;
+  set_tiles(p, kind, false, ceil_div(a.M, kRows[kind]));
+  return launch_by_group(p, kind, true, (unsigned)((size_t)p.tiles_m * p.tiles_n), r.E, a.stream);
 }
 
 }  // namespace w4a16

@@ -49,7 +49,9 @@ struct TileParams {
   int ldk, xs_ld;
   int up_blocks;     // GLU: blocks of a half
   int tiles_m, tiles_n;
-  int scale_rows;    // GROUPED with e4m3 out: rows of out_scales' blocks
+  int first;         // DENSE, over 0: the launch takes the tiles of twice its height from here on (tiles_m counts those)
+  int slice;         // DENSE: blocks of k of a workgroup; slice blockIdx.y's sums go to out + blockIdx.y M N (fp32)
+  int scale_rows;    // rows of out_scales' blocks
   GroupTiles groups;
 };
 
@@ -100,35 +102,43 @@ __device__ __forceinline__ void buffer_copy4_to_lds(__amdgpu_buffer_rsrc_t r, ui
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, (int)voff, (int)soff, 0, 0);
 }
 
-// WN x WM waves of NT x MT 16 x 16 outputs
-template <int WN, int WM, int NT, int MT>
+// WN x WM waves of NT x MT 16 x 16 outputs; ST stages of LDS, of which ST - 1 are filled ahead; ISSUE copies go out before
+// each of a block's MT steps; TOUCH: how many blocks ahead a block's lines are brought into L2
+template <int WN, int WM, int NT, int MT, int ST, int ISSUE, int TOUCH = 0>
 struct Tile {
-  static constexpr int kWN = WN, kWM = WM, kNT = NT, kMT = MT;
+  static constexpr int kWN = WN, kWM = WM, kNT = NT, kMT = MT, kStages = ST, kIssue = ISSUE, kTouch = TOUCH;
   static constexpr int kBN = WN * NT * 16, kBM = WM * MT * 16;
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
-  static constexpr int kCopies = (kBN + kBM) / 8 / kWaves;  // 1 KiB copies a wave and block
+  static constexpr int kCopiesX = kBM / 8 / kWaves, kCopiesW = kBN / 8 / kWaves;  // 1 KiB copies a wave and block
+  static constexpr int kLoads = kCopiesX + kCopiesW + 1;  // and one of scales
   static constexpr int kCodes = (kBN + kBM) * 128;
-  static constexpr int kStage = kCodes + (kBN + kBM) * 4;
-  static constexpr size_t kLdsBytes = 2 * kStage;
-  static_assert(kBN + kBM == kThreads, "a lane copies the scale of one row");
-  static_assert(kBM % (8 * kCopies) == 0 && kBM % 64 == 0, "a wave copies rows of one operand");
+  static constexpr int kStage = kCodes + kThreads * 4;
+  static constexpr size_t kLdsBytes = ST * kStage + (TOUCH ? kThreads * 4 : 0);
+  static constexpr int kScalesX = (kBM + 63) / 64 * 64;  // lanes for x's scales: whole waves
+  static_assert(kBM % (8 * kWaves) == 0 && kBN % (8 * kWaves) == 0, "each wave copies as many rows of each operand");
+  static_assert(kBN + kScalesX <= kThreads, "a lane copies the scale of one row");
+  static_assert((ST - 2) * kLoads + 1 < 64, "vmcnt holds 0..63");
+  static_assert(MT * ISSUE >= kLoads, "all of a block's copies go out within one");
+  static_assert(!TOUCH || (ST == 2 && kBN + kBM == kThreads && (kLoads + ISSUE - 1) / ISSUE < MT), "a lane touches one row");
 };
-typedef Tile<4, 2, 4, 8> Large;  // 256 x 256
-typedef Tile<2, 2, 4, 4> Small;  // 128 x 128
 
+// The tile at row tile tm and column tile tn
 template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
-__global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
+__device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, int tn) {
   constexpr int NT = T::kNT, MT = T::kMT, BN = T::kBN, BM = T::kBM;
   constexpr int OUT = GLU ? BN / 2 : BN;  // columns of out that a tile makes
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
+  constexpr int ST = T::kStages, ISSUE = T::kIssue;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % T::kWN, wm = wave / T::kWN;
-  const int t = tile_of(blockIdx.x, p.tiles_m * p.tiles_n);
-  const int tm = t % p.tiles_m, tn = t / p.tiles_m;  // neighbours share the weight's rows
   const int N = p.N, n0 = tn * OUT;
   int m0 = tm * BM, end = p.M, kb0 = 0, kb1 = p.KB, e = 0;
   size_t out_row = 0;
+  if constexpr (MODE == DENSE) {
+    kb0 = min((int)blockIdx.y * p.slice, p.KB);
+    kb1 = min(kb0 + p.slice, p.KB);
+    out_row = (size_t)blockIdx.y * p.M;
+  }
   if constexpr (MODE == GROUPED) {
     if (!group_tile(p.groups, tm, e, m0, end)) return;
     if constexpr (BM > 128) {
@@ -139,7 +149,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
       end = min(m0 + BM, last);
     }
     if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
-      if constexpr (GLU) {
+      if constexpr (GLU && OUT == 128) {
         if (p.out_dtype == kE4M3) {
           uint8_t* const codes = static_cast<uint8_t*>(p.out);
           const int cols = min(OUT, N - n0);
@@ -169,66 +179,82 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   }
   const int rows = min(BM, end - m0);
 
-  // This lane's copies: instruction j of the wave fills eight tile rows (x's first, then the weight's), lane l
-  // row l/8 and position l%8. Offsets are bytes from the tile's first row (gathered: from the first token's).
+  // This lane's copies: instruction j of the wave fills eight tile rows of x, then of the weight, lane l row l/8 and
+  // position l%8. Offsets are bytes from the tile's first row (gathered: from the first token's).
   const bool gathered = MODE == GROUPED && p.groups.tokens;
   // tile row r of the weight -> its row: GLU tiles hold BN/2 gate rows, then the matching up rows
   auto weight_row = [&](int r) __attribute__((always_inline)) {
     if constexpr (GLU) return min(n0 + r % OUT, N - 1) + (r / OUT) * N;
     else return min(n0 + r, N - 1);
   };
-  constexpr int WAVES_X = BM / (8 * T::kCopies);  // waves that copy x's rows
-  const bool mine_x = wave < WAVES_X;
-  const uint8_t* const xbase = p.x + (gathered ? 0 : (size_t)m0 * p.ldk);
-  const uint8_t* const wbase = p.w + (size_t)n0 * p.ldk;
+  auto x_row = [&](int r) __attribute__((always_inline)) {
+    int src = min(r, rows - 1);
+    if constexpr (MODE == GROUPED)
+      if (gathered) src = p.groups.plan[p.groups.token + m0 + src];
+    return src;
+  };
   const uint32_t wrows = (uint32_t)(GLU ? 2 * N - n0 : min(BN, N - n0));
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(
-      mine_x ? xbase : wbase, mine_x ? (uint32_t)(gathered ? p.groups.tokens : rows) * (uint32_t)p.ldk : wrows * (uint32_t)p.ldk);
-  uint32_t off[T::kCopies];
+  const __amdgpu_buffer_rsrc_t xrs = make_rsrc(p.x + (gathered ? 0 : (size_t)m0 * p.ldk),
+                                               (uint32_t)(gathered ? p.groups.tokens : rows) * (uint32_t)p.ldk);
+  const __amdgpu_buffer_rsrc_t wrs = make_rsrc(p.w + (size_t)n0 * p.ldk, wrows * (uint32_t)p.ldk);
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;  // of every copy: its rows start at a multiple of eight
+  uint32_t xoff[T::kCopiesX], woff[T::kCopiesW];
 #pragma unroll
-  for (int j = 0; j < T::kCopies; ++j) {
-    const int r = 8 * (wave * T::kCopies + j) + (lane >> 3);
-    int src;
-    if (mine_x) {
-      src = min(r, rows - 1);
-      if constexpr (MODE == GROUPED)
-        if (gathered) src = p.groups.plan[p.groups.token + m0 + src];
-    } else {
-      src = weight_row(r - BM) - n0;
-    }
-    off[j] = (uint32_t)src * (uint32_t)p.ldk + (uint32_t)(((lane & 7) ^ (r & 7)) * 16);
-  }
-  const int chunk = (lane & 7) ^ (lane >> 3);  // of every copy: its rows start at a multiple of eight
-  // and its scale: thread i that of tile row i
-  const bool scale_x = wave < BM / 64;
+  for (int j = 0; j < T::kCopiesX; ++j)
+    xoff[j] = (uint32_t)x_row(8 * (wave * T::kCopiesX + j) + (lane >> 3)) * (uint32_t)p.ldk + (uint32_t)chunk;
+#pragma unroll
+  for (int j = 0; j < T::kCopiesW; ++j)
+    woff[j] = (uint32_t)(weight_row(8 * (wave * T::kCopiesW + j) + (lane >> 3)) - n0) * (uint32_t)p.ldk + (uint32_t)chunk;
+  // and a scale: the first waves' lanes take x's rows', the next ones the weight's
+  const bool scale_x = wave < T::kScalesX / 64;
   uint32_t soff;
   {
-    const int r = threadIdx.x;
+    const int r = scale_x ? (int)threadIdx.x : (int)threadIdx.x - T::kScalesX;
     if (scale_x) {
-      int src = min(r, rows - 1);
-      if constexpr (MODE == GROUPED)
-        if (gathered) src = p.groups.plan[p.groups.token + m0 + src];
+      const int src = x_row(r);
       soff = (uint32_t)(gathered ? src : m0 + src) * 4u;
     } else if constexpr (WROWS) {
-      soff = (uint32_t)weight_row(r - BM) * 4u;
+      soff = (uint32_t)weight_row(r) * 4u;
     } else if constexpr (GLU) {
-      const int rr = r - BM;
-      soff = (uint32_t)((min(n0 + rr % OUT, N - 1) >> 7) + (rr / OUT) * p.up_blocks) * (uint32_t)p.KB * 4u;
+      soff = (uint32_t)((min(n0 + r % OUT, N - 1) >> 7) + (r / OUT) * p.up_blocks) * (uint32_t)p.KB * 4u;
     } else {
-      soff = (uint32_t)(weight_row(r - BM) >> 7) * (uint32_t)p.KB * 4u;
+      soff = (uint32_t)(weight_row(r) >> 7) * (uint32_t)p.KB * 4u;
     }
+    if (r >= (scale_x ? BM : BN)) soff = kOutOfRange;
   }
   const __amdgpu_buffer_rsrc_t srs = make_rsrc(scale_x ? p.xs : p.ws, 0x7FFFFFFFu);
   const uint32_t sstep = scale_x ? (uint32_t)p.xs_ld * 4u : WROWS ? (uint32_t)N * 4u : 4u;
 
-  auto copy = [&](int kb, int stage) __attribute__((always_inline)) {
+  // copy j of a block: x's rows, the weight's, the scales
+  auto copy = [&](int j, int kb, int stage) __attribute__((always_inline)) {
     uint8_t* const dst = lds8 + stage * T::kStage;
-    const bool in_k = kb * 128 + chunk * 16 < p.K;
-#pragma unroll
-    for (int j = 0; j < T::kCopies; ++j)
-      buffer_copy16_to_lds(rs, in_k ? off[j] : kOutOfRange, kb * 128,
-                           reinterpret_cast<uint16_t*>(dst + (wave * T::kCopies + j) * 1024));
-    buffer_copy4_to_lds(srs, soff, kb * sstep, dst + T::kCodes + wave * 256);
+    const bool in_k = kb < kb1 && kb * 128 + chunk < p.K;
+    if (j < T::kCopiesX) {
+      buffer_copy16_to_lds(xrs, in_k ? xoff[j] : kOutOfRange, kb * 128,
+                           reinterpret_cast<uint16_t*>(dst + (wave * T::kCopiesX + j) * 1024));
+    } else if (j < T::kCopiesX + T::kCopiesW) {
+      const int i = j - T::kCopiesX;
+      buffer_copy16_to_lds(wrs, in_k ? woff[i] : kOutOfRange, kb * 128,
+                           reinterpret_cast<uint16_t*>(dst + BM * 128 + (wave * T::kCopiesW + i) * 1024));
+    } else {
+      buffer_copy4_to_lds(srs, kb < kb1 ? soff : kOutOfRange, kb * sstep, dst + T::kCodes + wave * 256);
+    }
+  };
+
+  // Lines that are not in L2 yet hold the tiles that share them up for as long as memory takes. So a block's lines are
+  // touched some blocks ahead (into LDS that nothing reads), by lane r that of tile row r: of the weight's rows an eighth, of
+  // x's a quarter, as about eight and four tiles that run at once on an XCD share them (2048 rows of 8192x28672: 475 -> 424 us;
+  // every row by every tile 462).
+  uint32_t toff = kOutOfRange;
+  const bool touch_x = wave < BM / 64;
+  if constexpr (T::kTouch > 0) {
+    const int r = touch_x ? (int)threadIdx.x : (int)threadIdx.x - BM;
+    if (touch_x ? r % 4 == tn % 4 : r % 8 == tm % 8)
+      toff = (uint32_t)(touch_x ? x_row(r) : weight_row(r) - n0) * (uint32_t)p.ldk;
+  }
+  auto touch = [&](int kb) __attribute__((always_inline)) {
+    if constexpr (T::kTouch > 0)
+      buffer_copy4_to_lds(touch_x ? xrs : wrs, kb < kb1 ? toff : kOutOfRange, kb * 128, lds8 + ST * T::kStage + wave * 256);
   };
 
   f4_t acc[NT][MT];
@@ -243,71 +269,134 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     else return (wn * NT + nt) * 16;
   };
 
-  auto compute = [&](int stage) __attribute__((always_inline)) {
-    const uint8_t* const xt = lds8 + stage * T::kStage;
-    const uint8_t* const wt = xt + BM * 128;
-    const float* const xsc = reinterpret_cast<const float*>(xt + T::kCodes);
-    const float* const wsc = xsc + BM;
-    typename std::conditional<EXACT, Wide, i8v_t>::type a[NT];
+  // The sums of the last 16 rows multiplied, and their factors: added to the running sums while the next ones'
+  // MFMAs run (over the end of a block too)
+  f4_t part[NT];
+  float fac[2] = {0.f, 0.f};
+  f4_t facr[WROWS ? NT : 1];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const i8v_t f = read_fragment(wt, nrow(nt) + l16, q);
-      if constexpr (EXACT) a[nt] = widen(f);
-      else a[nt] = f;
+  for (int nt = 0; nt < NT; ++nt) part[nt] = f4_t{0.f, 0.f, 0.f, 0.f};
+  if constexpr (WROWS) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) facr[nt] = part[nt];
+  }
+  auto add = [&](int nt, int mt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f = GLU && nt >= NT / 2 ? fac[1] : fac[0];
+      if constexpr (WROWS) f = fac[0] * facr[nt][i];
+      acc[nt][mt][i] = __builtin_fmaf(part[nt][i], f, acc[nt][mt][i]);
     }
-    // block scales: one of the wave's rows stands for all (GLU: one of each half)
-    float sw[2];
-    f4_t swr[WROWS ? NT : 1];
+  };
+
+  typedef typename std::conditional<EXACT, Wide, i8v_t>::type Frag;
+  auto stage_x = [&](int stage) __attribute__((always_inline)) { return lds8 + stage * T::kStage; };
+  auto read_b = [&](int stage, int mt) __attribute__((always_inline)) {
+    return read_fragment(stage_x(stage), (wm * MT + mt) * 16 + l16, q);
+  };
+  auto read_a = [&](int stage, int nt) __attribute__((always_inline)) -> Frag {
+    const i8v_t f = read_fragment(stage_x(stage) + BM * 128, nrow(nt) + l16, q);
+    if constexpr (EXACT) return widen(f);
+    else return f;
+  };
+  auto scales_x = [&](int stage) __attribute__((always_inline)) {
+    return reinterpret_cast<const float*>(stage_x(stage) + T::kCodes);
+  };
+  // block scales: one of the wave's rows stands for all (GLU: one of each half)
+  Frag a[NT];
+  float sw[2];
+  f4_t swr[WROWS ? NT : 1];
+  auto read_sw = [&](int stage) __attribute__((always_inline)) {
+    const float* const wsc = scales_x(stage) + T::kScalesX;
     if constexpr (WROWS) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) swr[nt] = *reinterpret_cast<const f4_t*>(wsc + nrow(nt) + 4 * q);
     } else {
       sw[0] = wsc[nrow(0)];
-      sw[1] = GLU ? wsc[nrow(NT / 2)] : sw[0];
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = (wm * MT + mt) * 16 + l16;
-      const i8v_t b = read_fragment(xt, r, q);
-      const float sx = xsc[r];
-      f4_t part[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) part[nt] = f4_t{0.f, 0.f, 0.f, 0.f};
-      if constexpr (EXACT) {
-        const Wide bw = widen(b);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) part[nt] = mfma16(a[nt].k[s], bw.k[s], part[nt]);
-      } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) part[nt] = mfma_fp8(a[nt], b);
-      }
-      const float f0 = WROWS ? sx : sx * sw[0], f1 = GLU ? sx * sw[1] : f0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f = nt < NT / 2 ? f0 : f1;
-          if constexpr (WROWS) f = sx * swr[nt][i];
-          acc[nt][mt][i] = __builtin_fmaf(part[nt][i], f, acc[nt][mt][i]);
-        }
+      if constexpr (GLU) sw[1] = wsc[nrow(NT / 2)];
     }
   };
 
-  // Block i is multiplied while block i + 1 travels into the other stage. Each wave waits for its own copies; the
-  // barrier makes all waves' visible and frees the stage of block i - 1.
-  const int nb = kb1 - kb0;
-  if (nb > 0) copy(kb0, 0);
-  for (int i = 0; i < nb; ++i) {
-    wait_loads<0>();
+  // Block i is multiplied while the next ST - 1 travel into the other stages, a few copies at a time between the MFMAs
+  // (a burst of them would hold the wave while the address unit takes it in). Before a block's last 16 rows,
+  // whose operands are in registers by then, each wave waits for its own copies of the next block; the barrier
+  // makes all waves' visible and frees the block's own stage; and the next block's first fragments are read
+  // while the last rows are multiplied. Copies past the last block read out of range, so that the count
+  // of loads in flight is the same at every step.
+  auto meet = [&]() __attribute__((always_inline)) {
+    wait_loads<(ST - 2) * T::kLoads + (T::kTouch > 0)>();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
-    if (i + 1 < nb) copy(kb0 + i + 1, (i + 1) & 1);
-    compute(i & 1);
+  };
+  const int nb = kb1 - kb0;
+  if (nb > 0) {
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+#pragma unroll
+      for (int j = 0; j < T::kLoads; ++j) copy(j, kb0 + i, i);
+    touch(kb0 + ST - 1);
+    meet();
+    i8v_t b = read_b(0, 0);
+    float sx = scales_x(0)[wm * MT * 16 + l16];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) a[nt] = read_a(0, nt);
+    read_sw(0);
+    int stage = 0;
+    for (int i = 0; i < nb; ++i) {
+      const int free = stage == 0 ? ST - 1 : stage - 1, next = stage == ST - 1 ? 0 : stage + 1;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int j = mt * ISSUE; j < (mt + 1) * ISSUE && j < T::kLoads; ++j) copy(j, kb0 + i + ST - 1, free);
+        if (mt == (T::kLoads + ISSUE - 1) / ISSUE) touch(kb0 + i + T::kTouch);
+        if (mt == MT - 1) meet();
+        const i8v_t bn = mt + 1 < MT ? read_b(stage, mt + 1) : read_b(next, 0);
+        const float sxn = mt + 1 < MT ? scales_x(stage)[(wm * MT + mt + 1) * 16 + l16] : scales_x(next)[wm * MT * 16 + l16];
+        __builtin_amdgcn_sched_barrier(0);  // the reads travel while these rows are multiplied
+        const int before = mt == 0 ? MT - 1 : mt - 1;
+        f4_t now[NT];
+        if constexpr (EXACT) {
+          const Wide bw = widen(b);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) now[nt] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) now[nt] = mfma16(a[nt].k[s], bw.k[s], now[nt]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            add(nt, before);
+            if (mt == MT - 1) a[nt] = read_a(next, nt);
+          }
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            now[nt] = mfma_fp8(a[nt], b);
+            if (mt == MT - 1) a[nt] = read_a(next, nt);
+            add(nt, before);
+          }
+        }
+        fac[0] = WROWS ? sx : sx * sw[0];
+        if constexpr (GLU) fac[1] = sx * sw[1];
+        if constexpr (WROWS) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) facr[nt] = swr[nt];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) part[nt] = now[nt];
+        if (mt == MT - 1) read_sw(next);
+        b = bn;
+        sx = sxn;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      stage = next;
+    }
   }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) add(nt, MT - 1);
 
   // ---- epilogue ----
   // Each wave turns 16 rows m by its columns at a time through a slice of LDS of its own, and stores runs of a row.
@@ -329,7 +418,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
           const float g = acc[nt][mt][i], u = acc[nt + NT / 2][mt][i];
           acc[nt][mt][i] = g / (1.0f + __expf(-g)) * u;
         }
-    if (p.out_dtype == kE4M3) {
+    if (OUT == 128 && p.out_dtype == kE4M3) {
       static_assert(T::kWaves * 16 * PITCH * 4 + T::kWN * BM * 4 <= (int)T::kLdsBytes, "and the rows' maxima");
       // the largest |h| of a row over the tile's 128 columns: this wave's, then all waves' of the row
 #pragma unroll
@@ -361,7 +450,9 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     __builtin_amdgcn_wave_barrier();
     // a lane takes eight columns of a row
 #pragma unroll
-    for (int piece = lane; piece < 16 * COLS / 8; piece += 64) {
+    for (int pass = 0; pass < (16 * COLS / 8 + 63) / 64; ++pass) {
+      const int piece = lane + 64 * pass;
+      if (16 * COLS / 8 % 64 != 0 && piece >= 16 * COLS / 8) continue;
       const int r = piece / (COLS / 8), c = piece % (COLS / 8) * 8;
       if (r0 + r >= rows) continue;
       const float* src = slice + r * PITCH + c;
@@ -375,7 +466,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
       const int n = nw + c, some = N - n;
       if (some <= 0) continue;
       const size_t at = (out_row + m0 + r0 + r) * (size_t)N + n;
-      if (GLU && p.out_dtype == kE4M3) {
+      if (GLU && OUT == 128 && p.out_dtype == kE4M3) {
         uint32_t b = 0;
 #pragma unroll
         for (int w = 0; w < T::kWN; ++w) b = max(b, __builtin_bit_cast(uint32_t, most[w * BM + r0 + r]));
@@ -419,6 +510,58 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     }
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+// Kinds of kernel, by the rows of x of a tile
+enum Kind { STREAM = 0, LOW = 1, MID = 2, HALF = 3, WHOLE = 4 };
+typedef Tile<4, 1, 2, 2, 3, 3> Low;       // 32 rows, 128 columns
+typedef Tile<4, 1, 2, 4, 3, 2> Mid;       // 64, 128
+typedef Tile<4, 2, 4, 4, 3, 2> Half;      // 128, 256
+typedef Tile<4, 2, 4, 8, 2, 3, 3> Whole;  // 256, 256: results of 16 bits only (widened fragments would not fit)
+
+template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
+__global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
+  const int tiles = p.tiles_m * p.tiles_n;
+  int tm, tn;
+  if (MODE == DENSE && p.first > 0) {
+    // what whole rounds of tiles twice as high have left: the halves of their tiles from the first one on
+    const int b = tile_of(blockIdx.x, 2 * (tiles - p.first)), t = p.first + (b >> 1);
+    tm = 2 * (t % p.tiles_m) + (b & 1);
+    tn = t / p.tiles_m;
+    if (tm * T::kBM >= p.M) return;
+  } else {
+    const int t = tile_of(blockIdx.x, MODE == DENSE ? gridDim.x : tiles);  // neighbours share the weight's rows
+    tm = t % p.tiles_m;
+    tn = t / p.tiles_m;
+  }
+  fp8_tile<T, GLU, WROWS, MODE, EXACT>(p, lds8, tm, tn);
+}
+
+template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
+hipError_t launch_tile(const TileParams& p, unsigned grid, int gy, hipStream_t s) {
+  hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT>), dim3(grid, gy), dim3(T::kThreads), T::kLdsBytes, s, p);
+  return hipGetLastError();
+}
+
+template <bool GLU, bool WROWS, int MODE>
+hipError_t launch_kind(const TileParams& p, int kind, bool exact, unsigned grid, int gy, hipStream_t s) {
+  if (exact || WROWS) {
+    switch (kind) {
+      case LOW: return launch_tile<Low, GLU, WROWS, MODE, true>(p, grid, gy, s);
+      case MID: return launch_tile<Mid, GLU, WROWS, MODE, true>(p, grid, gy, s);
+      default: return launch_tile<Half, GLU, WROWS, MODE, true>(p, grid, gy, s);
+    }
+  }
+  if constexpr (!WROWS) {  // a weight's gradient has fp32 results only
+    switch (kind) {
+      case LOW: return launch_tile<Low, GLU, WROWS, MODE, false>(p, grid, gy, s);
+      case MID: return launch_tile<Mid, GLU, WROWS, MODE, false>(p, grid, gy, s);
+      case HALF: return launch_tile<Half, GLU, WROWS, MODE, false>(p, grid, gy, s);
+      default: return launch_tile<Whole, GLU, WROWS, MODE, false>(p, grid, gy, s);
+    }
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace fp8
