@@ -242,6 +242,12 @@ hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, hip
   return launch_stream(p, NT, grouped || M > 8 ? 2 : 1, W, glu, grouped, grid, s);
 }
 
+// Workgroups of a launch of so many tiles: with one a compute unit, each takes its share of the tiles in turn
+unsigned workgroups(int kind, long long tiles) {
+  const long long cus = device_cu_count();
+  return (unsigned)(kind == HALF && tiles > cus ? cus : tiles);
+}
+
 bool grid_fits(long long tiles_m, int N, int kind, bool glu, int S) {
   const long long cols = kind == STREAM ? 16 : kCols[kind] / (glu ? 2 : 1);
   return tiles_m * ((N + cols - 1) / cols) * 512 * S < (1LL << 32);
@@ -302,11 +308,11 @@ hipError_t launch_fp8(const Fp8Args& a) {
       p.first = (int)(tiles - left);
       TileParams whole = p;
       whole.first = 0;
-      e = launch(whole, WHOLE, exact, (unsigned)p.first, 1, a.stream);
+      e = launch(whole, WHOLE, exact, workgroups(WHOLE, p.first), 1, a.stream);
       if (e != hipSuccess) return e;
-      e = launch(p, HALF, exact, (unsigned)(2 * left), 1, a.stream);
+      e = launch(p, HALF, exact, workgroups(HALF, 2 * left), 1, a.stream);
     } else {
-      e = launch(p, kind, exact, (unsigned)tiles, c.S, a.stream);
+      e = launch(p, kind, exact, c.S > 1 ? (unsigned)tiles : workgroups(kind, tiles), c.S, a.stream);
     }
   }
   if (e != hipSuccess || !finish) return e;
@@ -380,7 +386,7 @@ hipError_t launch_fp8_grouped(const Fp8Args& a, const RouteLayout& r, const int3
   } else {
     set_tiles(p, kind, a.glu, p.groups.bound);
     const auto launch = a.glu ? launch_grouped_glu : launch_grouped_plain;
-    e = launch(p, kind, exact, (unsigned)((size_t)p.tiles_m * p.tiles_n), 1, a.stream);
+    e = launch(p, kind, exact, workgroups(kind, (long long)p.tiles_m * p.tiles_n), 1, a.stream);
   }
   if (e != hipSuccess || !finish) return e;
   return launch_finish(a.scratch, 1, r.S, a.N, false, a.out, a.out_dtype, a.out_scales, a.stream);
@@ -391,7 +397,7 @@ hipError_t launch_fp8_by_group(const Fp8Args& a, const RouteLayout& r, const int
   p.groups = group_tiles(r, plan, false, kTileLists - 1);
   // tall tiles where they still fill the chip
   const long long tall = (long long)ceil_div(a.M, kRows[HALF]) * ceil_div(a.N, kCols[HALF]) * r.E;
-  const int kind = tall >= device_cu_count() ? HALF : MID;
+  const int kind = forced_kind() >= 0 ? forced_kind() : tall >= device_cu_count() ? HALF : MID;
   set_tiles(p, kind, false, ceil_div(a.M, kRows[kind]));
   return launch_by_group(p, kind, true, (unsigned)((size_t)p.tiles_m * p.tiles_n), r.E, a.stream);
 }

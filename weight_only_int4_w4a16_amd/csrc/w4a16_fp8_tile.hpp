@@ -122,93 +122,54 @@ struct Tile {
   static_assert(!TOUCH || (ST == 2 && kBN + kBM == kThreads && (kLoads + ISSUE - 1) / ISSUE < MT), "a lane touches one row");
 };
 
-// The tile at row tile tm and column tile tn
-template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
-__device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, int tn) {
+// LOOP: a workgroup takes tiles blockIdx.x, blockIdx.x + gridDim.x, ..., and the first blocks of the next one are on their way
+// while it stores the last; else tile blockIdx.x alone. The loop's tiles cost the 256-row ones spills.
+template <class T, bool GLU, bool WROWS, int MODE, bool EXACT, bool LOOP>
+__global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   constexpr int NT = T::kNT, MT = T::kMT, BN = T::kBN, BM = T::kBM;
   constexpr int OUT = GLU ? BN / 2 : BN;  // columns of out that a tile makes
   constexpr int ST = T::kStages, ISSUE = T::kIssue;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % T::kWN, wm = wave / T::kWN;
-  const int N = p.N, n0 = tn * OUT;
-  int m0 = tm * BM, end = p.M, kb0 = 0, kb1 = p.KB, e = 0;
-  size_t out_row = 0;
-  if constexpr (MODE == DENSE) {
-    kb0 = min((int)blockIdx.y * p.slice, p.KB);
-    kb1 = min(kb0 + p.slice, p.KB);
-    out_row = (size_t)blockIdx.y * p.M;
-  }
-  if constexpr (MODE == GROUPED) {
-    if (!group_tile(p.groups, tm, e, m0, end)) return;
-    if constexpr (BM > 128) {
-      // the list's tiles have 128 rows: every second one of a group stands for itself and the next
-      const int first = e < p.groups.E ? p.groups.plan[e] : p.groups.plan[p.groups.E];
-      const int last = e < p.groups.E ? p.groups.plan[e + 1] : p.M;
-      if ((m0 - first) % BM) return;
-      end = min(m0 + BM, last);
-    }
-    if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
-      if constexpr (GLU && OUT == 128) {
-        if (p.out_dtype == kE4M3) {
-          uint8_t* const codes = static_cast<uint8_t*>(p.out);
-          const int cols = min(OUT, N - n0);
-          for (int i = threadIdx.x; i < (end - m0) * cols; i += T::kThreads)
-            codes[(size_t)(m0 + i / cols) * N + n0 + i % cols] = 0;
-          for (int i = threadIdx.x; i < end - m0; i += T::kThreads)
-            p.out_scales[(size_t)(n0 / 128) * p.scale_rows + m0 + i] = kLeastScale;
-          return;
-        }
-      }
-      zero_tile(p.out, p.out_dtype, m0, end - m0, N, n0, OUT);
-      return;
-    }
-    p.w += (size_t)e * (GLU ? 2 : 1) * N * p.ldk;
-    p.ws += (size_t)e * (GLU ? 2 * p.up_blocks : (N + 127) / 128) * p.KB;
-  }
-  if constexpr (MODE == BY_GROUP) {
-    // group e's blocks of k are its 128-row tiles: as many as earlier groups have come before them
-    e = blockIdx.y;
-    int before = 0;
-    for (int g = lane; g < e; g += 64) before += (p.groups.plan[g + 1] - p.groups.plan[g] + 127) / 128;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor(before, o);
-    kb0 = __builtin_amdgcn_readfirstlane(before);
-    kb1 = kb0 + __builtin_amdgcn_readfirstlane((p.groups.plan[e + 1] - p.groups.plan[e] + 127) / 128);
-    out_row = (size_t)e * p.M;
-  }
-  const int rows = min(BM, end - m0);
-
-  // This lane's copies: instruction j of the wave fills eight tile rows of x, then of the weight, lane l row l/8 and
-  // position l%8. Offsets are bytes from the tile's first row (gathered: from the first token's).
+  const int N = p.N;
   const bool gathered = MODE == GROUPED && p.groups.tokens;
-  // tile row r of the weight -> its row: GLU tiles hold BN/2 gate rows, then the matching up rows
-  auto weight_row = [&](int r) __attribute__((always_inline)) {
-    if constexpr (GLU) return min(n0 + r % OUT, N - 1) + (r / OUT) * N;
-    else return min(n0 + r, N - 1);
-  };
-  auto x_row = [&](int r) __attribute__((always_inline)) {
-    int src = min(r, rows - 1);
-    if constexpr (MODE == GROUPED)
-      if (gathered) src = p.groups.plan[p.groups.token + m0 + src];
-    return src;
-  };
-  const uint32_t wrows = (uint32_t)(GLU ? 2 * N - n0 : min(BN, N - n0));
-  const __amdgpu_buffer_rsrc_t xrs = make_rsrc(p.x + (gathered ? 0 : (size_t)m0 * p.ldk),
-                                               (uint32_t)(gathered ? p.groups.tokens : rows) * (uint32_t)p.ldk);
-  const __amdgpu_buffer_rsrc_t wrs = make_rsrc(p.w + (size_t)n0 * p.ldk, wrows * (uint32_t)p.ldk);
+
+  // ---- the tile at hand ----
+  int m0 = 0, rows = 0, n0 = 0, kb0 = 0, kb1 = 0;
+  size_t out_row = 0;
+  __amdgpu_buffer_rsrc_t xrs, wrs, srs;
+  uint32_t xoff[T::kCopiesX], woff[T::kCopiesW], soff = 0, toff = 0;
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;  // of every copy: its rows start at a multiple of eight
-  uint32_t xoff[T::kCopiesX], woff[T::kCopiesW];
+  const bool scale_x = wave < T::kScalesX / 64, touch_x = wave < BM / 64;
+  const uint32_t sstep = scale_x ? (uint32_t)p.xs_ld * 4u : WROWS ? (uint32_t)N * 4u : 4u;
+
+  // Copies: instruction j of the wave fills eight tile rows of x, then of the weight, lane l row l/8 and position l%8.
+  // Offsets are bytes from the tile's first row (gathered: from the first token's).
+  auto set = [&](const uint8_t* w, const float* ws, int tm, int tn) __attribute__((always_inline)) {
+    // tile row r of the weight -> its row: GLU tiles hold BN/2 gate rows, then the matching up rows
+    auto weight_row = [&](int r) __attribute__((always_inline)) {
+      if constexpr (GLU) return min(n0 + r % OUT, N - 1) + (r / OUT) * N;
+      else return min(n0 + r, N - 1);
+    };
+    auto x_row = [&](int r) __attribute__((always_inline)) {
+      int src = min(r, rows - 1);
+      if constexpr (MODE == GROUPED)
+        if (gathered) src = p.groups.plan[p.groups.token + m0 + src];
+      return src;
+    };
+    const uint32_t wrows = (uint32_t)(GLU ? 2 * N - n0 : min(BN, N - n0));
+    xrs = make_rsrc(p.x + (gathered ? 0 : (size_t)m0 * p.ldk), (uint32_t)(gathered ? p.groups.tokens : rows) * (uint32_t)p.ldk);
+    wrs = make_rsrc(w + (size_t)n0 * p.ldk, wrows * (uint32_t)p.ldk);
+    srs = make_rsrc(scale_x ? p.xs : ws, 0x7FFFFFFFu);
 #pragma unroll
-  for (int j = 0; j < T::kCopiesX; ++j)
-    xoff[j] = (uint32_t)x_row(8 * (wave * T::kCopiesX + j) + (lane >> 3)) * (uint32_t)p.ldk + (uint32_t)chunk;
+    for (int j = 0; j < T::kCopiesX; ++j)
+      xoff[j] = (uint32_t)x_row(8 * (wave * T::kCopiesX + j) + (lane >> 3)) * (uint32_t)p.ldk + (uint32_t)chunk;
 #pragma unroll
-  for (int j = 0; j < T::kCopiesW; ++j)
-    woff[j] = (uint32_t)(weight_row(8 * (wave * T::kCopiesW + j) + (lane >> 3)) - n0) * (uint32_t)p.ldk + (uint32_t)chunk;
-  // and a scale: the first waves' lanes take x's rows', the next ones the weight's
-  const bool scale_x = wave < T::kScalesX / 64;
-  uint32_t soff;
-  {
+    for (int j = 0; j < T::kCopiesW; ++j)
+      woff[j] = (uint32_t)(weight_row(8 * (wave * T::kCopiesW + j) + (lane >> 3)) - n0) * (uint32_t)p.ldk + (uint32_t)chunk;
+    // and a scale: the first waves' lanes take x's rows', the next ones the weight's
     const int r = scale_x ? (int)threadIdx.x : (int)threadIdx.x - T::kScalesX;
     if (scale_x) {
       const int src = x_row(r);
@@ -221,9 +182,91 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
       soff = (uint32_t)(weight_row(r) >> 7) * (uint32_t)p.KB * 4u;
     }
     if (r >= (scale_x ? BM : BN)) soff = kOutOfRange;
-  }
-  const __amdgpu_buffer_rsrc_t srs = make_rsrc(scale_x ? p.xs : p.ws, 0x7FFFFFFFu);
-  const uint32_t sstep = scale_x ? (uint32_t)p.xs_ld * 4u : WROWS ? (uint32_t)N * 4u : 4u;
+    // Lines that are not in L2 yet hold the tiles that share them up for as long as memory takes. So a block's lines
+    // are touched some blocks ahead (into LDS that nothing reads), by lane r that of tile row r: of the weight's rows an
+    // eighth, of x's a quarter, as about eight and four tiles that run at once on an XCD share them (2048 rows of
+    // 8192x28672: 475 -> 424 us; every row by every tile 462).
+    if constexpr (T::kTouch > 0) {
+      const int i = touch_x ? (int)threadIdx.x : (int)threadIdx.x - BM;
+      toff = kOutOfRange;
+      if (touch_x ? i % 4 == tn % 4 : i % 8 == tm % 8)
+        toff = (uint32_t)(touch_x ? x_row(i) : weight_row(i) - n0) * (uint32_t)p.ldk;
+    }
+  };
+
+  // The next tile that has something to multiply, or false
+  int turn = blockIdx.x;
+  const int live = MODE == GROUPED ? min(p.groups.plan[p.groups.list], p.tiles_m) : p.tiles_m;
+  const int tiles = live * p.tiles_n;
+  const int turns = MODE == DENSE && p.first > 0 ? 2 * (tiles - p.first) : tiles;
+  auto next_tile = [&]() __attribute__((always_inline)) -> bool {
+    if (turn >= turns) return false;
+    do {
+      int t = tile_of(turn, turns), e = 0, half = 0;
+      turn += gridDim.x;
+      if constexpr (MODE == DENSE) {
+        if (p.first > 0) {  // what whole rounds of tiles twice as high have left: the halves of their tiles from the first one on
+          half = t & 1;
+          t = p.first + (t >> 1);
+        }
+      }
+      // (a group's tiles go over all XCDs: groups differ in their rows)
+      if constexpr (MODE == BY_GROUP) e = blockIdx.y;
+      const int tm = MODE == DENSE && p.first > 0 ? 2 * (t % live) + half : t % live, tn = t / live;  // neighbours share the weight's rows
+      const uint8_t* w = p.w;
+      const float* ws = p.ws;
+      n0 = tn * OUT;
+      m0 = tm * BM;
+      int end = p.M;
+      kb0 = 0;
+      kb1 = p.KB;
+      if constexpr (MODE == DENSE) {
+        if (m0 >= p.M) continue;
+        kb0 = min((int)blockIdx.y * p.slice, p.KB);
+        kb1 = min(kb0 + p.slice, p.KB);
+        out_row = (size_t)blockIdx.y * p.M;
+      }
+      if constexpr (MODE == GROUPED) {
+        group_tile(p.groups, tm, e, m0, end);
+        if constexpr (BM > 128) {
+          // the list's tiles have 128 rows: every second one of a group stands for itself and the next
+          const int first = e < p.groups.E ? p.groups.plan[e] : p.groups.plan[p.groups.E];
+          const int last = e < p.groups.E ? p.groups.plan[e + 1] : p.M;
+          if ((m0 - first) % BM) continue;
+          end = min(m0 + BM, last);
+        }
+        if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
+          if (GLU && OUT == 128 && p.out_dtype == kE4M3) {
+            uint8_t* const codes = static_cast<uint8_t*>(p.out);
+            const int cols = min(OUT, N - n0);
+            for (int i = threadIdx.x; i < (end - m0) * cols; i += T::kThreads)
+              codes[(size_t)(m0 + i / cols) * N + n0 + i % cols] = 0;
+            for (int i = threadIdx.x; i < end - m0; i += T::kThreads)
+              p.out_scales[(size_t)(n0 / 128) * p.scale_rows + m0 + i] = kLeastScale;
+          } else {
+            zero_tile(p.out, p.out_dtype, m0, end - m0, N, n0, OUT);
+          }
+          continue;
+        }
+        w += (size_t)e * (GLU ? 2 : 1) * N * p.ldk;
+        ws += (size_t)e * (GLU ? 2 * p.up_blocks : (N + 127) / 128) * p.KB;
+      }
+      if constexpr (MODE == BY_GROUP) {
+        // group e's blocks of k are its 128-row tiles: as many as earlier groups have come before them
+        int before = 0;
+        for (int g = lane; g < e; g += 64) before += (p.groups.plan[g + 1] - p.groups.plan[g] + 127) / 128;
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor(before, o);
+        kb0 = __builtin_amdgcn_readfirstlane(before);
+        kb1 = kb0 + __builtin_amdgcn_readfirstlane((p.groups.plan[e + 1] - p.groups.plan[e] + 127) / 128);
+        out_row = (size_t)e * p.M;
+      }
+      rows = min(BM, end - m0);
+      set(w, ws, tm, tn);
+      return true;
+    } while (LOOP && turn < turns);
+    return false;
+  };
 
   // copy j of a block: x's rows, the weight's, the scales
   auto copy = [&](int j, int kb, int stage) __attribute__((always_inline)) {
@@ -240,28 +283,19 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
       buffer_copy4_to_lds(srs, kb < kb1 ? soff : kOutOfRange, kb * sstep, dst + T::kCodes + wave * 256);
     }
   };
-
-  // Lines that are not in L2 yet hold the tiles that share them up for as long as memory takes. So a block's lines are
-  // touched some blocks ahead (into LDS that nothing reads), by lane r that of tile row r: of the weight's rows an eighth, of
-  // x's a quarter, as about eight and four tiles that run at once on an XCD share them (2048 rows of 8192x28672: 475 -> 424 us;
-  // every row by every tile 462).
-  uint32_t toff = kOutOfRange;
-  const bool touch_x = wave < BM / 64;
-  if constexpr (T::kTouch > 0) {
-    const int r = touch_x ? (int)threadIdx.x : (int)threadIdx.x - BM;
-    if (touch_x ? r % 4 == tn % 4 : r % 8 == tm % 8)
-      toff = (uint32_t)(touch_x ? x_row(r) : weight_row(r) - n0) * (uint32_t)p.ldk;
-  }
   auto touch = [&](int kb) __attribute__((always_inline)) {
     if constexpr (T::kTouch > 0)
       buffer_copy4_to_lds(touch_x ? xrs : wrs, kb < kb1 ? toff : kOutOfRange, kb * 128, lds8 + ST * T::kStage + wave * 256);
   };
+  auto first_copies = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+#pragma unroll
+      for (int j = 0; j < T::kLoads; ++j) copy(j, kb0 + i, i);
+    touch(kb0 + ST - 1);
+  };
 
   f4_t acc[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f4_t{0.f, 0.f, 0.f, 0.f};
 
   // first tile row (of the weight) of this wave's 16 outputs nt
   auto nrow = [&](int nt) __attribute__((always_inline)) {
@@ -272,40 +306,30 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
   // The sums of the last 16 rows multiplied, and their factors: added to the running sums while the next ones'
   // MFMAs run (over the end of a block too)
   f4_t part[NT];
-  float fac[2] = {0.f, 0.f};
-  f4_t facr[WROWS ? NT : 1];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) part[nt] = f4_t{0.f, 0.f, 0.f, 0.f};
-  if constexpr (WROWS) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) facr[nt] = part[nt];
-  }
+  float fac[2];
+  // scales of the weight's blocks (one of the wave's rows stands for all; GLU: one of each half), or of its rows
+  float sw[2];
+  f4_t swr[WROWS ? NT : 1];
   auto add = [&](int nt, int mt) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float f = GLU && nt >= NT / 2 ? fac[1] : fac[0];
-      if constexpr (WROWS) f = fac[0] * facr[nt][i];
+      if constexpr (WROWS) f = fac[0] * swr[nt][i];
       acc[nt][mt][i] = __builtin_fmaf(part[nt][i], f, acc[nt][mt][i]);
     }
   };
 
-  typedef typename std::conditional<EXACT, Wide, i8v_t>::type Frag;
   auto stage_x = [&](int stage) __attribute__((always_inline)) { return lds8 + stage * T::kStage; };
   auto read_b = [&](int stage, int mt) __attribute__((always_inline)) {
     return read_fragment(stage_x(stage), (wm * MT + mt) * 16 + l16, q);
   };
-  auto read_a = [&](int stage, int nt) __attribute__((always_inline)) -> Frag {
-    const i8v_t f = read_fragment(stage_x(stage) + BM * 128, nrow(nt) + l16, q);
-    if constexpr (EXACT) return widen(f);
-    else return f;
+  auto read_a = [&](int stage, int nt) __attribute__((always_inline)) {
+    return read_fragment(stage_x(stage) + BM * 128, nrow(nt) + l16, q);
   };
   auto scales_x = [&](int stage) __attribute__((always_inline)) {
     return reinterpret_cast<const float*>(stage_x(stage) + T::kCodes);
   };
-  // block scales: one of the wave's rows stands for all (GLU: one of each half)
-  Frag a[NT];
-  float sw[2];
-  f4_t swr[WROWS ? NT : 1];
+  i8v_t a[NT];
   auto read_sw = [&](int stage) __attribute__((always_inline)) {
     const float* const wsc = scales_x(stage) + T::kScalesX;
     if constexpr (WROWS) {
@@ -330,19 +354,27 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
   };
-  const int nb = kb1 - kb0;
-  if (nb > 0) {
+  auto multiply = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int j = 0; j < T::kLoads; ++j) copy(j, kb0 + i, i);
-    touch(kb0 + ST - 1);
+      for (int j = 0; j < MT; ++j) acc[i][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) part[nt] = f4_t{0.f, 0.f, 0.f, 0.f};
+    if constexpr (WROWS) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) swr[nt] = part[nt];
+    }
+    fac[0] = fac[1] = 0.f;
     meet();
+    const int nb = kb1 - kb0;
+    if (nb <= 0) return;
     i8v_t b = read_b(0, 0);
     float sx = scales_x(0)[wm * MT * 16 + l16];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) a[nt] = read_a(0, nt);
-    read_sw(0);
+    if (!WROWS) read_sw(0);
+    Wide aw[EXACT ? NT : 1];
     int stage = 0;
     for (int i = 0; i < nb; ++i) {
       const int free = stage == 0 ? ST - 1 : stage - 1, next = stage == ST - 1 ? 0 : stage + 1;
@@ -358,13 +390,17 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
         const int before = mt == 0 ? MT - 1 : mt - 1;
         f4_t now[NT];
         if constexpr (EXACT) {
+          if (mt == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) aw[nt] = widen(a[nt]);
+          }
           const Wide bw = widen(b);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) now[nt] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) now[nt] = mfma16(a[nt].k[s], bw.k[s], now[nt]);
+            for (int nt = 0; nt < NT; ++nt) now[nt] = mfma16(aw[nt].k[s], bw.k[s], now[nt]);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -381,33 +417,31 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
         }
         fac[0] = WROWS ? sx : sx * sw[0];
         if constexpr (GLU) fac[1] = sx * sw[1];
-        if constexpr (WROWS) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) facr[nt] = swr[nt];
-        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) part[nt] = now[nt];
-        if (mt == MT - 1) read_sw(next);
+        // rows' scales are read once the last block's have been used
+        if (WROWS && mt == 0) read_sw(stage);
+        if (!WROWS && mt == MT - 1) read_sw(next);
         b = bn;
         sx = sxn;
         __builtin_amdgcn_sched_barrier(0);
       }
       stage = next;
     }
-  }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) add(nt, MT - 1);
+    for (int nt = 0; nt < NT; ++nt) add(nt, MT - 1);
+  };
 
-  // ---- epilogue ----
-  // Each wave turns 16 rows m by its columns at a time through a slice of LDS of its own, and stores runs of a row.
+  // Each wave turns 16 rows m by its columns at a time through a slice of LDS of its own (in the last stage, which the
+  // next tile's first copies do not fill), and stores runs of a row.
   constexpr int COLS = GLU ? NT / 2 * 16 : NT * 16;  // this wave's columns of out
   constexpr int PITCH = COLS + 4;                    // floats: rows start four banks apart
-  static_assert(T::kWaves * 16 * PITCH * 4 <= (int)T::kLdsBytes, "the waves' slices fit where the tiles were");
-  const int nw = n0 + wn * COLS;                     // its first column
-  wait_loads<0>();
-  __syncthreads();
-  float* const slice = reinterpret_cast<float*>(lds8) + wave * 16 * PITCH;
-  float* const most = reinterpret_cast<float*>(lds8) + T::kWaves * 16 * PITCH;  // [WN][BM], e4m3
+  static_assert(T::kWaves * 16 * PITCH * 4 + T::kWN * BM * 4 <= T::kStage, "the waves' slices and the rows' maxima fit a stage");
+  float* const slices = reinterpret_cast<float*>(lds8 + (ST - 1) * T::kStage);
+  float* const slice = slices + wave * 16 * PITCH;
+  float* const most = slices + T::kWaves * 16 * PITCH;  // [WN][BM], e4m3
+  auto store = [&](int m0, int rows, int n0, size_t out_row) __attribute__((always_inline)) {
+  const int nw = n0 + wn * COLS;  // this wave's first column
   if constexpr (GLU) {
 #pragma unroll
     for (int nt = 0; nt < NT / 2; ++nt)
@@ -416,10 +450,9 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float g = acc[nt][mt][i], u = acc[nt + NT / 2][mt][i];
-          acc[nt][mt][i] = g / (1.0f + __expf(-g)) * u;
+          acc[nt][mt][i] = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;  // the reciprocal to 1 ulp
         }
     if (OUT == 128 && p.out_dtype == kE4M3) {
-      static_assert(T::kWaves * 16 * PITCH * 4 + T::kWN * BM * 4 <= (int)T::kLdsBytes, "and the rows' maxima");
       // the largest |h| of a row over the tile's 128 columns: this wave's, then all waves' of the row
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -510,6 +543,35 @@ __device__ __forceinline__ void fp8_tile(TileParams p, uint8_t* lds8, int tm, in
     }
     __builtin_amdgcn_wave_barrier();
   }
+  };
+
+  if constexpr (LOOP) {
+    bool multiplied = false;
+    int at_m = 0, at_rows = 0, at_n = 0;
+    size_t at_row = 0;
+    while (true) {
+      const bool more = next_tile();
+      if (more) first_copies();
+      if (multiplied) store(at_m, at_rows, at_n, at_row);
+      if (!more) break;
+      multiply();
+      at_m = m0;
+      at_rows = rows;
+      at_n = n0;
+      at_row = out_row;
+      multiplied = true;
+      // every wave is done with the stages, and its last copies (of nothing) have landed
+      wait_loads<0>();
+      __syncthreads();
+    }
+  } else {
+    if (!next_tile()) return;
+    first_copies();
+    multiply();
+    wait_loads<0>();
+    __syncthreads();
+    store(m0, rows, n0, out_row);
+  }
 }
 
 // Kinds of kernel, by the rows of x of a tile
@@ -520,27 +582,9 @@ typedef Tile<4, 2, 4, 4, 3, 2> Half;      // 128, 256
 typedef Tile<4, 2, 4, 8, 2, 3, 3> Whole;  // 256, 256: results of 16 bits only (widened fragments would not fit)
 
 template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
-__global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
-  const int tiles = p.tiles_m * p.tiles_n;
-  int tm, tn;
-  if (MODE == DENSE && p.first > 0) {
-    // what whole rounds of tiles twice as high have left: the halves of their tiles from the first one on
-    const int b = tile_of(blockIdx.x, 2 * (tiles - p.first)), t = p.first + (b >> 1);
-    tm = 2 * (t % p.tiles_m) + (b & 1);
-    tn = t / p.tiles_m;
-    if (tm * T::kBM >= p.M) return;
-  } else {
-    const int t = tile_of(blockIdx.x, MODE == DENSE ? gridDim.x : tiles);  // neighbours share the weight's rows
-    tm = t % p.tiles_m;
-    tn = t / p.tiles_m;
-  }
-  fp8_tile<T, GLU, WROWS, MODE, EXACT>(p, lds8, tm, tn);
-}
-
-template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
 hipError_t launch_tile(const TileParams& p, unsigned grid, int gy, hipStream_t s) {
-  hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT>), dim3(grid, gy), dim3(T::kThreads), T::kLdsBytes, s, p);
+  constexpr bool LOOP = std::is_same<T, Half>::value && MODE != BY_GROUP;
+  hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT, LOOP>), dim3(grid, gy), dim3(T::kThreads), T::kLdsBytes, s, p);
   return hipGetLastError();
 }
 
