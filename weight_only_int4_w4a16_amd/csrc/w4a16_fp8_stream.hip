@@ -10,7 +10,9 @@ namespace {
 // (one row of 8192x10240, 16 columns, four waves: 18.6 us with two, 19.3, 25.6, 34.9 with four, six and eight)
 template <int NT, int XC, int W, bool GLU, bool GROUPED>
 hipError_t run(const StreamParams& p, unsigned grid, hipStream_t s) {
-  hipLaunchKernelGGL((fp8_stream_kernel<NT, XC, 2, W, GLU, GROUPED>), dim3(grid), dim3(64 * W), (Stream<NT, XC, 2>::lds_bytes(W)), s, p);
+  constexpr size_t lds = Stream<NT, XC, 2>::lds_bytes(W);
+  if (p.once) hipLaunchKernelGGL((fp8_stream_kernel<NT, XC, 2, W, GLU, GROUPED, true>), dim3(grid), dim3(64 * W), lds, s, p);
+  else hipLaunchKernelGGL((fp8_stream_kernel<NT, XC, 2, W, GLU, GROUPED, false>), dim3(grid), dim3(64 * W), lds, s, p);
   return hipGetLastError();
 }
 

@@ -28,6 +28,7 @@ struct StreamParams {
   int ldk, xs_ld;
   int up_blocks;  // GLU: blocks of a half
   int slice;      // blocks of k a wave
+  bool once;      // the weight is read past the caches
   int tiles_n, tiles_m;
   GroupTiles groups;
 };
@@ -50,7 +51,7 @@ struct Stream {
   }
 };
 
-template <int NT, int XC, int D, int W, bool GLU, bool GROUPED>
+template <int NT, int XC, int D, int W, bool GLU, bool GROUPED, bool ONCE>
 __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   typedef Stream<NT, XC, D> S;
   static_assert(!GLU || NT % 2 == 0, "a SwiGLU workgroup holds gate rows and the matching up rows");
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     const bool in_k = i < nb && kb * 128 + chunk < p.K;
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j)
-      buffer_copy16_to_lds(wrs, in_k ? woff[j] : kOutOfRange, kb * 128, reinterpret_cast<uint16_t*>(dst + j * 1024));
+      buffer_copy_weight_to_lds<ONCE>(wrs, in_k ? woff[j] : kOutOfRange, kb * 128, dst + j * 1024);
 #pragma unroll
     for (int j = 0; j < XC; ++j)
       buffer_copy16_to_lds(xrs, in_k ? xoff[j] : kOutOfRange, kb * 128,

@@ -49,7 +49,13 @@ struct TileParams {
   int ldk, xs_ld;
   int up_blocks;     // GLU: blocks of a half
   int tiles_m, tiles_n;
-  int first;         // DENSE, over 0: the launch takes the tiles of twice its height from here on (tiles_m counts those)
+  // tiles of up to 64 rows, over 0: column tile tn starts its blocks of k at the tn-th, so that workgroups side by side do
+  // not ask the same channels of memory for rows that lie a power of two apart
+  int turn;
+  bool once;         // the weight is read past the caches
+  // DENSE: the launch takes `count` tiles from the first on; or, with first over 0, the tiles of twice its height from there
+  // on in halves (tiles_m counts those)
+  int count, first;
   int slice;         // DENSE: blocks of k of a workgroup; slice blockIdx.y's sums go to out + blockIdx.y M N (fp32)
   int scale_rows;    // rows of out_scales' blocks
   GroupTiles groups;
@@ -97,6 +103,15 @@ __device__ __forceinline__ i8v_t read_fragment(const uint8_t* tile, int row, int
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// The weight's copies: non-temporal (ONCE) where few rows read a weight that the last-level cache (256 MiB) would not hold for
+// the next call anyway (one row of 8192x57344 83.8 -> 75.7 us, of 28672x8192 41.9 -> 37.7). A small one may be found
+// there: sixteen rows of 8192x10240 take 18.6 us cold and 18.0 non-temporal, but 15 where the last 252 MB read were three such.
+constexpr long long kOnceBytes = 128LL << 20;
+template <bool ONCE>
+__device__ __forceinline__ void buffer_copy_weight_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, (int)voff, (int)soff, 0, ONCE ? 2 : 0);
+}
+
 // 4 bytes per lane from global memory straight into LDS
 __device__ __forceinline__ void buffer_copy4_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, (int)voff, (int)soff, 0, 0);
@@ -124,7 +139,7 @@ struct Tile {
 
 // LOOP: a workgroup takes tiles blockIdx.x, blockIdx.x + gridDim.x, ..., and the first blocks of the next one are on their way
 // while it stores the last; else tile blockIdx.x alone. The loop's tiles cost the 256-row ones spills.
-template <class T, bool GLU, bool WROWS, int MODE, bool EXACT, bool LOOP>
+template <class T, bool GLU, bool WROWS, int MODE, bool EXACT, bool LOOP, bool ONCE>
 __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   constexpr int NT = T::kNT, MT = T::kMT, BN = T::kBN, BM = T::kBM;
   constexpr int OUT = GLU ? BN / 2 : BN;  // columns of out that a tile makes
@@ -137,7 +152,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   const bool gathered = MODE == GROUPED && p.groups.tokens;
 
   // ---- the tile at hand ----
-  int m0 = 0, rows = 0, n0 = 0, kb0 = 0, kb1 = 0;
+  int m0 = 0, rows = 0, n0 = 0, kb0 = 0, kb1 = 0, turned = 0;
   size_t out_row = 0;
   __amdgpu_buffer_rsrc_t xrs, wrs, srs;
   uint32_t xoff[T::kCopiesX], woff[T::kCopiesW], soff = 0, toff = 0;
@@ -198,7 +213,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   int turn = blockIdx.x;
   const int live = MODE == GROUPED ? min(p.groups.plan[p.groups.list], p.tiles_m) : p.tiles_m;
   const int tiles = live * p.tiles_n;
-  const int turns = MODE == DENSE && p.first > 0 ? 2 * (tiles - p.first) : tiles;
+  const int turns = MODE != DENSE ? tiles : p.first > 0 ? 2 * (tiles - p.first) : p.count;
   auto next_tile = [&]() __attribute__((always_inline)) -> bool {
     if (turn >= turns) return false;
     do {
@@ -262,6 +277,10 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
         out_row = (size_t)e * p.M;
       }
       rows = min(BM, end - m0);
+      if constexpr (BM <= 64) {
+        const int nb = kb1 - kb0;
+        turned = p.turn && nb > 0 ? tn % nb : 0;
+      }
       set(w, ws, tm, tn);
       return true;
     } while (LOOP && turn < turns);
@@ -269,30 +288,32 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   };
 
   // copy j of a block: x's rows, the weight's, the scales
-  auto copy = [&](int j, int kb, int stage) __attribute__((always_inline)) {
+  auto copy = [&](int j, int i, int stage) __attribute__((always_inline)) {
     uint8_t* const dst = lds8 + stage * T::kStage;
-    const bool in_k = kb < kb1 && kb * 128 + chunk < p.K;
+    const bool live = i < kb1 - kb0;
+    int kb = kb0 + i + turned;
+    kb = kb >= kb1 ? kb - (kb1 - kb0) : kb;
+    const bool in_k = live && kb * 128 + chunk < p.K;
     if (j < T::kCopiesX) {
       buffer_copy16_to_lds(xrs, in_k ? xoff[j] : kOutOfRange, kb * 128,
                            reinterpret_cast<uint16_t*>(dst + (wave * T::kCopiesX + j) * 1024));
     } else if (j < T::kCopiesX + T::kCopiesW) {
-      const int i = j - T::kCopiesX;
-      buffer_copy16_to_lds(wrs, in_k ? woff[i] : kOutOfRange, kb * 128,
-                           reinterpret_cast<uint16_t*>(dst + BM * 128 + (wave * T::kCopiesW + i) * 1024));
+      const int c = j - T::kCopiesX;
+      buffer_copy_weight_to_lds<ONCE>(wrs, in_k ? woff[c] : kOutOfRange, kb * 128, dst + BM * 128 + (wave * T::kCopiesW + c) * 1024);
     } else {
-      buffer_copy4_to_lds(srs, kb < kb1 ? soff : kOutOfRange, kb * sstep, dst + T::kCodes + wave * 256);
+      buffer_copy4_to_lds(srs, live ? soff : kOutOfRange, live ? kb * sstep : 0u, dst + T::kCodes + wave * 256);
     }
   };
-  auto touch = [&](int kb) __attribute__((always_inline)) {
+  auto touch = [&](int i) __attribute__((always_inline)) {
     if constexpr (T::kTouch > 0)
-      buffer_copy4_to_lds(touch_x ? xrs : wrs, kb < kb1 ? toff : kOutOfRange, kb * 128, lds8 + ST * T::kStage + wave * 256);
+      buffer_copy4_to_lds(touch_x ? xrs : wrs, i < kb1 - kb0 ? toff : kOutOfRange, (kb0 + i) * 128, lds8 + ST * T::kStage + wave * 256);
   };
   auto first_copies = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i)
 #pragma unroll
-      for (int j = 0; j < T::kLoads; ++j) copy(j, kb0 + i, i);
-    touch(kb0 + ST - 1);
+      for (int j = 0; j < T::kLoads; ++j) copy(j, i, i);
+    touch(ST - 1);
   };
 
   f4_t acc[NT][MT];
@@ -381,8 +402,8 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int j = mt * ISSUE; j < (mt + 1) * ISSUE && j < T::kLoads; ++j) copy(j, kb0 + i + ST - 1, free);
-        if (mt == (T::kLoads + ISSUE - 1) / ISSUE) touch(kb0 + i + T::kTouch);
+        for (int j = mt * ISSUE; j < (mt + 1) * ISSUE && j < T::kLoads; ++j) copy(j, i + ST - 1, free);
+        if (mt == (T::kLoads + ISSUE - 1) / ISSUE) touch(i + T::kTouch);
         if (mt == MT - 1) meet();
         const i8v_t bn = mt + 1 < MT ? read_b(stage, mt + 1) : read_b(next, 0);
         const float sxn = mt + 1 < MT ? scales_x(stage)[(wm * MT + mt + 1) * 16 + l16] : scales_x(next)[wm * MT * 16 + l16];
@@ -584,7 +605,14 @@ typedef Tile<4, 2, 4, 8, 2, 3, 3> Whole;  // 256, 256: results of 16 bits only (
 template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
 hipError_t launch_tile(const TileParams& p, unsigned grid, int gy, hipStream_t s) {
   constexpr bool LOOP = std::is_same<T, Half>::value && MODE != BY_GROUP;
-  hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT, LOOP>), dim3(grid, gy), dim3(T::kThreads), T::kLdsBytes, s, p);
+  const dim3 blocks(grid, gy), threads(T::kThreads);
+  if constexpr (T::kBM <= 64 && !WROWS) {
+    if (p.once) {
+      hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT, LOOP, true>), blocks, threads, T::kLdsBytes, s, p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT, LOOP, false>), blocks, threads, T::kLdsBytes, s, p);
   return hipGetLastError();
 }
 
