@@ -896,23 +896,17 @@ def lora_add(y, x, lora_a, lora_b, ids, scaling, routing: Routing | None = None,
 # scratch is torch's own (a call's alone, whatever stream or graph it is in).
 
 
-class _Device:
-    """Makes a tensor's device the current one for a launch."""
-
-    __slots__ = ("index", "before")
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        torch = _torch()
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *_):
-        if self.before != self.index:
-            _torch().cuda.set_device(self.before)
+def _fp8_call(f, name, device, *args):
+    """One call on ``device``, made the current one for the launch, with its current stream."""
+    torch = _torch()
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, _raw_stream(device))
+    if st:
+        _check(st, name)
 
 
 def _fp8_values(x, name):
@@ -945,10 +939,8 @@ def quantize_fp8(x):
     M, K, dt = _fp8_values(x, "x")
     codes = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
     scales = x.new_empty((_up128(K), M), dtype=torch.float32)
-    with _Device(x.device.index):
-        st = lib().w4a16_quantize_fp8(x.data_ptr(), M, K, dt, codes.data_ptr(), scales.data_ptr(), _raw_stream(x.device))
-    if st:
-        _check(st, "w4a16_quantize_fp8")
+    _fp8_call(lib().w4a16_quantize_fp8, "w4a16_quantize_fp8", x.device, x.data_ptr(), M, K, dt, codes.data_ptr(),
+              scales.data_ptr())
     return codes, scales
 
 
@@ -959,11 +951,8 @@ def quantize_fp8_columns(x):
     M, K, dt = _fp8_values(x, "x")
     codes = x.new_empty((K, (M + 15) // 16 * 16), dtype=torch.float8_e4m3fn)
     scales = x.new_empty((_up128(M), K), dtype=torch.float32)
-    with _Device(x.device.index):
-        st = lib().w4a16_quantize_fp8_columns(x.data_ptr(), M, K, dt, codes.data_ptr(), scales.data_ptr(),
-                                              _raw_stream(x.device))
-    if st:
-        _check(st, "w4a16_quantize_fp8_columns")
+    _fp8_call(lib().w4a16_quantize_fp8_columns, "w4a16_quantize_fp8_columns", x.device, x.data_ptr(), M, K, dt,
+              codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -980,11 +969,8 @@ def quantize_fp8_weight(w, transposed: bool = False):
         codes_t = w.new_empty((K, N), dtype=torch.float8_e4m3fn)
         scales_t = w.new_empty((_up128(K), _up128(N)), dtype=torch.float32)
         cp, sp = codes_t.data_ptr(), scales_t.data_ptr()
-    with _Device(w.device.index):
-        st = lib().w4a16_quantize_fp8_weight(w.data_ptr(), N, K, dt, codes.data_ptr(), scales.data_ptr(), cp, sp,
-                                             _raw_stream(w.device))
-    if st:
-        _check(st, "w4a16_quantize_fp8_weight")
+    _fp8_call(lib().w4a16_quantize_fp8_weight, "w4a16_quantize_fp8_weight", w.device, w.data_ptr(), N, K, dt,
+              codes.data_ptr(), scales.data_ptr(), cp, sp)
     return (codes, scales, codes_t, scales_t) if transposed else (codes, scales)
 
 
@@ -1076,11 +1062,8 @@ def _gemm_fp8(x, codes, scales, x_scales, glu, quantized, out_dtype, out, worksp
     out, dt, out_scales = _fp8_out(x, x_dt, M, N // 2 if glu else N, glu, quantized, out_dtype, out)
     L = lib()
     ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_workspace_bytes(M, K, N, x_dt, glu, dt), workspace)
-    with _Device(device.index):
-        st = L.w4a16_gemm_fp8(x.data_ptr(), x_dt, xsp, M, K, N, cp, sp, glu, out.data_ptr(), dt,
-                              None if out_scales is None else out_scales.data_ptr(), wp, nbytes, _raw_stream(device))
-    if st:
-        _check(st, "w4a16_gemm_fp8")
+    _fp8_call(L.w4a16_gemm_fp8, "w4a16_gemm_fp8", device, x.data_ptr(), x_dt, xsp, M, K, N, cp, sp, glu, out.data_ptr(), dt,
+              None if out_scales is None else out_scales.data_ptr(), wp, nbytes)
     return (out, out_scales) if quantized else out
 
 
@@ -1124,12 +1107,9 @@ def _gemm_fp8_grouped(x, routing, codes, scales, x_scales, glu, quantized, gathe
     L, gather = lib(), int(gather)
     need = L.w4a16_fp8_grouped_workspace_bytes(r.tokens, r.topk, r.groups, gather, K, N, x_dt, glu, dt)
     ws, wp, nbytes = _fp8_scratch(x, need, workspace)
-    with _Device(device.index):
-        st = L.w4a16_gemm_fp8_grouped(x.data_ptr(), x_dt, xsp, r.plan.data_ptr(), r.tokens, r.topk, r.groups, gather, K, N,
-                                      cp, sp, glu, out.data_ptr(), dt, None if out_scales is None else out_scales.data_ptr(),
-                                      wp, nbytes, _raw_stream(device))
-    if st:
-        _check(st, "w4a16_gemm_fp8_grouped")
+    _fp8_call(L.w4a16_gemm_fp8_grouped, "w4a16_gemm_fp8_grouped", device, x.data_ptr(), x_dt, xsp, r.plan.data_ptr(), r.tokens,
+              r.topk, r.groups, gather, K, N, cp, sp, glu, out.data_ptr(), dt,
+              None if out_scales is None else out_scales.data_ptr(), wp, nbytes)
     return (out, out_scales) if quantized else out
 
 
@@ -1186,11 +1166,8 @@ def gemm_fp8_backward(dy, x, codes_t, scales_t, workspace=None):
     dw = x.new_empty((N, K), dtype=torch.float32)
     L = lib()
     ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_backward_workspace_bytes(M, K, N), workspace)
-    with _Device(x.device.index):
-        st = L.w4a16_gemm_fp8_backward(yp, xp, M, K, N, dt, cp, sp, dx.data_ptr(), dw.data_ptr(), wp, nbytes,
-                                       _raw_stream(x.device))
-    if st:
-        _check(st, "w4a16_gemm_fp8_backward")
+    _fp8_call(L.w4a16_gemm_fp8_backward, "w4a16_gemm_fp8_backward", x.device, yp, xp, M, K, N, dt, cp, sp, dx.data_ptr(),
+              dw.data_ptr(), wp, nbytes)
     return dx, dw
 
 
@@ -1208,11 +1185,8 @@ def gemm_fp8_grouped_backward(dy, x, routing: Routing, codes_t, scales_t, worksp
     L = lib()
     need = L.w4a16_fp8_grouped_backward_workspace_bytes(r.tokens, r.topk, r.groups, K, N)
     ws, wp, nbytes = _fp8_scratch(x, need, workspace)
-    with _Device(x.device.index):
-        st = L.w4a16_gemm_fp8_grouped_backward(yp, xp, r.plan.data_ptr(), r.tokens, r.topk, r.groups, K, N, dt, cp, sp,
-                                               dx.data_ptr(), dw.data_ptr(), wp, nbytes, _raw_stream(x.device))
-    if st:
-        _check(st, "w4a16_gemm_fp8_grouped_backward")
+    _fp8_call(L.w4a16_gemm_fp8_grouped_backward, "w4a16_gemm_fp8_grouped_backward", x.device, yp, xp, r.plan.data_ptr(),
+              r.tokens, r.topk, r.groups, K, N, dt, cp, sp, dx.data_ptr(), dw.data_ptr(), wp, nbytes)
     return dx, dw
 
 

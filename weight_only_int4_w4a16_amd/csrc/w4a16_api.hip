@@ -733,7 +733,8 @@ static size_t fp8_rows_bytes(int M, int K) {
 // A product's operands; 16-bit x is quantized into the workspace first
 static w4a16_status fp8_operands(w4a16::Fp8Args& a, const void* x, w4a16_dtype x_dtype, const float* x_scales,
                                  int x_rows, int K, int N, const uint8_t* codes, const float* scales, int swiglu,
-                                 void* out, w4a16_dtype out_dtype, float* out_scales, void* workspace, void* stream) {
+                                 void* out, w4a16_dtype out_dtype, float* out_scales, void* workspace, void* stream,
+                                 bool dense) {
   char* ws = static_cast<char*>(workspace);
   a.K = a.ldk = K;
   a.N = swiglu ? N / 2 : N;
@@ -748,6 +749,9 @@ static w4a16_status fp8_operands(w4a16::Fp8Args& a, const void* x, w4a16_dtype x
   if (is_e4m3(x_dtype)) {
     a.x = static_cast<const uint8_t*>(x);
     a.xs = x_scales;
+  } else if (dense && w4a16::fp8_takes_values(x_rows, a.N, K, a.glu)) {
+    a.values = x;
+    a.values_dtype = (int)x_dtype;
   } else {
     uint8_t* const xq = reinterpret_cast<uint8_t*>(ws);
     float* const xs = reinterpret_cast<float*>(ws + w4a16::align256((size_t)x_rows * K));
@@ -763,7 +767,8 @@ static w4a16_status fp8_operands(w4a16::Fp8Args& a, const void* x, w4a16_dtype x
 
 size_t w4a16_fp8_workspace_bytes(int M, int K, int N, w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
   if (check_fp8(M, K, N, x_dtype, swiglu, out_dtype) != W4A16_OK || M == 0) return 0;
-  return (is_e4m3(x_dtype) ? 0 : fp8_rows_bytes(M, K)) +
+  const bool codes = is_e4m3(x_dtype) || w4a16::fp8_takes_values(M, swiglu ? N / 2 : N, K, swiglu != 0);
+  return (codes ? 0 : fp8_rows_bytes(M, K)) +
          w4a16::fp8_scratch_bytes(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype);
 }
 
@@ -780,7 +785,7 @@ w4a16_status w4a16_gemm_fp8(const void* x, w4a16_dtype x_dtype, const float* x_s
   if (st != W4A16_OK) return st;
   w4a16::Fp8Args a{};
   a.M = M;
-  st = fp8_operands(a, x, x_dtype, x_scales, M, K, N, codes, scales, swiglu, out, out_dtype, out_scales, workspace, stream);
+  st = fp8_operands(a, x, x_dtype, x_scales, M, K, N, codes, scales, swiglu, out, out_dtype, out_scales, workspace, stream, true);
   return st != W4A16_OK ? st : from_hip(w4a16::launch_fp8(a));
 }
 
@@ -822,7 +827,7 @@ w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const fl
   w4a16::Fp8Args a{};
   a.M = r.S;
   st = fp8_operands(a, x, x_dtype, x_scales, gather ? tokens : r.S, K, N, codes, scales, swiglu, out, out_dtype, out_scales,
-                    workspace, stream);
+                    workspace, stream, false);
   return st != W4A16_OK ? st : from_hip(w4a16::launch_fp8_grouped(a, r, plan, gather != 0));
 }
 
@@ -923,7 +928,7 @@ w4a16_status w4a16_gemm_fp8_backward(const void* dy, const void* x, int M, int K
   if (dx) {
     w4a16::Fp8Args a{};
     a.M = M;
-    st = fp8_operands(a, dy, act, nullptr, M, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream);
+    st = fp8_operands(a, dy, act, nullptr, M, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream, true);
     if (st != W4A16_OK) return st;
     const hipError_t e = w4a16::launch_fp8(a);
     if (e != hipSuccess) return W4A16_ERR_HIP;
@@ -976,7 +981,7 @@ w4a16_status w4a16_gemm_fp8_grouped_backward(const void* dy, const void* x, cons
   if (dx) {
     w4a16::Fp8Args a{};
     a.M = r.S;
-    st = fp8_operands(a, dy, act, nullptr, r.S, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream);
+    st = fp8_operands(a, dy, act, nullptr, r.S, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream, false);
     if (st != W4A16_OK) return st;
     const hipError_t e = w4a16::launch_fp8_grouped(a, r, plan, false);
     if (e != hipSuccess) return W4A16_ERR_HIP;

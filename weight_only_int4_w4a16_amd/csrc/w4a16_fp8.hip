@@ -220,7 +220,7 @@ void stream_shape(int M, int N, int K, bool glu, long long cus, long long tiles_
   W = tiles_m * ceil_div(N, glu ? 16 : 16 * NT) <= 2 * cus ? 8 : 4;
 }
 
-hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, hipStream_t s) {
+hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, const void* values, int values_dtype, hipStream_t s) {
   StreamParams p{};
   p.x = t.x;
   p.xs = t.xs;
@@ -237,6 +237,8 @@ hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, hip
   p.up_blocks = t.up_blocks;
   p.groups = t.groups;
   p.once = t.once;
+  p.values = values;
+  p.values_dtype = values_dtype;
   int NT, W;
   p.tiles_m = grouped ? t.groups.bound : ceil_div(t.M, 16);
   // of a grouped launch's tiles at most one a group is part-filled, and those past the list's end leave at once
@@ -245,7 +247,7 @@ hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, hip
   p.tiles_n = ceil_div(t.N, glu ? 8 * NT : 16 * NT);
   p.slice = ceil_div(t.KB, W);
   const unsigned grid = (unsigned)((size_t)p.tiles_m * p.tiles_n);
-  return launch_stream(p, NT, grouped || M > 8 ? 2 : 1, W, glu, grouped, grid, s);
+  return launch_stream(p, NT, values ? 0 : grouped || M > 8 ? 2 : 1, W, glu, grouped, grid, s);
 }
 
 // Workgroups of a launch of so many tiles: with one a compute unit, each takes its share of the tiles in turn
@@ -275,6 +277,15 @@ bool fp8_fits(int M, int N, int K, bool glu) {
   return grid_fits(ceil_div(M, kRows[c.kind]), N, c.kind, glu, c.S) && grid_fits(ceil_div(M, kRows[d.kind]), N, d.kind, glu, d.S);
 }
 
+// One or two rows of 16 bits: each workgroup quantizes the groups that its waves multiply, which saves a launch and its
+// scratch. More rows' groups would take as long as the weight does to arrive.
+bool fp8_takes_values(int M, int N, int K, bool glu) {
+  if (M > 2 || M < 1 || choose(M, glu ? 2 * N : N, K, glu, true).kind != STREAM) return false;
+  int NT, W;
+  stream_shape(M, N, K, glu, device_cu_count(), 1, NT, W);
+  return ceil_div((int)fp8_blocks(K), W) * M <= 64;
+}
+
 size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype) {
   const Plan c = choose(M, glu ? 2 * N : N, K, glu, out_dtype >= 2);
   if (c.S > 1) return align256((size_t)c.S * M * (glu ? 2 * (size_t)N : N) * 4);
@@ -300,7 +311,7 @@ hipError_t launch_fp8(const Fp8Args& a) {
   }
   hipError_t e;
   if (c.kind == STREAM && !a.w_rows) {
-    e = launch_rows16(p, a.M, a.glu, false, a.stream);
+    e = launch_rows16(p, a.M, a.glu, false, a.values, a.values_dtype, a.stream);
   } else {
     const bool glu = a.glu && c.S == 1;
     if (a.glu && !glu) p.N = 2 * a.N;
@@ -390,7 +401,7 @@ hipError_t launch_fp8_grouped(const Fp8Args& a, const RouteLayout& r, const int3
   }
   hipError_t e;
   if (kind == STREAM) {
-    e = launch_rows16(p, 16, a.glu, true, a.stream);
+    e = launch_rows16(p, 16, a.glu, true, nullptr, 0, a.stream);
   } else {
     set_tiles(p, kind, a.glu, p.groups.bound);
     const auto launch = a.glu ? launch_grouped_glu : launch_grouped_plain;

@@ -33,6 +33,8 @@ struct Fp8Args {
   void* out;
   int out_dtype;      // 0 fp16, 1 bf16, 2 fp32, 3 e4m3 (glu: codes with scales)
   float* out_scales;  // [ceil(N / 128)][M], for e4m3
+  const void* values; // x itself, of 16 bits, where the kernel quantizes it (fp8_takes_values; x and xs are not read)
+  int values_dtype;
   float* scratch;     // fp32 h [M][N] where a kernel cannot quantize it by itself
   hipStream_t stream;
 };
@@ -59,6 +61,8 @@ hipError_t launch_fp8_by_group(const Fp8Args& a, const RouteLayout& r, const int
 // bytes of Fp8Args::scratch that a launch needs (0: none)
 size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype);
 size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int K, bool glu, int out_dtype);
+// whether a dense product of 16-bit x quantizes it as it reads it
+bool fp8_takes_values(int M, int N, int K, bool glu);
 bool fp8_fits(int M, int N, int K, bool glu);  // whether launches can index it
 bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu);
 const char* fp8_name(int M, int N, int K, bool glu);
@@ -111,5 +115,75 @@ __device__ __forceinline__ uint32_t max_of_16_lanes(uint32_t v) {
   v = max(v, fp8_dpp<0x122>(v));
   return max(v, fp8_dpp<0x121>(v));
 }
+
+typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
+// 16 bytes at any address that its elements may have
+typedef u4_t u4_any_t __attribute__((aligned(2)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+
+// Eight consecutive values of a row, by their type (as w4a16_dtype)
+template <int DT>
+struct Eight;
+
+template <int DT>
+struct Eight16 {
+  u4_t v;
+  __device__ __forceinline__ void clear() { v = u4_t{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const void* row, size_t i) {
+    v = *reinterpret_cast<const u4_any_t*>(static_cast<const uint16_t*>(row) + i);
+  }
+  __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
+    clear();
+    for (int j = 0; j < 8; ++j)
+      if (j < n) v[j >> 1] |= (uint32_t)static_cast<const uint16_t*>(row)[i + j] << (16 * (j & 1));
+  }
+  __device__ __forceinline__ float value(int j) const {
+    const uint16_t b = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+    if constexpr (DT == 0) return (float)__builtin_bit_cast(_Float16, b);
+    else return __builtin_bit_cast(float, (uint32_t)b << 16);
+  }
+  // magnitudes, two a word
+  static constexpr int kWords = 4;
+  __device__ __forceinline__ uint32_t magnitude(int w) const { return v[w] & 0x7FFF7FFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, a), __builtin_bit_cast(us2_t, b)));
+  }
+  // the bits of a magnitude as a 32-bit float's: of value h of a word, or of the word's largest
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t w, int h) {
+    const uint16_t b = (uint16_t)(w >> (16 * h));
+    if constexpr (DT == 0) return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, b));
+    else return (uint32_t)b << 16;
+  }
+  static __device__ __forceinline__ uint32_t largest_bits(uint32_t w) { return float_bits(max(w & 0xFFFFu, w >> 16), 0); }
+  static constexpr int kPerWord = 2;
+};
+template <>
+struct Eight<0> : Eight16<0> {};
+template <>
+struct Eight<1> : Eight16<1> {};
+template <>
+struct Eight<2> {
+  float v[8];
+  __device__ __forceinline__ void clear() {
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  }
+  __device__ __forceinline__ void load(const void* row, size_t i) {
+    typedef f4_t f4_any_t __attribute__((aligned(4)));
+    const float* p = static_cast<const float*>(row) + i;
+    const f4_t a = *reinterpret_cast<const f4_any_t*>(p), b = *reinterpret_cast<const f4_any_t*>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+  }
+  __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? static_cast<const float*>(row)[i + j] : 0.f;
+  }
+  __device__ __forceinline__ float value(int j) const { return v[j]; }
+  static constexpr int kWords = 8;
+  __device__ __forceinline__ uint32_t magnitude(int w) const { return __builtin_bit_cast(uint32_t, v[w]) & 0x7FFFFFFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t w, int) { return w; }
+  static __device__ __forceinline__ uint32_t largest_bits(uint32_t w) { return w; }
+  static constexpr int kPerWord = 1;
+};
 
 }  // namespace w4a16

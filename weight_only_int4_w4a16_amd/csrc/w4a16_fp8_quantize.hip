@@ -11,80 +11,8 @@ namespace w4a16 {
 
 namespace {
 
-typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
-// 16 bytes at any address that its elements may have
-typedef u4_t u4_any_t __attribute__((aligned(2)));
-typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
 typedef u2_t u2_any_t __attribute__((aligned(1)));
 typedef u4_t u4_byte_t __attribute__((aligned(1)));
-
-// types of values, as w4a16_dtype
-template <int DT>
-struct Eight;  // eight consecutive values of a row
-
-template <int DT>
-struct Eight16 {
-  u4_t v;
-  __device__ __forceinline__ void clear() { v = u4_t{0u, 0u, 0u, 0u}; }
-  __device__ __forceinline__ void load(const void* row, size_t i) {
-    v = *reinterpret_cast<const u4_any_t*>(static_cast<const uint16_t*>(row) + i);
-  }
-  __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
-    clear();
-    for (int j = 0; j < 8; ++j)
-      if (j < n) v[j >> 1] |= (uint32_t)static_cast<const uint16_t*>(row)[i + j] << (16 * (j & 1));
-  }
-  __device__ __forceinline__ float value(int j) const {
-    const uint16_t b = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
-    if constexpr (DT == 0) return (float)__builtin_bit_cast(_Float16, b);
-    else return __builtin_bit_cast(float, (uint32_t)b << 16);
-  }
-  // magnitudes, two a word
-  static constexpr int kWords = 4;
-  __device__ __forceinline__ uint32_t magnitude(int w) const { return v[w] & 0x7FFF7FFFu; }
-  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, a), __builtin_bit_cast(us2_t, b)));
-  }
-  // the bits of a magnitude as a 32-bit float's: of value h of a word, or of the word's largest
-  static __device__ __forceinline__ uint32_t float_bits(uint32_t w, int h) {
-    const uint16_t b = (uint16_t)(w >> (16 * h));
-    if constexpr (DT == 0) return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, b));
-    else return (uint32_t)b << 16;
-  }
-  static __device__ __forceinline__ uint32_t largest_bits(uint32_t w) { return float_bits(max(w & 0xFFFFu, w >> 16), 0); }
-  static constexpr int kPerWord = 2;
-};
-template <>
-struct Eight<0> : Eight16<0> {};
-template <>
-struct Eight<1> : Eight16<1> {};
-template <>
-struct Eight<2> {
-  float v[8];
-  __device__ __forceinline__ void clear() {
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  }
-  __device__ __forceinline__ void load(const void* row, size_t i) {
-    typedef f4_t f4_any_t __attribute__((aligned(4)));
-    const float* p = static_cast<const float*>(row) + i;
-    const f4_t a = *reinterpret_cast<const f4_any_t*>(p), b = *reinterpret_cast<const f4_any_t*>(p + 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-  }
-  __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? static_cast<const float*>(row)[i + j] : 0.f;
-  }
-  __device__ __forceinline__ float value(int j) const { return v[j]; }
-  static constexpr int kWords = 8;
-  __device__ __forceinline__ uint32_t magnitude(int w) const { return __builtin_bit_cast(uint32_t, v[w]) & 0x7FFFFFFFu; }
-  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
-  static __device__ __forceinline__ uint32_t float_bits(uint32_t w, int) { return w; }
-  static __device__ __forceinline__ uint32_t largest_bits(uint32_t w) { return w; }
-  static constexpr int kPerWord = 1;
-};
-
-template <int DT>
-constexpr size_t kValueBytes = DT == 2 ? 4 : 2;
 
 // ---- rows ----
 // Sixteen lanes hold a group of 128, eight values each; a wave takes four groups of R rows, all of whose loads are

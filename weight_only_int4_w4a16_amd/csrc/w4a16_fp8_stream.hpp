@@ -29,6 +29,8 @@ struct StreamParams {
   int up_blocks;  // GLU: blocks of a half
   int slice;      // blocks of k a wave
   bool once;      // the weight is read past the caches
+  const void* values;  // XC 0: x itself, of 16 bits
+  int values_dtype;
   int tiles_n, tiles_m;
   GroupTiles groups;
 };
@@ -37,25 +39,29 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 
-// XC: 1 KiB copies of x a block (eight rows each)
+// XC: 1 KiB copies of x a block (eight rows each), or 0 where each workgroup quantizes x itself
 template <int NT, int XC, int D>
 struct Stream {
-  static constexpr int kSlot = NT * 2048 + XC * 1024 + 256;
-  static constexpr int kLoads = 2 * NT + XC + 1;  // a slot's copies
+  static constexpr int kSlot = NT * 2048 + (XC ? XC * 1024 + 256 : 0);
+  static constexpr int kLoads = 2 * NT + (XC ? XC + 1 : 0);  // a slot's copies
   static constexpr int kWave = D * kSlot;         // bytes of LDS a wave
   static_assert((D - 1) * kLoads < 64, "vmcnt holds 0..63");
   static constexpr int kSums = NT * 256;          // floats a wave
-  static constexpr size_t lds_bytes(int W) {
+  static constexpr size_t ring_bytes(int W) {
     const size_t ring = (size_t)W * kWave, sums = (size_t)W * kSums * 4;
     return ring > sums ? ring : sums;
   }
+  // groups: of x that a wave quantizes (its blocks of k by the rows)
+  static constexpr size_t lds_bytes(int W, int groups) { return ring_bytes(W) + W * group_bytes(groups); }
+  // their codes and scales, 16-byte aligned
+  static constexpr __host__ __device__ size_t group_bytes(int groups) { return ((size_t)groups * (128 + 4) + 15) & ~(size_t)15; }
 };
 
 template <int NT, int XC, int D, int W, bool GLU, bool GROUPED, bool ONCE>
 __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   typedef Stream<NT, XC, D> S;
   static_assert(!GLU || NT % 2 == 0, "a SwiGLU workgroup holds gate rows and the matching up rows");
-  static_assert(XC == 1 || XC == 2, "up to eight rows of x, or sixteen");
+  static_assert(XC == 1 || XC == 2 || (XC == 0 && !GROUPED), "up to eight rows of x, or sixteen");
   constexpr int OUT = (GLU ? NT / 2 : NT) * 16;  // columns of out a workgroup makes
   extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
@@ -85,7 +91,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   const __amdgpu_buffer_rsrc_t wrs = make_rsrc(p.w + (size_t)n0 * p.ldk, wrows * (uint32_t)p.ldk);
   const __amdgpu_buffer_rsrc_t xrs = make_rsrc(p.x + (gathered ? 0 : (size_t)m0 * p.ldk),
                                                (uint32_t)(gathered ? p.groups.tokens : rows) * (uint32_t)p.ldk);
-  uint32_t woff[2 * NT], xoff[XC];
+  uint32_t woff[2 * NT], xoff[XC ? XC : 1];
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
     const int r = 8 * j + (lane >> 3);
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     for (int j = 0; j < XC; ++j)
       buffer_copy16_to_lds(xrs, in_k ? xoff[j] : kOutOfRange, kb * 128,
                            reinterpret_cast<uint16_t*>(dst + NT * 2048 + j * 1024));
-    buffer_copy4_to_lds(srs, i < nb ? soff : kOutOfRange, kb * p.xs_ld * 4, dst + NT * 2048 + XC * 1024);
+    if constexpr (XC > 0) buffer_copy4_to_lds(srs, i < nb ? soff : kOutOfRange, kb * p.xs_ld * 4, dst + NT * 2048 + XC * 1024);
   };
 
   // the blocks' scales of the weight, one for all the workgroup's rows (GLU: of each half): lane l holds block l's
@@ -126,10 +132,53 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   const float* const ws0 = p.ws + (size_t)(n0 >> 7) * KB + kb0;
   const float* const ws1 = GLU ? ws0 + (size_t)p.up_blocks * KB : ws0;
   float wsc0 = lane < nb ? ws0[lane] : 0.f, wsc1 = GLU && lane < nb ? ws1[lane] : 0.f;
+  // XC 0: the wave's groups of x, block by block and row by row, four at a time by sixteen lanes each; the first sixteen
+  // are asked for before the weight
+  const int groups = nb * rows, g16 = lane >> 4;
+  uint8_t* const codes = lds8 + S::ring_bytes(W) + wave * S::group_bytes(p.slice * p.M);
+  float* const code_scales = reinterpret_cast<float*>(codes + (size_t)p.slice * p.M * 128);
+  u4_t asked[4];
+  auto ask = [&](int g) __attribute__((always_inline)) {
+    const int b = g / rows, k = (kb0 + b) * 128 + l16 * 8;
+    return g < groups && k < p.K ? *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(p.values) + (size_t)(m0 + g - b * rows) * p.K + k)
+                                 : u4_t{0u, 0u, 0u, 0u};
+  };
+  auto quantize = [&](int g, u4_t v, auto dtype) __attribute__((always_inline)) {
+    typedef Eight<decltype(dtype)::value> E;
+    E e;
+    e.v = v;
+    uint32_t w = e.magnitude(0);
+#pragma unroll
+    for (int i = 1; i < E::kWords; ++i) w = E::larger(w, e.magnitude(i));
+    const float s = fp8_scale(max_of_16_lanes(E::largest_bits(w)));
+    const Fp8Divisor d = fp8_divisor(s);
+    float c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = fp8_quotient(e.value(j), d);
+    if (g < groups) {
+      *reinterpret_cast<uint2*>(codes + g * 128 + l16 * 8) = uint2{fp8_pack(c[0], c[1], c[2], c[3]), fp8_pack(c[4], c[5], c[6], c[7])};
+      if (l16 == 0) code_scales[g] = s;
+    }
+  };
+  if constexpr (XC == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asked[j] = ask(4 * j + g16);
+  }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < D; ++i) copy(i);
   __builtin_amdgcn_sched_barrier(0);
+  if constexpr (XC == 0) {
+    auto all = [&](auto dtype) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (4 * j < groups) quantize(4 * j + g16, asked[j], dtype);
+      for (int g = 16; g < groups; g += 4) quantize(g + g16, ask(g + g16), dtype);
+    };
+    if (p.values_dtype == 0) all(std::integral_constant<int, 0>{});
+    else all(std::integral_constant<int, 1>{});
+    __builtin_amdgcn_wave_barrier();
+  }
 
   f4_t acc[NT];
 #pragma unroll
@@ -147,8 +196,19 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     const uint8_t* const xt = wt + NT * 2048;
     const float* const xsc = reinterpret_cast<const float*>(xt + XC * 1024);
     // (eight rows' copy: the other lanes read the same rows again, for columns that are not stored)
-    const Wide b = widen(read_fragment(xt, XC == 1 ? l16 & 7 : l16, q));
-    const float sx = xsc[l16];
+    i8v_t bf;
+    float sx;
+    if constexpr (XC == 0) {  // the codes lie in k order; lanes past the rows repeat the last one
+      const int g = i * rows + min(l16, rows - 1);
+      const i4v_t lo = *reinterpret_cast<const i4v_t*>(codes + g * 128 + q * 16);
+      const i4v_t hi = *reinterpret_cast<const i4v_t*>(codes + g * 128 + q * 16 + 64);
+      bf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      sx = code_scales[g];
+    } else {
+      bf = read_fragment(xt, XC == 1 ? l16 & 7 : l16, q);
+      sx = xsc[l16];
+    }
+    const Wide b = widen(bf);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const Wide a = widen(read_fragment(wt, nt * 16 + l16, q));
