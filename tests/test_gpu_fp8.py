@@ -460,6 +460,52 @@ def test_gradients(M, K, N, kind):
     _within(dw.cpu().double().numpy(), ref, bound, "dw")
 
 
+@pytest.mark.parametrize("M,K,N", [(1100, 144, 160), (2085, 256, 128), (5000, 272, 16), (40, 256, 8192), (3, 64, 16384)])
+def test_gradients_with_few_tiles(M, K, N):
+    """Deep products of few tiles, whose depth is cut: their partial sums have room of their own."""
+    import weight_only_int4_w4a16_amd as w4
+    _announce(f"gemm_fp8_backward {M}x{K}x{N}")
+    x, xv = _rows((M, K), "bf16", M + K)
+    dy, dyv = _rows((M, N), "bf16", M + N)
+    codes_t, scales_t, wt = _weight((), K, N, K + N)
+    dx, dw = w4.gemm_fp8_backward(dy, x, codes_t, scales_t)
+    v = F.rows_value(*F.quantize_rows(dyv))
+    ref = F.gemm_fp8_ref(v, wt)
+    _within(dx.cpu().double().numpy(), ref, _stored(ref, _sum_bound(v, wt, "bf16"), "bf16"), "dx")
+    ref, bound = _dw_bound(dyv, xv)
+    _within(dw.cpu().double().numpy(), ref, bound, "dw")
+
+
+@pytest.mark.parametrize("M,K,N", [(130, 144, 272), (1500, 128, 160)])
+def test_one_gradient_alone(M, K, N):
+    """A call for dx or dw alone (NULL for the other, and for what only that one reads) gives the bits of the call for both."""
+    import weight_only_int4_w4a16_amd as w4
+    from weight_only_int4_w4a16_amd import binding
+    torch = torch_mod()
+    L = binding.lib()
+    x, _ = _rows((M, K), "bf16", M + K)
+    dy, _ = _rows((M, N), "bf16", M + N)
+    codes_t, scales_t, _ = _weight((), K, N, K + N)
+    dx, dw = w4.gemm_fp8_backward(dy, x, codes_t, scales_t)
+    s = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(L.w4a16_fp8_backward_workspace_bytes(M, K, N), dtype=torch.uint8, device="cuda")
+    at = (ws.data_ptr(), ws.numel(), s)
+    one, other = torch.full_like(dx, 7), torch.full_like(dw, 7)
+    assert L.w4a16_gemm_fp8_backward(dy.data_ptr(), None, M, K, N, 1, codes_t.data_ptr(), scales_t.data_ptr(), one.data_ptr(), None, *at) == 0
+    assert L.w4a16_gemm_fp8_backward(dy.data_ptr(), x.data_ptr(), M, K, N, 1, None, None, None, other.data_ptr(), *at) == 0
+    assert np.array_equal(_bits(one), _bits(dx)) and np.array_equal(_bits(other), _bits(dw))
+    r = w4.route(torch.arange(M, device="cuda", dtype=torch.int32).reshape(-1, 1) % 4, 3)
+    codes_t, scales_t, _ = _weight((3,), K, N, K)
+    dx, dw = w4.gemm_fp8_grouped_backward(dy, x, r, codes_t, scales_t)
+    ws = torch.empty(L.w4a16_fp8_grouped_backward_workspace_bytes(M, 1, 3, K, N), dtype=torch.uint8, device="cuda")
+    at = (ws.data_ptr(), ws.numel(), s)
+    one, other = torch.full_like(dx, 7), torch.full_like(dw, 7)
+    plan = (r.plan.data_ptr(), M, 1, 3, K, N, 1)
+    assert L.w4a16_gemm_fp8_grouped_backward(dy.data_ptr(), None, *plan, codes_t.data_ptr(), scales_t.data_ptr(), one.data_ptr(), None, *at) == 0
+    assert L.w4a16_gemm_fp8_grouped_backward(dy.data_ptr(), x.data_ptr(), *plan, None, None, None, other.data_ptr(), *at) == 0
+    assert np.array_equal(_bits(one), _bits(dx)) and np.array_equal(_bits(other), _bits(dw))
+
+
 def test_gradients_against_differences():
     """Operands that their codes hold exactly (small whole numbers, each group's largest 448 / 64): then the calls are
     the gradients of <dy, x W^T> and central differences of the product itself give them."""

@@ -685,7 +685,7 @@ w4a16_status w4a16_quantize_fp8_columns(const void* x, int M, int K, w4a16_dtype
   if (!x || !codes || !scales || !aligned(x, dtype_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 4))
     return W4A16_ERR_ARG;
   return from_hip(w4a16::launch_fp8_columns(x, M, K, (int)dtype, codes, (size_t)w4a16::ceil16(M), scales, nullptr,
-                                            nullptr, static_cast<hipStream_t>(stream)));
+                                            nullptr, nullptr, nullptr, static_cast<hipStream_t>(stream)));
 }
 
 w4a16_status w4a16_quantize_fp8_weight(const void* w, int N, int K, w4a16_dtype dtype, uint8_t* codes,
@@ -831,17 +831,25 @@ w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const fl
   return st != W4A16_OK ? st : from_hip(w4a16::launch_fp8_grouped(a, r, plan, gather != 0));
 }
 
-// dy and x transposed for dw, `rows` deep with their padding: codes and scales of each
-struct Fp8ColumnsLayout {
-  size_t dy, dys, x, xs, total;
+// A backward call's scratch: dy's codes and scales by rows, for dx; dy's and x's by columns, `pitch` deep with their
+// padding, for dw; and the partial sums of either product where its depth is cut
+struct Fp8BackwardLayout {
+  size_t rows, row_scales, dy, dys, x, xs, scratch, total;
 };
-static Fp8ColumnsLayout fp8_columns_layout(size_t pitch, size_t blocks, int K, int N) {
-  Fp8ColumnsLayout l;
-  l.dy = 0;
+static Fp8BackwardLayout fp8_backward_layout(int rows, int K, int N, size_t pitch, bool dense) {
+  const size_t blocks = w4a16::fp8_blocks((int)pitch);
+  Fp8BackwardLayout l;
+  l.rows = 0;
+  l.row_scales = w4a16::align256((size_t)rows * N);
+  l.dy = fp8_rows_bytes(rows, N);
   l.dys = l.dy + w4a16::align256(pitch * N);
   l.x = l.dys + w4a16::align256(blocks * N * 4);
   l.xs = l.x + w4a16::align256(pitch * K);
-  l.total = l.xs + w4a16::align256(blocks * K * 4);
+  l.scratch = l.total = l.xs + w4a16::align256(blocks * K * 4);
+  if (dense) {
+    const size_t dx = w4a16::fp8_scratch_bytes(rows, K, N, false, W4A16_F16), dw = w4a16::fp8_scratch_bytes(N, K, (int)pitch, false, W4A16_F32);
+    l.total += dx > dw ? dx : dw;
+  }
   return l;
 }
 
@@ -851,12 +859,6 @@ static w4a16_status check_fp8_backward(int rows, size_t depth, int K, int N) {
   if (depth >= (1u << 23) || !fp8_quantize_fits((int)depth, K) || !fp8_quantize_fits((int)depth, N)) return W4A16_ERR_UNSUPPORTED;
   if (!w4a16::fp8_fits(rows, K, N, false) || !w4a16::fp8_fits(N, K, (int)depth, false)) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
-}
-
-// what dx's and dw's launches read stands in turn in the same scratch
-static size_t fp8_backward_bytes(int rows, int K, int N, size_t pitch, size_t blocks) {
-  const size_t dx = fp8_rows_bytes(rows, N), dw = fp8_columns_layout(pitch, blocks, K, N).total;
-  return dx > dw ? dx : dw;
 }
 
 static w4a16_status check_fp8_backward_pointers(const void* dy, const void* x, w4a16_dtype act, const uint8_t* codes_t,
@@ -870,8 +872,26 @@ static w4a16_status check_fp8_backward_pointers(const void* dy, const void* x, w
   return W4A16_OK;
 }
 
+// dx[m][k]: dy's rows by the transposed weight's
+static w4a16::Fp8Args fp8_dx_args(char* ws, const Fp8BackwardLayout& l, int rows, int K, int N, const uint8_t* codes_t,
+                                  const float* scales_t, void* dx, w4a16_dtype act, hipStream_t s) {
+  w4a16::Fp8Args a{};
+  a.x = reinterpret_cast<const uint8_t*>(ws + l.rows);
+  a.xs = reinterpret_cast<const float*>(ws + l.row_scales);
+  a.w = codes_t;
+  a.ws = scales_t;
+  a.M = a.xs_ld = rows;
+  a.N = K;
+  a.K = a.ldk = N;
+  a.out = dx;
+  a.out_dtype = (int)act;
+  a.scratch = reinterpret_cast<float*>(ws + l.scratch);
+  a.stream = s;
+  return a;
+}
+
 // dw[m = n][n = k]: dy's columns are the rows, x's the weight's
-static w4a16::Fp8Args fp8_dw_args(char* ws, const Fp8ColumnsLayout& l, size_t pitch, int K, int N, float* dw, hipStream_t s) {
+static w4a16::Fp8Args fp8_dw_args(char* ws, const Fp8BackwardLayout& l, size_t pitch, int K, int N, float* dw, hipStream_t s) {
   w4a16::Fp8Args a{};
   a.x = reinterpret_cast<const uint8_t*>(ws + l.dy);
   a.xs = reinterpret_cast<const float*>(ws + l.dys);
@@ -884,26 +904,30 @@ static w4a16::Fp8Args fp8_dw_args(char* ws, const Fp8ColumnsLayout& l, size_t pi
   a.xs_ld = N;
   a.out = dw;
   a.out_dtype = 2;
+  a.scratch = reinterpret_cast<float*>(ws + l.scratch);
   a.stream = s;
   return a;
 }
 
-// both operands of dw, through the tiles of a plan or plain
-static hipError_t fp8_dw_operands(const void* dy, const void* x, int rows, int K, int N, w4a16_dtype act, char* ws,
-                                  const Fp8ColumnsLayout& l, size_t pitch, const w4a16::RouteLayout* r,
-                                  const int32_t* plan, hipStream_t s) {
+// The codes that dx and dw need, through the tiles of a plan or plain; dy is read once for both
+static hipError_t fp8_backward_operands(const void* dy, const void* x, int rows, int K, int N, w4a16_dtype act, bool dx,
+                                        bool dw, char* ws, const Fp8BackwardLayout& l, size_t pitch,
+                                        const w4a16::RouteLayout* r, const int32_t* plan, hipStream_t s) {
+  uint8_t* const row_codes = reinterpret_cast<uint8_t*>(ws + l.rows);
+  float* const row_scales = reinterpret_cast<float*>(ws + l.row_scales);
+  if (!dw) return w4a16::launch_fp8_rows(dy, rows, N, (int)act, row_codes, row_scales, s);
   const hipError_t e = w4a16::launch_fp8_columns(dy, rows, N, (int)act, reinterpret_cast<uint8_t*>(ws + l.dy), pitch,
-                                                 reinterpret_cast<float*>(ws + l.dys), r, plan, s);
+                                                 reinterpret_cast<float*>(ws + l.dys), dx ? row_codes : nullptr, row_scales, r, plan, s);
   if (e != hipSuccess) return e;
   return w4a16::launch_fp8_columns(x, rows, K, (int)act, reinterpret_cast<uint8_t*>(ws + l.x), pitch,
-                                   reinterpret_cast<float*>(ws + l.xs), r, plan, s);
+                                   reinterpret_cast<float*>(ws + l.xs), nullptr, nullptr, r, plan, s);
 }
 
 size_t w4a16_fp8_backward_workspace_bytes(int M, int K, int N) {
   if (M < 0 || M > 0x7FFFFF00) return 0;
   const size_t pitch = (size_t)w4a16::ceil16(M);
   if (check_fp8_backward(M, pitch, K, N) != W4A16_OK || M == 0) return 0;
-  return fp8_backward_bytes(M, K, N, pitch, w4a16::fp8_blocks(M));
+  return fp8_backward_layout(M, K, N, pitch, true).total;
 }
 
 w4a16_status w4a16_gemm_fp8_backward(const void* dy, const void* x, int M, int K, int N, w4a16_dtype act,
@@ -918,28 +942,19 @@ w4a16_status w4a16_gemm_fp8_backward(const void* dy, const void* x, int M, int K
   if (M == 0) {
     if (!is_act(act) || (dw && !aligned(dw, 16))) return W4A16_ERR_ARG;
     if (!dw) return W4A16_OK;
-    w4a16::Fp8Args a = fp8_dw_args(nullptr, Fp8ColumnsLayout{}, 0, K, N, dw, s);  // a product of no depth
+    w4a16::Fp8Args a = fp8_dw_args(nullptr, Fp8BackwardLayout{}, 0, K, N, dw, s);  // a product of no depth
     return from_hip(w4a16::launch_fp8(a));
   }
   st = check_fp8_backward_pointers(dy, x, act, codes_t, scales_t, dx, dw, workspace, workspace_bytes,
                                    w4a16_fp8_backward_workspace_bytes(M, K, N));
   if (st != W4A16_OK) return st;
+  if (!dx && !dw) return W4A16_OK;
   char* ws = static_cast<char*>(workspace);
-  if (dx) {
-    w4a16::Fp8Args a{};
-    a.M = M;
-    st = fp8_operands(a, dy, act, nullptr, M, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream, true);
-    if (st != W4A16_OK) return st;
-    const hipError_t e = w4a16::launch_fp8(a);
-    if (e != hipSuccess) return W4A16_ERR_HIP;
-  }
-  if (dw) {
-    const Fp8ColumnsLayout l = fp8_columns_layout(pitch, w4a16::fp8_blocks(M), K, N);
-    hipError_t e = fp8_dw_operands(dy, x, M, K, N, act, ws, l, pitch, nullptr, nullptr, s);
-    if (e == hipSuccess) e = w4a16::launch_fp8(fp8_dw_args(ws, l, pitch, K, N, dw, s));
-    if (e != hipSuccess) return W4A16_ERR_HIP;
-  }
-  return W4A16_OK;
+  const Fp8BackwardLayout l = fp8_backward_layout(M, K, N, pitch, true);
+  hipError_t e = fp8_backward_operands(dy, x, M, K, N, act, dx, dw, ws, l, pitch, nullptr, nullptr, s);
+  if (e == hipSuccess && dx) e = w4a16::launch_fp8(fp8_dx_args(ws, l, M, K, N, codes_t, scales_t, dx, act, s));
+  if (e == hipSuccess && dw) e = w4a16::launch_fp8(fp8_dw_args(ws, l, pitch, K, N, dw, s));
+  return from_hip(e);
 }
 
 // rows of the sorted batch's tiles, each of 128
@@ -952,7 +967,7 @@ size_t w4a16_fp8_grouped_backward_workspace_bytes(int tokens, int topk, int grou
   const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
   const size_t depth = fp8_grouped_depth(r);
   if (check_fp8_backward(r.S, depth, K, N) != W4A16_OK) return 0;
-  return fp8_backward_bytes(r.S, K, N, depth, depth / 128);
+  return fp8_backward_layout(r.S, K, N, depth, false).total;
 }
 
 w4a16_status w4a16_gemm_fp8_grouped_backward(const void* dy, const void* x, const int32_t* plan, int tokens,
@@ -972,27 +987,18 @@ w4a16_status w4a16_gemm_fp8_grouped_backward(const void* dy, const void* x, cons
   if (tokens == 0) {  // the plan's offsets are zeros: every group's product has no depth
     if (!is_act(act) || (dw && !aligned(dw, 16))) return W4A16_ERR_ARG;
     if (!dw) return W4A16_OK;
-    return from_hip(w4a16::launch_fp8_by_group(fp8_dw_args(nullptr, Fp8ColumnsLayout{}, 0, K, N, dw, s), r, plan));
+    return from_hip(w4a16::launch_fp8_by_group(fp8_dw_args(nullptr, Fp8BackwardLayout{}, 0, K, N, dw, s), r, plan));
   }
   st = check_fp8_backward_pointers(dy, x, act, codes_t, scales_t, dx, dw, workspace, workspace_bytes,
                                    w4a16_fp8_grouped_backward_workspace_bytes(tokens, topk, groups, K, N));
   if (st != W4A16_OK) return st;
+  if (!dx && !dw) return W4A16_OK;
   char* ws = static_cast<char*>(workspace);
-  if (dx) {
-    w4a16::Fp8Args a{};
-    a.M = r.S;
-    st = fp8_operands(a, dy, act, nullptr, r.S, N, K, codes_t, scales_t, 0, dx, act, nullptr, ws, stream, false);
-    if (st != W4A16_OK) return st;
-    const hipError_t e = w4a16::launch_fp8_grouped(a, r, plan, false);
-    if (e != hipSuccess) return W4A16_ERR_HIP;
-  }
-  if (dw) {
-    const Fp8ColumnsLayout l = fp8_columns_layout(depth, depth / 128, K, N);
-    hipError_t e = fp8_dw_operands(dy, x, r.S, K, N, act, ws, l, depth, &r, plan, s);
-    if (e == hipSuccess) e = w4a16::launch_fp8_by_group(fp8_dw_args(ws, l, depth, K, N, dw, s), r, plan);
-    if (e != hipSuccess) return W4A16_ERR_HIP;
-  }
-  return W4A16_OK;
+  const Fp8BackwardLayout l = fp8_backward_layout(r.S, K, N, depth, false);
+  hipError_t e = fp8_backward_operands(dy, x, r.S, K, N, act, dx, dw, ws, l, depth, &r, plan, s);
+  if (e == hipSuccess && dx) e = w4a16::launch_fp8_grouped(fp8_dx_args(ws, l, r.S, K, N, codes_t, scales_t, dx, act, s), r, plan, false);
+  if (e == hipSuccess && dw) e = w4a16::launch_fp8_by_group(fp8_dw_args(ws, l, depth, K, N, dw, s), r, plan);
+  return from_hip(e);
 }
 
 w4a16_status w4a16_read_probe(const void* buf, size_t bytes, uint32_t* sink, void* stream) {

@@ -45,9 +45,11 @@ inline int ceil16(int n) { return (n + 15) & ~15; }
 // rows: codes [M][K], scales [ceil(K / 128)][M]; K % 16 == 0
 hipError_t launch_fp8_rows(const void* x, int M, int K, int dtype, uint8_t* codes, float* scales, hipStream_t s);
 // columns: codes [K][pitch] transposed, scales [row tiles][K]; a tile is 128 rows, or with a plan (r) one of
-// its 128-row tiles (those past its list are left alone; pitch: 128 times the list's bound)
+// its 128-row tiles (those past its list are left alone; pitch: 128 times the list's bound); with row_codes and
+// row_scales the rows' codes too, of the tiles' rows (16-bit x, K % 16 == 0)
 hipError_t launch_fp8_columns(const void* x, int M, int K, int dtype, uint8_t* codes, size_t pitch, float* scales,
-                              const RouteLayout* r, const int32_t* plan, hipStream_t s);
+                              uint8_t* row_codes, float* row_scales, const RouteLayout* r, const int32_t* plan,
+                              hipStream_t s);
 // blocks of 128 x 128: codes [N][K], scales [ceil(N / 128)][ceil(K / 128)]; codes_t, scales_t the same transposed, or NULL
 hipError_t launch_fp8_weight(const void* w, int N, int K, int dtype, uint8_t* codes, float* scales, uint8_t* codes_t,
                              float* scales_t, hipStream_t s);

@@ -53,9 +53,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(const void* __
   if (li < R && m0 + li < M && kb * 128 < K) scales[(size_t)kb * M + m0 + li] = mine;
 }
 
-// ---- columns, and blocks of a weight ----
+// ---- columns (and rows in the same pass), and blocks of a weight ----
 // A workgroup takes 128 x 128 values, a thread eight rows by eight columns of them. Column scales: the threads above
-// each other join their maxima through LDS; block scales: all threads do. The transposed codes go through LDS, eight
+// each other join their maxima through LDS; block scales: all threads do; row scales: the sixteen lanes side by side. The transposed codes go through LDS, eight
 // rows of a column (8 bytes) a store: column c's store t lies at slot t ^ (c / 8), so that the sixteen threads side by side
 // use every bank once, and leave as whole 16-byte pieces of a column.
 constexpr int kTileThreads = 256;
@@ -63,8 +63,9 @@ constexpr int kTileThreads = 256;
 struct Fp8TileParams {
   const void* x;
   int M, K;
-  uint8_t* codes;    // as they lie (blocks only)
-  float* scales;
+  uint8_t* codes;    // as they lie (blocks, and rows)
+  float* scales;     // of the blocks or columns
+  float* row_scales;
   uint8_t* codes_t;  // transposed, or NULL
   float* scales_t;   // blocks only
   size_t pitch;      // bytes between columns of codes_t
@@ -74,9 +75,12 @@ struct Fp8TileParams {
   int groups;
 };
 
-template <int DT, bool BLOCKS>
+enum Form { COLUMNS = 0, BLOCKS_OF_ALL = 1, COLUMNS_AND_ROWS = 2 };
+
+template <int DT, int FORM>
 __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p) {
   typedef Eight<DT> E;
+  constexpr bool BLOCKS = FORM == BLOCKS_OF_ALL;
   __shared__ __attribute__((aligned(16))) uint8_t lds[128 * 128];
   uint32_t* const red = reinterpret_cast<uint32_t*>(lds);  // [16][16 * kWords], before the codes
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -104,6 +108,25 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
     }
   }
   constexpr int WORDS = E::kWords;
+  if constexpr (FORM == COLUMNS_AND_ROWS) {  // K is a multiple of 16
+    float mine = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      uint32_t w = v[r].magnitude(0);
+#pragma unroll
+      for (int i = 1; i < WORDS; ++i) w = E::larger(w, v[r].magnitude(i));
+      const float s = fp8_scale(max_of_16_lanes(E::largest_bits(w)));
+      const Fp8Divisor d = fp8_divisor(s);
+      float q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = fp8_quotient(v[r].value(j), d);
+      const int row = row0 + ty * 8 + r;
+      if (row < end && some > 0)
+        *reinterpret_cast<u2_t*>(p.codes + (size_t)row * p.K + c) = u2_t{fp8_pack(q[0], q[1], q[2], q[3]), fp8_pack(q[4], q[5], q[6], q[7])};
+      if (tx == r) mine = s;
+    }
+    if (tx < 8 && row0 + ty * 8 + tx < end) p.row_scales[(size_t)tk * p.M + row0 + ty * 8 + tx] = mine;
+  }
   uint32_t most[WORDS];
 #pragma unroll
   for (int w = 0; w < WORDS; ++w) {
@@ -231,12 +254,12 @@ void launch_rows(const void* x, int M, int K, uint8_t* codes, float* scales, hip
     hipLaunchKernelGGL((fp8_rows_kernel<DT, 1>), grid(1), dim3(64 * kRowWaves), 0, s, x, M, K, codes, scales, chunks);
 }
 
-template <bool BLOCKS>
+template <int FORM>
 void launch_tiles(const Fp8TileParams& p, int tiles_m, int dtype, hipStream_t s) {
   const dim3 grid((unsigned)((size_t)tiles_m * p.tiles_k)), threads(kTileThreads);
-  if (dtype == 0) hipLaunchKernelGGL((fp8_tile_kernel<0, BLOCKS>), grid, threads, 0, s, p);
-  else if (dtype == 1) hipLaunchKernelGGL((fp8_tile_kernel<1, BLOCKS>), grid, threads, 0, s, p);
-  else hipLaunchKernelGGL((fp8_tile_kernel<2, BLOCKS>), grid, threads, 0, s, p);
+  if (dtype == 0) hipLaunchKernelGGL((fp8_tile_kernel<0, FORM>), grid, threads, 0, s, p);
+  else if (dtype == 1) hipLaunchKernelGGL((fp8_tile_kernel<1, FORM>), grid, threads, 0, s, p);
+  else if constexpr (FORM != COLUMNS_AND_ROWS) hipLaunchKernelGGL((fp8_tile_kernel<2, FORM>), grid, threads, 0, s, p);
 }
 
 }  // namespace
@@ -249,7 +272,8 @@ hipError_t launch_fp8_rows(const void* x, int M, int K, int dtype, uint8_t* code
 }
 
 hipError_t launch_fp8_columns(const void* x, int M, int K, int dtype, uint8_t* codes, size_t pitch, float* scales,
-                              const RouteLayout* r, const int32_t* plan, hipStream_t s) {
+                              uint8_t* row_codes, float* row_scales, const RouteLayout* r, const int32_t* plan,
+                              hipStream_t s) {
   Fp8TileParams p{};
   p.x = x;
   p.M = M;
@@ -265,7 +289,13 @@ hipError_t launch_fp8_columns(const void* x, int M, int K, int dtype, uint8_t* c
     p.groups = r->E;
     tiles = tile_bound(r->S, r->E, kTileLists - 1);
   }
-  launch_tiles<false>(p, tiles, dtype, s);
+  if (row_codes) {
+    p.codes = row_codes;
+    p.row_scales = row_scales;
+    launch_tiles<COLUMNS_AND_ROWS>(p, tiles, dtype, s);
+  } else {
+    launch_tiles<COLUMNS>(p, tiles, dtype, s);
+  }
   return hipGetLastError();
 }
 
@@ -282,7 +312,7 @@ hipError_t launch_fp8_weight(const void* w, int N, int K, int dtype, uint8_t* co
   p.pitch = (size_t)N;
   p.limit = N;
   p.tiles_k = (int)fp8_blocks(K);
-  launch_tiles<true>(p, (int)fp8_blocks(N), dtype, s);
+  launch_tiles<BLOCKS_OF_ALL>(p, (int)fp8_blocks(N), dtype, s);
   return hipGetLastError();
 }
 

@@ -20,8 +20,8 @@
 // Tiles. Both operands go from memory straight to LDS (buffer_load_dwordx4 ... lds), one block of k ahead of the
 // MFMAs, rows of 128 bytes whose 16-byte chunk c lies at position c ^ (row % 8), so that the fragment reads
 // of eight rows use every bank once. A lane's 32 bytes of a row are chunks l/16 and l/16 + 4: the same k for both operands,
-// in whatever order. Rows past the tile's end repeat the last one and are never stored; chunks past K are read out of
-// range and land as zeros. The block's scales of the tile's rows (and of its weights' rows) take one
+// in whatever order. Rows of the weight past its end repeat the last one and are never stored; chunks past K, and rows of
+// x past the tile's end, are read out of range and land as zeros. The block's scales of the tile's rows (and of its weights' rows) take one
 // 4-byte copy a lane.
 #pragma once
 
@@ -67,10 +67,11 @@ __device__ __forceinline__ int tile_of(int b, int G) {
   return x * q + (x < r ? x : r) + (b >> 3);
 }
 
-template <int n>
+// until n loads, and so many reads of LDS, are left in flight
+template <int n, int reads = 15>
 __device__ __forceinline__ void wait_loads() {
-  static_assert(n >= 0 && n < 64, "vmcnt holds 0..63");
-  __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  static_assert(n >= 0 && n < 64 && reads >= 0 && reads < 16, "vmcnt holds 0..63, lgkmcnt 0..15 (15: any)");
+  __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (reads << 8));
 }
 
 __device__ __forceinline__ f4_t mfma_fp8(i8v_t a, i8v_t b) {
@@ -179,8 +180,10 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     wrs = make_rsrc(w + (size_t)n0 * p.ldk, wrows * (uint32_t)p.ldk);
     srs = make_rsrc(scale_x ? p.xs : ws, 0x7FFFFFFFu);
 #pragma unroll
-    for (int j = 0; j < T::kCopiesX; ++j)
-      xoff[j] = (uint32_t)x_row(8 * (wave * T::kCopiesX + j) + (lane >> 3)) * (uint32_t)p.ldk + (uint32_t)chunk;
+    for (int j = 0; j < T::kCopiesX; ++j) {
+      const int r = 8 * (wave * T::kCopiesX + j) + (lane >> 3);
+      xoff[j] = r < rows ? (uint32_t)x_row(r) * (uint32_t)p.ldk + (uint32_t)chunk : kOutOfRange;
+    }
 #pragma unroll
     for (int j = 0; j < T::kCopiesW; ++j)
       woff[j] = (uint32_t)(weight_row(8 * (wave * T::kCopiesW + j) + (lane >> 3)) - n0) * (uint32_t)p.ldk + (uint32_t)chunk;
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     } else {
       soff = (uint32_t)(weight_row(r) >> 7) * (uint32_t)p.KB * 4u;
     }
-    if (r >= (scale_x ? BM : BN)) soff = kOutOfRange;
+    if (r >= (scale_x ? rows : BN)) soff = kOutOfRange;
     // Lines that are not in L2 yet hold the tiles that share them up for as long as memory takes. So a block's lines
     // are touched some blocks ahead (into LDS that nothing reads), by lane r that of tile row r: of the weight's rows an
     // eighth, of x's a quarter, as about eight and four tiles that run at once on an XCD share them (2048 rows of
@@ -369,7 +372,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   // while the last rows are multiplied. Copies past the last block read out of range, so that the count
   // of loads in flight is the same at every step.
   auto meet = [&]() __attribute__((always_inline)) {
-    wait_loads<(ST - 2) * T::kLoads + (T::kTouch > 0)>();
+    wait_loads<(ST - 2) * T::kLoads + (T::kTouch > 0), 0>();  // (and for its reads of this block: copies may overwrite it now)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -390,6 +393,22 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     meet();
     const int nb = kb1 - kb0;
     if (nb <= 0) return;
+    if constexpr (MODE == GROUPED) {
+      // of a tile that its group does not fill, a wave without rows takes part in the copies only (at this rate a
+      // product's time is its energy, so that zeros would be multiplied at the others' cost)
+      if (wm * MT * 16 >= rows) {
+        int stage = 0;
+        for (int i = 0; i < nb; ++i) {
+          const int free = stage == 0 ? ST - 1 : stage - 1;
+#pragma unroll
+          for (int j = 0; j < T::kLoads; ++j) copy(j, i + ST - 1, free);
+          touch(i + T::kTouch);
+          meet();
+          stage = stage == ST - 1 ? 0 : stage + 1;
+        }
+        return;
+      }
+    }
     i8v_t b = read_b(0, 0);
     float sx = scales_x(0)[wm * MT * 16 + l16];
 #pragma unroll
