@@ -120,7 +120,8 @@ int forced_kind() {
 
 struct Plan {
   int kind;
-  int S;  // slices of k, added by a second kernel
+  int S;     // slices of k, added by a second kernel
+  int pair;  // 2: two groups of waves share a workgroup's slice
 };
 
 // us of a product on tiles of a kind with k in S slices: 3 and, for each round of workgroups, the blocks of k by what
@@ -138,13 +139,15 @@ bool halved(int kind, int S, long long tiles, long long cus) {
   const long long left = tiles % cus;
   return kind == WHOLE && S == 1 && tiles > cus && left && 2 * left <= cus;
 }
-double model_us(int kind, int S, int M, int N, int KB, bool exact, long long cus) {
+double model_us(int kind, int S, int pair, int M, int N, int KB, bool exact, long long cus) {
   const long long wgs = (long long)ceil_div(M, kRows[kind]) * ceil_div(N, kCols[kind]) * S;
-  const int steps = ceil_div(KB, S);
+  const int steps = ceil_div(ceil_div(KB, S), pair);
   const BlockTimes& b = kBlock[exact][kind];
   const long long slots = kind <= MID ? 2 * cus : cus;
   double t = 3;
-  if (wgs <= cus) {
+  if (pair > 1) {
+    t += 1 + (double)((wgs + cus - 1) / cus) * steps * b.pair + 1.5 * (double)((wgs - 1) / cus);
+  } else if (wgs <= cus) {
     t += steps * (b.one + (b.full - b.one) * wgs / cus);
   } else {
     double rounds = (double)((wgs + slots - 1) / slots);
@@ -160,19 +163,21 @@ double model_us(int kind, int S, int M, int N, int KB, bool exact, long long cus
 Plan choose(int M, int N, int K, bool glu, bool exact) {
   // N: columns that are multiplied (GLU: both halves)
   const int KB = (int)fp8_blocks(K);
-  if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE)) return Plan{forced_kind(), 1};
-  if (M <= 16) return Plan{STREAM, 1};
+  if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE)) return Plan{forced_kind(), 1, 1};
+  if (M <= 16) return Plan{STREAM, 1, 1};
   const long long cus = device_cu_count();
   const bool sliced = !glu || (N / 2) % 128 == 0;  // sums of both halves as plain columns: their blocks follow each other
-  Plan best{MID, 1};
+  Plan best{MID, 1, 1};
   double least = 1e30;
   for (int kind = LOW; kind <= (exact ? HALF : WHOLE); ++kind)
     for (int S = 1; S <= (sliced ? 12 : 1); ++S) {
       if (S > 1 && KB < 4 * S) break;
-      const double t = model_us(kind, S, M, N, KB, exact, cus);
-      if (t < least * 0.999) {
-        least = t;
-        best = Plan{kind, S};
+      for (int pair = 1; pair <= (kind <= MID && KB >= 4 * S ? 2 : 1); ++pair) {
+        const double t = model_us(kind, S, pair, M, N, KB, exact, cus);
+        if (t < least * 0.999) {
+          least = t;
+          best = Plan{kind, S, pair};
+        }
       }
     }
   return best;
@@ -318,6 +323,7 @@ hipError_t launch_fp8(const Fp8Args& a) {
     const int kind = c.kind == STREAM ? LOW : c.kind;
     set_tiles(p, kind, glu, ceil_div(a.M, kRows[kind]));
     p.slice = ceil_div(p.KB, c.S);
+    p.pair = c.pair > 1;
     const auto launch = a.w_rows ? launch_columns : glu ? launch_glu : fp8::launch_dense;
     const long long tiles = (long long)p.tiles_m * p.tiles_n, cus = device_cu_count(), left = tiles % cus;
     if (halved(kind, c.S, tiles, cus)) {

@@ -139,6 +139,12 @@ struct Eight16 {
     for (int j = 0; j < 8; ++j)
       if (j < n) v[j >> 1] |= (uint32_t)static_cast<const uint16_t*>(row)[i + j] << (16 * (j & 1));
   }
+  // without the first n (of 1 to 7), zeros behind
+  __device__ __forceinline__ void drop(int n) {
+    if (n & 4) v = u4_t{v[2], v[3], 0u, 0u};
+    if (n & 2) v = u4_t{v[1], v[2], v[3], 0u};
+    if (n & 1) v = u4_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  }
   __device__ __forceinline__ float value(int j) const {
     const uint16_t b = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
     if constexpr (DT == 0) return (float)__builtin_bit_cast(_Float16, b);
@@ -178,6 +184,13 @@ struct Eight<2> {
   }
   __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
     for (int j = 0; j < 8; ++j) v[j] = j < n ? static_cast<const float*>(row)[i + j] : 0.f;
+  }
+  __device__ __forceinline__ void drop(int n) {
+#pragma unroll
+    for (int step = 4; step; step >>= 1)
+      if (n & step)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j + step < 8 ? v[(j + step) & 7] : 0.f;
   }
   __device__ __forceinline__ float value(int j) const { return v[j]; }
   static constexpr int kWords = 8;

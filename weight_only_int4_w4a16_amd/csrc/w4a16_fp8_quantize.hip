@@ -104,7 +104,13 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int row = row0 + ty * 8 + r;
-      if (row < end) v[r].load_some(p.x, (size_t)row * p.K + c, some);
+      if (row >= end) continue;
+      if (p.K >= 8) {  // the row's last eight, down to the ones asked for
+        v[r].load(p.x, (size_t)row * p.K + p.K - 8);
+        v[r].drop(8 - some);
+      } else {
+        v[r].load_some(p.x, (size_t)row * p.K + c, some);
+      }
     }
   }
   constexpr int WORDS = E::kWords;

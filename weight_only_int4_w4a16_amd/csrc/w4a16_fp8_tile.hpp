@@ -58,6 +58,7 @@ struct TileParams {
   int count, first;
   int slice;         // DENSE: blocks of k of a workgroup; slice blockIdx.y's sums go to out + blockIdx.y M N (fp32)
   int scale_rows;    // rows of out_scales' blocks
+  bool pair;         // DENSE, tiles of up to 64 rows: two groups of waves share a tile's blocks of k
   GroupTiles groups;
 };
 
@@ -140,14 +141,20 @@ struct Tile {
 
 // LOOP: a workgroup takes tiles blockIdx.x, blockIdx.x + gridDim.x, ..., and the first blocks of the next one are on their way
 // while it stores the last; else tile blockIdx.x alone. The loop's tiles cost the 256-row ones spills.
-template <class T, bool GLU, bool WROWS, int MODE, bool EXACT, bool LOOP, bool ONCE>
-__global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
+// KG: groups of waves that take a tile's blocks of k in turn, each with stages of its own; the second one's sums are added
+// to the first one's. With one workgroup on a compute unit, four waves' MFMAs wait for their own reads and copies.
+template <class T, bool GLU, bool WROWS, int MODE, bool EXACT, bool LOOP, bool ONCE, int KG = 1>
+__global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p) {
+  static_assert(KG == 1 || (KG == 2 && MODE == DENSE && !LOOP && T::kTouch == 0), "two groups: of dense tiles");
   constexpr int NT = T::kNT, MT = T::kMT, BN = T::kBN, BM = T::kBM;
   constexpr int OUT = GLU ? BN / 2 : BN;  // columns of out that a tile makes
   constexpr int ST = T::kStages, ISSUE = T::kIssue;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds_all[];
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = wave_of_all % T::kWaves, group = KG > 1 ? wave_of_all / T::kWaves : 0;
+  const int tid = wave * 64 + lane;
+  uint8_t* const lds8 = lds_all + group * T::kLdsBytes;
   const int wn = wave % T::kWN, wm = wave / T::kWN;
   const int N = p.N;
   const bool gathered = MODE == GROUPED && p.groups.tokens;
@@ -188,7 +195,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     for (int j = 0; j < T::kCopiesW; ++j)
       woff[j] = (uint32_t)(weight_row(8 * (wave * T::kCopiesW + j) + (lane >> 3)) - n0) * (uint32_t)p.ldk + (uint32_t)chunk;
     // and a scale: the first waves' lanes take x's rows', the next ones the weight's
-    const int r = scale_x ? (int)threadIdx.x : (int)threadIdx.x - T::kScalesX;
+    const int r = scale_x ? tid : tid - T::kScalesX;
     if (scale_x) {
       const int src = x_row(r);
       soff = (uint32_t)(gathered ? src : m0 + src) * 4u;
@@ -205,7 +212,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     // eighth, of x's a quarter, as about eight and four tiles that run at once on an XCD share them (2048 rows of
     // 8192x28672: 475 -> 424 us; every row by every tile 462).
     if constexpr (T::kTouch > 0) {
-      const int i = touch_x ? (int)threadIdx.x : (int)threadIdx.x - BM;
+      const int i = touch_x ? tid : tid - BM;
       toff = kOutOfRange;
       if (touch_x ? i % 4 == tn % 4 : i % 8 == tm % 8)
         toff = (uint32_t)(touch_x ? x_row(i) : weight_row(i) - n0) * (uint32_t)p.ldk;
@@ -293,6 +300,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
   // copy j of a block: x's rows, the weight's, the scales
   auto copy = [&](int j, int i, int stage) __attribute__((always_inline)) {
     uint8_t* const dst = lds8 + stage * T::kStage;
+    i = i * KG + group;
     const bool live = i < kb1 - kb0;
     int kb = kb0 + i + turned;
     kb = kb >= kb1 ? kb - (kb1 - kb0) : kb;
@@ -391,7 +399,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     }
     fac[0] = fac[1] = 0.f;
     meet();
-    const int nb = kb1 - kb0;
+    const int nb = (kb1 - kb0 + KG - 1) / KG;  // (a block past the last one is zeros)
     if (nb <= 0) return;
     if constexpr (MODE == GROUPED) {
       // of a tile that its group does not fill, a wave without rows takes part in the copies only (at this rate a
@@ -610,6 +618,21 @@ __global__ __launch_bounds__(T::kThreads) void fp8_tile_kernel(TileParams p) {
     multiply();
     wait_loads<0>();
     __syncthreads();
+    if constexpr (KG > 1) {
+      f4_t* const sums = reinterpret_cast<f4_t*>(lds_all) + tid;
+      static_assert(NT * MT * T::kThreads * 16 <= (ST - 1) * T::kStage, "the sums leave the stage that results are turned in");
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          if (group) sums[(nt * MT + mt) * T::kThreads] = acc[nt][mt];
+      __syncthreads();
+      if (group) return;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) acc[nt][mt] += sums[(nt * MT + mt) * T::kThreads];
+    }
     store(m0, rows, n0, out_row);
   }
 }
@@ -624,10 +647,22 @@ typedef Tile<4, 2, 4, 8, 2, 3, 3> Whole;  // 256, 256: results of 16 bits only (
 template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
 hipError_t launch_tile(const TileParams& p, unsigned grid, int gy, hipStream_t s) {
   constexpr bool LOOP = std::is_same<T, Half>::value && MODE != BY_GROUP;
-  const dim3 blocks(grid, gy), threads(T::kThreads);
+  const dim3 blocks(grid, gy), threads(T::kThreads), twice(2 * T::kThreads);
   if constexpr (T::kBM <= 64 && !WROWS) {
     if (p.once) {
+      if constexpr (MODE == DENSE) {
+        if (p.pair) {
+          hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT, LOOP, true, 2>), blocks, twice, 2 * T::kLdsBytes, s, p);
+          return hipGetLastError();
+        }
+      }
       hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT, LOOP, true>), blocks, threads, T::kLdsBytes, s, p);
+      return hipGetLastError();
+    }
+  }
+  if constexpr (T::kBM <= 64 && MODE == DENSE) {
+    if (p.pair) {
+      hipLaunchKernelGGL((fp8_tile_kernel<T, GLU, WROWS, MODE, EXACT, LOOP, false, 2>), blocks, twice, 2 * T::kLdsBytes, s, p);
       return hipGetLastError();
     }
   }
