@@ -215,7 +215,7 @@ def test_quantizers_at_odd_addresses():
 PRODUCTS = [
     # M, K, N: one token to many, depths and widths that divide nothing
     (1, 16, 1), (1, 4096, 512), (1, 14352, 96), (1, 33024, 48), (2, 144, 33), (2, 4112, 300), (2, 16400, 40), (3, 1040, 100), (7, 2048, 640), (15, 528, 1000), (16, 256, 256), (17, 4112, 130),
-    (31, 128, 2048), (33, 384, 129), (48, 640, 777), (63, 896, 128), (64, 1024, 384), (65, 512, 257), (100, 272, 1024),
+    (18, 1040, 4608), (20, 144, 100), (32, 8208, 48), (31, 128, 2048), (33, 384, 129), (48, 640, 777), (63, 896, 128), (64, 1024, 384), (65, 512, 257), (100, 272, 1024),
     (127, 1152, 255), (128, 2176, 512), (129, 160, 640), (200, 1280, 1001), (256, 640, 2048), (257, 400, 512), (333, 656, 501),
 ]
 
@@ -246,7 +246,7 @@ def test_products(M, K, N, kind):
         assert torch.equal(out[1:-1], y) and bool((out[0] == 7).all()) and bool((out[-1] == 7).all())
 
 
-@pytest.mark.parametrize("M,K,N2", [(1, 256, 2), (1, 2048, 512), (2, 4112, 160), (5, 144, 100), (16, 640, 704), (33, 1040, 258), (64, 512, 96),
+@pytest.mark.parametrize("M,K,N2", [(1, 256, 2), (1, 2048, 512), (2, 4112, 160), (5, 144, 100), (16, 640, 704), (17, 528, 98), (32, 4112, 288), (33, 1040, 258), (64, 512, 96),
                                     (70, 272, 640), (130, 384, 1000), (257, 256, 1024), (300, 528, 288)])
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 def test_swiglu(M, K, N2, kind):

@@ -847,7 +847,7 @@ static Fp8BackwardLayout fp8_backward_layout(int rows, int K, int N, size_t pitc
   l.xs = l.x + w4a16::align256(pitch * K);
   l.scratch = l.total = l.xs + w4a16::align256(blocks * K * 4);
   if (dense) {
-    const size_t dx = w4a16::fp8_scratch_bytes(rows, K, N, false, W4A16_F16), dw = w4a16::fp8_scratch_bytes(N, K, (int)pitch, false, W4A16_F32);
+    const size_t dx = w4a16::fp8_scratch_bytes(rows, K, N, false, W4A16_F16), dw = w4a16::fp8_scratch_bytes(N, K, (int)pitch, false, W4A16_F32, true);
     l.total += dx > dw ? dx : dw;
   }
   return l;

@@ -128,7 +128,8 @@ struct Plan {
 // one takes, and 1.5 more a round; at least the weight's bytes at 5.6 TB/s; and the slices' sums, written and read at
 // 4 TB/s with another launch. What a block takes was measured on 1024x4096 to 8192x32768, 24 to 2048 rows, S 1 to
 // 12, cold weights: `one` with few workgroups, `full` with one on every compute unit, `pair` with two on each (the kinds
-// of which two fit), or in later rounds.
+// of which two fit), or in later rounds. With two groups of waves to a workgroup (pair) each takes every second block, at
+// the pair's time (333 rows of 2896x5001 in fp32, 240 tiles of 64 rows: 27.7 us with one group, 23.8 with two).
 struct BlockTimes {
   double one, full, pair;
 };
@@ -156,19 +157,37 @@ double model_us(int kind, int S, int pair, int M, int N, int KB, bool exact, lon
   }
   const double memory = 3 + (double)N * KB * 128 / 5.6e6;
   if (t < memory) t = memory;
-  if (S > 1) t += 2.5 + 2.0 * S * M * N * 4 / 4e6;
+  if (S > 1) t += 4.5 + 2.0 * S * M * N * 4 / 4e6;
   return t;
 }
 
-Plan choose(int M, int N, int K, bool glu, bool exact) {
+// us of 17 to 32 rows by the sixteen-row products' kernel, eight waves to a workgroup and one workgroup to a compute
+// unit: a round of 16 or 32 columns by what each of a wave's blocks takes (20 rows of 4096x4096: 7.6 us, by tiles 11.7;
+// of 2048x7168 7.5 and 10.5; of 8192x8192 18.4 and 20.7; of 4096x14336 20.9 and 17.8). N: columns of out
+double stream32_us(int N, int KB, bool glu, long long cus, int& NT) {
+  const auto us = [&](int cols, double block) {
+    const long long rounds = (ceil_div(N, cols) + cus - 1) / cus;
+    return 3 + rounds * ceil_div(KB, 8) * block + 1.5 * (rounds - 1);
+  };
+  const double narrow = glu ? 1e30 : us(16, 1.05), two = us(glu ? 16 : 32, 1.95);
+  NT = narrow <= two ? 1 : 2;
+  return narrow <= two ? narrow : two;
+}
+
+Plan choose(int M, int N, int K, bool glu, bool exact, bool w_rows = false) {
   // N: columns that are multiplied (GLU: both halves)
   const int KB = (int)fp8_blocks(K);
-  if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE)) return Plan{forced_kind(), 1, 1};
-  if (M <= 16) return Plan{STREAM, 1, 1};
+  if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE) && !(w_rows && forced_kind() == STREAM)) return Plan{forced_kind(), 1, 1};
+  if (M <= 16 && !w_rows) return Plan{STREAM, 1, 1};
   const long long cus = device_cu_count();
   const bool sliced = !glu || (N / 2) % 128 == 0;  // sums of both halves as plain columns: their blocks follow each other
   Plan best{MID, 1, 1};
   double least = 1e30;
+  if (M <= 32 && !w_rows) {
+    int NT;
+    least = stream32_us(glu ? N / 2 : N, KB, glu, cus, NT);
+    best = Plan{STREAM, 1, 1};
+  }
   for (int kind = LOW; kind <= (exact ? HALF : WHOLE); ++kind)
     for (int S = 1; S <= (sliced ? 12 : 1); ++S) {
       if (S > 1 && KB < 4 * S) break;
@@ -245,14 +264,16 @@ hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, con
   p.values = values;
   p.values_dtype = values_dtype;
   int NT, W;
-  p.tiles_m = grouped ? t.groups.bound : ceil_div(t.M, 16);
+  const int XC = values ? 0 : grouped ? 2 : M > 16 ? 4 : M > 8 ? 2 : 1;
+  p.tiles_m = grouped ? t.groups.bound : ceil_div(t.M, XC == 4 ? 32 : 16);
   // of a grouped launch's tiles at most one a group is part-filled, and those past the list's end leave at once
   const long long full = grouped ? (t.groups.bound + 1) / 2 : p.tiles_m;
   stream_shape(M, t.N, t.K, glu, device_cu_count(), full, NT, W);
+  if (XC == 4) stream32_us(t.N, t.KB, glu, device_cu_count(), NT), W = 8;
   p.tiles_n = ceil_div(t.N, glu ? 8 * NT : 16 * NT);
   p.slice = ceil_div(t.KB, W);
   const unsigned grid = (unsigned)((size_t)p.tiles_m * p.tiles_n);
-  return launch_stream(p, NT, values ? 0 : grouped || M > 8 ? 2 : 1, W, glu, grouped, grid, s);
+  return launch_stream(p, NT, XC, W, glu, grouped, grid, s);
 }
 
 // Workgroups of a launch of so many tiles: with one a compute unit, each takes its share of the tiles in turn
@@ -291,8 +312,8 @@ bool fp8_takes_values(int M, int N, int K, bool glu) {
   return ceil_div((int)fp8_blocks(K), W) * M <= 64;
 }
 
-size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype) {
-  const Plan c = choose(M, glu ? 2 * N : N, K, glu, out_dtype >= 2);
+size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype, bool w_rows) {
+  const Plan c = choose(M, glu ? 2 * N : N, K, glu, out_dtype >= 2, w_rows);
   if (c.S > 1) return align256((size_t)c.S * M * (glu ? 2 * (size_t)N : N) * 4);
   return by_finish(c.kind, c.S, out_dtype) ? align256((size_t)M * N * 4) : 0;
 }
@@ -301,13 +322,13 @@ const char* fp8_name(int M, int N, int K, bool glu) {
   const Plan c = choose(M, glu ? 2 * N : N, K, glu, false);
   static const char* const names[2][5] = {
       {"w4a16_fp8_16", "w4a16_fp8_32x128", "w4a16_fp8_64x128", "w4a16_fp8_128x256", "w4a16_fp8_256x256"},
-      {"w4a16_fp8_16", "w4a16_fp8_32x128_splitk", "w4a16_fp8_64x128_splitk", "w4a16_fp8_128x256_splitk", "w4a16_fp8_256x256_splitk"}};
-  return names[c.S > 1][c.kind];
+      {"w4a16_fp8_32", "w4a16_fp8_32x128_splitk", "w4a16_fp8_64x128_splitk", "w4a16_fp8_128x256_splitk", "w4a16_fp8_256x256_splitk"}};
+  return names[c.kind == STREAM ? M > 16 : c.S > 1][c.kind];
 }
 
 hipError_t launch_fp8(const Fp8Args& a) {
   const bool exact = a.out_dtype >= 2;
-  const Plan c = choose(a.M, a.glu ? 2 * a.N : a.N, a.K, a.glu, exact);
+  const Plan c = choose(a.M, a.glu ? 2 * a.N : a.N, a.K, a.glu, exact, a.w_rows);
   TileParams p = tile_params(a);
   const bool finish = by_finish(c.kind, c.S, a.out_dtype);
   if (finish) {
@@ -315,12 +336,12 @@ hipError_t launch_fp8(const Fp8Args& a) {
     p.out_dtype = 2;
   }
   hipError_t e;
-  if (c.kind == STREAM && !a.w_rows) {
+  if (c.kind == STREAM) {
     e = launch_rows16(p, a.M, a.glu, false, a.values, a.values_dtype, a.stream);
   } else {
     const bool glu = a.glu && c.S == 1;
     if (a.glu && !glu) p.N = 2 * a.N;
-    const int kind = c.kind == STREAM ? LOW : c.kind;
+    const int kind = c.kind;
     set_tiles(p, kind, glu, ceil_div(a.M, kRows[kind]));
     p.slice = ceil_div(p.KB, c.S);
     p.pair = c.pair > 1;

@@ -1,4 +1,4 @@
-// w4a16_fp8_stream.hip - instantiations: products of up to sixteen rows (a tile).
+// w4a16_fp8_stream.hip - instantiations: products of up to sixteen rows (a tile), or 32.
 #include "w4a16_fp8_stream.hpp"
 
 namespace w4a16 {
@@ -23,19 +23,28 @@ hipError_t by_waves(const StreamParams& p, int W, unsigned grid, hipStream_t s) 
 
 }  // namespace
 
-// NT 1 (plain) or 2, XC 0 (x of 16 bits), 1 (ungrouped rows) or 2
+// NT 1 (plain) or 2; XC 0 (x of 16 bits), 1, 2 or 4 (the latter with eight waves); routed rows 2
 hipError_t launch_stream(const StreamParams& p, int NT, int XC, int W, bool glu, bool grouped, unsigned grid, hipStream_t s) {
   if (grouped) {
     if (glu) return by_waves<2, 2, true, true>(p, W, grid, s);
     return NT == 1 ? by_waves<1, 2, false, true>(p, W, grid, s) : by_waves<2, 2, false, true>(p, W, grid, s);
   }
-  if (XC == 0) {
-    if (glu) return by_waves<2, 0, true, false>(p, W, grid, s);
-    return NT == 1 ? by_waves<1, 0, false, false>(p, W, grid, s) : by_waves<2, 0, false, false>(p, W, grid, s);
+  const auto dense = [&](auto xc) {
+    constexpr int C = decltype(xc)::value;
+    if constexpr (C == 4) {
+      if (glu) return run<2, C, 8, true, false>(p, grid, s);
+      return NT == 1 ? run<1, C, 8, false, false>(p, grid, s) : run<2, C, 8, false, false>(p, grid, s);
+    } else {
+      if (glu) return by_waves<2, C, true, false>(p, W, grid, s);
+      return NT == 1 ? by_waves<1, C, false, false>(p, W, grid, s) : by_waves<2, C, false, false>(p, W, grid, s);
+    }
+  };
+  switch (XC) {
+    case 0: return dense(std::integral_constant<int, 0>{});
+    case 1: return dense(std::integral_constant<int, 1>{});
+    case 2: return dense(std::integral_constant<int, 2>{});
+    default: return dense(std::integral_constant<int, 4>{});
   }
-  if (glu) return XC == 1 ? by_waves<2, 1, true, false>(p, W, grid, s) : by_waves<2, 2, true, false>(p, W, grid, s);
-  if (NT == 1) return XC == 1 ? by_waves<1, 1, false, false>(p, W, grid, s) : by_waves<1, 2, false, false>(p, W, grid, s);
-  return XC == 1 ? by_waves<2, 1, false, false>(p, W, grid, s) : by_waves<2, 2, false, false>(p, W, grid, s);
 }
 
 }  // namespace fp8

@@ -1,7 +1,7 @@
 // w4a16_fp8_stream.hpp - products of e4m3 codes for few rows, bound by the weight's bytes: each must cross HBM once, at
 // full rate.
 //
-// A workgroup owns 16 NT rows of the weight and up to 16 rows of x; its W waves take contiguous slices of k and their
+// A workgroup owns 16 NT rows of the weight and up to 16 MT rows of x; its W waves take contiguous slices of k and their
 // partial sums are added through LDS in wave order. Each wave streams its slice through a ring of D slots of its own
 // in LDS, one block of 128 k a slot (both operands' codes and x's scales): copies go from memory straight to LDS, so that
 // what is in flight takes no registers, eight lanes read 128 consecutive bytes of a row (fragments read from memory
@@ -39,14 +39,15 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 
-// XC: 1 KiB copies of x a block (eight rows each), or 0 where each workgroup quantizes x itself
+// XC: 1 KiB copies of x a block (eight rows each), or 0 where each workgroup quantizes x itself (two rows at most)
 template <int NT, int XC, int D>
 struct Stream {
+  static constexpr int MT = XC == 4 ? 2 : 1;  // times sixteen rows of x
   static constexpr int kSlot = NT * 2048 + (XC ? XC * 1024 + 256 : 0);
   static constexpr int kLoads = 2 * NT + (XC ? XC + 1 : 0);  // a slot's copies
   static constexpr int kWave = D * kSlot;         // bytes of LDS a wave
   static_assert((D - 1) * kLoads < 64, "vmcnt holds 0..63");
-  static constexpr int kSums = NT * 256;          // floats a wave
+  static constexpr int kSums = NT * MT * 256;     // floats a wave
   static constexpr size_t ring_bytes(int W) {
     const size_t ring = (size_t)W * kWave, sums = (size_t)W * kSums * 4;
     return ring > sums ? ring : sums;
@@ -61,7 +62,8 @@ template <int NT, int XC, int D, int W, bool GLU, bool GROUPED, bool ONCE>
 __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   typedef Stream<NT, XC, D> S;
   static_assert(!GLU || NT % 2 == 0, "a SwiGLU workgroup holds gate rows and the matching up rows");
-  static_assert(XC == 1 || XC == 2 || (XC == 0 && !GROUPED), "up to eight rows of x, or sixteen");
+  static_assert(XC == 1 || XC == 2 || ((XC == 0 || XC == 4) && !GROUPED), "up to eight rows of x, or 16, or 32");
+  constexpr int MT = S::MT;
   constexpr int OUT = (GLU ? NT / 2 : NT) * 16;  // columns of out a workgroup makes
   extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
@@ -69,7 +71,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   const int t = tile_of(blockIdx.x, p.tiles_m * p.tiles_n);
   const int tm = t % p.tiles_m, tn = t / p.tiles_m;  // neighbours share the weight's rows
   const int N = p.N, n0 = tn * OUT, KB = p.KB;
-  int m0 = tm * 16, end = p.M, e = 0;
+  int m0 = tm * 16 * MT, end = p.M, e = 0;
   if constexpr (GROUPED) {
     if (!group_tile(p.groups, tm, e, m0, end)) return;
     if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
@@ -79,7 +81,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     p.w += (size_t)e * (GLU ? 2 : 1) * N * p.ldk;
     p.ws += (size_t)e * (GLU ? 2 * p.up_blocks : (N + 127) / 128) * KB;
   }
-  const int rows = min(16, end - m0);
+  const int rows = min(16 * MT, end - m0);
   const int kb0 = min(wave * p.slice, KB), nb = min(p.slice, KB - kb0);
   uint8_t* const ring = lds8 + wave * S::kWave;
 
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   }
   // x's scales: lane l that of row l (the last copy of a slot)
   const __amdgpu_buffer_rsrc_t srs = make_rsrc(p.xs, 0x7FFFFFFFu);
-  const int srow = lane < 16 ? x_row(lane) : -1;
+  const int srow = lane < 16 * MT ? x_row(lane) : -1;
   const uint32_t soff = srow < 0 ? kOutOfRange : (uint32_t)(gathered ? srow : m0 + srow) * 4u;
 
   auto copy = [&](int i) __attribute__((always_inline)) {  // block i of the slice, into slot i % D
@@ -180,9 +182,11 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     __builtin_amdgcn_wave_barrier();
   }
 
-  f4_t acc[NT];
+  f4_t acc[NT][MT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f4_t{0.f, 0.f, 0.f, 0.f};
   for (int i = 0; i < nb; ++i) {
     if (i && i % 64 == 0) {
       wsc0 = i + lane < nb ? ws0[i + lane] : 0.f;
@@ -195,42 +199,49 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     const uint8_t* const wt = ring + (i % D) * S::kSlot;
     const uint8_t* const xt = wt + NT * 2048;
     const float* const xsc = reinterpret_cast<const float*>(xt + XC * 1024);
-    // (eight rows' copy: the other lanes read the same rows again, for columns that are not stored)
-    i8v_t bf;
-    float sx;
-    if constexpr (XC == 0) {  // the codes lie in k order; lanes past the rows repeat the last one
-      const int g = i * rows + min(l16, rows - 1);
-      const i4v_t lo = *reinterpret_cast<const i4v_t*>(codes + g * 128 + q * 16);
-      const i4v_t hi = *reinterpret_cast<const i4v_t*>(codes + g * 128 + q * 16 + 64);
-      bf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      sx = code_scales[g];
-    } else {
-      bf = read_fragment(xt, XC == 1 ? l16 & 7 : l16, q);
-      sx = xsc[l16];
-    }
-    const Wide b = widen(bf);
+    Wide a[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const Wide a = widen(read_fragment(wt, nt * 16 + l16, q));
-      f4_t part = f4_t{0.f, 0.f, 0.f, 0.f};
+    for (int nt = 0; nt < NT; ++nt) a[nt] = widen(read_fragment(wt, nt * 16 + l16, q));
 #pragma unroll
-      for (int s = 0; s < 4; ++s) part = mfma16(a.k[s], b.k[s], part);
-      const float f = sx * (GLU && nt >= NT / 2 ? sw1 : sw0);
+    for (int mt = 0; mt < MT; ++mt) {
+      // (eight rows' copy: the other lanes read the same rows again, for columns that are not stored)
+      i8v_t bf;
+      float sx;
+      if constexpr (XC == 0) {  // the codes lie in k order; lanes past the rows repeat the last one
+        const int g = i * rows + min(l16, rows - 1);
+        const i4v_t lo = *reinterpret_cast<const i4v_t*>(codes + g * 128 + q * 16);
+        const i4v_t hi = *reinterpret_cast<const i4v_t*>(codes + g * 128 + q * 16 + 64);
+        bf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        sx = code_scales[g];
+      } else {
+        bf = read_fragment(xt, mt * 16 + (XC == 1 ? l16 & 7 : l16), q);
+        sx = xsc[mt * 16 + l16];
+      }
+      const Wide b = widen(bf);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[nt][r] = __builtin_fmaf(part[r], f, acc[nt][r]);
+      for (int nt = 0; nt < NT; ++nt) {
+        f4_t part = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) part = mfma16(a[nt].k[s], b.k[s], part);
+        const float f = sx * (GLU && nt >= NT / 2 ? sw1 : sw0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[nt][mt][r] = __builtin_fmaf(part[r], f, acc[nt][mt][r]);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     copy(i + D);
   }
 
   // ---- the waves' sums, in wave order ----
-  // [16 rows][16 NT columns] a wave, over its own ring (no copy of a slice is in flight into another's)
+  // [16 MT rows][16 NT columns] a wave, over its own ring (no copy of a slice is in flight into another's)
   wait_loads<0>();
   __syncthreads();
   float* const red = reinterpret_cast<float*>(lds8);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
-    *reinterpret_cast<f4_t*>(red + wave * S::kSums + l16 * (NT * 16) + nt * 16 + 4 * q) = acc[nt];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      *reinterpret_cast<f4_t*>(red + wave * S::kSums + (mt * 16 + l16) * (NT * 16) + nt * 16 + 4 * q) = acc[nt][mt];
   __syncthreads();
   constexpr int PIECES = OUT / 4;  // of a row
   for (int piece = threadIdx.x; piece < rows * PIECES; piece += 64 * W) {
