@@ -227,13 +227,16 @@ def test_sizes_and_names(L):
     assert L.w4a16_fp8_kernel_name(1, 60, 32, 0) == b"none"
 
 
-@pytest.mark.parametrize("M,K,N", [(2085, 256, 128), (1500, 128, 160), (40, 256, 8192), (2048, 128, 128)])
-def test_gradients_have_room_for_partial_sums(L, M, K, N):
+def test_gradients_have_room_for_partial_sums(L):
     """Products whose depth is cut keep fp32 sums of every slice beside the codes that all of them read."""
-    depth = (M + 15) // 16 * 16
-    sums = max(L.w4a16_fp8_workspace_bytes(N, depth, K, E4M3, 0, F32), L.w4a16_fp8_workspace_bytes(M, N, K, E4M3, 0, BF16))
-    assert sums > 0
-    assert L.w4a16_fp8_backward_workspace_bytes(M, K, N) >= sums + M * N + depth * (K + N)
+    most = 0
+    for M, K, N in [(2085, 256, 128), (1500, 128, 160), (40, 256, 8192), (2048, 128, 128), (8192, 256, 256), (64, 512, 16384)]:
+        depth = (M + 15) // 16 * 16
+        sums = max(L.w4a16_fp8_workspace_bytes(N, depth, K, E4M3, 0, F32) if N > 16 else 0,
+                   L.w4a16_fp8_workspace_bytes(M, N, K, E4M3, 0, BF16))
+        assert L.w4a16_fp8_backward_workspace_bytes(M, K, N) >= sums + M * N + depth * (K + N)
+        most = max(most, sums)
+    assert most > 0
 
 
 # ------------------------------------------------------------------ refusals of the binding (meta and host tensors)

@@ -460,7 +460,7 @@ def test_gradients(M, K, N, kind):
     _within(dw.cpu().double().numpy(), ref, bound, "dw")
 
 
-@pytest.mark.parametrize("M,K,N", [(1100, 144, 160), (2085, 256, 128), (5000, 272, 16), (40, 256, 8192), (3, 64, 16384)])
+@pytest.mark.parametrize("M,K,N", [(1100, 144, 160), (2085, 256, 128), (5000, 272, 16), (9000, 272, 160), (4100, 48, 16), (40, 256, 8192), (3, 64, 16384)])
 def test_gradients_with_few_tiles(M, K, N):
     """Deep products of few tiles, whose depth is cut: their partial sums have room of their own."""
     import weight_only_int4_w4a16_amd as w4

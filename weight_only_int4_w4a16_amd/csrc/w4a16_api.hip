@@ -806,8 +806,7 @@ size_t w4a16_fp8_grouped_workspace_bytes(int tokens, int topk, int groups, int g
                                          w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
   if (check_fp8_grouped(tokens, topk, groups, gather, K, N, x_dtype, swiglu, out_dtype) != W4A16_OK || tokens == 0) return 0;
   return (is_e4m3(x_dtype) ? 0 : fp8_rows_bytes(gather ? tokens : tokens * topk, K)) +
-         w4a16::fp8_grouped_scratch_bytes(w4a16::route_layout(tokens, topk, groups), swiglu ? N / 2 : N, K, swiglu != 0,
-                                          (int)out_dtype);
+         w4a16::fp8_grouped_scratch_bytes(w4a16::route_layout(tokens, topk, groups), swiglu ? N / 2 : N, (int)out_dtype);
 }
 
 w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const float* x_scales,
@@ -857,6 +856,7 @@ static w4a16_status check_fp8_backward(int rows, size_t depth, int K, int N) {
   if (rows < 0 || K <= 0 || N <= 0) return W4A16_ERR_ARG;
   if (K % 16 || N % 16) return W4A16_ERR_UNSUPPORTED;
   if (depth >= (1u << 23) || !fp8_quantize_fits((int)depth, K) || !fp8_quantize_fits((int)depth, N)) return W4A16_ERR_UNSUPPORTED;
+  if ((long long)w4a16::fp8_blocks((int)depth) * (K > N ? K : N) * 4 >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;  // offsets of scales
   if (!w4a16::fp8_fits(rows, K, N, false) || !w4a16::fp8_fits(N, K, (int)depth, false)) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }

@@ -16,7 +16,7 @@ W4A16_FP8_EXTERN(launch_grouped_plain);
 W4A16_FP8_EXTERN(launch_grouped_glu);
 W4A16_FP8_EXTERN(launch_columns);
 W4A16_FP8_EXTERN(launch_by_group);
-hipError_t launch_stream(const StreamParams& p, int NT, int XC, int W, bool glu, bool grouped, unsigned grid, hipStream_t s);
+hipError_t launch_stream(const StreamParams& p, int NT, int XC, int W, bool glu, unsigned grid, hipStream_t s);
 }  // namespace fp8
 
 namespace {
@@ -174,12 +174,18 @@ double stream32_us(int N, int KB, bool glu, long long cus, int& NT) {
   return narrow <= two ? narrow : two;
 }
 
+// Whether so many tiles leave at most an eighth of the chip idle. Of three to sixteen rows such a weight is read faster by
+// tiles of 32 rows, which ask for 128 of its rows at once (16 rows of 8192x28672 37.7 us, by sixteen columns 45.3; of
+// 8192x57344 72.4 and 77.1; of 4096x28672 25.1 and 27.9; but with 192 tiles, 8192x24576, 36.9 and 33.3, and with 320,
+// 8192x40960, 59.6 and 52.0). One row or two are quantized on the way by the other kernel.
+bool fills(long long tiles, long long cus) { return 8 * tiles >= 7 * ((tiles + cus - 1) / cus) * cus; }
+
 Plan choose(int M, int N, int K, bool glu, bool exact, bool w_rows = false) {
   // N: columns that are multiplied (GLU: both halves)
   const int KB = (int)fp8_blocks(K);
   if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE) && !(w_rows && forced_kind() == STREAM)) return Plan{forced_kind(), 1, 1};
-  if (M <= 16 && !w_rows) return Plan{STREAM, 1, 1};
   const long long cus = device_cu_count();
+  if (M <= 16 && !w_rows) return Plan{M > 2 && fills(ceil_div(N, 128), cus) ? LOW : STREAM, 1, 1};
   const bool sliced = !glu || (N / 2) % 128 == 0;  // sums of both halves as plain columns: their blocks follow each other
   Plan best{MID, 1, 1};
   double least = 1e30;
@@ -238,13 +244,13 @@ void set_tiles(TileParams& p, int kind, bool glu, int tiles_m) {
 //   4096x4096   8.5, 6.2, 9.7, 7.3;   8.2, 6.2, 10.4, 7.9    8192x10240  18.6, 19.2, 20.7, 24.2;  20.1, 22.1, 22.4, 25.3
 //   4096x14336  13.6, 15.1, 13.8, 16.9;  15.7, 17.0, 14.7, 17.8    14336x4096  24.8, 15.3, 28.5, 18.0;  23.5, 14.8, 30.7, 19.7
 //   28672x8192  53.4, 42.0, 57.6, 42.0;  51.1, 50.0, 64.1, 42.8
-void stream_shape(int M, int N, int K, bool glu, long long cus, long long tiles_m, int& NT, int& W) {
-  const long long tiles = tiles_m * ceil_div(N, 16);
+void stream_shape(int M, int N, int K, bool glu, long long cus, int& NT, int& W) {
+  const long long tiles = ceil_div(N, 16);
   NT = glu || tiles > 3 * cus || (M > 8 && K > 16384) ? 2 : 1;
-  W = tiles_m * ceil_div(N, glu ? 16 : 16 * NT) <= 2 * cus ? 8 : 4;
+  W = ceil_div(N, glu ? 16 : 16 * NT) <= 2 * cus ? 8 : 4;
 }
 
-hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, const void* values, int values_dtype, hipStream_t s) {
+hipError_t launch_rows16(const TileParams& t, bool glu, const void* values, int values_dtype, hipStream_t s) {
   StreamParams p{};
   p.x = t.x;
   p.xs = t.xs;
@@ -259,21 +265,18 @@ hipError_t launch_rows16(const TileParams& t, int M, bool glu, bool grouped, con
   p.ldk = t.ldk;
   p.xs_ld = t.xs_ld;
   p.up_blocks = t.up_blocks;
-  p.groups = t.groups;
   p.once = t.once;
   p.values = values;
   p.values_dtype = values_dtype;
   int NT, W;
-  const int XC = values ? 0 : grouped ? 2 : M > 16 ? 4 : M > 8 ? 2 : 1;
-  p.tiles_m = grouped ? t.groups.bound : ceil_div(t.M, XC == 4 ? 32 : 16);
-  // of a grouped launch's tiles at most one a group is part-filled, and those past the list's end leave at once
-  const long long full = grouped ? (t.groups.bound + 1) / 2 : p.tiles_m;
-  stream_shape(M, t.N, t.K, glu, device_cu_count(), full, NT, W);
+  const int XC = values ? 0 : t.M > 16 ? 4 : t.M > 8 ? 2 : 1;
+  p.tiles_m = ceil_div(t.M, XC == 4 ? 32 : 16);
+  stream_shape(t.M, t.N, t.K, glu, device_cu_count(), NT, W);
   if (XC == 4) stream32_us(t.N, t.KB, glu, device_cu_count(), NT), W = 8;
   p.tiles_n = ceil_div(t.N, glu ? 8 * NT : 16 * NT);
   p.slice = ceil_div(t.KB, W);
   const unsigned grid = (unsigned)((size_t)p.tiles_m * p.tiles_n);
-  return launch_stream(p, NT, XC, W, glu, grouped, grid, s);
+  return launch_stream(p, NT, XC, W, glu, grid, s);
 }
 
 // Workgroups of a launch of so many tiles: with one a compute unit, each takes its share of the tiles in turn
@@ -308,7 +311,7 @@ bool fp8_fits(int M, int N, int K, bool glu) {
 bool fp8_takes_values(int M, int N, int K, bool glu) {
   if (M > 2 || M < 1 || choose(M, glu ? 2 * N : N, K, glu, true).kind != STREAM) return false;
   int NT, W;
-  stream_shape(M, N, K, glu, device_cu_count(), 1, NT, W);
+  stream_shape(M, N, K, glu, device_cu_count(), NT, W);
   return ceil_div((int)fp8_blocks(K), W) * M <= 64;
 }
 
@@ -337,7 +340,7 @@ hipError_t launch_fp8(const Fp8Args& a) {
   }
   hipError_t e;
   if (c.kind == STREAM) {
-    e = launch_rows16(p, a.M, a.glu, false, a.values, a.values_dtype, a.stream);
+    e = launch_rows16(p, a.glu, a.values, a.values_dtype, a.stream);
   } else {
     const bool glu = a.glu && c.S == 1;
     if (a.glu && !glu) p.N = 2 * a.N;
@@ -368,20 +371,20 @@ hipError_t launch_fp8(const Fp8Args& a) {
 
 namespace {
 
-// The rows of each group are known on the device only, so the tile goes by their mean over the groups that can have rows
-int choose_grouped(const RouteLayout& r, int N, bool glu, bool exact) {
-  if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE)) return forced_kind();
+// The rows of each group are known on the device only, so the tile goes by their mean over the groups that can have rows.
+// us of 32, 64 and 128 rows a tile, plain results in bf16, random groups: 16 groups of 2048x1408 with a mean of 24 13.3,
+// 12.3, 13.8; of 48 12.9, 12.8, 15.2; of 96 19.5, 16.1, 17.4; of 128 23.6, 20.8, 19.2; of 384 54.7, 44.9, 35.7. 8 groups of
+// 4096x2048: 14.5, 14.8, 17.3; 16.5, 15.8, 19.0; 26.8, 20.5, 21.4; 33.8, 28.7, 22.8; 72.6, 56.2, 45.5 (tiles of 256 rows 62.3:
+// a group's last tile is half empty more often, and nothing hides its first blocks). The kernel of sixteen rows is
+// slower for the fewest rows too (32 tokens through two of 8 experts of 4096x14336: 254 us, tiles of 32 rows 226).
+int choose_grouped(const RouteLayout& r) {
+  if (forced_kind() >= 0) return forced_kind() < LOW ? LOW : forced_kind() > HALF ? HALF : forced_kind();
   const int groups = r.E < r.S ? r.E : r.S;
   const int mean = r.S / (groups > 0 ? groups : 1);
-  if (mean <= 8) return STREAM;
-  if (mean <= 24) return LOW;
-  if (mean <= 80) return MID;
-  if (exact || mean <= 160) return HALF;
-  const long long tiles = (r.S / 256 + (groups + 1) / 2) * (long long)ceil_div(glu ? 2 * N : N, 256);
-  return 2 * tiles >= device_cu_count() ? WHOLE : HALF;
+  return mean <= 24 ? LOW : mean <= 100 ? MID : HALF;
 }
 
-int list_of(int kind) { return kind < HALF ? kind : HALF; }  // the plan's lists have 16, 32, 64 and 128 rows a tile
+// (the plan's lists have 16, 32, 64 and 128 rows a tile: LOW's is list LOW, and so on)
 
 GroupTiles group_tiles(const RouteLayout& r, const int32_t* plan, bool gather, int list) {
   GroupTiles t;
@@ -402,38 +405,30 @@ bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu) {
   if ((long long)fp8_blocks(K) * r.S * 4 >= (1LL << 31) || (long long)(fp8_blocks(N) + 1) * 2 * fp8_blocks(K) * 4 >= (1LL << 31))
     return false;
   if ((long long)r.S * ceil_div(N, 512) >= (1LL << 25)) return false;
-  for (int exact = 0; exact < 2; ++exact) {
-    const int kind = choose_grouped(r, N, glu, exact != 0);
-    if (!grid_fits(tile_bound(r.S, r.E, list_of(kind)), N, kind, glu, 1)) return false;
-  }
-  return true;
+  const int kind = choose_grouped(r);
+  return grid_fits(tile_bound(r.S, r.E, kind), N, kind, glu, 1);
 }
 
-size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int, bool glu, int out_dtype) {
-  if (!by_finish(choose_grouped(r, N, glu, out_dtype >= 2), 1, out_dtype)) return 0;
+size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int out_dtype) {
+  if (!by_finish(choose_grouped(r), 1, out_dtype)) return 0;
   return align256((size_t)r.S * N * 4);
 }
 
 hipError_t launch_fp8_grouped(const Fp8Args& a, const RouteLayout& r, const int32_t* plan, bool gather) {
   const bool exact = a.out_dtype >= 2;
-  const int kind = choose_grouped(r, a.N, a.glu, exact);
+  const int kind = choose_grouped(r);
   TileParams p = tile_params(a);
   p.M = p.scale_rows = r.S;
   p.once = (long long)a.N * (a.glu ? 2 : 1) * a.K * (r.E < r.S ? r.E : r.S) >= kOnceBytes;  // of the groups that can have rows
-  p.groups = group_tiles(r, plan, gather, list_of(kind));
+  p.groups = group_tiles(r, plan, gather, kind);
   const bool finish = by_finish(kind, 1, a.out_dtype);
   if (finish) {
     p.out = a.scratch;
     p.out_dtype = 2;
   }
-  hipError_t e;
-  if (kind == STREAM) {
-    e = launch_rows16(p, 16, a.glu, true, nullptr, 0, a.stream);
-  } else {
-    set_tiles(p, kind, a.glu, p.groups.bound);
-    const auto launch = a.glu ? launch_grouped_glu : launch_grouped_plain;
-    e = launch(p, kind, exact, workgroups(kind, (long long)p.tiles_m * p.tiles_n), 1, a.stream);
-  }
+  set_tiles(p, kind, a.glu, p.groups.bound);
+  const auto launch = a.glu ? launch_grouped_glu : launch_grouped_plain;
+  const hipError_t e = launch(p, kind, exact, workgroups(kind, (long long)p.tiles_m * p.tiles_n), 1, a.stream);
   if (e != hipSuccess || !finish) return e;
   return launch_finish(a.scratch, 1, r.S, a.N, false, a.out, a.out_dtype, a.out_scales, a.stream);
 }
@@ -443,7 +438,7 @@ hipError_t launch_fp8_by_group(const Fp8Args& a, const RouteLayout& r, const int
   p.groups = group_tiles(r, plan, false, kTileLists - 1);
   // tall tiles where they still fill the chip
   const long long tall = (long long)ceil_div(a.M, kRows[HALF]) * ceil_div(a.N, kCols[HALF]) * r.E;
-  const int kind = forced_kind() >= 0 ? forced_kind() : tall >= device_cu_count() ? HALF : MID;
+  const int kind = tall >= device_cu_count() ? HALF : MID;
   set_tiles(p, kind, false, ceil_div(a.M, kRows[kind]));
   return launch_by_group(p, kind, true, (unsigned)((size_t)p.tiles_m * p.tiles_n), r.E, a.stream);
 }

@@ -32,7 +32,6 @@ struct StreamParams {
   const void* values;  // XC 0: x itself, of 16 bits
   int values_dtype;
   int tiles_n, tiles_m;
-  GroupTiles groups;
 };
 
 __device__ __forceinline__ float lane_value(float v, int lane) {
@@ -58,11 +57,11 @@ struct Stream {
   static constexpr __host__ __device__ size_t group_bytes(int groups) { return ((size_t)groups * (128 + 4) + 15) & ~(size_t)15; }
 };
 
-template <int NT, int XC, int D, int W, bool GLU, bool GROUPED, bool ONCE>
+template <int NT, int XC, int D, int W, bool GLU, bool ONCE>
 __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   typedef Stream<NT, XC, D> S;
   static_assert(!GLU || NT % 2 == 0, "a SwiGLU workgroup holds gate rows and the matching up rows");
-  static_assert(XC == 1 || XC == 2 || ((XC == 0 || XC == 4) && !GROUPED), "up to eight rows of x, or 16, or 32");
+  static_assert(XC == 0 || XC == 1 || XC == 2 || XC == 4, "up to two, eight, 16 or 32 rows of x");
   constexpr int MT = S::MT;
   constexpr int OUT = (GLU ? NT / 2 : NT) * 16;  // columns of out a workgroup makes
   extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
@@ -71,28 +70,16 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
   const int t = tile_of(blockIdx.x, p.tiles_m * p.tiles_n);
   const int tm = t % p.tiles_m, tn = t / p.tiles_m;  // neighbours share the weight's rows
   const int N = p.N, n0 = tn * OUT, KB = p.KB;
-  int m0 = tm * 16 * MT, end = p.M, e = 0;
-  if constexpr (GROUPED) {
-    if (!group_tile(p.groups, tm, e, m0, end)) return;
-    if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
-      zero_tile(p.out, p.out_dtype, m0, end - m0, N, n0, OUT);
-      return;
-    }
-    p.w += (size_t)e * (GLU ? 2 : 1) * N * p.ldk;
-    p.ws += (size_t)e * (GLU ? 2 * p.up_blocks : (N + 127) / 128) * KB;
-  }
-  const int rows = min(16 * MT, end - m0);
+  const int m0 = tm * 16 * MT, rows = min(16 * MT, p.M - m0);
   const int kb0 = min(wave * p.slice, KB), nb = min(p.slice, KB - kb0);
   uint8_t* const ring = lds8 + wave * S::kWave;
 
   // Copies: instruction j fills eight rows of a slot (the weight's 16 NT, then x's), lane l row l/8 and position
   // l%8, which holds chunk (l%8) ^ (row % 8). Offsets are bytes from the tile's first row.
-  const bool gathered = GROUPED && p.groups.tokens;
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
   const uint32_t wrows = (uint32_t)(GLU ? 2 * N - n0 : min(OUT, N - n0));
   const __amdgpu_buffer_rsrc_t wrs = make_rsrc(p.w + (size_t)n0 * p.ldk, wrows * (uint32_t)p.ldk);
-  const __amdgpu_buffer_rsrc_t xrs = make_rsrc(p.x + (gathered ? 0 : (size_t)m0 * p.ldk),
-                                               (uint32_t)(gathered ? p.groups.tokens : rows) * (uint32_t)p.ldk);
+  const __amdgpu_buffer_rsrc_t xrs = make_rsrc(p.x + (size_t)m0 * p.ldk, (uint32_t)rows * (uint32_t)p.ldk);
   uint32_t woff[2 * NT], xoff[XC ? XC : 1];
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
@@ -100,20 +87,14 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     const int src = GLU ? min(r % OUT, N - 1 - n0) + (r / OUT) * N : min(r, N - 1 - n0);
     woff[j] = (uint32_t)src * (uint32_t)p.ldk + (uint32_t)chunk;
   }
-  auto x_row = [&](int r) __attribute__((always_inline)) {
-    if constexpr (GROUPED)
-      if (gathered) return r < rows ? p.groups.plan[p.groups.token + m0 + r] : -1;
-    return r < rows ? r : -1;
-  };
 #pragma unroll
   for (int j = 0; j < XC; ++j) {  // rows past the tile's are zeros
-    const int src = x_row(8 * j + (lane >> 3));
-    xoff[j] = src < 0 ? kOutOfRange : (uint32_t)src * (uint32_t)p.ldk + (uint32_t)chunk;
+    const int r = 8 * j + (lane >> 3);
+    xoff[j] = r < rows ? (uint32_t)r * (uint32_t)p.ldk + (uint32_t)chunk : kOutOfRange;
   }
   // x's scales: lane l that of row l (the last copy of a slot)
   const __amdgpu_buffer_rsrc_t srs = make_rsrc(p.xs, 0x7FFFFFFFu);
-  const int srow = lane < 16 * MT ? x_row(lane) : -1;
-  const uint32_t soff = srow < 0 ? kOutOfRange : (uint32_t)(gathered ? srow : m0 + srow) * 4u;
+  const uint32_t soff = lane < rows ? (uint32_t)(m0 + lane) * 4u : kOutOfRange;
 
   auto copy = [&](int i) __attribute__((always_inline)) {  // block i of the slice, into slot i % D
     uint8_t* const dst = ring + (i % D) * S::kSlot;

@@ -253,13 +253,6 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
       }
       if constexpr (MODE == GROUPED) {
         group_tile(p.groups, tm, e, m0, end);
-        if constexpr (BM > 128) {
-          // the list's tiles have 128 rows: every second one of a group stands for itself and the next
-          const int first = e < p.groups.E ? p.groups.plan[e] : p.groups.plan[p.groups.E];
-          const int last = e < p.groups.E ? p.groups.plan[e + 1] : p.M;
-          if ((m0 - first) % BM) continue;
-          end = min(m0 + BM, last);
-        }
         if (e >= p.groups.E) {  // the slots of no group: their rows are zeros
           if (GLU && OUT == 128 && p.out_dtype == kE4M3) {
             uint8_t* const codes = static_cast<uint8_t*>(p.out);
@@ -401,7 +394,7 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
     meet();
     const int nb = (kb1 - kb0 + KG - 1) / KG;  // (a block past the last one is zeros)
     if (nb <= 0) return;
-    if constexpr (MODE == GROUPED) {
+    if constexpr (MODE == GROUPED && T::kWM > 1) {
       // of a tile that its group does not fill, a wave without rows takes part in the copies only (at this rate a
       // product's time is its energy, so that zeros would be multiplied at the others' cost)
       if (wm * MT * 16 >= rows) {
@@ -410,7 +403,6 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
           const int free = stage == 0 ? ST - 1 : stage - 1;
 #pragma unroll
           for (int j = 0; j < T::kLoads; ++j) copy(j, i + ST - 1, free);
-          touch(i + T::kTouch);
           meet();
           stage = stage == ST - 1 ? 0 : stage + 1;
         }
@@ -642,7 +634,7 @@ enum Kind { STREAM = 0, LOW = 1, MID = 2, HALF = 3, WHOLE = 4 };
 typedef Tile<4, 1, 2, 2, 3, 3> Low;       // 32 rows, 128 columns
 typedef Tile<4, 1, 2, 4, 3, 2> Mid;       // 64, 128
 typedef Tile<4, 2, 4, 4, 3, 2> Half;      // 128, 256
-typedef Tile<4, 2, 4, 8, 2, 3, 3> Whole;  // 256, 256: results of 16 bits only (widened fragments would not fit)
+typedef Tile<4, 2, 4, 8, 2, 3, 3> Whole;  // 256, 256: dense rows, results of 16 bits (widened fragments would not fit)
 
 template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
 hipError_t launch_tile(const TileParams& p, unsigned grid, int gy, hipStream_t s) {
@@ -674,7 +666,8 @@ template <bool GLU, bool WROWS, int MODE>
 hipError_t launch_kind(const TileParams& p, int kind, bool exact, unsigned grid, int gy, hipStream_t s) {
   if (exact || WROWS) {
     switch (kind) {
-      case LOW: return launch_tile<Low, GLU, WROWS, MODE, true>(p, grid, gy, s);
+      case LOW:
+        if constexpr (MODE != BY_GROUP) return launch_tile<Low, GLU, WROWS, MODE, true>(p, grid, gy, s);
       case MID: return launch_tile<Mid, GLU, WROWS, MODE, true>(p, grid, gy, s);
       default: return launch_tile<Half, GLU, WROWS, MODE, true>(p, grid, gy, s);
     }
@@ -684,7 +677,8 @@ hipError_t launch_kind(const TileParams& p, int kind, bool exact, unsigned grid,
       case LOW: return launch_tile<Low, GLU, WROWS, MODE, false>(p, grid, gy, s);
       case MID: return launch_tile<Mid, GLU, WROWS, MODE, false>(p, grid, gy, s);
       case HALF: return launch_tile<Half, GLU, WROWS, MODE, false>(p, grid, gy, s);
-      default: return launch_tile<Whole, GLU, WROWS, MODE, false>(p, grid, gy, s);
+      default:
+        if constexpr (MODE == DENSE) return launch_tile<Whole, GLU, WROWS, MODE, false>(p, grid, gy, s);
     }
   }
   return hipErrorInvalidValue;
