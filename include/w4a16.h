@@ -351,9 +351,13 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
  * rounded fp32 steps and one rounding to 8 bits, ties to even. A group of zeros has the least scale
  * and zero codes. A group that holds an infinity or a NaN has a NaN scale and NaN codes, so that
  * every result it enters is NaN.
- * Products: the codes' products of a block of 128 k are summed in fp32 on the matrix cores, the
- * block's sum is multiplied by its two scales and added to the result in fp32, which is rounded
- * once. Results are deterministic.
+ * Products: the codes' products of a block of 128 k are summed on the matrix cores, the block's sum
+ * is multiplied by its two scales and added to the result in fp32, which is rounded once. Results
+ * are deterministic. A block's sum is an fp32 one for fp32 results, for h that leaves as codes and in
+ * the kernels of 16 and 32 rows (w4a16_fp8_kernel_name). For other 16-bit results it comes from the
+ * 8-bit MFMA, which drops product bits about 17 below the block's largest: the sum is off by at most
+ * 2^-10 of its largest product, on normal operands 1.5e-5 of the result, an eighth of what rounding
+ * to fp16 costs.
  * Limits, else W4A16_ERR_UNSUPPORTED: a product's depth is a multiple of 16; operands whose
  * offsets 31 bits hold (K < 2^23; rows * K / 32 < 2^31; a SwiGLU weight below 2 GiB a group).
  * Codes, 16-bit x and dy need 16-byte alignment, other arrays that of their elements (outputs of
@@ -384,13 +388,14 @@ w4a16_status w4a16_quantize_fp8_weight(const void* w, int N, int K, w4a16_dtype 
                                        float* scales, uint8_t* codes_t, float* scales_t, void* stream);
 
 /* Bytes of scratch w4a16_gemm_fp8 needs on the current device: the codes and scales of a 16-bit x
- * (M * K and about M * K / 32 bytes), and for e4m3 out of shapes whose kernel cannot quantize it h in
- * fp32. 0 for M = 0 or bad shapes. */
+ * (M * K and about M * K / 32 bytes; none for one or two rows that the kernel quantizes by itself),
+ * fp32 sums of every slice where the depth is cut, and for e4m3 out of shapes whose kernel cannot
+ * quantize it h in fp32. 0 for M = 0 or bad shapes. */
 size_t w4a16_fp8_workspace_bytes(int M, int K, int N, w4a16_dtype x_dtype, int swiglu,
                                  w4a16_dtype out_dtype);
 
 /* y = x W^T for 8-bit weights.
- *   x         [in]  [M][K]: F16 or BF16 (quantized by a first kernel into the workspace), or E4M3
+ *   x         [in]  [M][K]: F16 or BF16 (quantized first, or by the kernel), or E4M3
  *                   codes with x_scales, as w4a16_quantize_fp8 writes them (NULL for 16-bit x)
  *   codes     [in]  [N][K], one row an output feature;  scales [in] float [ceil(N/128)][ceil(K/128)]
  *   out       [out] out_dtype [M][N]: x's 16-bit type or F32; any of F16, BF16, F32 for E4M3 x
@@ -422,11 +427,13 @@ w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const fl
                                     size_t workspace_bytes, void* stream);
 
 /* Gradients of y = x W^T: dx = dy W, with dy quantized by rows, and dw = dy^T x, with both quantized
- * by columns (each call quantizes them anew).
+ * by columns (each call quantizes them anew; dy is read once for both).
  *   dy       [in]  act [M][N], x [in] act [M][K]; N % 16 == 0, K % 16 == 0
  *   codes_t, scales_t [in] the transposed weight's [K][N] and float [ceil(K/128)][ceil(N/128)]
  *   dx       [out] act [M][K], or NULL;  dw [out] float [N][K], or NULL (x is read for dw alone,
  *                  codes_t and scales_t for dx alone)
+ *   workspace [in/out] >= w4a16_fp8_backward_workspace_bytes(...) whichever are asked for, 256-byte
+ *                  aligned: dy's row codes, both operands' column codes, and slices' sums
  * M = 0: dw is cleared. */
 size_t w4a16_fp8_backward_workspace_bytes(int M, int K, int N);
 w4a16_status w4a16_gemm_fp8_backward(const void* dy, const void* x, int M, int K, int N, w4a16_dtype act,

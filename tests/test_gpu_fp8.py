@@ -216,7 +216,7 @@ PRODUCTS = [
     # M, K, N: one token to many, depths and widths that divide nothing
     (1, 16, 1), (1, 4096, 512), (1, 14352, 96), (1, 33024, 48), (2, 144, 33), (2, 4112, 300), (2, 16400, 40), (3, 1040, 100), (7, 2048, 640), (15, 528, 1000), (16, 256, 256), (17, 4112, 130),
     (18, 1040, 4608), (20, 144, 100), (32, 8208, 48), (31, 128, 2048), (33, 384, 129), (48, 640, 777), (63, 896, 128), (64, 1024, 384), (65, 512, 257), (100, 272, 1024),
-    (127, 1152, 255), (128, 2176, 512), (129, 160, 640), (200, 1280, 1001), (256, 640, 2048), (257, 400, 512), (333, 656, 501),
+    (127, 1152, 255), (128, 2176, 512), (129, 160, 640), (200, 1280, 1001), (48, 1680, 300), (64, 8208, 200), (90, 3600, 400), (333, 2896, 700), (256, 640, 2048), (257, 400, 512), (333, 656, 501),
 ]
 
 
@@ -246,7 +246,7 @@ def test_products(M, K, N, kind):
         assert torch.equal(out[1:-1], y) and bool((out[0] == 7).all()) and bool((out[-1] == 7).all())
 
 
-@pytest.mark.parametrize("M,K,N2", [(1, 256, 2), (1, 2048, 512), (2, 4112, 160), (5, 144, 100), (16, 640, 704), (17, 528, 98), (32, 4112, 288), (33, 1040, 258), (64, 512, 96),
+@pytest.mark.parametrize("M,K,N2", [(1, 256, 2), (1, 2048, 512), (2, 4112, 160), (5, 144, 100), (16, 640, 704), (17, 528, 98), (32, 4112, 288), (33, 1040, 258), (48, 1680, 1056), (64, 8208, 512), (100, 4112, 1024), (64, 512, 96),
                                     (70, 272, 640), (130, 384, 1000), (257, 256, 1024), (300, 528, 288)])
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 def test_swiglu(M, K, N2, kind):
@@ -583,6 +583,65 @@ def test_no_rows():
     assert w4.gemm_fp8_grouped(x, r, codes, scales, gather=True).shape == (0, 64)
     dx, dw = w4.gemm_fp8_grouped_backward(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), x, r, *_weight((3,), 128, 64, 4)[:2])
     assert dw.shape == (3, 64, 128) and bool((dw == 0).all())
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_rows_of_more_than_2_to_the_32_values():
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    M, K = 262500, 16384
+    assert M * K > 2 ** 32
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    last, lv = _rows((5, K), "bf16", 1)
+    x[-5:] = last
+    codes, scales = w4.quantize_fp8(x)
+    q, s = F.quantize_rows(lv)
+    assert np.array_equal(_bits(codes[-5:]), q) and np.array_equal(scales[:, -5:].cpu().numpy(), s)
+    assert not bool(codes[:16].view(torch.uint8).any())
+    del codes, scales
+    codes, scales = w4.quantize_fp8_columns(x)
+    q, s = F.quantize_columns(np.concatenate([np.zeros((M % 128 - 5, 64), np.float32), lv[:, :64]]))
+    assert np.array_equal(_bits(codes[:64, M // 128 * 128:M]), q[:, :M % 128])
+    assert np.array_equal(scales[-1, :64].cpu().numpy(), s[0])
+
+
+def test_a_product_of_more_than_2_to_the_32_results():
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    M, K, N = 134300, 128, 32008
+    assert M * N > 2 ** 32
+    x, xv = _rows((300, K), "bf16", 1)
+    codes, scales, wv = _weight((), N, K, 2)
+    big = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    big[-300:] = x
+    y = w4.gemm_fp8(big, codes, scales)
+    v = F.rows_value(*F.quantize_rows(xv))
+    ref = F.gemm_fp8_ref(v, wv)
+    _within(y[-300:].cpu().double().numpy(), ref, _stored(ref, _sum_bound(v, wv, "bf16"), "bf16"), "last rows")
+    assert not bool(y[:1000].any())
+
+
+def test_experts_of_more_than_2_to_the_32_codes():
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    E, N, K = 33, 8192, 16384
+    assert E * N * K > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.empty(E, N, K, dtype=torch.uint8, device="cuda")
+    for e in range(E):  # magnitudes up to 4: no NaN among them
+        codes[e] = torch.randint(0, 0x48, (N, K), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.rand(E, N // 128, K // 128, device="cuda", generator=g) + 0.5
+    x, xv = _rows((60, K), "bf16", 4)
+    ids = torch.tensor([0, 16, 32] * 20, dtype=torch.int32, device="cuda").reshape(-1, 1)
+    r = w4.route(ids, E)
+    y = w4.gemm_fp8_grouped(x, r, codes.view(torch.float8_e4m3fn), scales, gather=True)
+    v = F.rows_value(*F.quantize_rows(xv))
+    for i, e in enumerate([0, 16, 32]):
+        wv = F.weight_value(codes[e, -128:].cpu().numpy(), scales[e, -1:].cpu().numpy())[28:]
+        ref = F.gemm_fp8_ref(v[i::3], wv)
+        got = y[20 * i:20 * i + 20, -100:].cpu().double().numpy()
+        _within(got, ref, _stored(ref, _sum_bound(v[i::3], wv, "bf16"), "bf16"), f"group {e}")
 
 
 # ------------------------------------------------------------------ as they are used

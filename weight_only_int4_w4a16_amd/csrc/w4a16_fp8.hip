@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void fp8_finish_kernel(const float* __restrict
       for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
       *reinterpret_cast<b8_t*>(static_cast<__bf16*>(out) + at) = o;
     }
-  } else if (some >= 8 && N % 4 == 0) {
+  } else if (some >= 8 && N % 4 == 0 && out_dtype == 2) {
     *reinterpret_cast<f4_t*>(static_cast<float*>(out) + at) = f4_t{v[0], v[1], v[2], v[3]};
     *reinterpret_cast<f4_t*>(static_cast<float*>(out) + at + 4) = f4_t{v[4], v[5], v[6], v[7]};
   } else {

@@ -17,12 +17,17 @@
 // widened in registers (one instruction for two codes) and four v_mfma_f32_16x16x32_f16 sum a block in full
 // fp32 (1e-8 of the result on the same operands), at half the rate: 1.7 PFLOP/s with the fmas.
 //
-// Tiles. Both operands go from memory straight to LDS (buffer_load_dwordx4 ... lds), one block of k ahead of the
+// Rates reached: 2048 rows of 8192x28672 in bf16 440 to 455 us, 2.1 PFLOP/s, in fp32 805 to 840, 1.2 PFLOP/s. With codes of
+// all zeros the same launches take 325 and 715 us: the chip lowers its clock under full load, so that past this point a
+// product's time is its energy. Eight fewer cycles in a hundred (the widened product by v_mfma_f32_32x32x16_f16) or half
+// the operand reads (v_mfma_f32_32x32x64_f8f6f4) changed the first figures by 0 to 3 %, up or down.
+//
+// Tiles. Both operands go from memory straight to LDS (buffer_load_dwordx4 ... lds), one or two blocks of k ahead of the
 // MFMAs, rows of 128 bytes whose 16-byte chunk c lies at position c ^ (row % 8), so that the fragment reads
 // of eight rows use every bank once. A lane's 32 bytes of a row are chunks l/16 and l/16 + 4: the same k for both operands,
 // in whatever order. Rows of the weight past its end repeat the last one and are never stored; chunks past K, and rows of
-// x past the tile's end, are read out of range and land as zeros. The block's scales of the tile's rows (and of its weights' rows) take one
-// 4-byte copy a lane.
+// x past the tile's end, are read out of range and land as zeros. The block's scales of the tile's rows (and of its
+// weights' rows) take one 4-byte copy a lane.
 #pragma once
 
 #include <type_traits>
@@ -481,108 +486,108 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
   float* const slice = slices + wave * 16 * PITCH;
   float* const most = slices + T::kWaves * 16 * PITCH;  // [WN][BM], e4m3
   auto store = [&](int m0, int rows, int n0, size_t out_row) __attribute__((always_inline)) {
-  const int nw = n0 + wn * COLS;  // this wave's first column
-  if constexpr (GLU) {
+    const int nw = n0 + wn * COLS;  // this wave's first column
+    if constexpr (GLU) {
 #pragma unroll
-    for (int nt = 0; nt < NT / 2; ++nt)
+      for (int nt = 0; nt < NT / 2; ++nt)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float g = acc[nt][mt][i], u = acc[nt + NT / 2][mt][i];
-          acc[nt][mt][i] = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;  // the reciprocal to 1 ulp
-        }
-    if (OUT == 128 && p.out_dtype == kE4M3) {
-      // the largest |h| of a row over the tile's 128 columns: this wave's, then all waves' of the row
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        uint32_t v = 0;
-#pragma unroll
-        for (int nt = 0; nt < NT / 2; ++nt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int n = nw + nt * 16 + 4 * q + i;
-            const float h = acc[nt][mt][i];  // (a bit cast of a vector's element itself takes the first one)
-            const uint32_t b = __builtin_bit_cast(uint32_t, h) & 0x7FFFFFFFu;
-            v = max(v, n < N ? b : 0u);
+            const float g = acc[nt][mt][i], u = acc[nt + NT / 2][mt][i];
+            acc[nt][mt][i] = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;  // the reciprocal to 1 ulp
           }
-        v = max(v, (uint32_t)__shfl_xor((int)v, 16));
-        v = max(v, (uint32_t)__shfl_xor((int)v, 32));
-        if (q == 0) most[wn * BM + (wm * MT + mt) * 16 + l16] = __builtin_bit_cast(float, v);
-      }
-      __syncthreads();
-    }
-  }
+      if (OUT == 128 && p.out_dtype == kE4M3) {
+        // the largest |h| of a row over the tile's 128 columns: this wave's, then all waves' of the row
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int r0 = (wm * MT + mt) * 16;
-    if (r0 >= rows) break;  // of this wave's rows, so of all its lanes
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t v = 0;
 #pragma unroll
-    for (int nt = 0; nt < COLS / 16; ++nt)
-      *reinterpret_cast<f4_t*>(slice + l16 * PITCH + nt * 16 + 4 * q) = acc[nt][mt];
-    __builtin_amdgcn_wave_barrier();
-    // a lane takes eight columns of a row
+          for (int nt = 0; nt < NT / 2; ++nt)
 #pragma unroll
-    for (int pass = 0; pass < (16 * COLS / 8 + 63) / 64; ++pass) {
-      const int piece = lane + 64 * pass;
-      if (16 * COLS / 8 % 64 != 0 && piece >= 16 * COLS / 8) continue;
-      const int r = piece / (COLS / 8), c = piece % (COLS / 8) * 8;
-      if (r0 + r >= rows) continue;
-      const float* src = slice + r * PITCH + c;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const f4_t f = *reinterpret_cast<const f4_t*>(src + 4 * i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * i + j] = f[j];
-      }
-      const int n = nw + c, some = N - n;
-      if (some <= 0) continue;
-      const size_t at = (out_row + m0 + r0 + r) * (size_t)N + n;
-      if (GLU && OUT == 128 && p.out_dtype == kE4M3) {
-        uint32_t b = 0;
-#pragma unroll
-        for (int w = 0; w < T::kWN; ++w) b = max(b, __builtin_bit_cast(uint32_t, most[w * BM + r0 + r]));
-        const float s = fp8_scale(b);
-        const Fp8Divisor d = fp8_divisor(s);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fp8_quotient(v[j], d);
-        const uint32_t lo = fp8_pack(v[0], v[1], v[2], v[3]), hi = fp8_pack(v[4], v[5], v[6], v[7]);
-        uint8_t* const dst = static_cast<uint8_t*>(p.out) + at;
-        if (some >= 8 && N % 8 == 0) {
-          *reinterpret_cast<uint2*>(dst) = uint2{lo, hi};
-        } else {
-          for (int j = 0; j < 8 && j < some; ++j) dst[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+            for (int i = 0; i < 4; ++i) {
+              const int n = nw + nt * 16 + 4 * q + i;
+              const float h = acc[nt][mt][i];  // (a bit cast of a vector's element itself takes the first one)
+              const uint32_t b = __builtin_bit_cast(uint32_t, h) & 0x7FFFFFFFu;
+              v = max(v, n < N ? b : 0u);
+            }
+          v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+          v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+          if (q == 0) most[wn * BM + (wm * MT + mt) * 16 + l16] = __builtin_bit_cast(float, v);
         }
-        if (wn == 0 && c == 0) p.out_scales[(size_t)(n0 / 128) * p.scale_rows + m0 + r0 + r] = s;
-        continue;
-      }
-      if (p.out_dtype == 2) {
-        float* const dst = static_cast<float*>(p.out) + at;
-        if (some >= 8 && N % 4 == 0) {
-          *reinterpret_cast<f4_t*>(dst) = f4_t{v[0], v[1], v[2], v[3]};
-          *reinterpret_cast<f4_t*>(dst + 4) = f4_t{v[4], v[5], v[6], v[7]};
-        } else {
-          for (int j = 0; j < 8 && j < some; ++j) dst[j] = v[j];
-        }
-      } else if (some >= 8 && N % 8 == 0) {
-        if (p.out_dtype == 0) {
-          h8_t o;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = (_Float16)v[j];
-          *reinterpret_cast<h8_t*>(static_cast<_Float16*>(p.out) + at) = o;
-        } else {
-          b8_t o;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
-          *reinterpret_cast<b8_t*>(static_cast<__bf16*>(p.out) + at) = o;
-        }
-      } else {
-        for (int j = 0; j < 8 && j < some; ++j) store_out(p.out, at + j, v[j], p.out_dtype);
+        __syncthreads();
       }
     }
-    __builtin_amdgcn_wave_barrier();
-  }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r0 = (wm * MT + mt) * 16;
+      if (r0 >= rows) break;  // of this wave's rows, so of all its lanes
+#pragma unroll
+      for (int nt = 0; nt < COLS / 16; ++nt)
+        *reinterpret_cast<f4_t*>(slice + l16 * PITCH + nt * 16 + 4 * q) = acc[nt][mt];
+      __builtin_amdgcn_wave_barrier();
+      // a lane takes eight columns of a row
+#pragma unroll
+      for (int pass = 0; pass < (16 * COLS / 8 + 63) / 64; ++pass) {
+        const int piece = lane + 64 * pass;
+        if (16 * COLS / 8 % 64 != 0 && piece >= 16 * COLS / 8) continue;
+        const int r = piece / (COLS / 8), c = piece % (COLS / 8) * 8;
+        if (r0 + r >= rows) continue;
+        const float* src = slice + r * PITCH + c;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f4_t f = *reinterpret_cast<const f4_t*>(src + 4 * i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * i + j] = f[j];
+        }
+        const int n = nw + c, some = N - n;
+        if (some <= 0) continue;
+        const size_t at = (out_row + m0 + r0 + r) * (size_t)N + n;
+        if (GLU && OUT == 128 && p.out_dtype == kE4M3) {
+          uint32_t b = 0;
+#pragma unroll
+          for (int w = 0; w < T::kWN; ++w) b = max(b, __builtin_bit_cast(uint32_t, most[w * BM + r0 + r]));
+          const float s = fp8_scale(b);
+          const Fp8Divisor d = fp8_divisor(s);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = fp8_quotient(v[j], d);
+          const uint32_t lo = fp8_pack(v[0], v[1], v[2], v[3]), hi = fp8_pack(v[4], v[5], v[6], v[7]);
+          uint8_t* const dst = static_cast<uint8_t*>(p.out) + at;
+          if (some >= 8 && N % 8 == 0) {
+            *reinterpret_cast<uint2*>(dst) = uint2{lo, hi};
+          } else {
+            for (int j = 0; j < 8 && j < some; ++j) dst[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+          }
+          if (wn == 0 && c == 0) p.out_scales[(size_t)(n0 / 128) * p.scale_rows + m0 + r0 + r] = s;
+          continue;
+        }
+        if (p.out_dtype == 2) {
+          float* const dst = static_cast<float*>(p.out) + at;
+          if (some >= 8 && N % 4 == 0) {
+            *reinterpret_cast<f4_t*>(dst) = f4_t{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f4_t*>(dst + 4) = f4_t{v[4], v[5], v[6], v[7]};
+          } else {
+            for (int j = 0; j < 8 && j < some; ++j) dst[j] = v[j];
+          }
+        } else if (some >= 8 && N % 8 == 0) {
+          if (p.out_dtype == 0) {
+            h8_t o;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = (_Float16)v[j];
+            *reinterpret_cast<h8_t*>(static_cast<_Float16*>(p.out) + at) = o;
+          } else {
+            b8_t o;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
+            *reinterpret_cast<b8_t*>(static_cast<__bf16*>(p.out) + at) = o;
+          }
+        } else {
+          for (int j = 0; j < 8 && j < some; ++j) store_out(p.out, at + j, v[j], p.out_dtype);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
   };
 
   if constexpr (LOOP) {
