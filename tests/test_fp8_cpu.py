@@ -239,6 +239,15 @@ def test_gradients_have_room_for_partial_sums(L):
     assert most > 0
 
 
+def test_workspace_covers_every_out_dtype(L):
+    import torch
+    import weight_only_int4_w4a16_amd as w4
+    for M, K, N in [(1, 256, 64), (20, 8192, 1024), (40, 2048, 4096), (64, 14336, 4096), (333, 2896, 5001)]:
+        for x, dt in ((torch.bfloat16, BF16), (torch.float8_e4m3fn, E4M3)):
+            have = w4.fp8_workspace_bytes(M, K, N, x)
+            assert have == max(L.w4a16_fp8_workspace_bytes(M, K, N, dt, 0, o) for o in (BF16, F32))
+
+
 # ------------------------------------------------------------------ refusals of the binding (meta and host tensors)
 
 def _refused(fn, match, status=ARG):

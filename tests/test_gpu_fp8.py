@@ -724,6 +724,85 @@ def test_two_streams_at_once():
         assert all(torch.equal(y, s[3]) for y in got[i])
 
 
+GUARD = 4096
+
+
+def _guarded(shape, dtype):
+    """An uninitialised tensor with bytes behind it that a call must leave alone, and a check of them."""
+    torch = torch_mod()
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    buf = torch.full((n + GUARD,), 0xA5, dtype=torch.uint8, device="cuda")
+    return buf[:n].view(dtype).view(shape), lambda what: bool((buf[n:] == 0xA5).all()) or pytest.fail(f"{what}: written past the end")
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 300), (2, 512, 4), (5, 1040, 36), (16, 512, 1000), (20, 8192, 1020), (20, 512, 100), (40, 4096, 300), (64, 8208, 404),
+                                   (100, 2048, 132), (333, 2896, 700), (300, 256, 1001), (257, 4096, 516), (2049, 256, 1300)])
+def test_nothing_past_the_ends(M, K, N):
+    """Outputs and workspaces of exactly the bytes they need, with bytes behind them that stay."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    x, _ = _rows((M, K), "bf16", M + N)
+    codes, scales, _ = _weight((), N, K, N)
+    q, s = w4.quantize_fp8(x)
+    for a, xs in ((x, None), (q, s)):
+        for dtype in (torch.bfloat16, torch.float32):
+            want = w4.gemm_fp8(a, codes, scales, x_scales=xs, out_dtype=dtype)
+            out, out_ends = _guarded((M, N), dtype)
+            ws, ws_ends = _guarded((max(1, w4.fp8_workspace_bytes(M, K, N, a.dtype)),), torch.uint8)
+            w4.gemm_fp8(a, codes, scales, x_scales=xs, out=out, workspace=ws)
+            out_ends(f"out {dtype}"), ws_ends(f"workspace {dtype}")
+            assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 64, 16384), (40, 256, 8192), (333, 272, 144), (9000, 272, 160)])
+def test_gradients_stay_in_their_workspace(M, K, N):
+    import weight_only_int4_w4a16_amd as w4
+    from weight_only_int4_w4a16_amd import binding
+    torch = torch_mod()
+    L = binding.lib()
+    x, _ = _rows((M, K), "bf16", 1)
+    dy, _ = _rows((M, N), "bf16", 2)
+    codes_t, scales_t, _ = _weight((), K, N, 3)
+    dx, dw = w4.gemm_fp8_backward(dy, x, codes_t, scales_t)
+    ws, ends = _guarded((L.w4a16_fp8_backward_workspace_bytes(M, K, N),), torch.uint8)
+    a, b = w4.gemm_fp8_backward(dy, x, codes_t, scales_t, workspace=ws)
+    ends("workspace")
+    assert torch.equal(a, dx) and torch.equal(b, dw)
+    if M > 1000:
+        return
+    r = w4.route(torch.arange(M, device="cuda", dtype=torch.int32).reshape(-1, 1) % 4, 3)
+    codes_t, scales_t, _ = _weight((3,), K, N, 4)
+    dx, dw = w4.gemm_fp8_grouped_backward(dy, x, r, codes_t, scales_t)
+    ws, ends = _guarded((L.w4a16_fp8_grouped_backward_workspace_bytes(M, 1, 3, K, N),), torch.uint8)
+    a, b = w4.gemm_fp8_grouped_backward(dy, x, r, codes_t, scales_t, workspace=ws)
+    ends("workspace of routed rows")
+    assert torch.equal(a, dx) and torch.equal(b, dw)
+
+
+def test_routed_products_stay_in_their_ends():
+    import weight_only_int4_w4a16_amd as w4
+    from weight_only_int4_w4a16_amd import binding
+    torch = torch_mod()
+    L = binding.lib()
+    for tokens, topk, E, K, N2 in [(7, 2, 3, 144, 96), (100, 2, 4, 256, 288), (600, 1, 2, 128, 416)]:
+        r = w4.route(torch.from_numpy(_ids(tokens, topk, E, tokens)).cuda(), E)
+        x, _ = _rows((tokens, K), "bf16", 1)
+        codes, scales, _ = _weight((E,), N2, K, 2, halves=2)
+        S = tokens * topk
+        for dtype, n in ((torch.bfloat16, 1), (torch.float32, 2)):
+            want = w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, out_dtype=dtype)
+            out, ends = _guarded((S, N2 // 2), dtype)
+            ws, ws_ends = _guarded((L.w4a16_fp8_grouped_workspace_bytes(tokens, topk, E, 1, K, N2, 1, 1, n),), torch.uint8)
+            w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, out=out, workspace=ws)
+            ends("out"), ws_ends("workspace")
+            assert torch.equal(out, want)
+        want = w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, quantized=True)
+        ws, ws_ends = _guarded((L.w4a16_fp8_grouped_workspace_bytes(tokens, topk, E, 1, K, N2, 1, 1, 3),), torch.uint8)
+        got = w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, quantized=True, workspace=ws)
+        ws_ends("workspace")
+        assert np.array_equal(_bits(got[0]), _bits(want[0])) and torch.equal(got[1], want[1])
+
+
 def test_caller_workspace_and_refusals_on_the_device():
     import weight_only_int4_w4a16_amd as w4
     torch = torch_mod()

@@ -1045,14 +1045,16 @@ def _fp8_scratch(x, need, workspace):
 
 
 def fp8_workspace_bytes(M: int, K: int, N: int, x_dtype, swiglu: bool = False, quantized: bool = False) -> int:
-    """Bytes that :func:`gemm_fp8` (``swiglu``: :func:`gemm_fp8_swiglu`) needs for ``x[M, K]`` of ``x_dtype``."""
+    """Bytes that :func:`gemm_fp8` (``swiglu``: :func:`gemm_fp8_swiglu`) needs for ``x[M, K]`` of ``x_dtype``, whatever its
+    out dtype."""
     torch = _torch()
     if not _dtypes:
         _load_dtypes()
     if max(M, K, N) > _INT_MAX:
         return 0
     dt = E4M3 if x_dtype is torch.float8_e4m3fn else _dtypes[x_dtype]
-    return int(lib().w4a16_fp8_workspace_bytes(M, K, N, dt, int(swiglu), E4M3 if quantized else F32))
+    outs = (E4M3,) if quantized else (F32, _dtypes[torch.bfloat16] if dt == E4M3 else dt)
+    return max(int(lib().w4a16_fp8_workspace_bytes(M, K, N, dt, int(swiglu), o)) for o in outs)
 
 
 def _gemm_fp8(x, codes, scales, x_scales, glu, quantized, out_dtype, out, workspace):

@@ -301,8 +301,9 @@ bool fp8_fits(int M, int N, int K, bool glu) {
   if ((long long)K >= (1LL << 23) || wrows * K >= (1LL << 31)) return false;
   if ((long long)fp8_blocks(K) * M * 4 >= (1LL << 31) || (long long)(fp8_blocks(N) + 1) * 2 * fp8_blocks(K) * 4 >= (1LL << 31))
     return false;
-  const Plan c = choose(M, glu ? 2 * N : N, K, glu, true), d = choose(M, glu ? 2 * N : N, K, glu, false);
   if ((long long)M * ceil_div(N, 512) >= (1LL << 25)) return false;
+  if ((long long)ceil_div(M, 16) * ceil_div(glu ? 2 * N : N, 16) * 512 * 12 < (1LL << 32)) return true;  // on any tile
+  const Plan c = choose(M, glu ? 2 * N : N, K, glu, true), d = choose(M, glu ? 2 * N : N, K, glu, false);
   return grid_fits(ceil_div(M, kRows[c.kind]), N, c.kind, glu, c.S) && grid_fits(ceil_div(M, kRows[d.kind]), N, d.kind, glu, d.S);
 }
 
