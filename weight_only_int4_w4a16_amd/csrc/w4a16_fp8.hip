@@ -36,8 +36,8 @@ __global__ __launch_bounds__(256) void fp8_finish_kernel(const float* __restrict
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
   auto add = [&](const float* row, float (&sum)[8]) __attribute__((always_inline)) {
-    if (some >= 8 && N % 4 == 0) {
-      const f4_t a = *reinterpret_cast<const f4_t*>(row), b = *reinterpret_cast<const f4_t*>(row + 4);
+    if (some >= 8) {
+      const f4_t a = *reinterpret_cast<const f4_any_t*>(row), b = *reinterpret_cast<const f4_any_t*>(row + 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum[j] += a[j], sum[4 + j] += b[j];
     } else {
@@ -69,25 +69,8 @@ __global__ __launch_bounds__(256) void fp8_finish_kernel(const float* __restrict
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + at) = uint2{fp8_pack(v[0], v[1], v[2], v[3]), fp8_pack(v[4], v[5], v[6], v[7])};
       if ((lane & 15) == 0) out_scales[(size_t)(n >> 7) * M + m] = sc;
     }
-  } else if (some >= 8 && N % 8 == 0 && out_dtype != 2) {
-    if (out_dtype == 0) {
-      h8_t o;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = (_Float16)v[j];
-      *reinterpret_cast<h8_t*>(static_cast<_Float16*>(out) + at) = o;
-    } else {
-      b8_t o;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
-      *reinterpret_cast<b8_t*>(static_cast<__bf16*>(out) + at) = o;
-    }
-  } else if (some >= 8 && N % 4 == 0 && out_dtype == 2) {
-    *reinterpret_cast<f4_t*>(static_cast<float*>(out) + at) = f4_t{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f4_t*>(static_cast<float*>(out) + at + 4) = f4_t{v[4], v[5], v[6], v[7]};
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < some) store_out(out, at + j, v[j], out_dtype);
+    fp8_store8(out, at, v, some, out_dtype);
   }
 }
 

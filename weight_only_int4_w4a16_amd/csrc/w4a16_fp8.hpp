@@ -119,9 +119,34 @@ __device__ __forceinline__ uint32_t max_of_16_lanes(uint32_t v) {
 }
 
 typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
-// 16 bytes at any address that its elements may have
+// vectors at any address that their elements may have (rows may start anywhere)
 typedef u4_t u4_any_t __attribute__((aligned(2)));
+typedef h8_t h8_any_t __attribute__((aligned(2)));
+typedef b8_t b8_any_t __attribute__((aligned(2)));
+typedef f4_t f4_any_t __attribute__((aligned(4)));
 typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+
+// Eight results of a row to out (as w4a16_dtype, not e4m3), of which the row still has `some`
+__device__ __forceinline__ void fp8_store8(void* out, size_t at, const float (&v)[8], int some, int dtype) {
+  if (some < 8) {
+    for (int j = 0; j < 8; ++j)
+      if (j < some) store_out(out, at + j, v[j], dtype);
+  } else if (dtype == 2) {
+    float* const dst = static_cast<float*>(out) + at;
+    *reinterpret_cast<f4_any_t*>(dst) = f4_t{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f4_any_t*>(dst + 4) = f4_t{v[4], v[5], v[6], v[7]};
+  } else if (dtype == 0) {
+    h8_t o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = (_Float16)v[j];
+    *reinterpret_cast<h8_any_t*>(static_cast<_Float16*>(out) + at) = o;
+  } else {
+    b8_t o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
+    *reinterpret_cast<b8_any_t*>(static_cast<__bf16*>(out) + at) = o;
+  }
+}
 
 // Eight consecutive values of a row, by their type (as w4a16_dtype)
 template <int DT>
@@ -176,7 +201,6 @@ struct Eight<2> {
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
   }
   __device__ __forceinline__ void load(const void* row, size_t i) {
-    typedef f4_t f4_any_t __attribute__((aligned(4)));
     const float* p = static_cast<const float*>(row) + i;
     const f4_t a = *reinterpret_cast<const f4_any_t*>(p), b = *reinterpret_cast<const f4_any_t*>(p + 4);
 #pragma unroll

@@ -562,29 +562,7 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
           if (wn == 0 && c == 0) p.out_scales[(size_t)(n0 / 128) * p.scale_rows + m0 + r0 + r] = s;
           continue;
         }
-        if (p.out_dtype == 2) {
-          float* const dst = static_cast<float*>(p.out) + at;
-          if (some >= 8 && N % 4 == 0) {
-            *reinterpret_cast<f4_t*>(dst) = f4_t{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f4_t*>(dst + 4) = f4_t{v[4], v[5], v[6], v[7]};
-          } else {
-            for (int j = 0; j < 8 && j < some; ++j) dst[j] = v[j];
-          }
-        } else if (some >= 8 && N % 8 == 0) {
-          if (p.out_dtype == 0) {
-            h8_t o;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = (_Float16)v[j];
-            *reinterpret_cast<h8_t*>(static_cast<_Float16*>(p.out) + at) = o;
-          } else {
-            b8_t o;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
-            *reinterpret_cast<b8_t*>(static_cast<__bf16*>(p.out) + at) = o;
-          }
-        } else {
-          for (int j = 0; j < 8 && j < some; ++j) store_out(p.out, at + j, v[j], p.out_dtype);
-        }
+        fp8_store8(p.out, at, v, some, p.out_dtype);
       }
       __builtin_amdgcn_wave_barrier();
     }
