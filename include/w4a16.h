@@ -359,7 +359,8 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
  * 2^-10 of its largest product, on normal operands 1.5e-5 of the result, an eighth of what rounding
  * to fp16 costs.
  * Limits, else W4A16_ERR_UNSUPPORTED: a product's depth is a multiple of 16; operands whose
- * offsets 31 bits hold (K < 2^23; rows * K / 32 < 2^31; a SwiGLU weight below 2 GiB a group).
+ * offsets 31 bits hold (K < 2^23; rows * K / 32 < 2^31; a SwiGLU weight below 2 GiB a group);
+ * up to 2^30 columns of a result.
  * Codes, 16-bit x and dy need 16-byte alignment, other arrays that of their elements (outputs of
  * products 16 bytes).
  * ------------------------------------------------------------------------------------------ */

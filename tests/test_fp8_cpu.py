@@ -168,7 +168,7 @@ GEMM_CASES = [
     (dict(xdt=E4M3, xs=0), ARG), (dict(xdt=E4M3, xs=Q + 1), ARG), (dict(glu=1, odt=E4M3, os=0), ARG),
     (dict(glu=1, odt=E4M3, os=Q, N=48), UNSUPPORTED), (dict(ws=0), WORKSPACE), (dict(ws=4 * P + 64), WORKSPACE),
     (dict(nb=1023), WORKSPACE), (dict(glu=1, odt=E4M3, os=Q, nb=1791), WORKSPACE), (dict(K=1 << 23), UNSUPPORTED),
-    (dict(M=1 << 27, K=1 << 16), UNSUPPORTED),
+    (dict(M=1 << 27, K=1 << 16), UNSUPPORTED), (dict(K=16, N=(1 << 30) + 16), UNSUPPORTED),
 ]
 
 
@@ -208,6 +208,7 @@ BACK = dict(dy=P, x=2 * P, M=4, K=64, N=32, act=BF16, codes=3 * P, scales=Q, dx=
     (dict(N=40), UNSUPPORTED), (dict(dy=0), ARG), (dict(dy=P + 8), ARG), (dict(x=0), ARG), (dict(x=2 * P + 2), ARG),
     (dict(codes=0), ARG), (dict(scales=0), ARG), (dict(dx=P), ARG), (dict(dx=4 * P + 4), ARG), (dict(dw=5 * P + 8), ARG),
     (dict(ws=0), WORKSPACE), (dict(nb=255), WORKSPACE), (dict(M=2 ** 31 - 1), UNSUPPORTED),
+    (dict(K=(1 << 30) + 16, N=16), UNSUPPORTED), (dict(M=1 << 22, K=1 << 17, N=16), UNSUPPORTED),
 ])
 def test_gradients_refuse(L, kw, status):
     a = {**BACK, **kw}

@@ -700,6 +700,9 @@ w4a16_status w4a16_quantize_fp8_weight(const void* w, int N, int K, w4a16_dtype 
                                            static_cast<hipStream_t>(stream)));
 }
 
+// (a tile past the last column still has a number of 31 bits)
+constexpr int kMostColumns = 1 << 30;
+
 // The sizes and types of a product; rows: of its output
 static w4a16_status check_fp8(int rows, int K, int N, w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
   if (rows < 0 || K <= 0 || N <= 0) return W4A16_ERR_ARG;
@@ -707,7 +710,7 @@ static w4a16_status check_fp8(int rows, int K, int N, w4a16_dtype x_dtype, int s
   if (is_e4m3(out_dtype) ? !swiglu : out_dtype != W4A16_F32 && !is_act(out_dtype)) return W4A16_ERR_ARG;
   if (is_act(x_dtype) && is_act(out_dtype) && x_dtype != out_dtype) return W4A16_ERR_ARG;
   if (swiglu && N % 2) return W4A16_ERR_ARG;
-  if (K % 16 || (is_e4m3(out_dtype) && N % 32)) return W4A16_ERR_UNSUPPORTED;
+  if (K % 16 || (is_e4m3(out_dtype) && N % 32) || N > kMostColumns) return W4A16_ERR_UNSUPPORTED;
   if (!fp8_quantize_fits(rows, K) || (is_e4m3(out_dtype) && !fp8_quantize_fits(rows, N / 2))) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }
@@ -854,7 +857,7 @@ static Fp8BackwardLayout fp8_backward_layout(int rows, int K, int N, size_t pitc
 
 static w4a16_status check_fp8_backward(int rows, size_t depth, int K, int N) {
   if (rows < 0 || K <= 0 || N <= 0) return W4A16_ERR_ARG;
-  if (K % 16 || N % 16) return W4A16_ERR_UNSUPPORTED;
+  if (K % 16 || N % 16 || K > kMostColumns || N > kMostColumns) return W4A16_ERR_UNSUPPORTED;
   if (depth >= (1u << 23) || !fp8_quantize_fits((int)depth, K) || !fp8_quantize_fits((int)depth, N)) return W4A16_ERR_UNSUPPORTED;
   if ((long long)w4a16::fp8_blocks((int)depth) * (K > N ? K : N) * 4 >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;  // offsets of scales
   if (!w4a16::fp8_fits(rows, K, N, false) || !w4a16::fp8_fits(N, K, (int)depth, false)) return W4A16_ERR_UNSUPPORTED;

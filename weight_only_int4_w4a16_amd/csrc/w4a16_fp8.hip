@@ -167,8 +167,9 @@ Plan choose(int M, int N, int K, bool glu, bool exact, bool w_rows = false) {
   // N: columns that are multiplied (GLU: both halves)
   const int KB = (int)fp8_blocks(K);
   if (forced_kind() >= 0 && !(exact && forced_kind() == WHOLE) && !(w_rows && forced_kind() == STREAM)) return Plan{forced_kind(), 1, 1};
+  if (M <= 2 && !w_rows) return Plan{STREAM, 1, 1};
   const long long cus = device_cu_count();
-  if (M <= 16 && !w_rows) return Plan{M > 2 && fills(ceil_div(N, 128), cus) ? LOW : STREAM, 1, 1};
+  if (M <= 16 && !w_rows) return Plan{fills(ceil_div(N, 128), cus) ? LOW : STREAM, 1, 1};
   const bool sliced = !glu || (N / 2) % 128 == 0;  // sums of both halves as plain columns: their blocks follow each other
   Plan best{MID, 1, 1};
   double least = 1e30;

@@ -209,13 +209,6 @@ struct Eight<2> {
   __device__ __forceinline__ void load_some(const void* row, size_t i, int n) {
     for (int j = 0; j < 8; ++j) v[j] = j < n ? static_cast<const float*>(row)[i + j] : 0.f;
   }
-  __device__ __forceinline__ void drop(int n) {
-#pragma unroll
-    for (int step = 4; step; step >>= 1)
-      if (n & step)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j + step < 8 ? v[(j + step) & 7] : 0.f;
-  }
   __device__ __forceinline__ float value(int j) const { return v[j]; }
   static constexpr int kWords = 8;
   __device__ __forceinline__ uint32_t magnitude(int w) const { return __builtin_bit_cast(uint32_t, v[w]) & 0x7FFFFFFFu; }

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(const void* __
 // each other join their maxima through LDS; block scales: all threads do; row scales: the sixteen lanes side by side. The
 // transposed codes go through LDS, eight rows of a column (8 bytes) a store: column c's store t lies at slot t ^ (c / 8),
 // so that the sixteen threads side by side use every bank once, and leave as whole 16-byte pieces of a column.
-// 14336x4096 in fp32 both ways 70 to 74 us (4.8 to 5.0 TB/s, a copy's rate); columns of 4096x14336 in bf16 40 us (4.4 TB/s),
+// 14336x4096 in fp32 both ways 70 us (5.0 TB/s, a copy's rate); columns of 4096x14336 in bf16 40 us (4.4 TB/s),
 // with the rows 65; of 4099x2885 14 us (2.6 TB/s): all workgroups run at once, so that reads and writes do not overlap.
 constexpr int kTileThreads = 256;
 
@@ -102,21 +102,23 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
     if (row < end && some >= 8) v[r].load(p.x, (size_t)row * p.K + c);
     else v[r].clear();
   }
-  if (some > 0 && some < 8) {
+  if (FORM != COLUMNS_AND_ROWS && some > 0 && some < 8) {  // (there K is a multiple of 16)
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int row = row0 + ty * 8 + r;
       if (row >= end) continue;
-      if (p.K >= 8) {  // the row's last eight, down to the ones asked for
-        v[r].load(p.x, (size_t)row * p.K + p.K - 8);
-        v[r].drop(8 - some);
-      } else {
-        v[r].load_some(p.x, (size_t)row * p.K + c, some);
+      if constexpr (DT != 2) {  // (of fp32 it would cost a wave of occupancy: 14336x4096 70.6 -> 75.5 us)
+        if (p.K >= 8) {  // the row's last eight, down to the ones asked for
+          v[r].load(p.x, (size_t)row * p.K + p.K - 8);
+          v[r].drop(8 - some);
+          continue;
+        }
       }
+      v[r].load_some(p.x, (size_t)row * p.K + c, some);
     }
   }
   constexpr int WORDS = E::kWords;
-  if constexpr (FORM == COLUMNS_AND_ROWS) {  // K is a multiple of 16
+  if constexpr (FORM == COLUMNS_AND_ROWS) {
     float mine = 0.f;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
