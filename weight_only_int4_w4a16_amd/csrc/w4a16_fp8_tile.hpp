@@ -349,19 +349,36 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
     }
   };
 
-  auto stage_x = [&](int stage) __attribute__((always_inline)) { return lds8 + stage * T::kStage; };
-  auto read_b = [&](int stage, int mt) __attribute__((always_inline)) {
-    return read_fragment(stage_x(stage), (wm * MT + mt) * 16 + l16, q);
+  // Fragments: chunks q and q + 4 of a row of 128 bytes, which lie at q ^ (row % 8) and its neighbour half a row away. All of
+  // a wave's rows have the same row % 8 and lie at constants from its first ones, so a stage takes five addresses, made anew
+  // when the reads go on to it (hidden from the compiler, which adds the stage to each read otherwise: 188 instead of 162 vector
+  // instructions a block of the 256-row tiles beside the MFMAs; 2048 rows of 8192x28672 426 -> 416 us).
+  const uint32_t lane_x = (uint32_t)(wm * MT * 16 + l16) * 128 + ((q ^ (l16 & 7)) << 4);
+  const uint32_t lane_w = (uint32_t)(BM + nrow(0) + l16) * 128 + ((q ^ (l16 & 7)) << 4);
+  uint32_t x_lo, x_hi, w_lo, w_hi, scale;
+  auto turn_to = [&](int stage) __attribute__((always_inline)) {
+    const uint32_t base = (uint32_t)(group * (int)T::kLdsBytes + stage * T::kStage);
+    x_lo = base + lane_x;
+    w_lo = base + lane_w;
+    x_hi = x_lo ^ 64;
+    w_hi = w_lo ^ 64;
+    scale = base + T::kCodes + (wm * MT * 16 + l16) * 4;
+    asm volatile("" : "+v"(x_lo), "+v"(x_hi), "+v"(w_lo), "+v"(w_hi), "+v"(scale));
   };
-  auto read_a = [&](int stage, int nt) __attribute__((always_inline)) {
-    return read_fragment(stage_x(stage) + BM * 128, nrow(nt) + l16, q);
+  static_assert(T::kStage % 128 == 0 && T::kLdsBytes % 128 == 0, "the half of a row is a bit of the address");
+  auto fragment = [&](uint32_t lo, uint32_t hi, int rows_on) __attribute__((always_inline)) {
+    const i4v_t a = *reinterpret_cast<const i4v_t*>(lds_all + lo + rows_on * 128);
+    const i4v_t b = *reinterpret_cast<const i4v_t*>(lds_all + hi + rows_on * 128);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  auto scales_x = [&](int stage) __attribute__((always_inline)) {
-    return reinterpret_cast<const float*>(stage_x(stage) + T::kCodes);
+  auto read_b = [&](int mt) __attribute__((always_inline)) { return fragment(x_lo, x_hi, mt * 16); };
+  auto read_a = [&](int nt) __attribute__((always_inline)) {
+    return fragment(w_lo, w_hi, GLU ? nt / (NT / 2) * OUT + nt % (NT / 2) * 16 : nt * 16);
   };
+  auto read_sx = [&](int mt) __attribute__((always_inline)) { return *reinterpret_cast<const float*>(lds_all + scale + mt * 64); };
   i8v_t a[NT];
   auto read_sw = [&](int stage) __attribute__((always_inline)) {
-    const float* const wsc = scales_x(stage) + T::kScalesX;
+    const float* const wsc = reinterpret_cast<const float*>(lds8 + stage * T::kStage + T::kCodes) + T::kScalesX;
     if constexpr (WROWS) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) swr[nt] = *reinterpret_cast<const f4_t*>(wsc + nrow(nt) + 4 * q);
@@ -414,10 +431,11 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
         return;
       }
     }
-    i8v_t b = read_b(0, 0);
-    float sx = scales_x(0)[wm * MT * 16 + l16];
+    turn_to(0);
+    i8v_t b = read_b(0);
+    float sx = read_sx(0);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) a[nt] = read_a(0, nt);
+    for (int nt = 0; nt < NT; ++nt) a[nt] = read_a(nt);
     if (!WROWS) read_sw(0);
     Wide aw[EXACT ? NT : 1];
     int stage = 0;
@@ -429,8 +447,9 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
         for (int j = mt * ISSUE; j < (mt + 1) * ISSUE && j < T::kLoads; ++j) copy(j, i + ST - 1, free);
         if (mt == (T::kLoads + ISSUE - 1) / ISSUE) touch(i + T::kTouch);
         if (mt == MT - 1) meet();
-        const i8v_t bn = mt + 1 < MT ? read_b(stage, mt + 1) : read_b(next, 0);
-        const float sxn = mt + 1 < MT ? scales_x(stage)[(wm * MT + mt + 1) * 16 + l16] : scales_x(next)[wm * MT * 16 + l16];
+        if (mt == MT - 1) turn_to(next);
+        const i8v_t bn = read_b((mt + 1) % MT);
+        const float sxn = read_sx((mt + 1) % MT);
         __builtin_amdgcn_sched_barrier(0);  // the reads travel while these rows are multiplied
         const int before = mt == 0 ? MT - 1 : mt - 1;
         f4_t now[NT];
@@ -450,13 +469,13 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             add(nt, before);
-            if (mt == MT - 1) a[nt] = read_a(next, nt);
+            if (mt == MT - 1) a[nt] = read_a(nt);
           }
         } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             now[nt] = mfma_fp8(a[nt], b);
-            if (mt == MT - 1) a[nt] = read_a(next, nt);
+            if (mt == MT - 1) a[nt] = read_a(nt);
             add(nt, before);
           }
         }
