@@ -17,10 +17,10 @@
 // widened in registers (one instruction for two codes) and four v_mfma_f32_16x16x32_f16 sum a block in full
 // fp32 (1e-8 of the result on the same operands), at half the rate: 1.7 PFLOP/s with the fmas.
 //
-// Rates reached: 2048 rows of 8192x28672 in bf16 440 to 455 us, 2.1 PFLOP/s, in fp32 805 to 840, 1.2 PFLOP/s. With codes of
-// all zeros the same launches take 325 and 715 us: the chip lowers its clock under full load, so that past this point a
-// product's time is its energy. Eight fewer cycles in a hundred (the widened product by v_mfma_f32_32x32x16_f16) or half
-// the operand reads (v_mfma_f32_32x32x64_f8f6f4) changed the first figures by 0 to 3 %, up or down.
+// Rates reached: 2048 rows of 8192x28672 in bf16 416 to 430 us, 2.3 PFLOP/s, in fp32 800, 1.2 PFLOP/s. With codes of all
+// zeros the first takes 324 us: the chip lowers its clock under full load, so that past this point a product's time is its
+// energy, and fewer waits do not shorten it (the widened product by v_mfma_f32_32x32x16_f16: 14 % fewer cycles, 1 % less
+// time; v_mfma_f32_32x32x64_f8f6f4, with half the operand reads: 6 % more). The blocks' scales are 50 us of the first.
 //
 // Tiles. Both operands go from memory straight to LDS (buffer_load_dwordx4 ... lds), one or two blocks of k ahead of the
 // MFMAs, rows of 128 bytes whose 16-byte chunk c lies at position c ^ (row % 8), so that the fragment reads
