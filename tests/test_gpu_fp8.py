@@ -214,7 +214,7 @@ def test_quantizers_at_odd_addresses():
 
 PRODUCTS = [
     # M, K, N: one token to many, depths and widths that divide nothing
-    (1, 16, 1), (1, 4096, 512), (1, 14352, 96), (1, 33024, 48), (2, 144, 33), (2, 4112, 300), (2, 16400, 40), (3, 1040, 100), (7, 2048, 640), (15, 528, 1000), (16, 256, 256), (17, 4112, 130),
+    (1, 16, 1), (1, 4096, 512), (1, 14352, 96), (1, 33024, 48), (2, 144, 33), (2, 4112, 300), (2, 16400, 40), (3, 1040, 100), (5, 144, 28800), (16, 256, 32768), (7, 2048, 640), (15, 528, 1000), (16, 256, 256), (17, 4112, 130),
     (18, 1040, 4608), (20, 144, 100), (32, 8208, 48), (31, 128, 2048), (33, 384, 129), (48, 640, 777), (63, 896, 128), (64, 1024, 384), (65, 512, 257), (100, 272, 1024),
     (127, 1152, 255), (128, 2176, 512), (129, 160, 640), (200, 1280, 1001), (48, 1680, 300), (64, 8208, 200), (90, 3600, 400), (333, 2896, 700), (256, 640, 2048), (257, 400, 512), (333, 656, 501),
 ]
@@ -246,7 +246,7 @@ def test_products(M, K, N, kind):
         assert torch.equal(out[1:-1], y) and bool((out[0] == 7).all()) and bool((out[-1] == 7).all())
 
 
-@pytest.mark.parametrize("M,K,N2", [(1, 256, 2), (1, 2048, 512), (2, 4112, 160), (5, 144, 100), (16, 640, 704), (17, 528, 98), (32, 4112, 288), (33, 1040, 258), (48, 1680, 1056), (64, 8208, 512), (100, 4112, 1024), (64, 512, 96),
+@pytest.mark.parametrize("M,K,N2", [(1, 256, 2), (1, 2048, 512), (2, 4112, 160), (5, 144, 100), (9, 272, 28672), (16, 640, 704), (17, 528, 98), (32, 4112, 288), (33, 1040, 258), (48, 1680, 1056), (64, 8208, 512), (100, 4112, 1024), (64, 512, 96),
                                     (70, 272, 640), (130, 384, 1000), (257, 256, 1024), (300, 528, 288)])
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 def test_swiglu(M, K, N2, kind):
@@ -620,6 +620,55 @@ def test_a_product_of_more_than_2_to_the_32_results():
     ref = F.gemm_fp8_ref(v, wv)
     _within(y[-300:].cpu().double().numpy(), ref, _stored(ref, _sum_bound(v, wv, "bf16"), "bf16"), "last rows")
     assert not bool(y[:1000].any())
+
+
+@pytest.mark.parametrize("M", [1, 9, 16, 25, 40, 64])
+def test_weights_read_past_the_caches(M):
+    """Weights of 128 MiB and more, plain, SwiGLU and routed: some columns of each."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    K, N = 4096, 33000
+    g = torch.Generator(device="cuda").manual_seed(M)
+    codes = torch.randint(0, 0x48, (N, K), dtype=torch.uint8, device="cuda", generator=g)
+    codes[::3] += 128  # and negative ones
+    scales = torch.rand(-(-N // 128), K // 128, device="cuda", generator=g) / 64 + 2.0 ** -7
+    x, xv = _rows((M, K), "bf16", M)
+    v = F.rows_value(*F.quantize_rows(xv))
+    w8 = codes.view(torch.float8_e4m3fn)
+
+    def rows_of(s, half, n):  # values of n rows of the weight from row 128 b of a half on
+        at, b = half * (N // 2) if half is not None else 0, n[0] // 128
+        c = codes[at + 128 * b:at + 128 * b + len(n)].cpu().numpy()
+        return F.weight_value(c, s[b:b + 1].cpu().numpy())
+
+    for dtype in ("bf16", "f32"):
+        y = w4.gemm_fp8(x, w8, scales, out_dtype=_dtype(dtype))
+        for b in (0, 100, N // 128):
+            n = np.arange(128 * b, min(128 * b + 128, N))
+            wv = rows_of(scales, None, n)
+            ref = F.gemm_fp8_ref(v, wv)
+            _within(y[:, n[0]:n[-1] + 1].cpu().double().numpy(), ref, _stored(ref, _sum_bound(v, wv, dtype), dtype), f"{dtype}, block {b}")
+    half = -(-N // 256)
+    gs, us = (torch.rand(half, K // 128, device="cuda", generator=g) / 4096 + 2.0 ** -13 for _ in range(2))
+    h = w4.gemm_fp8_swiglu(x, w8, torch.cat([gs, us]))
+    for b in (0, 60, half - 1):
+        n = np.arange(128 * b, min(128 * b + 128, N // 2))
+        wv = np.concatenate([rows_of(gs, 0, n), rows_of(us, 1, n)])
+        ref, bound = _glu_bound(v, wv, "bf16")
+        _within(h[:, n[0]:n[-1] + 1].cpu().double().numpy(), ref, _stored(ref, bound, "bf16"), f"h, block {b}")
+    if M < 16:
+        return
+    E = 3  # 11000 rows each
+    r = w4.route(torch.arange(M, device="cuda", dtype=torch.int32).reshape(-1, 1) % E, E)
+    es = torch.rand(E, -(-11000 // 128), K // 128, device="cuda", generator=g) / 64 + 2.0 ** -7
+    y = w4.gemm_fp8_grouped(x, r, w8.view(E, 11000, K), es, gather=True)
+    first = 0
+    for e in range(E):
+        mine = v[e::E]
+        wv = F.weight_value(codes[11000 * e + 128:11000 * e + 256].cpu().numpy(), es[e, 1:2].cpu().numpy())
+        ref = F.gemm_fp8_ref(mine, wv)
+        _within(y[first:first + len(mine), 128:256].cpu().double().numpy(), ref, _stored(ref, _sum_bound(mine, wv, "bf16"), "bf16"), f"group {e}")
+        first += len(mine)
 
 
 def test_experts_of_more_than_2_to_the_32_codes():
