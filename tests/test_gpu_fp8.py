@@ -196,6 +196,33 @@ def test_values_of_all_sizes(kind):
         _same_codes(_bits(codes), want[i:i + 1], "block")
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_every_quotient_of_16_bits(kind):
+    """Every significand under every largest value of a group, at every exponent that has a code: the codes of 16-bit values
+    (one step of the division) are those of the same values in 32 bits (two), and some rows' the oracle's."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    n = 1024 if kind == "f16" else 128
+    m = (1 + torch.arange(n, dtype=torch.float64, device="cuda") / n)
+    values = torch.cat([m * 2.0 ** (10 - e) for e in range(21)])
+    values = torch.cat([values, torch.zeros(-len(values) % 127, dtype=torch.float64, device="cuda")]).reshape(-1, 127)
+    values[:, 1::2] *= -1
+    for top in range(0, n, 128):
+        largest = (m[top:top + 128] * 2.0 ** 10).reshape(-1, 1, 1).expand(-1, len(values), 1)
+        v = values.expand(len(largest), -1, -1)
+        v = torch.where(v.abs() > largest, 0.0, v)
+        x = torch.cat([largest, v], dim=2).reshape(len(largest), -1).to(_dtype(kind))
+        codes, scales = w4.quantize_fp8(x)
+        codes32, scales32 = w4.quantize_fp8(x.float())
+        assert torch.equal(scales, scales32)
+        assert torch.equal(codes.view(torch.uint8), codes32.view(torch.uint8)), f"largest from {top}"
+        codes, _ = w4.quantize_fp8_columns(x.t().contiguous())
+        assert torch.equal(codes.view(torch.uint8), codes32.view(torch.uint8)), f"columns, largest from {top}"
+        some = [0, 5, 77]
+        want, wants = F.quantize_rows(x[some].float().cpu().numpy())
+        assert np.array_equal(_bits(codes[some]), want) and np.array_equal(scales[:, some].cpu().numpy(), wants)
+
+
 def test_quantizers_at_odd_addresses():
     import weight_only_int4_w4a16_amd as w4
     torch = torch_mod()

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void fp8_finish_kernel(const float* __restrict
     const float sc = fp8_scale(max_of_16_lanes(most));
     const Fp8Divisor d = fp8_divisor(sc);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = fp8_quotient(v[j], d);
+    for (int j = 0; j < 8; ++j) v[j] = fp8_quotient<2>(v[j], d);
     if (some > 0) {  // N is a multiple of 16
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + at) = uint2{fp8_pack(v[0], v[1], v[2], v[3]), fp8_pack(v[4], v[5], v[6], v[7])};
       if ((lane & 15) == 0) out_scales[(size_t)(n >> 7) * M + m] = sc;

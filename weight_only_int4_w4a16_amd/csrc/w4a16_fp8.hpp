@@ -81,6 +81,14 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax) {
 // Division by a scale, correctly rounded: with r = RN(1 / s), two steps of q += r (v - q s) after q = v r
 // give RN(v / s) (the remainders are exact). Scales under 2^-60 are taken 2^64 times as large, and so are
 // their values, so that no remainder reaches the subnormal numbers where the quotient's code is not 0.
+//
+// For v of 16 bits (DT 0, 1) one step gives the same codes. After it q = RN(v / s (1 + e)), |e| <= 2^-46, so that a code could
+// differ only where v / s lies within 2^-46 of b +- half an ulp, b one of the 5-bit numbers midway between two codes. Let
+// v = A 2^i and s = RN(B 2^j / 448), A and B integers under 2^11. Then 7 A 2^m and b B are integers (b's taken) under 2^17
+// within 2^-23 of each other, so they are equal, and s is off by exactly that half ulp: with s's 24 bits S,
+// 7 S - B 2^k = r, 0 < |r| <= 3, and |r| b 2^20 (or 21) = B 2^k, both being multiples of 2^12 under 2^27 that near. If 7 divides b it
+// divides B, and r is 0; if not, 7 A 2^m = b B = |r| b^2 2^n has no solution. A zero group's scale divides zeros, and no
+// other fp16 group has a scale under 2^-60.
 struct Fp8Divisor {
   float s, r, up;
 };
@@ -91,11 +99,12 @@ __device__ __forceinline__ Fp8Divisor fp8_divisor(float scale) {
   d.r = 1.0f / d.s;
   return d;
 }
+template <int DT>
 __device__ __forceinline__ float fp8_quotient(float v, const Fp8Divisor& d) {
-  v *= d.up;
+  if constexpr (DT != 0) v *= d.up;
   float q = v * d.r;
   q = __builtin_fmaf(__builtin_fmaf(-q, d.s, v), d.r, q);
-  q = __builtin_fmaf(__builtin_fmaf(-q, d.s, v), d.r, q);
+  if constexpr (DT == 2) q = __builtin_fmaf(__builtin_fmaf(-q, d.s, v), d.r, q);
   return __builtin_copysignf(q, v);  // the steps make +0 of -0
 }
 

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(const void* __
     const Fp8Divisor d = fp8_divisor(s);
     float q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = fp8_quotient(v[r].value(j), d);
+    for (int j = 0; j < 8; ++j) q[j] = fp8_quotient<DT>(v[r].value(j), d);
     if (in_k && m0 + r < M)
       *reinterpret_cast<u2_t*>(codes + (size_t)(m0 + r) * K + k) =
           u2_t{fp8_pack(q[0], q[1], q[2], q[3]), fp8_pack(q[4], q[5], q[6], q[7])};
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
       const Fp8Divisor d = fp8_divisor(s);
       float q[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = fp8_quotient(v[r].value(j), d);
+      for (int j = 0; j < 8; ++j) q[j] = fp8_quotient<DT>(v[r].value(j), d);
       const int row = row0 + ty * 8 + r;
       if (row < end && some > 0)
         *reinterpret_cast<u2_t*>(p.codes + (size_t)row * p.K + c) = u2_t{fp8_pack(q[0], q[1], q[2], q[3]), fp8_pack(q[4], q[5], q[6], q[7])};
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
     for (int r = 0; r < 8; ++r) {  // a row's eight codes
       float q[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = fp8_quotient(v[r].value(j), d[0]);
+      for (int j = 0; j < 8; ++j) q[j] = fp8_quotient<DT>(v[r].value(j), d[0]);
       const int row = row0 + ty * 8 + r;
       lo[r] = fp8_pack(q[0], q[1], q[2], q[3]);
       hi[r] = fp8_pack(q[4], q[5], q[6], q[7]);
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
     for (int j = 0; j < 8; ++j) {
       float q[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) q[r] = fp8_quotient(v[r].value(j), d[j]);
+      for (int r = 0; r < 8; ++r) q[r] = fp8_quotient<DT>(v[r].value(j), d[j]);
       lo[j] = fp8_pack(q[0], q[1], q[2], q[3]);
       hi[j] = fp8_pack(q[4], q[5], q[6], q[7]);
     }

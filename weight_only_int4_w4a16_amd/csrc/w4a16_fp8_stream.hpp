@@ -137,7 +137,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(StreamParams p) {
     const Fp8Divisor d = fp8_divisor(s);
     float c[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = fp8_quotient(e.value(j), d);
+    for (int j = 0; j < 8; ++j) c[j] = fp8_quotient<decltype(dtype)::value>(e.value(j), d);
     if (g < groups) {
       *reinterpret_cast<uint2*>(codes + g * 128 + l16 * 8) = uint2{fp8_pack(c[0], c[1], c[2], c[3]), fp8_pack(c[4], c[5], c[6], c[7])};
       if (l16 == 0) code_scales[g] = s;

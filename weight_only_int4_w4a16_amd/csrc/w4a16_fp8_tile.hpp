@@ -570,7 +570,7 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
           const float s = fp8_scale(b);
           const Fp8Divisor d = fp8_divisor(s);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = fp8_quotient(v[j], d);
+          for (int j = 0; j < 8; ++j) v[j] = fp8_quotient<2>(v[j], d);
           const uint32_t lo = fp8_pack(v[0], v[1], v[2], v[3]), hi = fp8_pack(v[4], v[5], v[6], v[7]);
           uint8_t* const dst = static_cast<uint8_t*>(p.out) + at;
           if (some >= 8 && N % 8 == 0) {
