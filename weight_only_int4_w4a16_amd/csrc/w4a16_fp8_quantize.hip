@@ -59,7 +59,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(const void* __
 // transposed codes go through LDS, eight rows of a column (8 bytes) a store: column c's store t lies at slot t ^ (c / 8),
 // so that the sixteen threads side by side use every bank once, and leave as whole 16-byte pieces of a column.
 // 14336x4096 in fp32 both ways 70 us (5.0 TB/s, a copy's rate); columns of 4096x14336 in bf16 40 us (4.4 TB/s),
-// with the rows 65; of 4099x2885 14 us (2.6 TB/s): all workgroups run at once, so that reads and writes do not overlap.
+// with the rows 59 (4.0); of 4099x2885 13 us (2.7 TB/s): all workgroups run at once, so that reads and writes do not overlap.
 constexpr int kTileThreads = 256;
 
 struct Fp8TileParams {
