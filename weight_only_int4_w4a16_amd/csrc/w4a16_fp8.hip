@@ -425,7 +425,9 @@ hipError_t launch_fp8_by_group(const Fp8Args& a, const RouteLayout& r, const int
   const long long tall = (long long)ceil_div(a.M, kRows[HALF]) * ceil_div(a.N, kCols[HALF]) * r.E;
   const int kind = tall >= device_cu_count() ? HALF : MID;
   set_tiles(p, kind, false, ceil_div(a.M, kRows[kind]));
-  return launch_by_group(p, kind, true, (unsigned)((size_t)p.tiles_m * p.tiles_n), r.E, a.stream);
+  const long long tiles = (long long)p.tiles_m * p.tiles_n;  // (a group's; of all groups fewer than 2^31, as dw would not fit otherwise)
+  const bool looping = kind == HALF;
+  return launch_by_group(p, kind, true, looping ? workgroups(kind, tiles * r.E) : (unsigned)tiles, looping ? 1 : r.E, a.stream);
 }
 
 }  // namespace w4a16

@@ -228,11 +228,13 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
   int turn = blockIdx.x;
   const int live = MODE == GROUPED ? min(p.groups.plan[p.groups.list], p.tiles_m) : p.tiles_m;
   const int tiles = live * p.tiles_n;
-  const int turns = MODE != DENSE ? tiles : p.first > 0 ? 2 * (tiles - p.first) : p.count;
+  const int turns = MODE == BY_GROUP && LOOP ? tiles * p.groups.E : MODE != DENSE ? tiles : p.first > 0 ? 2 * (tiles - p.first) : p.count;
   auto next_tile = [&]() __attribute__((always_inline)) -> bool {
     if (turn >= turns) return false;
     do {
-      int t = tile_of(turn, turns), e = 0, half = 0;
+      // (by group: each group's tiles go over all XCDs, as groups differ in their rows)
+      int e = MODE == BY_GROUP ? LOOP ? turn / tiles : blockIdx.y : 0, half = 0;
+      int t = MODE == BY_GROUP ? tile_of(LOOP ? turn - e * tiles : turn, tiles) : tile_of(turn, turns);
       turn += gridDim.x;
       if constexpr (MODE == DENSE) {
         if (p.first > 0) {  // what whole rounds of tiles twice as high have left: the halves of their tiles from the first one on
@@ -240,8 +242,6 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
           t = p.first + (t >> 1);
         }
       }
-      // (a group's tiles go over all XCDs: groups differ in their rows)
-      if constexpr (MODE == BY_GROUP) e = blockIdx.y;
       const int tm = MODE == DENSE && p.first > 0 ? 2 * (t % live) + half : t % live, tn = t / live;  // neighbours share the weight's rows
       const uint8_t* w = p.w;
       const float* ws = p.ws;
@@ -640,7 +640,7 @@ typedef Tile<4, 2, 4, 8, 2, 3, 3> Whole;  // 256, 256: dense rows, results of 16
 
 template <class T, bool GLU, bool WROWS, int MODE, bool EXACT>
 hipError_t launch_tile(const TileParams& p, unsigned grid, int gy, hipStream_t s) {
-  constexpr bool LOOP = std::is_same<T, Half>::value && MODE != BY_GROUP;
+  constexpr bool LOOP = std::is_same<T, Half>::value;
   const dim3 blocks(grid, gy), threads(T::kThreads), twice(2 * T::kThreads);
   if constexpr (T::kBM <= 64 && !WROWS) {
     if (p.once) {
