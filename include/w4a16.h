@@ -354,10 +354,9 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
  * Products: the codes' products of a block of 128 k are summed on the matrix cores, the block's sum
  * is multiplied by its two scales and added to the result in fp32, which is rounded once. Results
  * are deterministic. A block's sum is an fp32 one for fp32 results, for h that leaves as codes and in
- * the kernels of 16 and 32 rows (w4a16_fp8_kernel_name). For other 16-bit results it comes from the
- * 8-bit MFMA, which drops product bits about 17 below the block's largest: the sum is off by at most
- * 2^-10 of its largest product, on normal operands 1.5e-5 of the result, an eighth of what rounding
- * to fp16 costs.
+ * the kernels w4a16_fp8_16 and w4a16_fp8_32. For other 16-bit results it comes from the 8-bit MFMA,
+ * which drops product bits about 17 below the block's largest: the sum is off by at most 2^-10 of its
+ * largest product, on normal operands 1.5e-5 of the result, an eighth of what rounding to fp16 costs.
  * Limits, else W4A16_ERR_UNSUPPORTED: a product's depth is a multiple of 16; operands whose
  * offsets 31 bits hold (K < 2^23; rows * K / 32 < 2^31; a SwiGLU weight below 2 GiB a group);
  * up to 2^30 columns of a result.
@@ -411,7 +410,7 @@ w4a16_status w4a16_gemm_fp8(const void* x, w4a16_dtype x_dtype, const float* x_s
                             w4a16_dtype out_dtype, float* out_scales, void* workspace,
                             size_t workspace_bytes, void* stream);
 
-/* Name of the kernel w4a16_gemm_fp8 launches for the product ("none" for bad shapes). */
+/* Name of the kernel w4a16_gemm_fp8 launches for the product's 16-bit result ("none" for bad shapes). */
 const char* w4a16_fp8_kernel_name(int M, int K, int N, int swiglu);
 
 /* w4a16_gemm_fp8 of a plan's sorted rows with their groups' weights (codes [groups][N][K], scales

@@ -1074,8 +1074,10 @@ def gemm_fp8(x, codes, scales, x_scales=None, out_dtype=None, out=None, workspac
     (:func:`quantize_fp8_weight`).
 
     ``x[M, K]`` fp16 or bf16, quantized as by :func:`quantize_fp8` within the call, or codes with ``x_scales`` (made once
-    for the products that share them). Sums are fp32, each block of 128 scaled as it is added; the result is rounded
-    once to ``out_dtype``: x's dtype or float32 (for codes: bfloat16 unless given). K is a multiple of 16.
+    for the products that share them). Each block of 128 is scaled as it is added, in fp32; for 16-bit results of more
+    than a few rows its own sum is the 8-bit MFMA's, off by up to 2^-10 of its largest product (1.5e-5 of the result on
+    normal operands). The result is rounded once to ``out_dtype``: x's dtype or float32 (for codes: bfloat16 unless
+    given). K is a multiple of 16.
     ``workspace``: optional, ``fp8_workspace_bytes(...)``. The result has no autograd history."""
     return _gemm_fp8(x, codes, scales, x_scales, 0, False, out_dtype, out, workspace)
 
