@@ -1,0 +1,42 @@
+"""CPU checks of the 8-bit floating point calls as a whole: what sizes a call, makes its operands and launches it has to ask
+the same plan, sizes and types are refused where the launches end, and sizes of scratch are public (nothing is launched)."""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+F16, BF16, F32, E4M3 = 0, 1, 2, 3
+
+SIZES = [(1, 4096, 4096), (2, 256, 64), (1, 33024, 48), (2, 16400, 40)]
+
+PINNED = """
+import json, sys
+from weight_only_int4_w4a16_amd import binding
+L = binding.lib()
+out = []
+for M, K, N in json.loads(sys.argv[1]):
+    for glu in (0, 1):
+        out.append([M, K, N, glu, L.w4a16_fp8_kernel_name(M, K, N, glu).decode()] +
+                   [L.w4a16_fp8_workspace_bytes(M, K, N, 1, glu, o) for o in (1, 2)])
+print(json.dumps(out))
+"""
+
+
+@pytest.mark.parametrize("rows", [16, 32, 64, 128, 256])
+def test_pinned_tiles_have_codes_to_read(rows):
+    """W4A16_FP8_ROWS pins the row tile (read once a process, so each pin has one of its own). A tile reads codes, which a 16-bit
+    x has in the workspace; only the sixteen-row kernel quantizes one or two rows by itself."""
+    env = {**os.environ, "W4A16_FP8_ROWS": str(rows)}
+    run = subprocess.run([sys.executable, "-c", PINNED, json.dumps(SIZES)], cwd=ROOT, env=env, capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0, run.stderr
+    for M, K, N, glu, name, bf16, f32 in json.loads(run.stdout.splitlines()[-1]):
+        tile = {16: "16", 32: "32x128", 64: "64x128", 128: "128x256", 256: "256x256"}[rows]
+        assert name == f"w4a16_fp8_{tile}"
+        codes = M * K + 4 * M * -(-K // 128)
+        if rows > 16:
+            assert bf16 >= codes, (M, K, N, glu)
+        if 16 < rows < 256:  # 32-bit results have no tile of 256 rows: the pin does not hold for them
+            assert f32 >= codes, (M, K, N, glu)

@@ -752,7 +752,7 @@ static w4a16_status fp8_operands(w4a16::Fp8Args& a, const void* x, w4a16_dtype x
   if (is_e4m3(x_dtype)) {
     a.x = static_cast<const uint8_t*>(x);
     a.xs = x_scales;
-  } else if (dense && w4a16::fp8_takes_values(x_rows, a.N, K, a.glu)) {
+  } else if (dense && w4a16::fp8_takes_values(x_rows, a.N, K, a.glu, (int)out_dtype)) {
     a.values = x;
     a.values_dtype = (int)x_dtype;
   } else {
@@ -770,7 +770,7 @@ static w4a16_status fp8_operands(w4a16::Fp8Args& a, const void* x, w4a16_dtype x
 
 size_t w4a16_fp8_workspace_bytes(int M, int K, int N, w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
   if (check_fp8(M, K, N, x_dtype, swiglu, out_dtype) != W4A16_OK || M == 0) return 0;
-  const bool codes = is_e4m3(x_dtype) || w4a16::fp8_takes_values(M, swiglu ? N / 2 : N, K, swiglu != 0);
+  const bool codes = is_e4m3(x_dtype) || w4a16::fp8_takes_values(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype);
   return (codes ? 0 : fp8_rows_bytes(M, K)) +
          w4a16::fp8_scratch_bytes(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype);
 }

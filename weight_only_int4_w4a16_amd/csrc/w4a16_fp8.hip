@@ -192,6 +192,11 @@ Plan choose(int M, int N, int K, bool glu, bool exact, bool w_rows = false) {
   return best;
 }
 
+// The plan of a dense product, by its columns of out: what sizes its scratch, makes its operands and launches it all ask this
+Plan plan_of(int M, int N, int K, bool glu, int out_dtype, bool w_rows = false) {
+  return choose(M, glu ? 2 * N : N, K, glu, out_dtype >= 2, w_rows);
+}
+
 TileParams tile_params(const Fp8Args& a) {
   TileParams p{};
   p.x = a.x;
@@ -293,15 +298,15 @@ bool fp8_fits(int M, int N, int K, bool glu) {
 
 // One or two rows of 16 bits: each workgroup quantizes the groups that its waves multiply, which saves a launch and its
 // scratch. More rows' groups would take as long as the weight does to arrive.
-bool fp8_takes_values(int M, int N, int K, bool glu) {
-  if (M > 2 || M < 1 || choose(M, glu ? 2 * N : N, K, glu, true).kind != STREAM) return false;
+bool fp8_takes_values(int M, int N, int K, bool glu, int out_dtype) {
+  if (M > 2 || M < 1 || plan_of(M, N, K, glu, out_dtype).kind != STREAM) return false;
   int NT, W;
   stream_shape(M, N, K, glu, device_cu_count(), NT, W);
   return ceil_div((int)fp8_blocks(K), W) * M <= 64;
 }
 
 size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype, bool w_rows) {
-  const Plan c = choose(M, glu ? 2 * N : N, K, glu, out_dtype >= 2, w_rows);
+  const Plan c = plan_of(M, N, K, glu, out_dtype, w_rows);
   if (c.S > 1) return align256((size_t)c.S * M * (glu ? 2 * (size_t)N : N) * 4);
   return by_finish(c.kind, c.S, out_dtype) ? align256((size_t)M * N * 4) : 0;
 }
@@ -316,7 +321,8 @@ const char* fp8_name(int M, int N, int K, bool glu) {
 
 hipError_t launch_fp8(const Fp8Args& a) {
   const bool exact = a.out_dtype >= 2;
-  const Plan c = choose(a.M, a.glu ? 2 * a.N : a.N, a.K, a.glu, exact, a.w_rows);
+  const Plan c = plan_of(a.M, a.N, a.K, a.glu, a.out_dtype, a.w_rows);
+  if (a.values && c.kind != STREAM) return hipErrorInvalidValue;  // (tiles read codes)
   TileParams p = tile_params(a);
   const bool finish = by_finish(c.kind, c.S, a.out_dtype);
   if (finish) {

@@ -64,7 +64,7 @@ hipError_t launch_fp8_by_group(const Fp8Args& a, const RouteLayout& r, const int
 size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype, bool w_rows = false);
 size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int out_dtype);
 // whether a dense product of 16-bit x quantizes it as it reads it
-bool fp8_takes_values(int M, int N, int K, bool glu);
+bool fp8_takes_values(int M, int N, int K, bool glu, int out_dtype);
 bool fp8_fits(int M, int N, int K, bool glu);  // whether launches can index it
 bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu);
 const char* fp8_name(int M, int N, int K, bool glu);
