@@ -52,3 +52,55 @@ def test_pinned_tiles(rows):
                          capture_output=True, text=True, timeout=100)
     print(run.stdout, flush=True)
     assert run.returncode == 0, run.stderr[-3000:]
+
+
+# ------------------------------------------------------------------ SwiGLU far below zero
+
+@pytest.mark.parametrize("M,K,N2", [(2, 128, 256), (20, 128, 256), (64, 128, 256), (300, 256, 512), (2100, 256, 4096)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_swiglu_of_large_negative_gates(M, K, N2, kind):
+    """Gates down to -88.6, where SiLU(g) is 1e-36 and less and exp(-g) nears fp32's largest, under up values of 2^100: h is an
+    ordinary number and has to be right to the bounds of every other h. One code a row is not zero, so g and u are exact."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    T._announce(f"gemm_fp8_swiglu {M}x{K}x{N2} {kind}, gates from -88.6 to 8")
+    N = N2 // 2
+    x = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    x[:, 0] = 0x38  # 1
+    size = torch.linspace(-8, 88.6, M, device="cuda")
+    xs = torch.ones(K // 128, M, device="cuda")
+    xs[0] = size.abs()
+    x[size < 0, 0] = 0xB8  # -1
+    codes = torch.zeros(N2, K, dtype=torch.uint8, device="cuda")
+    codes[:N, 0], codes[N:, 0] = 0xB8, 0x38
+    scales = torch.ones(2 * -(-N // 128), K // 128, device="cuda")
+    scales[len(scales) // 2:] = 2.0 ** 100
+    h = w4.gemm_fp8_swiglu(x.view(torch.float8_e4m3fn), codes.view(torch.float8_e4m3fn), scales, x_scales=xs, out_dtype=T._dtype(kind))
+    v = size.cpu().double().numpy()
+    g, u = -v, v * 2.0 ** 100
+    want = g / (1 + np.exp(-g)) * u
+    bound = (np.abs(g) + 8) * 2.0 ** -22 * np.abs(want)
+    T._within(h.cpu().double().numpy(), want[:, None] + np.zeros(N), T._stored(want, bound, kind)[:, None], "h")
+
+
+@pytest.mark.parametrize("tokens", [40, 600])
+def test_grouped_swiglu_of_large_negative_gates(tokens):
+    """The same of routed rows."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    K, N2, E = 128, 256, 2
+    T._announce(f"gemm_fp8_grouped_swiglu {tokens} rows, gates from -88.6 to -1")
+    r = w4.route(torch.zeros(tokens, 1, dtype=torch.int32, device="cuda"), E)
+    x = torch.zeros(tokens, K, dtype=torch.uint8, device="cuda")
+    x[:, 0] = 0x38
+    size = torch.linspace(1, 88.6, tokens, device="cuda")
+    codes = torch.zeros(E, N2, K, dtype=torch.uint8, device="cuda")
+    codes[:, :N2 // 2, 0], codes[:, N2 // 2:, 0] = 0xB8, 0x38
+    scales = torch.ones(E, 2, 1, device="cuda")
+    scales[:, 1] = 2.0 ** 100
+    h = w4.gemm_fp8_grouped_swiglu(x.view(torch.float8_e4m3fn), r, codes.view(torch.float8_e4m3fn), scales, x_scales=size[None],
+                                   gather=True, out_dtype=torch.float32)
+    v = size.cpu().double().numpy()
+    want = -v / (1 + np.exp(v)) * v * 2.0 ** 100
+    bound = (v + 8) * 2.0 ** -22 * np.abs(want)
+    T._within(h.cpu().double().numpy(), want[:, None] + np.zeros(N2 // 2), T._stored(want, bound, "f32")[:, None], "h")

@@ -514,7 +514,7 @@ __global__ __launch_bounds__(T::kThreads* KG) void fp8_tile_kernel(TileParams p)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float g = acc[nt][mt][i], u = acc[nt + NT / 2][mt][i];
-            acc[nt][mt][i] = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;  // the reciprocal to 1 ulp
+            acc[nt][mt][i] = g / (1.0f + __expf(-g)) * u;  // (a reciprocal would be 0 where 1 + exp(-g) passes 2^126)
           }
       if (OUT == 128 && p.out_dtype == kE4M3) {
         // the largest |h| of a row over the tile's 128 columns: this wave's, then all waves' of the row
