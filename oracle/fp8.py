@@ -83,7 +83,7 @@ def quantize_rows(x: np.ndarray):
 
 
 def quantize_columns(x: np.ndarray):
-    """``(codes[K, M'], scales[ceil(M/128), K])``, M' the next multiple of 16 (its codes 0, or NaN in a NaN group)."""
+    """``(codes[K, M'], scales[ceil(M/128), K])``, M' the next multiple of 16, zero codes behind the last row."""
     codes, scales = quantize_rows(np.asarray(x, dtype=np.float32).T)
     pad = -codes.shape[1] % 16
     return np.concatenate([codes, np.zeros((codes.shape[0], pad), dtype=np.uint8)], axis=1), scales

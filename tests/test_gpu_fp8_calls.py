@@ -104,3 +104,21 @@ def test_grouped_swiglu_of_large_negative_gates(tokens):
     want = -v / (1 + np.exp(v)) * v * 2.0 ** 100
     bound = (v + 8) * 2.0 ** -22 * np.abs(want)
     T._within(h.cpu().double().numpy(), want[:, None] + np.zeros(N2 // 2), T._stored(want, bound, "f32")[:, None], "h")
+
+
+# ------------------------------------------------------------------ columns past the last row
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(1, 5), (130, 40), (249, 300)])
+def test_codes_past_the_last_row_are_zeros(M, K, kind):
+    """Also of a column that holds an infinity or a NaN, whose own codes are NaN."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    T._announce(f"columns {M}x{K} {kind}")
+    x, _ = T._rows((M, K), kind, M)
+    x[-1, 0], x[-1, 2], x[-1, 4] = float("inf"), float("nan"), float("-inf")
+    codes, scales = w4.quantize_fp8_columns(x)
+    want, wants = F.quantize_columns(x.cpu().float().numpy())
+    T._same_codes(T._bits(codes), want, "codes")
+    assert np.array_equal(scales.cpu().numpy(), wants, equal_nan=True)
+    assert not T._bits(codes)[:, M:].any()

@@ -241,8 +241,13 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
     const int piece = threadIdx.x + i * kTileThreads;
     const int col = piece >> 3, part = piece & 7, cx = col >> 3;
     const u4_t q = *reinterpret_cast<const u4_t*>(lds + col * 128 + ((part ^ (cx >> 1)) & 7) * 16);
-    const u4_t o = cx & 1 ? u4_t{q[2], q[3], q[0], q[1]} : q;
+    u4_t o = cx & 1 ? u4_t{q[2], q[3], q[0], q[1]} : q;
     const int at = tm * 128 + part * 16, n = p.limit - at;
+    if (!BLOCKS && end - row0 < 128) {  // behind the last row: zeros, also where the column's scale is NaN
+      const int rows = end - row0 - part * 16;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) o[w] &= rows >= 4 * w + 4 ? ~0u : rows <= 4 * w ? 0u : (1u << 8 * (rows - 4 * w)) - 1u;
+    }
     if (tk * 128 + col >= p.K || n <= 0) continue;
     uint8_t* const dst = p.codes_t + (size_t)(tk * 128 + col) * p.pitch + at;
     if (n >= 16) {
