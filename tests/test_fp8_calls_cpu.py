@@ -40,3 +40,33 @@ def test_pinned_tiles_have_codes_to_read(rows):
             assert bf16 >= codes, (M, K, N, glu)
         if 16 < rows < 256:  # 32-bit results have no tile of 256 rows: the pin does not hold for them
             assert f32 >= codes, (M, K, N, glu)
+
+
+# ------------------------------------------------------------------ where the launches end
+
+@pytest.fixture(scope="module")
+def L():
+    from weight_only_int4_w4a16_amd import binding
+    return binding.lib()
+
+
+OK, ARG, UNSUPPORTED = 0, 1, 2
+P, Q = 1 << 20, (1 << 20) + 4096  # aligned placeholder addresses, never dereferenced
+
+
+@pytest.mark.parametrize("M,K,status", [
+    # a wave takes 512 values of two rows: 2^24 workgroups of 256 threads are one too many
+    ((1 << 27) - 1, 16, UNSUPPORTED), ((1 << 27) - 7, 128, UNSUPPORTED), ((1 << 27) - 7, 512, UNSUPPORTED), ((1 << 27) - 8, 512, ARG),
+    (1 << 26, 528, UNSUPPORTED), ((1 << 26) - 8, 1024, ARG), (1, (1 << 31) - 16, ARG), (2 ** 31 - 1, 16, UNSUPPORTED),
+])
+def test_rows_end_where_their_launch_does(L, M, K, status):
+    # (no address: sizes are looked at first)
+    assert L.w4a16_quantize_fp8(None, M, K, BF16, 2 * P, Q, None) == status
+
+
+@pytest.mark.parametrize("M,K,status", [
+    ((1 << 31) - 128, 128, ARG), ((1 << 30) + 1, 256, UNSUPPORTED), (1 << 27, 1024, ARG), (1 << 27, 2048, UNSUPPORTED),
+])
+def test_tiles_end_where_their_launch_does(L, M, K, status):
+    assert L.w4a16_quantize_fp8_columns(None, M, K, BF16, 2 * P, Q, None) == status
+    assert L.w4a16_quantize_fp8_weight(None, M, K, BF16, 2 * P, Q, None, None, None) == status

@@ -122,3 +122,23 @@ def test_codes_past_the_last_row_are_zeros(M, K, kind):
     T._same_codes(T._bits(codes), want, "codes")
     assert np.array_equal(scales.cpu().numpy(), wants, equal_nan=True)
     assert not T._bits(codes)[:, M:].any()
+
+
+# ------------------------------------------------------------------ sizes next to the limits
+
+def test_rows_next_to_their_limit():
+    """2^27 - 8 rows, the most that one launch takes."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    M, K = (1 << 27) - 8, 16
+    T._announce(f"rows {M}x{K}")
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    last, lv = T._rows((9, K), "bf16", 3)
+    x[-9:] = last
+    codes, scales = w4.quantize_fp8(x)
+    want, wants = F.quantize_rows(lv)
+    T._same_codes(T._bits(codes[-9:]), want, "codes")
+    assert np.array_equal(scales[:, -9:].cpu().numpy(), wants)
+    assert not bool(codes[:1000].view(torch.uint8).any()) and bool((scales[0, :1000] == 2.0 ** -126).all())
+    with pytest.raises(w4.W4A16Error, match="unsupported"):
+        w4.quantize_fp8(torch.empty(M + 1, K, dtype=torch.bfloat16, device="cuda"))

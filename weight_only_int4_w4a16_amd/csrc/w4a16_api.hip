@@ -663,15 +663,10 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
 static bool is_act(w4a16_dtype d) { return d == W4A16_F16 || d == W4A16_BF16; }
 static bool is_e4m3(w4a16_dtype d) { return (int)d == w4a16::kE4M3; }
 
-// launches hold fewer than 2^32 threads: a tile of 128 x 128 values takes 256, a group of a row 16
-static bool fp8_quantize_fits(int M, int K) {
-  return (long long)w4a16::fp8_blocks(M) * w4a16::fp8_blocks(K) < (1 << 24) && (long long)M * w4a16::fp8_blocks(K) < (1LL << 27);
-}
-
 w4a16_status w4a16_quantize_fp8(const void* x, int M, int K, w4a16_dtype dtype, uint8_t* codes,
                                 float* scales, void* stream) {
   if (M < 0 || K <= 0 || !valid_dtype(dtype)) return W4A16_ERR_ARG;
-  if (K % 16 || !fp8_quantize_fits(M, K)) return W4A16_ERR_UNSUPPORTED;
+  if (K % 16 || !w4a16::fp8_rows_fit(M, K)) return W4A16_ERR_UNSUPPORTED;
   if (M == 0) return W4A16_OK;
   if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return W4A16_ERR_ARG;
   return from_hip(w4a16::launch_fp8_rows(x, M, K, (int)dtype, codes, scales, static_cast<hipStream_t>(stream)));
@@ -680,7 +675,7 @@ w4a16_status w4a16_quantize_fp8(const void* x, int M, int K, w4a16_dtype dtype, 
 w4a16_status w4a16_quantize_fp8_columns(const void* x, int M, int K, w4a16_dtype dtype, uint8_t* codes,
                                         float* scales, void* stream) {
   if (M < 0 || K <= 0 || !valid_dtype(dtype)) return W4A16_ERR_ARG;
-  if (M > 0x7FFFFFF0 || !fp8_quantize_fits(M, K)) return W4A16_ERR_UNSUPPORTED;
+  if (M > 0x7FFFFFF0 || !w4a16::fp8_tiles_fit(M, K)) return W4A16_ERR_UNSUPPORTED;
   if (M == 0) return W4A16_OK;
   if (!x || !codes || !scales || !aligned(x, dtype_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 4))
     return W4A16_ERR_ARG;
@@ -691,7 +686,7 @@ w4a16_status w4a16_quantize_fp8_columns(const void* x, int M, int K, w4a16_dtype
 w4a16_status w4a16_quantize_fp8_weight(const void* w, int N, int K, w4a16_dtype dtype, uint8_t* codes,
                                        float* scales, uint8_t* codes_t, float* scales_t, void* stream) {
   if (N < 0 || K <= 0 || !valid_dtype(dtype) || !codes_t != !scales_t) return W4A16_ERR_ARG;
-  if (!fp8_quantize_fits(N, K)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::fp8_tiles_fit(N, K)) return W4A16_ERR_UNSUPPORTED;
   if (N == 0) return W4A16_OK;
   if (!w || !codes || !scales || !aligned(w, dtype_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 4))
     return W4A16_ERR_ARG;
@@ -703,7 +698,7 @@ w4a16_status w4a16_quantize_fp8_weight(const void* w, int N, int K, w4a16_dtype 
 // (a tile past the last column still has a number of 31 bits)
 constexpr int kMostColumns = 1 << 30;
 
-// The sizes and types of a product; rows: of its output
+// The sizes and types of a product; rows: of x
 static w4a16_status check_fp8(int rows, int K, int N, w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
   if (rows < 0 || K <= 0 || N <= 0) return W4A16_ERR_ARG;
   if (!is_act(x_dtype) && !is_e4m3(x_dtype)) return W4A16_ERR_ARG;
@@ -711,7 +706,8 @@ static w4a16_status check_fp8(int rows, int K, int N, w4a16_dtype x_dtype, int s
   if (is_act(x_dtype) && is_act(out_dtype) && x_dtype != out_dtype) return W4A16_ERR_ARG;
   if (swiglu && N % 2) return W4A16_ERR_ARG;
   if (K % 16 || (is_e4m3(out_dtype) && N % 32) || N > kMostColumns) return W4A16_ERR_UNSUPPORTED;
-  if (!fp8_quantize_fits(rows, K) || (is_e4m3(out_dtype) && !fp8_quantize_fits(rows, N / 2))) return W4A16_ERR_UNSUPPORTED;
+  if ((long long)rows * w4a16::fp8_blocks(K) * 4 >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;  // offsets of scales
+  if (is_act(x_dtype) && !w4a16::fp8_rows_fit(rows, K)) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }
 
@@ -802,7 +798,7 @@ static w4a16_status check_fp8_grouped(int tokens, int topk, int groups, int gath
   const w4a16_status st = check_route(tokens, topk, groups);
   if (st != W4A16_OK) return st;
   if (gather && (long long)tokens * K >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;
-  return check_fp8(tokens * topk, K, N, x_dtype, swiglu, out_dtype);
+  return check_fp8(gather ? tokens : tokens * topk, K, N, x_dtype, swiglu, out_dtype);
 }
 
 size_t w4a16_fp8_grouped_workspace_bytes(int tokens, int topk, int groups, int gather, int K, int N,
@@ -858,7 +854,8 @@ static Fp8BackwardLayout fp8_backward_layout(int rows, int K, int N, size_t pitc
 static w4a16_status check_fp8_backward(int rows, size_t depth, int K, int N) {
   if (rows < 0 || K <= 0 || N <= 0) return W4A16_ERR_ARG;
   if (K % 16 || N % 16 || K > kMostColumns || N > kMostColumns) return W4A16_ERR_UNSUPPORTED;
-  if (depth >= (1u << 23) || !fp8_quantize_fits((int)depth, K) || !fp8_quantize_fits((int)depth, N)) return W4A16_ERR_UNSUPPORTED;
+  if (depth >= (1u << 23) || !w4a16::fp8_tiles_fit((int)depth, K) || !w4a16::fp8_tiles_fit((int)depth, N)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::fp8_rows_fit(rows, N)) return W4A16_ERR_UNSUPPORTED;  // dx alone
   if ((long long)w4a16::fp8_blocks((int)depth) * (K > N ? K : N) * 4 >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;  // offsets of scales
   if (!w4a16::fp8_fits(rows, K, N, false) || !w4a16::fp8_fits(N, K, (int)depth, false)) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;

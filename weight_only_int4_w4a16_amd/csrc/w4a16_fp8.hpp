@@ -50,6 +50,9 @@ hipError_t launch_fp8_rows(const void* x, int M, int K, int dtype, uint8_t* code
 hipError_t launch_fp8_columns(const void* x, int M, int K, int dtype, uint8_t* codes, size_t pitch, float* scales,
                               uint8_t* row_codes, float* row_scales, const RouteLayout* r, const int32_t* plan,
                               hipStream_t s);
+// Launches hold fewer than 2^32 threads: whether these do, for rows, and for columns and blocks of 128 x 128
+bool fp8_rows_fit(int M, int K);
+bool fp8_tiles_fit(int M, int K);
 // blocks of 128 x 128: codes [N][K], scales [ceil(N / 128)][ceil(K / 128)]; codes_t, scales_t the same transposed, or NULL
 hipError_t launch_fp8_weight(const void* w, int N, int K, int dtype, uint8_t* codes, float* scales, uint8_t* codes_t,
                              float* scales_t, hipStream_t s);

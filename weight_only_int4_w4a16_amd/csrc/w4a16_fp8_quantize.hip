@@ -258,16 +258,25 @@ __global__ __launch_bounds__(kTileThreads) void fp8_tile_kernel(Fp8TileParams p)
   }
 }
 
+// Four groups of a row to a wave. Two rows a wave for many: 4096x14336 in bf16 35.7 us with one, 30.9 with two (5.7 TB/s), 33.0
+// with four, 34.3 with eight; 4096x4096 12.7, 12.2, 13.4, 15.3; 4096x2048 7.5, 7.7, 8.6, 10.0; 16x8192 2.6, 3.0, 3.6, 4.8.
+struct RowsShape {
+  size_t chunks, rows, workgroups;  // chunks of a row; rows a wave
+};
+RowsShape rows_shape(int M, int K) {
+  RowsShape r;
+  r.chunks = (fp8_blocks(K) + 3) / 4;
+  r.rows = (size_t)M * r.chunks >= 32768 ? 2 : 1;
+  r.workgroups = r.chunks * (((size_t)M + kRowWaves * r.rows - 1) / (kRowWaves * r.rows));
+  return r;
+}
+
 template <int DT>
 void launch_rows(const void* x, int M, int K, uint8_t* codes, float* scales, hipStream_t s) {
-  const int chunks = (int)((fp8_blocks(K) + 3) / 4);
-  const auto grid = [&](int R) { return dim3((unsigned)((size_t)chunks * ((M + kRowWaves * R - 1) / (kRowWaves * R)))); };
-  // Two rows a wave for many: 4096x14336 in bf16 35.7 us with one, 30.9 with two (5.7 TB/s), 33.0 with four, 34.3 with eight;
-  // 4096x4096 12.7, 12.2, 13.4, 15.3; 4096x2048 7.5, 7.7, 8.6, 10.0; 16x8192 2.6, 3.0, 3.6, 4.8.
-  if ((size_t)M * chunks >= 32768)
-    hipLaunchKernelGGL((fp8_rows_kernel<DT, 2>), grid(2), dim3(64 * kRowWaves), 0, s, x, M, K, codes, scales, chunks);
-  else
-    hipLaunchKernelGGL((fp8_rows_kernel<DT, 1>), grid(1), dim3(64 * kRowWaves), 0, s, x, M, K, codes, scales, chunks);
+  const RowsShape r = rows_shape(M, K);
+  const dim3 grid((unsigned)r.workgroups), threads(64 * kRowWaves);
+  if (r.rows == 2) hipLaunchKernelGGL((fp8_rows_kernel<DT, 2>), grid, threads, 0, s, x, M, K, codes, scales, (int)r.chunks);
+  else hipLaunchKernelGGL((fp8_rows_kernel<DT, 1>), grid, threads, 0, s, x, M, K, codes, scales, (int)r.chunks);
 }
 
 template <int FORM>
@@ -279,6 +288,9 @@ void launch_tiles(const Fp8TileParams& p, int tiles_m, int dtype, hipStream_t s)
 }
 
 }  // namespace
+
+bool fp8_rows_fit(int M, int K) { return rows_shape(M, K).workgroups * 64 * kRowWaves < (1ULL << 32); }
+bool fp8_tiles_fit(int M, int K) { return fp8_blocks(M) * fp8_blocks(K) * kTileThreads < (1ULL << 32); }
 
 hipError_t launch_fp8_rows(const void* x, int M, int K, int dtype, uint8_t* codes, float* scales, hipStream_t s) {
   if (dtype == 0) launch_rows<0>(x, M, K, codes, scales, s);
