@@ -360,8 +360,8 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
  * Limits, else W4A16_ERR_UNSUPPORTED: a product's depth is a multiple of 16; operands whose
  * offsets 31 bits hold (K < 2^23; rows * K / 32 < 2^31; a SwiGLU weight below 2 GiB a group);
  * up to 2^30 columns of a result; launches of fewer than 2^32 threads: rows quantized a wave for two times 512
- * values, rows * ceil(K / 512) < 2^27 - 8; columns and blocks, fewer than 2^24 tiles of 128 x 128;
- * results, rows * ceil(columns / 512) < 2^25.
+ * values, rows * ceil(K / 512) < 2^27 - 8; columns and blocks, fewer than 2^24 tiles of 128 x 128; where a second
+ * kernel adds slices of k or quantizes h, rows * ceil(columns / 512) < 2^25.
  * Codes, 16-bit x and dy need 16-byte alignment, other arrays that of their elements (outputs of
  * products 16 bytes).
  * ------------------------------------------------------------------------------------------ */

@@ -70,3 +70,25 @@ def test_rows_end_where_their_launch_does(L, M, K, status):
 def test_tiles_end_where_their_launch_does(L, M, K, status):
     assert L.w4a16_quantize_fp8_columns(None, M, K, BF16, 2 * P, Q, None) == status
     assert L.w4a16_quantize_fp8_weight(None, M, K, BF16, 2 * P, Q, None, None, None) == status
+
+
+@pytest.mark.parametrize("M,K,N,xdt,glu,odt,status", [
+    # one kernel: its own grid alone counts
+    (1 << 17, 16, 1 << 17, BF16, 0, BF16, ARG), (1 << 17, 16, 1 << 17, BF16, 0, F32, ARG), (1 << 18, 128, 1 << 17, E4M3, 1, BF16, ARG),
+    ((1 << 27) - 8, 128, 64, E4M3, 0, BF16, ARG), ((1 << 29) - 1, 128, 64, E4M3, 0, BF16, ARG),
+    # a second one, of 512 columns a wave, quantizes h from tiles of 64 columns
+    (1 << 26, 16, 64, E4M3, 1, E4M3, UNSUPPORTED),
+    # rows quantized in the call
+    ((1 << 27) - 1, 128, 64, BF16, 0, BF16, UNSUPPORTED), (1 << 29, 128, 64, E4M3, 0, BF16, UNSUPPORTED),
+])
+def test_products_end_where_their_launches_do(L, M, K, N, xdt, glu, odt, status):
+    assert L.w4a16_gemm_fp8(None, xdt, None, M, K, N, 2 * P, Q, glu, 3 * P, odt, None, None, 0, None) == status
+
+
+def test_grouped_products_end_where_their_launches_do(L):
+    def call(tokens, K, N, glu, odt):
+        return L.w4a16_gemm_fp8_grouped(None, E4M3, None, Q, tokens, 1, 3, 0, K, N, 2 * P, Q, glu, 3 * P, odt, None, None, 0, None)
+    # (the plan's placeholder passes, x's missing address does not)
+    assert call(1 << 25, 128, 1024, 0, BF16) == ARG
+    assert call(1 << 26, 128, 1024, 1, E4M3) == ARG  # tiles of 128 columns quantize h themselves
+    assert call(1 << 26, 128, 8192, 0, BF16) == UNSUPPORTED

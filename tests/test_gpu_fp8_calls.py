@@ -126,6 +126,27 @@ def test_codes_past_the_last_row_are_zeros(M, K, kind):
 
 # ------------------------------------------------------------------ sizes next to the limits
 
+def test_a_square_of_2_to_the_34_results():
+    """131072 rows and columns: one kernel, whose grid is far from its limit."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    M = N = 1 << 17
+    K = 16
+    T._announce(f"gemm_fp8 {M}x{K}x{N}")
+    big = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x, xv = T._rows((70, K), "bf16", 1)
+    at = torch.cat([torch.arange(3), torch.arange(M - 67, M)]).cuda()
+    big[at] = x
+    codes, scales, wv = T._weight((), N, K, 2)
+    y = w4.gemm_fp8(big, codes, scales)
+    v = F.rows_value(*F.quantize_rows(xv))
+    some = np.concatenate([np.arange(300), np.arange(N - 300, N)])
+    ref = F.gemm_fp8_ref(v, wv[some])
+    got = y[at][:, torch.from_numpy(some).cuda()].cpu().double().numpy()
+    T._within(got, ref, T._stored(ref, T._sum_bound(v, wv[some], "bf16"), "bf16"), "corners")
+    assert not bool(y[3:1000].any()) and not bool(y[M - 1000:M - 67].any())
+
+
 def test_rows_next_to_their_limit():
     """2^27 - 8 rows, the most that one launch takes."""
     import weight_only_int4_w4a16_amd as w4

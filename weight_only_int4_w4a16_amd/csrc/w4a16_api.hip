@@ -777,7 +777,7 @@ w4a16_status w4a16_gemm_fp8(const void* x, w4a16_dtype x_dtype, const float* x_s
                             size_t workspace_bytes, void* stream) {
   w4a16_status st = check_fp8(M, K, N, x_dtype, swiglu, out_dtype);
   if (st != W4A16_OK) return st;
-  if (!w4a16::fp8_fits(M, swiglu ? N / 2 : N, K, swiglu != 0)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::fp8_fits(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype)) return W4A16_ERR_UNSUPPORTED;
   if (M == 0) return W4A16_OK;
   st = check_fp8_pointers(x, x_dtype, x_scales, codes, scales, out, out_dtype, out_scales, workspace, workspace_bytes,
                           w4a16_fp8_workspace_bytes(M, K, N, x_dtype, swiglu, out_dtype));
@@ -816,7 +816,7 @@ w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const fl
   w4a16_status st = check_fp8_grouped(tokens, topk, groups, gather, K, N, x_dtype, swiglu, out_dtype);
   if (st != W4A16_OK || tokens == 0) return st;
   const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
-  if (!w4a16::fp8_grouped_fits(r, swiglu ? N / 2 : N, K, swiglu != 0)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::fp8_grouped_fits(r, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype)) return W4A16_ERR_UNSUPPORTED;
   if (!plan || !aligned(plan, 256)) return W4A16_ERR_ARG;
   st = check_fp8_pointers(
       x, x_dtype, x_scales, codes, scales, out, out_dtype, out_scales, workspace, workspace_bytes,
@@ -857,7 +857,7 @@ static w4a16_status check_fp8_backward(int rows, size_t depth, int K, int N) {
   if (depth >= (1u << 23) || !w4a16::fp8_tiles_fit((int)depth, K) || !w4a16::fp8_tiles_fit((int)depth, N)) return W4A16_ERR_UNSUPPORTED;
   if (!w4a16::fp8_rows_fit(rows, N)) return W4A16_ERR_UNSUPPORTED;  // dx alone
   if ((long long)w4a16::fp8_blocks((int)depth) * (K > N ? K : N) * 4 >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;  // offsets of scales
-  if (!w4a16::fp8_fits(rows, K, N, false) || !w4a16::fp8_fits(N, K, (int)depth, false)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::fp8_fits(rows, K, N, false, W4A16_F16) || !w4a16::fp8_fits(N, K, (int)depth, false, W4A16_F32, true)) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }
 
@@ -981,7 +981,7 @@ w4a16_status w4a16_gemm_fp8_grouped_backward(const void* dy, const void* x, cons
   const size_t depth = fp8_grouped_depth(r);
   st = check_fp8_backward(r.S, depth, K, N);
   if (st != W4A16_OK) return st;
-  if (!w4a16::fp8_grouped_fits(r, K, N, false)) return W4A16_ERR_UNSUPPORTED;
+  if (!w4a16::fp8_grouped_fits(r, K, N, false, W4A16_F16)) return W4A16_ERR_UNSUPPORTED;
   if (!plan || !aligned(plan, 256)) return W4A16_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (tokens == 0) {  // the plan's offsets are zeros: every group's product has no depth

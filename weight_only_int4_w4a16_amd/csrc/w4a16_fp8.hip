@@ -284,16 +284,21 @@ bool by_finish(int kind, int S, int out_dtype) { return S > 1 || (out_dtype == k
 
 }  // namespace
 
-bool fp8_fits(int M, int N, int K, bool glu) {
+namespace {
+// the grid of the second kernel
+bool finish_fits(int M, int N) { return (long long)M * ceil_div(N, 512) < (1LL << 25); }
+}  // namespace
+
+bool fp8_fits(int M, int N, int K, bool glu, int out_dtype, bool w_rows) {
   // offsets within a tile's operands, and of scales, in 31 bits; fewer than 2^32 threads
   const long long wrows = glu ? 2LL * N : 256;
   if ((long long)K >= (1LL << 23) || wrows * K >= (1LL << 31)) return false;
   if ((long long)fp8_blocks(K) * M * 4 >= (1LL << 31) || (long long)(fp8_blocks(N) + 1) * 2 * fp8_blocks(K) * 4 >= (1LL << 31))
     return false;
-  if ((long long)M * ceil_div(N, 512) >= (1LL << 25)) return false;
-  if ((long long)ceil_div(M, 16) * ceil_div(glu ? 2 * N : N, 16) * 512 * 12 < (1LL << 32)) return true;  // on any tile
-  const Plan c = choose(M, glu ? 2 * N : N, K, glu, true), d = choose(M, glu ? 2 * N : N, K, glu, false);
-  return grid_fits(ceil_div(M, kRows[c.kind]), N, c.kind, glu, c.S) && grid_fits(ceil_div(M, kRows[d.kind]), N, d.kind, glu, d.S);
+  // on any tile
+  if ((long long)ceil_div(M, 16) * ceil_div(glu ? 2 * N : N, 16) * 512 * 12 < (1LL << 32) && finish_fits(M, N)) return true;
+  const Plan c = plan_of(M, N, K, glu, out_dtype, w_rows);
+  return grid_fits(ceil_div(M, kRows[c.kind]), N, c.kind, glu, c.S) && (!by_finish(c.kind, c.S, out_dtype) || finish_fits(M, N));
 }
 
 // One or two rows of 16 bits: each workgroup quantizes the groups that its waves multiply, which saves a launch and its
@@ -390,13 +395,13 @@ GroupTiles group_tiles(const RouteLayout& r, const int32_t* plan, bool gather, i
 
 }  // namespace
 
-bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu) {
+bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu, int out_dtype) {
   const long long wrows = glu ? 2LL * N : 256;
   if ((long long)K >= (1LL << 23) || wrows * K >= (1LL << 31)) return false;
   if ((long long)fp8_blocks(K) * r.S * 4 >= (1LL << 31) || (long long)(fp8_blocks(N) + 1) * 2 * fp8_blocks(K) * 4 >= (1LL << 31))
     return false;
-  if ((long long)r.S * ceil_div(N, 512) >= (1LL << 25)) return false;
   const int kind = choose_grouped(r);
+  if (by_finish(kind, 1, out_dtype) && !finish_fits(r.S, N)) return false;
   return grid_fits(tile_bound(r.S, r.E, kind), N, kind, glu, 1);
 }
 

@@ -68,8 +68,9 @@ size_t fp8_scratch_bytes(int M, int N, int K, bool glu, int out_dtype, bool w_ro
 size_t fp8_grouped_scratch_bytes(const RouteLayout& r, int N, int out_dtype);
 // whether a dense product of 16-bit x quantizes it as it reads it
 bool fp8_takes_values(int M, int N, int K, bool glu, int out_dtype);
-bool fp8_fits(int M, int N, int K, bool glu);  // whether launches can index it
-bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu);
+// whether the product's launches can index it
+bool fp8_fits(int M, int N, int K, bool glu, int out_dtype, bool w_rows = false);
+bool fp8_grouped_fits(const RouteLayout& r, int N, int K, bool glu, int out_dtype);
 const char* fp8_name(int M, int N, int K, bool glu);
 
 // ---- device side ----
