@@ -163,3 +163,71 @@ def test_rows_next_to_their_limit():
     assert not bool(codes[:1000].view(torch.uint8).any()) and bool((scales[0, :1000] == 2.0 ** -126).all())
     with pytest.raises(w4.W4A16Error, match="unsupported"):
         w4.quantize_fp8(torch.empty(M + 1, K, dtype=torch.bfloat16, device="cuda"))
+
+
+# ------------------------------------------------------------------ memory that a call reads and writes
+
+def _refused(fn, match):
+    import weight_only_int4_w4a16_amd as w4
+    with pytest.raises(w4.W4A16Error, match=match) as e:
+        fn()
+    assert e.value.status == 1
+
+
+def _inside(t, shape, dtype):
+    """A tensor over t's first bytes."""
+    torch = torch_mod()
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    return t.view(-1).view(torch.uint8)[:n].view(dtype).view(shape)
+
+
+def test_out_and_workspace_overlap_nothing_that_is_read():
+    """Results are stored while other workgroups still read: sharing memory with any input is refused, and so is a
+    workspace that shares it with an input or the output."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    M, K, N = 24, 512, 256
+    bf16, u8 = torch.bfloat16, torch.uint8
+    x, _ = T._rows((M, K), "bf16", 1)
+    q, s = w4.quantize_fp8(x)
+    codes, scales, _ = T._weight((), N, K, 2)
+    # scales next to a buffer of its own, so that an output can lie over them
+    room = torch.zeros(M * N + 4096, device="cuda")
+    own = room[:scales.numel()].view(scales.shape).copy_(scales)
+    own_s = room[64:64 + s.numel()].view(s.shape).copy_(s)
+    for out in (_inside(codes, (M, N), bf16), _inside(room, (M, N), bf16), _inside(x, (M, N), bf16)):
+        _refused(lambda: w4.gemm_fp8(x, codes, own, out=out), "out overlaps an input")
+    _refused(lambda: w4.gemm_fp8(q, codes, scales, x_scales=own_s, out=_inside(room, (M, N), bf16)), "out overlaps an input")
+    _refused(lambda: w4.gemm_fp8(q, codes, scales, x_scales=s, out=_inside(q, (M, N), bf16)), "out overlaps an input")
+    need = w4.fp8_workspace_bytes(M, K, N, bf16)
+    out = torch.empty(M, N, dtype=bf16, device="cuda")
+    big = torch.zeros(need + M * K * 2, dtype=u8, device="cuda")
+    inside = big[:M * K * 2].view(bf16).view(M, K).copy_(x)
+    over = big[:M * N * 2].view(bf16).view(M, N)
+    _refused(lambda: w4.gemm_fp8(inside, codes, scales, workspace=big), "workspace overlaps")
+    _refused(lambda: w4.gemm_fp8(x, codes, scales, out=over, workspace=big), "workspace overlaps")
+    _refused(lambda: w4.gemm_fp8(x, codes, room[:scales.numel()].view(scales.shape), workspace=room.view(u8)), "workspace overlaps")
+    assert torch.equal(w4.gemm_fp8(x, codes, scales, out=out, workspace=big), w4.gemm_fp8(x, codes, scales))
+
+    E = 2
+    r = w4.route(torch.arange(M, device="cuda", dtype=torch.int32).reshape(-1, 1) % E, E)
+    ecodes, escales, _ = T._weight((E,), N, K, 3)
+    eown = room[:escales.numel()].view(escales.shape).copy_(escales)
+    for out in (_inside(ecodes, (M, N), bf16), _inside(room, (M, N), bf16)):
+        _refused(lambda: w4.gemm_fp8_grouped(x, r, ecodes, eown, out=out), "out overlaps an input")
+    _refused(lambda: w4.gemm_fp8_grouped(inside, r, ecodes, escales, workspace=big), "workspace overlaps")
+    deep, _ = T._rows((4, 16), "bf16", 1)  # an output no larger than the plan
+    small = w4.route(torch.zeros(4, 1, dtype=torch.int32, device="cuda"), 1)
+    c1, s1, _ = T._weight((1,), 16, 16, 4)
+    _refused(lambda: w4.gemm_fp8_grouped(deep, small, c1, s1, out=_inside(small.plan, (4, 16), bf16)), "out overlaps an input")
+
+    codes_t, scales_t, _ = T._weight((), K, N, 5)
+    dy, _ = T._rows((M, N), "bf16", 6)
+    from weight_only_int4_w4a16_amd import binding
+    need = binding.lib().w4a16_fp8_backward_workspace_bytes(M, K, N)
+    big = torch.zeros(need + M * K * 2, dtype=u8, device="cuda")
+    inside = big[:M * K * 2].view(bf16).view(M, K).copy_(x)
+    _refused(lambda: w4.gemm_fp8_backward(dy, inside, codes_t, scales_t, workspace=big), "workspace overlaps")
+    a, b = w4.gemm_fp8_backward(dy, inside, codes_t, scales_t, workspace=big[(M * K * 2 + 255) // 256 * 256:])
+    c, d = w4.gemm_fp8_backward(dy, x, codes_t, scales_t)
+    assert torch.equal(a, c) and torch.equal(b, d)

@@ -570,7 +570,7 @@ def _apart(out, name, others):
     lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
     for t in others:
         if t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
-            _fail(f"{name} overlaps an input")
+            _fail(f"{name} overlaps {'an input' if name == 'out' else 'an input or the output'}")
 
 
 class Routing:
@@ -1013,8 +1013,9 @@ def _fp8_weight(codes, scales, lead, K, glu, device, kind="codes"):
     return N, cp, _need(scales, "scales" if kind == "codes" else "scales_t", (*lead, blocks, _up128(K)), torch.float32, device)
 
 
-def _fp8_out(x, x_dt, rows, width, glu, quantized, out_dtype, out):
-    """The output and its w4a16 dtype, and with ``quantized`` its scales."""
+def _fp8_out(x, x_dt, rows, width, quantized, out_dtype, out, reads):
+    """The output and its w4a16 dtype, and with ``quantized`` its scales. ``reads``: what the call reads (workgroups that
+    store results run beside others that still read scales and codes)."""
     torch = _torch()
     if quantized:
         if out is not None or out_dtype is not None:
@@ -1029,14 +1030,16 @@ def _fp8_out(x, x_dt, rows, width, glu, quantized, out_dtype, out):
     if out is None:
         return x.new_empty((rows, width), dtype=out_dtype), dt, None
     _need(out, "out", (rows, width), out_dtype, x.device)
-    _apart(out, "out", (x,))
+    _apart(out, "out", reads)
     return out, dt, None
 
 
-def _fp8_scratch(x, need, workspace):
-    """A call's workspace: the caller's, or one of torch's for this call. Returns it, its address and bytes."""
+def _fp8_scratch(x, need, workspace, others):
+    """A call's workspace: the caller's, apart from the ``others``, or one of torch's for this call. Returns it, its address
+    and bytes."""
     if workspace is not None:
         _expect_workspace(workspace, need, x.device)
+        _apart(workspace, "workspace", others)
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if not need:
         return None, None, 0
@@ -1061,9 +1064,10 @@ def _gemm_fp8(x, codes, scales, x_scales, glu, quantized, out_dtype, out, worksp
     M, K, x_dt, xsp = _fp8_x(x, x_scales)
     device = x.device
     N, cp, sp = _fp8_weight(codes, scales, (), K, glu, device)
-    out, dt, out_scales = _fp8_out(x, x_dt, M, N // 2 if glu else N, glu, quantized, out_dtype, out)
+    reads = (x, codes, scales) if xsp is None else (x, codes, scales, x_scales)
+    out, dt, out_scales = _fp8_out(x, x_dt, M, N // 2 if glu else N, quantized, out_dtype, out, reads)
     L = lib()
-    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_workspace_bytes(M, K, N, x_dt, glu, dt), workspace)
+    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_workspace_bytes(M, K, N, x_dt, glu, dt), workspace, (*reads, out))
     _fp8_call(L.w4a16_gemm_fp8, "w4a16_gemm_fp8", device, x.data_ptr(), x_dt, xsp, M, K, N, cp, sp, glu, out.data_ptr(), dt,
               None if out_scales is None else out_scales.data_ptr(), wp, nbytes)
     return (out, out_scales) if quantized else out
@@ -1107,10 +1111,11 @@ def _gemm_fp8_grouped(x, routing, codes, scales, x_scales, glu, quantized, gathe
     if x.device != device:
         _fail(f"x is on {x.device}, expected {device}")
     N, cp, sp = _fp8_weight(codes, scales, (r.groups,), K, glu, device)
-    out, dt, out_scales = _fp8_out(x, x_dt, r.rows, N // 2 if glu else N, glu, quantized, out_dtype, out)
+    reads = (x, codes, scales, r.plan) if xsp is None else (x, codes, scales, r.plan, x_scales)
+    out, dt, out_scales = _fp8_out(x, x_dt, r.rows, N // 2 if glu else N, quantized, out_dtype, out, reads)
     L, gather = lib(), int(gather)
     need = L.w4a16_fp8_grouped_workspace_bytes(r.tokens, r.topk, r.groups, gather, K, N, x_dt, glu, dt)
-    ws, wp, nbytes = _fp8_scratch(x, need, workspace)
+    ws, wp, nbytes = _fp8_scratch(x, need, workspace, (*reads, out))
     _fp8_call(L.w4a16_gemm_fp8_grouped, "w4a16_gemm_fp8_grouped", device, x.data_ptr(), x_dt, xsp, r.plan.data_ptr(), r.tokens,
               r.topk, r.groups, gather, K, N, cp, sp, glu, out.data_ptr(), dt,
               None if out_scales is None else out_scales.data_ptr(), wp, nbytes)
@@ -1169,7 +1174,7 @@ def gemm_fp8_backward(dy, x, codes_t, scales_t, workspace=None):
     dx = torch.empty_like(x)
     dw = x.new_empty((N, K), dtype=torch.float32)
     L = lib()
-    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_backward_workspace_bytes(M, K, N), workspace)
+    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_backward_workspace_bytes(M, K, N), workspace, (dy, x, codes_t, scales_t))
     _fp8_call(L.w4a16_gemm_fp8_backward, "w4a16_gemm_fp8_backward", x.device, yp, xp, M, K, N, dt, cp, sp, dx.data_ptr(),
               dw.data_ptr(), wp, nbytes)
     return dx, dw
@@ -1188,7 +1193,7 @@ def gemm_fp8_grouped_backward(dy, x, routing: Routing, codes_t, scales_t, worksp
     dw = x.new_empty((r.groups, N, K), dtype=torch.float32)
     L = lib()
     need = L.w4a16_fp8_grouped_backward_workspace_bytes(r.tokens, r.topk, r.groups, K, N)
-    ws, wp, nbytes = _fp8_scratch(x, need, workspace)
+    ws, wp, nbytes = _fp8_scratch(x, need, workspace, (dy, x, codes_t, scales_t, r.plan))
     _fp8_call(L.w4a16_gemm_fp8_grouped_backward, "w4a16_gemm_fp8_grouped_backward", x.device, yp, xp, r.plan.data_ptr(),
               r.tokens, r.topk, r.groups, K, N, dt, cp, sp, dx.data_ptr(), dw.data_ptr(), wp, nbytes)
     return dx, dw
