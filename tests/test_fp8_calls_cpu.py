@@ -92,3 +92,16 @@ def test_grouped_products_end_where_their_launches_do(L):
     assert call(1 << 25, 128, 1024, 0, BF16) == ARG
     assert call(1 << 26, 128, 1024, 1, E4M3) == ARG  # tiles of 128 columns quantize h themselves
     assert call(1 << 26, 128, 8192, 0, BF16) == UNSUPPORTED
+
+
+# ------------------------------------------------------------------ sizes of scratch
+
+def test_scratch_of_types_that_are_refused():
+    import torch
+    import weight_only_int4_w4a16_amd as w4
+    for dtype in (torch.float32, torch.float64, torch.uint8, torch.float8_e5m2, None):
+        for quantized in (False, True):
+            with pytest.raises(w4.W4A16Error, match="dtype") as e:
+                w4.fp8_workspace_bytes(40, 256, 64, dtype, quantized=quantized)
+            assert e.value.status == ARG
+    assert w4.fp8_workspace_bytes(40, 256, 64, torch.float16) >= 40 * 256

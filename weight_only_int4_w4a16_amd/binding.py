@@ -1047,16 +1047,24 @@ def _fp8_scratch(x, need, workspace, others):
     return ws, ws.data_ptr(), need
 
 
-def fp8_workspace_bytes(M: int, K: int, N: int, x_dtype, swiglu: bool = False, quantized: bool = False) -> int:
-    """Bytes that :func:`gemm_fp8` (``swiglu``: :func:`gemm_fp8_swiglu`) needs for ``x[M, K]`` of ``x_dtype``, whatever its
-    out dtype."""
+def _fp8_types(x_dtype, quantized):
+    """The w4a16 dtypes of a product's x and of the results it may have."""
     torch = _torch()
     if not _dtypes:
         _load_dtypes()
+    if x_dtype is torch.float8_e4m3fn:
+        return E4M3, (E4M3,) if quantized else (F32, BF16)
+    if x_dtype not in _act_dtypes:
+        _fail(f"x: dtype {x_dtype}, expected float16, bfloat16 or float8_e4m3fn")
+    return _dtypes[x_dtype], (E4M3,) if quantized else (F32, _dtypes[x_dtype])
+
+
+def fp8_workspace_bytes(M: int, K: int, N: int, x_dtype, swiglu: bool = False, quantized: bool = False) -> int:
+    """Bytes that :func:`gemm_fp8` (``swiglu``: :func:`gemm_fp8_swiglu`) needs for ``x[M, K]`` of ``x_dtype``, whatever its
+    out dtype. 0 for sizes that the product refuses."""
+    dt, outs = _fp8_types(x_dtype, quantized)
     if max(M, K, N) > _INT_MAX:
         return 0
-    dt = E4M3 if x_dtype is torch.float8_e4m3fn else _dtypes[x_dtype]
-    outs = (E4M3,) if quantized else (F32, _dtypes[torch.bfloat16] if dt == E4M3 else dt)
     return max(int(lib().w4a16_fp8_workspace_bytes(M, K, N, dt, int(swiglu), o)) for o in outs)
 
 
