@@ -104,4 +104,26 @@ def test_scratch_of_types_that_are_refused():
             with pytest.raises(w4.W4A16Error, match="dtype") as e:
                 w4.fp8_workspace_bytes(40, 256, 64, dtype, quantized=quantized)
             assert e.value.status == ARG
+            with pytest.raises(w4.W4A16Error, match="dtype"):
+                w4.fp8_grouped_workspace_bytes(20, 2, 3, 256, 64, dtype, quantized=quantized)
     assert w4.fp8_workspace_bytes(40, 256, 64, torch.float16) >= 40 * 256
+
+
+def test_scratch_of_every_call_that_takes_a_workspace(L):
+    import torch
+    import weight_only_int4_w4a16_amd as w4
+    for tokens, topk, groups, K, N in [(1, 1, 1, 256, 64), (20, 2, 3, 512, 256), (600, 4, 8, 2048, 1408)]:
+        for x, dt in ((torch.bfloat16, BF16), (torch.float16, F16), (torch.float8_e4m3fn, E4M3)):
+            for gather in (0, 1):
+                for glu, quantized in ((0, 0), (1, 0), (1, 1)):
+                    outs = (E4M3,) if quantized else (F32, BF16 if dt == E4M3 else dt)
+                    want = max(L.w4a16_fp8_grouped_workspace_bytes(tokens, topk, groups, gather, K, N, dt, glu, o) for o in outs)
+                    have = w4.fp8_grouped_workspace_bytes(tokens, topk, groups, K, N, x, bool(glu), bool(quantized), bool(gather))
+                    assert have == want and (dt == E4M3 or have >= tokens * (1 if gather else topk) * K)
+        M = tokens * topk
+        assert w4.fp8_backward_workspace_bytes(M, K, N) == L.w4a16_fp8_backward_workspace_bytes(M, K, N) > M * (2 * N + K)
+        have = w4.fp8_grouped_backward_workspace_bytes(tokens, topk, groups, K, N)
+        assert have == L.w4a16_fp8_grouped_backward_workspace_bytes(tokens, topk, groups, K, N) > M * (2 * N + K)
+    assert w4.fp8_backward_workspace_bytes(2 ** 32 + 4, 256, 64) == 0  # not the size of 4 rows
+    assert w4.fp8_grouped_backward_workspace_bytes(2 ** 32 + 4, 1, 1, 256, 64) == 0
+    assert w4.fp8_grouped_workspace_bytes(2 ** 32 + 4, 1, 1, 256, 64, torch.bfloat16) == 0

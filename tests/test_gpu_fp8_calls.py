@@ -231,3 +231,40 @@ def test_out_and_workspace_overlap_nothing_that_is_read():
     a, b = w4.gemm_fp8_backward(dy, inside, codes_t, scales_t, workspace=big[(M * K * 2 + 255) // 256 * 256:])
     c, d = w4.gemm_fp8_backward(dy, x, codes_t, scales_t)
     assert torch.equal(a, c) and torch.equal(b, d)
+
+
+def test_workspaces_of_the_public_sizes():
+    """Each call with a workspace of the bytes that its size function names, for every result type."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    tokens, topk, E, K, N = 40, 2, 3, 256, 192
+
+    def space(n):
+        ws, ends = T._guarded((max(n, 1),), torch.uint8)
+        return ws, ends
+
+    r = w4.route(torch.from_numpy(T._ids(tokens, topk, E, 1)).cuda(), E)
+    x, _ = T._rows((tokens, K), "f16", 1)
+    codes, scales, _ = T._weight((E,), N, K, 2, halves=2)
+    ws, ends = space(w4.fp8_grouped_workspace_bytes(tokens, topk, E, K, N, x.dtype, swiglu=True, gather=True))
+    for dtype in (torch.float16, torch.float32):
+        got = w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, out_dtype=dtype, workspace=ws)
+        assert torch.equal(got, w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, out_dtype=dtype))
+    ends("SwiGLU")
+    ws, ends = space(w4.fp8_grouped_workspace_bytes(tokens, topk, E, K, N, x.dtype, swiglu=True, quantized=True, gather=True))
+    q, s = w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, quantized=True, workspace=ws)
+    q2, s2 = w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, quantized=True)
+    ends("quantized")
+    assert np.array_equal(T._bits(q), T._bits(q2)) and torch.equal(s, s2)
+    S = tokens * topk
+    dy, _ = T._rows((S, N), "f16", 3)
+    xs, _ = T._rows((S, K), "f16", 4)
+    codes_t, scales_t, _ = T._weight((E,), K, N, 5)
+    ws, ends = space(w4.fp8_grouped_backward_workspace_bytes(tokens, topk, E, K, N))
+    got = w4.gemm_fp8_grouped_backward(dy, xs, r, codes_t, scales_t, workspace=ws)
+    ends("routed gradients")
+    assert all(map(torch.equal, got, w4.gemm_fp8_grouped_backward(dy, xs, r, codes_t, scales_t)))
+    ws, ends = space(w4.fp8_backward_workspace_bytes(S, K, N))
+    got = w4.gemm_fp8_backward(dy, xs, codes_t[0], scales_t[0], workspace=ws)
+    ends("gradients")
+    assert all(map(torch.equal, got, w4.gemm_fp8_backward(dy, xs, codes_t[0], scales_t[0])))

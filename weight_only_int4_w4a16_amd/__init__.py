@@ -15,7 +15,8 @@ from .binding import (W4A16Error, F16, BF16, F32, E4M3, lib, packed_bytes, works
                       grouped_kernel_name, lora_add, lora_workspace_bytes,
                       quantize_fp8, quantize_fp8_columns, quantize_fp8_weight, gemm_fp8, gemm_fp8_swiglu,
                       gemm_fp8_grouped, gemm_fp8_grouped_swiglu, gemm_fp8_backward, gemm_fp8_grouped_backward,
-                      fp8_kernel_name, fp8_workspace_bytes)
+                      fp8_kernel_name, fp8_workspace_bytes, fp8_grouped_workspace_bytes,
+                      fp8_backward_workspace_bytes, fp8_grouped_backward_workspace_bytes)
 
 __all__ = ["W4A16Error", "F16", "BF16", "F32", "E4M3", "lib", "packed_bytes", "workspace_bytes",
            "awq_workspace_bytes", "w4a8_workspace_bytes", "pack", "gemm", "gemm_static", "gemm_nf4", "gemm_awq",
@@ -26,4 +27,5 @@ __all__ = ["W4A16Error", "F16", "BF16", "F32", "E4M3", "lib", "packed_bytes", "w
            "grouped_kernel_name", "lora_add", "lora_workspace_bytes",
            "quantize_fp8", "quantize_fp8_columns", "quantize_fp8_weight", "gemm_fp8",
            "gemm_fp8_swiglu", "gemm_fp8_grouped", "gemm_fp8_grouped_swiglu", "gemm_fp8_backward",
-           "gemm_fp8_grouped_backward", "fp8_kernel_name", "fp8_workspace_bytes"]
+           "gemm_fp8_grouped_backward", "fp8_kernel_name", "fp8_workspace_bytes", "fp8_grouped_workspace_bytes",
+           "fp8_backward_workspace_bytes", "fp8_grouped_backward_workspace_bytes"]

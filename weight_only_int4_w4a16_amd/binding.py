@@ -1068,6 +1068,28 @@ def fp8_workspace_bytes(M: int, K: int, N: int, x_dtype, swiglu: bool = False, q
     return max(int(lib().w4a16_fp8_workspace_bytes(M, K, N, dt, int(swiglu), o)) for o in outs)
 
 
+def fp8_grouped_workspace_bytes(tokens: int, topk: int, groups: int, K: int, N: int, x_dtype, swiglu: bool = False,
+                                quantized: bool = False, gather: bool = False) -> int:
+    """The same of :func:`gemm_fp8_grouped` and :func:`gemm_fp8_grouped_swiglu` for the plan of ``tokens`` x ``topk`` slots."""
+    dt, outs = _fp8_types(x_dtype, quantized)
+    if max(tokens, topk, groups, K, N) > _INT_MAX:
+        return 0
+    f = lib().w4a16_fp8_grouped_workspace_bytes
+    return max(int(f(tokens, topk, groups, int(gather), K, N, dt, int(swiglu), o)) for o in outs)
+
+
+def fp8_backward_workspace_bytes(M: int, K: int, N: int) -> int:
+    """The same of :func:`gemm_fp8_backward` for ``dy[M, N]`` and ``x[M, K]``."""
+    return 0 if max(M, K, N) > _INT_MAX else int(lib().w4a16_fp8_backward_workspace_bytes(M, K, N))
+
+
+def fp8_grouped_backward_workspace_bytes(tokens: int, topk: int, groups: int, K: int, N: int) -> int:
+    """The same of :func:`gemm_fp8_grouped_backward`."""
+    if max(tokens, topk, groups, K, N) > _INT_MAX:
+        return 0
+    return int(lib().w4a16_fp8_grouped_backward_workspace_bytes(tokens, topk, groups, K, N))
+
+
 def _gemm_fp8(x, codes, scales, x_scales, glu, quantized, out_dtype, out, workspace):
     M, K, x_dt, xsp = _fp8_x(x, x_scales)
     device = x.device
@@ -1134,7 +1156,7 @@ def gemm_fp8_grouped(x, routing: Routing, codes, scales, x_scales=None, gather: 
                      workspace=None):
     """:func:`gemm_fp8` of sorted rows with their groups' weights ``codes[groups, N, K]``, ``scales[groups, ...]``: zeros
     in the rows of no group. ``x`` (and ``x_scales``) holds the sorted rows, or with ``gather`` the tokens', read
-    through the plan."""
+    through the plan. ``workspace``: optional, ``fp8_grouped_workspace_bytes(...)``."""
     return _gemm_fp8_grouped(x, routing, codes, scales, x_scales, 0, False, gather, out_dtype, out, workspace)
 
 
@@ -1176,7 +1198,7 @@ def gemm_fp8_backward(dy, x, codes_t, scales_t, workspace=None):
     weight ``codes_t[K, N]``, ``scales_t[ceil(K/128), ceil(N/128)]`` (:func:`quantize_fp8_weight`).
 
     ``dx = dy @ W`` in x's dtype, dy quantized by rows; ``dw = dy.T @ x`` in fp32 ``[N, K]``, both quantized by columns
-    (scales over 128 rows). N and K are multiples of 16."""
+    (scales over 128 rows). N and K are multiples of 16. ``workspace``: optional, ``fp8_backward_workspace_bytes(...)``."""
     torch = _torch()
     M, N, K, dt, yp, xp, cp, sp = _fp8_gradients(dy, x, None, (), codes_t, scales_t)
     dx = torch.empty_like(x)
@@ -1191,7 +1213,8 @@ def gemm_fp8_backward(dy, x, codes_t, scales_t, workspace=None):
 def gemm_fp8_grouped_backward(dy, x, routing: Routing, codes_t, scales_t, workspace=None):
     """:func:`gemm_fp8_backward` of sorted rows ``dy[rows, N]``, ``x[rows, K]`` and their groups' transposed weights
     ``codes_t[groups, K, N]``: ``dx[rows, K]`` with zeros in the rows of no group, ``dw[groups, N, K]`` with zeros for a
-    group of no rows. For ``dw`` a group's rows are cut in 128s from its first one."""
+    group of no rows. For ``dw`` a group's rows are cut in 128s from its first one. ``workspace``: optional,
+    ``fp8_grouped_backward_workspace_bytes(...)``."""
     _need_routing(routing)
     torch, r = _torch(), routing
     _, N, K, dt, yp, xp, cp, sp = _fp8_gradients(dy, x, r.rows, (r.groups,), codes_t, scales_t)
