@@ -43,15 +43,137 @@ def check_pinned():
                 T._within(y.cpu().double().numpy(), ref, T._stored(ref, bound, kind), kind)
 
 
-@pytest.mark.parametrize("rows", [16, 32, 64, 128, 256])
-def test_pinned_tiles(rows):
+def _pinned(rows, check):
     """The pin is read once a process: a child runs its products."""
     here = os.path.dirname(os.path.abspath(__file__))
     env = {**os.environ, "W4A16_FP8_ROWS": str(rows), "PYTHONPATH": os.pathsep.join([ROOT, here])}
-    run = subprocess.run([sys.executable, "-c", "import test_gpu_fp8_calls as t; t.check_pinned()"], cwd=ROOT, env=env,
+    run = subprocess.run([sys.executable, "-u", "-c", f"import test_gpu_fp8_calls as t; t.{check}()"], cwd=ROOT, env=env,
                          capture_output=True, text=True, timeout=100)
     print(run.stdout, flush=True)
     assert run.returncode == 0, run.stderr[-3000:]
+
+
+@pytest.mark.parametrize("rows", [16, 32, 64, 128, 256])
+def test_pinned_tiles(rows):
+    _pinned(rows, "check_pinned")
+
+
+def _check_gradients(M, K, N, kind, n_some=None, k_some=None):
+    """Both gradients, dw in some of its rows and columns."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    x, xv = T._rows((M, K), kind, M + K)
+    dy, dyv = T._rows((M, N), kind, M + N)
+    codes_t, scales_t, wt = T._weight((), K, N, K + N)
+    dx, dw = w4.gemm_fp8_backward(dy, x, codes_t, scales_t)
+    m = np.unique(np.concatenate([np.arange(0, M, 17), [M - 1]]))
+    v = F.rows_value(*F.quantize_rows(dyv[m]))
+    ref = F.gemm_fp8_ref(v, wt)
+    T._within(dx[torch.from_numpy(m).cuda()].cpu().double().numpy(), ref, T._stored(ref, T._sum_bound(v, wt, kind), kind), "dx")
+    n = np.arange(N) if n_some is None else n_some
+    k = np.arange(K) if k_some is None else k_some
+    ref, bound = T._dw_bound(dyv[:, n], xv[:, k])
+    T._within(dw.cpu().double().numpy()[np.ix_(n, k)], ref, bound, "dw")
+
+
+def _edges(size, step, tile):
+    """Indices all over 0 .. size - 1, both sides of the tiles' edges among them."""
+    at = np.arange(tile, size, tile)
+    return np.unique(np.concatenate([np.arange(0, size, step), at - 1, at, [size - 1]]))
+
+
+def check_pinned_families():
+    """Each kind of product on one tile: plain in 16 and 32 bits, SwiGLU and its codes, routed, and the gradients; a weight's
+    gradient on more tiles than the chip has compute units where the pinned tile loops."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    rows = int(os.environ["W4A16_FP8_ROWS"])
+    M, K, N = 300, 400, 1000
+    x, xv = T._rows((M, K), "f16", 1)
+    xv = F.rows_value(*F.quantize_rows(xv))
+    for halves, width in ((1, N), (2, 640)):
+        T._announce(f"pinned {rows}: {M}x{K}x{width}")
+        codes, scales, wv = T._weight((), width, K, 2, halves=halves)
+        f = w4.gemm_fp8 if halves == 1 else w4.gemm_fp8_swiglu
+        for kind in ("f16", "f32"):
+            ref, bound = (F.gemm_fp8_ref(xv, wv), T._sum_bound(xv, wv, kind)) if halves == 1 else T._glu_bound(xv, wv, kind)
+            y = f(x, codes, scales, out_dtype=T._dtype(kind))
+            T._within(y.cpu().double().numpy(), ref, T._stored(ref, bound, kind), kind)
+    q, s = w4.gemm_fp8_swiglu(x, codes, scales, quantized=True)
+    T._check_quantized(q, s, ref, bound, "quantized h")
+
+    tokens, topk, E, N2 = 300, 2, 5, 640
+    T._announce(f"pinned {rows}: routed {tokens}x{topk} groups={E} {K}x{N2}")
+    r, (offsets, order, _) = T._routed(T._ids(tokens, topk, E, 4), E)
+    n = int(offsets[-1])
+    sorted_rows = xv[order // topk]
+    codes, scales, wv = T._weight((E,), N2, K, 3, halves=2)
+    h, dh = T._each(lambda v, w: T._glu_bound(v, w, "f32"), offsets, sorted_rows, wv)
+    q, s = w4.gemm_fp8_grouped_swiglu(x, r, codes, scales, gather=True, quantized=True)
+    T._check_quantized(q, s, h, dh, "quantized h of routed rows")
+    assert not T._bits(q)[n:].any()
+    codes, scales, wv = T._weight((E,), N2, K, 5)
+    for kind in ("f16", "f32"):
+        ref, bound = T._each(lambda v, w: (F.gemm_fp8_ref(v, w), T._sum_bound(v, w, kind)), offsets, sorted_rows, wv)
+        y = w4.gemm_fp8_grouped(x, r, codes, scales, gather=True, out_dtype=T._dtype(kind))
+        T._within(y.cpu().double().numpy(), ref, T._stored(ref, bound, kind), f"routed {kind}")
+
+    if rows < 128:
+        T._announce(f"pinned {rows}: gradients of 300x272x400")
+        _check_gradients(300, 272, 400, "bf16")
+    elif rows == 128:
+        M, K, N = 700, 2064, 4112
+        cus = torch.cuda.get_device_properties(0).multi_processor_count
+        assert -(-N // 128) * -(-K // 256) > cus
+        T._announce(f"pinned {rows}: gradients of {M}x{K}x{N}")
+        _check_gradients(M, K, N, "bf16", _edges(N, 97, 128), _edges(K, 61, 256))
+
+
+@pytest.mark.parametrize("rows", [32, 64, 128, 256])
+def test_every_family_on_each_tile(rows):
+    _pinned(rows, "check_pinned_families")
+
+
+@pytest.mark.parametrize("M,K,N", [(700, 2064, 4112), (1030, 4112, 4208)])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_gradients_of_many_tiles(M, K, N, kind):
+    """Weights' gradients of several times as many tiles of any height as the chip has compute units, whose sizes no tile divides."""
+    T._announce(f"gemm_fp8_backward {M}x{K}x{N} {kind}")
+    _check_gradients(M, K, N, kind, _edges(N, 97, 128), _edges(K, 61, 256))
+
+
+@pytest.mark.parametrize("tokens,groups,K,N,how", [(1500, 12, 528, 1040, "skewed"), (2600, 40, 272, 1168, "mixed"), (3000, 40, 528, 1040, "skewed"), (900, 300, 16, 16, "mixed")])
+def test_grouped_gradients_of_many_tiles(tokens, groups, K, N, how):
+    """Weights' gradients by group on tiles of 128 x 256 that workgroups take in turn: more of them than compute units, of groups of
+    no row, of a few and of several blocks of 128."""
+    import weight_only_int4_w4a16_amd as w4
+    torch = torch_mod()
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert -(-N // 128) * -(-K // 256) * groups > cus
+    T._announce(f"grouped backward {tokens} groups={groups} {K}x{N} {how}")
+    ids = T._ids(tokens, 1, groups, tokens, how)
+    ids[ids == 1] = 0  # a group of no rows among the first
+    ids[:300] = 2      # and one of more than two blocks
+    ids[300:310] = -1
+    ids[-50:] = groups - 1
+    r, (offsets, _, _) = T._routed(ids, groups)
+    n = int(offsets[-1])
+    sizes = np.diff(offsets)
+    assert n < tokens and sizes.min() == 0 and sizes.max() > 256 and np.any((0 < sizes) & (sizes < 128))
+    x, xv = T._rows((tokens, K), "bf16", tokens + K)
+    dy, dyv = T._rows((tokens, N), "bf16", tokens + N)
+    x[n:], dy[n:] = float("nan"), float("inf")  # rows of no group reach nothing
+    codes_t, scales_t, _ = T._weight((groups,), K, N, K + N)
+    _, dw = w4.gemm_fp8_grouped_backward(dy, x, r, codes_t, scales_t)
+    rows, cols = _edges(N, 97, 128), _edges(K, 61, 256)
+    got = dw[:, torch.from_numpy(rows).cuda()][:, :, torch.from_numpy(cols).cuda()].cpu().double().numpy()
+    for e in range(groups):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if a == b:
+            assert not bool(dw[e].any()), f"group {e}"
+        else:
+            ref, bound = T._dw_bound(dyv[a:b][:, rows], xv[a:b][:, cols])
+            T._within(got[e], ref, bound, f"dw of group {e}")
 
 
 # ------------------------------------------------------------------ SwiGLU far below zero
