@@ -352,16 +352,17 @@ w4a16_status w4a16_lora_add(const void* x, const void* y, int M, int K, int N, w
  * and zero codes. A group that holds an infinity or a NaN has a NaN scale and NaN codes, so that
  * every result it enters is NaN.
  * Products: the codes' products of a block of 128 k are summed on the matrix cores, the block's sum
- * is multiplied by its two scales and added to the result in fp32, which is rounded once. Results
- * are deterministic. A block's sum is an fp32 one for fp32 results, for h that leaves as codes and in
+ * is multiplied by its two scales and added to the result in fp32, which is rounded once. The two scales
+ * are multiplied first: where their product passes 2^128 a block's part is infinite or NaN, and under
+ * 2^-126 it loses bits. SiLU(g) is 0 where exp(-g) passes 2^128 (g under -88.7). Results are deterministic. A block's sum is an fp32 one for fp32 results, for h that leaves as codes and in
  * the kernels w4a16_fp8_16 and w4a16_fp8_32. For other 16-bit results it comes from the 8-bit MFMA,
  * which drops product bits about 17 below the block's largest: the sum is off by at most 2^-10 of its
  * largest product, on normal operands 1.5e-5 of the result, an eighth of what rounding to fp16 costs.
  * Limits, else W4A16_ERR_UNSUPPORTED: a product's depth is a multiple of 16; operands whose
  * offsets 31 bits hold (K < 2^23; rows * K / 32 < 2^31; a SwiGLU weight below 2 GiB a group);
- * up to 2^30 columns of a result; launches of fewer than 2^32 threads: rows quantized a wave for two times 512
- * values, rows * ceil(K / 512) < 2^27 - 8; columns and blocks, fewer than 2^24 tiles of 128 x 128; where a second
- * kernel adds slices of k or quantizes h, rows * ceil(columns / 512) < 2^25.
+ * up to 2^30 columns of a result; launches of fewer than 2^32 threads: of rows that are quantized
+ * ceil(rows / 8) * ceil(K / 512) < 2^24, of columns and blocks fewer than 2^24 tiles of 128 x 128, and where
+ * a second kernel adds slices of k or quantizes h, rows * ceil(columns / 512) < 2^25.
  * Codes, 16-bit x and dy need 16-byte alignment, other arrays that of their elements (outputs of
  * products 16 bytes).
  * ------------------------------------------------------------------------------------------ */

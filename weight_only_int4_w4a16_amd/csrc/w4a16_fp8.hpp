@@ -35,7 +35,7 @@ struct Fp8Args {
   float* out_scales;  // [ceil(N / 128)][M], for e4m3
   const void* values; // x itself, of 16 bits, where the kernel quantizes it (fp8_takes_values; x and xs are not read)
   int values_dtype;
-  float* scratch;     // fp32 h [M][N] where a kernel cannot quantize it by itself
+  float* scratch;     // fp32 sums of each slice of k, or h [M][N] where a kernel cannot quantize it by itself
   hipStream_t stream;
 };
 
