@@ -127,3 +127,18 @@ def test_scratch_of_every_call_that_takes_a_workspace(L):
     assert w4.fp8_backward_workspace_bytes(2 ** 32 + 4, 256, 64) == 0  # not the size of 4 rows
     assert w4.fp8_grouped_backward_workspace_bytes(2 ** 32 + 4, 1, 1, 256, 64) == 0
     assert w4.fp8_grouped_workspace_bytes(2 ** 32 + 4, 1, 1, 256, 64, torch.bfloat16) == 0
+
+
+@pytest.mark.parametrize("M,K,N,glu", [(40, 1 << 23, 64, 0), (40, 1 << 15, 1 << 17, 1), (1, 1 << 23, 64, 0), ((1 << 29) - 1, 256, 64, 0)])
+def test_refused_sizes_have_no_scratch_and_no_kernel(L, M, K, N, glu):
+    for xdt, odt in ((E4M3, BF16), (BF16, BF16), (BF16, F32)):
+        assert L.w4a16_gemm_fp8(P, xdt, Q, M, K, N, 2 * P, Q, glu, 3 * P, odt, None, None, 0, None) == UNSUPPORTED
+        assert L.w4a16_fp8_workspace_bytes(M, K, N, xdt, glu, odt) == 0
+        if M < 1 << 20:
+            assert L.w4a16_gemm_fp8_grouped(P, xdt, Q, Q, M, 1, 2, 0, K, N, 2 * P, Q, glu, 3 * P, odt, None, None, 0, None) == UNSUPPORTED
+            assert L.w4a16_fp8_grouped_workspace_bytes(M, 1, 2, 0, K, N, xdt, glu, odt) == 0
+    assert L.w4a16_fp8_kernel_name(M, K, N, glu) == b"none"
+    if not glu:
+        assert L.w4a16_fp8_backward_workspace_bytes(M, N, K) == 0
+        if M < 1 << 20:
+            assert L.w4a16_fp8_grouped_backward_workspace_bytes(M, 1, 2, N, K) == 0

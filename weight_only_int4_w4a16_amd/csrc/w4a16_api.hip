@@ -766,6 +766,7 @@ static w4a16_status fp8_operands(w4a16::Fp8Args& a, const void* x, w4a16_dtype x
 
 size_t w4a16_fp8_workspace_bytes(int M, int K, int N, w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
   if (check_fp8(M, K, N, x_dtype, swiglu, out_dtype) != W4A16_OK || M == 0) return 0;
+  if (!w4a16::fp8_fits(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype)) return 0;
   const bool codes = is_e4m3(x_dtype) || w4a16::fp8_takes_values(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype);
   return (codes ? 0 : fp8_rows_bytes(M, K)) +
          w4a16::fp8_scratch_bytes(M, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype);
@@ -789,7 +790,8 @@ w4a16_status w4a16_gemm_fp8(const void* x, w4a16_dtype x_dtype, const float* x_s
 }
 
 const char* w4a16_fp8_kernel_name(int M, int K, int N, int swiglu) {
-  if (M <= 0 || check_fp8(M, K, N, W4A16_E4M3, swiglu, W4A16_F32) != W4A16_OK) return "none";
+  if (M <= 0 || check_fp8(M, K, N, W4A16_E4M3, swiglu, W4A16_F16) != W4A16_OK) return "none";
+  if (!w4a16::fp8_fits(M, swiglu ? N / 2 : N, K, swiglu != 0, W4A16_F16)) return "none";
   return w4a16::fp8_name(M, swiglu ? N / 2 : N, K, swiglu != 0);
 }
 
@@ -804,8 +806,10 @@ static w4a16_status check_fp8_grouped(int tokens, int topk, int groups, int gath
 size_t w4a16_fp8_grouped_workspace_bytes(int tokens, int topk, int groups, int gather, int K, int N,
                                          w4a16_dtype x_dtype, int swiglu, w4a16_dtype out_dtype) {
   if (check_fp8_grouped(tokens, topk, groups, gather, K, N, x_dtype, swiglu, out_dtype) != W4A16_OK || tokens == 0) return 0;
+  const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
+  if (!w4a16::fp8_grouped_fits(r, swiglu ? N / 2 : N, K, swiglu != 0, (int)out_dtype)) return 0;
   return (is_e4m3(x_dtype) ? 0 : fp8_rows_bytes(gather ? tokens : tokens * topk, K)) +
-         w4a16::fp8_grouped_scratch_bytes(w4a16::route_layout(tokens, topk, groups), swiglu ? N / 2 : N, (int)out_dtype);
+         w4a16::fp8_grouped_scratch_bytes(r, swiglu ? N / 2 : N, (int)out_dtype);
 }
 
 w4a16_status w4a16_gemm_fp8_grouped(const void* x, w4a16_dtype x_dtype, const float* x_scales,
@@ -966,7 +970,7 @@ size_t w4a16_fp8_grouped_backward_workspace_bytes(int tokens, int topk, int grou
   if (check_route(tokens, topk, groups) != W4A16_OK || tokens == 0) return 0;
   const w4a16::RouteLayout r = w4a16::route_layout(tokens, topk, groups);
   const size_t depth = fp8_grouped_depth(r);
-  if (check_fp8_backward(r.S, depth, K, N) != W4A16_OK) return 0;
+  if (check_fp8_backward(r.S, depth, K, N) != W4A16_OK || !w4a16::fp8_grouped_fits(r, K, N, false, W4A16_F16)) return 0;
   return fp8_backward_layout(r.S, K, N, depth, false).total;
 }
 
