@@ -1034,12 +1034,12 @@ def _fp8_out(x, x_dt, rows, width, quantized, out_dtype, out, reads):
     return out, dt, None
 
 
-def _fp8_scratch(x, need, workspace, others):
-    """A call's workspace: the caller's, apart from the ``others``, or one of torch's for this call. Returns it, its address
-    and bytes."""
+def _fp8_scratch(x, need, workspace, reads, out=None):
+    """A call's workspace: the caller's, apart from what the call reads and its output, or one of torch's for this call.
+    Returns it, its address and bytes."""
     if workspace is not None:
         _expect_workspace(workspace, need, x.device)
-        _apart(workspace, "workspace", others)
+        _apart(workspace, "workspace", reads if out is None else (*reads, out))
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if not need:
         return None, None, 0
@@ -1097,7 +1097,7 @@ def _gemm_fp8(x, codes, scales, x_scales, glu, quantized, out_dtype, out, worksp
     reads = (x, codes, scales) if xsp is None else (x, codes, scales, x_scales)
     out, dt, out_scales = _fp8_out(x, x_dt, M, N // 2 if glu else N, quantized, out_dtype, out, reads)
     L = lib()
-    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_workspace_bytes(M, K, N, x_dt, glu, dt), workspace, (*reads, out))
+    ws, wp, nbytes = _fp8_scratch(x, L.w4a16_fp8_workspace_bytes(M, K, N, x_dt, glu, dt), workspace, reads, out)
     _fp8_call(L.w4a16_gemm_fp8, "w4a16_gemm_fp8", device, x.data_ptr(), x_dt, xsp, M, K, N, cp, sp, glu, out.data_ptr(), dt,
               None if out_scales is None else out_scales.data_ptr(), wp, nbytes)
     return (out, out_scales) if quantized else out
@@ -1145,7 +1145,7 @@ def _gemm_fp8_grouped(x, routing, codes, scales, x_scales, glu, quantized, gathe
     out, dt, out_scales = _fp8_out(x, x_dt, r.rows, N // 2 if glu else N, quantized, out_dtype, out, reads)
     L, gather = lib(), int(gather)
     need = L.w4a16_fp8_grouped_workspace_bytes(r.tokens, r.topk, r.groups, gather, K, N, x_dt, glu, dt)
-    ws, wp, nbytes = _fp8_scratch(x, need, workspace, (*reads, out))
+    ws, wp, nbytes = _fp8_scratch(x, need, workspace, reads, out)
     _fp8_call(L.w4a16_gemm_fp8_grouped, "w4a16_gemm_fp8_grouped", device, x.data_ptr(), x_dt, xsp, r.plan.data_ptr(), r.tokens,
               r.topk, r.groups, gather, K, N, cp, sp, glu, out.data_ptr(), dt,
               None if out_scales is None else out_scales.data_ptr(), wp, nbytes)
